@@ -13,3 +13,4 @@ Importing it fails loudly when the CUDA library has not been built.
 from ._binding import *  # noqa: F401,F403
 from ._binding import StrataError, lib, strata_sampling_params  # noqa: F401
 from .sampler import Sampler  # noqa: F401
+from .tail import *  # noqa: F401,F403

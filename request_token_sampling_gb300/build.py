@@ -1,4 +1,4 @@
-"""Build the sampler's shared library in-tree with nvcc for sm_103a (no cmake, one translation unit)."""
+"""Build the sampler's shared library in-tree with nvcc for sm_103a (no cmake; its files compile side by side)."""
 from __future__ import annotations
 
 import os
@@ -10,10 +10,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libstrata_sample.so")
-SOURCES = [os.path.join(CSRC, "strata_sample.cu")]
-DEPENDS = SOURCES + [os.path.join(CSRC, "strata_kernel.cuh"), os.path.join(CSRC, "strata_device.cuh"),
-                     os.path.join(CSRC, "strata_resident.cuh"), os.path.join(CSRC, "strata_merge.cuh"),
-                     os.path.join(ROOT, "include", "strata_sample.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("strata_sample.cu", "strata_tail.cu", "strata_project.cu")]
+DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
+    "strata_kernel.cuh", "strata_device.cuh", "strata_resident.cuh", "strata_merge.cuh", "strata_host.h",
+    "strata_norm.cuh", "strata_draw.cuh", "strata_project.cuh")]
+DEPENDS += [os.path.join(ROOT, "include", f) for f in ("strata_sample.h", "strata_tail.h")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -37,15 +38,21 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "-I", os.path.join(ROOT, "include"), "-o", tmp, *SOURCES]
+    flags = [*ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    r = subprocess.run(cmd, capture_output=True, text=True)
+        flags.append("-Xptxas=-v")
+    objects = [os.path.join(LIB_DIR, os.path.splitext(os.path.basename(s))[0] + ".o") for s in SOURCES]
+    started = [subprocess.Popen([nvcc_path(), *flags, "-c", "-o", o, s], stdout=subprocess.PIPE,
+                                stderr=subprocess.STDOUT, text=True) for s, o in zip(SOURCES, objects)]
+    said = [p.communicate()[0] for p in started]
+    for p, text in zip(started, said):
+        if p.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + text)
+        if verbose:
+            print(text)
+    r = subprocess.run([nvcc_path(), *ARCH_FLAGS, "-shared", "-o", tmp, *objects], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
-    if verbose:
-        print(r.stdout + r.stderr)
+        raise RuntimeError("nvcc failed to link:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

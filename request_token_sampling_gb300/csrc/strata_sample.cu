@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "../../include/strata_sample.h"
+#include "strata_host.h"
 #include "strata_kernel.cuh"
 #include "strata_merge.cuh"
 #include "strata_resident.cuh"
@@ -39,6 +40,18 @@ int fail(int code, const char* fmt, ...) {
   va_end(ap);
   return code;
 }
+
+}  // namespace
+
+int strata::host_fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+namespace {
 
 // The kernel instance for a launch: streaming or resident chunk x logit type x allowed-id mask x
 // own outputs; the streaming kernel's latency shape (`two`: few blocks, no call alongside) takes

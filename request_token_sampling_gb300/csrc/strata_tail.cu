@@ -1,0 +1,72 @@
+// strata_tail.cu -- host side of strata_norm_rows and strata_draw_rows (include/strata_tail.h).
+#include <cuda_runtime.h>
+
+#include "../../include/strata_tail.h"
+#include "strata_draw.cuh"
+#include "strata_host.h"
+#include "strata_norm.cuh"
+
+using strata::host_fail;
+
+namespace {
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+int launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" int strata_norm_rows(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                                int dtype, int T, int H, float eps, void* residual_out, int64_t ldro, void* y,
+                                int64_t ldy, void* q, int64_t ldq, float* scale, void* stream) {
+  if (dtype != STRATA_DTYPE_F32 && dtype != STRATA_DTYPE_BF16) return host_fail(STRATA_EINVAL, "dtype %d", dtype);
+  if (T < 0) return host_fail(STRATA_EINVAL, "T=%d", T);
+  if (H < 1 || H > STRATA_TAIL_MAX_WIDTH) return host_fail(STRATA_ERANGE, "H=%d outside 1..%d", H, STRATA_TAIL_MAX_WIDTH);
+  if (!(eps >= 0.0f)) return host_fail(STRATA_EINVAL, "eps=%g is not a number of 0 or more", static_cast<double>(eps));
+  if (ldx < H || (residual != nullptr && ldr < H) || (residual_out != nullptr && ldro < H) || (y != nullptr && ldy < H) ||
+      (q != nullptr && ldq < H))
+    return host_fail(STRATA_EINVAL, "a row stride below H=%d", H);
+  if (T == 0) return STRATA_OK;
+  if (residual_out == nullptr && y == nullptr && q == nullptr) return host_fail(STRATA_EINVAL, "no output");
+  if ((q == nullptr) != (scale == nullptr)) return host_fail(STRATA_EINVAL, "q and scale must be given together");
+  if (x == nullptr || weight == nullptr) return host_fail(STRATA_EINVAL, "null x or weight");
+  const uintptr_t esz = dtype == STRATA_DTYPE_F32 ? 4 : 2;
+  if (misaligned(x, esz) || misaligned(residual, esz) || misaligned(weight, esz) || misaligned(residual_out, esz) ||
+      misaligned(y, esz) || misaligned(scale, 4))
+    return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
+  strata::NormArgs A{x, residual, weight, residual_out, y, q, scale, ldx, ldr, ldro, ldy, ldq, T, H, eps};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == STRATA_DTYPE_F32)
+    strata::norm_kernel<float><<<T, strata::NORM_THREADS, 0, s>>>(A);
+  else
+    strata::norm_kernel<__nv_bfloat16><<<T, strata::NORM_THREADS, 0, s>>>(A);
+  return launched("strata_norm_rows");
+}
+
+extern "C" int strata_draw_rows(const void* logits, int dtype, int B, int V, int64_t ld, const float* u,
+                                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                                int32_t* out_ids, float* out_lps, void* stream) {
+  if (dtype != STRATA_DTYPE_F32 && dtype != STRATA_DTYPE_BF16) return host_fail(STRATA_EINVAL, "dtype %d", dtype);
+  if (B < 0) return host_fail(STRATA_EINVAL, "B=%d", B);
+  if (V < 1 || V > STRATA_MAX_VOCAB) return host_fail(STRATA_ERANGE, "V=%d outside 1..%d", V, STRATA_MAX_VOCAB);
+  if (ld < V) return host_fail(STRATA_EINVAL, "ld=%lld below V=%d", static_cast<long long>(ld), V);
+  if (B == 0) return STRATA_OK;
+  if (logits == nullptr || u == nullptr || out_ids == nullptr) return host_fail(STRATA_EINVAL, "null logits, u or out_ids");
+  const int64_t esz = dtype == STRATA_DTYPE_F32 ? 4 : 2;
+  if (misaligned(logits, 16)) return host_fail(STRATA_EALIGN, "logits not 16-byte aligned");
+  if (ld * esz % 16 != 0)
+    return host_fail(STRATA_EALIGN, "row stride of %lld bytes not a multiple of 16", static_cast<long long>(ld * esz));
+  if (misaligned(u, 4) || misaligned(temperature, 4) || misaligned(top_k, 4) || misaligned(top_p, 4) ||
+      misaligned(min_p, 4) || misaligned(out_ids, 4) || misaligned(out_lps, 4))
+    return host_fail(STRATA_EALIGN, "a per-row array is not 4-byte aligned");
+  strata::DrawArgs A{logits, ld, V, u, temperature, top_p, min_p, top_k, out_ids, out_lps};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == STRATA_DTYPE_F32)
+    strata::draw_kernel<float><<<B, strata::DRAW_THREADS, 0, s>>>(A);
+  else
+    strata::draw_kernel<__nv_bfloat16><<<B, strata::DRAW_THREADS, 0, s>>>(A);
+  return launched("strata_draw_rows");
+}
