@@ -1,5 +1,9 @@
 // strata_project.cu -- host side of strata_project_rows (include/strata_tail.h).
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
 
 #include "../../include/strata_tail.h"
 #include "strata_host.h"
@@ -18,21 +22,81 @@ int cuda_fail(cudaError_t e, const char* what) {
   return host_fail(STRATA_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-template <typename E>
-void launch_simple(const strata::ProjectArgs& A, cudaStream_t s) {
-  if (A.S > 0) {
-    const int64_t warps = static_cast<int64_t>(A.T) * A.R;
-    strata::shrink_kernel<E><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(A);
-  }
-  const dim3 grid(static_cast<unsigned>((A.N + 7) / 8), static_cast<unsigned>((A.T + strata::PROJ_ROWS - 1) / strata::PROJ_ROWS));
-  strata::project_kernel<E><<<grid, 256, 0, s>>>(A);
+using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
+using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, strata::ProjectArgs);
+
+constexpr int MAX_ROWS = 1 << 19;  // rows times adapters of a tile count in 31 bits
+constexpr int BN_SIZES[4] = {16, 32, 64, 128};
+
+template <int BN>
+Kernel pick(bool f8, bool split) {
+  return f8 ? (split ? strata::project_kernel<BN, true, true> : strata::project_kernel<BN, true, false>)
+            : (split ? strata::project_kernel<BN, false, true> : strata::project_kernel<BN, false, false>);
 }
+
+Kernel kernel_for(int bn, bool f8, bool split) {
+  return bn == 16 ? pick<16>(f8, split) : bn == 32 ? pick<32>(f8, split) : bn == 64 ? pick<64>(f8, split) : pick<128>(f8, split);
+}
+
+// What the calls need to know of a device, found at the first call on it.
+struct Device {
+  int sms = 0;
+  uint32_t* errors = nullptr;
+  EncodeFn encode = nullptr;
+  cudaError_t status = cudaSuccess;
+};
+
+const Device& device_info(int id) {
+  static Device devices[64];
+  static std::once_flag once[64];
+  std::call_once(once[id], [id] {
+    Device& d = devices[id];
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if ((d.status = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, id)) != cudaSuccess) return;
+    if ((d.status = cudaGetSymbolAddress(&p, g_tail_errors)) != cudaSuccess) return;
+    d.errors = static_cast<uint32_t*>(p);
+    d.status = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+    if (d.status != cudaSuccess) return;
+    if (found != cudaDriverEntryPointSuccess || p == nullptr) {
+      d.status = cudaErrorNotSupported;
+      return;
+    }
+    d.encode = reinterpret_cast<EncodeFn>(p);
+    for (int bn : BN_SIZES)
+      for (int i = 0; i < 4 && d.status == cudaSuccess; ++i)
+        d.status = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel_for(bn, i & 1, i & 2)),
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, strata::proj_smem(bn));
+  });
+  return devices[id];
+}
+
+// A map of `dims` (innermost first; strides in bytes of the outer ones) cut into boxes of `box`.
+bool encode(EncodeFn fn, CUtensorMap* m, bool bytes, int rank, const void* p, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box, int line) {
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims,
+            strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of a tile: the fewest that hold the call's rows, 128 for more.  The products' cost grows with
+// them, and w is read once for each tile of rows.
+int tile_rows(int T) {
+  for (int bn : BN_SIZES)
+    if (T <= bn) return bn;
+  return 128;
+}
+
+int64_t lists_bytes(int t_tiles, int bn) { return (static_cast<int64_t>(t_tiles) * (bn + 1) * 4 + 255) / 256 * 256; }
 
 }  // namespace
 
 extern "C" int64_t strata_project_workspace(int T, int S, int R) {
   if (T <= 0 || S <= 0 || R <= 0) return 0;
-  return static_cast<int64_t>(T) * R * 4;
+  const int bn = tile_rows(T), t_tiles = (T + bn - 1) / bn;
+  return lists_bytes(t_tiles, bn) + static_cast<int64_t>(t_tiles) * std::min(S, bn) * bn * R * 2;
 }
 
 extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
@@ -41,7 +105,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
                                    int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream) {
   if (dtype != STRATA_DTYPE_BF16 && dtype != STRATA_DTYPE_F8) return host_fail(STRATA_EINVAL, "dtype %d", dtype);
   if (T < 0 || N < 1) return host_fail(STRATA_EINVAL, "T=%d N=%d", T, N);
-  if (T > 65535 * strata::PROJ_ROWS) return host_fail(STRATA_ERANGE, "T=%d", T);
+  if (T > MAX_ROWS) return host_fail(STRATA_ERANGE, "T=%d above %d", T, MAX_ROWS);
   if (K < 1 || K > STRATA_TAIL_MAX_WIDTH) return host_fail(STRATA_ERANGE, "K=%d outside 1..%d", K, STRATA_TAIL_MAX_WIDTH);
   if (S < 0 || S > STRATA_TAIL_MAX_ADAPTERS) return host_fail(STRATA_ERANGE, "S=%d outside 0..%d", S, STRATA_TAIL_MAX_ADAPTERS);
   if (S > 0 && (R < 16 || R > STRATA_TAIL_MAX_RANK || R % 16 != 0))
@@ -65,15 +129,99 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   const int64_t need = strata_project_workspace(T, S, R);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
     return host_fail(STRATA_EINVAL, "the workspace needs %lld bytes on 256 bytes of alignment", static_cast<long long>(need));
-  strata::ProjectArgs A{x, w, x_scale, w_scale, adapter_scale, static_cast<const __nv_bfloat16*>(a),
-                        static_cast<const __nv_bfloat16*>(b), row_adapter, static_cast<__nv_bfloat16*>(y),
-                        static_cast<float*>(workspace), ldx, ldw, ldy, T, N, K, S, R};
+  int id = -1;
+  cudaError_t e = cudaGetDevice(&id);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (id >= 64) return host_fail(STRATA_ERANGE, "device %d", id);
+  const Device& dev = device_info(id);
+  if (dev.status != cudaSuccess) return cuda_fail(dev.status, "strata_project_rows");
+
+  const int bn = tile_rows(T), t_tiles = (T + bn - 1) / bn, n_tiles = (N + strata::PROJ_M - 1) / strata::PROJ_M;
+  const int64_t tiles = static_cast<int64_t>(t_tiles) * n_tiles;
+  if (tiles > INT32_MAX) return host_fail(STRATA_ERANGE, "T=%d N=%d", T, N);
+  const int most = std::min(S, bn);
+  strata::ProjectArgs A{};
+  A.x = x;
+  A.x_scale = x_scale;
+  A.w_scale = w_scale;
+  A.adapter_scale = adapter_scale;
+  A.a = static_cast<const __nv_bfloat16*>(a);
+  A.b = static_cast<const __nv_bfloat16*>(b);
+  A.row_adapter = row_adapter;
+  A.y = static_cast<__nv_bfloat16*>(y);
+  A.lists = static_cast<int32_t*>(workspace);
+  A.spread = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + lists_bytes(t_tiles, bn));
+  A.errors = dev.errors;
+  A.ldx = ldx;
+  A.ldy = ldy;
+  A.T = T;
+  A.N = N;
+  A.K = K;
+  A.S = S;
+  A.R = R;
+  A.most = most;
+  A.rank_block = R % 64 == 0 ? 64 : R % 32 == 0 ? 32 : 16;
+  A.n_tiles = n_tiles;
+  A.t_tiles = t_tiles;
+
+  CUtensorMap mw, mx, mb{}, mh{};
+  const cuuint32_t elems = f8 ? 128 : 64;
+  {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldw * esz)};
+    const cuuint32_t box[2] = {elems, strata::PROJ_M};
+    if (!encode(dev.encode, &mw, f8, 2, w, dims, strides, box, 128)) return host_fail(STRATA_EINVAL, "w cannot be mapped");
+  }
+  {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldx * esz)};
+    const cuuint32_t box[2] = {elems, static_cast<cuuint32_t>(bn)};
+    if (!encode(dev.encode, &mx, f8, 2, x, dims, strides, box, 128)) return host_fail(STRATA_EINVAL, "x cannot be mapped");
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (f8)
-    launch_simple<__nv_fp8_e4m3>(A, s);
-  else
-    launch_simple<__nv_bfloat16>(A, s);
-  const cudaError_t e = cudaGetLastError();
+  if (S > 0) {
+    const cuuint64_t r = static_cast<cuuint64_t>(R), bytes = r * 2;
+    const cuuint64_t dims[3] = {r, static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(S)};
+    const cuuint64_t strides[2] = {bytes, bytes * static_cast<cuuint64_t>(N)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(A.rank_block), strata::PROJ_M, 1};
+    if (!encode(dev.encode, &mb, false, 3, b, dims, strides, box, A.rank_block * 2)) return host_fail(STRATA_EINVAL, "b cannot be mapped");
+    const cuuint64_t hdims[2] = {r, static_cast<cuuint64_t>(t_tiles) * most * bn};
+    const cuuint32_t hbox[2] = {static_cast<cuuint32_t>(A.rank_block), static_cast<cuuint32_t>(bn)};
+    if (!encode(dev.encode, &mh, false, 2, A.spread, hdims, strides, hbox, A.rank_block * 2))
+      return host_fail(STRATA_EINVAL, "the workspace cannot be mapped");
+    const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(R / 8));
+    if (f8)
+      strata::shrink_kernel<__nv_fp8_e4m3><<<grid, 256, 0, s>>>(A, bn);
+    else
+      strata::shrink_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(A, bn);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "strata_project_rows");
+  }
+  // Few tiles leave most of the GPU idle: then a cluster of blocks shares a tile, as many as still
+  // fit beside one another and have two stages each.
+  const int k_stages = static_cast<int>((K + elems - 1) / elems);
+  int ranks = 1;
+  while (ranks < 8 && tiles * ranks * 2 <= dev.sms && k_stages >= ranks * 4) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, dev.sms)), 1, 1);
+  cfg.blockDim = dim3(strata::PROJ_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(strata::proj_smem(bn));
+  cfg.stream = s;
+  cudaLaunchAttribute attrs[2];
+  int na = 0;
+  if (ranks > 1) {
+    attrs[na].id = cudaLaunchAttributeClusterDimension;
+    attrs[na].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attrs[na].val.clusterDim.y = attrs[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  if (S > 0) {  // starts beside the inner rows' kernel and waits for it before what it wrote
+    attrs[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+  }
+  cfg.attrs = attrs;
+  cfg.numAttrs = na;
+  e = cudaLaunchKernelEx(&cfg, kernel_for(bn, f8, ranks > 1), mw, mx, mb, mh, A);
   return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_project_rows");
 }
 

@@ -1,26 +1,135 @@
 // strata_project.cuh -- a projection shared by all rows plus each row's own low-rank adapter.
 //
 //   y[t] = sx[t] sw (x[t] w^T) + h[t] b_c^T,   h[t] = g_c sx[t] (x[t] a_c^T),   c = row_adapter[t]
+//
+// Two kernels.  shrink_kernel computes the inner rows h in 32 bits and writes them, rounded to bfloat16,
+// spread out: for each tile of rows and each adapter of the tile a block [tile rows][R] that holds h where
+// the row uses that adapter and zeros elsewhere.  project_kernel then treats b of the tile's adapters as
+// more of the sum's length: for a tile of 128 outputs and up to 128 rows,
+//   base += w[128][64] x[rows][64]^T  over K,     delta += b_j[128][R] spread_j[rows][R]^T  over the adapters j
+// with tcgen05.mma (outputs are its M, rows its N: a tile of w is read once for all rows).  base and delta
+// are separate accumulators: 8-bit rows scale base alone, and a product 0 * inf of a broken adapter,
+// which falls on other requests' rows in delta, is found there and taken back.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "strata_device.cuh"
+
 namespace strata {
 
 struct ProjectArgs {
-  const void *x, *w;
+  const void* x;
   const float *x_scale, *w_scale, *adapter_scale;
   const __nv_bfloat16 *a, *b;
   const int32_t* row_adapter;
   __nv_bfloat16* y;
-  float* h;  // workspace, [T][R]
-  int64_t ldx, ldw, ldy;
+  __nv_bfloat16* spread;  // [tiles][most][tile rows][R]
+  int32_t* lists;         // per tile: how many adapters, then their ids in ascending order ([1 + tile rows])
+  uint32_t* errors;
+  int64_t ldx, ldy;
   int T, N, K, S, R;
+  int most;               // adapters that a tile can have: min(S, tile rows)
+  int rank_block;         // R is cut into blocks of 64, 32 or 16 (one swizzle line of shared memory)
+  int n_tiles, t_tiles;
 };
 
+constexpr int PROJ_M = 128;        // outputs of a tile: the accumulator's lanes
+constexpr int PROJ_LINE = 128;     // bytes of a row that one stage holds (64 bfloat16 or 128 8-bit elements)
+constexpr int PROJ_THREADS = 192;  // warp 0 loads, warp 1 issues the products, warps 2-5 write the tile
+constexpr uint32_t PROJ_SPINS = 1u << 24;
+
+__host__ __device__ constexpr int proj_stage_bytes(int bn) { return (PROJ_M + bn) * PROJ_LINE; }
+__host__ __device__ constexpr int proj_stages(int bn) { return bn <= 16 ? 12 : bn <= 32 ? 11 : bn <= 64 ? 9 : 7; }
+__host__ __device__ constexpr int proj_smem(int bn) { return proj_stages(bn) * proj_stage_bytes(bn) + 1024 + 512; }
+
+// ------------------------------------------------------------------------------ PTX
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// Shared-memory operand descriptor: rows of one swizzle line (`line` = 128, 64 or 32 bytes), K along
+// the line, groups of eight rows `8 * line` bytes apart.
+__device__ __forceinline__ uint64_t mma_desc(uint32_t addr, uint32_t line) {
+  const uint64_t swizzle = line == 128 ? 2 : line == 64 ? 4 : 6;
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>((8 * line) >> 4) << 32) |
+         (1ull << 46) | (swizzle << 61);
+}
+
+// Instruction descriptor: 32-bit sums, both operands K-major, M = 128 outputs, N = `bn` rows.
+// Operand format 1 is bfloat16 in kind::f16, 0 is e4m3 in kind::f8f6f4.
+__device__ constexpr uint32_t mma_idesc(bool f8, int bn) {
+  return (1u << 4) | (f8 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(bn >> 3) << 17) |
+         (static_cast<uint32_t>(PROJ_M >> 4) << 24);
+}
+
+template <bool F8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  if constexpr (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ float dsmem_ld_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// ------------------------------------------------------------------------------ bounded waits
+// A wait that runs out raises an error bit and `dead`, which ends every other wait of the block.
+__device__ __forceinline__ bool proj_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* dead, uint32_t* errors,
+                                          uint32_t bit) {
+  for (uint32_t i = 0; i < PROJ_SPINS; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*dead != 0u) return false;
+  }
+  *dead = 1u;
+  atomicOr(errors, bit);
+  return false;
+}
+
+// ------------------------------------------------------------------------------ the inner rows
 __device__ __forceinline__ float proj_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float proj_f32(__nv_fp8_e4m3 v) { return static_cast<float>(v); }
 
@@ -30,50 +139,340 @@ __device__ __forceinline__ float proj_warp_sum(float v) {
   return v;
 }
 
-// h: one warp per row and rank.
+// Eight warps: the block of row t takes eight of its inner products, one to a warp.
 template <typename E>
-__global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A) {
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-  const int t = static_cast<int>(at / A.R), r = static_cast<int>(at % A.R), lane = threadIdx.x & 31;
-  if (t >= A.T) return;
+__global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A, int tile_rows) {
+  grid_dep_launch();
+  __shared__ uint32_t used[32];
+  const int t = blockIdx.x, tile = t / tile_rows, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * 8 + warp;
+  if (threadIdx.x < 32) used[threadIdx.x] = 0;
+  __syncthreads();
+  const int t0 = tile * tile_rows, rows = min(tile_rows, A.T - t0);
+  for (int i = threadIdx.x; i < rows; i += 256) {
+    const int c = A.row_adapter[t0 + i];
+    if (c >= 0 && c < A.S) atomicOr(&used[c >> 5], 1u << (c & 31));
+  }
+  __syncthreads();
   const int c = A.row_adapter[t];
-  if (c < 0 || c >= A.S) return;
-  const E* x = static_cast<const E*>(A.x) + t * A.ldx;
-  const __nv_bfloat16* a = A.a + (static_cast<int64_t>(c) * A.R + r) * A.K;
+  const bool mine = c >= 0 && c < A.S;
+  int count = 0, at = -1;
+  for (int w = 0; w < 32; ++w) {
+    if (mine && w == c >> 5) at = count + __popc(used[w] & ((1u << (c & 31)) - 1u));
+    count += __popc(used[w]);
+  }
+  if (t == t0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    int32_t* list = A.lists + static_cast<int64_t>(tile) * (tile_rows + 1);
+    list[0] = count;
+    int n = 1;
+    for (int w = 0; w < 32; ++w)
+      for (uint32_t bits = used[w]; bits; bits &= bits - 1) list[n++] = w * 32 + __ffs(bits) - 1;
+  }
   float s = 0.0f;
-  for (int k = lane; k < A.K; k += 32) s = fmaf(proj_f32(x[k]), proj_f32(a[k]), s);
-  s = proj_warp_sum(s);
-  if (lane == 0) A.h[at] = A.adapter_scale[c] * ((A.x_scale != nullptr ? A.x_scale[t] : 1.0f) * s);
+  if (mine) {
+    const E* x = static_cast<const E*>(A.x) + t * A.ldx;
+    const __nv_bfloat16* a = A.a + (static_cast<int64_t>(c) * A.R + r) * A.K;
+    for (int k = lane * 8; k < A.K; k += 256) {
+      __align__(16) __nv_bfloat16 av[8];
+      __align__(16) E xv[8];
+      *reinterpret_cast<uint4*>(av) = *reinterpret_cast<const uint4*>(a + k);
+      if constexpr (sizeof(E) == 2)
+        *reinterpret_cast<uint4*>(xv) = *reinterpret_cast<const uint4*>(x + k);
+      else
+        *reinterpret_cast<uint2*>(xv) = *reinterpret_cast<const uint2*>(x + k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(proj_f32(xv[i]), proj_f32(av[i]), s);
+    }
+    s = proj_warp_sum(s);
+    s = A.adapter_scale[c] * ((A.x_scale != nullptr ? A.x_scale[t] : 1.0f) * s);
+  }
+  // rounded to bfloat16 for the tensor cores: 2^-9 of h, as y's own rounding is of y
+  for (int j = lane; j < count; j += 32)
+    A.spread[((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - t0)) * A.R + r] =
+        __float2bfloat16_rn(j == at ? s : 0.0f);
 }
 
-// One warp per output of PROJ_ROWS rows: w is read once for them, x from L1.
-constexpr int PROJ_ROWS = 8;
-template <typename E>
-__global__ void __launch_bounds__(256) project_kernel(ProjectArgs A) {
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31;
-  if (n >= A.N) return;
-  const E* w = static_cast<const E*>(A.w) + n * A.ldw;
-  const int t0 = blockIdx.y * PROJ_ROWS, rows = min(PROJ_ROWS, A.T - t0);
-  float s[PROJ_ROWS] = {};
-  for (int k = lane; k < A.K; k += 32) {
-    const float wk = proj_f32(w[k]);
-#pragma unroll
-    for (int i = 0; i < PROJ_ROWS; ++i)
-      if (i < rows) s[i] = fmaf(proj_f32(static_cast<const E*>(A.x)[(t0 + i) * A.ldx + k]), wk, s[i]);
+// ------------------------------------------------------------------------------ the products
+template <int BN>
+struct ProjBars {
+  uint64_t full[proj_stages(BN)], empty[proj_stages(BN)], done[2], freed[2], drained;
+  uint32_t tmem, dead;
+};
+
+// delta for one output and row from its own adapter alone, where the tile's sum is not finite.
+__device__ __noinline__ float proj_own_delta(const ProjectArgs& A, int tile, int tile_rows, int t, int n) {
+  const int c = A.row_adapter[t];
+  if (c < 0 || c >= A.S) return 0.0f;
+  const int32_t* list = A.lists + static_cast<int64_t>(tile) * (tile_rows + 1);
+  int j = 0;
+  while (j < list[0] && list[1 + j] != c) ++j;
+  const __nv_bfloat16* h = A.spread + ((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - tile * tile_rows)) * A.R;
+  const __nv_bfloat16* b = A.b + (static_cast<int64_t>(c) * A.N + n) * A.R;
+  float d = 0.0f;
+  for (int r = 0; r < A.R; ++r) d = fmaf(proj_f32(h[r]), proj_f32(b[r]), d);
+  return d;
+}
+
+template <int BN, bool F8>
+__device__ __forceinline__ void proj_write(const ProjectArgs& A, int t_tile, int t, int n, float sw, float base, float delta,
+                                           bool adapters) {
+  float v = base;
+  if constexpr (F8) v *= A.x_scale[t] * sw;
+  if (adapters) {
+    if (!(fabsf(delta) < __int_as_float(0x7F800000))) delta = proj_own_delta(A, t_tile, BN, t, n);
+    v += delta;
   }
-#pragma unroll
-  for (int i = 0; i < PROJ_ROWS; ++i) {
-    if (i >= rows) break;
-    const int t = t0 + i, c = A.S > 0 ? A.row_adapter[t] : -1;
-    float v = proj_warp_sum(s[i]), d = 0.0f;
-    if (A.x_scale != nullptr) v *= A.x_scale[t] * A.w_scale[n];
-    if (c >= 0 && c < A.S) {
-      const __nv_bfloat16* b = A.b + (static_cast<int64_t>(c) * A.N + n) * A.R;
-      for (int r = lane; r < A.R; r += 32) d = fmaf(A.h[static_cast<int64_t>(t) * A.R + r], proj_f32(b[r]), d);
-      v += proj_warp_sum(d);
+  A.y[t * A.ldy + n] = __float2bfloat16_rn(v);
+}
+
+// A block per SM goes through tiles (SPLIT false), or a cluster's blocks share one tile's stages and
+// join their sums through shared memory in rank order (SPLIT: few tiles, all of the GPU to be kept busy).
+template <int BN, bool F8, bool SPLIT>
+__global__ void __launch_bounds__(PROJ_THREADS, 1)
+    project_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                   const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mh,
+                   const __grid_constant__ ProjectArgs A) {
+  constexpr int STAGES = proj_stages(BN), STAGE = proj_stage_bytes(BN);
+  constexpr int ELEMS = F8 ? 128 : 64;  // of the sum's length in one stage
+  constexpr uint32_t TMEM_COLS = 4 * BN;  // two tiles' base and delta
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  ProjBars<BN>* B = reinterpret_cast<ProjBars<BN>*>(smem + STAGES * STAGE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile uint32_t* dead = &B->dead;
+  const uint32_t bit = 0x08u;  // STRATA_DEVERR_TIMEOUT
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&B->full[i], 1);
+      mbar_init(&B->empty[i], 1);
     }
-    if (lane == 0) A.y[t * A.ldy + n] = __float2bfloat16_rn(v);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->done[i], 1);
+      mbar_init(&B->freed[i], 4);
+    }
+    mbar_init(&B->drained, 1);
+    B->dead = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B->tmem)), "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem;
+
+  const int k_stages = (A.K + ELEMS - 1) / ELEMS;
+  const int blocks = A.S > 0 ? A.R / A.rank_block : 0;          // rank blocks of an adapter
+  const int per_stage = A.S > 0 ? 64 / A.rank_block : 1;        // rank blocks in a stage
+  const uint32_t line = static_cast<uint32_t>(A.rank_block) * 2;
+  uint32_t rank = 0, ranks = 1;
+  if constexpr (SPLIT) {
+    rank = cluster_ctarank();
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  }
+  const int first = SPLIT ? blockIdx.x / ranks : blockIdx.x;
+  const int step = SPLIT ? A.n_tiles * A.t_tiles : gridDim.x;
+  const int tiles = A.n_tiles * A.t_tiles;
+  auto adapters_of = [&](int t_tile) {
+    return A.S > 0 ? *(A.lists + static_cast<int64_t>(t_tile) * (BN + 1)) : 0;
+  };
+  // the stages of a tile that this block takes: [from, to) of k_stages + ceil(sub-blocks / per_stage)
+  auto share = [&](int all, int& from, int& to) {
+    from = SPLIT ? static_cast<int>(static_cast<int64_t>(all) * rank / ranks) : 0;
+    to = SPLIT ? static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / ranks) : all;
+  };
+  // `lists` and `spread` are the previous kernel's: wait for it before the first look at them.  A
+  // split tile's shares depend on how many adapters it has, so there everybody waits first.
+  auto wait_shrink = [&]() {
+    if (A.S > 0) grid_dep_wait();
+  };
+  if constexpr (SPLIT) wait_shrink();
+
+  if (warp == 0 && lane == 0) {
+    uint32_t it = 0;
+    bool alive = true, waited = SPLIT;
+    for (int tile = first; tile < tiles && alive; tile += step) {
+      const int n0 = tile / A.t_tiles * PROJ_M, t_tile = tile % A.t_tiles;
+      int from = 0, to = k_stages, subs = 0;
+      if constexpr (SPLIT) {
+        subs = adapters_of(t_tile) * blocks;
+        share(k_stages + (subs + per_stage - 1) / per_stage, from, to);
+      }
+      for (int s = from; alive; ++s, ++it) {
+        if (!SPLIT && s == k_stages) {  // now what the adapters add
+          if (!waited) wait_shrink(), waited = true;
+          subs = adapters_of(t_tile) * blocks;
+          to = k_stages + (subs + per_stage - 1) / per_stage;
+        }
+        if (s >= to) break;
+        const uint32_t slot = it % STAGES;
+        if (it >= STAGES && !proj_wait(&B->empty[slot], (it / STAGES + 1) & 1, dead, A.errors, bit)) {
+          alive = false;
+          break;
+        }
+        const uint32_t at = smem_u32(smem + slot * STAGE), bar = smem_u32(&B->full[slot]);
+        if (s < k_stages) {
+          mbar_arrive_expect_tx(&B->full[slot], STAGE);
+          tma_2d(at, &mw, s * ELEMS, n0, bar);
+          tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * ELEMS, t_tile * BN, bar);
+        } else {
+          const int sub0 = (s - k_stages) * per_stage, n = min(per_stage, subs - sub0);
+          mbar_arrive_expect_tx(&B->full[slot], static_cast<uint32_t>(n) * (PROJ_M + BN) * line);
+          for (int i = 0; i < n; ++i) {
+            const int j = (sub0 + i) / blocks, rb = (sub0 + i) % blocks;
+            const int c = A.lists[static_cast<int64_t>(t_tile) * (BN + 1) + 1 + j];
+            tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, c, bar);
+            tma_2d(at + PROJ_M * PROJ_LINE + i * BN * line, &mh, rb * A.rank_block, (t_tile * A.most + j) * BN, bar);
+          }
+        }
+      }
+    }
+    if (!alive) {  // a wait ran out: no copy of this block may be in flight when it ends
+      const uint32_t begun = it, left = begun < STAGES ? begun : STAGES;
+      for (uint32_t i = begun - left; i < begun; ++i)
+        for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->full[i % STAGES], (i / STAGES) & 1); ++spin) {
+        }
+    }
+  } else if (warp == 1 && lane == 0) {
+    uint32_t it = 0, turn = 0;
+    bool alive = true, waited = SPLIT;
+    for (int tile = first; tile < tiles && alive; tile += step, ++turn) {
+      const int t_tile = tile % A.t_tiles;
+      const uint32_t buf = turn & 1, base = tmem + buf * 2 * BN, delta = base + BN;
+      if (turn >= 2 && !proj_wait(&B->freed[buf], (turn / 2 + 1) & 1, dead, A.errors, bit)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      int from = 0, to = k_stages, subs = 0;
+      if constexpr (SPLIT) {
+        subs = adapters_of(t_tile) * blocks;
+        share(k_stages + (subs + per_stage - 1) / per_stage, from, to);
+      }
+      bool add_base = false, add_delta = false;
+      for (int s = from; alive; ++s, ++it) {
+        if (!SPLIT && s == k_stages) {
+          if (!waited) wait_shrink(), waited = true;
+          subs = adapters_of(t_tile) * blocks;
+          to = k_stages + (subs + per_stage - 1) / per_stage;
+        }
+        if (s >= to) break;
+        const uint32_t slot = it % STAGES;
+        if (!proj_wait(&B->full[slot], (it / STAGES) & 1, dead, A.errors, bit)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = smem_u32(smem + slot * STAGE);
+        if (s < k_stages) {
+          const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + PROJ_M * PROJ_LINE, PROJ_LINE);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // 32 bytes of each row at a time
+            mma<F8>(base, da + 2 * i, db + 2 * i, mma_idesc(F8, BN), add_base);
+            add_base = true;
+          }
+        } else {
+          const int n = min(per_stage, subs - (s - k_stages) * per_stage);
+          for (int i = 0; i < n; ++i) {
+            const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
+            const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * BN * line, line);
+            for (int q = 0; q < A.rank_block / 16; ++q) {
+              mma<false>(delta, da + 2 * q, db + 2 * q, mma_idesc(false, BN), add_delta);
+              add_delta = true;
+            }
+          }
+        }
+        mma_commit(&B->empty[slot]);
+      }
+      if (alive) mma_commit(&B->done[buf]);
+    }
+    if (!alive) {  // the products in flight end before the block gives its tensor memory back
+      mma_commit(&B->drained);
+      for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->drained, 0); ++spin) {
+      }
+    }
+  } else if (warp >= 2) {
+    const uint32_t quarter = warp & 3;  // the 32 lanes of tensor memory that this warp may read
+    uint32_t turn = 0;
+    if constexpr (!SPLIT) wait_shrink();
+    for (int tile = first; tile < tiles; tile += step, ++turn) {
+      const int t_tile = tile % A.t_tiles, t0 = t_tile * BN, n = tile / A.t_tiles * PROJ_M + quarter * 32 + lane;
+      const uint32_t buf = turn & 1;
+      const int adapters = adapters_of(t_tile);
+      const bool ok = proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      const uint32_t base = tmem + buf * 2 * BN + (quarter << 21);
+      const int rows = min(BN, A.T - t0);
+      if constexpr (!SPLIT) {
+        const float sw = F8 && n < A.N ? A.w_scale[n] : 1.0f;
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 16) {
+          float vb[16], vd[16] = {};
+          tmem_ld16(base + c, vb);
+          if (adapters > 0) tmem_ld16(base + BN + c, vd);
+          tmem_wait_ld();
+          if (n < A.N) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c + i < rows) proj_write<BN, F8>(A, t_tile, t0 + c + i, n, sw, vb[i], vd[i], adapters > 0);
+          }
+        }
+      } else {
+        // this block's sums to its own shared memory: [base, delta][row][output]
+        int from, to;
+        share(k_stages + (adapters * blocks + per_stage - 1) / per_stage, from, to);
+        const bool has_base = from < k_stages && to > from, has_delta = to > k_stages && to > from;
+        float* mine = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 16) {
+          float vb[16] = {}, vd[16] = {};
+          if (has_base) tmem_ld16(base + c, vb);
+          if (has_delta) tmem_ld16(base + BN + c, vd);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            mine[(c + i) * PROJ_M + quarter * 32 + lane] = vb[i];
+            if (adapters > 0) mine[(BN + c + i) * PROJ_M + quarter * 32 + lane] = vd[i];
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->freed[buf]);
+    }
+  }
+  __syncthreads();
+  if constexpr (SPLIT) {
+    cluster_arrive();
+    cluster_wait();
+    if (*dead == 0u) {
+      const int tile = first, t_tile = tile % A.t_tiles, t0 = t_tile * BN, n0 = tile / A.t_tiles * PROJ_M;
+      const int rows = min(BN, A.T - t0), adapters = adapters_of(t_tile);
+      const uint32_t own = smem_u32(smem);
+      for (int e = rank * PROJ_THREADS + threadIdx.x; e < rows * PROJ_M; e += ranks * PROJ_THREADS) {
+        const int t = e / PROJ_M, n = n0 + e % PROJ_M;
+        if (n >= A.N) continue;
+        float vb = 0.0f, vd = 0.0f;
+        for (uint32_t q = 0; q < ranks; ++q) {
+          const uint32_t at = dsmem_addr(own, q);
+          vb += dsmem_ld_f32(at + e * 4);
+          if (adapters > 0) vd += dsmem_ld_f32(at + (BN * PROJ_M + e) * 4);
+        }
+        proj_write<BN, F8>(A, t_tile, t0 + t, n, F8 ? A.w_scale[n] : 1.0f, vb, vd, adapters > 0);
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
   }
 }
 
