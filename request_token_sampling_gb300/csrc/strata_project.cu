@@ -89,9 +89,28 @@ int tile_rows(int T) {
   return 128;
 }
 
+// The current device's entry (checked: it is usable), or an error code.
+int current_device(const Device** dev) {
+  int id = -1;
+  const cudaError_t e = cudaGetDevice(&id);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (id >= 64) return host_fail(STRATA_ERANGE, "device %d", id);
+  *dev = &device_info(id);
+  return (*dev)->status == cudaSuccess ? STRATA_OK : cuda_fail((*dev)->status, "device setup");
+}
+
 int64_t lists_bytes(int t_tiles, int bn) { return (static_cast<int64_t>(t_tiles) * (bn + 1) * 4 + 255) / 256 * 256; }
 
 }  // namespace
+
+int strata::tail_device(uint32_t** errors, int* sms) {
+  const Device* dev = nullptr;
+  const int rc = current_device(&dev);
+  if (rc != STRATA_OK) return rc;
+  *errors = dev->errors;
+  *sms = dev->sms;
+  return STRATA_OK;
+}
 
 extern "C" int64_t strata_project_workspace(int T, int S, int R) {
   if (T <= 0 || S <= 0 || R <= 0) return 0;
@@ -129,12 +148,10 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   const int64_t need = strata_project_workspace(T, S, R);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
     return host_fail(STRATA_EINVAL, "the workspace needs %lld bytes on 256 bytes of alignment", static_cast<long long>(need));
-  int id = -1;
-  cudaError_t e = cudaGetDevice(&id);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (id >= 64) return host_fail(STRATA_ERANGE, "device %d", id);
-  const Device& dev = device_info(id);
-  if (dev.status != cudaSuccess) return cuda_fail(dev.status, "strata_project_rows");
+  const Device* found = nullptr;
+  if (const int rc = current_device(&found); rc != STRATA_OK) return rc;
+  const Device& dev = *found;
+  cudaError_t e = cudaSuccess;
 
   const int bn = tile_rows(T), t_tiles = (T + bn - 1) / bn, n_tiles = (N + strata::PROJ_M - 1) / strata::PROJ_M;
   const int64_t tiles = static_cast<int64_t>(t_tiles) * n_tiles;

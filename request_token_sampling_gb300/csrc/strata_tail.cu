@@ -10,6 +10,11 @@ using strata::host_fail;
 
 namespace {
 
+constexpr int64_t DRAW_BYTES = 64 * 1024;   // of a row in one block: two such blocks fit an SM
+constexpr int DRAW_LEAST = 4096;            // ids of a block below which splitting a row further costs more than it saves
+constexpr int64_t DRAW_SMEM = 200 * 1024;   // 2^19 float32 ids in 16 blocks and the block's own part
+static_assert(STRATA_MAX_VOCAB * 4 / strata::DRAW_MAX_CLUSTER + sizeof(strata::DrawShared) + 64 <= DRAW_SMEM, "a row fits a cluster");
+
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 int launched(const char* what) {
@@ -62,11 +67,36 @@ extern "C" int strata_draw_rows(const void* logits, int dtype, int B, int V, int
   if (misaligned(u, 4) || misaligned(temperature, 4) || misaligned(top_k, 4) || misaligned(top_p, 4) ||
       misaligned(min_p, 4) || misaligned(out_ids, 4) || misaligned(out_lps, 4))
     return host_fail(STRATA_EALIGN, "a per-row array is not 4-byte aligned");
-  strata::DrawArgs A{logits, ld, V, u, temperature, top_p, min_p, top_k, out_ids, out_lps};
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == STRATA_DTYPE_F32)
-    strata::draw_kernel<float><<<B, strata::DRAW_THREADS, 0, s>>>(A);
-  else
-    strata::draw_kernel<__nv_bfloat16><<<B, strata::DRAW_THREADS, 0, s>>>(A);
-  return launched("strata_draw_rows");
+  uint32_t* errors = nullptr;
+  int sms = 0;
+  if (const int rc = strata::tail_device(&errors, &sms); rc != STRATA_OK) return rc;
+  const bool f32 = dtype == STRATA_DTYPE_F32;
+  const void* kernel = f32 ? reinterpret_cast<const void*>(strata::draw_kernel<float>)
+                           : reinterpret_cast<const void*>(strata::draw_kernel<__nv_bfloat16>);
+  // Blocks of a row: as few as hold it with two blocks to an SM, more where few rows would leave
+  // the GPU idle and a block still has DRAW_LEAST ids.
+  int ranks = 1;
+  while (ranks < strata::DRAW_MAX_CLUSTER &&
+         (V * esz > static_cast<int64_t>(ranks) * DRAW_BYTES ||
+          (static_cast<int64_t>(B) * ranks * 2 <= sms && V >= ranks * 2 * DRAW_LEAST)))
+    ranks *= 2;
+  const int chunk = ((V + ranks - 1) / ranks + 15) / 16 * 16;
+  const size_t smem = (sizeof(strata::DrawShared) + 15) / 16 * 16 + static_cast<size_t>(chunk) * esz;
+  strata::DrawArgs A{logits, ld, V, chunk, u, temperature, top_p, min_p, top_k, out_ids, out_lps, errors};
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(DRAW_SMEM));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return host_fail(STRATA_ECUDA, "strata_draw_rows: %s", cudaGetErrorString(e));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(B) * ranks, 1, 1);
+  cfg.blockDim = dim3(strata::DRAW_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = f32 ? cudaLaunchKernelEx(&cfg, strata::draw_kernel<float>, A) : cudaLaunchKernelEx(&cfg, strata::draw_kernel<__nv_bfloat16>, A);
+  return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_draw_rows: %s", cudaGetErrorString(e));
 }
