@@ -1,16 +1,19 @@
-"""ctypes binding of the operators around the sampler (include/strata_tail.h).
+"""Binding of the operators around the sampler (include/strata_tail.h).
 
 ``strata_norm_rows``, ``strata_project_rows``, ``strata_draw_rows`` and ``strata_tail_errors`` keep the C names
 and write into the caller's tensors.  ``norm_rows``, ``project_rows`` and ``draw_rows`` allocate their outputs
 (and the projection's workspace) with PyTorch, on the stream that they run on.
+
+The calls go through a small compiled module (csrc/tail_binding.cpp), which checks the tensors, allocates and makes
+the C call; ``lib`` holds the C functions themselves for ctypes.
 """
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+import os
 
-from ._binding import (STRATA_DTYPE_BF16, STRATA_DTYPE_F32, StrataError, _check, _logits_args, _stream, _typed,  # noqa: F401
-                       lib)
+from ._binding import _check, _stream, lib
+from .build import MODULE_PATH
 
 STRATA_DTYPE_F8 = 2
 STRATA_TAIL_MAX_WIDTH = 131072
@@ -43,54 +46,40 @@ def _declare() -> None:
 _declare()
 
 
-def _rows(t, name, width=None, dtype=None, rows=None):
-    """(address, row stride) of a [rows, width] CUDA tensor whose rows are contiguous; None -> (None, 0)."""
-    if t is None:
-        return None, 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows, width] with contiguous rows")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if (width is not None and t.shape[1] != width) or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} is {tuple(t.shape)}, expected [{rows}, {width}]")
-    return t.data_ptr(), int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]))
+def _load_module():
+    """The compiled half of this binding (csrc/tail_binding.cpp); like the library it calls, it has to be built."""
+    from importlib.machinery import ExtensionFileLoader
+    from importlib.util import module_from_spec, spec_from_loader
+    if not os.path.exists(MODULE_PATH):
+        raise ImportError(f"the PyTorch binding is not built ({MODULE_PATH}); "
+                          "run `python -c 'import __graft_entry__ as g; g.build()'`")
+    import torch  # noqa: F401  (its libraries and types come first)
+    loader = ExtensionFileLoader("_strata_tail", MODULE_PATH)
+    module = module_from_spec(spec_from_loader("_strata_tail", loader))
+    loader.exec_module(module)
+    return module
 
 
-def _vector(t, n, dtype, name) -> Optional[int]:
-    if t is not None and (t.dim() != 1 or t.shape[0] != n):
-        raise ValueError(f"{name} is {tuple(t.shape)}, expected [{n}]")
-    return _typed(t, dtype, name)
+_module = _load_module()
+_norm, _project, _draw = _module.norm, _module.project, _module.draw
 
 
-def _same_device(*tensors):
-    import torch
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != here:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+def _done(out):
+    """What a compiled call gave: its outputs, or a C error code."""
+    if out.__class__ is int:
+        _check(out)
+    return out
+
+
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 # ------------------------------------------------------------------------------ C-named calls
 def strata_norm_rows(x, weight, residual=None, eps: float = 1e-6, residual_out=None, y=None, q=None, scale=None,
                      stream=None) -> None:
-    import torch
-    if x.dtype == torch.float32:
-        dt = STRATA_DTYPE_F32
-    elif x.dtype == torch.bfloat16:
-        dt = STRATA_DTYPE_BF16
-    else:
-        raise TypeError(f"unsupported row dtype {x.dtype}")
-    px, ldx = _rows(x, "x")
-    T, H = int(x.shape[0]), int(x.shape[1])
-    _same_device(x, weight, residual, residual_out, y, q, scale)
-    pr, ldr = _rows(residual, "residual", H, x.dtype, T)
-    pro, ldro = _rows(residual_out, "residual_out", H, x.dtype, T)
-    py, ldy = _rows(y, "y", H, x.dtype, T)
-    pq, ldq = _rows(q, "q", H, torch.float8_e4m3fn, T)
-    _check(lib.strata_norm_rows(px, ldx, pr, ldr, _vector(weight, H, x.dtype, "weight"), dt, T, H, float(eps), pro, ldro,
-                                py, ldy, pq, ldq, _vector(scale, T, torch.float32, "scale"), _stream(stream)))
+    _done(_norm(x, weight, residual, eps, False, False, False, dict(residual=residual_out, y=y, q=q, scale=scale),
+                _handle(stream)))
 
 
 def strata_project_workspace(T: int, S: int, R: int) -> int:
@@ -99,46 +88,13 @@ def strata_project_workspace(T: int, S: int, R: int) -> int:
 
 def strata_project_rows(x, w, y, x_scale=None, w_scale=None, a=None, b=None, row_adapter=None, adapter_scale=None,
                         workspace=None, stream=None) -> None:
-    import torch
-    if x.dtype == torch.bfloat16:
-        dt = STRATA_DTYPE_BF16
-    elif x.dtype == torch.float8_e4m3fn:
-        dt = STRATA_DTYPE_F8
-    else:
-        raise TypeError(f"unsupported row dtype {x.dtype}")
-    px, ldx = _rows(x, "x")
-    T, K = int(x.shape[0]), int(x.shape[1])
-    pw, ldw = _rows(w, "w", K, x.dtype)
-    N = int(w.shape[0])
-    _same_device(x, w, y, x_scale, w_scale, a, b, row_adapter, adapter_scale, workspace)
-    py, ldy = _rows(y, "y", N, torch.bfloat16, T)
-    S = R = 0
-    if a is not None or b is not None:
-        if a is None or b is None or row_adapter is None or adapter_scale is None:
-            raise ValueError("a, b, row_adapter and adapter_scale go together")
-        S, R = int(a.shape[0]), int(a.shape[1])
-        if tuple(a.shape) != (S, R, K) or tuple(b.shape) != (S, N, R):
-            raise ValueError(f"a is {tuple(a.shape)} and b {tuple(b.shape)}, expected [S, R, {K}] and [S, {N}, R]")
-    _check(lib.strata_project_rows(
-        px, ldx, _vector(x_scale, T, torch.float32, "x_scale"), pw, ldw, _vector(w_scale, N, torch.float32, "w_scale"), dt,
-        T, N, K, _typed(a, torch.bfloat16, "a"), _typed(b, torch.bfloat16, "b"), S, R,
-        _vector(row_adapter, T, torch.int32, "row_adapter") if S else None,
-        _vector(adapter_scale, S, torch.float32, "adapter_scale") if S else None, py, ldy,
-        _typed(workspace, torch.uint8, "workspace"), 0 if workspace is None else int(workspace.numel()), _stream(stream)))
+    _done(_project(x, w, x_scale, w_scale, a, b, row_adapter, adapter_scale, y, workspace, False, _handle(stream)))
 
 
 def strata_draw_rows(logits, u, out_ids, temperature=None, top_k=None, top_p=None, min_p=None, out_lps=None, V=None,
                      stream=None) -> None:
-    import torch
-    ptr, dt, B, V, ld = _logits_args(logits, V)
-    if B == 1:
-        ld = max(ld, V + (-V) % 8)          # the stride of one row means nothing
-    _same_device(logits, u, out_ids, temperature, top_k, top_p, min_p, out_lps)
-    f32 = torch.float32
-    _check(lib.strata_draw_rows(
-        ptr, dt, B, V, ld, _vector(u, B, f32, "u"), _vector(temperature, B, f32, "temperature"),
-        _vector(top_k, B, torch.int32, "top_k"), _vector(top_p, B, f32, "top_p"), _vector(min_p, B, f32, "min_p"),
-        _vector(out_ids, B, torch.int32, "out_ids"), _vector(out_lps, B, f32, "out_lps"), _stream(stream)))
+    _done(_draw(logits, u, temperature, top_k, top_p, min_p, V, False, False, dict(ids=out_ids, lps=out_lps),
+                _handle(stream)))
 
 
 def strata_tail_errors(stream=None) -> int:
@@ -148,69 +104,39 @@ def strata_tail_errors(stream=None) -> int:
 
 
 # ------------------------------------------------------------------------------ calls that allocate
-class _on:
-    """Allocate on the stream that the call runs on, so that the memory is not given away before it is done."""
-
-    def __init__(self, stream, like):
-        import torch
-        self.ctx = None
-        if stream is not None:
-            self.ctx = torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)
-                                         if isinstance(stream, int) else stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _side(stream, like):
+    """A context in which PyTorch allocates for `stream`: memory of a call belongs to the stream it runs on, or
+    the allocator could give it away before the call is done."""
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream)
 
 
 def norm_rows(x, weight, residual=None, eps: float = 1e-6, y: bool = True, f8: bool = False, stream=None,
               out=None) -> dict:
     """The norm of hidden rows: ``y`` and, with ``f8``, ``q`` and ``scale``; with a residual also ``residual``,
     the sum that the next layer adds to."""
-    import torch
-    o = out if out is not None else {}
-    with _on(stream, x):
-        if residual is not None and "residual" not in o:
-            o["residual"] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if y and "y" not in o:
-            o["y"] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if f8 and "q" not in o:
-            o["q"] = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        if f8 and "scale" not in o:
-            o["scale"] = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-    strata_norm_rows(x, weight, residual, eps, o.get("residual"), o.get("y"), o.get("q"), o.get("scale"), stream)
-    return o
+    if stream is not None:
+        with _side(stream, x):
+            return norm_rows(x, weight, residual, eps, y, f8, None, out)
+    return _done(_norm(x, weight, residual, eps, residual is not None, bool(y), bool(f8), {} if out is None else out, None))
 
 
 def project_rows(x, w, x_scale=None, w_scale=None, a=None, b=None, row_adapter=None, adapter_scale=None, stream=None,
                  out=None):
     """``x w^T`` with the rows' low-rank adapters, as a bfloat16 [T, N] tensor."""
-    import torch
-    T, N = int(x.shape[0]), int(w.shape[0])
-    need = strata_project_workspace(T, a.shape[0], a.shape[1]) if a is not None else 0
-    with _on(stream, x):
-        y = torch.empty(T, N, dtype=torch.bfloat16, device=x.device) if out is None else out
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    strata_project_rows(x, w, y, x_scale, w_scale, a, b, row_adapter, adapter_scale, ws, stream)
-    return y
+    if stream is not None:
+        with _side(stream, x):
+            return project_rows(x, w, x_scale, w_scale, a, b, row_adapter, adapter_scale, None, out)
+    return _done(_project(x, w, x_scale, w_scale, a, b, row_adapter, adapter_scale, out, None, True, None))
 
 
 def draw_rows(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, V=None, lps: bool = True, stream=None,
               out=None) -> dict:
     """One id per logit row from the random numbers ``u`` (one in [0, 1) for each row): ``ids`` and ``lps``."""
-    import torch
-    o = out if out is not None else {}
-    with _on(stream, logits):
-        if "ids" not in o:
-            o["ids"] = torch.empty(logits.shape[0], dtype=torch.int32, device=logits.device)
-        if lps and "lps" not in o:
-            o["lps"] = torch.empty(logits.shape[0], dtype=torch.float32, device=logits.device)
-    strata_draw_rows(logits, u, o["ids"], temperature, top_k, top_p, min_p, o.get("lps"), V, stream)
-    return o
+    if stream is not None:
+        with _side(stream, logits):
+            return draw_rows(logits, u, temperature, top_k, top_p, min_p, V, lps, None, out)
+    return _done(_draw(logits, u, temperature, top_k, top_p, min_p, V, True, bool(lps), {} if out is None else out, None))
 
 
 def tail_errors(stream=None) -> int:
