@@ -39,7 +39,7 @@ extern "C" {
  *   h = x + residual            (32 bits; residual NULL: h = x)
  *   y = h * rsqrt(mean(h * h) + eps) * weight
  * and writes what has a pointer: residual_out = h and y, rounded to `dtype` (x's, the residual's and
- * the weight's: F32 or BF16), and the 8-bit row q = e4m3(y / scale) with
+ * the weight's: F32 or BF16), and the 8-bit row q = e4m3(y * (1 / scale)) with
  * scale = max(max|y| / 448, 2^-100), computed from y in 32 bits, before any rounding.
  * Strides count elements; rows may be any distance >= H apart and need only their element's
  * alignment (rows that start on 16 bytes run faster).  residual_out may be the residual or x

@@ -1,6 +1,8 @@
 // strata_tail.cu -- host side of strata_norm_rows and strata_draw_rows (include/strata_tail.h).
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "../../include/strata_tail.h"
 #include "strata_draw.cuh"
 #include "strata_host.h"
@@ -17,9 +19,40 @@ static_assert(STRATA_MAX_VOCAB * 4 / strata::DRAW_MAX_CLUSTER + sizeof(strata::D
 
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
-int launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+// The shape of a call.  Many rows are bound by HBM: a thread takes up to four packs, so that enough
+// bytes are on their way, as long as that leaves no lane of a warp without any (T=5000, H=4096, 22.7 us
+// with four and 22.8 with two; T=8000, H=301, 8.7 with four and 6.3 with two).  Few rows are bound by
+// latency: a row goes to as many threads as it has packs.
+template <typename E, int N, int PER, bool SHIFT>
+bool launch_norm(const strata::NormArgs& A, int least, cudaStream_t s) {
+  if constexpr (PER <= (N == 1 ? 16 : 4)) {
+    const int packs = (A.H + N - 1) / N, need = std::max((packs + PER - 1) / PER, SHIFT ? 2 * (N - 1) : 1);
+    if (PER >= least && need <= strata::norm_most_threads(N, PER)) {
+      if (need <= 32) {
+        constexpr int ROWS = 4;
+        strata::norm_kernel<E, N, PER, false, SHIFT><<<(A.T + ROWS - 1) / ROWS, 32 * ROWS, 0, s>>>(A);
+      } else {
+        strata::norm_kernel<E, N, PER, true, SHIFT><<<A.T, (need + 31) / 32 * 32, 0, s>>>(A);
+      }
+      return true;
+    }
+    return launch_norm<E, N, PER * 2, SHIFT>(A, least, s);
+  } else {
+    return false;
+  }
+}
+
+// `packed`: all rows lie on 16 bytes; `alike`: they lie anywhere, but all tensors the same way.
+template <typename E>
+cudaError_t launch_norm(const strata::NormArgs& A, bool packed, bool alike, int sms, cudaStream_t s) {
+  constexpr int N = 16 / static_cast<int>(sizeof(E));
+  const int packs = A.H / (packed || alike ? N : 1);
+  const int least = A.T < 2 * sms ? 1 : packs >= 128 ? 4 : packs >= 64 ? 2 : 1;
+  if (!(packed  ? launch_norm<E, N, 1, false>(A, least, s)
+        : alike ? launch_norm<E, N, 1, true>(A, least, s)
+                : launch_norm<E, 1, 1, false>(A, least, s)))
+    strata::norm_wide_kernel<E><<<A.T, 1024, 0, s>>>(A);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -44,11 +77,23 @@ extern "C" int strata_norm_rows(const void* x, int64_t ldx, const void* residual
     return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
   strata::NormArgs A{x, residual, weight, residual_out, y, q, scale, ldx, ldr, ldro, ldy, ldq, T, H, eps};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == STRATA_DTYPE_F32)
-    strata::norm_kernel<float><<<T, strata::NORM_THREADS, 0, s>>>(A);
-  else
-    strata::norm_kernel<__nv_bfloat16><<<T, strata::NORM_THREADS, 0, s>>>(A);
-  return launched("strata_norm_rows");
+  uint32_t* errors = nullptr;
+  int sms = 0;
+  if (const int rc = strata::tail_device(&errors, &sms); rc != STRATA_OK) return rc;
+  // 16 bytes at a time where the width, every stride and every address allow it
+  const int64_t n = 16 / static_cast<int64_t>(esz);
+  auto fits = [&](const void* p, int64_t ld, int64_t size) {
+    return p == nullptr || ((reinterpret_cast<uintptr_t>(p) % (n * size)) == 0 && (T == 1 || ld % n == 0));
+  };
+  const bool packed = H % n == 0 && fits(x, ldx, esz) && fits(residual, ldr, esz) && fits(weight, 0, esz) &&
+                      fits(residual_out, ldro, esz) && fits(y, ldy, esz) && fits(q, ldq, 1);
+  auto like_x = [&](const void* p, int64_t ld) {
+    return p == nullptr || ((reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(x)) % 16 == 0 && (T == 1 || (ld - ldx) % n == 0));
+  };
+  const bool alike = like_x(residual, ldr) && like_x(residual_out, ldro) && like_x(y, ldy);
+  const cudaError_t e = dtype == STRATA_DTYPE_F32 ? launch_norm<float>(A, packed, alike, sms, s)
+                                                  : launch_norm<__nv_bfloat16>(A, packed, alike, sms, s);
+  return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_norm_rows: %s", cudaGetErrorString(e));
 }
 
 extern "C" int strata_draw_rows(const void* logits, int dtype, int B, int V, int64_t ld, const float* u,
