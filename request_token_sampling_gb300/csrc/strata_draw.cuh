@@ -7,10 +7,12 @@
 // depend on the order or the split it was made in.
 //
 // A cluster of blocks holds one row in its shared memory, so the row is read from HBM once and every
-// further step runs on chip.  Its blocks count the row into 2048 equal steps of distance from the
-// largest logit.  Where the counts show that what the cuts leave is among at most DRAW_LIST entries
-// (the usual case), those go to the first block, which orders them and finishes alone.  Otherwise the
-// cluster narrows K down by counts (top_k) or weights (top_p), a range of keys at a time.
+// further step runs on chip.  The usual cuts leave few entries.  Each thread's largest logit shows where
+// they end: the bin in which the threads' maxima are k, or weigh top_p's share, has all that the cuts can
+// reach above it.  The entries up to there (a list of at most DRAW_LIST) go to the first block, which
+// orders them and finishes alone.  Where they are more, the cluster counts or weighs the whole row into
+// 2048 equal steps of distance from the largest logit, and orders the entries of the step that a cut
+// falls into.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,6 +42,7 @@ constexpr int DRAW_BINS = 2048;
 constexpr int DRAW_PER_THREAD = DRAW_BINS / DRAW_THREADS;
 constexpr float DRAW_STEPS = 64.0f;     // bins per unit of logit: 32 units, beyond which a weight is 0
 constexpr int DRAW_LIST = 2048;
+constexpr int DRAW_COARSE = DRAW_THREADS;  // bins of the threads' maxima, a quarter as fine
 constexpr int DRAW_PIECES = 4;          // parts a block's ids arrive in
 constexpr int DRAW_MAX_CLUSTER = 16;
 constexpr float DRAW_ONE = 0x1p43f;     // V <= 2^19 weights of at most 2^43 sum below 2^63
@@ -83,20 +86,25 @@ __device__ __forceinline__ uint32_t draw_ld_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ u64 draw_ld_u64(uint32_t addr) {
-  u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void draw_ld_v4(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void dsmem_st_u64(uint32_t addr, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
 struct DrawShared {
   uint64_t bars[DRAW_PIECES];
-  u64 slot[2][2];            // what this block tells the others: two values, two turns
+  u64 slot[2][2][DRAW_MAX_CLUSTER];  // what each block told: two turns of two values
   u64 warp[DRAW_WARPS];
   u64 found;
   uint32_t listed;           // entries in the first block's list
-  uint32_t lo[DRAW_BINS];    // counts, or the lower and upper halves of 64-bit sums
-  uint32_t hi[DRAW_BINS];
+  alignas(16) uint32_t lo[DRAW_BINS];  // the lower and upper halves of the bins' sums
+  alignas(16) uint32_t hi[DRAW_BINS];
+  uint32_t count[DRAW_COARSE];
   u64 list[DRAW_LIST];       // key << 32 | ~index: the order of the chain, descending
 };
 
@@ -128,19 +136,20 @@ struct DrawRow {
     for (int v = threadIdx.x; v < vecs; v += DRAW_THREADS) vec(v, f);
   }
 
-  // Every block's pair of values to every block: `sum` and the sum over lower ranks, or the maximum.
-  __device__ void tell(u64 a, u64 b) {  // called by one thread, before meet()
-    sh->slot[turn & 1][0] = a;
-    sh->slot[turn & 1][1] = b;
+  // Two values of each block to all blocks of the row: tell() by one warp, meet(), heard().  A block reads
+  // its own shared memory only, so the others may end.
+  __device__ void tell(u64 a, u64 b) {
+    if (static_cast<uint32_t>(lane) < ranks) {
+      dsmem_st_u64(dsmem_addr(smem_u32(&sh->slot[turn & 1][0][rank]), lane), a);
+      dsmem_st_u64(dsmem_addr(smem_u32(&sh->slot[turn & 1][1][rank]), lane), b);
+    }
   }
   __device__ void meet() {
     cluster_arrive();
     cluster_wait();
     ++turn;
   }
-  __device__ u64 heard(int which, uint32_t from) const {
-    return draw_ld_u64(dsmem_addr(smem_u32(&sh->slot[(turn + 1) & 1][which]), from));
-  }
+  __device__ u64 heard(int which, uint32_t from) const { return sh->slot[(turn + 1) & 1][which][from]; }
   __device__ u64 heard_sum(int which, u64* before = nullptr) const {
     const u64 v = static_cast<uint32_t>(lane) < ranks ? heard(which, lane) : 0;
     if (before != nullptr) *before = draw_warp_sum(static_cast<uint32_t>(lane) < rank ? v : 0);
@@ -161,7 +170,7 @@ struct DrawRow {
     __syncthreads();
     if (warp == 0) {
       s = draw_warp_sum(lane < DRAW_WARPS ? sh->warp[lane] : 0);
-      if (lane == 0) tell(s, 0);
+      tell(s, 0);
     }
     meet();
     return heard_sum(0, before);
@@ -169,7 +178,7 @@ struct DrawRow {
   // After parts(f): the first index whose running sum exceeds `target` (< the row's sum), to all blocks.
   template <typename F>
   __device__ int find(F f, u64 target, u64 before) {
-    if (threadIdx.x == 0) tell(0, 0);
+    if (threadIdx.x == 0) sh->found = 0;
     __syncthreads();
     for (int w = 0; w < warp; ++w) before += sh->warp[w];
     if (before <= target && target - before < sh->warp[warp]) {
@@ -188,13 +197,15 @@ struct DrawRow {
               run += f(base + i, x);
               if (at < 0 && run > target) at = base + i;
             });
-            tell(static_cast<u64>(at) + 1, 0);
+            sh->found = static_cast<u64>(at) + 1;
           }
           break;
         }
         before += __shfl_sync(0xFFFFFFFFu, upto, 31);
       }
     }
+    __syncthreads();
+    if (warp == 0) tell(sh->found, 0);
     meet();
     return static_cast<int>(heard_sum(0)) - 1;
   }
@@ -212,17 +223,16 @@ struct DrawRow {
     if (h) atomicAdd(&sh->hi[b], h);
   }
   // After a meet(): the cluster's sums of this thread's bins, and over all lower bins.
-  __device__ u64 all_bins(u64 (&v)[DRAW_PER_THREAD], bool wide) {
+  __device__ u64 all_bins(u64 (&v)[DRAW_PER_THREAD]) {
+    static_assert(DRAW_PER_THREAD == 4, "16-byte loads");
 #pragma unroll
     for (int i = 0; i < DRAW_PER_THREAD; ++i) v[i] = 0;
     for (uint32_t q = 0; q < ranks; ++q) {
-      const uint32_t l = dsmem_addr(smem_u32(&sh->lo[threadIdx.x * DRAW_PER_THREAD]), q);
-      const uint32_t h = dsmem_addr(smem_u32(&sh->hi[threadIdx.x * DRAW_PER_THREAD]), q);
+      uint32_t l[4], h[4];
+      draw_ld_v4(dsmem_addr(smem_u32(&sh->lo[threadIdx.x * 4]), q), l);
+      draw_ld_v4(dsmem_addr(smem_u32(&sh->hi[threadIdx.x * 4]), q), h);
 #pragma unroll
-      for (int i = 0; i < DRAW_PER_THREAD; ++i) {
-        v[i] += draw_ld_u32(l + 4 * i);
-        if (wide) v[i] += static_cast<u64>(draw_ld_u32(h + 4 * i)) << 32;
-      }
+      for (int i = 0; i < 4; ++i) v[i] += static_cast<u64>(h[i]) << 32 | l[i];
     }
     u64 s = 0;
 #pragma unroll
@@ -272,7 +282,7 @@ struct DrawRow {
     });
     __syncthreads();
     meet();
-    u64 below = all_bins(v, true), under;
+    u64 below = all_bins(v), under;
     int b = cross(v, below, target, &under);
     over += under;
     // the least and the greatest key in there
@@ -289,7 +299,7 @@ struct DrawRow {
     __syncthreads();
     if (lane == 0) sh->warp[warp] = static_cast<u64>(lo) << 32 | hi;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (warp == 0) {
       for (int w = 0; w < DRAW_WARPS; ++w) {
         lo = min(lo, static_cast<uint32_t>(sh->warp[w] >> 32));
         hi = max(hi, static_cast<uint32_t>(sh->warp[w]));
@@ -311,7 +321,7 @@ struct DrawRow {
       });
       __syncthreads();
       meet();
-      below = all_bins(v, true);
+      below = all_bins(v);
       b = cross(v, below, target - over, &under);
       over += under;
       const uint32_t width = 1u << shift, from = hi - (static_cast<uint32_t>(b) << shift);
@@ -347,6 +357,86 @@ struct DrawRow {
       }
     }
   }
+
+  // Appends an entry to the first block's list (with the others of this warp that are here).
+  __device__ __forceinline__ void append(int i, float x) {
+    const uint32_t here = __activemask(), first = __ffs(here) - 1;
+    uint32_t at = 0;
+    if (static_cast<uint32_t>(lane) == first) at = dsmem_atomic_add(dsmem_addr(smem_u32(&sh->listed), 0), __popc(here));
+    at = __shfl_sync(here, at, first) + __popc(here & ((1u << lane) - 1u));
+    if (at < DRAW_LIST)
+      dsmem_st_v2(dsmem_addr(smem_u32(&sh->list[0]), 0) + 8 * at, ~static_cast<uint32_t>(base + i), draw_key(x));
+  }
+  // The block's sum of one value per thread, to thread 0 of warp 0 at least.
+  __device__ u64 block_sum(u64 v) {
+    v = draw_warp_sum(v);
+    __syncthreads();
+    if (lane == 0) sh->warp[warp] = v;
+    __syncthreads();
+    return draw_warp_sum(lane < DRAW_WARPS ? sh->warp[lane] : 0);
+  }
+
+  // The cut that leaves sum(f) >= target, 1 <= target <= the row's sum, with as few entries as can be:
+  // the last of them.  f is 0 for what earlier cuts took.
+  template <typename F>
+  __device__ void narrow(F f, float top, u64 target, uint32_t* K, int* I) {
+    meet();  // the bins and the list of the step before are read
+    if (threadIdx.x == 0) sh->listed = 0;
+    clear_bins();
+    each([&](int i, float x) {
+      const u64 w = f(base + i, x);
+      if (w) add_bin(bin(x, top), w);
+    });
+    __syncthreads();
+    meet();
+    u64 v[DRAW_PER_THREAD], under;
+    const u64 below = all_bins(v);
+    const int b = cross(v, below, target, &under);
+    u64 mine = 0;
+    each([&](int i, float x) {
+      if (bin(x, top) == b && f(base + i, x)) {
+        append(i, x);
+        ++mine;
+      }
+    });
+    mine = block_sum(mine);
+    if (warp == 0) tell(mine, 0);
+    meet();
+    const u64 entries = heard_sum(0);
+    if (entries > DRAW_LIST) {  // a great many alike
+      u64 above;
+      const uint32_t key = select(f, top, target, &above);
+      const u64 one = f(-1, draw_val(key));
+      auto same = [&](int i, float x) -> u64 { return draw_key(x) == key && f(i, x); };
+      u64 before;
+      parts(same, &before);
+      *I = find(same, (target - above + one - 1) / one - 1, before);
+      *K = key;
+      return;
+    }
+    if (rank == 0) {
+      sort(static_cast<int>(entries));
+      constexpr int PER = DRAW_LIST / DRAW_THREADS;
+      u64 w[PER], s = 0;
+      for (int i = 0; i < PER; ++i) {
+        const int at = static_cast<int>(threadIdx.x) * PER + i;
+        const u64 e = at < static_cast<int>(entries) ? sh->list[at] : 0;
+        w[i] = e ? f(static_cast<int>(~static_cast<uint32_t>(e)), draw_val(static_cast<uint32_t>(e >> 32))) : 0;
+        s += w[i];
+      }
+      u64 run = under + block_scan(s) - s;
+      for (int i = 0; i < PER; ++i) {
+        if (run < target && run + w[i] >= target) sh->found = sh->list[threadIdx.x * PER + i];
+        run += w[i];
+      }
+      __syncthreads();
+      if (warp == 0) tell(sh->found, 0);
+    }
+    meet();
+    const u64 e = heard(0, 0);
+    *K = static_cast<uint32_t>(e >> 32);
+    *I = static_cast<int>(~static_cast<uint32_t>(e));
+  }
 };
 
 template <typename E>
@@ -369,6 +459,8 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   R.vecs = (n + VEC - 1) / VEC;
   const E* from = static_cast<const E*>(A.logits) + row * A.ld + R.base;
 
+  cluster_arrive_relaxed();  // this block runs: its shared memory may be written by the others
+
   // The block's part of the row, in pieces; what does not fill 16 bytes by plain loads.
   const int whole = n / VEC, piece = (whole + DRAW_PIECES - 1) / DRAW_PIECES;
   if (threadIdx.x == 0) {
@@ -390,16 +482,20 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     else
       ids[i] = i < n ? from[i] : __ushort_as_bfloat16(0x7FC0);
   }
+  for (int i = threadIdx.x; i < DRAW_COARSE; i += DRAW_THREADS) sh->count[i] = sh->lo[i] = sh->hi[i] = 0;
   const float T = A.temperature != nullptr ? A.temperature[row] : 1.0f;
   const float P = A.top_p != nullptr ? A.top_p[row] : 1.0f, m = A.min_p != nullptr ? A.min_p[row] : 0.0f;
   const int k = A.top_k != nullptr ? A.top_k[row] : 0;
   __syncthreads();
 
-  // The largest logit and its lowest index.
-  u64 best = 0;
+  // The thread's largest logit and its lowest index, then the row's.
+  float most = -INFINITY;
+  int most_at = -1;
   auto look = [&](int i, float x) {
-    const u64 e = static_cast<u64>(draw_key(x)) << 32 | static_cast<uint32_t>(~(R.base + i));
-    best = best < e ? e : best;
+    if (x > most) {  // not for NaN and -inf
+      most = x;
+      most_at = i;
+    }
   };
   for (int p = 0; p < DRAW_PIECES; ++p) {
     const int v0 = min(whole, p * piece), v1 = min(whole, v0 + piece);
@@ -414,12 +510,16 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     }
   }
   if (threadIdx.x == 0 && whole < R.vecs) R.vec(whole, look);
+  u64 best = most_at < 0 ? 0 : static_cast<u64>(draw_key(most)) << 32 | static_cast<uint32_t>(~(R.base + most_at));
   best = warp_max_u64(best);
   if (R.lane == 0) sh->warp[R.warp] = best;
   __syncthreads();
   if (R.warp == 0) {
     best = warp_max_u64(R.lane < DRAW_WARPS ? sh->warp[R.lane] : 0);
-    if (R.lane == 0) R.tell(best, 0);
+  }
+  cluster_wait();
+  if (R.warp == 0) {
+    R.tell(best, 0);
   }
   R.meet();
   best = warp_max_u64(static_cast<uint32_t>(R.lane) < R.ranks ? R.heard(0, R.lane) : 0);
@@ -438,7 +538,6 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     if (lead && threadIdx.x == 0)
       answer(top_key == NO_KEY ? -1 : static_cast<int>(~static_cast<uint32_t>(best)),
              top_key == NO_KEY ? __int_as_float(0x7FC00000) : 0.0f);
-    R.meet();  // nobody leaves while another block may still read its values
     return;
   }
   const float inv = 1.0f / T, u = A.u[row];
@@ -450,179 +549,129 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   int I = A.V - 1;
   auto left = [&](int i, uint32_t key) { return key > K || (key == K && i <= I); };
 
-  if (k_on || p_on) {
-    R.clear_bins();
+  auto flat = [&](float x) { return draw_weight(x == top ? 0.0f : x - top); };  // at temperature 1
+  bool try_list = k_on ? k <= DRAW_LIST / 2 : p_on;
+  if (try_list) {
+    // What top_k alone leaves, or (without it) what min_p leaves and top_p weighs, from the threads' maxima.
     u64 mass = 0;
-    const bool need_mass = p_on && !k_on;
-    const bool all = !k_on;  // top_k counts every entry, top_p those that min_p left
-    R.each([&](int, float x) {
-      if (!(x > -INFINITY) || (all && !(x >= least))) return;
-      atomicAdd(&sh->lo[DrawRow<E>::bin(x, top)], 1u);
-      if (need_mass) mass += draw_weight(x == top ? 0.0f : x - top);
-    });
-    mass = draw_warp_sum(mass);
-    __syncthreads();
-    if (R.lane == 0) sh->warp[R.warp] = mass;
-    __syncthreads();
-    if (R.warp == 0) {
-      mass = draw_warp_sum(R.lane < DRAW_WARPS ? sh->warp[R.lane] : 0);
-      if (R.lane == 0) R.tell(mass, 0);
+    if (!k_on) {
+      R.each([&](int, float x) { mass += x >= least && x > -INFINITY ? flat(x) : 0; });
+      mass = R.block_sum(mass);
+      if (R.warp == 0) R.tell(mass, 0);
+    }
+    if (most_at >= 0) {
+      const int b = DrawRow<E>::bin(most, top) / (DRAW_BINS / DRAW_COARSE);
+      atomicAdd(&sh->count[b], 1u);
+      if (!k_on && most >= least) R.add_bin(b, flat(most));
     }
     R.meet();
-    mass = R.heard_sum(0);
-    u64 v[DRAW_PER_THREAD];
-    const u64 below = R.all_bins(v, false);
-    // the last bin that the cuts can reach into
-    int cut = DRAW_BINS - 1;
-    bool whole_set = true;  // the bins up to `cut` hold all that top_k and min_p leave
-    if (k_on) {
-      const int b = R.cross(v, below, k, nullptr);
-      if (b < DRAW_BINS) cut = b;
+    u64 v = 0, w = 0;
+    for (uint32_t q = 0; q < R.ranks; ++q) {
+      v += draw_ld_u32(dsmem_addr(smem_u32(&sh->count[threadIdx.x]), q));
+      if (!k_on)
+        w += static_cast<u64>(draw_ld_u32(dsmem_addr(smem_u32(&sh->hi[threadIdx.x]), q))) << 32 |
+             draw_ld_u32(dsmem_addr(smem_u32(&sh->lo[threadIdx.x]), q));
     }
-    if (!(m <= 0.0f)) cut = min(cut, DrawRow<E>::bin(least, top));
-    auto count_to = [&](int b) {
-      __syncthreads();
-      u64 run = below;
-      for (int i = 0; i < DRAW_PER_THREAD; ++i) {
-        run += v[i];
-        if (static_cast<int>(threadIdx.x) * DRAW_PER_THREAD + i == b) sh->found = run;
+    // the first bin by which the maxima are k or weigh the share; without one, the last with few maxima
+    const u64 target = k_on ? static_cast<u64>(k) : draw_share(p24, mass = R.heard_sum(0));
+    const u64 upto = R.block_scan(v), reach = k_on ? upto : R.block_scan(w);
+    __syncthreads();
+    if (threadIdx.x == 0) sh->found = 0;
+    __syncthreads();
+    if (reach - (k_on ? v : w) < target && reach >= target) sh->found = static_cast<u64>(threadIdx.x) + 1;
+    __syncthreads();
+    int cut = static_cast<int>(sh->found) - 1;
+    if (cut < 0) cut = __syncthreads_count(upto <= DRAW_LIST / 4) - 1;
+    const float width = static_cast<float>(cut + 1) * (DRAW_BINS / DRAW_COARSE) / DRAW_STEPS;
+    const bool rest = cut >= DRAW_COARSE - 1;  // the last bin holds everything further away
+    u64 mine = 0, listed_mass = 0;
+    R.each([&](int i, float x) {
+      if (x > -INFINITY && x >= least && (rest || x == top || top - x < width)) {
+        R.append(i, x);
+        ++mine;
+        if (!k_on) listed_mass += flat(x);
       }
-      __syncthreads();
-      return sh->found;
-    };
-    u64 entries = count_to(cut);
-    const u64 target_all = draw_share(p24, mass);
-    if (entries > DRAW_LIST && need_mass) {
-      // a lower bound of the bins' weights: enough of them to reach top_p's share for certain
-      u64 lower[DRAW_PER_THREAD], s = 0;
-      for (int i = 0; i < DRAW_PER_THREAD; ++i) {
-        const float edge = -static_cast<float>(threadIdx.x * DRAW_PER_THREAD + i + 1) / DRAW_STEPS;
-        lower[i] = v[i] * __float2ull_rz(expf(edge) * (DRAW_ONE * (1.0f - 0x1p-18f)));
-        s += lower[i];
-      }
-      const u64 under = R.block_scan(s) - s;
-      const int b = R.cross(lower, under, target_all, nullptr);
-      if (b < cut) {
-        cut = b;
-        whole_set = false;
-        entries = count_to(cut);
-      }
-    }
-    if (entries <= DRAW_LIST) {
-      // to the first block's list, in any order
-      const uint32_t there = dsmem_addr(smem_u32(&sh->list[0]), 0), counter = dsmem_addr(smem_u32(&sh->listed), 0);
-      R.each([&](int i, float x) {
-        if (x > -INFINITY && DrawRow<E>::bin(x, top) <= cut && (!all || x >= least)) {
-          const uint32_t here = __activemask(), first = __ffs(here) - 1;  // one addition for these lanes
-          uint32_t at = 0;
-          if (static_cast<uint32_t>(R.lane) == first) at = dsmem_atomic_add(counter, __popc(here));
-          at = __shfl_sync(here, at, first) + __popc(here & ((1u << R.lane) - 1u));
-          if (at < DRAW_LIST) dsmem_st_v2(there + 8 * at, ~static_cast<uint32_t>(R.base + i), draw_key(x));
-        }
-      });
-      R.meet();
+    });
+    mine = R.block_sum(mine);
+    if (!k_on) listed_mass = R.block_sum(listed_mass);
+    if (R.warp == 0) R.tell(mine, listed_mass);
+    R.meet();
+    const u64 entries = R.heard_sum(0);
+    // top_k needs the bin of the k-th maximum, top_p its share: else the row is narrowed down as a whole
+    try_list = entries <= DRAW_LIST && (k_on ? sh->found != 0 || rest : R.heard_sum(1) >= target);
+    if (try_list) {
       if (!lead) return;
-      const int listed = min(static_cast<int>(sh->listed), DRAW_LIST);
+      const int listed = static_cast<int>(entries);
       R.sort(listed);
-      // top_k is the list's length now, min_p a key, top_p a running sum
       int kept = k_on ? min(k, listed) : listed;
-      {
-        int mine = 0;
-        for (int i = threadIdx.x; i < kept; i += DRAW_THREADS) mine += draw_val(sh->list[i] >> 32) >= least;
-        mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-        __syncthreads();
-        if (R.lane == 0) sh->warp[R.warp] = mine;
-        __syncthreads();
-        kept = 0;
-        for (int w = 0; w < DRAW_WARPS; ++w) kept += static_cast<int>(sh->warp[w]);
-      }
       constexpr int PER = DRAW_LIST / DRAW_THREADS;
-      auto sums = [&](int count, auto weight, u64 (&w)[PER], u64* sum) {  // each thread PER entries in a row
+      u64 ws[PER], sum;
+      auto sums = [&](int count, auto weight) {  // each thread PER entries in a row; what comes before them
         u64 s = 0;
+#pragma unroll
         for (int i = 0; i < PER; ++i) {
           const int at = static_cast<int>(threadIdx.x) * PER + i;
-          w[i] = at < count ? weight(sh->list[at]) : 0;
-          s += w[i];
+          ws[i] = at < count ? weight(sh->list[at]) : 0;
+          s += ws[i];
         }
         const u64 upto = R.block_scan(s);
-        u64 whole = 0;
-        for (int q = 0; q < DRAW_WARPS; ++q) whole += sh->warp[q];
-        *sum = whole;
+        sum = 0;
+        for (int q = 0; q < DRAW_WARPS; ++q) sum = sh->warp[q] + sum;
         return upto - s;
       };
-      u64 w[PER], sum;
       if (p_on) {
-        u64 run = sums(kept, [&](u64 e) { const float x = draw_val(e >> 32); return draw_weight(x == top ? 0.0f : x - top); }, w, &sum);
-        const u64 target = whole_set ? draw_share(p24, sum) : target_all;
-        int mine = 0;
+        u64 run = sums(kept, [&](u64 e) { return flat(draw_val(static_cast<uint32_t>(e >> 32))); });
+        const u64 share = k_on ? draw_share(p24, sum) : target;
+        u64 under = 0;
+#pragma unroll
         for (int i = 0; i < PER; ++i) {
           const int at = static_cast<int>(threadIdx.x) * PER + i;
-          mine += at < kept && (at == 0 || run < target);
-          run += w[i];
+          under += at < kept && (at == 0 || run < share);
+          run += ws[i];
         }
-        mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-        __syncthreads();
-        if (R.lane == 0) sh->warp[R.warp] = mine;
-        __syncthreads();
-        kept = 0;
-        for (int q = 0; q < DRAW_WARPS; ++q) kept += static_cast<int>(sh->warp[q]);
+        kept = static_cast<int>(R.block_sum(under));
       }
       // index order: swap the halves, so that the greatest ~index comes first
       __syncthreads();
       for (int i = threadIdx.x; i < kept; i += DRAW_THREADS) sh->list[i] = sh->list[i] << 32 | sh->list[i] >> 32;
       __syncthreads();
       R.sort(kept);
-      u64 run = sums(kept, [&](u64 e) { return draw_weight(tempered(draw_val(static_cast<uint32_t>(e)))); }, w, &sum);
-      const u64 target = draw_share(u24, sum);
+      u64 run = sums(kept, [&](u64 e) { return draw_weight(tempered(draw_val(static_cast<uint32_t>(e)))); });
+      const u64 draw = draw_share(u24, sum);
+#pragma unroll
       for (int i = 0; i < PER; ++i) {
-        if (run <= target && run + w[i] > target) {
+        if (run <= draw && run + ws[i] > draw) {
           const u64 e = sh->list[threadIdx.x * PER + i];
           answer(static_cast<int>(~static_cast<uint32_t>(e >> 32)),
                  tempered(draw_val(static_cast<uint32_t>(e))) - logf(static_cast<float>(sum) * (1.0f / DRAW_ONE)));
         }
-        run += w[i];
+        run += ws[i];
       }
       return;
     }
-    // Too many: narrow K down over the whole row.
-    auto keep_first = [&](uint32_t key, u64 ties) {  // keeps the first `ties` (>= 1) of what is left at `key`
-      const uint32_t k0 = K;
-      const int i0 = I;
-      auto f = [&](int i, float x) -> u64 {
-        const uint32_t kk = draw_key(x);
-        return kk == key && (kk > k0 || i <= i0);
-      };
-      u64 before;
-      R.parts(f, &before);
-      I = R.find(f, ties - 1, before);
-      K = key;
-    };
-    if (k_on) {
-      const uint32_t least_key = K;
-      K = 1;
-      auto f = [&](int, float x) -> u64 { return x > -INFINITY; };
-      u64 before;
-      if (static_cast<u64>(k) < R.parts(f, &before)) {
-        u64 above;
-        const uint32_t key = R.select(f, top, k, &above);
-        keep_first(key, k - above);
-      }
+  }
+  if (k_on) {
+    auto f = [&](int, float x) -> u64 { return x > -INFINITY; };
+    u64 before;
+    const uint32_t least_key = K;
+    if (static_cast<u64>(k) < R.parts(f, &before)) {
+      R.narrow(f, top, k, &K, &I);
       if (least_key > K) {
         K = least_key;
         I = A.V - 1;
       }
     }
-    if (p_on) {
-      auto f = [&](int i, float x) -> u64 {
-        return left(i, draw_key(x)) ? draw_weight(x == top ? 0.0f : x - top) : 0ull;
-      };
-      u64 before;
-      const u64 target = draw_share(p24, R.parts(f, &before));
-      u64 above;
-      const uint32_t key = R.select(f, top, target, &above);
-      const u64 one = draw_weight(key == top_key ? 0.0f : draw_val(key) - top);
-      keep_first(key, (target - above + one - 1) / one);
-    }
+  }
+  if (p_on) {
+    const uint32_t K0 = K;
+    const int I0 = I;
+    auto f = [&](int i, float x) -> u64 {
+      const uint32_t key = draw_key(x);
+      return key > K0 || (key == K0 && i <= I0) ? flat(x) : 0ull;
+    };
+    u64 before;
+    const u64 target = draw_share(p24, R.parts(f, &before));
+    R.narrow(f, top, target, &K, &I);
   }
   auto f = [&](int i, float x) -> u64 { return left(i, draw_key(x)) ? draw_weight(tempered(x)) : 0ull; };
   u64 before;
@@ -636,7 +685,6 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
       x = __bfloat162float(ids[at - R.base]);
     answer(at, tempered(x) - logf(static_cast<float>(all) * (1.0f / DRAW_ONE)));
   }
-  R.meet();
 }
 
 }  // namespace strata

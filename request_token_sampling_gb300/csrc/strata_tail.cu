@@ -20,8 +20,8 @@ static_assert(STRATA_MAX_VOCAB * 4 / strata::DRAW_MAX_CLUSTER + sizeof(strata::D
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 // The shape of a call.  Many rows are bound by HBM: a thread takes up to four packs, so that enough
-// bytes are on their way, as long as that leaves no lane of a warp without any (T=5000, H=4096, 22.7 us
-// with four and 22.8 with two; T=8000, H=301, 8.7 with four and 6.3 with two).  Few rows are bound by
+// bytes are on their way, but no more than put the row into one warp (T=8000, H=301: two packs and a warp
+// to a row 6.3 us, four 8.7, one and two warps 7.8).  Few rows are bound by
 // latency: a row goes to as many threads as it has packs.
 template <typename E, int N, int PER, bool SHIFT>
 bool launch_norm(const strata::NormArgs& A, int least, cudaStream_t s) {
@@ -47,7 +47,7 @@ template <typename E>
 cudaError_t launch_norm(const strata::NormArgs& A, bool packed, bool alike, int sms, cudaStream_t s) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   const int packs = A.H / (packed || alike ? N : 1);
-  const int least = A.T < 2 * sms ? 1 : packs >= 128 ? 4 : packs >= 64 ? 2 : 1;
+  const int least = A.T < 2 * sms ? 1 : packs > 64 ? 4 : packs > 32 ? 2 : 1;
   if (!(packed  ? launch_norm<E, N, 1, false>(A, least, s)
         : alike ? launch_norm<E, N, 1, true>(A, least, s)
                 : launch_norm<E, 1, 1, false>(A, least, s)))
