@@ -8,19 +8,24 @@
 //
 // A cluster of blocks holds one row in its shared memory, so the row is read from HBM once and every
 // further step runs on chip.
-//   top_k of up to DRAW_LIST / 2: the bin in which the threads' largest logits are k has all of the
-//     top_k at or above it.  The entries up to there (the list) go to the first block, which orders
-//     them and finishes alone.
+//   A small top_k: four threads' largest logit, from all blocks, show a threshold that has all of the top_k
+//     at or above it.  The entries up to there (the list) go to the first block, which orders them and
+//     finishes alone.
 //   top_p alone: the row is weighed into DRAW_BINS equal steps of distance from the largest logit.  Few
 //     entries up to the step that top_p falls into: a list, as above.  Many: only that step's entries
 //     are listed and ordered, which gives K and I.
 //   a larger top_k: K and I the same way, from counts.
 // What K and I leave is summed by contiguous parts, and the part that the random number falls into is
 // summed again entry by entry.
+//
+// Reading another block's shared memory runs at about 16 bytes a cycle for an SM and an exchange of two
+// values takes about 700 cycles (measured), so the blocks' bins are summed by shares and what all need
+// to know is pushed.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "strata_device.cuh"
@@ -43,9 +48,9 @@ using u64 = unsigned long long;
 constexpr int DRAW_THREADS = 512;
 constexpr int DRAW_WARPS = DRAW_THREADS / 32;
 constexpr int DRAW_BINS = 2048;
-constexpr int DRAW_PER_THREAD = DRAW_BINS / DRAW_THREADS;
 constexpr float DRAW_STEPS = 64.0f;     // bins per unit of logit: 32 units, beyond which a weight is 0
-constexpr int DRAW_COARSE = DRAW_THREADS;  // bins of the threads' maxima, a quarter as fine
+constexpr int DRAW_COARSE = DRAW_THREADS;  // bins of the maxima, a quarter as fine
+constexpr int DRAW_MAXIMA = DRAW_THREADS / 4;  // of a block: the largest logit of each four threads
 constexpr int DRAW_LIST = 2048;
 constexpr int DRAW_PIECES = 4;          // parts a block's ids arrive in
 constexpr int DRAW_MAX_CLUSTER = 16;
@@ -66,10 +71,13 @@ __device__ __forceinline__ float draw_val(uint32_t k) {
 // rate).  2^19 weights of at most 2^43 sum below 2^63.
 __device__ __forceinline__ u64 draw_weight(float dt) {
   const uint32_t e = __float_as_uint(expf(dt));
-  const int s = static_cast<int>(e >> 23) - 107;  // of a unit in the last place of the 24 bits
-  const uint32_t up = static_cast<uint32_t>(max(s, 0)), down = static_cast<uint32_t>(min(max(-s, 0), 31));
-  const uint32_t m = ((e & 0x7FFFFFu) | 0x800000u) >> down;
-  return static_cast<u64>(__funnelshift_l(m, 0u, up)) << 32 | (m << up);
+  const uint32_t s = (e >> 23) - 107u;  // of a unit in the last place of the 24 bits; negative: downwards
+  const uint32_t m = (e & 0x7FFFFFu) | 0x800000u;
+  uint32_t up, down, hi;  // a shift by 32 or more (a negative one too) gives 0
+  asm("shl.b32 %0, %1, %2;" : "=r"(up) : "r"(m), "r"(s));
+  asm("shr.u32 %0, %1, %2;" : "=r"(down) : "r"(m), "r"(0u - s));
+  asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(m), "r"(32u - s));
+  return static_cast<u64>(hi) << 32 | (up | down);
 }
 constexpr float DRAW_UNIT = 0x1p-43f;
 // floor(of * total / 2^24) for of <= 2^24 and total < 2^63
@@ -81,10 +89,11 @@ __device__ __forceinline__ u64 draw_warp_sum(u64 v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-__device__ __forceinline__ u64 draw_warp_scan(u64 v, int lane) {  // inclusive
+template <typename T>
+__device__ __forceinline__ T draw_warp_scan(T v, int lane) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const u64 up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    const T up = __shfl_up_sync(0xFFFFFFFFu, v, o);
     if (lane >= o) v += up;
   }
   return v;
@@ -94,27 +103,27 @@ __device__ __forceinline__ uint32_t draw_ld_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void draw_ld_v4(uint32_t addr, uint32_t (&v)[4]) {
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-               : "r"(addr)
-               : "memory");
-}
 __device__ __forceinline__ void dsmem_st_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
 struct DrawShared {
   uint64_t bars[DRAW_PIECES];
-  u64 slot[2][2][DRAW_MAX_CLUSTER];    // what each block told: two turns of two values
+  u64 slot[2][2][DRAW_MAX_CLUSTER];  // what each block told: two turns of two values
   u64 warp[DRAW_WARPS];
   u64 found, found_sum;
-  uint32_t listed;                     // entries in the first block's list
-  alignas(16) uint32_t lo[DRAW_BINS];  // the lower and upper halves of the bins' sums
-  alignas(16) uint32_t hi[DRAW_BINS];
-  uint32_t count[DRAW_COARSE];         // threads' maxima
-  u64 list[DRAW_LIST];                 // key << 32 | ~index: the order of the chain, descending
+  uint32_t listed;                   // entries in the first block's list
+  uint32_t local;                    // entries in this block's own
+  // Sums of bins in three parts of 15, 15 and 14 bits, so that 2^15 weights add up without a carry.
+  // Before: the maxima of all blocks (part 0) and their counts (part 2).  After: this block's own list.
+  union alignas(16) {
+    uint32_t part[3][DRAW_BINS];
+    u64 own[DRAW_LIST];
+  };
+  alignas(16) u64 list[DRAW_LIST];   // key << 32 | ~index: the order of the chain, descending
 };
+static_assert(offsetof(DrawShared, part) % 16 == 0 && offsetof(DrawShared, list) % 16 == 0, "16-byte accesses");
+static_assert(DRAW_MAXIMA * DRAW_MAX_CLUSTER <= DRAW_BINS, "the maxima fit part 0");
 
 template <typename E>
 struct DrawRow {
@@ -174,14 +183,17 @@ struct DrawRow {
     return draw_warp_sum(lane < DRAW_WARPS ? sh->warp[lane] : 0);
   }
   // Inclusive sum over the block's threads, and the whole sum.
-  __device__ u64 block_scan(u64 s, u64* all = nullptr) {
-    const u64 upto = draw_warp_scan(s, lane);
+  template <typename T>
+  __device__ T block_scan(T s, T* all = nullptr) {
+    const T upto = draw_warp_scan(s, lane);
+    T* to = reinterpret_cast<T*>(sh->warp);
     __syncthreads();
-    if (lane == 31) sh->warp[warp] = upto;
+    if (lane == 31) to[warp] = upto;
     __syncthreads();
-    const u64 w = lane < DRAW_WARPS ? sh->warp[lane] : 0;
-    if (all != nullptr) *all = draw_warp_sum(w);
-    return draw_warp_sum(lane < warp ? w : 0) + upto;
+    const T w = draw_warp_scan(lane < DRAW_WARPS ? to[lane] : T(0), lane);
+    const T below = __shfl_sync(0xFFFFFFFFu, w, max(warp - 1, 0));
+    if (all != nullptr) *all = __shfl_sync(0xFFFFFFFFu, w, DRAW_WARPS - 1);
+    return upto + (warp > 0 ? below : T(0));
   }
 
   // Sums f over the row by contiguous parts, one to a warp (sh->warp holds this block's): the row's
@@ -241,77 +253,93 @@ struct DrawRow {
     return b >= DRAW_BINS ? -3.402823466e38f : fmaxf(-3.402823466e38f, top - b * (1.0001f / DRAW_STEPS));
   }
 
-  __device__ void clear_bins() {
-    for (int b = threadIdx.x; b < DRAW_BINS / 4; b += DRAW_THREADS)
-      reinterpret_cast<uint4*>(sh->lo)[b] = reinterpret_cast<uint4*>(sh->hi)[b] = make_uint4(0, 0, 0, 0);
+  // Sums f over the row into bins at(x) and adds the blocks' bins up, each block a share of them: the row's
+  // sum.  cross() then finds the first bin whose inclusive sum reaches `target` >= 1 (one does), and the
+  // sum below it.
+  struct Bins {
+    u64 v[4], below;  // this thread's bins (one to four in a row) and what lies before them
+  };
+  template <typename F, typename At>
+  __device__ u64 weigh(F f, At at, Bins* bins) {
     __syncthreads();
-  }
-  // 64-bit addition from two 32-bit ones: the carry is known from the old lower half, whatever the order.
-  __device__ __forceinline__ void add_bin(int b, u64 v) {
-    const uint32_t l = static_cast<uint32_t>(v);
-    uint32_t h = static_cast<uint32_t>(v >> 32);
-    const uint32_t old = atomicAdd(&sh->lo[b], l);
-    h += (old + l < old);
-    if (h) atomicAdd(&sh->hi[b], h);
-  }
-  // After a meet(): the cluster's sums of this thread's bins, over all lower bins, and over all.
-  __device__ u64 all_bins(u64 (&v)[DRAW_PER_THREAD], u64* all) {
-    static_assert(DRAW_PER_THREAD == 4, "16-byte loads");
+    for (int b = threadIdx.x; b < 3 * DRAW_BINS / 4; b += DRAW_THREADS)
+      reinterpret_cast<uint4*>(sh->part)[b] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    each([&](int i, float x) {
+      const u64 w = f(base + i, x);
+      if (w == 0) return;
+      const int b = at(x);
+      const uint32_t w0 = static_cast<uint32_t>(w) & 0x7FFFu, w1 = static_cast<uint32_t>(w >> 15) & 0x7FFFu,
+                     w2 = static_cast<uint32_t>(w >> 30);
+      atomicAdd(&sh->part[0][b], w0);
+      if (w1) atomicAdd(&sh->part[1][b], w1);
+      if (w2) atomicAdd(&sh->part[2][b], w2);
+    });
+    __syncthreads();
+    meet();
+    const int share = DRAW_BINS / static_cast<int>(ranks);  // 128 to 2048 bins
+    const int per = max(1, share / DRAW_THREADS), first = static_cast<int>(rank) * share;
+    u64 s = 0;
+    if (share >= DRAW_THREADS) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = 0;
-    const uint32_t lo = smem_u32(&sh->lo[threadIdx.x * 4]), hi = smem_u32(&sh->hi[threadIdx.x * 4]);
-    for (uint32_t q0 = 0; q0 < ranks; q0 += 4) {
-      uint32_t l[4][4], h[4][4];
-#pragma unroll
-      for (uint32_t q = 0; q < 4; ++q) {  // the loads of four blocks on their way at once
-        draw_ld_v4(dsmem_addr(lo, min(q0 + q, ranks - 1)), l[q]);
-        draw_ld_v4(dsmem_addr(hi, min(q0 + q, ranks - 1)), h[q]);
+      for (int i = 0; i < 4; ++i) {
+        bins->v[i] = 0;
+        if (i < per)
+          for (uint32_t q = 0; q < ranks; ++q) bins->v[i] += bin_of(first + threadIdx.x * per + i, q);
+        s += bins->v[i];
       }
+    } else {
+      // several threads to a bin, four blocks to each
+      const int b = threadIdx.x % share, group = threadIdx.x / share, groups = DRAW_THREADS / share;
 #pragma unroll
-      for (uint32_t q = 0; q < 4; ++q)
-        if (q0 + q < ranks)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += static_cast<u64>(h[q][i]) << 32 | l[q][i];
+      for (int q = 0; q < 4; ++q) s += bin_of(first + b, min(group * 4 + q, static_cast<int>(ranks) - 1));
+      __syncthreads();
+      sh->list[threadIdx.x] = s;  // nobody's list is in use
+      __syncthreads();
+      s = 0;
+      if (group == 0)
+        for (int g = 0; g < groups; ++g) s += sh->list[g * share + b];
+      bins->v[0] = s;
+      bins->v[1] = bins->v[2] = bins->v[3] = 0;
     }
-    const u64 s = v[0] + v[1] + v[2] + v[3];
-    return block_scan(s, all) - s;
+    u64 here, before;
+    const u64 upto = block_scan(s, &here);
+    if (warp == 0) tell(here, 0);
+    meet();
+    const u64 all = heard_sum(0, &before);
+    bins->below = before + upto - s;
+    return all;
   }
-  // The cluster's number of maxima in coarse bin `b`.
-  __device__ uint32_t all_maxima(int b) {
-    const uint32_t at = smem_u32(&sh->count[b]);
-    uint32_t s = 0;
-#pragma unroll
-    for (uint32_t q = 0; q < DRAW_MAX_CLUSTER; ++q) {
-      const uint32_t v = draw_ld_u32(dsmem_addr(at, min(q, ranks - 1)));
-      s += q < ranks ? v : 0;
-    }
-    return s;
+  __device__ __forceinline__ u64 bin_of(int b, uint32_t q) const {
+    const uint32_t at = dsmem_addr(smem_u32(&sh->part[0][b]), q);
+    return static_cast<u64>(draw_ld_u32(at)) + (static_cast<u64>(draw_ld_u32(at + 4 * DRAW_BINS)) << 15) +
+           (static_cast<u64>(draw_ld_u32(at + 8 * DRAW_BINS)) << 30);
   }
-  // The first of all bins whose inclusive sum reaches `target` >= 1 (DRAW_BINS: none), and the sum
-  // below it.  `below` and `v` as all_bins gave them.
-  __device__ int cross(const u64 (&v)[DRAW_PER_THREAD], u64 below, u64 target, u64* under) {
+  __device__ int cross(const Bins& bins, u64 target, u64* under) {
     __syncthreads();
-    if (threadIdx.x == 0) sh->found = DRAW_BINS;
+    if (threadIdx.x == 0) sh->found = sh->found_sum = 0;
     __syncthreads();
-    u64 run = below;
+    const int share = DRAW_BINS / static_cast<int>(ranks), per = max(1, share / DRAW_THREADS);
+    u64 run = bins.below;
 #pragma unroll
-    for (int i = 0; i < DRAW_PER_THREAD; ++i) {
-      if (run < target && run + v[i] >= target) {
-        sh->found = threadIdx.x * DRAW_PER_THREAD + i;
+    for (int i = 0; i < 4; ++i) {
+      if (run < target && run + bins.v[i] >= target) {
+        sh->found = static_cast<u64>(rank * share + threadIdx.x * per + i) + 1;
         sh->found_sum = run;
       }
-      run += v[i];
+      run += bins.v[i];
     }
     __syncthreads();
-    *under = sh->found_sum;
-    return static_cast<int>(sh->found);
+    if (warp == 0) tell(sh->found, sh->found_sum);
+    meet();
+    *under = heard_sum(1);
+    return static_cast<int>(heard_sum(0)) - 1;
   }
 
   // The key K with sum(key > K) < target <= sum(key >= K) of f over the row's bin `b`, of which `over`
   // lies above, by ever finer equal ranges of keys: for bins of any number of equal logits.
   template <typename F>
   __device__ uint32_t select(F f, int b, u64 over, u64 target, u64* above) {
-    u64 v[DRAW_PER_THREAD], under, all;
     uint32_t lo = 0xFFFFFFFFu, hi = 0;
     each([&](int i, float x) {
       if (f(base + i, x) && bin(x) == b) {
@@ -338,26 +366,22 @@ struct DrawRow {
     while (lo < hi) {
       int shift = 0;
       while (((hi - lo) >> shift) >= DRAW_BINS) ++shift;
-      clear_bins();
-      each([&](int i, float x) {
-        const uint32_t k = draw_key(x);
-        if (k < lo || k > hi) return;
-        const u64 w = f(base + i, x);
-        if (w) add_bin((hi - k) >> shift, w);
-      });
-      __syncthreads();
-      meet();
-      const u64 below = all_bins(v, &all);
-      const int at = cross(v, below, target - over, &under);
+      Bins bins;
+      weigh([&](int i, float x) -> u64 { const uint32_t k = draw_key(x); return k >= lo && k <= hi ? f(i, x) : 0; },
+            [&](float x) { return (hi - draw_key(x)) >> shift; }, &bins);
+      u64 under;
+      const int at = cross(bins, target - over, &under);
       over += under;
       const uint32_t width = 1u << shift, from = hi - (static_cast<uint32_t>(at) << shift);
       lo = from - lo < width ? lo : from - width + 1;
       hi = from;
-      meet();
     }
     *above = over;
     return hi;
   }
+
+  // A barrier of the first `threads` threads (whole warps).
+  __device__ __forceinline__ void some_sync(int threads) const { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
 
   // Orders list[0, n) descending; what is beyond n up to a power of two is filled with zeros.
   __device__ void sort(int n) {
@@ -367,24 +391,26 @@ struct DrawRow {
     __syncthreads();
     if (size <= DRAW_THREADS) {
       // an entry to a thread: steps of less than a warp go from lane to lane
-      u64 a = static_cast<int>(threadIdx.x) < size ? sh->list[threadIdx.x] : 0;
-      for (int k = 2; k <= size; k *= 2) {
-        for (int j = k / 2; j > 0; j /= 2) {
-          u64 b;
-          if (j >= 32) {
-            __syncthreads();
-            if (static_cast<int>(threadIdx.x) < size) sh->list[threadIdx.x] = a;
-            __syncthreads();
-            b = static_cast<int>(threadIdx.x) < size ? sh->list[threadIdx.x ^ j] : 0;
-          } else {
-            b = __shfl_xor_sync(0xFFFFFFFFu, a, j);
+      if (static_cast<int>(threadIdx.x) < size) {
+        u64 a = sh->list[threadIdx.x];
+        for (int k = 2; k <= size; k *= 2) {
+          for (int j = k / 2; j > 0; j /= 2) {
+            u64 b;
+            if (j >= 32) {
+              some_sync(size);
+              sh->list[threadIdx.x] = a;
+              some_sync(size);
+              b = sh->list[threadIdx.x ^ j];
+            } else {
+              b = __shfl_xor_sync(0xFFFFFFFFu, a, j);
+            }
+            const bool larger = ((threadIdx.x & k) == 0) == ((threadIdx.x & j) == 0);  // of the two, this thread keeps it
+            a = larger == (a < b) ? b : a;
           }
-          const bool larger = ((threadIdx.x & k) == 0) == ((threadIdx.x & j) == 0);  // of the two, this thread keeps it
-          a = larger == (a < b) ? b : a;
         }
+        some_sync(size);
+        sh->list[threadIdx.x] = a;
       }
-      __syncthreads();
-      if (static_cast<int>(threadIdx.x) < size) sh->list[threadIdx.x] = a;
       __syncthreads();
       return;
     }
@@ -403,33 +429,35 @@ struct DrawRow {
     }
   }
 
-  // Appends an entry to the first block's list (with the others of this warp that are here).
-  __device__ __forceinline__ void append(int i, float x) {
-    const uint32_t here = __activemask(), first = __ffs(here) - 1;
-    uint32_t at = 0;
-    if (static_cast<uint32_t>(lane) == first) at = dsmem_atomic_add(dsmem_addr(smem_u32(&sh->listed), 0), __popc(here));
-    at = __shfl_sync(here, at, first) + __popc(here & ((1u << lane) - 1u));
-    if (at < DRAW_LIST)
-      dsmem_st_v2(dsmem_addr(smem_u32(&sh->list[0]), 0) + 8 * at, ~static_cast<uint32_t>(base + i), draw_key(x));
-  }
-  // Lists the entries from `least` to `most` that take(index, x) wants, in any order; the row's number
-  // of them (the list has the first DRAW_LIST).  A vector without any costs a comparison an entry.
+  // Lists the entries from `least` to `most` that take(index, x) wants, in any order, in the first block (the
+  // list has the first DRAW_LIST); the row's number of them.  A vector without any costs a comparison an
+  // entry.  A block lists its own first: an addition in another block's memory takes as long as meet().
   template <typename F>
   __device__ u64 gather(float least, float most, F take) {
-    uint32_t mine = 0;
+    __syncthreads();
+    if (threadIdx.x == 0) sh->local = 0;
+    __syncthreads();
     for (int v = threadIdx.x; v < vecs; v += DRAW_THREADS) {
       bool any = false;
       vec(v, [&](int, float x) { any |= x >= least && x <= most; });
       if (!any) continue;
       vec(v, [&](int i, float x) {
         if (x >= least && x <= most && take(base + i, x)) {
-          append(i, x);
-          ++mine;
+          const uint32_t at = atomicAdd(&sh->local, 1u);
+          if (at < DRAW_LIST) sh->own[at] = static_cast<u64>(draw_key(x)) << 32 | static_cast<uint32_t>(~(base + i));
         }
       });
     }
-    const u64 s = block_sum(mine);
-    if (warp == 0) tell(s, 0);
+    __syncthreads();
+    const uint32_t here = sh->local;
+    if (here > 0) {  // the same in all threads
+      if (threadIdx.x == 0) sh->found = dsmem_atomic_add(dsmem_addr(smem_u32(&sh->listed), 0), here);
+      __syncthreads();
+      const uint32_t from = static_cast<uint32_t>(sh->found), there = dsmem_addr(smem_u32(&sh->list[0]), 0);
+      for (uint32_t i = threadIdx.x; i < min(here, static_cast<uint32_t>(DRAW_LIST)); i += DRAW_THREADS)
+        if (from + i < DRAW_LIST) dsmem_st_u64(there + 8 * (from + i), sh->own[i]);
+    }
+    if (warp == 0) tell(here, 0);
     meet();
     return heard_sum(0);
   }
@@ -526,8 +554,8 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     else
       ids[i] = i < n ? from[i] : __ushort_as_bfloat16(0x7FC0);
   }
-  sh->count[threadIdx.x] = 0;
-  R.clear_bins();
+  sh->part[2][threadIdx.x] = 0;  // DRAW_COARSE counts
+  __syncthreads();
 
   // The thread's largest logit and its lowest index, then the row's.
   float most = -INFINITY;
@@ -551,19 +579,33 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     }
   }
   if (threadIdx.x == 0 && whole < R.vecs) R.vec(whole, look);
-  u64 best = most_at < 0 ? 0 : static_cast<u64>(draw_key(most)) << 32 | static_cast<uint32_t>(~(R.base + most_at));
-  best = warp_max_u64(best);
-  if (R.lane == 0) sh->warp[R.warp] = best;
+  // The largest of four threads to all blocks: to each block by 32 threads, four to a store.
+  const uint32_t own_key = most_at < 0 ? NO_KEY : draw_key(most);
+  {
+    uint32_t four = max(own_key, __shfl_xor_sync(0xFFFFFFFFu, own_key, 1));
+    four = max(four, __shfl_xor_sync(0xFFFFFFFFu, four, 2));
+    uint32_t* mine = reinterpret_cast<uint32_t*>(sh->list);
+    if ((R.lane & 3) == 0) mine[threadIdx.x / 4] = four;
+  }
   __syncthreads();
   cluster_wait();
-  if (R.warp == 0) {
-    best = warp_max_u64(R.lane < DRAW_WARPS ? sh->warp[R.lane] : 0);
-    R.tell(best, 0);
+  if (static_cast<uint32_t>(R.warp) < R.ranks) {
+    const uint4 keys = reinterpret_cast<const uint4*>(sh->list)[R.lane];
+    dsmem_st_v4(dsmem_addr(smem_u32(&sh->part[0][R.rank * DRAW_MAXIMA + R.lane * 4]), R.warp), keys.x, keys.y, keys.z, keys.w);
   }
   R.meet();
-  best = warp_max_u64(static_cast<uint32_t>(R.lane) < R.ranks ? R.heard(0, R.lane) : 0);
+  uint32_t maxima[DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS], top_key = NO_KEY;
+#pragma unroll
+  for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i) {
+    const int at = i * DRAW_THREADS + threadIdx.x;
+    maxima[i] = at < static_cast<int>(R.ranks) * DRAW_MAXIMA ? sh->part[0][at] : NO_KEY;
+    top_key = max(top_key, maxima[i]);
+  }
+  top_key = __reduce_max_sync(0xFFFFFFFFu, top_key);
+  if (R.lane == 0) sh->warp[R.warp] = top_key;
+  __syncthreads();
+  top_key = __reduce_max_sync(0xFFFFFFFFu, R.lane < DRAW_WARPS ? static_cast<uint32_t>(sh->warp[R.lane]) : NO_KEY);
 
-  const uint32_t top_key = static_cast<uint32_t>(best >> 32);
   const float top = draw_val(top_key);
   R.top = top;
   const bool lead = R.rank == 0;
@@ -574,10 +616,22 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   const float least = !(m <= 0.0f) ? top + logf(m) : -INFINITY;  // min_p's threshold
   const bool k_on = k > 0 && k < A.V, p_on = !(P >= 1.0f);
   const u64 p24 = P > 0.0f ? static_cast<u64>(fminf(P, 1.0f) * 0x1p24f) : 0ull;
-  if (top_key == NO_KEY || !(T > 0.0f) || (!(m <= 0.0f) && !(top >= least)) || (p_on && p24 == 0)) {
-    if (lead && threadIdx.x == 0)
-      answer(top_key == NO_KEY ? -1 : static_cast<int>(~static_cast<uint32_t>(best)),
-             top_key == NO_KEY ? __int_as_float(0x7FC00000) : 0.0f);
+  if (top_key == NO_KEY) {
+    if (lead && threadIdx.x == 0) answer(-1, __int_as_float(0x7FC00000));
+    return;
+  }
+  if (!(T > 0.0f) || (!(m <= 0.0f) && !(top >= least)) || (p_on && p24 == 0)) {  // the first in order
+    uint32_t first = __reduce_min_sync(0xFFFFFFFFu, own_key == top_key ? static_cast<uint32_t>(R.base + most_at) : 0xFFFFFFFFu);
+    __syncthreads();
+    if (R.lane == 0) sh->warp[R.warp] = first;
+    __syncthreads();
+    if (R.warp == 0) {
+      first = __reduce_min_sync(0xFFFFFFFFu, R.lane < DRAW_WARPS ? static_cast<uint32_t>(sh->warp[R.lane]) : 0xFFFFFFFFu);
+      R.tell(first, 0);
+    }
+    R.meet();
+    first = __reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(R.lane) < R.ranks ? static_cast<uint32_t>(R.heard(0, R.lane)) : 0xFFFFFFFFu);
+    if (lead && threadIdx.x == 0) answer(static_cast<int>(first), 0.0f);
     return;
   }
   const float inv = 1.0f / T;
@@ -586,8 +640,8 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   auto tempered = [&](float x) { return x == top ? 0.0f : fmaxf((x - top) * inv, -1000.0f); };
   auto flat = [&](float x) { return draw_weight(x == top ? 0.0f : x - top); };  // at temperature 1
 
-  // what is left: keys above K, and of the keys equal to K the indices up to I
-  uint32_t K = max(1u, m <= 0.0f ? 1u : draw_key(least));
+  // what is left: logits above `edge`, and of the logits equal to it the indices up to I
+  float edge = fmaxf(least, -3.402823466e38f);
   int I = A.V - 1;
 
   // The first block's list holds all that the cuts leave, and maybe more below: it finishes alone.
@@ -618,7 +672,7 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
         under += i < per && at < kept && (at == 0 || run < share);
         run += ws[i];
       }
-      kept = static_cast<int>(R.block_sum(under));
+      kept = per == 1 ? __syncthreads_count(static_cast<int>(under)) : static_cast<int>(R.block_sum(under));
     }
     // index order: swap the halves, so that the greatest ~index comes first
     __syncthreads();
@@ -636,97 +690,84 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
       run += ws[i];
     }
   };
-  auto count_maximum = [&]() {
-    if (most_at >= 0) atomicAdd(&sh->count[R.bin(most) / (DRAW_BINS / DRAW_COARSE)], 1u);
-  };
   auto all = [](int, float) { return true; };
-  bool listed_before = false;
-  auto new_list = [&]() {  // with at least one meet() before the next entry
+  auto by_distance = [&](float x) { return R.bin(x); };
+  auto new_list = [&]() {  // between two meetings
     if (threadIdx.x == 0) sh->listed = 0;
-    listed_before = false;
+  };
+  auto pinned = [&](uint32_t key, int i) {
+    edge = draw_val(key);
+    I = i;
   };
 
-  u64 v[DRAW_PER_THREAD], under, sum, before;
-  if (k_on && k <= DRAW_LIST / 2) {
-    count_maximum();
-    R.meet();
-    const u64 here = R.all_maxima(threadIdx.x), upto = R.block_scan(here);
-    __syncthreads();
-    if (threadIdx.x == 0) sh->found = DRAW_COARSE;
-    __syncthreads();
-    if (upto - here < static_cast<u64>(k) && upto >= static_cast<u64>(k)) sh->found = threadIdx.x;
-    __syncthreads();
-    // fewer maxima than k: every entry
-    const int last = (static_cast<int>(sh->found) + 1) * (DRAW_BINS / DRAW_COARSE);
-    const u64 entries = R.gather(fmaxf(least, R.floor_of(last)), top, all);
+  typename DrawRow<E>::Bins bins;
+  u64 under, before;
+  bool used = false;  // the list
+  if (k_on && (A.V <= DRAW_LIST || k <= static_cast<int>(R.ranks) * DRAW_MAXIMA / 2)) {
+    float from = edge;
+    if (A.V > DRAW_LIST) {
+      // the bin in which the maxima are k
+#pragma unroll
+      for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i)
+        if (maxima[i] != NO_KEY) atomicAdd(&sh->part[2][R.bin(draw_val(maxima[i])) / (DRAW_BINS / DRAW_COARSE)], 1u);
+      if (threadIdx.x == 0) sh->found = DRAW_COARSE;
+      __syncthreads();
+      const uint32_t here = sh->part[2][threadIdx.x], upto = R.block_scan(here);
+      if (upto - here < static_cast<uint32_t>(k) && upto >= static_cast<uint32_t>(k)) sh->found = threadIdx.x;
+      __syncthreads();
+      // fewer maxima than k: every entry
+      from = fmaxf(from, R.floor_of((static_cast<int>(sh->found) + 1) * (DRAW_BINS / DRAW_COARSE)));
+    }
+    const u64 entries = R.gather(from, top, all);
     if (entries <= DRAW_LIST) {
       if (lead) finish(static_cast<int>(entries), 0);
       return;
     }
-    listed_before = true;
+    used = true;
   }
   if (k_on) {
-    if (listed_before) new_list();
+    if (used) new_list();
     auto one = [&](int, float x) -> u64 { return x > -INFINITY; };
-    R.each([&](int, float x) {
-      if (x > -INFINITY) atomicAdd(&sh->lo[R.bin(x)], 1u);
-    });
-    __syncthreads();
-    R.meet();
-    const u64 below = R.all_bins(v, &sum);
-    if (static_cast<u64>(k) < sum) {
-      const uint32_t least_key = K;
-      const int b = R.cross(v, below, k, &under);
-      R.pin(one, b, under, k, &K, &I);
-      listed_before = true;
-      if (least_key > K) {
-        K = least_key;
-        I = A.V - 1;
-      }
+    if (static_cast<u64>(k) < R.weigh(one, by_distance, &bins)) {
+      const int b = R.cross(bins, k, &under);
+      uint32_t key;
+      int i;
+      R.pin(one, b, under, k, &key, &i);
+      used = true;
+      if (draw_val(key) >= edge) pinned(key, i);
     }
   }
   if (p_on) {
-    const uint32_t K0 = K;
+    if (used) new_list();
+    const float edge0 = edge;
     const int I0 = I;
-    auto weight = [&](int i, float x) -> u64 {
-      const uint32_t key = draw_key(x);
-      return key > K0 || (key == K0 && i <= I0) ? flat(x) : 0ull;
-    };
-    if (k_on) {
-      R.meet();  // the bins and the list of the step before are read
-      if (listed_before) new_list();
-      R.clear_bins();
-    } else {
-      count_maximum();
-    }
-    R.each([&](int i, float x) {
-      const u64 w = weight(R.base + i, x);
-      if (w) R.add_bin(R.bin(x), w);
-    });
-    __syncthreads();
-    R.meet();
-    const u64 below = R.all_bins(v, &sum), share = draw_share(p24, sum);
-    const int b = R.cross(v, below, share, &under);
-    bool few = false;
-    if (!k_on) {  // how many entries there are up to b: about as many as maxima, where they are few
-      const int last = b / (DRAW_BINS / DRAW_COARSE);
-      few = R.block_sum(static_cast<int>(threadIdx.x) <= last ? R.all_maxima(threadIdx.x) : 0) <= DRAW_LIST / 4;
-    }
-    if (few) {
-      const u64 entries = R.gather(fmaxf(least, R.floor_of(b + 1)), top, all);
-      if (entries <= DRAW_LIST) {
-        if (lead) finish(static_cast<int>(entries), share);
-        return;
+    auto weight = [&](int i, float x) -> u64 { return x > edge0 || (x == edge0 && i <= I0) ? flat(x) : 0ull; };
+    const u64 share = draw_share(p24, R.weigh(weight, by_distance, &bins));
+    const int b = R.cross(bins, share, &under);
+    if (!k_on) {
+      // how many entries there are up to b: about as many as maxima, where they are few
+      uint32_t few = 0;
+#pragma unroll
+      for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i)
+        few += maxima[i] != NO_KEY && R.bin(draw_val(maxima[i])) <= b;
+      if (R.block_sum(few) <= R.ranks * DRAW_MAXIMA / 2) {
+        const u64 entries = R.gather(fmaxf(edge, R.floor_of(b + 1)), top, all);
+        if (entries <= DRAW_LIST) {
+          if (lead) finish(static_cast<int>(entries), share);
+          return;
+        }
+        new_list();
+        R.meet();
       }
-      R.meet();
-      new_list();
-      R.meet();
     }
-    R.pin(weight, b, under, share, &K, &I);
+    uint32_t key;
+    int i;
+    R.pin(weight, b, under, share, &key, &i);
+    pinned(key, i);
   }
   auto left = [&](int i, float x) -> u64 {
-    const uint32_t key = draw_key(x);
-    return key > K || (key == K && i <= I) ? draw_weight(tempered(x)) : 0ull;
+    const u64 w = draw_weight(tempered(x));
+    return x > edge || (x == edge && i <= I) ? w : 0ull;
   };
   const u64 total = R.parts(left, &before);
   const int at = R.find(left, draw_share(u24, total), before);
