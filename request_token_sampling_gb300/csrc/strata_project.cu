@@ -26,6 +26,7 @@ using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
 using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, strata::ProjectArgs);
 
 constexpr int MAX_ROWS = 1 << 19;  // rows times adapters of a tile count in 31 bits
+constexpr int SHRINK_ROWS = 32;     // a call with more takes its inner rows from the tensor cores
 constexpr int BN_SIZES[4] = {16, 32, 64, 128};
 
 template <int BN>
@@ -67,6 +68,15 @@ const Device& device_info(int id) {
       for (int i = 0; i < 4 && d.status == cudaSuccess; ++i)
         d.status = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel_for(bn, i & 1, i & 2)),
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, strata::proj_smem(bn));
+    if (d.status == cudaSuccess)
+      d.status = cudaFuncSetAttribute(reinterpret_cast<const void*>(strata::pair_kernel),
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, strata::pair_smem());
+    if (d.status == cudaSuccess)
+      d.status = cudaFuncSetAttribute(reinterpret_cast<const void*>(strata::inner_kernel<false>),
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, strata::inner_smem(false));
+    if (d.status == cudaSuccess)
+      d.status = cudaFuncSetAttribute(reinterpret_cast<const void*>(strata::inner_kernel<true>),
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, strata::inner_smem(true));
   });
   return devices[id];
 }
@@ -77,16 +87,47 @@ bool encode(EncodeFn fn, CUtensorMap* m, bool bytes, int rank, const void* p, co
   const cuuint32_t ones[3] = {1, 1, 1};
   return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims,
             strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+            line == 0   ? CU_TENSOR_MAP_SWIZZLE_NONE
+            : line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B 
+            : line == 64  ? CU_TENSOR_MAP_SWIZZLE_64B
+                          : CU_TENSOR_MAP_SWIZZLE_32B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a tile: the fewest that hold the call's rows, 128 for more.  The products' cost grows with
-// them, and w is read once for each tile of rows.
+// Rows of a tile on one SM: the fewest that hold the call's rows, 128 for more.  The products' cost grows
+// with them, and w is read once for each tile of rows.
 int tile_rows(int T) {
   for (int bn : BN_SIZES)
     if (T <= bn) return bn;
   return 128;
+}
+
+// Few tiles leave most of the GPU idle: then a cluster of blocks shares a tile, as many as still fit beside
+// one another and have two stages each.
+int split_ranks(int64_t tiles, int k_stages, int sms) {
+  int ranks = 1;
+  while (ranks < 8 && tiles * ranks * 2 <= sms && k_stages >= ranks * 4) ranks *= 2;
+  return ranks;
+}
+
+// Rows of a tile of the pair kernel, or 0 where tiles on one SM take less time.  Both are bound by what an
+// SM takes in from L2, about 58 bytes a cycle (128 x 128 tiles on one SM ran at that: 840 TFLOP/s), or by
+// its tensor core, 4096 products a cycle: cycles of a 64-deep stage, times stages one after another.
+int pair_rows(int T, int N, int k_stages, int sms) {
+  const int64_t n_pairs = (N + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M), n_tiles = (N + strata::PROJ_M - 1) / strata::PROJ_M;
+  auto waves = [](int64_t tiles, int64_t at_once) { return (tiles + at_once - 1) / at_once; };
+  const int64_t tiles = n_tiles * ((T + 127) / 128);
+  int64_t best = waves(tiles, sms) * (2 * strata::PROJ_M * strata::PROJ_LINE / 58) / split_ranks(tiles, k_stages, sms);
+  int rows = 0;
+  for (int r = 256; r >= 64; r -= 16) {
+    const int64_t stage = std::max<int64_t>((strata::PROJ_M + r / 2) * strata::PROJ_LINE / 58, 2 * r);
+    const int64_t cost = waves(n_pairs * ((T + r - 1) / r), sms / 2) * stage;
+    if (cost < best) {
+      best = cost;
+      rows = r;
+    }
+  }
+  return rows;
 }
 
 // The current device's entry (checked: it is usable), or an error code.
@@ -114,8 +155,9 @@ int strata::tail_device(uint32_t** errors, int* sms) {
 
 extern "C" int64_t strata_project_workspace(int T, int S, int R) {
   if (T <= 0 || S <= 0 || R <= 0) return 0;
-  const int bn = tile_rows(T), t_tiles = (T + bn - 1) / bn;
-  return lists_bytes(t_tiles, bn) + static_cast<int64_t>(t_tiles) * std::min(S, bn) * bn * R * 2;
+  if (T <= 128) return lists_bytes(1, 128) + static_cast<int64_t>(std::min(S, 128)) * 128 * R * 2;
+  // whatever tiles the call takes: 64 to 256 rows each
+  return lists_bytes((T + 63) / 64, 256) + (static_cast<int64_t>(T) + 256) * std::min(S, 256) * R * 2;
 }
 
 extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
@@ -153,7 +195,11 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   const Device& dev = *found;
   cudaError_t e = cudaSuccess;
 
-  const int bn = tile_rows(T), t_tiles = (T + bn - 1) / bn, n_tiles = (N + strata::PROJ_M - 1) / strata::PROJ_M;
+  const cuuint32_t elems = f8 ? 128 : 64;
+  const int k_stages = (K + static_cast<int>(elems) - 1) / static_cast<int>(elems);
+  const int pair = T > 128 && !f8 ? pair_rows(T, N, k_stages, dev.sms) : 0;  // tiles of two SMs
+  const int bn = pair > 0 ? pair : tile_rows(T), t_tiles = (T + bn - 1) / bn;
+  const int n_tiles = pair > 0 ? (N + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M) : (N + strata::PROJ_M - 1) / strata::PROJ_M;
   const int64_t tiles = static_cast<int64_t>(t_tiles) * n_tiles;
   if (tiles > INT32_MAX) return host_fail(STRATA_ERANGE, "T=%d N=%d", T, N);
   const int most = std::min(S, bn);
@@ -180,9 +226,11 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   A.rank_block = R % 64 == 0 ? 64 : R % 32 == 0 ? 32 : 16;
   A.n_tiles = n_tiles;
   A.t_tiles = t_tiles;
+  A.tile_rows = bn;
+  A.w = w;
+  A.ldw = ldw;
 
   CUtensorMap mw, mx, mb{}, mh{};
-  const cuuint32_t elems = f8 ? 128 : 64;
   {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldw * esz)};
@@ -192,7 +240,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(T)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldx * esz)};
-    const cuuint32_t box[2] = {elems, static_cast<cuuint32_t>(bn)};
+    const cuuint32_t box[2] = {elems, static_cast<cuuint32_t>(pair > 0 ? bn / 2 : bn)};
     if (!encode(dev.encode, &mx, f8, 2, x, dims, strides, box, 128)) return host_fail(STRATA_EINVAL, "x cannot be mapped");
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -203,25 +251,54 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(A.rank_block), strata::PROJ_M, 1};
     if (!encode(dev.encode, &mb, false, 3, b, dims, strides, box, A.rank_block * 2)) return host_fail(STRATA_EINVAL, "b cannot be mapped");
     const cuuint64_t hdims[2] = {r, static_cast<cuuint64_t>(t_tiles) * most * bn};
-    const cuuint32_t hbox[2] = {static_cast<cuuint32_t>(A.rank_block), static_cast<cuuint32_t>(bn)};
+    const cuuint32_t hbox[2] = {static_cast<cuuint32_t>(A.rank_block), static_cast<cuuint32_t>(pair > 0 ? bn / 2 : bn)};
     if (!encode(dev.encode, &mh, false, 2, A.spread, hdims, strides, hbox, A.rank_block * 2))
       return host_fail(STRATA_EINVAL, "the workspace cannot be mapped");
-    const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(R / 8));
-    if (f8)
-      strata::shrink_kernel<__nv_fp8_e4m3><<<grid, 256, 0, s>>>(A, bn);
-    else
-      strata::shrink_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(A, bn);
+    if (T <= SHRINK_ROWS) {
+      const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(R / 8));
+      if (f8)
+        strata::shrink_kernel<__nv_fp8_e4m3><<<grid, 256, 0, s>>>(A, bn);
+      else
+        strata::shrink_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(A, bn);
+    } else {
+      CUtensorMap ma, mt;
+      const int box_rows = R % 128 == 0 ? 128 : R % 64 == 0 ? 64 : R % 32 == 0 ? 32 : 16;
+      const cuuint64_t adims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(S) * R};
+      const cuuint64_t astrides[1] = {static_cast<cuuint64_t>(K) * 2};
+      const cuuint32_t abox[2] = {64, static_cast<cuuint32_t>(box_rows)};
+      const cuuint64_t xdims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(T)};
+      const cuuint64_t xstrides[1] = {static_cast<cuuint64_t>(ldx * esz)};
+      const cuuint32_t xbox[2] = {64, static_cast<cuuint32_t>(bn)};
+      if (!encode(dev.encode, &ma, false, 2, a, adims, astrides, abox, 128) ||
+          !encode(dev.encode, &mt, f8, 2, x, xdims, xstrides, xbox, f8 ? 0 : 128))
+        return host_fail(STRATA_EINVAL, "a or x cannot be mapped");
+      // clusters of a tile: one where the tiles fill the GPU, as many as there can be work for where they do not
+      const int groups = std::min((most * R + strata::PROJ_M - 1) / strata::PROJ_M,
+                                  std::max(1, dev.sms / strata::INNER_SPLIT / t_tiles));
+      cudaLaunchConfig_t in = {};
+      in.gridDim = dim3(static_cast<unsigned>(t_tiles) * groups * strata::INNER_SPLIT, 1, 1);
+      in.blockDim = dim3(strata::PROJ_THREADS, 1, 1);
+      in.dynamicSmemBytes = static_cast<size_t>(strata::inner_smem(f8));
+      in.stream = s;
+      cudaLaunchAttribute cluster = {};
+      cluster.id = cudaLaunchAttributeClusterDimension;
+      cluster.val.clusterDim.x = strata::INNER_SPLIT;
+      cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+      in.attrs = &cluster;
+      in.numAttrs = 1;
+      e = cudaLaunchKernelEx(&in, f8 ? strata::inner_kernel<true> : strata::inner_kernel<false>, ma, mt, A, groups, box_rows);
+      if (e != cudaSuccess) return cuda_fail(e, "strata_project_rows");
+    }
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "strata_project_rows");
   }
-  // Few tiles leave most of the GPU idle: then a cluster of blocks shares a tile, as many as still
-  // fit beside one another and have two stages each.
-  const int k_stages = static_cast<int>((K + elems - 1) / elems);
-  int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= dev.sms && k_stages >= ranks * 4) ranks *= 2;
+  const int ranks = pair > 0 ? 1 : split_ranks(tiles, k_stages, dev.sms);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, dev.sms)), 1, 1);
+  if (pair > 0)
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, dev.sms / 2)), 1, 1);
+  else
+    cfg.gridDim = dim3(static_cast<unsigned>(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, dev.sms)), 1, 1);
   cfg.blockDim = dim3(strata::PROJ_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(strata::proj_smem(bn));
+  cfg.dynamicSmemBytes = static_cast<size_t>(pair > 0 ? strata::pair_smem() : strata::proj_smem(bn));
   cfg.stream = s;
   cudaLaunchAttribute attrs[2];
   int na = 0;
@@ -238,7 +315,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   }
   cfg.attrs = attrs;
   cfg.numAttrs = na;
-  e = cudaLaunchKernelEx(&cfg, kernel_for(bn, f8, ranks > 1), mw, mx, mb, mh, A);
+  e = cudaLaunchKernelEx(&cfg, pair > 0 ? strata::pair_kernel : kernel_for(bn, f8, ranks > 1), mw, mx, mb, mh, A);
   return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_project_rows");
 }
 

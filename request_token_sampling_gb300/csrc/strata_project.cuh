@@ -2,7 +2,7 @@
 //
 //   y[t] = sx[t] sw (x[t] w^T) + h[t] b_c^T,   h[t] = g_c sx[t] (x[t] a_c^T),   c = row_adapter[t]
 //
-// Two kernels.  shrink_kernel computes the inner rows h in 32 bits and writes them, rounded to bfloat16,
+// Two kernels.  shrink_kernel (few rows) or inner_kernel (many) computes the inner rows h in 32 bits and writes them, rounded to bfloat16,
 // spread out: for each tile of rows and each adapter of the tile a block [tile rows][R] that holds h where
 // the row uses that adapter and zeros elsewhere.  project_kernel then treats b of the tile's adapters as
 // more of the sum's length: for a tile of 128 outputs and up to 128 rows,
@@ -14,6 +14,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -35,7 +36,9 @@ struct ProjectArgs {
   int T, N, K, S, R;
   int most;               // adapters that a tile can have: min(S, tile rows)
   int rank_block;         // R is cut into blocks of 64, 32 or 16 (one swizzle line of shared memory)
-  int n_tiles, t_tiles;
+  int n_tiles, t_tiles, tile_rows;
+  int64_t ldw;            // of w, for sums that are taken again
+  const void* w;
 };
 
 constexpr int PROJ_M = 128;        // outputs of a tile: the accumulator's lanes
@@ -139,35 +142,50 @@ __device__ __forceinline__ float proj_warp_sum(float v) {
   return v;
 }
 
+// The adapters of a tile of rows, as the bits of 32 words, and whether a row has none; the whole block.
+struct TileAdapters {
+  uint32_t bits[32], none;
+};
+__device__ __forceinline__ void tile_adapters(const ProjectArgs& A, int t0, int rows, TileAdapters* used) {
+  if (threadIdx.x < 32) used->bits[threadIdx.x] = 0;
+  if (threadIdx.x == 0) used->none = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows; i += blockDim.x) {
+    const int c = A.row_adapter[t0 + i];
+    if (c >= 0 && c < A.S)
+      atomicOr(&used->bits[c >> 5], 1u << (c & 31));
+    else
+      used->none = 1;
+  }
+  __syncthreads();
+}
+// A tile's list: how many adapters it has (and whether its rows differ in them), then their ids.
+constexpr int32_t LIST_COUNT = 0xFFFF, LIST_MIXED = 1 << 30;
+__device__ __forceinline__ void write_list(const ProjectArgs& A, int tile, int tile_rows, const TileAdapters& used) {
+  int32_t* list = A.lists + static_cast<int64_t>(tile) * (tile_rows + 1);
+  int n = 0;
+  for (int w = 0; w < 32; ++w)
+    for (uint32_t bits = used.bits[w]; bits; bits &= bits - 1) list[1 + n++] = w * 32 + __ffs(bits) - 1;
+  list[0] = n | (n > 1 || (n == 1 && used.none) ? LIST_MIXED : 0);
+}
+
 // Eight warps: the block of row t takes eight of its inner products, one to a warp.
 template <typename E>
 __global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A, int tile_rows) {
   grid_dep_launch();
-  __shared__ uint32_t used[32];
+  __shared__ TileAdapters used;
   const int t = blockIdx.x, tile = t / tile_rows, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + warp;
-  if (threadIdx.x < 32) used[threadIdx.x] = 0;
-  __syncthreads();
-  const int t0 = tile * tile_rows, rows = min(tile_rows, A.T - t0);
-  for (int i = threadIdx.x; i < rows; i += 256) {
-    const int c = A.row_adapter[t0 + i];
-    if (c >= 0 && c < A.S) atomicOr(&used[c >> 5], 1u << (c & 31));
-  }
-  __syncthreads();
+  const int t0 = tile * tile_rows;
+  tile_adapters(A, t0, min(tile_rows, A.T - t0), &used);
   const int c = A.row_adapter[t];
   const bool mine = c >= 0 && c < A.S;
   int count = 0, at = -1;
   for (int w = 0; w < 32; ++w) {
-    if (mine && w == c >> 5) at = count + __popc(used[w] & ((1u << (c & 31)) - 1u));
-    count += __popc(used[w]);
+    if (mine && w == c >> 5) at = count + __popc(used.bits[w] & ((1u << (c & 31)) - 1u));
+    count += __popc(used.bits[w]);
   }
-  if (t == t0 && blockIdx.y == 0 && threadIdx.x == 0) {
-    int32_t* list = A.lists + static_cast<int64_t>(tile) * (tile_rows + 1);
-    list[0] = count;
-    int n = 1;
-    for (int w = 0; w < 32; ++w)
-      for (uint32_t bits = used[w]; bits; bits &= bits - 1) list[n++] = w * 32 + __ffs(bits) - 1;
-  }
+  if (t == t0 && blockIdx.y == 0 && threadIdx.x == 0) write_list(A, tile, tile_rows, used);
   float s = 0.0f;
   if (mine) {
     const E* x = static_cast<const E*>(A.x) + t * A.ldx;
@@ -192,6 +210,214 @@ __global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A, int tile_row
         __float2bfloat16_rn(j == at ? s : 0.0f);
 }
 
+// Many rows: the same inner rows on the tensor cores.  A cluster of INNER_SPLIT blocks takes 128 of the
+// inner products (the matrices a of a tile's adapters one below another) for all rows of a tile, each
+// block a part of K, and adds the parts up in rank order.  8-bit rows are widened to bfloat16 (exactly)
+// on their way to the operand by the four warps that later write the result.
+constexpr int INNER_SPLIT = 8, INNER_ROWS = 256;
+constexpr int INNER_A = PROJ_M * PROJ_LINE;
+__host__ __device__ constexpr int inner_stages(bool f8) { return f8 ? 3 : 4; }
+__host__ __device__ constexpr int inner_stage_bytes(bool f8) { return INNER_A + INNER_ROWS * PROJ_LINE * (f8 ? 3 : 2) / 2; }
+__host__ __device__ constexpr int inner_smem(bool f8) { return inner_stages(f8) * inner_stage_bytes(f8) + 1024 + 512; }
+
+struct InnerBars {
+  uint64_t full[4], wide[4], empty[4], done, drained;
+  uint32_t tmem, dead;
+  TileAdapters used;
+};
+
+template <bool F8>
+__global__ void __launch_bounds__(PROJ_THREADS, 1)
+    inner_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mx,
+                 const __grid_constant__ ProjectArgs A, int groups, int box_rows) {
+  constexpr int STAGES = inner_stages(F8), STAGE = inner_stage_bytes(F8), X = INNER_A, RAW = INNER_A + INNER_ROWS * PROJ_LINE;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  InnerBars* B = reinterpret_cast<InnerBars*>(smem + STAGES * STAGE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows_max = A.tile_rows;
+  const uint32_t rank = cluster_ctarank();
+  const int unit = blockIdx.x / INNER_SPLIT, tile = unit / groups, first = unit % groups;
+  volatile uint32_t* dead = &B->dead;
+  const uint32_t bit = 0x08u;  // STRATA_DEVERR_TIMEOUT
+  grid_dep_launch();
+
+  const int t0 = tile * rows_max, rows = min(rows_max, A.T - t0);
+  tile_adapters(A, t0, rows, &B->used);
+  int count = 0;
+  for (int w = 0; w < 32; ++w) count += __popc(B->used.bits[w]);
+  auto adapter = [&](int j) {  // the j-th of them
+    for (int w = 0; w < 32; ++w) {
+      uint32_t bits = B->used.bits[w];
+      const int n = __popc(bits);
+      if (j >= n) {
+        j -= n;
+        continue;
+      }
+      while (j-- > 0) bits &= bits - 1;
+      return w * 32 + __ffs(bits) - 1;
+    }
+    return 0;
+  };
+  if (first == 0 && rank == 0 && threadIdx.x == 0) write_list(A, tile, rows_max, B->used);
+  const int stack = count * A.R;               // the adapters' matrices one below another
+  if (first * PROJ_M >= stack) return;         // the whole cluster
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&B->full[i], 1);
+      mbar_init(&B->wide[i], 128);
+      mbar_init(&B->empty[i], 1);
+    }
+    mbar_init(&B->done, 1);
+    mbar_init(&B->drained, 1);
+    B->dead = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B->tmem)), "r"(256u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem;
+  const int k_stages = (A.K + 63) / 64;
+  const int from = static_cast<int>(static_cast<int64_t>(k_stages) * rank / INNER_SPLIT);
+  const int to = static_cast<int>(static_cast<int64_t>(k_stages) * (rank + 1) / INNER_SPLIT);
+  uint32_t begun = 0, turn = 0;  // stages before this group
+
+  for (int q0 = first * PROJ_M; q0 < stack; q0 += groups * PROJ_M, begun += to - from, ++turn) {
+    const int mine = min(PROJ_M, stack - q0);
+    if (warp == 0 && lane == 0) {
+      const int boxes = (mine + box_rows - 1) / box_rows;
+      int at_row[PROJ_M / 16];
+      for (int i = 0; i < boxes; ++i) {
+        const int q = q0 + i * box_rows;
+        at_row[i] = adapter(q / A.R) * A.R + q % A.R;
+      }
+      const uint32_t bytes = static_cast<uint32_t>(boxes * box_rows * PROJ_LINE + rows_max * (F8 ? 64 : PROJ_LINE));
+      bool alive = *dead == 0u;
+      uint32_t it = begun;
+      for (int s = from; s < to && alive; ++s, ++it) {
+        const uint32_t slot = it % STAGES;
+        if (it >= STAGES && !proj_wait(&B->empty[slot], (it / STAGES + 1) & 1, dead, A.errors, bit)) {
+          alive = false;
+          break;
+        }
+        const uint32_t at = smem_u32(smem + slot * STAGE), bar = smem_u32(&B->full[slot]);
+        mbar_arrive_expect_tx(&B->full[slot], bytes);
+        for (int i = 0; i < boxes; ++i) tma_2d(at + i * box_rows * PROJ_LINE, &ma, s * 64, at_row[i], bar);
+        tma_2d(at + (F8 ? RAW : X), &mx, s * 64, t0, bar);
+      }
+      if (!alive)
+        for (uint32_t i = it - min(it, static_cast<uint32_t>(STAGES)); i < it; ++i)
+          for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->full[i % STAGES], (i / STAGES) & 1); ++spin) {
+          }
+    } else if (warp == 1 && lane == 0) {
+      bool alive = *dead == 0u, add = false;
+      uint32_t it = begun;
+      const uint32_t idesc = mma_idesc(false, rows_max);
+      for (int s = from; s < to && alive; ++s, ++it) {
+        const uint32_t slot = it % STAGES;
+        if (!proj_wait(&B->full[slot], (it / STAGES) & 1, dead, A.errors, bit) ||
+            (F8 && !proj_wait(&B->wide[slot], (it / STAGES) & 1, dead, A.errors, bit))) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = smem_u32(smem + slot * STAGE);
+        const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + X, PROJ_LINE);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mma<false>(tmem, da + 2 * i, db + 2 * i, idesc, add);
+          add = true;
+        }
+        mma_commit(&B->empty[slot]);
+      }
+      if (alive) {
+        mma_commit(&B->done);
+      } else {
+        mma_commit(&B->drained);
+        for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->drained, 0); ++spin) {
+        }
+      }
+    } else if (warp >= 2) {
+      if constexpr (F8) {
+        uint32_t it = begun;
+        for (int s = from; s < to; ++s, ++it) {
+          const uint32_t slot = it % STAGES;
+          if (!__all_sync(0xFFFFFFFFu, proj_wait(&B->full[slot], (it / STAGES) & 1, dead, A.errors, bit))) break;
+          uint8_t* stage = smem + slot * STAGE;
+          for (int r = threadIdx.x - 64; r < rows_max; r += 128) {
+            const uint4* in = reinterpret_cast<const uint4*>(stage + RAW + r * 64);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // 16 elements: two 16-byte pieces of the operand's line
+              const uint4 v = in[c];
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+                const __nv_bfloat162 b = __float22bfloat162_rn(__half22float2(__half2(h)));
+                o[i] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+              uint8_t* to_line = stage + X + r * PROJ_LINE;
+              *reinterpret_cast<uint4*>(to_line + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(to_line + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&B->wide[slot]);
+        }
+      }
+      const uint32_t quarter = warp & 3;
+      const bool ok = proj_wait(&B->done, turn & 1, dead, A.errors, bit);
+      if (__all_sync(0xFFFFFFFFu, ok)) {
+        tc_fence_after();
+        float* sums = reinterpret_cast<float*>(smem);  // [row][product]: every stage is free by now
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 16) {
+          float v[16] = {};
+          if (to > from) tmem_ld16(tmem + (quarter << 21) + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sums[(c + i) * PROJ_M + quarter * 32 + lane] = v[i];
+        }
+        tc_fence_before();
+      }
+    }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    if (*dead == 0u) {
+      // a thread's product is the same for all its rows: PROJ_M of the cluster's threads to a row
+      constexpr int GO = INNER_SPLIT * PROJ_THREADS / PROJ_M;
+      const uint32_t own = smem_u32(smem);
+      const int id = static_cast<int>(rank) * PROJ_THREADS + threadIdx.x, q = q0 + id % PROJ_M, j = q / A.R;
+      if (q < stack) {
+        const int c = adapter(j);
+        const float by = A.adapter_scale[c];
+        for (int t = id / PROJ_M; t < rows; t += GO) {
+          float v = 0.0f;
+#pragma unroll
+          for (uint32_t i = 0; i < INNER_SPLIT; ++i) v += dsmem_ld_f32(dsmem_addr(own, i) + (t * PROJ_M + id % PROJ_M) * 4);
+          v = A.row_adapter[t0 + t] == c ? by * ((A.x_scale != nullptr ? A.x_scale[t0 + t] : 1.0f) * v) : 0.0f;
+          A.spread[((static_cast<int64_t>(tile) * A.most + j) * rows_max + t) * A.R + q % A.R] = __float2bfloat16_rn(v);
+        }
+      }
+    }
+    // the next group's copies overwrite the sums that generic stores wrote and the others read
+    fence_proxy_async_smem();
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256u) : "memory");
+  }
+}
+
 // ------------------------------------------------------------------------------ the products
 template <int BN>
 struct ProjBars {
@@ -205,7 +431,7 @@ __device__ __noinline__ float proj_own_delta(const ProjectArgs& A, int tile, int
   if (c < 0 || c >= A.S) return 0.0f;
   const int32_t* list = A.lists + static_cast<int64_t>(tile) * (tile_rows + 1);
   int j = 0;
-  while (j < list[0] && list[1 + j] != c) ++j;
+  while (j < (list[0] & LIST_COUNT) && list[1 + j] != c) ++j;
   const __nv_bfloat16* h = A.spread + ((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - tile * tile_rows)) * A.R;
   const __nv_bfloat16* b = A.b + (static_cast<int64_t>(c) * A.N + n) * A.R;
   float d = 0.0f;
@@ -279,7 +505,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   const int step = SPLIT ? A.n_tiles * A.t_tiles : gridDim.x;
   const int tiles = A.n_tiles * A.t_tiles;
   auto adapters_of = [&](int t_tile) {
-    return A.S > 0 ? *(A.lists + static_cast<int64_t>(t_tile) * (BN + 1)) : 0;
+    return A.S > 0 ? *(A.lists + static_cast<int64_t>(t_tile) * (BN + 1)) & LIST_COUNT : 0;
   };
   // the stages of a tile that this block takes: [from, to) of k_stages + ceil(sub-blocks / per_stage)
   auto share = [&](int all, int& from, int& to) {
@@ -473,6 +699,264 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------------------ prompts
+// Many rows of bfloat16: two blocks of a cluster, one on each of two SMs, share a tile of 256 outputs and up
+// to 256 rows (A.tile_rows, a multiple of 16).  Each holds its 128 outputs of w and half of the rows, and
+// the pair's products read the other half from the other SM, so that an SM takes in 64 bytes a cycle
+// where a tile of 128 x 128 on one SM would need 128.  base and delta are one accumulator here, and two
+// tiles have room in tensor memory: a tile is written while the next is summed.  What a broken adapter
+// spoils in other requests' rows is therefore found in the sum, and that sum is taken again.
+constexpr int PAIR_STAGES = 7, PAIR_STAGE = 2 * PROJ_M * PROJ_LINE;
+__host__ __device__ constexpr int pair_smem() { return PAIR_STAGES * PAIR_STAGE + 1024 + 512; }
+
+struct PairBars {
+  uint64_t full[PAIR_STAGES], empty[PAIR_STAGES], done[2], freed[2], drained;
+  uint32_t tmem, dead;
+};
+
+__device__ __forceinline__ void pair_tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(m), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_tma_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// Arrives on this barrier of both blocks when the products so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"(static_cast<uint16_t>(3))
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// One output of one row from its own operands alone.
+__device__ __noinline__ float proj_own_sum(const ProjectArgs& A, int tile, int t, int n) {
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(A.x) + t * A.ldx;
+  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(A.w) + n * A.ldw;
+  float s = 0.0f;
+  for (int k = 0; k < A.K; ++k) s = fmaf(proj_f32(x[k]), proj_f32(w[k]), s);
+  return s + proj_own_delta(A, tile, A.tile_rows, t, n);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mh,
+                const __grid_constant__ ProjectArgs A) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  PairBars* B = reinterpret_cast<PairBars*>(smem + PAIR_STAGES * PAIR_STAGE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool lead = rank == 0;
+  volatile uint32_t* dead = &B->dead;
+  const uint32_t bit = 0x08u;  // STRATA_DEVERR_TIMEOUT
+  constexpr uint32_t TMEM_COLS = 512;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < PAIR_STAGES; ++i) {
+      mbar_init(&B->full[i], 1);
+      mbar_init(&B->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->done[i], 1);
+      mbar_init(&B->freed[i], 8);  // the first block's: four warps of each
+    }
+    mbar_init(&B->drained, 1);
+    B->dead = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B->tmem)), "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem;
+
+  const int rows_max = A.tile_rows, half = rows_max / 2;
+  const int k_stages = (A.K + 63) / 64;
+  const int blocks = A.S > 0 ? A.R / A.rank_block : 0, per_stage = A.S > 0 ? 64 / A.rank_block : 1;
+  const uint32_t line = static_cast<uint32_t>(A.rank_block) * 2;
+  const int tiles = A.n_tiles * A.t_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
+  auto list_of = [&](int t_tile) { return A.lists + static_cast<int64_t>(t_tile) * (rows_max + 1); };
+  auto wait_inner = [&]() {
+    if (A.S > 0) grid_dep_wait();
+  };
+
+  if (warp == 0 && lane == 0) {
+    uint32_t it = 0;
+    bool alive = true, waited = false;
+    for (int tile = first; tile < tiles && alive; tile += step) {
+      const int n0 = (tile / A.t_tiles * 2 + rank) * PROJ_M, t_tile = tile % A.t_tiles, t0 = t_tile * rows_max + rank * half;
+      int to = k_stages, subs = 0;
+      for (int s = 0; alive; ++s, ++it) {
+        if (s == k_stages && A.S > 0) {
+          if (!waited) wait_inner(), waited = true;
+          subs = (list_of(t_tile)[0] & LIST_COUNT) * blocks;
+          to = k_stages + (subs + per_stage - 1) / per_stage;
+        }
+        if (s >= to) break;
+        const uint32_t slot = it % PAIR_STAGES;
+        if (it >= PAIR_STAGES && !proj_wait(&B->empty[slot], (it / PAIR_STAGES + 1) & 1, dead, A.errors, bit)) {
+          alive = false;
+          break;
+        }
+        const uint32_t at = smem_u32(smem + slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[slot]), 0);
+        if (s < k_stages) {
+          if (lead) mbar_arrive_expect_tx(&B->full[slot], static_cast<uint32_t>(2 * (PROJ_M + half) * PROJ_LINE));
+          pair_tma_2d(at, &mw, s * 64, n0, bar);
+          pair_tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * 64, t0, bar);
+        } else {
+          const int sub0 = (s - k_stages) * per_stage, n = min(per_stage, subs - sub0);
+          if (lead) mbar_arrive_expect_tx(&B->full[slot], static_cast<uint32_t>(2 * n * (PROJ_M + half)) * line);
+          for (int i = 0; i < n; ++i) {
+            const int j = (sub0 + i) / blocks, rb = (sub0 + i) % blocks;
+            pair_tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, list_of(t_tile)[1 + j], bar);
+            pair_tma_2d(at + PROJ_M * PROJ_LINE + i * half * line, &mh, rb * A.rank_block,
+                        (t_tile * A.most + j) * rows_max + rank * half, bar);
+          }
+        }
+      }
+    }
+    if (!alive && lead) {
+      const uint32_t left = it < PAIR_STAGES ? it : PAIR_STAGES;
+      for (uint32_t i = it - left; i < it; ++i)
+        for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->full[i % PAIR_STAGES], (i / PAIR_STAGES) & 1); ++spin) {
+        }
+    }
+  } else if (warp == 1 && lane == 0 && lead) {
+    // 256 outputs: M counts in sixteens
+    const uint32_t idesc = (mma_idesc(false, rows_max) & 0x00FFFFFFu) | (16u << 24);
+    uint32_t it = 0, turn = 0;
+    bool alive = true, waited = false;
+    for (int tile = first; tile < tiles && alive; tile += step, ++turn) {
+      const int t_tile = tile % A.t_tiles;
+      const uint32_t buf = turn & 1, sum = tmem + buf * 256;
+      if (turn >= 2 && !proj_wait(&B->freed[buf], (turn / 2 + 1) & 1, dead, A.errors, bit)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      int to = k_stages, subs = 0;
+      bool add = false;
+      for (int s = 0; alive; ++s, ++it) {
+        if (s == k_stages && A.S > 0) {
+          if (!waited) wait_inner(), waited = true;
+          subs = (list_of(t_tile)[0] & LIST_COUNT) * blocks;
+          to = k_stages + (subs + per_stage - 1) / per_stage;
+        }
+        if (s >= to) break;
+        const uint32_t slot = it % PAIR_STAGES;
+        if (!proj_wait(&B->full[slot], (it / PAIR_STAGES) & 1, dead, A.errors, bit)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = smem_u32(smem + slot * PAIR_STAGE);
+        if (s < k_stages) {
+          const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + PROJ_M * PROJ_LINE, PROJ_LINE);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            pair_mma(sum, da + 2 * i, db + 2 * i, idesc, add);
+            add = true;
+          }
+        } else {
+          const int n = min(per_stage, subs - (s - k_stages) * per_stage);
+          for (int i = 0; i < n; ++i) {
+            const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
+            const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * half * line, line);
+            for (int q = 0; q < A.rank_block / 16; ++q) pair_mma(sum, da + 2 * q, db + 2 * q, idesc, true);
+          }
+        }
+        pair_commit(&B->empty[slot]);
+      }
+      if (alive) pair_commit(&B->done[buf]);
+    }
+    if (!alive) {
+      pair_commit(&B->drained);
+      for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->drained, 0); ++spin) {
+      }
+    }
+  } else if (warp >= 2) {
+    const uint32_t quarter = warp & 3;
+    uint32_t turn = 0;
+    wait_inner();
+    for (int tile = first; tile < tiles; tile += step, ++turn) {
+      const int t_tile = tile % A.t_tiles, t0 = t_tile * rows_max;
+      const int n = (tile / A.t_tiles * 2 + rank) * PROJ_M + quarter * 32 + lane;
+      const uint32_t buf = turn & 1;
+      const bool mixed = A.S > 0 && (list_of(t_tile)[0] & LIST_MIXED) != 0;
+      const bool ok = proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      const uint32_t sum = tmem + buf * 256 + (quarter << 21);
+      const int rows = min(rows_max, A.T - t0);
+#pragma unroll 1
+      for (int c = 0; c < rows; c += 32) {  // the last columns of a buffer's 256 may be stale: they are not used
+        float v[32];
+        tmem_ld32(sum + c, v);
+        tmem_wait_ld();
+        if (n < A.N) {
+          __nv_bfloat16* y = A.y + (t0 + c) * A.ldy + n;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (c + i < rows) {
+              if (mixed && !(fabsf(v[i]) < __int_as_float(0x7F800000))) v[i] = proj_own_sum(A, t_tile, t0 + c + i, n);
+              y[i * A.ldy] = __float2bfloat16_rn(v[i]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(dsmem_addr(smem_u32(&B->freed[buf]), 0));
+    }
+  }
+  __syncthreads();
+  cluster_arrive();  // neither block's shared or tensor memory is given back while the other's products use it
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
   }
 }
 

@@ -196,6 +196,43 @@ def test_project_whole_prompts(G, T):
     check_project(s, G.project_rows(**s))
 
 
+@pytest.mark.parametrize("T,N,K,S,R", [(2100, 4100, 1096, 5, 64), (1027, 8200, 520, 300, 16), (3000, 2304, 2048, 2, 48),
+                                       (600, 20000, 264, 9, 128), (4099, 1281, 160, 1, 32)])
+def test_project_many_rows(G, T, N, K, S, R):
+    """Calls that take the tiles of two SMs: adapters at random, in runs, and none."""
+    s = project_case(T, N, K, S, R, "bf16", T)
+    check_project(s, G.project_rows(**s))
+    runs = project_case(T, N, K, S, R, "bf16", T, of=[(i * 7 // T) % (S + 1) - 1 for i in range(T)])
+    check_project(runs, G.project_rows(**runs))
+    bare = {k: v for k, v in s.items() if k in ("x", "w", "x_scale", "w_scale")}
+    check_project(bare, G.project_rows(**bare))
+    assert G.tail_errors() == 0
+
+
+def test_project_many_rows_with_a_broken_adapter(G):
+    """NaN and infinities in one adapter of a tile: the other rows stay right (their sums may be taken again, in
+    another order), its own are not finite where the formula says so."""
+    T, N, K, S, R = 1500, 3000, 128, 3, 16
+    of = [(0, 1, 2, -1)[i % 4] if i < 700 else 2 for i in range(T)]
+    s = project_case(T, N, K, S, R, "bf16", 1, of=of)
+    b = s["b"].clone()
+    b[1, 3, 5], b[1, 1300, 0], b[1, 2999, 15] = math.inf, math.nan, -math.inf
+    broken = G.project_rows(**dict(s, b=b))
+    mine = torch.tensor(of, device="cuda") == 1
+    hit = torch.zeros(N, dtype=torch.bool, device="cuda")
+    hit[[3, 1300, 2999]] = True
+    assert (~broken[mine][:, hit].isfinite()).all()
+    fixed = broken.clone()
+    fixed[mine.nonzero(), hit.nonzero().T] = G.project_rows(**s)[mine.nonzero(), hit.nonzero().T]
+    check_project(s, fixed)
+    x = s["x"].clone()
+    x[2, 9] = math.nan
+    broken = G.project_rows(**dict(s, x=x))
+    rest = torch.arange(T, device="cuda") != 2
+    assert broken[2].isnan().all() and torch.equal(broken[rest], G.project_rows(**s)[rest])
+    assert G.tail_errors() == 0
+
+
 def test_project_strides(G):
     g = _gen(3)
     s = project_case(19, 333, 320, 3, 16, "bf16", 3)
