@@ -120,17 +120,47 @@ __device__ __forceinline__ float dsmem_ld_f32(uint32_t addr) {
 }
 
 // ------------------------------------------------------------------------------ bounded waits
-// A wait that runs out raises an error bit and `dead`, which ends every other wait of the block.
+// A wait of a whole warp.  One that runs out raises an error bit and `dead`, which ends every other wait of
+// the block.
 __device__ __forceinline__ bool proj_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* dead, uint32_t* errors,
                                           uint32_t bit) {
   for (uint32_t i = 0; i < PROJ_SPINS; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*dead != 0u) return false;
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xFFFFFFFFu, *dead != 0u)) return false;
   }
   *dead = 1u;
   atomicOr(errors, bit);
   return false;
 }
+// The stages' ring as one warp goes through it.
+template <int STAGES>
+struct Ring {
+  uint32_t slot = 0, phase = 0, begun = 0;
+  __device__ __forceinline__ void next() {
+    ++begun;
+    if (++slot == STAGES) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  // Waits until the copies of the newest stages have landed: no copy of a block may be in flight when it ends.
+  __device__ __forceinline__ void drain(uint64_t* full) {
+    for (uint32_t i = 0; i < STAGES && begun > 0; ++i, --begun) {
+      phase ^= slot == 0;
+      slot = slot == 0 ? STAGES - 1 : slot - 1;
+      for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&full[slot], phase); ++spin) {
+      }
+    }
+  }
+};
+// One lane of a warp, known to the compiler as such: the loops that issue copies and products are run by whole
+// warps with their state in uniform registers, where a lone thread's 100 instructions a stage took 350 ns.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
 
 // ------------------------------------------------------------------------------ the inner rows
 __device__ __forceinline__ float proj_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -234,7 +264,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   InnerBars* B = reinterpret_cast<InnerBars*>(smem + STAGES * STAGE);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows_max = A.tile_rows;
+  const int warp = warp_index(), lane = threadIdx.x & 31, rows_max = A.tile_rows;
   const uint32_t rank = cluster_ctarank();
   const int unit = blockIdx.x / INNER_SPLIT, tile = unit / groups, first = unit % groups;
   volatile uint32_t* dead = &B->dead;
@@ -286,10 +316,11 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   const int from = static_cast<int>(static_cast<int64_t>(k_stages) * rank / INNER_SPLIT);
   const int to = static_cast<int>(static_cast<int64_t>(k_stages) * (rank + 1) / INNER_SPLIT);
   uint32_t begun = 0, turn = 0;  // stages before this group
+  Ring<STAGES> ring;             // of the loading and of the issuing warp
 
   for (int q0 = first * PROJ_M; q0 < stack; q0 += groups * PROJ_M, begun += to - from, ++turn) {
     const int mine = min(PROJ_M, stack - q0);
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       const int boxes = (mine + box_rows - 1) / box_rows;
       int at_row[PROJ_M / 16];
       for (int i = 0; i < boxes; ++i) {
@@ -297,57 +328,49 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         at_row[i] = adapter(q / A.R) * A.R + q % A.R;
       }
       const uint32_t bytes = static_cast<uint32_t>(boxes * box_rows * PROJ_LINE + rows_max * (F8 ? 64 : PROJ_LINE));
-      bool alive = *dead == 0u;
-      uint32_t it = begun;
-      for (int s = from; s < to && alive; ++s, ++it) {
-        const uint32_t slot = it % STAGES;
-        if (it >= STAGES && !proj_wait(&B->empty[slot], (it / STAGES + 1) & 1, dead, A.errors, bit)) {
+      bool alive = true;
+      for (int s = from; s < to; ++s, ring.next()) {
+        if (ring.begun >= STAGES && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) {
           alive = false;
           break;
         }
-        const uint32_t at = smem_u32(smem + slot * STAGE), bar = smem_u32(&B->full[slot]);
-        mbar_arrive_expect_tx(&B->full[slot], bytes);
-        for (int i = 0; i < boxes; ++i) tma_2d(at + i * box_rows * PROJ_LINE, &ma, s * 64, at_row[i], bar);
-        tma_2d(at + (F8 ? RAW : X), &mx, s * 64, t0, bar);
+        const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&B->full[ring.slot], bytes);
+          for (int i = 0; i < boxes; ++i) tma_2d(at + i * box_rows * PROJ_LINE, &ma, s * 64, at_row[i], bar);
+          tma_2d(at + (F8 ? RAW : X), &mx, s * 64, t0, bar);
+        }
       }
-      if (!alive)
-        for (uint32_t i = it - min(it, static_cast<uint32_t>(STAGES)); i < it; ++i)
-          for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->full[i % STAGES], (i / STAGES) & 1); ++spin) {
-          }
-    } else if (warp == 1 && lane == 0) {
-      bool alive = *dead == 0u, add = false;
-      uint32_t it = begun;
+      if (!alive) ring.drain(B->full);
+    } else if (warp == 1) {
+      bool alive = true, add = false;
       const uint32_t idesc = mma_idesc(false, rows_max);
-      for (int s = from; s < to && alive; ++s, ++it) {
-        const uint32_t slot = it % STAGES;
-        if (!proj_wait(&B->full[slot], (it / STAGES) & 1, dead, A.errors, bit) ||
-            (F8 && !proj_wait(&B->wide[slot], (it / STAGES) & 1, dead, A.errors, bit))) {
+      for (int s = from; s < to; ++s, ring.next()) {
+        if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit) ||
+            (F8 && !proj_wait(&B->wide[ring.slot], ring.phase, dead, A.errors, bit))) {
           alive = false;
           break;
         }
         tc_fence_after();
-        const uint32_t at = smem_u32(smem + slot * STAGE);
+        const uint32_t at = smem_u32(smem + ring.slot * STAGE);
         const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + X, PROJ_LINE);
+        if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mma<false>(tmem, da + 2 * i, db + 2 * i, idesc, add);
-          add = true;
+          for (int i = 0; i < 4; ++i) mma<false>(tmem, da + 2 * i, db + 2 * i, idesc, add || i > 0);
+          mma_commit(&B->empty[ring.slot]);
         }
-        mma_commit(&B->empty[slot]);
+        add = true;
       }
-      if (alive) {
-        mma_commit(&B->done);
-      } else {
-        mma_commit(&B->drained);
+      if (elect_one()) mma_commit(alive ? &B->done : &B->drained);
+      if (!alive)
         for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->drained, 0); ++spin) {
         }
-      }
     } else if (warp >= 2) {
       if constexpr (F8) {
         uint32_t it = begun;
         for (int s = from; s < to; ++s, ++it) {
           const uint32_t slot = it % STAGES;
-          if (!__all_sync(0xFFFFFFFFu, proj_wait(&B->full[slot], (it / STAGES) & 1, dead, A.errors, bit))) break;
+          if (!proj_wait(&B->full[slot], (it / STAGES) & 1, dead, A.errors, bit)) break;
           uint8_t* stage = smem + slot * STAGE;
           for (int r = threadIdx.x - 64; r < rows_max; r += 128) {
             const uint4* in = reinterpret_cast<const uint4*>(stage + RAW + r * 64);
@@ -373,7 +396,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
       }
       const uint32_t quarter = warp & 3;
       const bool ok = proj_wait(&B->done, turn & 1, dead, A.errors, bit);
-      if (__all_sync(0xFFFFFFFFu, ok)) {
+      if (ok) {
         tc_fence_after();
         float* sums = reinterpret_cast<float*>(smem);  // [row][product]: every stage is free by now
 #pragma unroll 1
@@ -464,7 +487,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   ProjBars<BN>* B = reinterpret_cast<ProjBars<BN>*>(smem + STAGES * STAGE);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   volatile uint32_t* dead = &B->dead;
   const uint32_t bit = 0x08u;  // STRATA_DEVERR_TIMEOUT
 
@@ -519,9 +542,13 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   };
   if constexpr (SPLIT) wait_shrink();
 
-  if (warp == 0 && lane == 0) {
-    uint32_t it = 0;
+  if (warp == 0) {
+    Ring<STAGES> ring;
     bool alive = true, waited = SPLIT;
+    auto room = [&]() {  // in the next stage
+      if (ring.begun >= STAGES && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) alive = false;
+      return alive;
+    };
     for (int tile = first; tile < tiles && alive; tile += step) {
       const int n0 = tile / A.t_tiles * PROJ_M, t_tile = tile % A.t_tiles;
       int from = 0, to = k_stages, subs = 0;
@@ -529,44 +556,44 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         subs = adapters_of(t_tile) * blocks;
         share(k_stages + (subs + per_stage - 1) / per_stage, from, to);
       }
-      for (int s = from; alive; ++s, ++it) {
-        if (!SPLIT && s == k_stages) {  // now what the adapters add
-          if (!waited) wait_shrink(), waited = true;
-          subs = adapters_of(t_tile) * blocks;
-          to = k_stages + (subs + per_stage - 1) / per_stage;
-        }
-        if (s >= to) break;
-        const uint32_t slot = it % STAGES;
-        if (it >= STAGES && !proj_wait(&B->empty[slot], (it / STAGES + 1) & 1, dead, A.errors, bit)) {
-          alive = false;
-          break;
-        }
-        const uint32_t at = smem_u32(smem + slot * STAGE), bar = smem_u32(&B->full[slot]);
-        if (s < k_stages) {
-          mbar_arrive_expect_tx(&B->full[slot], STAGE);
+      for (int s = from; s < min(to, k_stages) && room(); ++s, ring.next()) {
+        const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&B->full[ring.slot], STAGE);
           tma_2d(at, &mw, s * ELEMS, n0, bar);
           tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * ELEMS, t_tile * BN, bar);
-        } else {
-          const int sub0 = (s - k_stages) * per_stage, n = min(per_stage, subs - sub0);
-          mbar_arrive_expect_tx(&B->full[slot], static_cast<uint32_t>(n) * (PROJ_M + BN) * line);
+        }
+      }
+      if (A.S == 0) continue;
+      if constexpr (!SPLIT) {  // now what the adapters add
+        if (!waited) wait_shrink(), waited = true;
+        subs = adapters_of(t_tile) * blocks;
+        to = k_stages + (subs + per_stage - 1) / per_stage;
+      }
+      const int32_t* ids = A.lists + static_cast<int64_t>(t_tile) * (BN + 1) + 1;
+      for (int s = max(from, k_stages); s < to && room(); ++s, ring.next()) {
+        const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
+        const int sub0 = (s - k_stages) * per_stage, n = min(per_stage, subs - sub0);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(n) * (PROJ_M + BN) * line);
           for (int i = 0; i < n; ++i) {
             const int j = (sub0 + i) / blocks, rb = (sub0 + i) % blocks;
-            const int c = A.lists[static_cast<int64_t>(t_tile) * (BN + 1) + 1 + j];
-            tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, c, bar);
+            tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, ids[j], bar);
             tma_2d(at + PROJ_M * PROJ_LINE + i * BN * line, &mh, rb * A.rank_block, (t_tile * A.most + j) * BN, bar);
           }
         }
       }
     }
-    if (!alive) {  // a wait ran out: no copy of this block may be in flight when it ends
-      const uint32_t begun = it, left = begun < STAGES ? begun : STAGES;
-      for (uint32_t i = begun - left; i < begun; ++i)
-        for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->full[i % STAGES], (i / STAGES) & 1); ++spin) {
-        }
-    }
-  } else if (warp == 1 && lane == 0) {
-    uint32_t it = 0, turn = 0;
+    if (!alive) ring.drain(B->full);
+  } else if (warp == 1) {
+    Ring<STAGES> ring;
+    uint32_t turn = 0;
     bool alive = true, waited = SPLIT;
+    auto landed = [&]() {  // the next stage
+      if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit)) alive = false;
+      tc_fence_after();
+      return alive;
+    };
     for (int tile = first; tile < tiles && alive; tile += step, ++turn) {
       const int t_tile = tile % A.t_tiles;
       const uint32_t buf = turn & 1, base = tmem + buf * 2 * BN, delta = base + BN;
@@ -580,45 +607,42 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         subs = adapters_of(t_tile) * blocks;
         share(k_stages + (subs + per_stage - 1) / per_stage, from, to);
       }
-      bool add_base = false, add_delta = false;
-      for (int s = from; alive; ++s, ++it) {
-        if (!SPLIT && s == k_stages) {
+      for (int s = from; s < min(to, k_stages) && landed(); ++s, ring.next()) {
+        const uint32_t at = smem_u32(smem + ring.slot * STAGE);
+        const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + PROJ_M * PROJ_LINE, PROJ_LINE);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // 32 bytes of each row at a time
+            mma<F8>(base, da + 2 * i, db + 2 * i, mma_idesc(F8, BN), s > from || i > 0);
+          mma_commit(&B->empty[ring.slot]);
+        }
+      }
+      if (A.S > 0) {
+        if constexpr (!SPLIT) {
           if (!waited) wait_shrink(), waited = true;
           subs = adapters_of(t_tile) * blocks;
           to = k_stages + (subs + per_stage - 1) / per_stage;
         }
-        if (s >= to) break;
-        const uint32_t slot = it % STAGES;
-        if (!proj_wait(&B->full[slot], (it / STAGES) & 1, dead, A.errors, bit)) {
-          alive = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t at = smem_u32(smem + slot * STAGE);
-        if (s < k_stages) {
-          const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + PROJ_M * PROJ_LINE, PROJ_LINE);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // 32 bytes of each row at a time
-            mma<F8>(base, da + 2 * i, db + 2 * i, mma_idesc(F8, BN), add_base);
-            add_base = true;
-          }
-        } else {
+        bool add = false;
+        for (int s = max(from, k_stages); s < to && alive && landed(); ++s, ring.next()) {
+          const uint32_t at = smem_u32(smem + ring.slot * STAGE);
           const int n = min(per_stage, subs - (s - k_stages) * per_stage);
-          for (int i = 0; i < n; ++i) {
-            const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
-            const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * BN * line, line);
-            for (int q = 0; q < A.rank_block / 16; ++q) {
-              mma<false>(delta, da + 2 * q, db + 2 * q, mma_idesc(false, BN), add_delta);
-              add_delta = true;
+          if (elect_one()) {
+            for (int i = 0; i < n; ++i) {
+              const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
+              const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * BN * line, line);
+              for (int q = 0; q < A.rank_block / 16; ++q)
+                mma<false>(delta, da + 2 * q, db + 2 * q, mma_idesc(false, BN), add || i > 0 || q > 0);
             }
+            mma_commit(&B->empty[ring.slot]);
           }
+          add = true;
         }
-        mma_commit(&B->empty[slot]);
       }
-      if (alive) mma_commit(&B->done[buf]);
+      if (alive && elect_one()) mma_commit(&B->done[buf]);
     }
     if (!alive) {  // the products in flight end before the block gives its tensor memory back
-      mma_commit(&B->drained);
+      if (elect_one()) mma_commit(&B->drained);
       for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->drained, 0); ++spin) {
       }
     }
@@ -631,7 +655,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
       const uint32_t buf = turn & 1;
       const int adapters = adapters_of(t_tile);
       const bool ok = proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (!ok) break;
       tc_fence_after();
       const uint32_t base = tmem + buf * 2 * BN + (quarter << 21);
       const int rows = min(BN, A.T - t0);
@@ -779,7 +803,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   PairBars* B = reinterpret_cast<PairBars*>(smem + PAIR_STAGES * PAIR_STAGE);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool lead = rank == 0;
   volatile uint32_t* dead = &B->dead;
@@ -822,52 +846,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
     if (A.S > 0) grid_dep_wait();
   };
 
-  if (warp == 0 && lane == 0) {
-    uint32_t it = 0;
+  if (warp == 0) {
+    Ring<PAIR_STAGES> ring;
     bool alive = true, waited = false;
+    auto room = [&]() {  // in the next stage
+      if (ring.begun >= PAIR_STAGES && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) alive = false;
+      return alive;
+    };
     for (int tile = first; tile < tiles && alive; tile += step) {
       const int n0 = (tile / A.t_tiles * 2 + rank) * PROJ_M, t_tile = tile % A.t_tiles, t0 = t_tile * rows_max + rank * half;
-      int to = k_stages, subs = 0;
-      for (int s = 0; alive; ++s, ++it) {
-        if (s == k_stages && A.S > 0) {
-          if (!waited) wait_inner(), waited = true;
-          subs = (list_of(t_tile)[0] & LIST_COUNT) * blocks;
-          to = k_stages + (subs + per_stage - 1) / per_stage;
-        }
-        if (s >= to) break;
-        const uint32_t slot = it % PAIR_STAGES;
-        if (it >= PAIR_STAGES && !proj_wait(&B->empty[slot], (it / PAIR_STAGES + 1) & 1, dead, A.errors, bit)) {
-          alive = false;
-          break;
-        }
-        const uint32_t at = smem_u32(smem + slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[slot]), 0);
-        if (s < k_stages) {
-          if (lead) mbar_arrive_expect_tx(&B->full[slot], static_cast<uint32_t>(2 * (PROJ_M + half) * PROJ_LINE));
+      for (int s = 0; s < k_stages && room(); ++s, ring.next()) {
+        const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
+        if (elect_one()) {
+          if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(2 * (PROJ_M + half) * PROJ_LINE));
           pair_tma_2d(at, &mw, s * 64, n0, bar);
           pair_tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * 64, t0, bar);
-        } else {
-          const int sub0 = (s - k_stages) * per_stage, n = min(per_stage, subs - sub0);
-          if (lead) mbar_arrive_expect_tx(&B->full[slot], static_cast<uint32_t>(2 * n * (PROJ_M + half)) * line);
+        }
+      }
+      if (A.S == 0) continue;
+      if (!waited) wait_inner(), waited = true;
+      const int32_t* list = list_of(t_tile);
+      const int subs = (list[0] & LIST_COUNT) * blocks;
+      for (int sub0 = 0; sub0 < subs && alive && room(); sub0 += per_stage, ring.next()) {
+        const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
+        const int n = min(per_stage, subs - sub0);
+        if (elect_one()) {
+          if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(2 * n * (PROJ_M + half)) * line);
           for (int i = 0; i < n; ++i) {
             const int j = (sub0 + i) / blocks, rb = (sub0 + i) % blocks;
-            pair_tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, list_of(t_tile)[1 + j], bar);
+            pair_tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, list[1 + j], bar);
             pair_tma_2d(at + PROJ_M * PROJ_LINE + i * half * line, &mh, rb * A.rank_block,
                         (t_tile * A.most + j) * rows_max + rank * half, bar);
           }
         }
       }
     }
-    if (!alive && lead) {
-      const uint32_t left = it < PAIR_STAGES ? it : PAIR_STAGES;
-      for (uint32_t i = it - left; i < it; ++i)
-        for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->full[i % PAIR_STAGES], (i / PAIR_STAGES) & 1); ++spin) {
-        }
-    }
-  } else if (warp == 1 && lane == 0 && lead) {
+    if (!alive && lead) ring.drain(B->full);
+  } else if (warp == 1 && lead) {
     // 256 outputs: M counts in sixteens
     const uint32_t idesc = (mma_idesc(false, rows_max) & 0x00FFFFFFu) | (16u << 24);
-    uint32_t it = 0, turn = 0;
+    Ring<PAIR_STAGES> ring;
+    uint32_t turn = 0;
     bool alive = true, waited = false;
+    auto landed = [&]() {  // the next stage
+      if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit)) alive = false;
+      tc_fence_after();
+      return alive;
+    };
     for (int tile = first; tile < tiles && alive; tile += step, ++turn) {
       const int t_tile = tile % A.t_tiles;
       const uint32_t buf = turn & 1, sum = tmem + buf * 256;
@@ -876,43 +901,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
         break;
       }
       tc_fence_after();
-      int to = k_stages, subs = 0;
-      bool add = false;
-      for (int s = 0; alive; ++s, ++it) {
-        if (s == k_stages && A.S > 0) {
-          if (!waited) wait_inner(), waited = true;
-          subs = (list_of(t_tile)[0] & LIST_COUNT) * blocks;
-          to = k_stages + (subs + per_stage - 1) / per_stage;
-        }
-        if (s >= to) break;
-        const uint32_t slot = it % PAIR_STAGES;
-        if (!proj_wait(&B->full[slot], (it / PAIR_STAGES) & 1, dead, A.errors, bit)) {
-          alive = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t at = smem_u32(smem + slot * PAIR_STAGE);
-        if (s < k_stages) {
-          const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + PROJ_M * PROJ_LINE, PROJ_LINE);
+      for (int s = 0; s < k_stages && landed(); ++s, ring.next()) {
+        const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE);
+        const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + PROJ_M * PROJ_LINE, PROJ_LINE);
+        if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            pair_mma(sum, da + 2 * i, db + 2 * i, idesc, add);
-            add = true;
-          }
-        } else {
-          const int n = min(per_stage, subs - (s - k_stages) * per_stage);
-          for (int i = 0; i < n; ++i) {
-            const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
-            const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * half * line, line);
-            for (int q = 0; q < A.rank_block / 16; ++q) pair_mma(sum, da + 2 * q, db + 2 * q, idesc, true);
+          for (int i = 0; i < 4; ++i) pair_mma(sum, da + 2 * i, db + 2 * i, idesc, s > 0 || i > 0);
+          pair_commit(&B->empty[ring.slot]);
+        }
+      }
+      if (A.S > 0) {
+        if (!waited) wait_inner(), waited = true;
+        const int subs = (list_of(t_tile)[0] & LIST_COUNT) * blocks;
+        for (int sub0 = 0; sub0 < subs && alive && landed(); sub0 += per_stage, ring.next()) {
+          const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE);
+          const int n = min(per_stage, subs - sub0);
+          if (elect_one()) {
+            for (int i = 0; i < n; ++i) {
+              const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
+              const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * half * line, line);
+              for (int q = 0; q < A.rank_block / 16; ++q) pair_mma(sum, da + 2 * q, db + 2 * q, idesc, true);
+            }
+            pair_commit(&B->empty[ring.slot]);
           }
         }
-        pair_commit(&B->empty[slot]);
       }
-      if (alive) pair_commit(&B->done[buf]);
+      if (alive && elect_one()) pair_commit(&B->done[buf]);
     }
     if (!alive) {
-      pair_commit(&B->drained);
+      if (elect_one()) pair_commit(&B->drained);
       for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->drained, 0); ++spin) {
       }
     }
@@ -925,24 +942,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
       const int n = (tile / A.t_tiles * 2 + rank) * PROJ_M + quarter * 32 + lane;
       const uint32_t buf = turn & 1;
       const bool mixed = A.S > 0 && (list_of(t_tile)[0] & LIST_MIXED) != 0;
-      const bool ok = proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (!proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit)) break;
       tc_fence_after();
       const uint32_t sum = tmem + buf * 256 + (quarter << 21);
       const int rows = min(rows_max, A.T - t0);
+      __nv_bfloat16* y = A.y + t0 * A.ldy + n;
 #pragma unroll 1
       for (int c = 0; c < rows; c += 32) {  // the last columns of a buffer's 256 may be stale: they are not used
         float v[32];
         tmem_ld32(sum + c, v);
         tmem_wait_ld();
-        if (n < A.N) {
-          __nv_bfloat16* y = A.y + (t0 + c) * A.ldy + n;
+        if (mixed) {
+          // a sum that is not finite is taken again, from its row's own operands
+          uint32_t bad = 0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (c + i < rows) {
-              if (mixed && !(fabsf(v[i]) < __int_as_float(0x7F800000))) v[i] = proj_own_sum(A, t_tile, t0 + c + i, n);
-              y[i * A.ldy] = __float2bfloat16_rn(v[i]);
-            }
+          for (int i = 0; i < 32; ++i) bad |= fabsf(v[i]) < __int_as_float(0x7F800000) ? 0u : 1u << i;
+          if (n >= A.N) bad = 0;
+          if (rows - c < 32) bad &= (1u << (rows - c)) - 1u;
+          if (__any_sync(0xFFFFFFFFu, bad != 0)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (bad >> i & 1u) v[i] = proj_own_sum(A, t_tile, t0 + c + i, n);
+          }
+        }
+        if (n < A.N) {
+          if (rows - c >= 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i, y += A.ldy) *y = __float2bfloat16_rn(v[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i, y += A.ldy)
+              if (c + i < rows) *y = __float2bfloat16_rn(v[i]);
           }
         }
       }
