@@ -119,6 +119,12 @@ __device__ __forceinline__ float dsmem_ld_f32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float4 dsmem_ld_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // ------------------------------------------------------------------------------ bounded waits
 // A wait of a whole warp.  One that runs out raises an error bit and `dead`, which ends every other wait of
 // the block.
@@ -414,19 +420,35 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
     cluster_arrive();
     cluster_wait();
     if (*dead == 0u) {
-      // a thread's product is the same for all its rows: PROJ_M of the cluster's threads to a row
-      constexpr int GO = INNER_SPLIT * PROJ_THREADS / PROJ_M;
+      // four products of a row to a thread, the same four for all its rows; a row's sums of other adapters
+      // are not looked at
+      constexpr int FOURS = PROJ_M / 4, GO = INNER_SPLIT * PROJ_THREADS / FOURS;
       const uint32_t own = smem_u32(smem);
-      const int id = static_cast<int>(rank) * PROJ_THREADS + threadIdx.x, q = q0 + id % PROJ_M, j = q / A.R;
+      const int id = static_cast<int>(rank) * PROJ_THREADS + threadIdx.x, m = id % FOURS * 4, q = q0 + m, j = q / A.R;
       if (q < stack) {
         const int c = adapter(j);
         const float by = A.adapter_scale[c];
-        for (int t = id / PROJ_M; t < rows; t += GO) {
-          float v = 0.0f;
+        __nv_bfloat16* to_row = A.spread + (static_cast<int64_t>(tile) * A.most + j) * rows_max * A.R + q % A.R;
+        for (int t = id / FOURS; t < rows; t += GO) {
+          uint2 packed = make_uint2(0, 0);
+          if (A.row_adapter[t0 + t] == c) {
+            float4 v[INNER_SPLIT];
 #pragma unroll
-          for (uint32_t i = 0; i < INNER_SPLIT; ++i) v += dsmem_ld_f32(dsmem_addr(own, i) + (t * PROJ_M + id % PROJ_M) * 4);
-          v = A.row_adapter[t0 + t] == c ? by * ((A.x_scale != nullptr ? A.x_scale[t0 + t] : 1.0f) * v) : 0.0f;
-          A.spread[((static_cast<int64_t>(tile) * A.most + j) * rows_max + t) * A.R + q % A.R] = __float2bfloat16_rn(v);
+            for (uint32_t i = 0; i < INNER_SPLIT; ++i) v[i] = dsmem_ld_v4(dsmem_addr(own, i) + (t * PROJ_M + m) * 4);
+            float4 sum = v[0];
+#pragma unroll
+            for (uint32_t i = 1; i < INNER_SPLIT; ++i) {
+              sum.x += v[i].x;
+              sum.y += v[i].y;
+              sum.z += v[i].z;
+              sum.w += v[i].w;
+            }
+            const float sx = A.x_scale != nullptr ? A.x_scale[t0 + t] : 1.0f;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(by * (sx * sum.x), by * (sx * sum.y)),
+                                 hi = __floats2bfloat162_rn(by * (sx * sum.z), by * (sx * sum.w));
+            packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          }
+          *reinterpret_cast<uint2*>(to_row + t * A.R) = packed;
         }
       }
     }
