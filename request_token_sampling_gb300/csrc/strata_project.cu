@@ -110,18 +110,18 @@ int split_ranks(int64_t tiles, int k_stages, int sms) {
   return ranks;
 }
 
-// Rows of a tile of the pair kernel, or 0 where tiles on one SM take less time.  Both are bound by what an
-// SM takes in from L2, about 58 bytes a cycle (128 x 128 tiles on one SM ran at that: 840 TFLOP/s), or by
-// its tensor core, 4096 products a cycle: cycles of a 64-deep stage, times stages one after another.
-int pair_rows(int T, int N, int k_stages, int sms) {
+// Rows of a tile of the pair kernel, or 0 where tiles on one SM take less time.  A 64-deep stage of a pair's tile
+// of r rows was measured at about 1.02 (80 + r) ns (193 ns for 128 rows, 265 for 192, 342 for 256), one of 128 x 128 on
+// one SM at 220 ns: the cost of a choice is its tiles one after another on an SM times that.
+int pair_rows(int T, int N, int k_stages, bool adapters, int sms) {
   const int64_t n_pairs = (N + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M), n_tiles = (N + strata::PROJ_M - 1) / strata::PROJ_M;
   auto waves = [](int64_t tiles, int64_t at_once) { return (tiles + at_once - 1) / at_once; };
   const int64_t tiles = n_tiles * ((T + 127) / 128);
-  int64_t best = waves(tiles, sms) * (2 * strata::PROJ_M * strata::PROJ_LINE / 58) / split_ranks(tiles, k_stages, sms);
+  int64_t best = waves(tiles, sms) * 215 / split_ranks(tiles, k_stages, sms);
   int rows = 0;
   for (int r = 256; r >= 64; r -= 16) {
-    const int64_t stage = std::max<int64_t>((strata::PROJ_M + r / 2) * strata::PROJ_LINE / 58, 2 * r);
-    const int64_t cost = waves(n_pairs * ((T + r - 1) / r), sms / 2) * stage;
+    const int64_t t_tiles = (T + r - 1) / r;
+    const int64_t cost = waves(n_pairs * t_tiles + (adapters ? t_tiles : 0), sms / 2) * (80 + r);  // mostly one unit a tile of rows
     if (cost < best) {
       best = cost;
       rows = r;
@@ -140,7 +140,8 @@ int current_device(const Device** dev) {
   return (*dev)->status == cudaSuccess ? STRATA_OK : cuda_fail((*dev)->status, "device setup");
 }
 
-int64_t lists_bytes(int t_tiles, int bn) { return (static_cast<int64_t>(t_tiles) * (bn + 1) * 4 + 255) / 256 * 256; }
+// The lists and the words beside them.
+int64_t lists_bytes(int t_tiles, int bn) { return (static_cast<int64_t>(t_tiles) * (bn + 2) * 4 + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -197,7 +198,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
 
   const cuuint32_t elems = f8 ? 128 : 64;
   const int k_stages = (K + static_cast<int>(elems) - 1) / static_cast<int>(elems);
-  const int pair = T > 128 && !f8 ? pair_rows(T, N, k_stages, dev.sms) : 0;  // tiles of two SMs
+  const int pair = T > 128 && !f8 ? pair_rows(T, N, k_stages, S > 0, dev.sms) : 0;  // tiles of two SMs
   const int bn = pair > 0 ? pair : tile_rows(T), t_tiles = (T + bn - 1) / bn;
   const int n_tiles = pair > 0 ? (N + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M) : (N + strata::PROJ_M - 1) / strata::PROJ_M;
   const int64_t tiles = static_cast<int64_t>(t_tiles) * n_tiles;
@@ -213,6 +214,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   A.row_adapter = row_adapter;
   A.y = static_cast<__nv_bfloat16*>(y);
   A.lists = static_cast<int32_t*>(workspace);
+  A.ready = static_cast<uint32_t*>(workspace) + static_cast<int64_t>(t_tiles) * (bn + 1);
   A.spread = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + lists_bytes(t_tiles, bn));
   A.errors = dev.errors;
   A.ldx = ldx;
@@ -230,7 +232,8 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   A.w = w;
   A.ldw = ldw;
 
-  CUtensorMap mw, mx, mb{}, mh{};
+  CUtensorMap mw, mx, mb{}, mh{}, ma{};
+  const int box_rows = R % 128 == 0 ? 128 : R % 64 == 0 ? 64 : R % 32 == 0 ? 32 : 16;  // of a, in one copy
   {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldw * esz)};
@@ -254,23 +257,27 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
     const cuuint32_t hbox[2] = {static_cast<cuuint32_t>(A.rank_block), static_cast<cuuint32_t>(pair > 0 ? bn / 2 : bn)};
     if (!encode(dev.encode, &mh, false, 2, A.spread, hdims, strides, hbox, A.rank_block * 2))
       return host_fail(STRATA_EINVAL, "the workspace cannot be mapped");
+    auto map_a = [&]() {
+      const cuuint64_t adims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(S) * R};
+      const cuuint64_t astrides[1] = {static_cast<cuuint64_t>(K) * 2};
+      const cuuint32_t abox[2] = {64, static_cast<cuuint32_t>(box_rows)};
+      return encode(dev.encode, &ma, false, 2, a, adims, astrides, abox, 128);
+    };
     if (T <= SHRINK_ROWS) {
       const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(R / 8));
       if (f8)
         strata::shrink_kernel<__nv_fp8_e4m3><<<grid, 256, 0, s>>>(A, bn);
       else
         strata::shrink_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(A, bn);
+    } else if (pair > 0) {
+      if (!map_a()) return host_fail(STRATA_EINVAL, "a cannot be mapped");
+      strata::plan_kernel<<<static_cast<unsigned>(t_tiles), 256, 0, s>>>(A);
     } else {
-      CUtensorMap ma, mt;
-      const int box_rows = R % 128 == 0 ? 128 : R % 64 == 0 ? 64 : R % 32 == 0 ? 32 : 16;
-      const cuuint64_t adims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(S) * R};
-      const cuuint64_t astrides[1] = {static_cast<cuuint64_t>(K) * 2};
-      const cuuint32_t abox[2] = {64, static_cast<cuuint32_t>(box_rows)};
+      CUtensorMap mt;
       const cuuint64_t xdims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(T)};
       const cuuint64_t xstrides[1] = {static_cast<cuuint64_t>(ldx * esz)};
       const cuuint32_t xbox[2] = {64, static_cast<cuuint32_t>(bn)};
-      if (!encode(dev.encode, &ma, false, 2, a, adims, astrides, abox, 128) ||
-          !encode(dev.encode, &mt, f8, 2, x, xdims, xstrides, xbox, f8 ? 0 : 128))
+      if (!map_a() || !encode(dev.encode, &mt, f8, 2, x, xdims, xstrides, xbox, f8 ? 0 : 128))
         return host_fail(STRATA_EINVAL, "a or x cannot be mapped");
       // clusters of a tile: one where the tiles fill the GPU, as many as there can be work for where they do not
       const int groups = std::min((most * R + strata::PROJ_M - 1) / strata::PROJ_M,
@@ -293,8 +300,9 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   }
   const int ranks = pair > 0 ? 1 : split_ranks(tiles, k_stages, dev.sms);
   cudaLaunchConfig_t cfg = {};
+  const int64_t units = S > 0 ? static_cast<int64_t>(t_tiles) * ((most * R + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M)) : 0;
   if (pair > 0)
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, dev.sms / 2)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles + units, dev.sms / 2)), 1, 1);
   else
     cfg.gridDim = dim3(static_cast<unsigned>(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, dev.sms)), 1, 1);
   cfg.blockDim = dim3(strata::PROJ_THREADS, 1, 1);
@@ -315,7 +323,8 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   }
   cfg.attrs = attrs;
   cfg.numAttrs = na;
-  e = cudaLaunchKernelEx(&cfg, pair > 0 ? strata::pair_kernel : kernel_for(bn, f8, ranks > 1), mw, mx, mb, mh, A);
+  e = pair > 0 ? cudaLaunchKernelEx(&cfg, strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows)
+               : cudaLaunchKernelEx(&cfg, kernel_for(bn, f8, ranks > 1), mw, mx, mb, mh, A);
   return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_project_rows");
 }
 

@@ -31,6 +31,7 @@ struct ProjectArgs {
   __nv_bfloat16* y;
   __nv_bfloat16* spread;  // [tiles][most][tile rows][R]
   int32_t* lists;         // per tile: how many adapters, then their ids in ascending order ([1 + tile rows])
+  uint32_t* ready;        // per tile: warps that have written their part of its inner rows (pair_kernel)
   uint32_t* errors;
   int64_t ldx, ldy;
   int T, N, K, S, R;
@@ -480,7 +481,7 @@ __device__ __noinline__ float proj_own_delta(const ProjectArgs& A, int tile, int
   const __nv_bfloat16* h = A.spread + ((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - tile * tile_rows)) * A.R;
   const __nv_bfloat16* b = A.b + (static_cast<int64_t>(c) * A.N + n) * A.R;
   float d = 0.0f;
-  for (int r = 0; r < A.R; ++r) d = fmaf(proj_f32(h[r]), proj_f32(b[r]), d);
+  for (int r = 0; r < A.R; ++r) d = fmaf(proj_f32(__ldcg(h + r)), proj_f32(b[r]), d);
   return d;
 }
 
@@ -552,33 +553,29 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   auto adapters_of = [&](int t_tile) {
     return A.S > 0 ? *(A.lists + static_cast<int64_t>(t_tile) * (BN + 1)) & LIST_COUNT : 0;
   };
-  // the stages of a tile that this block takes: [from, to) of k_stages + ceil(sub-blocks / per_stage)
-  auto share = [&](int all, int& from, int& to) {
-    from = SPLIT ? static_cast<int>(static_cast<int64_t>(all) * rank / ranks) : 0;
-    to = SPLIT ? static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / ranks) : all;
+  // what a block takes of `all` stages: of the base's and, on its own, of the adapters' (whose number is known
+  // only when the previous kernel is done: `lists` and `spread` are its outputs)
+  auto share = [&](int all, uint32_t of, int& from, int& to) {
+    from = SPLIT ? static_cast<int>(static_cast<int64_t>(all) * of / ranks) : 0;
+    to = SPLIT ? static_cast<int>(static_cast<int64_t>(all) * (of + 1) / ranks) : all;
   };
-  // `lists` and `spread` are the previous kernel's: wait for it before the first look at them.  A
-  // split tile's shares depend on how many adapters it has, so there everybody waits first.
+  auto stages_of = [&](int subs) { return (subs + per_stage - 1) / per_stage; };
   auto wait_shrink = [&]() {
     if (A.S > 0) grid_dep_wait();
   };
-  if constexpr (SPLIT) wait_shrink();
 
   if (warp == 0) {
     Ring<STAGES> ring;
-    bool alive = true, waited = SPLIT;
+    bool alive = true, waited = false;
     auto room = [&]() {  // in the next stage
       if (ring.begun >= STAGES && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) alive = false;
       return alive;
     };
     for (int tile = first; tile < tiles && alive; tile += step) {
       const int n0 = tile / A.t_tiles * PROJ_M, t_tile = tile % A.t_tiles;
-      int from = 0, to = k_stages, subs = 0;
-      if constexpr (SPLIT) {
-        subs = adapters_of(t_tile) * blocks;
-        share(k_stages + (subs + per_stage - 1) / per_stage, from, to);
-      }
-      for (int s = from; s < min(to, k_stages) && room(); ++s, ring.next()) {
+      int from, to;
+      share(k_stages, rank, from, to);
+      for (int s = from; s < to && room(); ++s, ring.next()) {
         const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
         if (elect_one()) {
           mbar_arrive_expect_tx(&B->full[ring.slot], STAGE);
@@ -586,16 +583,14 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
           tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * ELEMS, t_tile * BN, bar);
         }
       }
-      if (A.S == 0) continue;
-      if constexpr (!SPLIT) {  // now what the adapters add
-        if (!waited) wait_shrink(), waited = true;
-        subs = adapters_of(t_tile) * blocks;
-        to = k_stages + (subs + per_stage - 1) / per_stage;
-      }
+      if (A.S == 0 || !alive) continue;
+      if (!waited) wait_shrink(), waited = true;  // now what the adapters add
+      const int subs = adapters_of(t_tile) * blocks;
+      share(stages_of(subs), rank, from, to);
       const int32_t* ids = A.lists + static_cast<int64_t>(t_tile) * (BN + 1) + 1;
-      for (int s = max(from, k_stages); s < to && room(); ++s, ring.next()) {
+      for (int s = from; s < to && room(); ++s, ring.next()) {
         const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
-        const int sub0 = (s - k_stages) * per_stage, n = min(per_stage, subs - sub0);
+        const int sub0 = s * per_stage, n = min(per_stage, subs - sub0);
         if (elect_one()) {
           mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(n) * (PROJ_M + BN) * line);
           for (int i = 0; i < n; ++i) {
@@ -610,7 +605,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   } else if (warp == 1) {
     Ring<STAGES> ring;
     uint32_t turn = 0;
-    bool alive = true, waited = SPLIT;
+    bool alive = true, waited = false;
     auto landed = [&]() {  // the next stage
       if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit)) alive = false;
       tc_fence_after();
@@ -624,12 +619,9 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         break;
       }
       tc_fence_after();
-      int from = 0, to = k_stages, subs = 0;
-      if constexpr (SPLIT) {
-        subs = adapters_of(t_tile) * blocks;
-        share(k_stages + (subs + per_stage - 1) / per_stage, from, to);
-      }
-      for (int s = from; s < min(to, k_stages) && landed(); ++s, ring.next()) {
+      int from, to;
+      share(k_stages, rank, from, to);
+      for (int s = from; s < to && landed(); ++s, ring.next()) {
         const uint32_t at = smem_u32(smem + ring.slot * STAGE);
         const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + PROJ_M * PROJ_LINE, PROJ_LINE);
         if (elect_one()) {
@@ -639,16 +631,14 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
           mma_commit(&B->empty[ring.slot]);
         }
       }
-      if (A.S > 0) {
-        if constexpr (!SPLIT) {
-          if (!waited) wait_shrink(), waited = true;
-          subs = adapters_of(t_tile) * blocks;
-          to = k_stages + (subs + per_stage - 1) / per_stage;
-        }
+      if (A.S > 0 && alive) {
+        if (!waited) wait_shrink(), waited = true;
+        const int subs = adapters_of(t_tile) * blocks;
+        share(stages_of(subs), rank, from, to);
         bool add = false;
-        for (int s = max(from, k_stages); s < to && alive && landed(); ++s, ring.next()) {
+        for (int s = from; s < to && landed(); ++s, ring.next()) {
           const uint32_t at = smem_u32(smem + ring.slot * STAGE);
-          const int n = min(per_stage, subs - (s - k_stages) * per_stage);
+          const int n = min(per_stage, subs - s * per_stage);
           if (elect_one()) {
             for (int i = 0; i < n; ++i) {
               const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
@@ -671,7 +661,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   } else if (warp >= 2) {
     const uint32_t quarter = warp & 3;  // the 32 lanes of tensor memory that this warp may read
     uint32_t turn = 0;
-    if constexpr (!SPLIT) wait_shrink();
+    wait_shrink();
     for (int tile = first; tile < tiles; tile += step, ++turn) {
       const int t_tile = tile % A.t_tiles, t0 = t_tile * BN, n = tile / A.t_tiles * PROJ_M + quarter * 32 + lane;
       const uint32_t buf = turn & 1;
@@ -698,8 +688,10 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
       } else {
         // this block's sums to its own shared memory: [base, delta][row][output]
         int from, to;
-        share(k_stages + (adapters * blocks + per_stage - 1) / per_stage, from, to);
-        const bool has_base = from < k_stages && to > from, has_delta = to > k_stages && to > from;
+        share(k_stages, rank, from, to);
+        const bool has_base = to > from;
+        share(stages_of(adapters * blocks), rank, from, to);
+        const bool has_delta = to > from;
         float* mine = reinterpret_cast<float*>(smem);
 #pragma unroll 1
         for (int c = 0; c < rows; c += 16) {
@@ -710,7 +702,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             mine[(c + i) * PROJ_M + quarter * 32 + lane] = vb[i];
-            if (adapters > 0) mine[(BN + c + i) * PROJ_M + quarter * 32 + lane] = vd[i];
+            if (has_delta) mine[(BN + c + i) * PROJ_M + quarter * 32 + lane] = vd[i];
           }
         }
       }
@@ -726,17 +718,36 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
     if (*dead == 0u) {
       const int tile = first, t_tile = tile % A.t_tiles, t0 = t_tile * BN, n0 = tile / A.t_tiles * PROJ_M;
       const int rows = min(BN, A.T - t0), adapters = adapters_of(t_tile);
+      // four outputs of a row to a thread; delta lies with the ranks that had stages of it
+      constexpr int FOURS = PROJ_M / 4, MOST = 8;
       const uint32_t own = smem_u32(smem);
-      for (int e = rank * PROJ_THREADS + threadIdx.x; e < rows * PROJ_M; e += ranks * PROJ_THREADS) {
-        const int t = e / PROJ_M, n = n0 + e % PROJ_M;
-        if (n >= A.N) continue;
-        float vb = 0.0f, vd = 0.0f;
-        for (uint32_t q = 0; q < ranks; ++q) {
-          const uint32_t at = dsmem_addr(own, q);
-          vb += dsmem_ld_f32(at + e * 4);
-          if (adapters > 0) vd += dsmem_ld_f32(at + (BN * PROJ_M + e) * 4);
+      const int m = threadIdx.x % FOURS * 4, n = n0 + m, d_stages = stages_of(adapters * blocks);
+      const int outs = min(4, A.N - n);
+      float sw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sw[i] = F8 && i < outs ? A.w_scale[n + i] : 1.0f;
+      for (int t = (static_cast<int>(rank) * PROJ_THREADS + threadIdx.x) / FOURS; t < rows && outs > 0;
+           t += static_cast<int>(ranks) * PROJ_THREADS / FOURS) {
+        float4 vb[MOST], vd[MOST];
+#pragma unroll
+        for (uint32_t q = 0; q < MOST; ++q) {
+          vb[q] = vd[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (q >= ranks) continue;
+          const uint32_t at = dsmem_addr(own, q) + (t * PROJ_M + m) * 4;
+          vb[q] = dsmem_ld_v4(at);
+          int from, to;
+          share(d_stages, q, from, to);
+          if (to > from) vd[q] = dsmem_ld_v4(at + BN * PROJ_M * 4);
         }
-        proj_write<BN, F8>(A, t_tile, t0 + t, n, F8 ? A.w_scale[n] : 1.0f, vb, vd, adapters > 0);
+#pragma unroll
+        for (uint32_t q = 1; q < MOST; ++q) {
+          vb[0].x += vb[q].x, vb[0].y += vb[q].y, vb[0].z += vb[q].z, vb[0].w += vb[q].w;
+          vd[0].x += vd[q].x, vd[0].y += vd[q].y, vd[0].z += vd[q].z, vd[0].w += vd[q].w;
+        }
+        const float b4[4] = {vb[0].x, vb[0].y, vb[0].z, vb[0].w}, d4[4] = {vd[0].x, vd[0].y, vd[0].z, vd[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < outs) proj_write<BN, F8>(A, t_tile, t0 + t, n + i, sw[i], b4[i], d4[i], adapters > 0);
       }
     }
     cluster_arrive();
@@ -755,6 +766,9 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
 // where a tile of 128 x 128 on one SM would need 128.  base and delta are one accumulator here, and two
 // tiles have room in tensor memory: a tile is written while the next is summed.  What a broken adapter
 // spoils in other requests' rows is therefore found in the sum, and that sum is taken again.
+// The inner rows are tiles of the same kind, before all others: 256 of a tile's stacked products a unit, with
+// the matrices a in w's place.  A tile of outputs adds its adapters last, and waits before that until its
+// rows' units are done.  They are the lowest tiles, so they are taken first and wait for nothing.
 constexpr int PAIR_STAGES = 7, PAIR_STAGE = 2 * PROJ_M * PROJ_LINE;
 __host__ __device__ constexpr int pair_smem() { return PAIR_STAGES * PAIR_STAGE + 1024 + 512; }
 
@@ -818,10 +832,22 @@ __device__ __noinline__ float proj_own_sum(const ProjectArgs& A, int tile, int t
   return s + proj_own_delta(A, tile, A.tile_rows, t, n);
 }
 
+// The lists of a call's tiles; no unit is done.
+__global__ void __launch_bounds__(256) plan_kernel(const __grid_constant__ ProjectArgs A) {
+  __shared__ TileAdapters used;
+  grid_dep_launch();
+  const int tile = blockIdx.x, t0 = tile * A.tile_rows;
+  tile_adapters(A, t0, min(A.tile_rows, A.T - t0), &used);
+  if (threadIdx.x == 0) {
+    write_list(A, tile, A.tile_rows, used);
+    A.ready[tile] = 0;
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
     pair_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                 const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mh,
-                const __grid_constant__ ProjectArgs A) {
+                const __grid_constant__ CUtensorMap ma, const __grid_constant__ ProjectArgs A, int box_rows) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   PairBars* B = reinterpret_cast<PairBars*>(smem + PAIR_STAGES * PAIR_STAGE);
@@ -862,21 +888,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
   const int k_stages = (A.K + 63) / 64;
   const int blocks = A.S > 0 ? A.R / A.rank_block : 0, per_stage = A.S > 0 ? 64 / A.rank_block : 1;
   const uint32_t line = static_cast<uint32_t>(A.rank_block) * 2;
-  const int tiles = A.n_tiles * A.t_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
   auto list_of = [&](int t_tile) { return A.lists + static_cast<int64_t>(t_tile) * (rows_max + 1); };
-  auto wait_inner = [&]() {
-    if (A.S > 0) grid_dep_wait();
+  auto stack_of = [&](int t_tile) { return (list_of(t_tile)[0] & LIST_COUNT) * A.R; };  // inner products
+  auto units_of = [&](int t_tile) { return (stack_of(t_tile) + 2 * PROJ_M - 1) / (2 * PROJ_M); };
+  int units = 0;
+  if (A.S > 0) {
+    grid_dep_wait();
+    for (int t = lane; t < A.t_tiles; t += 32) units += units_of(t);
+    units = __reduce_add_sync(0xFFFFFFFFu, units);
+  }
+  const int tiles = units + A.n_tiles * A.t_tiles;
+  // The rows and, of a unit, the first inner product (else -1) of tile `tile`, asked for in ascending order.
+  struct Place {
+    int t_tile = 0, before = 0;
+  };
+  auto unit_of = [&](int tile, Place& at) {
+    if (tile >= units) {
+      at.t_tile = (tile - units) % A.t_tiles;
+      return -1;
+    }
+    for (int n; tile >= at.before + (n = units_of(at.t_tile)); ++at.t_tile) at.before += n;
+    return (tile - at.before) * 2 * PROJ_M;
   };
 
   if (warp == 0) {
     Ring<PAIR_STAGES> ring;
-    bool alive = true, waited = false;
+    bool alive = true;
+    Place place;
     auto room = [&]() {  // in the next stage
       if (ring.begun >= PAIR_STAGES && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) alive = false;
       return alive;
     };
     for (int tile = first; tile < tiles && alive; tile += step) {
-      const int n0 = (tile / A.t_tiles * 2 + rank) * PROJ_M, t_tile = tile % A.t_tiles, t0 = t_tile * rows_max + rank * half;
+      const int q0 = unit_of(tile, place), t_tile = place.t_tile, t0 = t_tile * rows_max + rank * half;
+      if (q0 >= 0) {
+        const int stack = stack_of(t_tile);
+        auto boxes_of = [&](int r) { return (max(0, min(PROJ_M, stack - q0 - r * PROJ_M)) + box_rows - 1) / box_rows; };
+        const int boxes = boxes_of(rank);
+        const uint32_t bytes = static_cast<uint32_t>(((boxes_of(0) + boxes_of(1)) * box_rows + rows_max) * PROJ_LINE);
+        for (int s = 0; s < k_stages && room(); ++s, ring.next()) {
+          const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
+          if (elect_one()) {
+            if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], bytes);
+            for (int i = 0; i < boxes; ++i) {
+              const int q = q0 + rank * PROJ_M + i * box_rows;
+              pair_tma_2d(at + i * box_rows * PROJ_LINE, &ma, s * 64, list_of(t_tile)[1 + q / A.R] * A.R + q % A.R, bar);
+            }
+            pair_tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * 64, t0, bar);
+          }
+        }
+        continue;
+      }
+      const int n0 = ((tile - units) / A.t_tiles * 2 + rank) * PROJ_M;
       for (int s = 0; s < k_stages && room(); ++s, ring.next()) {
         const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
         if (elect_one()) {
@@ -885,8 +949,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
           pair_tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * 64, t0, bar);
         }
       }
-      if (A.S == 0) continue;
-      if (!waited) wait_inner(), waited = true;
+      if (A.S == 0 || !alive) continue;
+      {  // its rows' units: eight warps of a pair write each
+        const uint32_t need = static_cast<uint32_t>(units_of(t_tile)) * 8;
+        uint32_t spin = 0, seen;
+        do {
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(A.ready + t_tile) : "memory");
+          if (!__any_sync(0xFFFFFFFFu, seen != need)) break;
+          if (__any_sync(0xFFFFFFFFu, *dead != 0u)) alive = false;
+        } while (alive && ++spin < PROJ_SPINS);
+        if (alive && spin >= PROJ_SPINS) {
+          *dead = 1u;
+          atomicOr(A.errors, bit);
+          alive = false;
+        }
+        asm volatile("fence.proxy.async;" ::: "memory");
+      }
       const int32_t* list = list_of(t_tile);
       const int subs = (list[0] & LIST_COUNT) * blocks;
       for (int sub0 = 0; sub0 < subs && alive && room(); sub0 += per_stage, ring.next()) {
@@ -909,14 +987,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
     const uint32_t idesc = (mma_idesc(false, rows_max) & 0x00FFFFFFu) | (16u << 24);
     Ring<PAIR_STAGES> ring;
     uint32_t turn = 0;
-    bool alive = true, waited = false;
+    bool alive = true;
+    Place place;
     auto landed = [&]() {  // the next stage
       if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit)) alive = false;
       tc_fence_after();
       return alive;
     };
     for (int tile = first; tile < tiles && alive; tile += step, ++turn) {
-      const int t_tile = tile % A.t_tiles;
+      const int q0 = unit_of(tile, place);
       const uint32_t buf = turn & 1, sum = tmem + buf * 256;
       if (turn >= 2 && !proj_wait(&B->freed[buf], (turn / 2 + 1) & 1, dead, A.errors, bit)) {
         alive = false;
@@ -932,9 +1011,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
           pair_commit(&B->empty[ring.slot]);
         }
       }
-      if (A.S > 0) {
-        if (!waited) wait_inner(), waited = true;
-        const int subs = (list_of(t_tile)[0] & LIST_COUNT) * blocks;
+      if (A.S > 0 && q0 < 0) {
+        const int subs = (list_of(place.t_tile)[0] & LIST_COUNT) * blocks;
         for (int sub0 = 0; sub0 < subs && alive && landed(); sub0 += per_stage, ring.next()) {
           const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE);
           const int n = min(per_stage, subs - sub0);
@@ -958,16 +1036,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
   } else if (warp >= 2) {
     const uint32_t quarter = warp & 3;
     uint32_t turn = 0;
-    wait_inner();
+    Place place;
     for (int tile = first; tile < tiles; tile += step, ++turn) {
-      const int t_tile = tile % A.t_tiles, t0 = t_tile * rows_max;
-      const int n = (tile / A.t_tiles * 2 + rank) * PROJ_M + quarter * 32 + lane;
-      const uint32_t buf = turn & 1;
-      const bool mixed = A.S > 0 && (list_of(t_tile)[0] & LIST_MIXED) != 0;
+      const int q0 = unit_of(tile, place), t_tile = place.t_tile, t0 = t_tile * rows_max;
+      const int rows = min(rows_max, A.T - t0), lane_at = rank * PROJ_M + quarter * 32 + lane;
+      const uint32_t buf = turn & 1, sum = tmem + buf * 256 + (quarter << 21);
       if (!proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit)) break;
       tc_fence_after();
-      const uint32_t sum = tmem + buf * 256 + (quarter << 21);
-      const int rows = min(rows_max, A.T - t0);
+      if (q0 >= 0) {
+        // inner rows: zeros where a row has another adapter
+        const int q = q0 + lane_at, j = q / A.R;
+        const bool some = q < stack_of(t_tile);
+        const int c = some ? list_of(t_tile)[1 + j] : -1;
+        const float by = some ? A.adapter_scale[c] : 0.0f;
+        __nv_bfloat16* h = A.spread + (static_cast<int64_t>(t_tile) * A.most + j) * rows_max * A.R + q % A.R;
+#pragma unroll 1
+        for (int c0 = 0; c0 < rows; c0 += 32) {
+          const int of = c0 + lane < rows ? A.row_adapter[t0 + c0 + lane] : -1;
+          float v[32];
+          tmem_ld32(sum + c0, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i, h += A.R) {
+            const int its = __shfl_sync(0xFFFFFFFFu, of, i);
+            if (some && c0 + i < rows) *h = __float2bfloat16_rn(its == c ? by * v[i] : 0.0f);
+          }
+        }
+        tc_fence_before();
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+          atomicAdd(A.ready + t_tile, 1u);
+          mbar_arrive_remote(dsmem_addr(smem_u32(&B->freed[buf]), 0));
+        }
+        continue;
+      }
+      const int n = (tile - units) / A.t_tiles * 2 * PROJ_M + lane_at;
+      const bool mixed = A.S > 0 && (list_of(t_tile)[0] & LIST_MIXED) != 0;
       __nv_bfloat16* y = A.y + t0 * A.ldy + n;
 #pragma unroll 1
       for (int c = 0; c < rows; c += 32) {  // the last columns of a buffer's 256 may be stale: they are not used
