@@ -79,6 +79,23 @@ __device__ __forceinline__ u64 draw_weight(float dt) {
   asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(m), "r"(32u - s));
   return static_cast<u64>(hi) << 32 | (up | down);
 }
+// Sums of such weights, of up to 2^9 of them, in six instructions each: e = A 2^-20 + r, where an addition of 8
+// rounded towards zero leaves A in the low bits of the float, and one of 2^-20 does so for r 2^43.
+struct DrawSum {
+  uint32_t a = 0, b = 0, n = 0;
+  __device__ __forceinline__ void add(float dt, uint32_t* top20 = nullptr, uint32_t* low23 = nullptr) {
+    const float e = expf(dt), t = __fadd_rz(e, 8.0f);
+    const uint32_t ta = __float_as_uint(t), tb = __float_as_uint(__fadd_rz(e - (t - 8.0f), 0x1p-20f));
+    a += ta;
+    b += tb;
+    ++n;
+    if (top20 != nullptr) *top20 = ta - 0x41000000u;
+    if (low23 != nullptr) *low23 = tb - 0x35800000u;
+  }
+  __device__ __forceinline__ u64 sum() const {
+    return (static_cast<u64>(a - n * 0x41000000u) << 23) + (b - n * 0x35800000u);
+  }
+};
 constexpr float DRAW_UNIT = 0x1p-43f;
 // floor(of * total / 2^24) for of <= 2^24 and total < 2^63
 __device__ __forceinline__ u64 draw_share(u64 of, u64 total) {
@@ -149,6 +166,18 @@ struct DrawRow {
       f(v * VEC + i, x);
     }
   }
+  // The largest of a vector, -inf where it has none; a NaN is passed over.
+  __device__ __forceinline__ float vec_max(int v) const {
+    const uint4 raw = reinterpret_cast<const uint4*>(ids)[v];
+    if constexpr (sizeof(E) == 4) {
+      return fmaxf(fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)), fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w))),
+                   -INFINITY);
+    } else {
+      auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+      const __nv_bfloat162 m = __hmax2(__hmax2(two(raw.x), two(raw.y)), __hmax2(two(raw.z), two(raw.w)));
+      return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
+    }
+  }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     for (int v = threadIdx.x; v < vecs; v += DRAW_THREADS) vec(v, f);
@@ -204,6 +233,18 @@ struct DrawRow {
     const int to = min(vecs, (warp + 1) * part);
     u64 s = 0;
     for (int v = warp * part + lane; v < to; v += 32) vec(v, [&](int i, float x) { s += f(base + i, x); });
+    return told(s, before);
+  }
+  // The same of the weights of the distances dist(index, x).
+  template <typename F>
+  __device__ u64 weight_parts(F dist, u64* before) {
+    const int part = (vecs + DRAW_WARPS - 1) / DRAW_WARPS;  // at most 2^9 logits to a lane
+    const int to = min(vecs, (warp + 1) * part);
+    DrawSum s;
+    for (int v = warp * part + lane; v < to; v += 32) vec(v, [&](int i, float x) { s.add(dist(base + i, x)); });
+    return told(s.sum(), before);
+  }
+  __device__ u64 told(u64 s, u64* before) {
     s = block_sum(s);
     if (warp == 0) tell(s, 0);
     meet();
@@ -245,36 +286,76 @@ struct DrawRow {
     return static_cast<int>(heard_sum(0)) - 1;
   }
 
+  // The step of distance that a logit is in.  Truncated by an addition of 2^23 rounded towards zero: a conversion
+  // would share its unit with the exponential.  An infinite largest logit leaves infinities in step 0.
   __device__ __forceinline__ int bin(float x) const {
-    return x == top ? 0 : min(DRAW_BINS - 1, static_cast<int>((top - x) * DRAW_STEPS));
+    const float d = fminf(fmaxf(fminf(top, 3.402823466e38f) - x, 0.0f), (DRAW_BINS - 0.5f) / DRAW_STEPS);
+    return __float_as_int(__fmaf_rz(d, DRAW_STEPS, 8388608.0f)) & (2 * DRAW_BINS - 1);
   }
   // A logit at or below every entry of the bins before `b`, and above -inf.
   __device__ __forceinline__ float floor_of(int b) const {
     return b >= DRAW_BINS ? -3.402823466e38f : fmaxf(-3.402823466e38f, top - b * (1.0001f / DRAW_STEPS));
   }
 
-  // Sums f over the row into bins at(x) and adds the blocks' bins up, each block a share of them: the row's
-  // sum.  cross() then finds the first bin whose inclusive sum reaches `target` >= 1 (one does), and the
-  // sum below it.
+  // Sums f over the row into bins at(x), of the logits from `least` on, and adds the blocks' bins up, each block
+  // a share of them: the sum of the whole row, and that of the bins.  cross() then finds the first bin whose
+  // inclusive sum reaches `target` >= 1 (one does), and the sum below it.
   struct Bins {
     u64 v[4], below;  // this thread's bins (one to four in a row) and what lies before them
   };
   template <typename F, typename At>
-  __device__ u64 weigh(F f, At at, Bins* bins) {
+  __device__ u64 weigh(F f, At at, float least, Bins* bins, u64* binned) {
+    clear_bins();
+    u64 row = 0;
+    each([&](int i, float x) {
+      const u64 w = f(base + i, x);
+      row += w;
+      add_if(w != 0 && x >= least, at(x), static_cast<uint32_t>(w) & 0x7FFFu, static_cast<uint32_t>(w >> 15) & 0x7FFFu,
+             static_cast<uint32_t>(w >> 30));
+    });
+    return join(row, bins, binned);
+  }
+  // The same of the weights of the distances dist(index, x), by distance.
+  template <typename F>
+  __device__ u64 weigh_distances(F dist, float least, Bins* bins, u64* binned) {
+    clear_bins();
+    DrawSum row;
+    each([&](int i, float x) {
+      uint32_t a, b;  // the weight is a 2^23 + b
+      row.add(dist(base + i, x), &a, &b);
+      add_if((a | b) != 0 && x >= least, bin(x), b & 0x7FFFu, (b >> 15) | (a & 0x7Fu) << 8, a >> 7);
+    });
+    return join(row.sum(), bins, binned);
+  }
+  // And of a count of the logits above -inf.
+  __device__ u64 count(float least, Bins* bins, u64* binned) {
+    clear_bins();
+    uint32_t row = 0;
+    each([&](int, float x) {
+      row += x > -INFINITY;
+      red_if(x >= least && x > -INFINITY, &sh->part[0][bin(x)], 1u);
+    });
+    return join(row, bins, binned);
+  }
+  __device__ __forceinline__ void clear_bins() {
     __syncthreads();
     for (int b = threadIdx.x; b < 3 * DRAW_BINS / 4; b += DRAW_THREADS)
       reinterpret_cast<uint4*>(sh->part)[b] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    each([&](int i, float x) {
-      const u64 w = f(base + i, x);
-      if (w == 0) return;
-      const int b = at(x);
-      const uint32_t w0 = static_cast<uint32_t>(w) & 0x7FFFu, w1 = static_cast<uint32_t>(w >> 15) & 0x7FFFu,
-                     w2 = static_cast<uint32_t>(w >> 30);
-      atomicAdd(&sh->part[0][b], w0);
-      if (w1) atomicAdd(&sh->part[1][b], w1);
-      if (w2) atomicAdd(&sh->part[2][b], w2);
-    });
+  }
+  // Without a branch, so that a vector's logits go through side by side.
+  __device__ __forceinline__ void red_if(bool on, uint32_t* to, uint32_t v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p red.shared.add.u32 [%1], %2;\n\t}" ::"r"(
+                     static_cast<uint32_t>(on)),
+                 "r"(smem_u32(to)), "r"(v)
+                 : "memory");
+  }
+  __device__ __forceinline__ void add_if(bool on, int b, uint32_t w0, uint32_t w1, uint32_t w2) {
+    red_if(on, &sh->part[0][b], w0);
+    red_if(on && w1 != 0, &sh->part[1][b], w1);
+    red_if(on && w2 != 0, &sh->part[2][b], w2);
+  }
+  __device__ u64 join(u64 row, Bins* bins, u64* binned) {
     __syncthreads();
     meet();
     const int share = DRAW_BINS / static_cast<int>(ranks);  // 128 to 2048 bins
@@ -304,11 +385,12 @@ struct DrawRow {
     }
     u64 here, before;
     const u64 upto = block_scan(s, &here);
-    if (warp == 0) tell(here, 0);
+    row = block_sum(row);
+    if (warp == 0) tell(here, row);
     meet();
-    const u64 all = heard_sum(0, &before);
+    *binned = heard_sum(0, &before);
     bins->below = before + upto - s;
-    return all;
+    return heard_sum(1);
   }
   __device__ __forceinline__ u64 bin_of(int b, uint32_t q) const {
     const uint32_t at = dsmem_addr(smem_u32(&sh->part[0][b]), q);
@@ -336,40 +418,17 @@ struct DrawRow {
     return static_cast<int>(heard_sum(0)) - 1;
   }
 
-  // The key K with sum(key > K) < target <= sum(key >= K) of f over the row's bin `b`, of which `over`
-  // lies above, by ever finer equal ranges of keys: for bins of any number of equal logits.
+  // The key K with sum(key > K) < target <= sum(key >= K) of f, between the keys lo and hi, above which lies
+  // `over`, by ever finer equal ranges of keys.
   template <typename F>
-  __device__ uint32_t select(F f, int b, u64 over, u64 target, u64* above) {
-    uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    each([&](int i, float x) {
-      if (f(base + i, x) && bin(x) == b) {
-        const uint32_t k = draw_key(x);
-        lo = min(lo, k);
-        hi = max(hi, k);
-      }
-    });
-    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-    __syncthreads();
-    if (lane == 0) sh->warp[warp] = static_cast<u64>(lo) << 32 | hi;
-    __syncthreads();
-    if (warp == 0) {
-      for (int w = 0; w < DRAW_WARPS; ++w) {
-        lo = min(lo, static_cast<uint32_t>(sh->warp[w] >> 32));
-        hi = max(hi, static_cast<uint32_t>(sh->warp[w]));
-      }
-      tell(lo, hi);
-    }
-    meet();
-    lo = __reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(lane) < ranks ? static_cast<uint32_t>(heard(0, lane)) : 0xFFFFFFFFu);
-    hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(lane) < ranks ? static_cast<uint32_t>(heard(1, lane)) : 0u);
+  __device__ uint32_t select(F f, uint32_t lo, uint32_t hi, u64 over, u64 target, u64* above) {
     while (lo < hi) {
       int shift = 0;
       while (((hi - lo) >> shift) >= DRAW_BINS) ++shift;
       Bins bins;
-      weigh([&](int i, float x) -> u64 { const uint32_t k = draw_key(x); return k >= lo && k <= hi ? f(i, x) : 0; },
-            [&](float x) { return (hi - draw_key(x)) >> shift; }, &bins);
       u64 under;
+      weigh([&](int i, float x) -> u64 { const uint32_t k = draw_key(x); return k >= lo && k <= hi ? f(i, x) : 0; },
+            [&](float x) { return (hi - draw_key(x)) >> shift; }, -INFINITY, &bins, &under);
       const int at = cross(bins, target - over, &under);
       over += under;
       const uint32_t width = 1u << shift, from = hi - (static_cast<uint32_t>(at) << shift);
@@ -429,20 +488,17 @@ struct DrawRow {
     }
   }
 
-  // Lists the entries from `least` to `most` that take(index, x) wants, in any order, in the first block (the
-  // list has the first DRAW_LIST); the row's number of them.  A vector without any costs a comparison an
-  // entry.  A block lists its own first: an addition in another block's memory takes as long as meet().
-  template <typename F>
-  __device__ u64 gather(float least, float most, F take) {
+  // Lists the entries from `least` (above -inf) on, in any order, in the first block (the list has the first
+  // DRAW_LIST); the row's number of them.  A vector without any costs little more than its largest.  A block lists its own first: an addition in another block's memory takes as long as meet().  Once a
+  // row: the list's counter starts at 0.
+  __device__ u64 gather(float least) {
     __syncthreads();
     if (threadIdx.x == 0) sh->local = 0;
     __syncthreads();
     for (int v = threadIdx.x; v < vecs; v += DRAW_THREADS) {
-      bool any = false;
-      vec(v, [&](int, float x) { any |= x >= least && x <= most; });
-      if (!any) continue;
+      if (!(vec_max(v) >= least)) continue;
       vec(v, [&](int i, float x) {
-        if (x >= least && x <= most && take(base + i, x)) {
+        if (x >= least) {
           const uint32_t at = atomicAdd(&sh->local, 1u);
           if (at < DRAW_LIST) sh->own[at] = static_cast<u64>(draw_key(x)) << 32 | static_cast<uint32_t>(~(base + i));
         }
@@ -464,46 +520,71 @@ struct DrawRow {
 
   // The last entry that a cut leaves: with as few as can be, sum(f) reaches `target`, 1 <= target <= the row's
   // sum.  It is in bin `b`, and `under` is the sum of the bins before.  f is 0 for what earlier cuts took.
-  // The list is empty.
   template <typename F>
   __device__ void pin(F f, int b, u64 under, u64 target, uint32_t* K, int* I) {
-    const float most = b == 0 ? top : fminf(top, top - b * (0.9999f / DRAW_STEPS));
-    const u64 entries = gather(floor_of(b + 1), most, [&](int i, float x) { return bin(x) == b && f(i, x) != 0; });
-    if (entries > DRAW_LIST) {  // a great many alike
-      u64 above;
-      const uint32_t key = select(f, b, under, target, &above);
-      const u64 one = f(-1, draw_val(key));
-      auto same = [&](int i, float x) -> u64 { return draw_key(x) == key && f(i, x) != 0; };
-      u64 before;
-      parts(same, &before);
-      *I = find(same, (target - above + one - 1) / one - 1, before);
-      *K = key;
-      return;
+    const float least = floor_of(b + 1), most = b == 0 ? top : fminf(top, top - b * (0.9999f / DRAW_STEPS));
+    __syncthreads();
+    if (threadIdx.x == 0) sh->local = 0;
+    __syncthreads();
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    for (int v = threadIdx.x; v < vecs; v += DRAW_THREADS) {
+      bool any = false;
+      vec(v, [&](int, float x) { any |= x >= least && x <= most; });
+      if (!any) continue;
+      vec(v, [&](int i, float x) {
+        if (x >= least && x <= most && bin(x) == b && f(base + i, x) != 0) {
+          const uint32_t at = atomicAdd(&sh->local, 1u), key = draw_key(x);
+          if (at < DRAW_LIST) sh->own[at] = static_cast<u64>(key) << 32 | static_cast<uint32_t>(~(base + i));
+          lo = min(lo, key);
+          hi = max(hi, key);
+        }
+      });
     }
-    if (rank == 0) {
-      sort(static_cast<int>(entries));
-      constexpr int PER = DRAW_LIST / DRAW_THREADS;
-      u64 w[PER], s = 0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int at = static_cast<int>(threadIdx.x) * PER + i;
-        const u64 e = at < static_cast<int>(entries) ? sh->list[at] : 0;
-        w[i] = e ? f(static_cast<int>(~static_cast<uint32_t>(e)), draw_val(static_cast<uint32_t>(e >> 32))) : 0;
-        s += w[i];
-      }
-      u64 run = under + block_scan(s) - s;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if (run < target && run + w[i] >= target) sh->found = sh->list[threadIdx.x * PER + i];
-        run += w[i];
-      }
-      __syncthreads();
-      if (warp == 0) tell(sh->found, 0);
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    if (lane == 0) sh->warp[warp] = static_cast<u64>(lo) << 32 | hi;
+    __syncthreads();
+    if (warp == 0) {
+      const u64 w = lane < DRAW_WARPS ? sh->warp[lane] : 0xFFFFFFFF00000000ull;
+      lo = __reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(w >> 32));
+      hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(w));
+      tell(sh->local, static_cast<u64>(lo) << 32 | hi);
     }
     meet();
-    const u64 e = heard(0, 0);
-    *K = static_cast<uint32_t>(e >> 32);
-    *I = static_cast<int>(~static_cast<uint32_t>(e));
+    u64 ahead;
+    const u64 entries = heard_sum(0, &ahead);
+    const u64 told_keys = static_cast<uint32_t>(lane) < ranks ? heard(1, lane) : 0xFFFFFFFF00000000ull;
+    lo = __reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(told_keys >> 32));
+    hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(told_keys));
+    if (lo < hi && entries <= DRAW_THREADS) {  // the first block orders them
+      const uint32_t there = dsmem_addr(smem_u32(&sh->list[0]), 0) + 8 * static_cast<uint32_t>(ahead), here = sh->local;
+      for (uint32_t i = threadIdx.x; i < here; i += DRAW_THREADS) dsmem_st_u64(there + 8 * i, sh->own[i]);
+      meet();
+      if (rank == 0) {
+        sort(static_cast<int>(entries));
+        const u64 e = threadIdx.x < entries ? sh->list[threadIdx.x] : 0;
+        const u64 w = e ? f(static_cast<int>(~static_cast<uint32_t>(e)), draw_val(static_cast<uint32_t>(e >> 32))) : 0;
+        const u64 upto = under + block_scan(w);
+        if (upto - w < target && upto >= target) sh->found = e;
+        __syncthreads();
+        if (warp == 0) tell(sh->found, 0);
+      }
+      meet();
+      const u64 e = heard(0, 0);
+      *K = static_cast<uint32_t>(e >> 32);
+      *I = static_cast<int>(~static_cast<uint32_t>(e));
+      return;
+    }
+    // one logit many times over, or too many: the logit, then how many of it
+    u64 above = under;
+    const uint32_t key = select(f, lo, hi, under, target, &above);
+    const float val = draw_val(key);
+    const u64 one = f(-1, val);
+    auto same = [&](int i, float x) -> u64 { return x == val && f(i, x) != 0; };
+    u64 before;
+    parts(same, &before);
+    *I = find(same, (target - above + one - 1) / one - 1, before);
+    *K = key;
   }
 };
 
@@ -557,13 +638,14 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   sh->part[2][threadIdx.x] = 0;  // DRAW_COARSE counts
   __syncthreads();
 
-  // The thread's largest logit and its lowest index, then the row's.
+  // The thread's largest logit and the first vector that has it, then the row's.
   float most = -INFINITY;
-  int most_at = -1;
-  auto look = [&](int i, float x) {
-    if (x > most) {  // not for NaN and -inf
-      most = x;
-      most_at = i;
+  int most_in = -1;
+  auto look = [&](int v) {
+    const float m = R.vec_max(v);
+    if (m > most) {  // not for a vector of NaN and -inf
+      most = m;
+      most_in = v;
     }
   };
   for (int p = 0; p < DRAW_PIECES; ++p) {
@@ -575,12 +657,12 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
           atomicOr(A.errors, 0x08u);  // STRATA_DEVERR_TIMEOUT
           break;
         }
-      for (int v = v0 + threadIdx.x; v < v1; v += DRAW_THREADS) R.vec(v, look);
+      for (int v = v0 + threadIdx.x; v < v1; v += DRAW_THREADS) look(v);
     }
   }
-  if (threadIdx.x == 0 && whole < R.vecs) R.vec(whole, look);
+  if (threadIdx.x == 0 && whole < R.vecs) look(whole);
   // The largest of four threads to all blocks: to each block by 32 threads, four to a store.
-  const uint32_t own_key = most_at < 0 ? NO_KEY : draw_key(most);
+  const uint32_t own_key = draw_key(most);
   {
     uint32_t four = max(own_key, __shfl_xor_sync(0xFFFFFFFFu, own_key, 1));
     four = max(four, __shfl_xor_sync(0xFFFFFFFFu, four, 2));
@@ -621,7 +703,12 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     return;
   }
   if (!(T > 0.0f) || (!(m <= 0.0f) && !(top >= least)) || (p_on && p24 == 0)) {  // the first in order
-    uint32_t first = __reduce_min_sync(0xFFFFFFFFu, own_key == top_key ? static_cast<uint32_t>(R.base + most_at) : 0xFFFFFFFFu);
+    uint32_t first = 0xFFFFFFFFu;
+    if (own_key == top_key)
+      R.vec(most_in, [&](int i, float x) {
+        if (x == top) first = min(first, static_cast<uint32_t>(R.base + i));
+      });
+    first = __reduce_min_sync(0xFFFFFFFFu, first);
     __syncthreads();
     if (R.lane == 0) sh->warp[R.warp] = first;
     __syncthreads();
@@ -690,19 +777,27 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
       run += ws[i];
     }
   };
-  auto all = [](int, float) { return true; };
-  auto by_distance = [&](float x) { return R.bin(x); };
-  auto new_list = [&]() {  // between two meetings
-    if (threadIdx.x == 0) sh->listed = 0;
-  };
   auto pinned = [&](uint32_t key, int i) {
     edge = draw_val(key);
     I = i;
   };
 
+  // A logit that few lie above: binning starts 4 below the smallest of the maxima, and from the lowest logit
+  // where the cut turns out to lie further down.
+  float start;
+  {
+    uint32_t low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i) low = min(low, maxima[i] - 1u);  // NO_KEY: the greatest
+    low = __reduce_min_sync(0xFFFFFFFFu, low);
+    __syncthreads();
+    if (R.lane == 0) sh->warp[R.warp] = low;
+    __syncthreads();
+    low = __reduce_min_sync(0xFFFFFFFFu, R.lane < DRAW_WARPS ? static_cast<uint32_t>(sh->warp[R.lane]) : 0xFFFFFFFFu);
+    start = draw_val(low + 1u) - 4.0f;
+  }
   typename DrawRow<E>::Bins bins;
-  u64 under, before;
-  bool used = false;  // the list
+  u64 under, before, binned;
   if (k_on && (A.V <= DRAW_LIST || k <= static_cast<int>(R.ranks) * DRAW_MAXIMA / 2)) {
     float from = edge;
     if (A.V > DRAW_LIST) {
@@ -718,31 +813,33 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
       // fewer maxima than k: every entry
       from = fmaxf(from, R.floor_of((static_cast<int>(sh->found) + 1) * (DRAW_BINS / DRAW_COARSE)));
     }
-    const u64 entries = R.gather(from, top, all);
+    const u64 entries = R.gather(from);
     if (entries <= DRAW_LIST) {
       if (lead) finish(static_cast<int>(entries), 0);
       return;
     }
-    used = true;
   }
   if (k_on) {
-    if (used) new_list();
     auto one = [&](int, float x) -> u64 { return x > -INFINITY; };
-    if (static_cast<u64>(k) < R.weigh(one, by_distance, &bins)) {
+    if (static_cast<u64>(k) < R.count(start, &bins, &binned)) {
+      if (static_cast<u64>(k) > binned) R.count(-INFINITY, &bins, &binned);
       const int b = R.cross(bins, k, &under);
       uint32_t key;
       int i;
       R.pin(one, b, under, k, &key, &i);
-      used = true;
       if (draw_val(key) >= edge) pinned(key, i);
     }
   }
   if (p_on) {
-    if (used) new_list();
     const float edge0 = edge;
     const int I0 = I;
     auto weight = [&](int i, float x) -> u64 { return x > edge0 || (x == edge0 && i <= I0) ? flat(x) : 0ull; };
-    const u64 share = draw_share(p24, R.weigh(weight, by_distance, &bins));
+    auto distance = [&](int i, float x) {
+      const float d = x == top ? 0.0f : x - top;
+      return x > edge0 || (x == edge0 && i <= I0) ? d : -1000.0f;
+    };
+    const u64 share = draw_share(p24, R.weigh_distances(distance, start, &bins, &binned));
+    if (share > binned) R.weigh_distances(distance, -INFINITY, &bins, &binned);
     const int b = R.cross(bins, share, &under);
     if (!k_on) {
       // how many entries there are up to b: about as many as maxima, where they are few
@@ -751,13 +848,11 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
       for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i)
         few += maxima[i] != NO_KEY && R.bin(draw_val(maxima[i])) <= b;
       if (R.block_sum(few) <= R.ranks * DRAW_MAXIMA / 2) {
-        const u64 entries = R.gather(fmaxf(edge, R.floor_of(b + 1)), top, all);
+        const u64 entries = R.gather(fmaxf(edge, R.floor_of(b + 1)));
         if (entries <= DRAW_LIST) {
           if (lead) finish(static_cast<int>(entries), share);
           return;
         }
-        new_list();
-        R.meet();
       }
     }
     uint32_t key;
@@ -769,7 +864,13 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     const u64 w = draw_weight(tempered(x));
     return x > edge || (x == edge && i <= I) ? w : 0ull;
   };
-  const u64 total = R.parts(left, &before);
+  // the same as distances: without infinities a product alone, and without a cut through equal logits one comparison
+  auto finite = [&](float x) { return fmaxf((x - top) * inv, -1000.0f); };
+  const bool usual = top <= 3.402823466e38f && inv <= 3.402823466e38f;
+  const u64 total =
+      usual && I == A.V - 1 ? R.weight_parts([&](int, float x) { return x >= edge ? finite(x) : -1000.0f; }, &before)
+      : usual ? R.weight_parts([&](int i, float x) { return x > edge || (x == edge && i <= I) ? finite(x) : -1000.0f; }, &before)
+              : R.weight_parts([&](int i, float x) { return x > edge || (x == edge && i <= I) ? tempered(x) : -1000.0f; }, &before);
   const int at = R.find(left, draw_share(u24, total), before);
   if (at >= R.base && at < R.base + n && threadIdx.x == 0) {
     float x;
