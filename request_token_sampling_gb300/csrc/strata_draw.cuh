@@ -36,6 +36,8 @@ struct DrawArgs {
   const void* logits;
   int64_t ld;
   int V, chunk;  // chunk: ids of a block, a multiple of 16
+  int B;
+  bool sorted;   // rows that may take long first (B <= DRAW_SORT_MOST)
   const float *u, *temperature, *top_p, *min_p;
   const int32_t* top_k;
   int32_t* ids;
@@ -52,8 +54,11 @@ constexpr float DRAW_STEPS = 64.0f;     // bins per unit of logit: 32 units, bey
 constexpr int DRAW_COARSE = DRAW_THREADS;  // bins of the maxima, a quarter as fine
 constexpr int DRAW_MAXIMA = DRAW_THREADS / 4;  // of a block: the largest logit of each four threads
 constexpr int DRAW_LIST = 2048;
+constexpr int DRAW_SORT_MOST = 2048;    // rows whose order every block finds for itself
+constexpr int DRAW_PICKED = 512;        // of a warp's part of at most 2048 logits
 constexpr int DRAW_PIECES = 4;          // parts a block's ids arrive in
 constexpr int DRAW_MAX_CLUSTER = 16;
+constexpr float DRAW_REACH = 0.75f;     // below the smallest maximum, of its distance to their mean
 constexpr uint32_t NO_KEY = 0u;         // NaN and -inf: below every key that can be chosen
 constexpr uint32_t DRAW_SPINS = 1u << 24;
 
@@ -137,10 +142,17 @@ struct DrawShared {
     uint32_t part[3][DRAW_BINS];
     u64 own[DRAW_LIST];
   };
-  alignas(16) u64 list[DRAW_LIST];   // key << 32 | ~index: the order of the chain, descending
+  // key << 32 | ~index, the order of the chain, descending: the first block's list.  Or, of every block, each
+  // warp's part of the row without the logits that no cut reaches: places in it, ascending.
+  union {
+    alignas(16) u64 list[DRAW_LIST];
+    uint16_t picked[DRAW_WARPS][DRAW_PICKED];
+  };
+  u64 few[DRAW_THREADS];             // entries of one bin, likewise; scratch of the bins' sums before
 };
 static_assert(offsetof(DrawShared, part) % 16 == 0 && offsetof(DrawShared, list) % 16 == 0, "16-byte accesses");
 static_assert(DRAW_MAXIMA * DRAW_MAX_CLUSTER <= DRAW_BINS, "the maxima fit part 0");
+static_assert(DRAW_PICKED <= DRAW_THREADS, "find() takes an entry to a thread");
 
 template <typename E>
 struct DrawRow {
@@ -151,6 +163,8 @@ struct DrawRow {
   uint32_t rank, ranks, turn;
   int warp, lane;
   float top;           // the row's largest logit
+  bool compact = false;  // this block goes through what it picked, else through all of its part of the row
+  int picked = 0;        // of this warp
 
   template <typename F>
   __device__ __forceinline__ void vec(int v, F f) const {
@@ -178,9 +192,49 @@ struct DrawRow {
       return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
     }
   }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (sizeof(E) == 4)
+      return ids[i];
+    else
+      return __bfloat162float(ids[i]);
+  }
+  // f(place in the block's part, logit) of this warp's contiguous part of that (or of what was picked of it).
+  __device__ __forceinline__ int part_vecs() const { return (vecs + DRAW_WARPS - 1) / DRAW_WARPS; }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    for (int v = threadIdx.x; v < vecs; v += DRAW_THREADS) vec(v, f);
+    if (compact) {
+      for (int i = lane; i < picked; i += 32) {
+        const int at = sh->picked[warp][i];
+        f(at, value(at));
+      }
+    } else {
+      const int to = min(vecs, (warp + 1) * part_vecs());
+      for (int v = warp * part_vecs() + lane; v < to; v += 32) vec(v, f);
+    }
+  }
+  // Goes through the warp's part once with f, and picks the logits from `least` (above -inf) on, in their order.
+  template <typename F>
+  __device__ void pick(float least, F f) {
+    const int to = min(vecs, (warp + 1) * part_vecs());
+    int n = 0;
+    bool fits = true;
+    for (int v0 = warp * part_vecs(); v0 < to; v0 += 32) {
+      const int v = v0 + lane;
+      uint32_t mask = 0;
+      if (v < to)
+        vec(v, [&](int i, float x) {
+          f(i, x);
+          mask |= (x >= least ? 1u : 0u) << (i % VEC);
+        });
+      const int own = __popc(mask), upto = draw_warp_scan(own, lane);
+      const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+      fits = fits && n + all <= DRAW_PICKED;
+      if (fits)
+        for (int at = n + upto - own; mask != 0; mask &= mask - 1) sh->picked[warp][at++] = static_cast<uint16_t>(v * VEC + __ffs(mask) - 1);
+      n += all;
+    }
+    picked = n;
+    compact = __syncthreads_and(fits);
   }
 
   // Two values of each block to all blocks of the row: tell() by one warp, meet(), heard().  A block reads
@@ -229,19 +283,15 @@ struct DrawRow {
   // sum and what comes before this block.
   template <typename F>
   __device__ u64 parts(F f, u64* before) {
-    const int part = (vecs + DRAW_WARPS - 1) / DRAW_WARPS;
-    const int to = min(vecs, (warp + 1) * part);
     u64 s = 0;
-    for (int v = warp * part + lane; v < to; v += 32) vec(v, [&](int i, float x) { s += f(base + i, x); });
+    each([&](int i, float x) { s += f(base + i, x); });
     return told(s, before);
   }
   // The same of the weights of the distances dist(index, x).
   template <typename F>
   __device__ u64 weight_parts(F dist, u64* before) {
-    const int part = (vecs + DRAW_WARPS - 1) / DRAW_WARPS;  // at most 2^9 logits to a lane
-    const int to = min(vecs, (warp + 1) * part);
-    DrawSum s;
-    for (int v = warp * part + lane; v < to; v += 32) vec(v, [&](int i, float x) { s.add(dist(base + i, x)); });
+    DrawSum s;  // at most 2^9 logits to a lane
+    each([&](int i, float x) { s.add(dist(base + i, x)); });
     return told(s.sum(), before);
   }
   __device__ u64 told(u64 s, u64* before) {
@@ -251,7 +301,7 @@ struct DrawRow {
     return heard_sum(0, before);
   }
   // After parts(f): the first index whose running sum exceeds `target` (< the row's sum), to all blocks.
-  // The whole block sums the part again, a vector to a thread.
+  // The whole block sums the part again, a vector or an entry to a thread.
   template <typename F>
   __device__ int find(F f, u64 target, u64 before) {
     if (threadIdx.x == 0) sh->found = 0;
@@ -261,23 +311,32 @@ struct DrawRow {
     if (over != 0) {  // in this block
       const int hit = __ffs(over) - 1;
       u64 run = __shfl_sync(0xFFFFFFFFu, upto - mine, hit);
-      const int part = (vecs + DRAW_WARPS - 1) / DRAW_WARPS;
-      const int to = min(vecs, (hit + 1) * part);
-      for (int v0 = hit * part; v0 < to; v0 += DRAW_THREADS) {
-        const int v = v0 + static_cast<int>(threadIdx.x);
-        u64 own = 0, all;
-        if (v < to) vec(v, [&](int i, float x) { own += f(base + i, x); });
-        const u64 here = run + block_scan(own, &all);
-        if (here - own <= target && target < here) {
-          u64 sum = here - own;
-          int at = -1;
-          vec(v, [&](int i, float x) {
-            sum += f(base + i, x);
-            if (at < 0 && sum > target) at = base + i;
-          });
-          sh->found = static_cast<u64>(at) + 1;
+      if (compact) {
+        // an entry to a thread; entries that were not picked are at the end of a warp's places, and weigh nothing
+        if (warp == hit && lane == 0) sh->local = static_cast<uint32_t>(picked);
+        __syncthreads();
+        const int at = threadIdx.x < sh->local ? sh->picked[hit][threadIdx.x] : -1;
+        const u64 own = at >= 0 ? f(base + at, value(at)) : 0;
+        const u64 here = run + block_scan(own);
+        if (here - own <= target && target < here) sh->found = static_cast<u64>(base + at) + 1;
+      } else {
+        const int to = min(vecs, (hit + 1) * part_vecs());
+        for (int v0 = hit * part_vecs(); v0 < to; v0 += DRAW_THREADS) {
+          const int v = v0 + static_cast<int>(threadIdx.x);
+          u64 own = 0, all;
+          if (v < to) vec(v, [&](int i, float x) { own += f(base + i, x); });
+          const u64 here = run + block_scan(own, &all);
+          if (here - own <= target && target < here) {
+            u64 sum = here - own;
+            int at = -1;
+            vec(v, [&](int i, float x) {
+              sum += f(base + i, x);
+              if (at < 0 && sum > target) at = base + i;
+            });
+            sh->found = static_cast<u64>(at) + 1;
+          }
+          run += all;
         }
-        run += all;
       }
     }
     __syncthreads();
@@ -315,26 +374,23 @@ struct DrawRow {
     });
     return join(row, bins, binned);
   }
-  // The same of the weights of the distances dist(index, x), by distance.
+  // The same of the weights of the distances dist(index, x), by distance; `row` is what they sum to in the block,
+  // or it is taken of what each() goes through.
   template <typename F>
-  __device__ u64 weigh_distances(F dist, float least, Bins* bins, u64* binned) {
+  __device__ u64 weigh_distances(F dist, float least, const DrawSum* row, Bins* bins, u64* binned) {
     clear_bins();
-    DrawSum row;
+    DrawSum mine;
     each([&](int i, float x) {
       uint32_t a, b;  // the weight is a 2^23 + b
-      row.add(dist(base + i, x), &a, &b);
+      mine.add(dist(base + i, x), &a, &b);
       add_if((a | b) != 0 && x >= least, bin(x), b & 0x7FFFu, (b >> 15) | (a & 0x7Fu) << 8, a >> 7);
     });
-    return join(row.sum(), bins, binned);
+    return join((row != nullptr ? *row : mine).sum(), bins, binned);
   }
-  // And of a count of the logits above -inf.
-  __device__ u64 count(float least, Bins* bins, u64* binned) {
+  // And of a count of logits, of which this thread saw `row` in all.
+  __device__ u64 count(float least, uint32_t row, Bins* bins, u64* binned) {
     clear_bins();
-    uint32_t row = 0;
-    each([&](int, float x) {
-      row += x > -INFINITY;
-      red_if(x >= least && x > -INFINITY, &sh->part[0][bin(x)], 1u);
-    });
+    each([&](int, float x) { red_if(x >= least && x > -INFINITY, &sh->part[0][bin(x)], 1u); });
     return join(row, bins, binned);
   }
   __device__ __forceinline__ void clear_bins() {
@@ -375,11 +431,11 @@ struct DrawRow {
 #pragma unroll
       for (int q = 0; q < 4; ++q) s += bin_of(first + b, min(group * 4 + q, static_cast<int>(ranks) - 1));
       __syncthreads();
-      sh->list[threadIdx.x] = s;  // nobody's list is in use
+      sh->few[threadIdx.x] = s;
       __syncthreads();
       s = 0;
       if (group == 0)
-        for (int g = 0; g < groups; ++g) s += sh->list[g * share + b];
+        for (int g = 0; g < groups; ++g) s += sh->few[g * share + b];
       bins->v[0] = s;
       bins->v[1] = bins->v[2] = bins->v[3] = 0;
     }
@@ -442,24 +498,24 @@ struct DrawRow {
   // A barrier of the first `threads` threads (whole warps).
   __device__ __forceinline__ void some_sync(int threads) const { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
 
-  // Orders list[0, n) descending; what is beyond n up to a power of two is filled with zeros.
-  __device__ void sort(int n) {
+  // Orders a[0, n) descending; what is beyond n up to a power of two is filled with zeros.
+  __device__ void sort(u64* list, int n) {
     int size = 32;
     while (size < n) size *= 2;
-    for (int i = n + threadIdx.x; i < size; i += DRAW_THREADS) sh->list[i] = 0;
+    for (int i = n + threadIdx.x; i < size; i += DRAW_THREADS) list[i] = 0;
     __syncthreads();
     if (size <= DRAW_THREADS) {
       // an entry to a thread: steps of less than a warp go from lane to lane
       if (static_cast<int>(threadIdx.x) < size) {
-        u64 a = sh->list[threadIdx.x];
+        u64 a = list[threadIdx.x];
         for (int k = 2; k <= size; k *= 2) {
           for (int j = k / 2; j > 0; j /= 2) {
             u64 b;
             if (j >= 32) {
               some_sync(size);
-              sh->list[threadIdx.x] = a;
+              list[threadIdx.x] = a;
               some_sync(size);
-              b = sh->list[threadIdx.x ^ j];
+              b = list[threadIdx.x ^ j];
             } else {
               b = __shfl_xor_sync(0xFFFFFFFFu, a, j);
             }
@@ -468,7 +524,7 @@ struct DrawRow {
           }
         }
         some_sync(size);
-        sh->list[threadIdx.x] = a;
+        list[threadIdx.x] = a;
       }
       __syncthreads();
       return;
@@ -477,10 +533,10 @@ struct DrawRow {
       for (int j = k / 2; j > 0; j /= 2) {
         for (int p = threadIdx.x; p < size / 2; p += DRAW_THREADS) {
           const int i = (p & ~(j - 1)) * 2 + (p & (j - 1));
-          const u64 a = sh->list[i], b = sh->list[i + j];
+          const u64 a = list[i], b = list[i + j];
           if ((a < b) == ((i & k) == 0)) {
-            sh->list[i] = b;
-            sh->list[i + j] = a;
+            list[i] = b;
+            list[i + j] = a;
           }
         }
         __syncthreads();
@@ -527,19 +583,14 @@ struct DrawRow {
     if (threadIdx.x == 0) sh->local = 0;
     __syncthreads();
     uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    for (int v = threadIdx.x; v < vecs; v += DRAW_THREADS) {
-      bool any = false;
-      vec(v, [&](int, float x) { any |= x >= least && x <= most; });
-      if (!any) continue;
-      vec(v, [&](int i, float x) {
-        if (x >= least && x <= most && bin(x) == b && f(base + i, x) != 0) {
-          const uint32_t at = atomicAdd(&sh->local, 1u), key = draw_key(x);
-          if (at < DRAW_LIST) sh->own[at] = static_cast<u64>(key) << 32 | static_cast<uint32_t>(~(base + i));
-          lo = min(lo, key);
-          hi = max(hi, key);
-        }
-      });
-    }
+    each([&](int i, float x) {
+      if (x >= least && x <= most && bin(x) == b && f(base + i, x) != 0) {
+        const uint32_t at = atomicAdd(&sh->local, 1u), key = draw_key(x);
+        if (at < DRAW_LIST) sh->own[at] = static_cast<u64>(key) << 32 | static_cast<uint32_t>(~(base + i));
+        lo = min(lo, key);
+        hi = max(hi, key);
+      }
+    });
     lo = __reduce_min_sync(0xFFFFFFFFu, lo);
     hi = __reduce_max_sync(0xFFFFFFFFu, hi);
     if (lane == 0) sh->warp[warp] = static_cast<u64>(lo) << 32 | hi;
@@ -557,12 +608,12 @@ struct DrawRow {
     lo = __reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(told_keys >> 32));
     hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(told_keys));
     if (lo < hi && entries <= DRAW_THREADS) {  // the first block orders them
-      const uint32_t there = dsmem_addr(smem_u32(&sh->list[0]), 0) + 8 * static_cast<uint32_t>(ahead), here = sh->local;
+      const uint32_t there = dsmem_addr(smem_u32(&sh->few[0]), 0) + 8 * static_cast<uint32_t>(ahead), here = sh->local;
       for (uint32_t i = threadIdx.x; i < here; i += DRAW_THREADS) dsmem_st_u64(there + 8 * i, sh->own[i]);
       meet();
       if (rank == 0) {
-        sort(static_cast<int>(entries));
-        const u64 e = threadIdx.x < entries ? sh->list[threadIdx.x] : 0;
+        sort(sh->few, static_cast<int>(entries));
+        const u64 e = threadIdx.x < entries ? sh->few[threadIdx.x] : 0;
         const u64 w = e ? f(static_cast<int>(~static_cast<uint32_t>(e)), draw_val(static_cast<uint32_t>(e >> 32))) : 0;
         const u64 upto = under + block_scan(w);
         if (upto - w < target && upto >= target) sh->found = e;
@@ -588,6 +639,43 @@ struct DrawRow {
   }
 };
 
+// Where rows are more than run at once, those whose keys may take long (a large top_k, top_p without top_k) come
+// first, so that the last to start are short: the row that is `at`-th in that order.
+__device__ __forceinline__ bool draw_long(const DrawArgs& A, int row, int list_k) {
+  const float T = A.temperature != nullptr ? A.temperature[row] : 1.0f, P = A.top_p != nullptr ? A.top_p[row] : 1.0f;
+  const int k = A.top_k != nullptr ? A.top_k[row] : 0;
+  const bool k_on = k > 0 && k < A.V;
+  return T > 0.0f && (k_on ? k > list_k : !(P >= 1.0f));
+}
+__device__ __forceinline__ int row_in_order(const DrawArgs& A, int at, uint32_t* words) {
+  uint32_t ranks;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int list_k = static_cast<int>(ranks) * DRAW_MAXIMA / 2, groups = (A.B + 31) / 32;
+  for (int g = threadIdx.x >> 5; g < groups; g += DRAW_WARPS) {
+    const int row = g * 32 + (threadIdx.x & 31);
+    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, row < A.B && draw_long(A, row, list_k));
+    if ((threadIdx.x & 31) == 0) words[g] = bits;
+  }
+  __syncthreads();
+  int all = 0;
+  for (int g = 0; g < groups; ++g) all += __popc(words[g]);
+  const bool is_long = at < all;
+  int left = is_long ? at : at - all, row = 0;
+  for (int g = 0; g < groups; ++g) {
+    uint32_t bits = is_long ? words[g] : ~words[g];
+    const int n = __popc(bits);
+    if (left >= n) {
+      left -= n;
+      continue;
+    }
+    while (left-- > 0) bits &= bits - 1;
+    row = g * 32 + __ffs(bits) - 1;
+    break;
+  }
+  __syncthreads();
+  return row;
+}
+
 template <typename E>
 __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_constant__ DrawArgs A) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -601,7 +689,7 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   R.turn = 0;
   R.warp = threadIdx.x >> 5;
   R.lane = threadIdx.x & 31;
-  const int row = blockIdx.x / R.ranks;
+  const int row = A.sorted ? row_in_order(A, blockIdx.x / R.ranks, reinterpret_cast<uint32_t*>(sh->part)) : blockIdx.x / R.ranks;
   R.base = static_cast<int>(R.rank) * A.chunk;
   const int n = max(0, min(A.chunk, A.V - R.base));
   constexpr int VEC = DrawRow<E>::VEC;
@@ -734,7 +822,7 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   // The first block's list holds all that the cuts leave, and maybe more below: it finishes alone.
   // `share`: top_p's part of the weight, 0 where it is of the list after top_k.
   auto finish = [&](int listed, u64 share) {
-    R.sort(listed);
+    R.sort(sh->list, listed);
     constexpr int PER = DRAW_LIST / DRAW_THREADS;
     int kept = k_on ? min(k, listed) : listed;
     const int per = listed <= DRAW_THREADS ? 1 : PER;  // entries of a thread, in a row
@@ -764,7 +852,7 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     // index order: swap the halves, so that the greatest ~index comes first
     __syncthreads();
     for (int i = threadIdx.x; i < kept; i += DRAW_THREADS) sh->list[i] = sh->list[i] << 32 | sh->list[i] >> 32;
-    R.sort(kept);
+    R.sort(sh->list, kept);
     u64 run = sums(kept, [&](u64 e) { return draw_weight(tempered(draw_val(static_cast<uint32_t>(e)))); });
     const u64 draw = draw_share(u24, sum);
 #pragma unroll
@@ -782,20 +870,6 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     I = i;
   };
 
-  // A logit that few lie above: binning starts 4 below the smallest of the maxima, and from the lowest logit
-  // where the cut turns out to lie further down.
-  float start;
-  {
-    uint32_t low = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i) low = min(low, maxima[i] - 1u);  // NO_KEY: the greatest
-    low = __reduce_min_sync(0xFFFFFFFFu, low);
-    __syncthreads();
-    if (R.lane == 0) sh->warp[R.warp] = low;
-    __syncthreads();
-    low = __reduce_min_sync(0xFFFFFFFFu, R.lane < DRAW_WARPS ? static_cast<uint32_t>(sh->warp[R.lane]) : 0xFFFFFFFFu);
-    start = draw_val(low + 1u) - 4.0f;
-  }
   typename DrawRow<E>::Bins bins;
   u64 under, before, binned;
   if (k_on && (A.V <= DRAW_LIST || k <= static_cast<int>(R.ranks) * DRAW_MAXIMA / 2)) {
@@ -819,15 +893,53 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
       return;
     }
   }
+  // Cuts that leave many mostly leave a small part of the row all the same: it is gone through once, and what
+  // lies further below the smallest of the maxima than DRAW_REACH of their mean's way up is left out from then on (a
+  // twelfth is left of a normal distribution).  Where a cut turns out to lie further down, the row is taken whole.
+  float start = 0.0f;
+  if (k_on || p_on) {
+    uint32_t low = 0xFFFFFFFFu;
+    float sum = 0.0f, some = 0.0f;
+#pragma unroll
+    for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i) {
+      low = min(low, maxima[i] - 1u);  // NO_KEY: the greatest
+      sum += maxima[i] != NO_KEY ? draw_val(maxima[i]) : 0.0f;
+      some += maxima[i] != NO_KEY ? 1.0f : 0.0f;
+    }
+    low = __reduce_min_sync(0xFFFFFFFFu, low);
+    sum = warp_sum(sum);
+    some = warp_sum(some);
+    __syncthreads();
+    float* to = reinterpret_cast<float*>(sh->part[2]);
+    if (R.lane == 0) {
+      sh->warp[R.warp] = low;
+      to[R.warp] = sum;
+      to[DRAW_WARPS + R.warp] = some;
+    }
+    __syncthreads();
+    low = __reduce_min_sync(0xFFFFFFFFu, R.lane < DRAW_WARPS ? static_cast<uint32_t>(sh->warp[R.lane]) : 0xFFFFFFFFu);
+    sum = warp_sum(R.lane < DRAW_WARPS ? to[R.lane] : 0.0f);
+    some = warp_sum(R.lane < DRAW_WARPS ? to[DRAW_WARPS + R.lane] : 0.0f);
+    const float least_maximum = draw_val(low + 1u);
+    start = fmaxf(least_maximum - DRAW_REACH * (sum / some - least_maximum), -3.402823466e38f);
+    __syncthreads();
+  }
   if (k_on) {
     auto one = [&](int, float x) -> u64 { return x > -INFINITY; };
-    if (static_cast<u64>(k) < R.count(start, &bins, &binned)) {
-      if (static_cast<u64>(k) > binned) R.count(-INFINITY, &bins, &binned);
+    uint32_t row = 0;
+    R.pick(start, [&](int, float x) { row += x > -INFINITY; });
+    if (static_cast<u64>(k) < R.count(start, row, &bins, &binned)) {
+      if (static_cast<u64>(k) > binned) {
+        R.compact = false;
+        R.count(-INFINITY, row, &bins, &binned);
+      }
       const int b = R.cross(bins, k, &under);
       uint32_t key;
       int i;
       R.pin(one, b, under, k, &key, &i);
       if (draw_val(key) >= edge) pinned(key, i);
+    } else {
+      R.compact = false;
     }
   }
   if (p_on) {
@@ -838,8 +950,18 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
       const float d = x == top ? 0.0f : x - top;
       return x > edge0 || (x == edge0 && i <= I0) ? d : -1000.0f;
     };
-    const u64 share = draw_share(p24, R.weigh_distances(distance, start, &bins, &binned));
-    if (share > binned) R.weigh_distances(distance, -INFINITY, &bins, &binned);
+    DrawSum row;
+    if (!k_on) {
+      if (top <= 3.402823466e38f)
+        R.pick(start, [&](int, float x) { row.add(x >= edge0 ? x - top : -1000.0f); });
+      else
+        R.pick(start, [&](int i, float x) { row.add(distance(R.base + i, x)); });
+    }
+    const u64 share = draw_share(p24, R.weigh_distances(distance, k_on ? -INFINITY : start, k_on ? nullptr : &row, &bins, &binned));
+    if (share > binned) {  // not after a top_k: what it leaves is all there
+      R.compact = false;
+      R.weigh_distances(distance, -INFINITY, nullptr, &bins, &binned);
+    }
     const int b = R.cross(bins, share, &under);
     if (!k_on) {
       // how many entries there are up to b: about as many as maxima, where they are few
@@ -853,6 +975,7 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
           if (lead) finish(static_cast<int>(entries), share);
           return;
         }
+        R.compact = false;  // the list lies where the picked were
       }
     }
     uint32_t key;

@@ -127,7 +127,8 @@ extern "C" int strata_draw_rows(const void* logits, int dtype, int B, int V, int
     ranks *= 2;
   const int chunk = ((V + ranks - 1) / ranks + 15) / 16 * 16;
   const size_t smem = (sizeof(strata::DrawShared) + 15) / 16 * 16 + static_cast<size_t>(chunk) * esz;
-  strata::DrawArgs A{logits, ld, V, chunk, u, temperature, top_p, min_p, top_k, out_ids, out_lps, errors};
+  const bool sorted = static_cast<int64_t>(B) * ranks > 2 * sms && B <= strata::DRAW_SORT_MOST && (top_k != nullptr || top_p != nullptr);
+  strata::DrawArgs A{logits, ld, V, chunk, B, sorted, u, temperature, top_p, min_p, top_k, out_ids, out_lps, errors};
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(DRAW_SMEM));
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return host_fail(STRATA_ECUDA, "strata_draw_rows: %s", cudaGetErrorString(e));
