@@ -487,6 +487,29 @@ def test_draw_agrees_with_the_sampler_on_the_cut(G):
     assert got == set(kept)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_draw_many_rows_and_the_largest_vocabulary(G, dtype):
+    """More rows than run at once (long ones go first) and a row of 2^19 logits."""
+    check_draw(G, logits(700, 1000, dtype, 5), *keys(700, 1000, 5))
+    check_draw(G, logits(5, 524288, dtype, 6), *keys(5, 524288, 6))
+    B = 2500
+    x = logits(B, 64, dtype, 7)
+    u = torch.rand(B, generator=torch.Generator().manual_seed(7)).tolist()
+    check_draw(G, x, u, k=[1 + b % 70 for b in range(B)], p=[0.5 + 0.5 * (b % 3) for b in range(B)])
+
+
+@pytest.mark.parametrize("spread", [0.01, 1.0, 30.0])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_draw_wide_cuts(G, dtype, spread):
+    """Cuts that leave thousands: flat rows, steep ones, cuts near either end."""
+    V, B = 60000, 12
+    x = logits(B, V, dtype, 31, spread, 0)
+    u = [(b + 0.5) / B for b in range(B)]
+    check_draw(G, x, u, k=[1000, 2000, 5000, 20000, 40000, 55000, 59000, 59999, 3000, 700, 30000, 10000])
+    check_draw(G, x, u, p=[0.1, 0.3, 0.5, 0.7, 0.8, 0.9, 0.95, 0.99, 0.999, 0.9999, 0.6, 0.2])
+    check_draw(G, x, u, k=[50000, 30000] * 6, p=[0.9, 0.5, 0.99] * 4, m=[0.0, 1e-3, 1e-6, 0.0] * 3)
+
+
 # ------------------------------------------------------------------------------ together
 def test_on_another_stream_and_in_a_graph(G):
     """The three calls in a row, on a side stream and replayed from a graph, give what they give on their own."""
@@ -523,3 +546,18 @@ def test_on_another_stream_and_in_a_graph(G):
         torch.cuda.synchronize()
         assert torch.equal(y3, y) and torch.equal(o3["ids"], o["ids"])
     assert G.tail_errors() == 0
+
+
+def test_the_example_runs_the_tail(G):
+    """The decode example: a captured step gives the tokens of the uncaptured one; slot 0 is greedy."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_tail.py")
+    spec = importlib.util.spec_from_file_location("decode_tail", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    ids, lps = mod.decode(6, 4096, 512, 5)
+    again, lps2 = mod.decode(6, 4096, 512, 5, graph=False)
+    assert torch.equal(ids, again) and torch.equal(lps, lps2)
+    assert ((ids >= 0) & (ids < 4096)).all() and (lps <= 0).all() and (lps[:, 0] == 0).all()
+    assert len({tuple(c.tolist()) for c in ids.T}) > 1
