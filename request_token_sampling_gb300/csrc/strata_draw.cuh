@@ -689,6 +689,8 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   R.turn = 0;
   R.warp = threadIdx.x >> 5;
   R.lane = threadIdx.x & 31;
+  grid_dep_wait();
+  grid_dep_launch();
   const int row = A.sorted ? row_in_order(A, blockIdx.x / R.ranks, reinterpret_cast<uint32_t*>(sh->part)) : blockIdx.x / R.ranks;
   R.base = static_cast<int>(R.rank) * A.chunk;
   const int n = max(0, min(A.chunk, A.V - R.base));

@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "strata_device.cuh"
+
 namespace strata {
 
 struct NormArgs {
@@ -144,6 +146,8 @@ __host__ __device__ constexpr int norm_most_threads(int n, int per) { return n *
 template <typename E, int N, int PER, bool BLOCK, bool SHIFT>
 __global__ void __launch_bounds__(BLOCK ? norm_most_threads(N, PER) : 128) norm_kernel(const __grid_constant__ NormArgs A) {
   __shared__ float part[2][32];
+  grid_dep_wait();
+  grid_dep_launch();
   const int threads = BLOCK ? blockDim.x : 32, me = BLOCK ? threadIdx.x : threadIdx.x & 31;
   const int64_t t = BLOCK ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (!BLOCK && t >= A.T) return;
@@ -240,6 +244,8 @@ __global__ void __launch_bounds__(BLOCK ? norm_most_threads(N, PER) : 128) norm_
 template <typename E>
 __global__ void __launch_bounds__(1024) norm_wide_kernel(const __grid_constant__ NormArgs A) {
   __shared__ float part[2][32];
+  grid_dep_wait();
+  grid_dep_launch();
   const int64_t t = blockIdx.x;
   const E* x = static_cast<const E*>(A.x) + t * A.ldx;
   const E* r = A.residual != nullptr ? static_cast<const E*>(A.residual) + t * A.ldr : nullptr;

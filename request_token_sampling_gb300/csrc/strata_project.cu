@@ -246,7 +246,6 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
     const cuuint32_t box[2] = {elems, static_cast<cuuint32_t>(pair > 0 ? bn / 2 : bn)};
     if (!encode(dev.encode, &mx, f8, 2, x, dims, strides, box, 128)) return host_fail(STRATA_EINVAL, "x cannot be mapped");
   }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (S > 0) {
     const cuuint64_t r = static_cast<cuuint64_t>(R), bytes = r * 2;
     const cuuint64_t dims[3] = {r, static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(S)};
@@ -264,14 +263,12 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
       return encode(dev.encode, &ma, false, 2, a, adims, astrides, abox, 128);
     };
     if (T <= SHRINK_ROWS) {
-      const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(R / 8));
-      if (f8)
-        strata::shrink_kernel<__nv_fp8_e4m3><<<grid, 256, 0, s>>>(A, bn);
-      else
-        strata::shrink_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(A, bn);
+      strata::Launch launch(static_cast<unsigned>(T), 256, 0, stream);
+      launch.cfg.gridDim.y = static_cast<unsigned>(R / 8);
+      e = f8 ? launch(strata::shrink_kernel<__nv_fp8_e4m3>, A, bn) : launch(strata::shrink_kernel<__nv_bfloat16>, A, bn);
     } else if (pair > 0) {
       if (!map_a()) return host_fail(STRATA_EINVAL, "a cannot be mapped");
-      strata::plan_kernel<<<static_cast<unsigned>(t_tiles), 256, 0, s>>>(A);
+      e = strata::Launch(static_cast<unsigned>(t_tiles), 256, 0, stream)(strata::plan_kernel, A);
     } else {
       CUtensorMap mt;
       const cuuint64_t xdims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(T)};
@@ -282,49 +279,23 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
       // clusters of a tile: one where the tiles fill the GPU, as many as there can be work for where they do not
       const int groups = std::min((most * R + strata::PROJ_M - 1) / strata::PROJ_M,
                                   std::max(1, dev.sms / strata::INNER_SPLIT / t_tiles));
-      cudaLaunchConfig_t in = {};
-      in.gridDim = dim3(static_cast<unsigned>(t_tiles) * groups * strata::INNER_SPLIT, 1, 1);
-      in.blockDim = dim3(strata::PROJ_THREADS, 1, 1);
-      in.dynamicSmemBytes = static_cast<size_t>(strata::inner_smem(f8));
-      in.stream = s;
-      cudaLaunchAttribute cluster = {};
-      cluster.id = cudaLaunchAttributeClusterDimension;
-      cluster.val.clusterDim.x = strata::INNER_SPLIT;
-      cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-      in.attrs = &cluster;
-      in.numAttrs = 1;
-      e = cudaLaunchKernelEx(&in, f8 ? strata::inner_kernel<true> : strata::inner_kernel<false>, ma, mt, A, groups, box_rows);
-      if (e != cudaSuccess) return cuda_fail(e, "strata_project_rows");
+      const strata::Launch launch(static_cast<unsigned>(t_tiles) * groups * strata::INNER_SPLIT, strata::PROJ_THREADS,
+                                  strata::inner_smem(f8), stream, strata::INNER_SPLIT);
+      e = launch(f8 ? strata::inner_kernel<true> : strata::inner_kernel<false>, ma, mt, A, groups, box_rows);
     }
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "strata_project_rows");
+    if (e != cudaSuccess) return cuda_fail(e, "strata_project_rows");
   }
   const int ranks = pair > 0 ? 1 : split_ranks(tiles, k_stages, dev.sms);
-  cudaLaunchConfig_t cfg = {};
+  // starts beside the inner rows' kernel and waits for it before what it wrote
   const int64_t units = S > 0 ? static_cast<int64_t>(t_tiles) * ((most * R + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M)) : 0;
-  if (pair > 0)
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles + units, dev.sms / 2)), 1, 1);
-  else
-    cfg.gridDim = dim3(static_cast<unsigned>(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, dev.sms)), 1, 1);
-  cfg.blockDim = dim3(strata::PROJ_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(pair > 0 ? strata::pair_smem() : strata::proj_smem(bn));
-  cfg.stream = s;
-  cudaLaunchAttribute attrs[2];
-  int na = 0;
-  if (ranks > 1) {
-    attrs[na].id = cudaLaunchAttributeClusterDimension;
-    attrs[na].val.clusterDim.x = static_cast<unsigned>(ranks);
-    attrs[na].val.clusterDim.y = attrs[na].val.clusterDim.z = 1;
-    ++na;
+  if (pair > 0) {
+    const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles + units, dev.sms / 2));
+    e = strata::Launch(2 * pairs, strata::PROJ_THREADS, strata::pair_smem(), stream)(strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows);
+  } else {
+    const unsigned grid = static_cast<unsigned>(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, dev.sms));
+    e = strata::Launch(grid, strata::PROJ_THREADS, strata::proj_smem(bn), stream, static_cast<unsigned>(ranks))(
+        kernel_for(bn, f8, ranks > 1), mw, mx, mb, mh, A);
   }
-  if (S > 0) {  // starts beside the inner rows' kernel and waits for it before what it wrote
-    attrs[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[na].val.programmaticStreamSerializationAllowed = 1;
-    ++na;
-  }
-  cfg.attrs = attrs;
-  cfg.numAttrs = na;
-  e = pair > 0 ? cudaLaunchKernelEx(&cfg, strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows)
-               : cudaLaunchKernelEx(&cfg, kernel_for(bn, f8, ranks > 1), mw, mx, mb, mh, A);
   return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_project_rows");
 }
 

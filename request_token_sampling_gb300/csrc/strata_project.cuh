@@ -209,6 +209,7 @@ __device__ __forceinline__ void write_list(const ProjectArgs& A, int tile, int t
 // Eight warps: the block of row t takes eight of its inner products, one to a warp.
 template <typename E>
 __global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A, int tile_rows) {
+  grid_dep_wait();    // first: the next kernel relies on what was before this one being done
   grid_dep_launch();
   __shared__ TileAdapters used;
   const int t = blockIdx.x, tile = t / tile_rows, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -276,6 +277,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   const int unit = blockIdx.x / INNER_SPLIT, tile = unit / groups, first = unit % groups;
   volatile uint32_t* dead = &B->dead;
   const uint32_t bit = 0x08u;  // STRATA_DEVERR_TIMEOUT
+  grid_dep_wait();    // first: the next kernel relies on what was before this one being done
   grid_dep_launch();
 
   const int t0 = tile * rows_max, rows = min(rows_max, A.T - t0);
@@ -534,6 +536,8 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
+  if (A.S == 0) grid_dep_wait();  // nothing ran before it in this call
+  grid_dep_launch();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem;
@@ -835,6 +839,7 @@ __device__ __noinline__ float proj_own_sum(const ProjectArgs& A, int tile, int t
 // The lists of a call's tiles; no unit is done.
 __global__ void __launch_bounds__(256) plan_kernel(const __grid_constant__ ProjectArgs A) {
   __shared__ TileAdapters used;
+  grid_dep_wait();    // first: the next kernel relies on what was before this one being done
   grid_dep_launch();
   const int tile = blockIdx.x, t0 = tile * A.tile_rows;
   tile_adapters(A, t0, min(A.tile_rows, A.T - t0), &used);
@@ -878,6 +883,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
+  if (A.S == 0) grid_dep_wait();
+  grid_dep_launch();
   __syncthreads();
   cluster_arrive();
   cluster_wait();

@@ -24,35 +24,28 @@ bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_
 // to a row 6.3 us, four 8.7, one and two warps 7.8).  Few rows are bound by
 // latency: a row goes to as many threads as it has packs.
 template <typename E, int N, int PER, bool SHIFT>
-bool launch_norm(const strata::NormArgs& A, int least, cudaStream_t s) {
+cudaError_t launch_norm(const strata::NormArgs& A, int least, void* stream) {
   if constexpr (PER <= (N == 1 ? 16 : 4)) {
     const int packs = (A.H + N - 1) / N, need = std::max((packs + PER - 1) / PER, SHIFT ? 2 * (N - 1) : 1);
-    if (PER >= least && need <= strata::norm_most_threads(N, PER)) {
-      if (need <= 32) {
-        constexpr int ROWS = 4;
-        strata::norm_kernel<E, N, PER, false, SHIFT><<<(A.T + ROWS - 1) / ROWS, 32 * ROWS, 0, s>>>(A);
-      } else {
-        strata::norm_kernel<E, N, PER, true, SHIFT><<<A.T, (need + 31) / 32 * 32, 0, s>>>(A);
-      }
-      return true;
-    }
-    return launch_norm<E, N, PER * 2, SHIFT>(A, least, s);
+    if (PER < least || need > strata::norm_most_threads(N, PER)) return launch_norm<E, N, PER * 2, SHIFT>(A, least, stream);
+    constexpr int ROWS = 4;
+    if (need <= 32)
+      return strata::Launch((A.T + ROWS - 1) / ROWS, 32 * ROWS, 0, stream)(strata::norm_kernel<E, N, PER, false, SHIFT>, A);
+    return strata::Launch(A.T, (need + 31) / 32 * 32, 0, stream)(strata::norm_kernel<E, N, PER, true, SHIFT>, A);
   } else {
-    return false;
+    return strata::Launch(A.T, 1024, 0, stream)(strata::norm_wide_kernel<E>, A);
   }
 }
 
 // `packed`: all rows lie on 16 bytes; `alike`: they lie anywhere, but all tensors the same way.
 template <typename E>
-cudaError_t launch_norm(const strata::NormArgs& A, bool packed, bool alike, int sms, cudaStream_t s) {
+cudaError_t launch_norm(const strata::NormArgs& A, bool packed, bool alike, int sms, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   const int packs = A.H / (packed || alike ? N : 1);
   const int least = A.T < 2 * sms ? 1 : packs > 64 ? 4 : packs > 32 ? 2 : 1;
-  if (!(packed  ? launch_norm<E, N, 1, false>(A, least, s)
-        : alike ? launch_norm<E, N, 1, true>(A, least, s)
-                : launch_norm<E, 1, 1, false>(A, least, s)))
-    strata::norm_wide_kernel<E><<<A.T, 1024, 0, s>>>(A);
-  return cudaGetLastError();
+  return packed  ? launch_norm<E, N, 1, false>(A, least, stream)
+         : alike ? launch_norm<E, N, 1, true>(A, least, stream)
+                 : launch_norm<E, 1, 1, false>(A, least, stream);
 }
 
 }  // namespace
@@ -76,7 +69,6 @@ extern "C" int strata_norm_rows(const void* x, int64_t ldx, const void* residual
       misaligned(y, esz) || misaligned(scale, 4))
     return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
   strata::NormArgs A{x, residual, weight, residual_out, y, q, scale, ldx, ldr, ldro, ldy, ldq, T, H, eps};
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* errors = nullptr;
   int sms = 0;
   if (const int rc = strata::tail_device(&errors, &sms); rc != STRATA_OK) return rc;
@@ -91,8 +83,8 @@ extern "C" int strata_norm_rows(const void* x, int64_t ldx, const void* residual
     return p == nullptr || ((reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(x)) % 16 == 0 && (T == 1 || (ld - ldx) % n == 0));
   };
   const bool alike = like_x(residual, ldr) && like_x(residual_out, ldro) && like_x(y, ldy);
-  const cudaError_t e = dtype == STRATA_DTYPE_F32 ? launch_norm<float>(A, packed, alike, sms, s)
-                                                  : launch_norm<__nv_bfloat16>(A, packed, alike, sms, s);
+  const cudaError_t e = dtype == STRATA_DTYPE_F32 ? launch_norm<float>(A, packed, alike, sms, stream)
+                                                  : launch_norm<__nv_bfloat16>(A, packed, alike, sms, stream);
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_norm_rows: %s", cudaGetErrorString(e));
 }
 
@@ -132,17 +124,7 @@ extern "C" int strata_draw_rows(const void* logits, int dtype, int B, int V, int
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(DRAW_SMEM));
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return host_fail(STRATA_ECUDA, "strata_draw_rows: %s", cudaGetErrorString(e));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(B) * ranks, 1, 1);
-  cfg.blockDim = dim3(strata::DRAW_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(ranks);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = f32 ? cudaLaunchKernelEx(&cfg, strata::draw_kernel<float>, A) : cudaLaunchKernelEx(&cfg, strata::draw_kernel<__nv_bfloat16>, A);
+  const strata::Launch launch(static_cast<unsigned>(B) * ranks, strata::DRAW_THREADS, smem, stream, static_cast<unsigned>(ranks));
+  e = f32 ? launch(strata::draw_kernel<float>, A) : launch(strata::draw_kernel<__nv_bfloat16>, A);
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_draw_rows: %s", cudaGetErrorString(e));
 }
