@@ -300,11 +300,11 @@ struct DrawRow {
     meet();
     return heard_sum(0, before);
   }
-  // After parts(f): the first index whose running sum exceeds `target` (< the row's sum), to all blocks.
-  // The whole block sums the part again, a vector or an entry to a thread.
+  // After parts(f): the first index whose running sum exceeds `target` (< the row's sum); -1 in all threads of
+  // the cluster but the one that finds it.  The whole block sums the part again, a vector or an entry to a thread.
   template <typename F>
-  __device__ int find(F f, u64 target, u64 before) {
-    if (threadIdx.x == 0) sh->found = 0;
+  __device__ int locate(F f, u64 target, u64 before) {
+    int found = -1;
     const u64 mine = lane < DRAW_WARPS ? sh->warp[lane] : 0;
     const u64 upto = before + draw_warp_scan(mine, lane);
     const uint32_t over = __ballot_sync(0xFFFFFFFFu, lane < DRAW_WARPS && upto - mine <= target && target < upto);
@@ -318,7 +318,7 @@ struct DrawRow {
         const int at = threadIdx.x < sh->local ? sh->picked[hit][threadIdx.x] : -1;
         const u64 own = at >= 0 ? f(base + at, value(at)) : 0;
         const u64 here = run + block_scan(own);
-        if (here - own <= target && target < here) sh->found = static_cast<u64>(base + at) + 1;
+        if (here - own <= target && target < here) found = base + at;
       } else {
         const int to = min(vecs, (hit + 1) * part_vecs());
         for (int v0 = hit * part_vecs(); v0 < to; v0 += DRAW_THREADS) {
@@ -333,12 +333,22 @@ struct DrawRow {
               sum += f(base + i, x);
               if (at < 0 && sum > target) at = base + i;
             });
-            sh->found = static_cast<u64>(at) + 1;
+            found = at;
           }
           run += all;
         }
       }
     }
+    return found;
+  }
+  // The same to all threads of the cluster.
+  template <typename F>
+  __device__ int find(F f, u64 target, u64 before) {
+    __syncthreads();
+    if (threadIdx.x == 0) sh->found = 0;
+    const int at = locate(f, target, before);
+    __syncthreads();
+    if (at >= 0) sh->found = static_cast<u64>(at) + 1;
     __syncthreads();
     if (warp == 0) tell(sh->found, 0);
     meet();
@@ -1027,15 +1037,8 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
       usual && I == A.V - 1 ? R.weight_parts([&](int, float x) { return x >= edge ? finite(x) : -1000.0f; }, &before)
       : usual ? R.weight_parts([&](int i, float x) { return x > edge || (x == edge && i <= I) ? finite(x) : -1000.0f; }, &before)
               : R.weight_parts([&](int i, float x) { return x > edge || (x == edge && i <= I) ? tempered(x) : -1000.0f; }, &before);
-  const int at = R.find(left, draw_share(u24, total), before);
-  if (at >= R.base && at < R.base + n && threadIdx.x == 0) {
-    float x;
-    if constexpr (sizeof(E) == 4)
-      x = ids[at - R.base];
-    else
-      x = __bfloat162float(ids[at - R.base]);
-    answer(at, tempered(x) - logf(static_cast<float>(total) * DRAW_UNIT));
-  }
+  const int at = R.locate(left, draw_share(u24, total), before);
+  if (at >= 0) answer(at, tempered(R.value(at - R.base)) - logf(static_cast<float>(total) * DRAW_UNIT));
 }
 
 }  // namespace strata
