@@ -937,10 +937,11 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     }
   }
   // Cuts that leave many mostly leave a small part of the row all the same: it is gone through once, and what
-  // lies further below the smallest of the maxima than DRAW_REACH of their mean's way up is left out from then on (a
-  // twelfth is left of a normal distribution).  Where a cut turns out to lie further down, the row is taken whole.
+  // is out of their reach is left out from then on.  Where a cut turns out to lie further down, the row is taken
+  // whole.  top_p reaches below the smallest of the maxima by DRAW_REACH of its distance to their mean (a
+  // twelfth of a normal distribution is left).
   float start = 0.0f;
-  if (k_on || p_on) {
+  if (!k_on && p_on) {
     uint32_t low = 0xFFFFFFFFu;
     float sum = 0.0f, some = 0.0f;
 #pragma unroll
@@ -966,6 +967,27 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     const float least_maximum = draw_val(low + 1u);
     start = fmaxf(least_maximum - DRAW_REACH * (sum / some - least_maximum), -3.402823466e38f);
     __syncthreads();
+  }
+  if (k_on) {
+    // The reach of a large top_k, from a sample: each thread's first vector, counted in coarse bins.  It is set a few
+    // standard deviations further than the sample's k-th, and to the furthest of the blocks'.
+    __syncthreads();
+    sh->part[2][threadIdx.x] = 0;
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < R.vecs)
+      R.vec(threadIdx.x, [&](int, float x) { R.red_if(x > -INFINITY, &sh->part[2][R.bin(x) / (DRAW_BINS / DRAW_COARSE)], 1u); });
+    if (threadIdx.x == 0) sh->found = DRAW_COARSE;
+    __syncthreads();
+    uint32_t sample;
+    const uint32_t here = sh->part[2][threadIdx.x], upto = R.block_scan(here, &sample);
+    const float share = static_cast<float>(k) / static_cast<float>(A.V) * static_cast<float>(sample);
+    const uint32_t want = static_cast<uint32_t>(share + 3.0f * sqrtf(share) + 3.0f);
+    if (upto - here < want && upto >= want) sh->found = threadIdx.x;
+    __syncthreads();
+    start = R.floor_of((static_cast<int>(sh->found) + 1) * (DRAW_BINS / DRAW_COARSE));
+    if (R.warp == 0) R.tell(draw_key(start), 0);
+    R.meet();
+    start = draw_val(__reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(R.lane) < R.ranks ? static_cast<uint32_t>(R.heard(0, R.lane)) : 0xFFFFFFFFu));
   }
   if (k_on) {
     auto one = [&](int, float x) -> u64 { return x > -INFINITY; };
