@@ -14,6 +14,8 @@
  * calls need no context: they run on the calling thread's current device, every buffer they use is
  * an argument, and calls on several streams are independent as long as their buffers are.  All of
  * them may be captured in a CUDA graph.  A call with no rows does nothing and returns STRATA_OK.
+ * Their launches are set up while the kernel before them on the stream runs (programmatic dependent
+ * launch) and wait on the GPU for it to end before they touch memory.
  */
 #ifndef STRATA_TAIL_H
 #define STRATA_TAIL_H
@@ -54,8 +56,9 @@ int strata_norm_rows(const void* x, int64_t ldx, const void* residual, int64_t l
  *           + adapter_scale[c] * sum_r (x_scale[t] * sum_k x[t][k] a[c][r][k]) * b[c][n][r],   c = row_adapter[t]
  * x and w are `dtype`: BF16 (no scales: pass NULL) or F8 (both scales).  a [S][R][K], b [S][N][R]
  * and y are bfloat16, a and b packed; a row whose row_adapter is outside 0..S-1 has no adapter.
- * S = 0 (the adapter pointers may be NULL) is the projection alone.  Sums are held in 32 bits.
- * An adapter's infinities and NaNs reach the rows that use it and no others.
+ * S = 0 (the adapter pointers may be NULL) is the projection alone.  Sums are held in 32 bits; the inner row
+ * (adapter_scale * x_scale * x a^T) is rounded to bfloat16 between its two products.
+ * An adapter's infinities and NaNs reach the rows that use it and no others.  T is at most 524,288.
  * x, w, a and b start on 16 bytes, and K and the strides ldx and ldw are multiples of 16 bytes; R is
  * a multiple of 16 (pad smaller ranks with zeros).  ldy >= N is any stride, y any bfloat16 address.
  * `workspace`: strata_project_workspace(T, S, R) bytes on 256 bytes of alignment, free to be reused

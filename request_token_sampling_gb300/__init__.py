@@ -7,6 +7,9 @@ token from Philox(seed, position) with a per-slot counter that persists across c
 take the penalised argmax.  The same launch can return raw-logit log-probabilities (the chosen
 token's, the top 0..20 alternatives, and allowed_token_ids renormalisation).
 
+Around it (``include/strata_tail.h``): ``norm_rows``, ``project_rows`` and ``draw_rows``, the final norm with an
+8-bit output, a projection with each row's low-rank adapter, and sampling from the caller's random numbers.
+
 This package is the thin Python binding (ctypes; PyTorch tensors for device memory and streams).
 Importing it fails loudly when the CUDA library has not been built.
 """

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace strata {
 
 // Stores a one-line message for strata_last_error() and returns `code`.
@@ -14,24 +16,35 @@ __attribute__((visibility("hidden"), format(printf, 2, 3))) int host_fail(int co
 // The current device's word of STRATA_DEVERR_* bits and its number of SMs.
 __attribute__((visibility("hidden"))) int tail_device(uint32_t** errors, int* sms);
 
+// Whether a sampling call with STRATA_FLAG_OWN_OUTPUTS was launched in this process.  Its kernel waits for nothing
+// before it, so that its end says nothing of what came earlier on its stream.
+inline std::atomic<bool>& waitless_launched() {
+  static std::atomic<bool> seen{false};
+  return seen;
+}
+
 // A launch that may be set up while the kernel before it on the stream still runs: the kernel waits for that one
-// (griddepcontrol.wait) before it reads or writes anything of the caller's, or of the workspace.
+// (griddepcontrol.wait) before it reads or writes anything of the caller's, or of the workspace, and that one has
+// waited for those before it.  Where a kernel without such a wait may be among them, the launch is an ordinary
+// one, unless it `follows` a kernel of the same call.
 struct Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[2];
-  Launch(unsigned grid, unsigned block, size_t smem, void* stream, unsigned cluster = 1) {
+  Launch(unsigned grid, unsigned block, size_t smem, void* stream, unsigned cluster = 1, bool follows = false) {
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(block, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
     if (cluster > 1) {
-      attrs[1].id = cudaLaunchAttributeClusterDimension;
-      attrs[1].val.clusterDim.x = cluster;
-      attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
-      cfg.numAttrs = 2;
+      attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+      attrs[cfg.numAttrs].val.clusterDim.x = cluster;
+      attrs[cfg.numAttrs].val.clusterDim.y = attrs[cfg.numAttrs].val.clusterDim.z = 1;
+      ++cfg.numAttrs;
+    }
+    if (follows || !waitless_launched().load(std::memory_order_acquire)) {
+      attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attrs[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+      ++cfg.numAttrs;
     }
     cfg.attrs = attrs;
   }

@@ -290,10 +290,10 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   const int64_t units = S > 0 ? static_cast<int64_t>(t_tiles) * ((most * R + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M)) : 0;
   if (pair > 0) {
     const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles + units, dev.sms / 2));
-    e = strata::Launch(2 * pairs, strata::PROJ_THREADS, strata::pair_smem(), stream)(strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows);
+    e = strata::Launch(2 * pairs, strata::PROJ_THREADS, strata::pair_smem(), stream, 1, S > 0)(strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows);
   } else {
     const unsigned grid = static_cast<unsigned>(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, dev.sms));
-    e = strata::Launch(grid, strata::PROJ_THREADS, strata::proj_smem(bn), stream, static_cast<unsigned>(ranks))(
+    e = strata::Launch(grid, strata::PROJ_THREADS, strata::proj_smem(bn), stream, static_cast<unsigned>(ranks), S > 0)(
         kernel_for(bn, f8, ranks > 1), mw, mx, mb, mh, A);
   }
   return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_project_rows");

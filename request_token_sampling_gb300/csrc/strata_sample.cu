@@ -389,6 +389,7 @@ int launch(strata_ctx* c, const KParams& P, int dtype, const Shape& sh, uint32_t
   cudaError_t e;
   const bool mask = P.mode == strata::MODE_SAMPLE && (flags & STRATA_FLAG_ALLOWED_MASK) != 0u && P.allowed_off != nullptr;
   const bool own = (flags & STRATA_FLAG_OWN_OUTPUTS) != 0u && (flags & STRATA_FLAG_EARLY_LOAD) != 0u;
+  if (own && (flags & STRATA_FLAG_PDL) != 0u) strata::waitless_launched().store(true, std::memory_order_release);
   e = cudaLaunchKernelEx(&cfg, kernel_for(dtype, mask, own, sh.resident, sh.two), P);
   if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
   (void)c;

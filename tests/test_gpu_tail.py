@@ -548,6 +548,25 @@ def test_on_another_stream_and_in_a_graph(G):
     assert G.tail_errors() == 0
 
 
+def test_after_a_sampling_call_that_waits_for_nothing(G):
+    """The sampler's own-outputs calls do not wait for what is before them; what follows them still does."""
+    x = logits(4, 30000, F32, 77)
+    big = torch.empty(1 << 26, device="cuda")
+    h, w = torch.randn(4, 512, device="cuda").to(BF), torch.ones(512, dtype=BF, device="cuda")
+    y = G.norm_rows(h, w)["y"]
+    flags = G.STRATA_FLAG_PDL | G.STRATA_FLAG_EARLY_LOAD | G.STRATA_FLAG_OWN_OUTPUTS
+    slot, pos = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+    with G.Sampler(device=0, max_slots=1, max_vocab=30000, max_rows=4) as s:
+        s.set_slot(0, dict(temperature=0.7, seed=3))
+        torch.cuda.synchronize()
+        for i in range(20):
+            late = torch.zeros_like(h)
+            big.normal_()
+            late.copy_(h)                       # behind the long fill
+            s.sample(x, slot, pos, flags=flags)
+            assert torch.equal(G.norm_rows(late, w)["y"], y), i
+
+
 def test_the_example_runs_the_tail(G):
     """The decode example: a captured step gives the tokens of the uncaptured one; slot 0 is greedy."""
     import importlib.util
