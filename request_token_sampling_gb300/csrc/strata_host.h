@@ -29,8 +29,9 @@ inline std::atomic<bool>& waitless_launched() {
 // one, unless it `follows` a kernel of the same call.
 struct Launch {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attrs[2];
-  Launch(unsigned grid, unsigned block, size_t smem, void* stream, unsigned cluster = 1, bool follows = false) {
+  cudaLaunchAttribute attrs[3];
+  Launch(unsigned grid, unsigned block, size_t smem, void* stream, unsigned cluster = 1, bool follows = false,
+         bool together = false) {
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(block, 1, 1);
     cfg.dynamicSmemBytes = smem;
@@ -44,6 +45,11 @@ struct Launch {
     if (follows || !waitless_launched().load(std::memory_order_acquire)) {
       attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       attrs[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+      ++cfg.numAttrs;
+    }
+    if (together) {  // blocks wait on one another: all of them run at the same time
+      attrs[cfg.numAttrs].id = cudaLaunchAttributeCooperative;
+      attrs[cfg.numAttrs].val.cooperative = 1;
       ++cfg.numAttrs;
     }
     cfg.attrs = attrs;

@@ -136,7 +136,11 @@ int current_device(const Device** dev) {
   const cudaError_t e = cudaGetDevice(&id);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   if (id >= 64) return host_fail(STRATA_ERANGE, "device %d", id);
-  *dev = &device_info(id);
+  try {
+    *dev = &device_info(id);
+  } catch (...) {  // no exception leaves a C call
+    return host_fail(STRATA_ECUDA, "device setup");
+  }
   return (*dev)->status == cudaSuccess ? STRATA_OK : cuda_fail((*dev)->status, "device setup");
 }
 
@@ -290,7 +294,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   const int64_t units = S > 0 ? static_cast<int64_t>(t_tiles) * ((most * R + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M)) : 0;
   if (pair > 0) {
     const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles + units, dev.sms / 2));
-    e = strata::Launch(2 * pairs, strata::PROJ_THREADS, strata::pair_smem(), stream, 1, S > 0)(strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows);
+    e = strata::Launch(2 * pairs, strata::PROJ_THREADS, strata::pair_smem(), stream, 1, S > 0, S > 0)(strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows);
   } else {
     const unsigned grid = static_cast<unsigned>(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, dev.sms));
     e = strata::Launch(grid, strata::PROJ_THREADS, strata::proj_smem(bn), stream, static_cast<unsigned>(ranks), S > 0)(

@@ -779,7 +779,8 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
 // spoils in other requests' rows is therefore found in the sum, and that sum is taken again.
 // The inner rows are tiles of the same kind, before all others: 256 of a tile's stacked products a unit, with
 // the matrices a in w's place.  A tile of outputs adds its adapters last, and waits before that until its
-// rows' units are done.  They are the lowest tiles, so they are taken first and wait for nothing.
+// rows' units are done.  They are the lowest tiles, so they are taken first and wait for nothing; the launch is
+// cooperative, so the pairs that have them run.
 //
 // Bound by the tensor cores (and their power) in the loop: 4,256 x 4,096 x 4,096 without adapters takes 77 us
 // (1.86 PFLOP/s).  4,099 rows with 8 adapters of rank 64 take 96 us: their units, the first tiles' wait for
