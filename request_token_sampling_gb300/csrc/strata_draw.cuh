@@ -57,7 +57,8 @@ constexpr int DRAW_WARPS = DRAW_THREADS / 32;
 constexpr int DRAW_BINS = 2048;
 constexpr float DRAW_STEPS = 64.0f;     // bins per unit of logit: 32 units, beyond which a weight is 0
 constexpr int DRAW_COARSE = DRAW_THREADS;  // bins of the maxima, a quarter as fine
-constexpr int DRAW_MAXIMA = DRAW_THREADS / 4;  // of a block: the largest logit of each four threads
+constexpr int DRAW_MAXIMA = DRAW_THREADS / 4;  // of a block: the largest logit of each four threads, or (a row in one or
+                                               // two blocks) of each thread
 constexpr int DRAW_LIST = 2048;
 constexpr int DRAW_SORT_MOST = 2048;    // rows whose order every block finds for itself
 constexpr int DRAW_PICKED = 512;        // of a warp's part of at most 2048 logits
@@ -665,7 +666,7 @@ __device__ __forceinline__ bool draw_long(const DrawArgs& A, int row, int list_k
 __device__ __forceinline__ int row_in_order(const DrawArgs& A, int at, uint32_t* words) {
   uint32_t ranks;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-  const int list_k = static_cast<int>(ranks) * DRAW_MAXIMA / 2, groups = (A.B + 31) / 32;
+  const int list_k = static_cast<int>(ranks) * (ranks <= 2 ? DRAW_THREADS : DRAW_MAXIMA) / 2, groups = (A.B + 31) / 32;
   for (int g = threadIdx.x >> 5; g < groups; g += DRAW_WARPS) {
     const int row = g * 32 + (threadIdx.x & 31);
     const uint32_t bits = __ballot_sync(0xFFFFFFFFu, row < A.B && draw_long(A, row, list_k));
@@ -766,9 +767,11 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
     }
   }
   if (threadIdx.x == 0 && whole < R.vecs) look(whole);
-  // The largest of four threads to all blocks: to each block by 32 threads, four to a store.
+  // The largest of four threads to all blocks: to each block by 32 threads, four to a store.  Or each thread's own.
   const uint32_t own_key = draw_key(most);
-  {
+  const bool fine = R.ranks <= 2;
+  const int row_maxima = static_cast<int>(R.ranks) * (fine ? DRAW_THREADS : DRAW_MAXIMA);
+  if (!fine) {
     uint32_t four = max(own_key, __shfl_xor_sync(0xFFFFFFFFu, own_key, 1));
     four = max(four, __shfl_xor_sync(0xFFFFFFFFu, four, 2));
     uint32_t* mine = reinterpret_cast<uint32_t*>(sh->list);
@@ -776,7 +779,10 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   }
   __syncthreads();
   cluster_wait();
-  if (static_cast<uint32_t>(R.warp) < R.ranks) {
+  if (fine) {
+    for (uint32_t q = 0; q < R.ranks; ++q)
+      dsmem_st_u32(dsmem_addr(smem_u32(&sh->part[0][R.rank * DRAW_THREADS + threadIdx.x]), q), own_key);
+  } else if (static_cast<uint32_t>(R.warp) < R.ranks) {
     const uint4 keys = reinterpret_cast<const uint4*>(sh->list)[R.lane];
     dsmem_st_v4(dsmem_addr(smem_u32(&sh->part[0][R.rank * DRAW_MAXIMA + R.lane * 4]), R.warp), keys.x, keys.y, keys.z, keys.w);
   }
@@ -785,7 +791,7 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i) {
     const int at = i * DRAW_THREADS + threadIdx.x;
-    maxima[i] = at < static_cast<int>(R.ranks) * DRAW_MAXIMA ? sh->part[0][at] : NO_KEY;
+    maxima[i] = at < row_maxima ? sh->part[0][at] : NO_KEY;
     top_key = max(top_key, maxima[i]);
   }
   top_key = __reduce_max_sync(0xFFFFFFFFu, top_key);
@@ -920,9 +926,9 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
 
   typename DrawRow<E>::Bins bins;
   u64 under, before, binned;
-  if (k_on && (A.V <= DRAW_LIST || k <= static_cast<int>(R.ranks) * DRAW_MAXIMA / 2)) {
+  if (k_on && (A.V <= DRAW_LIST || k <= row_maxima / 2)) {
     float from = edge;
-    if (A.V > DRAW_LIST) {
+    if (k <= row_maxima / 2) {
       // the bin in which the maxima are k
 #pragma unroll
       for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i)
@@ -1039,7 +1045,7 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < DRAW_MAXIMA * DRAW_MAX_CLUSTER / DRAW_THREADS; ++i)
         few += maxima[i] != NO_KEY && R.bin(draw_val(maxima[i])) <= b;
-      if (R.block_sum(few) <= R.ranks * DRAW_MAXIMA / 2) {
+      if (R.block_sum(few) <= row_maxima / 2) {
         const u64 entries = R.gather(fmaxf(edge, R.floor_of(b + 1)));
         if (entries <= DRAW_LIST) {
           if (lead) finish(static_cast<int>(entries), share);
