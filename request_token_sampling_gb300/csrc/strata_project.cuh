@@ -14,8 +14,8 @@
 //
 // Few rows are bound by reading w and b from HBM: w comes by TMA through up to 12 stages of shared memory,
 // 200 KB on their way to an SM.  Measured (one GB300, us on the GPU, sizes rows x outputs x width):
-// 8 x 248,320 x 2,048 bfloat16 with 8 adapters of rank 16 165 (6.6 TB/s), 64 rows of 8 bits with 32 adapters of
-// rank 32 158 (6.7 TB/s), 1 x 32,000 x 1,024 17 (4 TB/s: 250 tiles on 152 SMs, and the start).
+// 8 x 248,320 x 2,048 bfloat16 with 8 adapters of rank 16 163 (6.6 TB/s), 64 rows of 8 bits with 32 adapters of
+// rank 32 156 (6.8 TB/s), 1 x 32,000 x 1,024 17 (4 TB/s: 250 tiles on 152 SMs, and the start).
 #pragma once
 
 #include <cuda.h>
@@ -683,17 +683,43 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
       const uint32_t base = tmem + buf * 2 * BN + (quarter << 21);
       const int rows = min(BN, A.T - t0);
       if constexpr (!SPLIT) {
+        // few instructions an output: a warp writes its 32 outputs of all rows while the next tile is summed, and
+        // the last tile's writing is waited for
         const float sw = F8 && n < A.N ? A.w_scale[n] : 1.0f;
+        __nv_bfloat16* y = A.y + t0 * A.ldy + n;
 #pragma unroll 1
         for (int c = 0; c < rows; c += 16) {
           float vb[16], vd[16] = {};
           tmem_ld16(base + c, vb);
           if (adapters > 0) tmem_ld16(base + BN + c, vd);
+          const float scale = F8 && lane < 16 && c + lane < rows ? A.x_scale[t0 + c + lane] : 0.0f;  // of row c + lane
           tmem_wait_ld();
-          if (n < A.N) {
+          if (adapters > 0) {
+            uint32_t bad = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c + i < rows) proj_write<BN, F8>(A, t_tile, t0 + c + i, n, sw, vb[i], vd[i], adapters > 0);
+            for (int i = 0; i < 16; ++i) bad |= fabsf(vd[i]) < __int_as_float(0x7F800000) ? 0u : 1u << i;
+            if (n >= A.N) bad = 0;
+            if (rows - c < 16) bad &= (1u << (rows - c)) - 1u;
+            if (__any_sync(0xFFFFFFFFu, bad != 0)) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (bad >> i & 1u) vd[i] = proj_own_delta(A, t_tile, BN, t0 + c + i, n);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if constexpr (F8) vb[i] *= __shfl_sync(0xFFFFFFFFu, scale, i) * sw;
+            vb[i] += vd[i];
+          }
+          if (n < A.N) {
+            if (rows - c >= 16) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i, y += A.ldy) *y = __float2bfloat16_rn(vb[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i, y += A.ldy)
+                if (c + i < rows) *y = __float2bfloat16_rn(vb[i]);
+            }
           }
         }
       } else {
