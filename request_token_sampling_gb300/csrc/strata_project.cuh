@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A, int tile_row
 // block a part of K, and adds the parts up in rank order (few tiles have work, so K is split eight ways).  8-bit rows
 // are widened to bfloat16 (exactly)
 // on their way to the operand by the four warps that later write the result.
-constexpr int INNER_SPLIT = 8, INNER_ROWS = 256;
+constexpr int INNER_SPLIT = 8, INNER_ROWS = 128;
 constexpr int INNER_A = PROJ_M * PROJ_LINE;
 __host__ __device__ constexpr int inner_stages(bool f8) { return f8 ? 3 : 4; }
 __host__ __device__ constexpr int inner_stage_bytes(bool f8) { return INNER_A + INNER_ROWS * PROJ_LINE * (f8 ? 3 : 2) / 2; }
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
     fence_proxy_async_smem();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B->tmem)), "r"(256u) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B->tmem)), "r"(static_cast<uint32_t>(INNER_ROWS)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
     tc_fence_after();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256u) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(INNER_ROWS)) : "memory");
   }
 }
 
