@@ -82,7 +82,7 @@ int call_device(const Tensor& t, const char* name) {
 }
 
 int narrow(int64_t v, const char* name) {
-  if (v > INT32_MAX) refuse(PyExc_ValueError, name, "is too large");
+  if (v < 0 || v > INT32_MAX) refuse(PyExc_ValueError, name, "is out of range");
   return static_cast<int>(v);
 }
 
@@ -234,6 +234,8 @@ TAIL_CALL(draw) {
   if (a[6] != Py_None) {
     V = PyLong_AsLongLong(a[6]);
     if (V == -1 && PyErr_Occurred()) throw Refused();
+    // the C call can only compare V with the stride, which may reach past the tensor
+    if (V < 1 || V > width) refuse(PyExc_ValueError, "V", "must be 1 to the logits' width");
   }
   Rows rl = rows(&logits, "logits", B, width, type, device);
   if (B <= 1) rl.ld = (rl.ld + 7) / 8 * 8;
