@@ -361,15 +361,17 @@ struct DrawRow {
     return static_cast<int>(heard_sum(0)) - 1;
   }
 
+  // Distances count from here, so that an infinite largest logit shares step 0 with the greatest finite ones.
+  __device__ __forceinline__ float finite_top() const { return fminf(top, 3.402823466e38f); }
   // The step of distance that a logit is in.  Truncated by an addition of 2^23 rounded towards zero: a conversion
-  // would share its unit with the exponential.  An infinite largest logit leaves infinities in step 0.
+  // would share its unit with the exponential.
   __device__ __forceinline__ int bin(float x) const {
-    const float d = fminf(fmaxf(fminf(top, 3.402823466e38f) - x, 0.0f), (DRAW_BINS - 0.5f) / DRAW_STEPS);
+    const float d = fminf(fmaxf(finite_top() - x, 0.0f), (DRAW_BINS - 0.5f) / DRAW_STEPS);
     return __float_as_int(__fmaf_rz(d, DRAW_STEPS, 8388608.0f)) & (2 * DRAW_BINS - 1);
   }
   // A logit at or below every entry of the bins before `b`, and above -inf.
   __device__ __forceinline__ float floor_of(int b) const {
-    return b >= DRAW_BINS ? -3.402823466e38f : fmaxf(-3.402823466e38f, top - b * (1.0001f / DRAW_STEPS));
+    return b >= DRAW_BINS ? -3.402823466e38f : fmaxf(-3.402823466e38f, finite_top() - b * (1.0001f / DRAW_STEPS));
   }
 
   // Sums f over the row into bins at(x), of the logits from `least` on, and adds the blocks' bins up, each block
@@ -594,7 +596,7 @@ struct DrawRow {
   // sum.  It is in bin `b`, and `under` is the sum of the bins before.  f is 0 for what earlier cuts took.
   template <typename F>
   __device__ void pin(F f, int b, u64 under, u64 target, uint32_t* K, int* I) {
-    const float least = floor_of(b + 1), most = b == 0 ? top : fminf(top, top - b * (0.9999f / DRAW_STEPS));
+    const float least = floor_of(b + 1), most = b == 0 ? top : finite_top() - b * (0.9999f / DRAW_STEPS);
     __syncthreads();
     if (threadIdx.x == 0) sh->local = 0;
     __syncthreads();
