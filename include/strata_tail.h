@@ -15,7 +15,9 @@
  * an argument, and calls on several streams are independent as long as their buffers are.  All of
  * them may be captured in a CUDA graph.  A call with no rows does nothing and returns STRATA_OK.
  * Their launches are set up while the kernel before them on the stream runs (programmatic dependent
- * launch) and wait on the GPU for it to end before they touch memory.
+ * launch) and wait on the GPU for it to end before they touch memory.  Beside sampling calls of the
+ * same stream: the first of them behind a call with STRATA_FLAG_OWN_OUTPUTS (which waits for nothing)
+ * and the first call with STRATA_FLAG_EARLY_LOAD behind one of them are launched without that overlap.
  */
 #ifndef STRATA_TAIL_H
 #define STRATA_TAIL_H

@@ -12,7 +12,7 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libstrata_sample.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("strata_sample.cu", "strata_tail.cu", "strata_project.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
-    "strata_kernel.cuh", "strata_device.cuh", "strata_resident.cuh", "strata_merge.cuh", "strata_host.h",
+    "strata_kernel.cuh", "strata_device.cuh", "strata_resident.cuh", "strata_merge.cuh", "strata_host.h", "strata_chain.h",
     "strata_norm.cuh", "strata_draw.cuh", "strata_project.cuh")]
 DEPENDS += [os.path.join(ROOT, "include", f) for f in ("strata_sample.h", "strata_tail.h")]
 MODULE_PATH = os.path.join(LIB_DIR, "_strata_tail.so")

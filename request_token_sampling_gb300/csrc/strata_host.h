@@ -6,32 +6,20 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
-
 namespace strata {
 
 // Stores a one-line message for strata_last_error() and returns `code`.
 __attribute__((visibility("hidden"), format(printf, 2, 3))) int host_fail(int code, const char* fmt, ...);
 
-// The current device's word of STRATA_DEVERR_* bits and its number of SMs.
-__attribute__((visibility("hidden"))) int tail_device(uint32_t** errors, int* sms);
+// The current device, its word of STRATA_DEVERR_* bits and its number of SMs.
+__attribute__((visibility("hidden"))) int tail_device(int* device, uint32_t** errors, int* sms);
 
-// Whether a sampling call with STRATA_FLAG_OWN_OUTPUTS was launched in this process.  Its kernel waits for nothing
-// before it, so that its end says nothing of what came earlier on its stream.
-inline std::atomic<bool>& waitless_launched() {
-  static std::atomic<bool> seen{false};
-  return seen;
-}
-
-// A launch that may be set up while the kernel before it on the stream still runs: the kernel waits for that one
-// (griddepcontrol.wait) before it reads or writes anything of the caller's, or of the workspace, and that one has
-// waited for those before it.  Where a kernel without such a wait may be among them, the launch is an ordinary
-// one, unless it `follows` a kernel of the same call.
+// A launch.  One that overlaps may be set up while the kernel before it on the stream still runs: the kernel waits
+// for that one (griddepcontrol.wait) before it reads or writes anything of the caller's, or of the workspace.
 struct Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[3];
-  Launch(unsigned grid, unsigned block, size_t smem, void* stream, unsigned cluster = 1, bool follows = false,
-         bool together = false) {
+  Launch(unsigned grid, unsigned block, size_t smem, void* stream, bool overlaps, unsigned cluster = 1, bool together = false) {
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(block, 1, 1);
     cfg.dynamicSmemBytes = smem;
@@ -42,7 +30,7 @@ struct Launch {
       attrs[cfg.numAttrs].val.clusterDim.y = attrs[cfg.numAttrs].val.clusterDim.z = 1;
       ++cfg.numAttrs;
     }
-    if (follows || !waitless_launched().load(std::memory_order_acquire)) {
+    if (overlaps) {
       attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       attrs[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
       ++cfg.numAttrs;

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "../../include/strata_tail.h"
+#include "strata_chain.h"
 #include "strata_host.h"
 #include "strata_project.cuh"
 
@@ -131,11 +132,12 @@ int pair_rows(int T, int N, int k_stages, bool adapters, int sms) {
 }
 
 // The current device's entry (checked: it is usable), or an error code.
-int current_device(const Device** dev) {
+int current_device(const Device** dev, int* device) {
   int id = -1;
   const cudaError_t e = cudaGetDevice(&id);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   if (id >= 64) return host_fail(STRATA_ERANGE, "device %d", id);
+  *device = id;
   try {
     *dev = &device_info(id);
   } catch (...) {  // no exception leaves a C call
@@ -149,9 +151,9 @@ int64_t lists_bytes(int t_tiles, int bn) { return (static_cast<int64_t>(t_tiles)
 
 }  // namespace
 
-int strata::tail_device(uint32_t** errors, int* sms) {
+int strata::tail_device(int* device, uint32_t** errors, int* sms) {
   const Device* dev = nullptr;
-  const int rc = current_device(&dev);
+  const int rc = current_device(&dev, device);
   if (rc != STRATA_OK) return rc;
   *errors = dev->errors;
   *sms = dev->sms;
@@ -196,9 +198,9 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
     return host_fail(STRATA_EINVAL, "the workspace needs %lld bytes on 256 bytes of alignment", static_cast<long long>(need));
   const Device* found = nullptr;
-  if (const int rc = current_device(&found); rc != STRATA_OK) return rc;
+  int device = 0;
+  if (const int rc = current_device(&found, &device); rc != STRATA_OK) return rc;
   const Device& dev = *found;
-  cudaError_t e = cudaSuccess;
 
   const cuuint32_t elems = f8 ? 128 : 64;
   const int k_stages = (K + static_cast<int>(elems) - 1) / static_cast<int>(elems);
@@ -236,7 +238,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   A.w = w;
   A.ldw = ldw;
 
-  CUtensorMap mw, mx, mb{}, mh{}, ma{};
+  CUtensorMap mw, mx, mb{}, mh{}, ma{}, mt{};
   const int box_rows = R % 128 == 0 ? 128 : R % 64 == 0 ? 64 : R % 32 == 0 ? 32 : 16;  // of a, in one copy
   {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N)};
@@ -260,46 +262,52 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
     const cuuint32_t hbox[2] = {static_cast<cuuint32_t>(A.rank_block), static_cast<cuuint32_t>(pair > 0 ? bn / 2 : bn)};
     if (!encode(dev.encode, &mh, false, 2, A.spread, hdims, strides, hbox, A.rank_block * 2))
       return host_fail(STRATA_EINVAL, "the workspace cannot be mapped");
-    auto map_a = [&]() {
+    if (T > SHRINK_ROWS) {
       const cuuint64_t adims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(S) * R};
       const cuuint64_t astrides[1] = {static_cast<cuuint64_t>(K) * 2};
       const cuuint32_t abox[2] = {64, static_cast<cuuint32_t>(box_rows)};
-      return encode(dev.encode, &ma, false, 2, a, adims, astrides, abox, 128);
-    };
-    if (T <= SHRINK_ROWS) {
-      strata::Launch launch(static_cast<unsigned>(T), 256, 0, stream);
-      launch.cfg.gridDim.y = static_cast<unsigned>(R / 8);
-      e = f8 ? launch(strata::shrink_kernel<__nv_fp8_e4m3>, A, bn) : launch(strata::shrink_kernel<__nv_bfloat16>, A, bn);
-    } else if (pair > 0) {
-      if (!map_a()) return host_fail(STRATA_EINVAL, "a cannot be mapped");
-      e = strata::Launch(static_cast<unsigned>(t_tiles), 256, 0, stream)(strata::plan_kernel, A);
-    } else {
-      CUtensorMap mt;
+      if (!encode(dev.encode, &ma, false, 2, a, adims, astrides, abox, 128)) return host_fail(STRATA_EINVAL, "a cannot be mapped");
+    }
+    if (T > SHRINK_ROWS && pair == 0) {
       const cuuint64_t xdims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(T)};
       const cuuint64_t xstrides[1] = {static_cast<cuuint64_t>(ldx * esz)};
       const cuuint32_t xbox[2] = {64, static_cast<cuuint32_t>(bn)};
-      if (!map_a() || !encode(dev.encode, &mt, f8, 2, x, xdims, xstrides, xbox, f8 ? 0 : 128))
-        return host_fail(STRATA_EINVAL, "a or x cannot be mapped");
-      // clusters of a tile: one where the tiles fill the GPU, as many as there can be work for where they do not
-      const int groups = std::min((most * R + strata::PROJ_M - 1) / strata::PROJ_M,
-                                  std::max(1, dev.sms / strata::INNER_SPLIT / t_tiles));
-      const strata::Launch launch(static_cast<unsigned>(t_tiles) * groups * strata::INNER_SPLIT, strata::PROJ_THREADS,
-                                  strata::inner_smem(f8), stream, strata::INNER_SPLIT);
-      e = launch(f8 ? strata::inner_kernel<true> : strata::inner_kernel<false>, ma, mt, A, groups, box_rows);
+      if (!encode(dev.encode, &mt, f8, 2, x, xdims, xstrides, xbox, f8 ? 0 : 128)) return host_fail(STRATA_EINVAL, "x cannot be mapped");
     }
-    if (e != cudaSuccess) return cuda_fail(e, "strata_project_rows");
   }
-  const int ranks = pair > 0 ? 1 : split_ranks(tiles, k_stages, dev.sms);
+  // the inner rows (or, for pairs, the lists alone)
+  auto launch_inner = [&](bool overlaps) {
+    if (T <= SHRINK_ROWS) {
+      strata::Launch launch(static_cast<unsigned>(T), 256, 0, stream, overlaps);
+      launch.cfg.gridDim.y = static_cast<unsigned>(R / 8);
+      return f8 ? launch(strata::shrink_kernel<__nv_fp8_e4m3>, A, bn) : launch(strata::shrink_kernel<__nv_bfloat16>, A, bn);
+    }
+    if (pair > 0) return strata::Launch(static_cast<unsigned>(t_tiles), 256, 0, stream, overlaps)(strata::plan_kernel, A);
+    // clusters of a tile: one where the tiles fill the GPU, as many as there can be work for where they do not
+    const int groups = std::min((most * R + strata::PROJ_M - 1) / strata::PROJ_M,
+                                std::max(1, dev.sms / strata::INNER_SPLIT / t_tiles));
+    const strata::Launch launch(static_cast<unsigned>(t_tiles) * groups * strata::INNER_SPLIT, strata::PROJ_THREADS,
+                                strata::inner_smem(f8), stream, overlaps, strata::INNER_SPLIT);
+    return launch(f8 ? strata::inner_kernel<true> : strata::inner_kernel<false>, ma, mt, A, groups, box_rows);
+  };
   // starts beside the inner rows' kernel and waits for it before what it wrote
-  const int64_t units = S > 0 ? static_cast<int64_t>(t_tiles) * ((most * R + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M)) : 0;
-  if (pair > 0) {
-    const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles + units, dev.sms / 2));
-    e = strata::Launch(2 * pairs, strata::PROJ_THREADS, strata::pair_smem(), stream, 1, S > 0, S > 0)(strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows);
-  } else {
+  auto launch_products = [&](bool overlaps) {
+    if (pair > 0) {
+      const int64_t units = S > 0 ? static_cast<int64_t>(t_tiles) * ((most * R + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M)) : 0;
+      const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles + units, dev.sms / 2));
+      return strata::Launch(2 * pairs, strata::PROJ_THREADS, strata::pair_smem(), stream, overlaps, 1, S > 0)(
+          strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows);
+    }
+    const int ranks = split_ranks(tiles, k_stages, dev.sms);
     const unsigned grid = static_cast<unsigned>(ranks > 1 ? tiles * ranks : std::min<int64_t>(tiles, dev.sms));
-    e = strata::Launch(grid, strata::PROJ_THREADS, strata::proj_smem(bn), stream, static_cast<unsigned>(ranks), S > 0)(
+    return strata::Launch(grid, strata::PROJ_THREADS, strata::proj_smem(bn), stream, overlaps, static_cast<unsigned>(ranks))(
         kernel_for(bn, f8, ranks > 1), mw, mx, mb, mh, A);
-  }
+  };
+  const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
+    if (S == 0) return launch_products(overlaps);
+    const cudaError_t first = launch_inner(overlaps);
+    return first == cudaSuccess ? launch_products(true) : first;
+  });
   return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_project_rows");
 }
 

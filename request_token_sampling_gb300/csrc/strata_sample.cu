@@ -17,9 +17,11 @@
 #include <cstring>
 #include <mutex>
 #include <new>
+#include <optional>
 #include <vector>
 
 #include "../../include/strata_sample.h"
+#include "strata_chain.h"
 #include "strata_host.h"
 #include "strata_kernel.cuh"
 #include "strata_merge.cuh"
@@ -358,7 +360,7 @@ bool trace_on() {
   return on;
 }
 
-int launch(strata_ctx* c, const KParams& P, int dtype, const Shape& sh, uint32_t flags, cudaStream_t stream,
+int launch(const KParams& P, int dtype, const Shape& sh, uint32_t flags, cudaStream_t stream,
            const char* entry) {
   if (trace_on())
     std::fprintf(stderr,
@@ -379,20 +381,33 @@ int launch(strata_ctx* c, const KParams& P, int dtype, const Shape& sh, uint32_t
   attrs[na].val.clusterDim.y = 1;
   attrs[na].val.clusterDim.z = 1;
   ++na;
-  if (flags & STRATA_FLAG_PDL) {
+  const bool mask = P.mode == strata::MODE_SAMPLE && (flags & STRATA_FLAG_ALLOWED_MASK) != 0u && P.allowed_off != nullptr;
+  const bool early = (flags & STRATA_FLAG_EARLY_LOAD) != 0u, own = early && (flags & STRATA_FLAG_OWN_OUTPUTS) != 0u;
+  bool overlaps = (flags & STRATA_FLAG_PDL) != 0u;
+  // beside the operators of strata_tail.h on the same stream: see strata_chain.h
+  if (own && overlaps) strata::waitless_used().store(true);
+  std::optional<strata::Chain> chain;
+  cudaError_t e;
+  if (strata::operators_used().load()) {
+    try {
+      int device = 0;  // there may be no context
+      if ((e = cudaGetDevice(&device)) != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+      chain.emplace(device, stream);
+    } catch (...) {  // no exception leaves a C call
+      return fail(STRATA_ECUDA, "kernel launch: out of host memory");
+    }
+    overlaps = overlaps && (*chain)->sampling_overlaps(early);
+  }
+  if (overlaps) {
     attrs[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[na].val.programmaticStreamSerializationAllowed = 1;
     ++na;
   }
   cfg.attrs = attrs;
   cfg.numAttrs = na;
-  cudaError_t e;
-  const bool mask = P.mode == strata::MODE_SAMPLE && (flags & STRATA_FLAG_ALLOWED_MASK) != 0u && P.allowed_off != nullptr;
-  const bool own = (flags & STRATA_FLAG_OWN_OUTPUTS) != 0u && (flags & STRATA_FLAG_EARLY_LOAD) != 0u;
-  if (own && (flags & STRATA_FLAG_PDL) != 0u) strata::waitless_launched().store(true, std::memory_order_release);
   e = cudaLaunchKernelEx(&cfg, kernel_for(dtype, mask, own, sh.resident, sh.two), P);
   if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
-  (void)c;
+  if (chain) (*chain)->sampling_launched(overlaps, early, own);
   return STRATA_OK;
 }
 
@@ -794,7 +809,7 @@ static int sample_rows_impl(strata_ctx* c, const void* logits, int dtype, int B,
   P.done = c->d_done;
   P.ring = kept_hist ? c->d_ring : nullptr;
   P.hlen = kept_hist ? c->d_hlen : nullptr;
-  rc = launch(c, P, dtype, sh, flags, static_cast<cudaStream_t>(stream),
+  rc = launch(P, dtype, sh, flags, static_cast<cudaStream_t>(stream),
               row_draft != nullptr ? "sample_verify" : "sample_rows");
   if (rc == STRATA_OK) c->late_counters_pending = pending_after(c->late_counters_pending, flags, true);
   return rc;
@@ -864,7 +879,7 @@ int strata_logprobs_rows(strata_ctx* c, const void* logits, int dtype, int B, in
   P.qw = sh.qw;
   flags = launch_flags(flags, c->late_counters_pending);
   P.flags = flags;
-  rc = launch(c, P, dtype, sh, flags, static_cast<cudaStream_t>(stream), "logprobs_rows");
+  rc = launch(P, dtype, sh, flags, static_cast<cudaStream_t>(stream), "logprobs_rows");
   if (rc == STRATA_OK) c->late_counters_pending = pending_after(c->late_counters_pending, flags, false);
   return rc;
 }
@@ -916,7 +931,7 @@ int strata_shard_rows(strata_ctx* c, const void* logits, int dtype, int B, int V
   P.flags = flags;
   P.id_off = id_offset;
   P.rec = static_cast<unsigned char*>(records);
-  rc = launch(c, P, dtype, sh, flags, static_cast<cudaStream_t>(stream), "shard_rows");
+  rc = launch(P, dtype, sh, flags, static_cast<cudaStream_t>(stream), "shard_rows");
   if (rc == STRATA_OK) c->late_counters_pending = pending_after(c->late_counters_pending, flags, false);
   return rc;
 }
@@ -1148,5 +1163,5 @@ extern "C" int strata_sample_rows_noalloc(const void* logits, int dtype, int B, 
   P.nslot = sh.nslot;
   P.qw = sh.qw;
   P.flags = 0;
-  return launch(nullptr, P, dtype, sh, 0u, s, "sample_rows_noalloc");
+  return launch(P, dtype, sh, 0u, s, "sample_rows_noalloc");
 }

@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "../../include/strata_tail.h"
+#include "strata_chain.h"
 #include "strata_draw.cuh"
 #include "strata_host.h"
 #include "strata_norm.cuh"
@@ -24,28 +25,28 @@ bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_
 // to a row 6.3 us, four 8.7, one and two warps 7.8).  Few rows are bound by
 // latency: a row goes to as many threads as it has packs.
 template <typename E, int N, int PER, bool SHIFT>
-cudaError_t launch_norm(const strata::NormArgs& A, int least, void* stream) {
+cudaError_t launch_norm(const strata::NormArgs& A, int least, bool overlaps, void* stream) {
   if constexpr (PER <= (N == 1 ? 16 : 4)) {
     const int packs = (A.H + N - 1) / N, need = std::max((packs + PER - 1) / PER, SHIFT ? 2 * (N - 1) : 1);
-    if (PER < least || need > strata::norm_most_threads(N, PER)) return launch_norm<E, N, PER * 2, SHIFT>(A, least, stream);
+    if (PER < least || need > strata::norm_most_threads(N, PER)) return launch_norm<E, N, PER * 2, SHIFT>(A, least, overlaps, stream);
     constexpr int ROWS = 4;
     if (need <= 32)
-      return strata::Launch((A.T + ROWS - 1) / ROWS, 32 * ROWS, 0, stream)(strata::norm_kernel<E, N, PER, false, SHIFT>, A);
-    return strata::Launch(A.T, (need + 31) / 32 * 32, 0, stream)(strata::norm_kernel<E, N, PER, true, SHIFT>, A);
+      return strata::Launch((A.T + ROWS - 1) / ROWS, 32 * ROWS, 0, stream, overlaps)(strata::norm_kernel<E, N, PER, false, SHIFT>, A);
+    return strata::Launch(A.T, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::norm_kernel<E, N, PER, true, SHIFT>, A);
   } else {
-    return strata::Launch(A.T, 1024, 0, stream)(strata::norm_wide_kernel<E>, A);
+    return strata::Launch(A.T, 1024, 0, stream, overlaps)(strata::norm_wide_kernel<E>, A);
   }
 }
 
 // `packed`: all rows lie on 16 bytes; `alike`: they lie anywhere, but all tensors the same way.
 template <typename E>
-cudaError_t launch_norm(const strata::NormArgs& A, bool packed, bool alike, int sms, void* stream) {
+cudaError_t launch_norm(const strata::NormArgs& A, bool packed, bool alike, int sms, bool overlaps, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   const int packs = A.H / (packed || alike ? N : 1);
   const int least = A.T < 2 * sms ? 1 : packs > 64 ? 4 : packs > 32 ? 2 : 1;
-  return packed  ? launch_norm<E, N, 1, false>(A, least, stream)
-         : alike ? launch_norm<E, N, 1, true>(A, least, stream)
-                 : launch_norm<E, 1, 1, false>(A, least, stream);
+  return packed  ? launch_norm<E, N, 1, false>(A, least, overlaps, stream)
+         : alike ? launch_norm<E, N, 1, true>(A, least, overlaps, stream)
+                 : launch_norm<E, 1, 1, false>(A, least, overlaps, stream);
 }
 
 }  // namespace
@@ -70,8 +71,8 @@ extern "C" int strata_norm_rows(const void* x, int64_t ldx, const void* residual
     return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
   strata::NormArgs A{x, residual, weight, residual_out, y, q, scale, ldx, ldr, ldro, ldy, ldq, T, H, eps};
   uint32_t* errors = nullptr;
-  int sms = 0;
-  if (const int rc = strata::tail_device(&errors, &sms); rc != STRATA_OK) return rc;
+  int device = 0, sms = 0;
+  if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
   // 16 bytes at a time where the width, every stride and every address allow it
   const int64_t n = 16 / static_cast<int64_t>(esz);
   auto fits = [&](const void* p, int64_t ld, int64_t size) {
@@ -83,8 +84,10 @@ extern "C" int strata_norm_rows(const void* x, int64_t ldx, const void* residual
     return p == nullptr || ((reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(x)) % 16 == 0 && (T == 1 || (ld - ldx) % n == 0));
   };
   const bool alike = like_x(residual, ldr) && like_x(residual_out, ldro) && like_x(y, ldy);
-  const cudaError_t e = dtype == STRATA_DTYPE_F32 ? launch_norm<float>(A, packed, alike, sms, stream)
-                                                  : launch_norm<__nv_bfloat16>(A, packed, alike, sms, stream);
+  const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
+    return dtype == STRATA_DTYPE_F32 ? launch_norm<float>(A, packed, alike, sms, overlaps, stream)
+                                     : launch_norm<__nv_bfloat16>(A, packed, alike, sms, overlaps, stream);
+  });
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_norm_rows: %s", cudaGetErrorString(e));
 }
 
@@ -105,8 +108,8 @@ extern "C" int strata_draw_rows(const void* logits, int dtype, int B, int V, int
       misaligned(min_p, 4) || misaligned(out_ids, 4) || misaligned(out_lps, 4))
     return host_fail(STRATA_EALIGN, "a per-row array is not 4-byte aligned");
   uint32_t* errors = nullptr;
-  int sms = 0;
-  if (const int rc = strata::tail_device(&errors, &sms); rc != STRATA_OK) return rc;
+  int device = 0, sms = 0;
+  if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
   const bool f32 = dtype == STRATA_DTYPE_F32;
   const void* kernel = f32 ? reinterpret_cast<const void*>(strata::draw_kernel<float>)
                            : reinterpret_cast<const void*>(strata::draw_kernel<__nv_bfloat16>);
@@ -126,7 +129,9 @@ extern "C" int strata_draw_rows(const void* logits, int dtype, int B, int V, int
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(DRAW_SMEM));
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return host_fail(STRATA_ECUDA, "strata_draw_rows: %s", cudaGetErrorString(e));
-  const strata::Launch launch(static_cast<unsigned>(B) * ranks, strata::DRAW_THREADS, smem, stream, static_cast<unsigned>(ranks));
-  e = f32 ? launch(strata::draw_kernel<float>, A) : launch(strata::draw_kernel<__nv_bfloat16>, A);
+  e = strata::launch_operator(device, stream, [&](bool overlaps) {
+    const strata::Launch launch(static_cast<unsigned>(B) * ranks, strata::DRAW_THREADS, smem, stream, overlaps, static_cast<unsigned>(ranks));
+    return f32 ? launch(strata::draw_kernel<float>, A) : launch(strata::draw_kernel<__nv_bfloat16>, A);
+  });
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_draw_rows: %s", cudaGetErrorString(e));
 }

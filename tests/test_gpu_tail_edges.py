@@ -60,3 +60,99 @@ def test_draw_infinity_above_the_largest_finite_logits(G, dtype, V):
         assert (o["ids"] >= 0).all() and (o["lps"] <= 0).all() and (o["lps"] > -20).all()
     check_draw(G, x, u, p=[0.5, 0.99] * (B // 2))
     check_draw(G, x, u, m=[0.5] * B, t=[0.3] * B)
+
+
+# ------------------------------------------------------------------------------ beside the sampler
+def _projection(V, H=2048, T=8):
+    g = torch.Generator(device="cuda").manual_seed(V)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    return dict(x=r(T, H).to(BF), w=r(V, H).mul_(H ** -0.5).to(BF), a=r(2, 16, H).mul_(H ** -0.5).to(BF),
+                b=r(2, V, 16).mul_(0.25).to(BF), adapter_scale=torch.ones(2, device="cuda"),
+                row_adapter=(torch.arange(T, device="cuda") % 2).int())
+
+
+@pytest.mark.parametrize("between", ["own outputs", "early load", "own outputs twice"])
+def test_sampling_calls_behind_a_projection_see_all_of_it(G, between):
+    """A projection lets the next call start at once.  A sampling call of other logits that waits for nothing, or late,
+    comes between it and the calls that read its rows."""
+    V, T = 131072, 8
+    s = _projection(V)
+    want = G.project_rows(**s)
+    other = torch.randn(T, 4096, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    slot, pos = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
+    flags = G.STRATA_FLAG_PDL | G.STRATA_FLAG_EARLY_LOAD
+    between_flags = flags if between == "early load" else flags | G.STRATA_FLAG_OWN_OUTPUTS
+    reading = flags if between == "early load" else G.STRATA_FLAG_PDL
+    ones = torch.ones(T, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream), G.Sampler(device=0, max_slots=1, max_vocab=V, max_rows=T) as sampler:
+        sampler.set_slot(0, dict(temperature=0.0, seed=1))
+        stream.synchronize()
+        ref = sampler.sample(want, slot, pos, chosen_lp=True, flags=reading)  # the flags choose the split, and so the last bits
+        ref_draw = G.draw_rows(want, ones * 0.5)
+        y = torch.empty_like(want)
+        for i in range(10):
+            y.zero_()
+            own = [torch.empty(T, dtype=torch.int32, device="cuda") for _ in range(2)]
+            assert sampler.errors() == 0   # drains the stream: the flag counts again
+            G.project_rows(**s, out=y)
+            for ids in own[:2 if between == "own outputs twice" else 1]:
+                sampler.sample(other, slot, pos, flags=between_flags, out=dict(ids=ids))
+            o = sampler.sample(y, slot, pos, chosen_lp=True, flags=reading)
+            d = G.draw_rows(y, ones * 0.5)
+            assert torch.equal(o["ids"], ref["ids"]) and torch.equal(o["chosen_lp"], ref["chosen_lp"]), i
+            assert torch.equal(d["ids"], ref_draw["ids"]) and torch.equal(d["lps"], ref_draw["lps"]), i
+        assert sampler.errors() == 0 and G.tail_errors() == 0
+
+
+def test_operators_in_a_row_after_own_outputs_on_two_streams(G):
+    """norm -> project -> draw on two streams, each behind sampling calls that wait for nothing, eager and captured."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T, H, V = 8, 2048, 32000
+    s = _projection(V, H)
+    h = torch.randn(T, H, generator=g, device="cuda").to(BF)
+    weight, u = torch.ones(H, dtype=BF, device="cuda"), torch.rand(T, generator=g, device="cuda")
+    other = torch.randn(T, V, generator=g, device="cuda")
+    slot, pos = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
+    flags = G.STRATA_FLAG_PDL | G.STRATA_FLAG_EARLY_LOAD | G.STRATA_FLAG_OWN_OUTPUTS
+
+    def step(x):
+        y = G.project_rows(**dict(s, x=G.norm_rows(x, weight)["y"]))
+        return y, G.draw_rows(y, u)
+
+    want = step(h)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    contexts = [G.Sampler(device=0, max_slots=1, max_vocab=V, max_rows=T) for _ in streams]
+    try:
+        for c in contexts:
+            c.set_slot(0, dict(temperature=0.7, seed=3))
+        torch.cuda.synchronize()
+        got, own = [], []
+        for _ in range(10):
+            for stream, c in zip(streams, contexts):
+                with torch.cuda.stream(stream):
+                    late = torch.zeros_like(h)
+                    late.copy_(h)
+                    own.append(c.sample(other, slot, pos, flags=flags))
+                    got += [step(late), step(late)]
+        graph = torch.cuda.CUDAGraph()
+        x = torch.zeros_like(h)
+        outs = [torch.empty(T, dtype=torch.int32, device="cuda") for _ in range(2)]
+        with torch.cuda.graph(graph):
+            x.copy_(h)
+            contexts[0].sample(other, slot, pos, flags=flags, out=dict(ids=outs[0]))
+            captured = step(x)
+            contexts[0].sample(other, slot, pos, flags=flags, out=dict(ids=outs[1]))
+            captured2 = step(x)
+        for _ in range(3):
+            x.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for y, d in [*got, captured, captured2]:
+            assert torch.equal(y, want[0]) and torch.equal(d["ids"], want[1]["ids"]) and torch.equal(d["lps"], want[1]["lps"])
+        assert all(c.errors() == 0 for c in contexts) and G.tail_errors() == 0
+    finally:
+        for c in contexts:
+            c.close()
