@@ -12,8 +12,9 @@
  * on `stream` only, STRATA_OK or a negative STRATA_E* code with strata_last_error(), and argument
  * checks before any work is enqueued (a call that returns an error has launched nothing).  These
  * calls need no context: they run on the calling thread's current device, every buffer they use is
- * an argument, and calls on several streams are independent as long as their buffers are.  All of
- * them may be captured in a CUDA graph.  A call with no rows does nothing and returns STRATA_OK.
+ * an argument, and calls on several streams are independent as long as their buffers are.  The three
+ * operators may be captured in a CUDA graph (strata_tail_errors waits, and may not).  A call with no rows
+ * does nothing and returns STRATA_OK.
  * Their launches are set up while the kernel before them on the stream runs (programmatic dependent
  * launch) and wait on the GPU for it to end before they touch memory.  Beside sampling calls of the
  * same stream: the first of them behind a call with STRATA_FLAG_OWN_OUTPUTS (which waits for nothing)
@@ -94,8 +95,9 @@ int strata_draw_rows(const void* logits, int dtype, int B, int V, int64_t ld, co
 
 /*
  * Bits that the kernels of the calls above raised on the current device since the last call, read
- * after the stream's work so far (this call waits for it) and cleared: STRATA_DEVERR_TIMEOUT, a
- * bounded wait inside a kernel ran out and the call's output is not valid.
+ * after the stream's work so far (this call waits for it) and cleared in one step: STRATA_DEVERR_TIMEOUT,
+ * a bounded wait inside a kernel ran out and the call's output is not valid.  The bits are those of all
+ * streams: each is told to one caller.
  */
 int strata_tail_errors(uint32_t* bits, void* stream);
 

@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "../../include/strata_tail.h"
@@ -311,12 +312,26 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_project_rows");
 }
 
+// The bits and their clearing in one step, which no kernel of another stream comes between.  A call has a word of its
+// own for the answer while it waits.
+constexpr unsigned ERROR_CALLS = 64;
+__device__ uint32_t g_told[ERROR_CALLS];
+__global__ void take_errors(unsigned call) { g_told[call] = atomicExch(&g_tail_errors, 0u); }
+
 extern "C" int strata_tail_errors(uint32_t* bits, void* stream) {
   if (bits == nullptr) return host_fail(STRATA_EINVAL, "null bits");
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_tail_errors, sizeof(*bits), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_tail_errors, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_tail_errors");
+  static std::atomic<unsigned> calls{0};
+  static std::mutex busy[ERROR_CALLS];
+  try {
+    const unsigned call = calls.fetch_add(1) % ERROR_CALLS;
+    std::lock_guard<std::mutex> hold(busy[call]);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    take_errors<<<1, 1, 0, s>>>(call);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(bits, g_told, sizeof(*bits), call * sizeof(*bits), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_tail_errors");
+  } catch (...) {  // no exception leaves a C call
+    return host_fail(STRATA_ECUDA, "strata_tail_errors");
+  }
 }
