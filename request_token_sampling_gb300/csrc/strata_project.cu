@@ -236,8 +236,6 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   A.n_tiles = n_tiles;
   A.t_tiles = t_tiles;
   A.tile_rows = bn;
-  A.w = w;
-  A.ldw = ldw;
 
   CUtensorMap mw, mx, mb{}, mh{}, ma{}, mt{};
   const int box_rows = R % 128 == 0 ? 128 : R % 64 == 0 ? 64 : R % 32 == 0 ? 32 : 16;  // of a, in one copy

@@ -44,8 +44,6 @@ struct ProjectArgs {
   int most;               // adapters that a tile can have: min(S, tile rows)
   int rank_block;         // R is cut into blocks of 64, 32 or 16 (one swizzle line of shared memory)
   int n_tiles, t_tiles, tile_rows;
-  int64_t ldw;            // of w, for sums that are taken again
-  const void* w;
 };
 
 constexpr int PROJ_M = 128;        // outputs of a tile: the accumulator's lanes
@@ -480,18 +478,77 @@ struct ProjBars {
   uint32_t tmem, dead;
 };
 
-// delta for one output and row from its own adapter alone, where the tile's sum is not finite.
-__device__ __noinline__ float proj_own_delta(const ProjectArgs& A, int tile, int tile_rows, int t, int n) {
+// Where a row's inner row lies in the spread of its tile, or -1 for a row without an adapter.
+__device__ __forceinline__ int64_t proj_place(const ProjectArgs& A, int tile, int tile_rows, int t) {
   const int c = A.row_adapter[t];
-  if (c < 0 || c >= A.S) return 0.0f;
+  if (c < 0 || c >= A.S) return -1;
   const int32_t* list = A.lists + static_cast<int64_t>(tile) * (tile_rows + 1);
-  int j = 0;
-  while (j < (list[0] & LIST_COUNT) && list[1 + j] != c) ++j;
-  const __nv_bfloat16* h = A.spread + ((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - tile * tile_rows)) * A.R;
-  const __nv_bfloat16* b = A.b + (static_cast<int64_t>(c) * A.N + n) * A.R;
+  int j = 0;  // its adapter's place among the list's ascending ids
+  for (int to = (list[0] & LIST_COUNT) - 1; j < to;) {
+    const int at = (j + to) / 2;
+    if (list[1 + at] < c)
+      j = at + 1;
+    else
+      to = at;
+  }
+  return ((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - tile * tile_rows)) * A.R;
+}
+// delta for one output and row from its own adapter alone, where the tile's sum is not finite.
+__device__ __noinline__ float proj_own_delta(const ProjectArgs& A, int64_t place, int t, int n) {
+  const uint4* h = reinterpret_cast<const uint4*>(A.spread + place);
+  const uint4* b = reinterpret_cast<const uint4*>(A.b + (static_cast<int64_t>(A.row_adapter[t]) * A.N + n) * A.R);
   float d = 0.0f;
-  for (int r = 0; r < A.R; ++r) d = fmaf(proj_f32(__ldcg(h + r)), proj_f32(b[r]), d);
+#pragma unroll 4
+  for (int i = 0; i < A.R / 8; ++i) {
+    const uint4 hv = __ldcg(h + i), bv = b[i];
+    const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w}, bw[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      d = fmaf(__uint_as_float(hw[e] << 16), __uint_as_float(bw[e] << 16), d);
+      d = fmaf(__uint_as_float(hw[e] & 0xFFFF0000u), __uint_as_float(bw[e] & 0xFFFF0000u), d);
+    }
+  }
   return d;
+}
+
+// The same of the rows t .. t + 3, where `bad` has their bits; `some`: of any lane.  The rows go side by side, so that
+// their loads do not wait for one another: one row after another took 1.3 us each.
+__device__ __forceinline__ void proj_own_deltas(const ProjectArgs& A, int tile, int tile_rows, int t, int n, uint32_t bad,
+                                                uint32_t some, float* d) {
+  const int lane = threadIdx.x & 31;
+  const int64_t place = lane < 4 && (some >> lane & 1u) ? proj_place(A, tile, tile_rows, t + lane) : -1;  // of row t + lane
+  const int c = place >= 0 ? A.row_adapter[t + lane] : -1;
+  const uint4 *h[4], *b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t its = __shfl_sync(0xFFFFFFFFu, place, i);
+    const int ci = __shfl_sync(0xFFFFFFFFu, c, i);
+    if (bad >> i & 1u) d[i] = 0.0f;
+    if (ci < 0) bad &= ~(1u << i);
+    h[i] = reinterpret_cast<const uint4*>(A.spread + max(its, static_cast<int64_t>(0)));
+    b[i] = reinterpret_cast<const uint4*>(A.b + (static_cast<int64_t>(max(ci, 0)) * A.N + n) * A.R);
+  }
+#pragma unroll 1
+  for (int r = 0; r < A.R / 8; ++r) {
+    uint4 hv[4], bv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (bad >> i & 1u) {
+        hv[i] = __ldcg(h[i] + r);
+        bv[i] = b[i][r];
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (bad >> i & 1u) {
+        const uint32_t hw[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w}, bw[4] = {bv[i].x, bv[i].y, bv[i].z, bv[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          d[i] = fmaf(__uint_as_float(hw[e] << 16), __uint_as_float(bw[e] << 16), d[i]);
+          d[i] = fmaf(__uint_as_float(hw[e] & 0xFFFF0000u), __uint_as_float(bw[e] & 0xFFFF0000u), d[i]);
+        }
+      }
+  }
+  __syncwarp();
 }
 
 template <int BN, bool F8>
@@ -500,7 +557,10 @@ __device__ __forceinline__ void proj_write(const ProjectArgs& A, int t_tile, int
   float v = base;
   if constexpr (F8) v *= A.x_scale[t] * sw;
   if (adapters) {
-    if (!(fabsf(delta) < __int_as_float(0x7F800000))) delta = proj_own_delta(A, t_tile, BN, t, n);
+    if (!(fabsf(delta) < __int_as_float(0x7F800000))) {
+      const int64_t place = proj_place(A, t_tile, BN, t);
+      delta = place < 0 ? 0.0f : proj_own_delta(A, place, t, n);
+    }
     v += delta;
   }
   A.y[t * A.ldy + n] = __float2bfloat16_rn(v);
@@ -700,10 +760,10 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
             for (int i = 0; i < 16; ++i) bad |= fabsf(vd[i]) < __int_as_float(0x7F800000) ? 0u : 1u << i;
             if (n >= A.N) bad = 0;
             if (rows - c < 16) bad &= (1u << (rows - c)) - 1u;
-            if (__any_sync(0xFFFFFFFFu, bad != 0)) {
+            if (const uint32_t some = __reduce_or_sync(0xFFFFFFFFu, bad); some != 0) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (bad >> i & 1u) vd[i] = proj_own_delta(A, t_tile, BN, t0 + c + i, n);
+              for (int i = 0; i < 16; i += 4)
+                if (some >> i & 15u) proj_own_deltas(A, t_tile, BN, t0 + c + i, n, bad >> i & 15u, some >> i & 15u, vd + i);
             }
           }
 #pragma unroll
@@ -802,7 +862,10 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
 // the pair's products read the other half from the other SM, so that an SM takes in 64 bytes a cycle
 // where a tile of 128 x 128 on one SM would need 128.  base and delta are one accumulator here, and two
 // tiles have room in tensor memory: a tile is written while the next is summed.  What a broken adapter
-// spoils in other requests' rows is therefore found in the sum, and that sum is taken again.
+// spoils in other requests' rows is therefore found in the sums: where one is not finite and an adapter of the tile
+// has an infinity or a NaN for that output, the pair goes through such tiles again at the end, with base in one
+// accumulator and the sound adapters, then each broken one alone, in the other, and writes such outputs anew
+// (4,099 x 4,096 x 4,096, us: sound 101, one infinity in an adapter 161, an adapter of NaN 195, 400 rows of NaN 111).
 // The inner rows are tiles of the same kind, before all others: 256 of a tile's stacked products a unit, with
 // the matrices a in w's place.  A tile of outputs adds its adapters last, and waits before that until its
 // rows' units are done.  They are the lowest tiles, so they are taken first and wait for nothing; the launch is
@@ -816,7 +879,8 @@ __host__ __device__ constexpr int pair_smem() { return PAIR_STAGES * PAIR_STAGE 
 
 struct PairBars {
   uint64_t full[PAIR_STAGES], empty[PAIR_STAGES], done[2], freed[2], drained;
-  uint32_t tmem, dead;
+  uint32_t tmem, dead, again;
+  uint32_t which[8];  // of a tile's list: adapters with an infinity or a NaN for one of the pair's 256 outputs
 };
 
 __device__ __forceinline__ void pair_tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
@@ -865,13 +929,36 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// One output of one row from its own operands alone.
-__device__ __noinline__ float proj_own_sum(const ProjectArgs& A, int tile, int t, int n) {
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(A.x) + t * A.ldx;
-  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(A.w) + n * A.ldw;
-  float s = 0.0f;
-  for (int k = 0; k < A.K; ++k) s = fmaf(proj_f32(x[k]), proj_f32(w[k]), s);
-  return s + proj_own_delta(A, tile, A.tile_rows, t, n);
+__device__ __forceinline__ void dsmem_or_u32(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// For which of the outputs n .. n + 31 a tile's adapters have an infinity or a NaN, as bits; the whole warp.  With `which`
+// (a shared address), the bits of such adapters' places in the list are set there, in both blocks of the pair.
+__device__ __noinline__ uint32_t proj_broken(const ProjectArgs& A, const int32_t* list, int n, uint32_t which) {
+  const int count = list[0] & LIST_COUNT, pieces = A.R / 8, lane = threadIdx.x & 31;  // pieces of 16 bytes to an output
+  uint32_t broken = 0;
+  for (int k = lane; k < 32 * pieces; k += 32) {
+    const int of = k / pieces;
+    if (n + of >= A.N) break;
+    bool any = false;
+    for (int j0 = 0; j0 < count; j0 += 16) {  // sixteen loads on their way
+      uint4 v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = reinterpret_cast<const uint4*>(A.b + (static_cast<int64_t>(list[1 + min(j0 + i, count - 1)]) * A.N + n) * A.R)[k];
+      uint32_t found = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        for (const uint32_t w : {v[i].x, v[i].y, v[i].z, v[i].w})
+          if ((w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u) found |= 1u << min(i, count - 1 - j0);
+      any |= found != 0;
+      if (found != 0 && which != 0u)
+        for (uint32_t q = 0; q < 2; ++q) dsmem_or_u32(dsmem_addr(which + 4 * (j0 >> 5), q), found << (j0 & 31));
+    }
+    broken |= static_cast<uint32_t>(any) << of;
+  }
+  __syncwarp();
+  return __reduce_or_sync(0xFFFFFFFFu, broken);
 }
 
 // The lists of a call's tiles; no unit is done.
@@ -911,7 +998,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
       mbar_init(&B->freed[i], 8);  // the first block's: four warps of each
     }
     mbar_init(&B->drained, 1);
-    B->dead = 0;
+    B->dead = B->again = 0;
+    for (uint32_t& w : B->which) w = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -957,14 +1045,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
     return (tile - at.before) * 2 * PROJ_M;
   };
 
+  Ring<PAIR_STAGES> ring;  // of the loading and of the issuing warp
+  bool alive = true;
+  uint32_t turn = 0;       // tiles so far, of the issuing warp and of those that write
+  auto room = [&]() {      // in the next stage
+    if (ring.begun >= PAIR_STAGES && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) alive = false;
+    return alive;
+  };
+  auto landed = [&]() {  // the next stage
+    if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit)) alive = false;
+    tc_fence_after();
+    return alive;
+  };
+  // 256 outputs: M counts in sixteens
+  const uint32_t idesc = (mma_idesc(false, rows_max) & 0x00FFFFFFu) | (16u << 24);
+  // a stage of rank blocks: `n` of them from rank block `rb` of the list's adapter j on
+  auto load_blocks = [&](int t_tile, int n0, int j, int rb, int n) {
+    const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
+    if (elect_one()) {
+      if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(2 * n * (PROJ_M + half)) * line);
+      for (int i = 0; i < n; ++i) {
+        pair_tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, list_of(t_tile)[1 + j], bar);
+        pair_tma_2d(at + PROJ_M * PROJ_LINE + i * half * line, &mh, rb * A.rank_block,
+                    (t_tile * A.most + j) * rows_max + rank * half, bar);
+        if (++rb == blocks) rb = 0, ++j;
+      }
+    }
+  };
+  auto add_blocks = [&](uint32_t sum, int n, bool add) {
+    const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE);
+    if (elect_one()) {
+      for (int i = 0; i < n; ++i) {
+        const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
+        const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * half * line, line);
+        for (int q = 0; q < A.rank_block / 16; ++q) pair_mma(sum, da + 2 * q, db + 2 * q, idesc, add || i > 0 || q > 0);
+      }
+      pair_commit(&B->empty[ring.slot]);
+    }
+  };
+  auto load_base = [&](int t0, int n0) {
+    for (int s = 0; s < k_stages && room(); ++s, ring.next()) {
+      const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
+      if (elect_one()) {
+        if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(2 * (PROJ_M + half) * PROJ_LINE));
+        pair_tma_2d(at, &mw, s * 64, n0, bar);
+        pair_tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * 64, t0, bar);
+      }
+    }
+  };
+  auto add_base = [&](uint32_t sum) {
+    for (int s = 0; s < k_stages && landed(); ++s, ring.next()) {
+      const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE);
+      const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + PROJ_M * PROJ_LINE, PROJ_LINE);
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pair_mma(sum, da + 2 * i, db + 2 * i, idesc, s > 0 || i > 0);
+        pair_commit(&B->empty[ring.slot]);
+      }
+    }
+  };
+  auto freed_all = [&]() {  // the products in flight end before the blocks give their tensor memory back
+    if (elect_one()) pair_commit(&B->drained);
+    for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->drained, 0); ++spin) {
+    }
+  };
+
   if (warp == 0) {
-    Ring<PAIR_STAGES> ring;
-    bool alive = true;
     Place place;
-    auto room = [&]() {  // in the next stage
-      if (ring.begun >= PAIR_STAGES && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) alive = false;
-      return alive;
-    };
     for (int tile = first; tile < tiles && alive; tile += step) {
       const int q0 = unit_of(tile, place), t_tile = place.t_tile, t0 = t_tile * rows_max + rank * half;
       if (q0 >= 0) {
@@ -986,14 +1133,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
         continue;
       }
       const int n0 = ((tile - units) / A.t_tiles * 2 + rank) * PROJ_M;
-      for (int s = 0; s < k_stages && room(); ++s, ring.next()) {
-        const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
-        if (elect_one()) {
-          if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(2 * (PROJ_M + half) * PROJ_LINE));
-          pair_tma_2d(at, &mw, s * 64, n0, bar);
-          pair_tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * 64, t0, bar);
-        }
-      }
+      load_base(t0, n0);
       if (A.S == 0 || !alive) continue;
       {  // its rows' units: eight warps of a pair write each
         const uint32_t need = static_cast<uint32_t>(units_of(t_tile)) * 8;
@@ -1010,35 +1150,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
         }
         asm volatile("fence.proxy.async;" ::: "memory");
       }
-      const int32_t* list = list_of(t_tile);
-      const int subs = (list[0] & LIST_COUNT) * blocks;
-      for (int sub0 = 0; sub0 < subs && alive && room(); sub0 += per_stage, ring.next()) {
-        const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
-        const int n = min(per_stage, subs - sub0);
-        if (elect_one()) {
-          if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(2 * n * (PROJ_M + half)) * line);
-          for (int i = 0; i < n; ++i) {
-            const int j = (sub0 + i) / blocks, rb = (sub0 + i) % blocks;
-            pair_tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, list[1 + j], bar);
-            pair_tma_2d(at + PROJ_M * PROJ_LINE + i * half * line, &mh, rb * A.rank_block,
-                        (t_tile * A.most + j) * rows_max + rank * half, bar);
-          }
-        }
-      }
+      const int subs = (list_of(t_tile)[0] & LIST_COUNT) * blocks;
+      for (int sub0 = 0; sub0 < subs && alive && room(); sub0 += per_stage, ring.next())
+        load_blocks(t_tile, n0, sub0 / blocks, sub0 % blocks, min(per_stage, subs - sub0));
     }
     if (!alive && lead) ring.drain(B->full);
   } else if (warp == 1 && lead) {
-    // 256 outputs: M counts in sixteens
-    const uint32_t idesc = (mma_idesc(false, rows_max) & 0x00FFFFFFu) | (16u << 24);
-    Ring<PAIR_STAGES> ring;
-    uint32_t turn = 0;
-    bool alive = true;
     Place place;
-    auto landed = [&]() {  // the next stage
-      if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit)) alive = false;
-      tc_fence_after();
-      return alive;
-    };
     for (int tile = first; tile < tiles && alive; tile += step, ++turn) {
       const int q0 = unit_of(tile, place);
       const uint32_t buf = turn & 1, sum = tmem + buf * 256;
@@ -1047,46 +1165,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
         break;
       }
       tc_fence_after();
-      for (int s = 0; s < k_stages && landed(); ++s, ring.next()) {
-        const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE);
-        const uint64_t da = mma_desc(at, PROJ_LINE), db = mma_desc(at + PROJ_M * PROJ_LINE, PROJ_LINE);
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) pair_mma(sum, da + 2 * i, db + 2 * i, idesc, s > 0 || i > 0);
-          pair_commit(&B->empty[ring.slot]);
-        }
-      }
+      add_base(sum);
       if (A.S > 0 && q0 < 0) {
         const int subs = (list_of(place.t_tile)[0] & LIST_COUNT) * blocks;
-        for (int sub0 = 0; sub0 < subs && alive && landed(); sub0 += per_stage, ring.next()) {
-          const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE);
-          const int n = min(per_stage, subs - sub0);
-          if (elect_one()) {
-            for (int i = 0; i < n; ++i) {
-              const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
-              const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * half * line, line);
-              for (int q = 0; q < A.rank_block / 16; ++q) pair_mma(sum, da + 2 * q, db + 2 * q, idesc, true);
-            }
-            pair_commit(&B->empty[ring.slot]);
-          }
-        }
+        for (int sub0 = 0; sub0 < subs && alive && landed(); sub0 += per_stage, ring.next())
+          add_blocks(sum, min(per_stage, subs - sub0), true);
       }
       if (alive && elect_one()) pair_commit(&B->done[buf]);
     }
-    if (!alive) {
-      if (elect_one()) pair_commit(&B->drained);
-      for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->drained, 0); ++spin) {
-      }
-    }
+    if (!alive) freed_all();
   } else if (warp >= 2) {
     const uint32_t quarter = warp & 3;
-    uint32_t turn = 0;
     Place place;
     for (int tile = first; tile < tiles; tile += step, ++turn) {
       const int q0 = unit_of(tile, place), t_tile = place.t_tile, t0 = t_tile * rows_max;
       const int rows = min(rows_max, A.T - t0), lane_at = rank * PROJ_M + quarter * 32 + lane;
       const uint32_t buf = turn & 1, sum = tmem + buf * 256 + (quarter << 21);
-      if (!proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit)) break;
+      if (!proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit)) {
+        alive = false;
+        break;
+      }
       tc_fence_after();
       if (q0 >= 0) {
         // inner rows: zeros where a row has another adapter
@@ -1119,6 +1217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
       }
       const int n = (tile - units) / A.t_tiles * 2 * PROJ_M + lane_at;
       const bool mixed = A.S > 0 && (list_of(t_tile)[0] & LIST_MIXED) != 0;
+      bool looked = false;  // at what the adapters have for the warp's outputs
       __nv_bfloat16* y = A.y + t0 * A.ldy + n;
 #pragma unroll 1
       for (int c = 0; c < rows; c += 32) {  // the last columns of a buffer's 256 may be stale: they are not used
@@ -1126,16 +1225,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
         tmem_ld32(sum + c, v);
         tmem_wait_ld();
         if (mixed) {
-          // a sum that is not finite is taken again, from its row's own operands
           uint32_t bad = 0;
 #pragma unroll
           for (int i = 0; i < 32; ++i) bad |= fabsf(v[i]) < __int_as_float(0x7F800000) ? 0u : 1u << i;
-          if (n >= A.N) bad = 0;
           if (rows - c < 32) bad &= (1u << (rows - c)) - 1u;
-          if (__any_sync(0xFFFFFFFFu, bad != 0)) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (bad >> i & 1u) v[i] = proj_own_sum(A, t_tile, t0 + c + i, n);
+          // a row's own operands may be the reason: then its sum stands
+          if (!looked && __any_sync(0xFFFFFFFFu, bad != 0 && n < A.N)) {
+            looked = true;
+            const uint32_t again = *static_cast<volatile uint32_t*>(&B->again);
+            if (__all_sync(0xFFFFFFFFu, again == 0u) && proj_broken(A, list_of(t_tile), n - lane, 0u) != 0u && lane < 2)
+              dsmem_st_u32(dsmem_addr(smem_u32(&B->again), lane), 1u);
+            __syncwarp();
           }
         }
         if (n < A.N) {
@@ -1155,8 +1255,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
     }
   }
   __syncthreads();
-  cluster_arrive();  // neither block's shared or tensor memory is given back while the other's products use it
+  cluster_arrive();
   cluster_wait();
+  if (B->again != 0u) {  // the same in both blocks
+    // Base in the first buffer, adapters in the second.  Both are free; what waits for them counts on with the first
+    // one's barriers.
+    tc_fence_after();
+    const bool died = !alive;
+    const uint32_t quarter = warp & 3, base = tmem, delta = tmem + 256;
+    uint32_t round = (turn + 1) / 2;  // of done[0] and freed[0]
+#pragma unroll 1
+    for (int tile = first; tile < tiles; tile += step) {
+      const int t_tile = tile < units ? 0 : (tile - units) % A.t_tiles, t0 = t_tile * rows_max;
+      const int32_t* list = list_of(t_tile);
+      if (tile < units || (list[0] & LIST_MIXED) == 0) continue;
+      const int n0 = ((tile - units) / A.t_tiles * 2 + rank) * PROJ_M, count = list[0] & LIST_COUNT;
+      const int rows = min(rows_max, A.T - t0), n = n0 + quarter * 32 + lane;
+      uint32_t columns = 0;  // of this warp's, those to write
+      if (warp >= 2) columns = proj_broken(A, list, n - lane, smem_u32(B->which));
+      __syncthreads();
+      cluster_arrive();
+      cluster_wait();
+      uint32_t some = 0;
+      for (int i = 0; i < 8; ++i) some |= B->which[i];
+      auto is_broken = [&](int j) { return (B->which[j >> 5] >> (j & 31) & 1u) != 0u; };
+      // a round for the sound ones (-1), then one for each broken one
+      auto next_broken = [&](int j) {
+        for (++j; j < count && !is_broken(j); ++j) {
+        }
+        return j;
+      };
+      if (some != 0u) {
+        if (warp == 0) {
+          if (alive) load_base(t0 + rank * half, n0);
+          for (int own = -1; own < count && alive; own = next_broken(own))
+            for (int j = max(own, 0); j < (own < 0 ? count : own + 1); ++j) {
+              if (own < 0 && is_broken(j)) continue;
+              for (int rb = 0; rb < blocks && alive && room(); rb += per_stage, ring.next())
+                load_blocks(t_tile, n0, j, rb, min(per_stage, blocks - rb));
+            }
+        } else if (warp == 1 && lead) {
+          uint32_t in_tile = 0;
+          for (int own = -1; own < count && alive; own = next_broken(own), ++round, ++in_tile) {
+            // the round before has been written (the last tile's last one before the barrier)
+            if (in_tile > 0 && !proj_wait(&B->freed[0], (round + 1) & 1, dead, A.errors, bit)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            if (own < 0) add_base(base);
+            bool add = false;
+            for (int j = max(own, 0); j < (own < 0 ? count : own + 1); ++j) {
+              if (own < 0 && is_broken(j)) continue;
+              for (int rb = 0; rb < blocks && alive && landed(); rb += per_stage, ring.next()) {
+                add_blocks(delta, min(per_stage, blocks - rb), add);
+                add = true;
+              }
+            }
+            if (alive && elect_one()) pair_commit(&B->done[0]);
+          }
+        } else if (warp >= 2) {
+          const bool mine = columns >> lane & 1u;
+          for (int own = -1; own < count && alive; own = next_broken(own), ++round) {
+            if (!proj_wait(&B->done[0], round & 1, dead, A.errors, bit)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < rows && columns != 0; c0 += 32) {
+              const int of = c0 + lane < rows ? A.row_adapter[t0 + c0 + lane] : -1;
+              const bool has = of >= 0 && of < A.S;
+              bool now = own < 0 ? c0 + lane < rows : of == list[1 + own];
+              if (own < 0)
+                for (int j = next_broken(-1); j < count; j = next_broken(j)) now = now && of != list[1 + j];
+              const uint32_t writes = __ballot_sync(0xFFFFFFFFu, now), adds = __ballot_sync(0xFFFFFFFFu, now && has);
+              if (writes == 0) continue;
+              float v[32], d[32];
+              tmem_ld32(base + (quarter << 21) + c0, v);
+              tmem_ld32(delta + (quarter << 21) + c0, d);
+              tmem_wait_ld();
+              if (mine) {
+                __nv_bfloat16* y = A.y + (t0 + c0) * A.ldy + n;
+#pragma unroll
+                for (int i = 0; i < 32; ++i, y += A.ldy)
+                  if (writes >> i & 1u) *y = __float2bfloat16_rn(adds >> i & 1u ? v[i] + d[i] : v[i]);
+              }
+              __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(dsmem_addr(smem_u32(&B->freed[0]), 0));
+          }
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x < 8) B->which[threadIdx.x] = 0;
+      cluster_arrive();
+      cluster_wait();
+      tc_fence_after();
+    }
+    if (!alive && !died && lead) {
+      if (warp == 0) ring.drain(B->full);
+      if (warp == 1) freed_all();
+    }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+  }
+  // neither block's shared or tensor memory is given back while the other's products use it: both are past a barrier
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");

@@ -62,6 +62,81 @@ def test_draw_infinity_above_the_largest_finite_logits(G, dtype, V):
     check_draw(G, x, u, m=[0.5] * B, t=[0.3] * B)
 
 
+# ------------------------------------------------------------------------------ project_rows
+def _time(f):
+    """Median of five calls, in ms."""
+    f()
+    times = []
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    return sorted(times)[2]
+
+
+@pytest.mark.parametrize("T,N,K,S,R,spread", [(2049, 4096, 4096, 8, 64, True), (4099, 4096, 4096, 8, 64, False), (1500, 3001, 1096, 40, 16, True),
+                                              (1031, 4100, 520, 3, 48, False), (2500, 2304, 264, 2, 256, True), (700, 20000, 136, 300, 32, True)])
+def test_project_broken_requests_stay_alone_and_cost_little(G, T, N, K, S, R, spread):
+    """Prompts with infinities and NaN in one request's adapter or rows: the other rows are what they were, the call takes
+    no more than a few times as long, and no wait runs out."""
+    from test_gpu_tail import check_project, project_case
+    of = None if spread else [(i // 300) % (S + 1) - 1 for i in range(T)]
+    s = project_case(T, N, K, S, R, "bf16", T + K, of=of)
+    c = int(s["row_adapter"][T // 2].clamp(min=0))
+    s["row_adapter"][7] = -1
+    mine = s["row_adapter"] == c
+    assert mine.any() and (~mine).any()
+    y = G.project_rows(**s)
+    check_project(s, y)
+    sound = _time(lambda: G.project_rows(**s))
+    inf, nan = math.inf, math.nan
+
+    def run(**over):
+        t = dict(s, **over)
+        got = G.project_rows(**t)
+        assert _time(lambda: G.project_rows(**t)) < 10 * sound + 0.05
+        assert G.tail_errors() == 0
+        return got
+
+    def same_but(got, rows, columns):
+        """The rows' outputs in these columns are not finite, all others in these columns right, the rest the same bits."""
+        hit = torch.zeros_like(y, dtype=torch.bool)
+        hit[rows.nonzero(), columns] = True
+        assert not got[hit].isfinite().any()
+        rest = torch.ones(N, dtype=torch.bool, device="cuda")
+        rest[columns] = False
+        assert torch.equal(got[:, rest], y[:, rest])
+        check_project(s, torch.where(hit, y, got))
+
+    b = s["b"].clone()
+    b[c, 100, 3] = inf
+    same_but(run(b=b), mine, torch.tensor([100], device="cuda"))
+    b[c, 101, 0], b[c, N - 1, R - 1], b[c, 0, 5] = nan, -inf, nan
+    same_but(run(b=b), mine, torch.tensor([0, 100, 101, N - 1], device="cuda"))
+    b[c] = nan
+    same_but(run(b=b), mine, torch.arange(N, device="cuda"))
+    a = s["a"].clone()
+    a[c, 2, K // 2] = nan
+    got = run(a=a)
+    assert got[mine].isnan().all() and torch.equal(got[~mine], y[~mine])
+    x = s["x"].clone()
+    x[mine] = nan
+    got = run(x=x)
+    assert got[mine].isnan().all() and torch.equal(got[~mine], y[~mine])
+    # broken rows of one request and a broken adapter of another
+    other = (s["row_adapter"] >= 0) & ~mine
+    d = int(s["row_adapter"][other][0])
+    b = s["b"].clone()
+    b[d, 50] = inf
+    got = run(x=x, b=b)
+    assert got[mine].isnan().all() and not got[s["row_adapter"] == d, 50].isfinite().any()
+    keep = ~mine & (s["row_adapter"] != d)
+    assert torch.equal(got[keep][:, 51:], y[keep][:, 51:]) and got[keep].isfinite().all()
+
+
 # ------------------------------------------------------------------------------ beside the sampler
 def _projection(V, H=2048, T=8):
     g = torch.Generator(device="cuda").manual_seed(V)
