@@ -28,23 +28,29 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def torch_dir() -> str | None:
+    """Where PyTorch is installed, if it is (it is not imported)."""
+    from importlib.util import find_spec
+    spec = find_spec("torch")
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(MODULE_PATH):
+    made = [LIB_PATH] + ([MODULE_PATH] if torch_dir() else [])
+    if not all(os.path.exists(p) for p in made):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MODULE_PATH))
+    t = min(os.path.getmtime(p) for p in made)
     return all(os.path.getmtime(p) <= t for p in DEPENDS)
 
 
-def module_commands(out: str):
-    """Compile and link the PyTorch binding (host code only) against the installed PyTorch and Python."""
+def module_commands(out: str, torch: str):
+    """Compile and link the PyTorch binding (host code only) against the PyTorch in `torch` and this Python."""
     import sysconfig
-    from importlib.util import find_spec
-    torch_dir = os.path.dirname(find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
-    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
     obj = os.path.join(LIB_DIR, "tail_binding.o")
-    libs = os.path.join(torch_dir, "lib")
+    libs = os.path.join(torch, "lib")
     compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[f for d in inc for f in ("-isystem", d)], "-c", "-o",
                 obj, MODULE_SOURCE]
     link = ["g++", "-shared", "-o", out, obj, "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
@@ -53,7 +59,8 @@ def module_commands(out: str):
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/ into _lib/: libstrata_sample.so (statically linked CUDA runtime) and the PyTorch binding."""
+    """Compile csrc/ into _lib/: libstrata_sample.so (statically linked CUDA runtime) and, where PyTorch is
+    installed, the operators' PyTorch binding."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
@@ -64,8 +71,10 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     objects = [os.path.join(LIB_DIR, os.path.splitext(os.path.basename(s))[0] + ".o") for s in SOURCES]
     started = [subprocess.Popen([nvcc_path(), *flags, "-c", "-o", o, s], stdout=subprocess.PIPE,
                                 stderr=subprocess.STDOUT, text=True) for s, o in zip(SOURCES, objects)]
-    compile_module, link_module = module_commands(MODULE_PATH + ".tmp")
-    started.append(subprocess.Popen(compile_module, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+    torch = torch_dir()
+    if torch:
+        compile_module, link_module = module_commands(MODULE_PATH + ".tmp", torch)
+        started.append(subprocess.Popen(compile_module, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
     said = [p.communicate()[0] for p in started]
     for p, text in zip(started, said):
         if p.returncode != 0:
@@ -76,10 +85,11 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("nvcc failed to link:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB_PATH)
-    r = subprocess.run(link_module, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("g++ failed to link:\n" + r.stdout + r.stderr)
-    os.replace(MODULE_PATH + ".tmp", MODULE_PATH)
+    if torch:
+        r = subprocess.run(link_module, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("g++ failed to link:\n" + r.stdout + r.stderr)
+        os.replace(MODULE_PATH + ".tmp", MODULE_PATH)
     return LIB_PATH
 
 

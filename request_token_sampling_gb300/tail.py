@@ -4,8 +4,8 @@
 and write into the caller's tensors.  ``norm_rows``, ``project_rows`` and ``draw_rows`` allocate their outputs
 (and the projection's workspace) with PyTorch, on the stream that they run on.
 
-The calls go through a small compiled module (csrc/tail_binding.cpp), which checks the tensors, allocates and makes
-the C call; ``lib`` holds the C functions themselves for ctypes.
+The calls go through a small compiled module (csrc/tail_binding.cpp, loaded by the first of them), which checks the
+tensors, allocates and makes the C call; ``lib`` holds the C functions themselves for ctypes.
 """
 from __future__ import annotations
 
@@ -46,22 +46,35 @@ def _declare() -> None:
 _declare()
 
 
-def _load_module():
-    """The compiled half of this binding (csrc/tail_binding.cpp); like the library it calls, it has to be built."""
+def _load_module() -> None:
+    """Load the compiled half of this binding (csrc/tail_binding.cpp) at the first call of an operator: the rest of
+    the package does not need it, nor PyTorch.  Like the library that it calls, it has to be built."""
+    global _norm, _project, _draw
     from importlib.machinery import ExtensionFileLoader
     from importlib.util import module_from_spec, spec_from_loader
+    import torch  # noqa: F401  (its libraries and types come first)
     if not os.path.exists(MODULE_PATH):
         raise ImportError(f"the PyTorch binding is not built ({MODULE_PATH}); "
                           "run `python -c 'import __graft_entry__ as g; g.build()'`")
-    import torch  # noqa: F401  (its libraries and types come first)
     loader = ExtensionFileLoader("_strata_tail", MODULE_PATH)
     module = module_from_spec(spec_from_loader("_strata_tail", loader))
     loader.exec_module(module)
-    return module
+    _norm, _project, _draw = module.norm, module.project, module.draw
 
 
-_module = _load_module()
-_norm, _project, _draw = _module.norm, _module.project, _module.draw
+def _norm(*args):
+    _load_module()
+    return _norm(*args)
+
+
+def _project(*args):
+    _load_module()
+    return _project(*args)
+
+
+def _draw(*args):
+    _load_module()
+    return _draw(*args)
 
 
 def _done(out):
