@@ -136,7 +136,8 @@ def norm_rows(x, weight, residual=None, eps: float = 1e-6, y: bool = True, f8: b
 
 def project_rows(x, w, x_scale=None, w_scale=None, a=None, b=None, row_adapter=None, adapter_scale=None, stream=None,
                  out=None):
-    """``x w^T`` with the rows' low-rank adapters, as a bfloat16 [T, N] tensor."""
+    """``x w^T`` with the rows' low-rank adapters, as a bfloat16 [T, N] tensor.  Rows that are allocated here start on
+    16 bytes, whatever N is: they can go to ``draw_rows`` and to the sampler as they are."""
     if stream is not None:
         with _side(stream, x):
             return project_rows(x, w, x_scale, w_scale, a, b, row_adapter, adapter_scale, None, out)

@@ -247,3 +247,42 @@ def test_no_error_bit_is_lost(G, tmp_path):
     assert r.returncode == 0, r.stderr[-2000:]
     r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout[-500:]
+
+
+# ------------------------------------------------------------------------------ from one to the next
+@pytest.mark.parametrize("N", [50257, 32001, 1003, 7, 1])
+@pytest.mark.parametrize("T", [1, 2, 40, 300])
+def test_projected_rows_go_to_the_draw_and_to_the_sampler(G, N, T):
+    """Logits of any vocabulary, as project_rows allocates them, are taken by draw_rows and by the sampler."""
+    from test_gpu_tail import check_project, project_case
+    s = project_case(T, N, 128, 3, 16, "bf16", N + T)
+    y = G.project_rows(**s)
+    check_project(s, y)
+    wide = torch.full((T, (N + 7) // 8 * 8 + 8), math.nan, dtype=BF, device="cuda")
+    wide[:, :N] = y
+    wide = wide[:, :N]
+    u = torch.rand(T, generator=torch.Generator(device="cuda").manual_seed(N), device="cuda")
+    keys = dict(temperature=torch.full((T,), 0.8, device="cuda"), top_k=torch.full((T,), 100, dtype=torch.int32, device="cuda"))
+    got, want = G.draw_rows(y, u, **keys), G.draw_rows(wide, u, **keys)
+    assert torch.equal(got["ids"], want["ids"]) and torch.equal(got["lps"], want["lps"])
+    slot, pos = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.arange(T, dtype=torch.int64, device="cuda")
+    with G.Sampler(device=0, max_slots=1, max_vocab=max(N, 64), max_rows=T) as sampler:
+        for rows in (y, wide):
+            sampler.set_slot(0, dict(temperature=0.7, top_k=20, top_p=0.95, seed=5), reset_counter=True)
+            got = sampler.sample(rows, slot, pos, chosen_lp=True)
+            if rows is y:
+                first = got
+        assert torch.equal(first["ids"], got["ids"]) and torch.equal(first["chosen_lp"], got["chosen_lp"])
+        assert ((got["ids"] >= 0) & (got["ids"] < N)).all() and sampler.errors() == 0
+
+
+def test_the_example_takes_any_vocabulary(G):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_tail.py")
+    spec = importlib.util.spec_from_file_location("decode_tail", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    ids, lps = mod.decode(5, 4099, 256, 4)
+    again, _ = mod.decode(5, 4099, 256, 4, graph=False)
+    assert torch.equal(ids, again) and ((ids >= 0) & (ids < 4099)).all() and (lps <= 0).all()
