@@ -41,46 +41,39 @@ Kernel kernel_for(int bn, bool f8, bool split) {
   return bn == 16 ? pick<16>(f8, split) : bn == 32 ? pick<32>(f8, split) : bn == 64 ? pick<64>(f8, split) : pick<128>(f8, split);
 }
 
-// What the calls need to know of a device, found at the first call on it.
+// What the calls need to know of a device, found at the first call on it that needs it.  A failure is not kept: the
+// next call tries again.
 struct Device {
+  std::mutex lock;
+  std::atomic<bool> known{false}, projects{false};
   int sms = 0;
   uint32_t* errors = nullptr;
-  EncodeFn encode = nullptr;
-  cudaError_t status = cudaSuccess;
+  EncodeFn encode = nullptr;  // this and the kernels' attributes: for projections
 };
 
-const Device& device_info(int id) {
-  static Device devices[64];
-  static std::once_flag once[64];
-  std::call_once(once[id], [id] {
-    Device& d = devices[id];
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if ((d.status = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, id)) != cudaSuccess) return;
-    if ((d.status = cudaGetSymbolAddress(&p, g_tail_errors)) != cudaSuccess) return;
-    d.errors = static_cast<uint32_t*>(p);
-    d.status = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
-    if (d.status != cudaSuccess) return;
-    if (found != cudaDriverEntryPointSuccess || p == nullptr) {
-      d.status = cudaErrorNotSupported;
-      return;
-    }
-    d.encode = reinterpret_cast<EncodeFn>(p);
-    for (int bn : BN_SIZES)
-      for (int i = 0; i < 4 && d.status == cudaSuccess; ++i)
-        d.status = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel_for(bn, i & 1, i & 2)),
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, strata::proj_smem(bn));
-    if (d.status == cudaSuccess)
-      d.status = cudaFuncSetAttribute(reinterpret_cast<const void*>(strata::pair_kernel),
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, strata::pair_smem());
-    if (d.status == cudaSuccess)
-      d.status = cudaFuncSetAttribute(reinterpret_cast<const void*>(strata::inner_kernel<false>),
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, strata::inner_smem(false));
-    if (d.status == cudaSuccess)
-      d.status = cudaFuncSetAttribute(reinterpret_cast<const void*>(strata::inner_kernel<true>),
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, strata::inner_smem(true));
-  });
-  return devices[id];
+cudaError_t find_device(Device& d, int id) {
+  void* p = nullptr;
+  cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, id);
+  if (e == cudaSuccess) e = cudaGetSymbolAddress(&p, g_tail_errors);
+  d.errors = static_cast<uint32_t*>(p);
+  return e;
+}
+
+cudaError_t find_projects(Device& d) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+  if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || p == nullptr)) e = cudaErrorNotSupported;
+  d.encode = reinterpret_cast<EncodeFn>(p);
+  auto shared = [&](const void* kernel, int bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  for (int bn : BN_SIZES)
+    for (int i = 0; i < 4; ++i) shared(reinterpret_cast<const void*>(kernel_for(bn, i & 1, i & 2)), strata::proj_smem(bn));
+  shared(reinterpret_cast<const void*>(strata::pair_kernel), strata::pair_smem());
+  shared(reinterpret_cast<const void*>(strata::inner_kernel<false>), strata::inner_smem(false));
+  shared(reinterpret_cast<const void*>(strata::inner_kernel<true>), strata::inner_smem(true));
+  return e;
 }
 
 // A map of `dims` (innermost first; strides in bytes of the outer ones) cut into boxes of `box`.
@@ -132,19 +125,32 @@ int pair_rows(int T, int N, int k_stages, bool adapters, int sms) {
   return rows;
 }
 
-// The current device's entry (checked: it is usable), or an error code.
-int current_device(const Device** dev, int* device) {
+// The current device's entry, with what projections need or without, or an error code.
+int current_device(const Device** dev, int* device, bool projects) {
+  static Device devices[64];
   int id = -1;
-  const cudaError_t e = cudaGetDevice(&id);
+  cudaError_t e = cudaGetDevice(&id);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   if (id >= 64) return host_fail(STRATA_ERANGE, "device %d", id);
-  *device = id;
-  try {
-    *dev = &device_info(id);
-  } catch (...) {  // no exception leaves a C call
-    return host_fail(STRATA_ECUDA, "device setup");
+  Device& d = devices[id];
+  if (!(projects ? d.projects : d.known).load(std::memory_order_acquire)) {
+    try {
+      std::lock_guard<std::mutex> hold(d.lock);
+      if (!d.known.load()) {
+        if ((e = find_device(d, id)) != cudaSuccess) return cuda_fail(e, "device setup");
+        d.known.store(true, std::memory_order_release);
+      }
+      if (projects && !d.projects.load()) {
+        if ((e = find_projects(d)) != cudaSuccess) return cuda_fail(e, "device setup");
+        d.projects.store(true, std::memory_order_release);
+      }
+    } catch (...) {  // no exception leaves a C call
+      return host_fail(STRATA_ECUDA, "device setup");
+    }
   }
-  return (*dev)->status == cudaSuccess ? STRATA_OK : cuda_fail((*dev)->status, "device setup");
+  *dev = &d;
+  *device = id;
+  return STRATA_OK;
 }
 
 // The lists and the words beside them.
@@ -154,7 +160,7 @@ int64_t lists_bytes(int t_tiles, int bn) { return (static_cast<int64_t>(t_tiles)
 
 int strata::tail_device(int* device, uint32_t** errors, int* sms) {
   const Device* dev = nullptr;
-  const int rc = current_device(&dev, device);
+  const int rc = current_device(&dev, device, false);
   if (rc != STRATA_OK) return rc;
   *errors = dev->errors;
   *sms = dev->sms;
@@ -200,7 +206,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
     return host_fail(STRATA_EINVAL, "the workspace needs %lld bytes on 256 bytes of alignment", static_cast<long long>(need));
   const Device* found = nullptr;
   int device = 0;
-  if (const int rc = current_device(&found, &device); rc != STRATA_OK) return rc;
+  if (const int rc = current_device(&found, &device, true); rc != STRATA_OK) return rc;
   const Device& dev = *found;
 
   const cuuint32_t elems = f8 ? 128 : 64;

@@ -99,3 +99,8 @@ def test_the_library_builds_without_pytorch(monkeypatch, tmp_path):
         assert os.path.exists(mod.MODULE_PATH) == installed
         assert any("g++" in a[0] for a in ran) == installed
         monkeypatch.undo()
+
+
+def test_a_failed_device_setup_is_tried_again(tmp_path):
+    r = subprocess.run([_program(tmp_path, "setup_check")], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.endswith("0 bad\n"), r.stdout[-2000:]
