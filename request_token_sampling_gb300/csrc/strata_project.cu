@@ -28,6 +28,7 @@ using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
 using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, strata::ProjectArgs);
 
 constexpr int MAX_ROWS = 1 << 19;  // rows times adapters of a tile count in 31 bits
+constexpr int MAX_OUTPUTS = INT32_MAX - 2 * strata::PROJ_M;  // outputs of the last tile, and beyond N, too
 constexpr int SHRINK_ROWS = 32;     // a call with more takes its inner rows from the tensor cores
 constexpr int BN_SIZES[4] = {16, 32, 64, 128};
 
@@ -171,7 +172,7 @@ extern "C" int64_t strata_project_workspace(int T, int S, int R) {
   if (T <= 0 || S <= 0 || R <= 0) return 0;
   if (T <= 128) return lists_bytes(1, 128) + static_cast<int64_t>(std::min(S, 128)) * 128 * R * 2;
   // whatever tiles the call takes: 64 to 256 rows each
-  return lists_bytes((T + 63) / 64, 256) + (static_cast<int64_t>(T) + 256) * std::min(S, 256) * R * 2;
+  return lists_bytes(static_cast<int>((static_cast<int64_t>(T) + 63) / 64), 256) + (static_cast<int64_t>(T) + 256) * std::min(S, 256) * R * 2;
 }
 
 extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
@@ -181,6 +182,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   if (dtype != STRATA_DTYPE_BF16 && dtype != STRATA_DTYPE_F8) return host_fail(STRATA_EINVAL, "dtype %d", dtype);
   if (T < 0 || N < 1) return host_fail(STRATA_EINVAL, "T=%d N=%d", T, N);
   if (T > MAX_ROWS) return host_fail(STRATA_ERANGE, "T=%d above %d", T, MAX_ROWS);
+  if (N > MAX_OUTPUTS) return host_fail(STRATA_ERANGE, "N=%d above %d", N, MAX_OUTPUTS);
   if (K < 1 || K > STRATA_TAIL_MAX_WIDTH) return host_fail(STRATA_ERANGE, "K=%d outside 1..%d", K, STRATA_TAIL_MAX_WIDTH);
   if (S < 0 || S > STRATA_TAIL_MAX_ADAPTERS) return host_fail(STRATA_ERANGE, "S=%d outside 0..%d", S, STRATA_TAIL_MAX_ADAPTERS);
   if (S > 0 && (R < 16 || R > STRATA_TAIL_MAX_RANK || R % 16 != 0))
@@ -215,8 +217,10 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   const int bn = pair > 0 ? pair : tile_rows(T), t_tiles = (T + bn - 1) / bn;
   const int n_tiles = pair > 0 ? (N + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M) : (N + strata::PROJ_M - 1) / strata::PROJ_M;
   const int64_t tiles = static_cast<int64_t>(t_tiles) * n_tiles;
-  if (tiles > INT32_MAX) return host_fail(STRATA_ERANGE, "T=%d N=%d", T, N);
   const int most = std::min(S, bn);
+  // tiles of inner products before the pairs' others
+  const int64_t units = pair > 0 && S > 0 ? static_cast<int64_t>(t_tiles) * ((most * R + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M)) : 0;
+  if (tiles + units > INT32_MAX - dev.sms) return host_fail(STRATA_ERANGE, "T=%d N=%d", T, N);  // they are counted in steps of the grid
   strata::ProjectArgs A{};
   A.x = x;
   A.x_scale = x_scale;
@@ -298,7 +302,6 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   // starts beside the inner rows' kernel and waits for it before what it wrote
   auto launch_products = [&](bool overlaps) {
     if (pair > 0) {
-      const int64_t units = S > 0 ? static_cast<int64_t>(t_tiles) * ((most * R + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M)) : 0;
       const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles + units, dev.sms / 2));
       return strata::Launch(2 * pairs, strata::PROJ_THREADS, strata::pair_smem(), stream, overlaps, 1, S > 0)(
           strata::pair_kernel, mw, mx, mb, mh, ma, A, box_rows);

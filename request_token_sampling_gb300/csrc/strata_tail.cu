@@ -31,7 +31,7 @@ cudaError_t launch_norm(const strata::NormArgs& A, int least, bool overlaps, voi
     if (PER < least || need > strata::norm_most_threads(N, PER)) return launch_norm<E, N, PER * 2, SHIFT>(A, least, overlaps, stream);
     constexpr int ROWS = 4;
     if (need <= 32)
-      return strata::Launch((A.T + ROWS - 1) / ROWS, 32 * ROWS, 0, stream, overlaps)(strata::norm_kernel<E, N, PER, false, SHIFT>, A);
+      return strata::Launch((static_cast<unsigned>(A.T) + ROWS - 1) / ROWS, 32 * ROWS, 0, stream, overlaps)(strata::norm_kernel<E, N, PER, false, SHIFT>, A);
     return strata::Launch(A.T, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::norm_kernel<E, N, PER, true, SHIFT>, A);
   } else {
     return strata::Launch(A.T, 1024, 0, stream, overlaps)(strata::norm_wide_kernel<E>, A);

@@ -62,6 +62,18 @@ def test_draw_infinity_above_the_largest_finite_logits(G, dtype, V):
     check_draw(G, x, u, m=[0.5] * B, t=[0.3] * B)
 
 
+# ------------------------------------------------------------------------------ norm_rows
+def test_norm_of_as_many_rows_as_an_int_counts(G):
+    T = 2 ** 31 - 2
+    x = torch.ones(T, 1, dtype=BF, device="cuda")
+    x[::3] = -2
+    y = G.norm_rows(x, torch.full((1,), 3.0, dtype=BF, device="cuda"), eps=0.0)["y"]
+    x.sign_().mul_(3)
+    assert y.shape == (T, 1)
+    for at in range(0, T, 1 << 28):
+        assert torch.equal(y[at:at + (1 << 28)], x[at:at + (1 << 28)])
+
+
 # ------------------------------------------------------------------------------ project_rows
 def _time(f):
     """Median of five calls, in ms."""

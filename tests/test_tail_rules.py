@@ -104,3 +104,14 @@ def test_the_library_builds_without_pytorch(monkeypatch, tmp_path):
 def test_a_failed_device_setup_is_tried_again(tmp_path):
     r = subprocess.run([_program(tmp_path, "setup_check")], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and r.stdout.endswith("0 bad\n"), r.stdout[-2000:]
+
+
+@pytest.mark.parametrize("N", [2 ** 31 - 1, 2 ** 31 - 128, 2 ** 31 - 256])
+def test_project_refuses_more_outputs_than_it_counts(N):
+    """Before any CUDA call: the outputs of the last tile count in 31 bits."""
+    _build_module().build_library()
+    import request_token_sampling_gb300 as S
+    P = 1 << 20
+    args = [P, 64, None, P, 64, None, S.STRATA_DTYPE_BF16, 4, N, 64, None, None, 0, 0, None, None, P, N, None, 0, None]
+    assert S.lib.strata_project_rows(*args) == S.STRATA_ERANGE
+    assert S.strata_project_workspace(2 ** 31 - 1, 1, 16) > 0
