@@ -60,7 +60,7 @@ int strata_norm_rows(const void* x, int64_t ldx, const void* residual, int64_t l
  * x and w are `dtype`: BF16 (no scales: pass NULL) or F8 (both scales).  a [S][R][K], b [S][N][R]
  * and y are bfloat16, a and b packed; a row whose row_adapter is outside 0..S-1 has no adapter.
  * S = 0 (the adapter pointers may be NULL) is the projection alone.  Sums are held in 32 bits; the inner row
- * (adapter_scale * x_scale * x a^T) is rounded to bfloat16 between its two products.
+ * (adapter_scale * x_scale * x a^T) is held as two bfloat16 (2^-16) between its two products.
  * An adapter's infinities and NaNs reach the rows that use it and no others.  T is at most 524,288, N 2^31 - 257.
  * x, w, a and b start on 16 bytes, and K and the strides ldx and ldw are multiples of 16 bytes; R is
  * a multiple of 16 (pad smaller ranks with zeros).  ldy >= N is any stride, y any bfloat16 address.

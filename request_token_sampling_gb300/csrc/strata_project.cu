@@ -170,9 +170,9 @@ int strata::tail_device(int* device, uint32_t** errors, int* sms) {
 
 extern "C" int64_t strata_project_workspace(int T, int S, int R) {
   if (T <= 0 || S <= 0 || R <= 0) return 0;
-  if (T <= 128) return lists_bytes(1, 128) + static_cast<int64_t>(std::min(S, 128)) * 128 * R * 2;
+  if (T <= 128) return lists_bytes(1, 128) + static_cast<int64_t>(std::min(S, 128)) * 128 * R * 4;
   // whatever tiles the call takes: 64 to 256 rows each
-  return lists_bytes(static_cast<int>((static_cast<int64_t>(T) + 63) / 64), 256) + (static_cast<int64_t>(T) + 256) * std::min(S, 256) * R * 2;
+  return lists_bytes(static_cast<int>((static_cast<int64_t>(T) + 63) / 64), 256) + (static_cast<int64_t>(T) + 256) * std::min(S, 256) * R * 4;
 }
 
 extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
@@ -233,6 +233,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   A.lists = static_cast<int32_t*>(workspace);
   A.ready = static_cast<uint32_t*>(workspace) + static_cast<int64_t>(t_tiles) * (bn + 1);
   A.spread = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + lists_bytes(t_tiles, bn));
+  A.low = static_cast<int64_t>(t_tiles) * most * bn * R;
   A.errors = dev.errors;
   A.ldx = ldx;
   A.ldy = ldy;
@@ -267,7 +268,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
     const cuuint64_t strides[2] = {bytes, bytes * static_cast<cuuint64_t>(N)};
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(A.rank_block), strata::PROJ_M, 1};
     if (!encode(dev.encode, &mb, false, 3, b, dims, strides, box, A.rank_block * 2)) return host_fail(STRATA_EINVAL, "b cannot be mapped");
-    const cuuint64_t hdims[2] = {r, static_cast<cuuint64_t>(t_tiles) * most * bn};
+    const cuuint64_t hdims[2] = {r, 2 * static_cast<cuuint64_t>(t_tiles) * most * bn};
     const cuuint32_t hbox[2] = {static_cast<cuuint32_t>(A.rank_block), static_cast<cuuint32_t>(pair > 0 ? bn / 2 : bn)};
     if (!encode(dev.encode, &mh, false, 2, A.spread, hdims, strides, hbox, A.rank_block * 2))
       return host_fail(STRATA_EINVAL, "the workspace cannot be mapped");

@@ -2,11 +2,11 @@
 //
 //   y[t] = sx[t] sw (x[t] w^T) + h[t] b_c^T,   h[t] = g_c sx[t] (x[t] a_c^T),   c = row_adapter[t]
 //
-// Two kernels.  shrink_kernel (few rows) or inner_kernel (many) computes the inner rows h in 32 bits and writes them, rounded to bfloat16,
-// spread out: for each tile of rows and each adapter of the tile a block [tile rows][R] that holds h where
-// the row uses that adapter and zeros elsewhere.  project_kernel then treats b of the tile's adapters as
+// Two kernels.  shrink_kernel (few rows) or inner_kernel (many) computes the inner rows h in 32 bits and writes them, as
+// two bfloat16 each, spread out: for each tile of rows and each adapter of the tile a block [tile rows][R] that holds h
+// where the row uses that adapter and zeros elsewhere.  project_kernel then treats b of the tile's adapters as
 // more of the sum's length: for a tile of 128 outputs and up to 128 rows,
-//   base += w[128][64] x[rows][64]^T  over K,     delta += b_j[128][R] spread_j[rows][R]^T  over the adapters j
+//   base += w[128][64] x[rows][64]^T  over K,     delta += b_j[128][R] spread_j[rows][R]^T  over the adapters j, both parts
 // with tcgen05.mma (outputs are its M, rows its N: a tile of w is read once for all rows).  base and delta
 // are separate accumulators: 8-bit rows scale base alone, and a product 0 * inf of a broken adapter,
 // which falls on other requests' rows in delta, is found there and taken back.  More than 128 rows of
@@ -35,7 +35,8 @@ struct ProjectArgs {
   const __nv_bfloat16 *a, *b;
   const int32_t* row_adapter;
   __nv_bfloat16* y;
-  __nv_bfloat16* spread;  // [tiles][most][tile rows][R]
+  __nv_bfloat16* spread;  // [upper, lower part][tiles][most][tile rows][R]
+  int64_t low;            // the lower parts' distance from the upper ones: tiles x most x tile rows x R
   int32_t* lists;         // per tile: how many adapters, then their ids in ascending order ([1 + tile rows])
   uint32_t* ready;        // per tile: warps that have written their part of its inner rows (pair_kernel)
   uint32_t* errors;
@@ -53,6 +54,8 @@ constexpr uint32_t PROJ_SPINS = 1u << 24;
 
 __host__ __device__ constexpr int proj_stage_bytes(int bn) { return (PROJ_M + bn) * PROJ_LINE; }
 __host__ __device__ constexpr int proj_stages(int bn) { return bn <= 16 ? 12 : bn <= 32 ? 11 : bn <= 64 ? 9 : 7; }
+// Stages of adapters whose inner rows' lower parts share one stage before them: as many as have room there.
+__host__ __device__ constexpr int proj_group(int bn) { return proj_stage_bytes(bn) / (bn * PROJ_LINE); }
 __host__ __device__ constexpr int proj_smem(int bn) { return proj_stages(bn) * proj_stage_bytes(bn) + 1024 + 512; }
 
 // ------------------------------------------------------------------------------ PTX
@@ -183,6 +186,14 @@ __device__ __forceinline__ float proj_warp_sum(float v) {
   return v;
 }
 
+// An inner product as two bfloat16 for the tensor cores, 16 of its 24 bits: with one of them alone its rounding
+// was a tenth of y's error.  What is not finite is all in the upper part.
+__device__ __forceinline__ void proj_split(float v, __nv_bfloat16& hi, __nv_bfloat16& lo) {
+  hi = __float2bfloat16_rn(v);
+  const float rest = v - __bfloat162float(hi);
+  lo = __float2bfloat16_rn(fabsf(rest) < __int_as_float(0x7F800000) ? rest : 0.0f);
+}
+
 // The adapters of a tile of rows, as the bits of 32 words, and whether a row has none; the whole block.
 struct TileAdapters {
   uint32_t bits[32], none;
@@ -246,10 +257,14 @@ __global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A, int tile_row
     s = proj_warp_sum(s);
     s = A.adapter_scale[c] * ((A.x_scale != nullptr ? A.x_scale[t] : 1.0f) * s);
   }
-  // rounded to bfloat16 for the tensor cores: up to 2^-8 of h, as y's own rounding is of y
-  for (int j = lane; j < count; j += 32)
-    A.spread[((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - t0)) * A.R + r] =
-        __float2bfloat16_rn(j == at ? s : 0.0f);
+  __nv_bfloat16 hi, lo;
+  proj_split(s, hi, lo);
+  const __nv_bfloat16 zero = __float2bfloat16_rn(0.0f);
+  for (int j = lane; j < count; j += 32) {
+    __nv_bfloat16* h = A.spread + ((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - t0)) * A.R + r;
+    h[0] = j == at ? hi : zero;
+    h[A.low] = j == at ? lo : zero;
+  }
 }
 
 // Many rows: the same inner rows on the tensor cores.  A cluster of INNER_SPLIT blocks takes 128 of the
@@ -438,7 +453,8 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         const float by = A.adapter_scale[c];
         __nv_bfloat16* to_row = A.spread + (static_cast<int64_t>(tile) * A.most + j) * rows_max * A.R + q % A.R;
         for (int t = id / FOURS; t < rows; t += GO) {
-          uint2 packed = make_uint2(0, 0);
+          __align__(8) __nv_bfloat16 hi[4], lo[4];
+          *reinterpret_cast<uint2*>(hi) = *reinterpret_cast<uint2*>(lo) = make_uint2(0, 0);
           if (A.row_adapter[t0 + t] == c) {
             float4 v[INNER_SPLIT];
 #pragma unroll
@@ -452,11 +468,12 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
               sum.w += v[i].w;
             }
             const float sx = A.x_scale != nullptr ? A.x_scale[t0 + t] : 1.0f;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(by * (sx * sum.x), by * (sx * sum.y)),
-                                 hi = __floats2bfloat162_rn(by * (sx * sum.z), by * (sx * sum.w));
-            packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            const float four[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) proj_split(by * (sx * four[i]), hi[i], lo[i]);
           }
-          *reinterpret_cast<uint2*>(to_row + t * A.R) = packed;
+          *reinterpret_cast<uint2*>(to_row + t * A.R) = *reinterpret_cast<const uint2*>(hi);
+          *reinterpret_cast<uint2*>(to_row + t * A.R + A.low) = *reinterpret_cast<const uint2*>(lo);
         }
       }
     }
@@ -493,20 +510,23 @@ __device__ __forceinline__ int64_t proj_place(const ProjectArgs& A, int tile, in
   }
   return ((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - tile * tile_rows)) * A.R;
 }
+// d + sum of eight (h + l) b
+__device__ __forceinline__ void proj_add8(const uint4& h, const uint4& l, const uint4& b, float& d) {
+  const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    d = fmaf(__uint_as_float(hw[e] << 16) + __uint_as_float(lw[e] << 16), __uint_as_float(bw[e] << 16), d);
+    d = fmaf(__uint_as_float(hw[e] & 0xFFFF0000u) + __uint_as_float(lw[e] & 0xFFFF0000u), __uint_as_float(bw[e] & 0xFFFF0000u), d);
+  }
+}
 // delta for one output and row from its own adapter alone, where the tile's sum is not finite.
 __device__ __noinline__ float proj_own_delta(const ProjectArgs& A, int64_t place, int t, int n) {
-  const uint4* h = reinterpret_cast<const uint4*>(A.spread + place);
+  const uint4 *h = reinterpret_cast<const uint4*>(A.spread + place), *l = reinterpret_cast<const uint4*>(A.spread + A.low + place);
   const uint4* b = reinterpret_cast<const uint4*>(A.b + (static_cast<int64_t>(A.row_adapter[t]) * A.N + n) * A.R);
   float d = 0.0f;
 #pragma unroll 4
   for (int i = 0; i < A.R / 8; ++i) {
-    const uint4 hv = __ldcg(h + i), bv = b[i];
-    const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w}, bw[4] = {bv.x, bv.y, bv.z, bv.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      d = fmaf(__uint_as_float(hw[e] << 16), __uint_as_float(bw[e] << 16), d);
-      d = fmaf(__uint_as_float(hw[e] & 0xFFFF0000u), __uint_as_float(bw[e] & 0xFFFF0000u), d);
-    }
+    proj_add8(__ldcg(h + i), __ldcg(l + i), b[i], d);
   }
   return d;
 }
@@ -530,23 +550,17 @@ __device__ __forceinline__ void proj_own_deltas(const ProjectArgs& A, int tile, 
   }
 #pragma unroll 1
   for (int r = 0; r < A.R / 8; ++r) {
-    uint4 hv[4], bv[4];
+    uint4 hv[4], lv[4], bv[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (bad >> i & 1u) {
         hv[i] = __ldcg(h[i] + r);
+        lv[i] = __ldcg(h[i] + A.low / 8 + r);
         bv[i] = b[i][r];
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (bad >> i & 1u) {
-        const uint32_t hw[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w}, bw[4] = {bv[i].x, bv[i].y, bv[i].z, bv[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          d[i] = fmaf(__uint_as_float(hw[e] << 16), __uint_as_float(bw[e] << 16), d[i]);
-          d[i] = fmaf(__uint_as_float(hw[e] & 0xFFFF0000u), __uint_as_float(bw[e] & 0xFFFF0000u), d[i]);
-        }
-      }
+      if (bad >> i & 1u) proj_add8(hv[i], lv[i], bv[i], d[i]);
   }
   __syncwarp();
 }
@@ -576,6 +590,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
   constexpr int STAGES = proj_stages(BN), STAGE = proj_stage_bytes(BN);
   constexpr int ELEMS = F8 ? 128 : 64;  // of the sum's length in one stage
   constexpr uint32_t TMEM_COLS = 4 * BN;  // two tiles' base and delta
+  constexpr int GROUP = proj_group(BN);
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   ProjBars<BN>* B = reinterpret_cast<ProjBars<BN>*>(smem + STAGES * STAGE);
@@ -660,6 +675,19 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
       share(stages_of(subs), rank, from, to);
       const int32_t* ids = A.lists + static_cast<int64_t>(t_tile) * (BN + 1) + 1;
       for (int s = from; s < to && room(); ++s, ring.next()) {
+        if ((s - from) % GROUP == 0) {  // the lower parts of the next stages' inner rows
+          const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
+          const int sub0 = s * per_stage, n = min(min(GROUP, to - s) * per_stage, subs - sub0);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(n) * BN * line);
+            for (int i = 0; i < n; ++i) {
+              const int j = (sub0 + i) / blocks, rb = (sub0 + i) % blocks;
+              tma_2d(at + i * BN * line, &mh, rb * A.rank_block, ((A.t_tiles + t_tile) * A.most + j) * BN, bar);
+            }
+          }
+          ring.next();
+          if (!room()) break;
+        }
         const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
         const int sub0 = s * per_stage, n = min(per_stage, subs - sub0);
         if (elect_one()) {
@@ -707,17 +735,27 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         const int subs = adapters_of(t_tile) * blocks;
         share(stages_of(subs), rank, from, to);
         bool add = false;
+        uint32_t low = 0;
         for (int s = from; s < to && landed(); ++s, ring.next()) {
-          const uint32_t at = smem_u32(smem + ring.slot * STAGE);
+          if ((s - from) % GROUP == 0) {
+            low = ring.slot;
+            ring.next();
+            if (!landed()) break;
+          }
+          const uint32_t at = smem_u32(smem + ring.slot * STAGE), at_h = at + PROJ_M * PROJ_LINE;
+          const uint32_t at_low = smem_u32(smem + low * STAGE) + (s - from) % GROUP * per_stage * BN * line;
           const int n = min(per_stage, subs - s * per_stage);
           if (elect_one()) {
             for (int i = 0; i < n; ++i) {
               const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
-              const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * BN * line, line);
-              for (int q = 0; q < A.rank_block / 16; ++q)
+              const uint64_t db = mma_desc(at_h + i * BN * line, line), dl = mma_desc(at_low + i * BN * line, line);
+              for (int q = 0; q < A.rank_block / 16; ++q) {
                 mma<false>(delta, da + 2 * q, db + 2 * q, mma_idesc(false, BN), add || i > 0 || q > 0);
+                mma<false>(delta, da + 2 * q, dl + 2 * q, mma_idesc(false, BN), true);
+              }
             }
             mma_commit(&B->empty[ring.slot]);
+            if ((s - from) % GROUP == GROUP - 1 || s + 1 == to) mma_commit(&B->empty[low]);
           }
           add = true;
         }
@@ -1059,28 +1097,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
   };
   // 256 outputs: M counts in sixteens
   const uint32_t idesc = (mma_idesc(false, rows_max) & 0x00FFFFFFu) | (16u << 24);
-  // a stage of rank blocks: `n` of them from rank block `rb` of the list's adapter j on
-  auto load_blocks = [&](int t_tile, int n0, int j, int rb, int n) {
-    const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
-    if (elect_one()) {
-      if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(2 * n * (PROJ_M + half)) * line);
+  // Rank blocks from rank block 0 of the list's adapter `j` on, `subs` of them: for every two stages of b with the upper parts
+  // of the inner rows, one stage before them with the lower parts.
+  auto load_blocks = [&](int t_tile, int n0, int j, int subs) {
+    auto load_rows = [&](uint32_t at, uint32_t bar, int part, int sub0, int n) {
       for (int i = 0; i < n; ++i) {
-        pair_tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, list_of(t_tile)[1 + j], bar);
-        pair_tma_2d(at + PROJ_M * PROJ_LINE + i * half * line, &mh, rb * A.rank_block,
-                    (t_tile * A.most + j) * rows_max + rank * half, bar);
-        if (++rb == blocks) rb = 0, ++j;
+        const int jj = j + (sub0 + i) / blocks, rb = (sub0 + i) % blocks;
+        pair_tma_2d(at + i * half * line, &mh, rb * A.rank_block, ((part * A.t_tiles + t_tile) * A.most + jj) * rows_max + rank * half, bar);
+      }
+    };
+    for (int s = 0; s * per_stage < subs && alive && room(); ++s, ring.next()) {
+      const int sub0 = s * per_stage, n = min(per_stage, subs - sub0);
+      if (s % 2 == 0) {
+        const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
+        const int both = min(2 * per_stage, subs - sub0);
+        if (elect_one()) {
+          if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(2 * both * half) * line);
+          load_rows(at, bar, 1, sub0, both);
+        }
+        ring.next();
+        if (!room()) break;
+      }
+      const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), bar = dsmem_addr(smem_u32(&B->full[ring.slot]), 0);
+      if (elect_one()) {
+        if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(2 * n * (PROJ_M + half)) * line);
+        for (int i = 0; i < n; ++i)
+          pair_tma_3d(at + i * PROJ_M * line, &mb, (sub0 + i) % blocks * A.rank_block, n0, list_of(t_tile)[1 + j + (sub0 + i) / blocks], bar);
+        load_rows(at + PROJ_M * PROJ_LINE, bar, 0, sub0, n);
       }
     }
   };
-  auto add_blocks = [&](uint32_t sum, int n, bool add) {
-    const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE);
-    if (elect_one()) {
-      for (int i = 0; i < n; ++i) {
-        const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
-        const uint64_t db = mma_desc(at + PROJ_M * PROJ_LINE + i * half * line, line);
-        for (int q = 0; q < A.rank_block / 16; ++q) pair_mma(sum, da + 2 * q, db + 2 * q, idesc, add || i > 0 || q > 0);
+  auto add_blocks = [&](uint32_t sum, int subs, bool add) {
+    uint32_t low = 0;
+    for (int s = 0; s * per_stage < subs && alive && landed(); ++s, ring.next()) {
+      if (s % 2 == 0) {
+        low = ring.slot;
+        ring.next();
+        if (!landed()) break;
       }
-      pair_commit(&B->empty[ring.slot]);
+      const int n = min(per_stage, subs - s * per_stage);
+      const uint32_t at = smem_u32(smem + ring.slot * PAIR_STAGE), at_h = at + PROJ_M * PROJ_LINE;
+      const uint32_t at_low = smem_u32(smem + low * PAIR_STAGE) + s % 2 * per_stage * half * line;
+      if (elect_one()) {
+        for (int i = 0; i < n; ++i) {
+          const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
+          const uint64_t db = mma_desc(at_h + i * half * line, line), dl = mma_desc(at_low + i * half * line, line);
+          for (int q = 0; q < A.rank_block / 16; ++q) {
+            pair_mma(sum, da + 2 * q, db + 2 * q, idesc, add || s > 0 || i > 0 || q > 0);
+            pair_mma(sum, da + 2 * q, dl + 2 * q, idesc, true);
+          }
+        }
+        pair_commit(&B->empty[ring.slot]);
+        if (s % 2 == 1 || (s + 1) * per_stage >= subs) pair_commit(&B->empty[low]);
+      }
     }
   };
   auto load_base = [&](int t0, int n0) {
@@ -1150,9 +1219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
         }
         asm volatile("fence.proxy.async;" ::: "memory");
       }
-      const int subs = (list_of(t_tile)[0] & LIST_COUNT) * blocks;
-      for (int sub0 = 0; sub0 < subs && alive && room(); sub0 += per_stage, ring.next())
-        load_blocks(t_tile, n0, sub0 / blocks, sub0 % blocks, min(per_stage, subs - sub0));
+      load_blocks(t_tile, n0, 0, (list_of(t_tile)[0] & LIST_COUNT) * blocks);
     }
     if (!alive && lead) ring.drain(B->full);
   } else if (warp == 1 && lead) {
@@ -1166,11 +1233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
       }
       tc_fence_after();
       add_base(sum);
-      if (A.S > 0 && q0 < 0) {
-        const int subs = (list_of(place.t_tile)[0] & LIST_COUNT) * blocks;
-        for (int sub0 = 0; sub0 < subs && alive && landed(); sub0 += per_stage, ring.next())
-          add_blocks(sum, min(per_stage, subs - sub0), true);
-      }
+      if (A.S > 0 && q0 < 0) add_blocks(sum, (list_of(place.t_tile)[0] & LIST_COUNT) * blocks, true);
       if (alive && elect_one()) pair_commit(&B->done[buf]);
     }
     if (!alive) freed_all();
@@ -1202,7 +1265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i, h += A.R) {
             const int its = __shfl_sync(0xFFFFFFFFu, of, i);
-            if (some && c0 + i < rows) *h = __float2bfloat16_rn(its == c ? by * v[i] : 0.0f);
+            if (some && c0 + i < rows) proj_split(its == c ? by * v[i] : 0.0f, h[0], h[A.low]);
           }
         }
         tc_fence_before();
@@ -1291,8 +1354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
           for (int own = -1; own < count && alive; own = next_broken(own))
             for (int j = max(own, 0); j < (own < 0 ? count : own + 1); ++j) {
               if (own < 0 && is_broken(j)) continue;
-              for (int rb = 0; rb < blocks && alive && room(); rb += per_stage, ring.next())
-                load_blocks(t_tile, n0, j, rb, min(per_stage, blocks - rb));
+              load_blocks(t_tile, n0, j, blocks);
             }
         } else if (warp == 1 && lead) {
           uint32_t in_tile = 0;
@@ -1307,10 +1369,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
             bool add = false;
             for (int j = max(own, 0); j < (own < 0 ? count : own + 1); ++j) {
               if (own < 0 && is_broken(j)) continue;
-              for (int rb = 0; rb < blocks && alive && landed(); rb += per_stage, ring.next()) {
-                add_blocks(delta, min(per_stage, blocks - rb), add);
-                add = true;
-              }
+              add_blocks(delta, blocks, add);
+              add = true;
             }
             if (alive && elect_one()) pair_commit(&B->done[0]);
           }

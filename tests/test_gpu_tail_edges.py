@@ -149,6 +149,32 @@ def test_project_broken_requests_stay_alone_and_cost_little(G, T, N, K, S, R, sp
     assert torch.equal(got[keep][:, 51:], y[keep][:, 51:]) and got[keep].isfinite().all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f8"])
+@pytest.mark.parametrize("T,N", [(1, 1000), (20, 4000), (64, 300), (100, 30000), (300, 700), (2049, 4096)])
+def test_project_inner_rows_keep_their_bits(G, kind, T, N):
+    """Adapters whose two halves nearly cancel: what is left of the output shows the rounding of the inner rows, which is
+    2^-16 at most (two bfloat16 of 2^-8 each), next to 32-bit sums of K and of R products."""
+    from test_gpu_tail import HALF, U, project_case
+    K, S, R = 64, 3, 32
+    s = project_case(T, N, K, S, R, kind, T + N)
+    s["w"].zero_()
+    a, b = s["a"], s["b"]
+    a[:, R // 2:] = a[:, :R // 2]
+    a[:, R // 2:, ::16] *= 1.0625
+    b[:, :, R // 2:] = -b[:, :, :R // 2]
+    y = G.project_rows(**s).double()
+    x = s["x"].double() * (1 if s["x_scale"] is None else s["x_scale"].double()[:, None])
+    want, off = torch.zeros_like(y), torch.zeros_like(y)
+    for c in range(S):
+        rows = (s["row_adapter"] == c).nonzero().flatten()
+        ad, bd, g = a[c].double(), b[c].double(), s["adapter_scale"][c].double()
+        h, hb = g * (x[rows] @ ad.T), g * (x[rows].abs() @ ad.abs().T)
+        want[rows] = h @ bd.T
+        off[rows] = (2.0 ** -16 * h.abs() + (K + 4) * U * hb) @ bd.abs().T + (R + 4) * U * (h.abs() @ bd.abs().T)
+    assert ((y - want).abs() <= off + (want.abs() + off) * HALF).all()
+    assert (want.abs() > 4 * off).double().mean() > 0.5 or T < 5
+
+
 # ------------------------------------------------------------------------------ beside the sampler
 def _projection(V, H=2048, T=8):
     g = torch.Generator(device="cuda").manual_seed(V)
