@@ -208,9 +208,10 @@ TAIL_CALL(project) {
       }
     }
   }
-  // rows start on 16 bytes, as draw_rows and the sampler want them
-  Tensor y = y_given != nullptr ? *y_given : fresh({T, (N + 7) / 8 * 8}, at::kBFloat16, x);
-  if (y_given == nullptr && N % 8 != 0) y = y.narrow(1, 0, N);
+  // rows start on 16 bytes, as draw_rows and the sampler want them (narrow() would take a microsecond and more)
+  const int64_t ld = (N + 7) / 8 * 8;
+  const Tensor y = y_given != nullptr ? *y_given : fresh({T, ld}, at::kBFloat16, x);
+  if (y_given == nullptr && ld != N) y.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef({T, N}), at::IntArrayRef({ld, int64_t{1}}));
   const Rows ry = rows(&y, "y", T, N, at::kBFloat16, device);
   void* stream = stream_of(a[11], device);
   const int t32 = narrow(T, "T"), n32 = narrow(N, "N"), k32 = narrow(K, "K"), s32 = narrow(S, "S"), r32 = narrow(R, "R");
