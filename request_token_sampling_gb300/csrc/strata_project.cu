@@ -233,7 +233,9 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   A.lists = static_cast<int32_t*>(workspace);
   A.ready = static_cast<uint32_t*>(workspace) + static_cast<int64_t>(t_tiles) * (bn + 1);
   A.spread = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + lists_bytes(t_tiles, bn));
-  A.low = static_cast<int64_t>(t_tiles) * most * bn * R;
+  const bool beside = pair == 0 && strata::parts_beside(bn);
+  A.low = beside ? static_cast<int64_t>(bn) * R : static_cast<int64_t>(t_tiles) * most * bn * R;
+  A.block_rows = beside ? 2 * bn : bn;
   A.errors = dev.errors;
   A.ldx = ldx;
   A.ldy = ldy;
@@ -269,7 +271,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(A.rank_block), strata::PROJ_M, 1};
     if (!encode(dev.encode, &mb, false, 3, b, dims, strides, box, A.rank_block * 2)) return host_fail(STRATA_EINVAL, "b cannot be mapped");
     const cuuint64_t hdims[2] = {r, 2 * static_cast<cuuint64_t>(t_tiles) * most * bn};
-    const cuuint32_t hbox[2] = {static_cast<cuuint32_t>(A.rank_block), static_cast<cuuint32_t>(pair > 0 ? bn / 2 : bn)};
+    const cuuint32_t hbox[2] = {static_cast<cuuint32_t>(A.rank_block), static_cast<cuuint32_t>(pair > 0 ? bn / 2 : A.block_rows)};
     if (!encode(dev.encode, &mh, false, 2, A.spread, hdims, strides, hbox, A.rank_block * 2))
       return host_fail(STRATA_EINVAL, "the workspace cannot be mapped");
     if (T > SHRINK_ROWS) {

@@ -35,8 +35,9 @@ struct ProjectArgs {
   const __nv_bfloat16 *a, *b;
   const int32_t* row_adapter;
   __nv_bfloat16* y;
-  __nv_bfloat16* spread;  // [upper, lower part][tiles][most][tile rows][R]
-  int64_t low;            // the lower parts' distance from the upper ones: tiles x most x tile rows x R
+  __nv_bfloat16* spread;  // [tiles][most][upper, lower part][tile rows][R], or the parts outermost (parts_beside())
+  int64_t low;            // the lower parts' distance from the upper ones
+  int block_rows;         // of one adapter of a tile: its rows, twice where the parts are beside one another
   int32_t* lists;         // per tile: how many adapters, then their ids in ascending order ([1 + tile rows])
   uint32_t* ready;        // per tile: warps that have written their part of its inner rows (pair_kernel)
   uint32_t* errors;
@@ -52,9 +53,12 @@ constexpr int PROJ_LINE = 128;     // bytes of a row that one stage holds (64 bf
 constexpr int PROJ_THREADS = 192;  // warp 0 loads, warp 1 issues the products, warps 2-5 write the tile
 constexpr uint32_t PROJ_SPINS = 1u << 24;
 
-__host__ __device__ constexpr int proj_stage_bytes(int bn) { return (PROJ_M + bn) * PROJ_LINE; }
-__host__ __device__ constexpr int proj_stages(int bn) { return bn <= 16 ? 12 : bn <= 32 ? 11 : bn <= 64 ? 9 : 7; }
-// Stages of adapters whose inner rows' lower parts share one stage before them: as many as have room there.
+// Both parts of up to 64 inner rows are one operand of twice the rows, for the same products' price; 128 would not fit tensor
+// memory so, nor would the stages be many.
+__host__ __device__ constexpr bool parts_beside(int bn) { return bn <= 64; }
+__host__ __device__ constexpr int proj_stage_bytes(int bn) { return (PROJ_M + (parts_beside(bn) ? 2 : 1) * bn) * PROJ_LINE; }
+__host__ __device__ constexpr int proj_stages(int bn) { return bn <= 16 ? 11 : bn <= 32 ? 9 : 7; }
+// Else: stages of adapters whose inner rows' lower parts share one stage before them, as many as have room there.
 __host__ __device__ constexpr int proj_group(int bn) { return proj_stage_bytes(bn) / (bn * PROJ_LINE); }
 __host__ __device__ constexpr int proj_smem(int bn) { return proj_stages(bn) * proj_stage_bytes(bn) + 1024 + 512; }
 
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A, int tile_row
   proj_split(s, hi, lo);
   const __nv_bfloat16 zero = __float2bfloat16_rn(0.0f);
   for (int j = lane; j < count; j += 32) {
-    __nv_bfloat16* h = A.spread + ((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - t0)) * A.R + r;
+    __nv_bfloat16* h = A.spread + ((static_cast<int64_t>(tile) * A.most + j) * A.block_rows + (t - t0)) * A.R + r;
     h[0] = j == at ? hi : zero;
     h[A.low] = j == at ? lo : zero;
   }
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
       if (q < stack) {
         const int c = adapter(j);
         const float by = A.adapter_scale[c];
-        __nv_bfloat16* to_row = A.spread + (static_cast<int64_t>(tile) * A.most + j) * rows_max * A.R + q % A.R;
+        __nv_bfloat16* to_row = A.spread + (static_cast<int64_t>(tile) * A.most + j) * A.block_rows * A.R + q % A.R;
         for (int t = id / FOURS; t < rows; t += GO) {
           __align__(8) __nv_bfloat16 hi[4], lo[4];
           *reinterpret_cast<uint2*>(hi) = *reinterpret_cast<uint2*>(lo) = make_uint2(0, 0);
@@ -508,7 +512,7 @@ __device__ __forceinline__ int64_t proj_place(const ProjectArgs& A, int tile, in
     else
       to = at;
   }
-  return ((static_cast<int64_t>(tile) * A.most + j) * tile_rows + (t - tile * tile_rows)) * A.R;
+  return ((static_cast<int64_t>(tile) * A.most + j) * A.block_rows + (t - tile * tile_rows)) * A.R;
 }
 // d + sum of eight (h + l) b
 __device__ __forceinline__ void proj_add8(const uint4& h, const uint4& l, const uint4& b, float& d) {
@@ -589,8 +593,11 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
                    const __grid_constant__ ProjectArgs A) {
   constexpr int STAGES = proj_stages(BN), STAGE = proj_stage_bytes(BN);
   constexpr int ELEMS = F8 ? 128 : 64;  // of the sum's length in one stage
-  constexpr uint32_t TMEM_COLS = 4 * BN;  // two tiles' base and delta
-  constexpr int GROUP = proj_group(BN);
+  constexpr bool BESIDE = parts_beside(BN);
+  constexpr int H_ROWS = BESIDE ? 2 * BN : BN, GROUP = proj_group(BN);
+  constexpr uint32_t BUF_COLS = BN + H_ROWS;  // a tile's base and delta; there are two
+  constexpr uint32_t TMEM_COLS = BN == 16 ? 128 : BN == 32 ? 256 : 512;
+  static_assert(2 * BUF_COLS <= TMEM_COLS, "two tiles in tensor memory");
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   ProjBars<BN>* B = reinterpret_cast<ProjBars<BN>*>(smem + STAGES * STAGE);
@@ -664,7 +671,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
       for (int s = from; s < to && room(); ++s, ring.next()) {
         const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
         if (elect_one()) {
-          mbar_arrive_expect_tx(&B->full[ring.slot], STAGE);
+          mbar_arrive_expect_tx(&B->full[ring.slot], (PROJ_M + BN) * PROJ_LINE);
           tma_2d(at, &mw, s * ELEMS, n0, bar);
           tma_2d(at + PROJ_M * PROJ_LINE, &mx, s * ELEMS, t_tile * BN, bar);
         }
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
       share(stages_of(subs), rank, from, to);
       const int32_t* ids = A.lists + static_cast<int64_t>(t_tile) * (BN + 1) + 1;
       for (int s = from; s < to && room(); ++s, ring.next()) {
-        if ((s - from) % GROUP == 0) {  // the lower parts of the next stages' inner rows
+        if (!BESIDE && (s - from) % GROUP == 0) {  // the lower parts of the next stages' inner rows
           const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
           const int sub0 = s * per_stage, n = min(min(GROUP, to - s) * per_stage, subs - sub0);
           if (elect_one()) {
@@ -691,11 +698,11 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         const uint32_t at = smem_u32(smem + ring.slot * STAGE), bar = smem_u32(&B->full[ring.slot]);
         const int sub0 = s * per_stage, n = min(per_stage, subs - sub0);
         if (elect_one()) {
-          mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(n) * (PROJ_M + BN) * line);
+          mbar_arrive_expect_tx(&B->full[ring.slot], static_cast<uint32_t>(n) * (PROJ_M + H_ROWS) * line);
           for (int i = 0; i < n; ++i) {
             const int j = (sub0 + i) / blocks, rb = (sub0 + i) % blocks;
             tma_3d(at + i * PROJ_M * line, &mb, rb * A.rank_block, n0, ids[j], bar);
-            tma_2d(at + PROJ_M * PROJ_LINE + i * BN * line, &mh, rb * A.rank_block, (t_tile * A.most + j) * BN, bar);
+            tma_2d(at + PROJ_M * PROJ_LINE + i * H_ROWS * line, &mh, rb * A.rank_block, (t_tile * A.most + j) * H_ROWS, bar);
           }
         }
       }
@@ -712,7 +719,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
     };
     for (int tile = first; tile < tiles && alive; tile += step, ++turn) {
       const int t_tile = tile % A.t_tiles;
-      const uint32_t buf = turn & 1, base = tmem + buf * 2 * BN, delta = base + BN;
+      const uint32_t buf = turn & 1, base = tmem + buf * BUF_COLS, delta = base + BN;
       if (turn >= 2 && !proj_wait(&B->freed[buf], (turn / 2 + 1) & 1, dead, A.errors, bit)) {
         alive = false;
         break;
@@ -737,7 +744,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         bool add = false;
         uint32_t low = 0;
         for (int s = from; s < to && landed(); ++s, ring.next()) {
-          if ((s - from) % GROUP == 0) {
+          if (!BESIDE && (s - from) % GROUP == 0) {
             low = ring.slot;
             ring.next();
             if (!landed()) break;
@@ -748,14 +755,14 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
           if (elect_one()) {
             for (int i = 0; i < n; ++i) {
               const uint64_t da = mma_desc(at + i * PROJ_M * line, line);
-              const uint64_t db = mma_desc(at_h + i * BN * line, line), dl = mma_desc(at_low + i * BN * line, line);
+              const uint64_t db = mma_desc(at_h + i * H_ROWS * line, line), dl = mma_desc(at_low + i * BN * line, line);
               for (int q = 0; q < A.rank_block / 16; ++q) {
-                mma<false>(delta, da + 2 * q, db + 2 * q, mma_idesc(false, BN), add || i > 0 || q > 0);
-                mma<false>(delta, da + 2 * q, dl + 2 * q, mma_idesc(false, BN), true);
+                mma<false>(delta, da + 2 * q, db + 2 * q, mma_idesc(false, H_ROWS), add || i > 0 || q > 0);
+                if constexpr (!BESIDE) mma<false>(delta, da + 2 * q, dl + 2 * q, mma_idesc(false, BN), true);
               }
             }
             mma_commit(&B->empty[ring.slot]);
-            if ((s - from) % GROUP == GROUP - 1 || s + 1 == to) mma_commit(&B->empty[low]);
+            if (!BESIDE && ((s - from) % GROUP == GROUP - 1 || s + 1 == to)) mma_commit(&B->empty[low]);
           }
           add = true;
         }
@@ -778,7 +785,18 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
       const bool ok = proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t base = tmem + buf * 2 * BN + (quarter << 21);
+      const uint32_t base = tmem + buf * BUF_COLS + (quarter << 21);
+      // a delta's columns, both parts
+      auto load_delta = [&](int c, float(&v)[16]) {
+        tmem_ld16(base + BN + c, v);
+        if constexpr (BESIDE) {
+          float low[16];
+          tmem_ld16(base + 2 * BN + c, low);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += low[i];
+        }
+      };
       const int rows = min(BN, A.T - t0);
       if constexpr (!SPLIT) {
         // few instructions an output: a warp writes its 32 outputs of all rows while the next tile is summed, and
@@ -789,7 +807,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         for (int c = 0; c < rows; c += 16) {
           float vb[16], vd[16] = {};
           tmem_ld16(base + c, vb);
-          if (adapters > 0) tmem_ld16(base + BN + c, vd);
+          if (adapters > 0) load_delta(c, vd);
           const float scale = F8 && lane < 16 && c + lane < rows ? A.x_scale[t0 + c + lane] : 0.0f;  // of row c + lane
           tmem_wait_ld();
           if (adapters > 0) {
@@ -832,7 +850,7 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
         for (int c = 0; c < rows; c += 16) {
           float vb[16] = {}, vd[16] = {};
           if (has_base) tmem_ld16(base + c, vb);
-          if (has_delta) tmem_ld16(base + BN + c, vd);
+          if (has_delta) load_delta(c, vd);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
