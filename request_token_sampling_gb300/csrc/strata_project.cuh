@@ -1292,15 +1292,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROJ_THREADS, 1)
           tmem_ld32(sum + c0, v);
           tmem_wait_ld();
           const int q = q0 + lane_at;
-          __nv_bfloat16* h = A.spread + ((static_cast<int64_t>(t_tile) * A.most + q / A.R) * rows_max + c0) * A.R + q % A.R;
-          const bool some = q < stack;
+          // two rows at a time: of both lanes of a pair the even one stores the first row, four bytes, and the odd one the second
+          const int odd = lane & 1;
+          __nv_bfloat16* h = A.spread + ((static_cast<int64_t>(t_tile) * A.most + q / A.R) * rows_max + c0 + odd) * A.R + (q - odd) % A.R;
+          const int upto = q < stack ? rows - c0 - odd : 0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            __nv_bfloat16 hi, lo;
-            proj_split(mine >> i & 1u ? by * v[i] : 0.0f, hi, lo);
-            if (some && c0 + i < rows) {
-              h[i * A.R] = hi;
-              h[i * A.R + A.low] = lo;
+          for (int i = 0; i < 32; i += 2) {
+            __nv_bfloat162 hi, lo;
+            proj_split(mine >> i & 1u ? by * v[i] : 0.0f, hi.x, lo.x);
+            proj_split(mine >> (i + 1) & 1u ? by * v[i + 1] : 0.0f, hi.y, lo.y);
+            const uint32_t hw = *reinterpret_cast<const uint32_t*>(&hi), lw = *reinterpret_cast<const uint32_t*>(&lo);
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, __byte_perm(hw, lw, odd ? 0x5410 : 0x7632), 1);
+            if (i < upto) {
+              *reinterpret_cast<uint32_t*>(h + i * A.R) = __byte_perm(hw, other, odd ? 0x3254 : 0x5410);
+              *reinterpret_cast<uint32_t*>(h + i * A.R + A.low) = __byte_perm(lw, other, odd ? 0x3276 : 0x7610);
             }
           }
         }
