@@ -96,7 +96,8 @@ int strata_draw_rows(const void* logits, int dtype, int B, int V, int64_t ld, co
 /*
  * Bits that the kernels of the calls above raised on the current device since the last call, read
  * after the stream's work so far (this call waits for it) and cleared in one step: STRATA_DEVERR_TIMEOUT,
- * a bounded wait inside a kernel ran out and the call's output is not valid.  The bits are those of all
+ * a bounded wait inside a kernel ran out and the call's output is not valid (a draw gives each such row id
+ * -1 and NaN).  The bits are those of all
  * streams: each is told to one caller.
  */
 int strata_tail_errors(uint32_t* bits, void* stream);

@@ -66,6 +66,7 @@ constexpr int DRAW_PIECES = 4;          // parts a block's ids arrive in
 constexpr int DRAW_MAX_CLUSTER = 16;
 constexpr float DRAW_REACH = 0.75f;     // below the smallest maximum, of its distance to their mean
 constexpr uint32_t NO_KEY = 0u;         // NaN and -inf: below every key that can be chosen
+constexpr uint32_t DRAW_DEAD = 0xFFFFFFFFu;  // above every logit's key: a wait for a part of the row ran out
 constexpr uint32_t DRAW_SPINS = 1u << 24;
 
 // Order-preserving key; -0.0 and +0.0 share one.  -inf maps to 0x007FFFFF, NaN is taken out first.
@@ -694,7 +695,8 @@ __device__ __forceinline__ int row_in_order(const DrawArgs& A, int at, uint32_t*
   return row;
 }
 
-template <typename E>
+// SPINS: looks at a copy before it counts as lost.  A row that lost one gets id -1 and NaN, once its copies are over.
+template <typename E, uint32_t SPINS = DRAW_SPINS>
 __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_constant__ DrawArgs A) {
   extern __shared__ __align__(16) uint8_t raw[];
   DrawShared* sh = reinterpret_cast<DrawShared*>(raw);
@@ -756,21 +758,23 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
       most_in = v;
     }
   };
-  for (int p = 0; p < DRAW_PIECES; ++p) {
+  bool lost = false;
+  for (int p = 0; p < DRAW_PIECES && !lost; ++p) {
     const int v0 = min(whole, p * piece), v1 = min(whole, v0 + piece);
     if (v1 > v0) {
       uint32_t spin = 0;
-      while (!mbar_try_wait(&sh->bars[p], 0))
-        if (++spin >= DRAW_SPINS) {
-          atomicOr(A.errors, 0x08u);  // STRATA_DEVERR_TIMEOUT
-          break;
-        }
+      while (spin < SPINS && !mbar_try_wait(&sh->bars[p], 0)) ++spin;
+      lost = spin >= SPINS;
+      if (lost) {
+        atomicOr(A.errors, 0x08u);  // STRATA_DEVERR_TIMEOUT
+        break;
+      }
       for (int v = v0 + threadIdx.x; v < v1; v += DRAW_THREADS) look(v);
     }
   }
   if (threadIdx.x == 0 && whole < R.vecs) look(whole);
   // The largest of four threads to all blocks: to each block by 32 threads, four to a store.  Or each thread's own.
-  const uint32_t own_key = draw_key(most);
+  const uint32_t own_key = lost ? DRAW_DEAD : draw_key(most);
   const bool fine = R.ranks <= 2;
   const int row_maxima = static_cast<int>(R.ranks) * (fine ? DRAW_THREADS : DRAW_MAXIMA);
   if (!fine) {
@@ -811,8 +815,14 @@ __global__ void __launch_bounds__(DRAW_THREADS, 2) draw_kernel(const __grid_cons
   const float least = !(m <= 0.0f) ? top + logf(m) : -INFINITY;  // min_p's threshold
   const bool k_on = k > 0 && k < A.V, p_on = !(P >= 1.0f);
   const u64 p24 = P > 0.0f ? static_cast<u64>(fminf(P, 1.0f) * 0x1p24f) : 0ull;
-  if (top_key == NO_KEY) {
+  if (top_key == NO_KEY || top_key == DRAW_DEAD) {
     if (lead && threadIdx.x == 0) answer(-1, __int_as_float(0x7FC00000));
+    if (top_key == DRAW_DEAD) {  // no copy of a block may be in flight when it ends
+      uint32_t spin = 0;
+      for (int p = 0; p < DRAW_PIECES; ++p)
+        if (min(whole, (p + 1) * piece) > min(whole, p * piece))
+          while (spin < DRAW_SPINS && !mbar_try_wait(&sh->bars[p], 0)) ++spin;
+    }
     return;
   }
   if (!(T > 0.0f) || (!(m <= 0.0f) && !(top >= least)) || (p_on && p24 == 0)) {  // the first in order

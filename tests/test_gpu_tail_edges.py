@@ -272,16 +272,18 @@ def test_operators_in_a_row_after_own_outputs_on_two_streams(G):
 
 
 # ------------------------------------------------------------------------------ error bits
-def test_no_error_bit_is_lost(G, tmp_path):
-    """A program that raises bits on one stream and asks for them on another."""
+@pytest.mark.parametrize("name", ["errors_check", "draw_wait_check"])
+def test_errors_are_told(G, tmp_path, name):
+    """Programs with the library's source: bits raised on one stream and asked for on another, none is lost; draws whose waits
+    run out."""
     import os
     import shutil
     import subprocess
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
-    exe = str(tmp_path / "errors_check")
+    exe = str(tmp_path / name)
     r = subprocess.run([nvcc, "-O1", "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-I", os.path.join(root, "include"),
-                        "-o", exe, os.path.join(root, "tests", "errors_check.cu")], capture_output=True, text=True, timeout=600)
+                        "-o", exe, os.path.join(root, "tests", name + ".cu")], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr[-2000:]
     r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout[-500:]
