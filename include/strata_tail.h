@@ -65,7 +65,8 @@ int strata_norm_rows(const void* x, int64_t ldx, const void* residual, int64_t l
  * x, w, a and b start on 16 bytes, and K and the strides ldx and ldw are multiples of 16 bytes; R is
  * a multiple of 16 (pad smaller ranks with zeros).  ldy >= N is any stride, y any bfloat16 address.
  * `workspace`: strata_project_workspace(T, S, R) bytes on 256 bytes of alignment, free to be reused
- * when the stream has passed the call.
+ * when the stream has passed the call.  It grows with rows times adapters up to 256 MB (or what 2,048
+ * rows take); larger calls go through their rows in slabs.
  */
 int64_t strata_project_workspace(int T, int S, int R);
 int strata_project_rows(const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,

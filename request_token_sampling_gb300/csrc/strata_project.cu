@@ -168,56 +168,39 @@ int strata::tail_device(int* device, uint32_t** errors, int* sms) {
   return STRATA_OK;
 }
 
-extern "C" int64_t strata_project_workspace(int T, int S, int R) {
-  if (T <= 0 || S <= 0 || R <= 0) return 0;
-  if (T <= 128) return lists_bytes(1, 128) + static_cast<int64_t>(std::min(S, 128)) * 128 * R * 4;
-  // whatever tiles the call takes: 64 to 256 rows each
-  return lists_bytes(static_cast<int>((static_cast<int64_t>(T) + 63) / 64), 256) + (static_cast<int64_t>(T) + 256) * std::min(S, 256) * R * 4;
+namespace {
+
+// The inner rows are spread out over a tile's adapters, so the workspace grows with rows times adapters.  Calls that
+// would take more than 256 MB go through their rows in slabs that use it one after another, of 2,048 rows at least (a layer of
+// 4,096 outputs keeps the GPU busy for two waves).
+int slab_rows(int S, int R) {
+  const int64_t rows = (int64_t{256} << 20) / (static_cast<int64_t>(std::min(S, 256)) * R * 4) / 256 * 256;
+  return static_cast<int>(std::min<int64_t>(MAX_ROWS, std::max<int64_t>(2048, rows)));
 }
 
-extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
-                                   const float* w_scale, int dtype, int T, int N, int K, const void* a, const void* b,
-                                   int S, int R, const int32_t* row_adapter, const float* adapter_scale, void* y,
-                                   int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream) {
-  if (dtype != STRATA_DTYPE_BF16 && dtype != STRATA_DTYPE_F8) return host_fail(STRATA_EINVAL, "dtype %d", dtype);
-  if (T < 0 || N < 1) return host_fail(STRATA_EINVAL, "T=%d N=%d", T, N);
-  if (T > MAX_ROWS) return host_fail(STRATA_ERANGE, "T=%d above %d", T, MAX_ROWS);
-  if (N > MAX_OUTPUTS) return host_fail(STRATA_ERANGE, "N=%d above %d", N, MAX_OUTPUTS);
-  if (K < 1 || K > STRATA_TAIL_MAX_WIDTH) return host_fail(STRATA_ERANGE, "K=%d outside 1..%d", K, STRATA_TAIL_MAX_WIDTH);
-  if (S < 0 || S > STRATA_TAIL_MAX_ADAPTERS) return host_fail(STRATA_ERANGE, "S=%d outside 0..%d", S, STRATA_TAIL_MAX_ADAPTERS);
-  if (S > 0 && (R < 16 || R > STRATA_TAIL_MAX_RANK || R % 16 != 0))
-    return host_fail(STRATA_ERANGE, "R=%d is not a multiple of 16 up to %d", R, STRATA_TAIL_MAX_RANK);
-  if (ldx < K || ldw < K || ldy < N) return host_fail(STRATA_EINVAL, "a row stride below its row");
-  const bool f8 = dtype == STRATA_DTYPE_F8;
-  if ((x_scale != nullptr) != f8 || (w_scale != nullptr) != f8)
-    return host_fail(STRATA_EINVAL, "x_scale and w_scale go with 8-bit rows, and only with them");
-  if (T == 0) return STRATA_OK;
-  if (x == nullptr || w == nullptr || y == nullptr) return host_fail(STRATA_EINVAL, "null x, w or y");
-  if (S > 0 && (a == nullptr || b == nullptr || row_adapter == nullptr || adapter_scale == nullptr))
-    return host_fail(STRATA_EINVAL, "null a, b, row_adapter or adapter_scale");
-  const int64_t esz = f8 ? 1 : 2;
-  if (misaligned(x, 16) || misaligned(w, 16) || (S > 0 && (misaligned(a, 16) || misaligned(b, 16))))
-    return host_fail(STRATA_EALIGN, "x, w, a or b not 16-byte aligned");
-  if (K * esz % 16 != 0 || ldx * esz % 16 != 0 || ldw * esz % 16 != 0 || (S > 0 && K % 8 != 0))
-    return host_fail(STRATA_EALIGN, "K or a row stride is not a multiple of 16 bytes");
-  if (misaligned(y, 2) || misaligned(x_scale, 4) || misaligned(w_scale, 4) || misaligned(row_adapter, 4) ||
-      misaligned(adapter_scale, 4))
-    return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
-  const int64_t need = strata_project_workspace(T, S, R);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
-    return host_fail(STRATA_EINVAL, "the workspace needs %lld bytes on 256 bytes of alignment", static_cast<long long>(need));
-  const Device* found = nullptr;
-  int device = 0;
-  if (const int rc = current_device(&found, &device, true); rc != STRATA_OK) return rc;
-  const Device& dev = *found;
+}  // namespace
 
+extern "C" int64_t strata_project_workspace(int T, int S, int R) {
+  if (T <= 0 || S <= 0 || R <= 0) return 0;
+  if (T <= 128) return lists_bytes(1, 128) + static_cast<int64_t>(std::min(S, T)) * tile_rows(T) * R * 4;
+  // whatever tiles the call takes: 64 to 256 rows each
+  const int rows = std::min(T, slab_rows(S, R));
+  return lists_bytes((rows + 63) / 64, 256) + (static_cast<int64_t>(rows) + 256) * std::min(S, 256) * R * 4;
+}
+
+// One slab of rows, its arguments checked.
+static int project_slab(const Device& dev, int device, const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
+                        const float* w_scale, bool f8, int T, int N, int K, const void* a, const void* b, int S, int R,
+                        const int32_t* row_adapter, const float* adapter_scale, __nv_bfloat16* y, int64_t ldy, void* workspace,
+                        void* stream) {
+  const int64_t esz = f8 ? 1 : 2;
   const cuuint32_t elems = f8 ? 128 : 64;
   const int k_stages = (K + static_cast<int>(elems) - 1) / static_cast<int>(elems);
   const int pair = T > 128 && !f8 ? pair_rows(T, N, k_stages, S > 0, dev.sms) : 0;  // tiles of two SMs
   const int bn = pair > 0 ? pair : tile_rows(T), t_tiles = (T + bn - 1) / bn;
   const int n_tiles = pair > 0 ? (N + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M) : (N + strata::PROJ_M - 1) / strata::PROJ_M;
   const int64_t tiles = static_cast<int64_t>(t_tiles) * n_tiles;
-  const int most = std::min(S, bn);
+  const int most = std::min(S, std::min(T, bn));
   // tiles of inner products before the pairs' others
   const int64_t units = pair > 0 && S > 0 ? static_cast<int64_t>(t_tiles) * ((most * R + 2 * strata::PROJ_M - 1) / (2 * strata::PROJ_M)) : 0;
   if (tiles + units > INT32_MAX - dev.sms) return host_fail(STRATA_ERANGE, "T=%d N=%d", T, N);  // they are counted in steps of the grid
@@ -229,7 +212,7 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
   A.a = static_cast<const __nv_bfloat16*>(a);
   A.b = static_cast<const __nv_bfloat16*>(b);
   A.row_adapter = row_adapter;
-  A.y = static_cast<__nv_bfloat16*>(y);
+  A.y = y;
   A.lists = static_cast<int32_t*>(workspace);
   A.ready = static_cast<uint32_t*>(workspace) + static_cast<int64_t>(t_tiles) * (bn + 1);
   A.spread = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(workspace) + lists_bytes(t_tiles, bn));
@@ -320,6 +303,50 @@ extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_sc
     return first == cudaSuccess ? launch_products(true) : first;
   });
   return e == cudaSuccess ? STRATA_OK : cuda_fail(e, "strata_project_rows");
+}
+
+extern "C" int strata_project_rows(const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
+                                   const float* w_scale, int dtype, int T, int N, int K, const void* a, const void* b,
+                                   int S, int R, const int32_t* row_adapter, const float* adapter_scale, void* y,
+                                   int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (dtype != STRATA_DTYPE_BF16 && dtype != STRATA_DTYPE_F8) return host_fail(STRATA_EINVAL, "dtype %d", dtype);
+  if (T < 0 || N < 1) return host_fail(STRATA_EINVAL, "T=%d N=%d", T, N);
+  if (T > MAX_ROWS) return host_fail(STRATA_ERANGE, "T=%d above %d", T, MAX_ROWS);
+  if (N > MAX_OUTPUTS) return host_fail(STRATA_ERANGE, "N=%d above %d", N, MAX_OUTPUTS);
+  if (K < 1 || K > STRATA_TAIL_MAX_WIDTH) return host_fail(STRATA_ERANGE, "K=%d outside 1..%d", K, STRATA_TAIL_MAX_WIDTH);
+  if (S < 0 || S > STRATA_TAIL_MAX_ADAPTERS) return host_fail(STRATA_ERANGE, "S=%d outside 0..%d", S, STRATA_TAIL_MAX_ADAPTERS);
+  if (S > 0 && (R < 16 || R > STRATA_TAIL_MAX_RANK || R % 16 != 0))
+    return host_fail(STRATA_ERANGE, "R=%d is not a multiple of 16 up to %d", R, STRATA_TAIL_MAX_RANK);
+  if (ldx < K || ldw < K || ldy < N) return host_fail(STRATA_EINVAL, "a row stride below its row");
+  const bool f8 = dtype == STRATA_DTYPE_F8;
+  if ((x_scale != nullptr) != f8 || (w_scale != nullptr) != f8)
+    return host_fail(STRATA_EINVAL, "x_scale and w_scale go with 8-bit rows, and only with them");
+  if (T == 0) return STRATA_OK;
+  if (x == nullptr || w == nullptr || y == nullptr) return host_fail(STRATA_EINVAL, "null x, w or y");
+  if (S > 0 && (a == nullptr || b == nullptr || row_adapter == nullptr || adapter_scale == nullptr))
+    return host_fail(STRATA_EINVAL, "null a, b, row_adapter or adapter_scale");
+  const int64_t esz = f8 ? 1 : 2;
+  if (misaligned(x, 16) || misaligned(w, 16) || (S > 0 && (misaligned(a, 16) || misaligned(b, 16))))
+    return host_fail(STRATA_EALIGN, "x, w, a or b not 16-byte aligned");
+  if (K * esz % 16 != 0 || ldx * esz % 16 != 0 || ldw * esz % 16 != 0 || (S > 0 && K % 8 != 0))
+    return host_fail(STRATA_EALIGN, "K or a row stride is not a multiple of 16 bytes");
+  if (misaligned(y, 2) || misaligned(x_scale, 4) || misaligned(w_scale, 4) || misaligned(row_adapter, 4) ||
+      misaligned(adapter_scale, 4))
+    return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
+  const int64_t need = strata_project_workspace(T, S, R);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
+    return host_fail(STRATA_EINVAL, "the workspace needs %lld bytes on 256 bytes of alignment", static_cast<long long>(need));
+  const Device* found = nullptr;
+  int device = 0;
+  if (const int rc = current_device(&found, &device, true); rc != STRATA_OK) return rc;
+  const int slab = S > 0 ? slab_rows(S, R) : T;
+  for (int t = 0; t < T; t += slab) {
+    const int rc = project_slab(*found, device, static_cast<const char*>(x) + t * ldx * esz, ldx, f8 ? x_scale + t : nullptr, w, ldw, w_scale, f8,
+                                std::min(slab, T - t), N, K, a, b, S, R, S > 0 ? row_adapter + t : nullptr, adapter_scale,
+                                static_cast<__nv_bfloat16*>(y) + t * ldy, ldy, workspace, stream);
+    if (rc != STRATA_OK) return rc;
+  }
+  return STRATA_OK;
 }
 
 // The bits and their clearing in one step, which no kernel of another stream comes between.  A call has a word of its

@@ -175,6 +175,36 @@ def test_project_inner_rows_keep_their_bits(G, kind, T, N):
     assert (want.abs() > 4 * off).double().mean() > 0.5 or T < 5
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f8"])
+@pytest.mark.parametrize("T,S,R", [(4099, 256, 64), (4500, 300, 128), (9001, 128, 64)])
+def test_project_rows_in_slabs(G, kind, T, S, R):
+    """More rows times adapters than the workspace takes at once: each slab is the call of its own rows."""
+    from test_gpu_tail import check_project, project_case
+    s = project_case(T, 500, 128, S, R, kind, T)
+    wide = torch.full((T, 504 + 8), -7.0, dtype=BF, device="cuda")
+    y = G.project_rows(**s, out=wide[:, 4:504])
+    check_project(s, y)
+    assert (wide[:, :4] == -7).all() and (wide[:, 504:] == -7).all()
+    rows = slice(T - 700, T)
+    part = dict(s, x=s["x"][rows], row_adapter=s["row_adapter"][rows].contiguous())
+    if kind == "f8":
+        part["x_scale"] = s["x_scale"][rows].contiguous()
+    check_project(part, y[rows])
+    assert G.tail_errors() == 0
+
+
+def test_project_rows_do_not_see_other_rows(G):
+    """What a row gives does not depend on what the other rows of the call hold: the same bits with others in their place."""
+    from test_gpu_tail import project_case
+    for T, kind in ((5, "bf16"), (40, "f8"), (100, "bf16"), (300, "bf16"), (2049, "bf16")):
+        s = project_case(T, 1000, 520 if kind == "bf16" else 528, 4, 32, kind, T)
+        y = G.project_rows(**s)
+        x = s["x"].clone()
+        rest = torch.arange(T, device="cuda") % 3 != 1
+        x[rest] = s["x"][rest.nonzero().flatten().flip(0)]
+        assert torch.equal(G.project_rows(**dict(s, x=x))[~rest], y[~rest])
+
+
 # ------------------------------------------------------------------------------ beside the sampler
 def _projection(V, H=2048, T=8):
     g = torch.Generator(device="cuda").manual_seed(V)

@@ -115,3 +115,18 @@ def test_project_refuses_more_outputs_than_it_counts(N):
     args = [P, 64, None, P, 64, None, S.STRATA_DTYPE_BF16, 4, N, 64, None, None, 0, 0, None, None, P, N, None, 0, None]
     assert S.lib.strata_project_rows(*args) == S.STRATA_ERANGE
     assert S.strata_project_workspace(2 ** 31 - 1, 1, 16) > 0
+
+
+def test_the_workspace_has_a_limit():
+    """Rows times adapters of the largest calls go through it in slabs: 256 MB and the lists, or 2,048 rows' if that is more.  A
+    single row takes no more than its own adapter's."""
+    _build_module().build_library()
+    import request_token_sampling_gb300 as S
+    for T in (129, 4099, 16384, 524288):
+        for n in (1, 64, 256, 1024):
+            for R in (16, 64, 256):
+                row = min(n, 256) * R * 4
+                lists = 20 * T + 4096
+                assert S.strata_project_workspace(T, n, R) <= min(T * row, max(256 << 20, 2048 * row)) + 256 * row + lists
+    for n in (1, 64, 1024):
+        assert S.strata_project_workspace(1, n, 64) <= 16 * 64 * 4 + 1024
