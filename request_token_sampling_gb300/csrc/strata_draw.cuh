@@ -20,7 +20,7 @@
 //
 // Bound by latency: a step that runs once a row costs its barriers, exchanges and first instructions, and a row of
 // 248,320 has ten to thirty of them.  Measured (one GB300, us on the GPU): one row of 32,000 with all cuts
-// 7.8, 5 rows of 248,320 10.7, 19 rows of 151,001 with nothing cut 13.7, 64 bfloat16 rows of 248,320 with keys of
+// 7.5 to 8.1, 5 rows of 248,320 10.6 to 11.0, 19 rows of 151,001 with nothing cut 13.7, 64 bfloat16 rows of 248,320 with keys of
 // every kind 56 (a large top_k with top_p is the longest), with nothing cut 29.
 //
 // Reading another block's shared memory runs at about 16 bytes a cycle for an SM and an exchange of two

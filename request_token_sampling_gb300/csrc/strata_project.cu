@@ -285,7 +285,8 @@ static int project_slab(const Device& dev, int device, const void* x, int64_t ld
                                 strata::inner_smem(f8), stream, overlaps, strata::INNER_SPLIT);
     return launch(f8 ? strata::inner_kernel<true> : strata::inner_kernel<false>, ma, mt, A, groups, box_rows);
   };
-  // starts beside the inner rows' kernel and waits for it before what it wrote
+  // set up while the inner rows' kernel runs, and waits for it before what it wrote; up to 32 rows its blocks also run beside
+  // that one's, above they start on the SMs that it leaves free
   auto launch_products = [&](bool overlaps) {
     if (pair > 0) {
       const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles + units, dev.sms / 2));

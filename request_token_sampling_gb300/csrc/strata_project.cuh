@@ -12,10 +12,11 @@
 // which falls on other requests' rows in delta, is found there and taken back.  More than 128 rows of
 // bfloat16 go to pair_kernel, below.
 //
-// Few rows are bound by reading w and b from HBM: w comes by TMA through up to 12 stages of shared memory,
-// 200 KB on their way to an SM.  Measured (one GB300, us on the GPU, sizes rows x outputs x width):
-// 8 x 248,320 x 2,048 bfloat16 with 8 adapters of rank 16 163 (6.6 TB/s), 64 rows of 8 bits with 32 adapters of
-// rank 32 156 (6.8 TB/s), 1 x 32,000 x 1,024 17 (4 TB/s: 250 tiles on 152 SMs, and the start).
+// Few rows are bound by reading w and b from HBM: w comes by TMA through up to 11 stages of shared memory, 112 to 176 KB
+// of it on their way to an SM.  Measured (one GB300, us on the GPU, sizes rows x outputs x width):
+// 8 x 248,320 x 2,048 bfloat16 with 8 adapters of rank 16 163 to 166 (6.5 TB/s), 64 rows of 8 bits with 32 adapters of
+// rank 32 155 (6.8 TB/s), 1 x 32,000 x 1,024 16.6 (4 TB/s: 250 tiles on 152 SMs, and the start).  128 x 32,000 x 2,048
+// with 64 adapters of rank 64 takes 96: zeros of the spread inner rows are what L2 has to bring.
 #pragma once
 
 #include <cuda.h>
@@ -225,7 +226,8 @@ __device__ __forceinline__ void write_list(const ProjectArgs& A, int tile, int t
   list[0] = n | (n > 1 || (n == 1 && used.none) ? LIST_MIXED : 0);
 }
 
-// Eight warps: the block of row t takes eight of its inner products, one to a warp.
+// Eight warps: the block of row t takes eight of its inner products, one to a warp.  Bound by a few loads one after
+// another (8 rows x 2,048, 8 adapters of rank 16: 9.6 us cold and alone, most of it beside the first tiles).
 template <typename E>
 __global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A, int tile_rows) {
   grid_dep_wait();    // first: the next kernel relies on what was before this one being done
@@ -274,8 +276,9 @@ __global__ void __launch_bounds__(256) shrink_kernel(ProjectArgs A, int tile_row
 // Many rows: the same inner rows on the tensor cores.  A cluster of INNER_SPLIT blocks takes 128 of the
 // inner products (the matrices a of a tile's adapters one below another) for all rows of a tile, each
 // block a part of K, and adds the parts up in rank order (few tiles have work, so K is split eight ways).  8-bit rows
-// are widened to bfloat16 (exactly)
-// on their way to the operand by the four warps that later write the result.
+// are widened to bfloat16 (exactly) on their way to the operand by the four warps that later write the result.
+// Bound by latency: start, a short loop, two cluster barriers (cold, us: 64 8-bit rows x 2,048 with 32 adapters of rank 32
+// 13.6, 2,180 x 1,776 with 8 22.4).
 constexpr int INNER_SPLIT = 8, INNER_ROWS = 128;
 constexpr int INNER_A = PROJ_M * PROJ_LINE;
 __host__ __device__ constexpr int inner_stages(bool f8) { return f8 ? 3 : 4; }
@@ -921,15 +924,15 @@ __global__ void __launch_bounds__(PROJ_THREADS, 1)
 // spoils in other requests' rows is therefore found in the sums: where one is not finite and an adapter of the tile
 // has an infinity or a NaN for that output, the pair goes through such tiles again at the end, with base in one
 // accumulator and the sound adapters, then each broken one alone, in the other, and writes such outputs anew
-// (4,099 x 4,096 x 4,096, us: sound 101, one infinity in an adapter 161, an adapter of NaN 195, 400 rows of NaN 111).
+// (4,099 x 4,096 x 4,096, us: sound 106, one infinity in an adapter 174, an adapter of NaN 204, 400 rows of NaN 116).
 // The inner rows are tiles of the same kind, before all others: 256 of a tile's stacked products a unit, with
 // the matrices a in w's place.  A tile of outputs adds its adapters last, and waits before that until its
 // rows' units are done.  They are the lowest tiles, so they are taken first and wait for nothing; the launch is
 // cooperative, so the pairs that have them run.
 //
-// Bound by the tensor cores (and their power) in the loop: 4,256 x 4,096 x 4,096 without adapters takes 77 us
-// (1.86 PFLOP/s).  4,099 rows with 8 adapters of rank 64 take 96 us: their units, the first tiles' wait for
-// them, and tiles that do not come out even on 76 pairs are the rest.
+// Bound by the tensor cores (and their power) in the loop: 4,099 x 4,096 x 4,096 without adapters takes 72 us (1.9 PFLOP/s).
+// With 8 adapters of rank 64 it takes 100: their units, the first tiles' wait for them, the lower parts' products, and tiles
+// that do not come out even on 76 pairs are the rest.
 constexpr int PAIR_STAGES = 7, PAIR_STAGE = 2 * PROJ_M * PROJ_LINE;
 __host__ __device__ constexpr int pair_smem() { return PAIR_STAGES * PAIR_STAGE + 1024 + 512; }
 
