@@ -44,7 +44,7 @@ struct ProjectArgs {
   uint32_t* errors;
   int64_t ldx, ldy;
   int T, N, K, S, R;
-  int most;               // adapters that a tile can have: min(S, tile rows)
+  int most;               // adapters that a tile can have: min(S, T, tile rows)
   int rank_block;         // R is cut into blocks of 64, 32 or 16 (one swizzle line of shared memory)
   int n_tiles, t_tiles, tile_rows;
 };
