@@ -8,7 +8,9 @@ take the penalised argmax.  The same launch can return raw-logit log-probabiliti
 token's, the top 0..20 alternatives, and allowed_token_ids renormalisation).
 
 Around it (``include/strata_tail.h``): ``norm_rows``, ``project_rows`` and ``draw_rows``, the final norm with an
-8-bit output, a projection with each row's low-rank adapter, and sampling from the caller's random numbers.
+8-bit output, a projection with each row's low-rank adapter, and sampling from the caller's random numbers.  And to score and
+train the end of a model (``include/strata_train.h``): ``layer_norm_rows``, ``cross_entropy_rows`` and ``distill_rows``, losses
+over the whole vocabulary without a logits tensor, with the gradients of each.
 
 This package is the thin Python binding (ctypes; PyTorch tensors for device memory and streams).
 Importing it fails loudly when the CUDA library has not been built.
@@ -17,3 +19,4 @@ from ._binding import *  # noqa: F401,F403
 from ._binding import StrataError, lib, strata_sampling_params  # noqa: F401
 from .sampler import Sampler  # noqa: F401
 from .tail import *  # noqa: F401,F403
+from .train import *  # noqa: F401,F403

@@ -10,11 +10,12 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libstrata_sample.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("strata_sample.cu", "strata_tail.cu", "strata_project.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("strata_sample.cu", "strata_tail.cu", "strata_project.cu", "strata_layer_norm.cu", "strata_loss.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
     "strata_kernel.cuh", "strata_device.cuh", "strata_resident.cuh", "strata_merge.cuh", "strata_host.h", "strata_chain.h",
-    "strata_norm.cuh", "strata_draw.cuh", "strata_project.cuh")]
-DEPENDS += [os.path.join(ROOT, "include", f) for f in ("strata_sample.h", "strata_tail.h")]
+    "strata_norm.cuh", "strata_draw.cuh", "strata_project.cuh", "strata_mma.cuh",
+    "strata_layer_norm.cuh", "strata_loss.cuh")]
+DEPENDS += [os.path.join(ROOT, "include", f) for f in ("strata_sample.h", "strata_tail.h", "strata_train.h")]
 MODULE_PATH = os.path.join(LIB_DIR, "_strata_tail.so")
 MODULE_SOURCE = os.path.join(CSRC, "tail_binding.cpp")
 DEPENDS += [MODULE_SOURCE]

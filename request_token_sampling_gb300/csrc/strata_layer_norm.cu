@@ -1,0 +1,181 @@
+// strata_layer_norm.cu -- host side of strata_layer_norm_rows and strata_layer_norm_grad (include/strata_train.h).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/strata_train.h"
+#include "strata_chain.h"
+#include "strata_host.h"
+#include "strata_layer_norm.cuh"
+
+using strata::host_fail;
+
+namespace {
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+// 16 bytes at a time where the width, every stride and every address allow it.
+struct Packs {
+  int T, n;
+  bool all;
+  Packs(int T, int H, int esz) : T(T), n(16 / esz), all(H % (16 / esz) == 0) {}
+  void look(const void* p, int64_t ld) { all = all && (p == nullptr || (!misaligned(p, 16) && (T == 1 || ld % n == 0))); }
+};
+
+// The shape of a call, as the root-mean-square norm's: many rows are bound by HBM, a thread takes up to 16
+// elements, so that enough bytes are on their way; few rows are bound by latency: a row goes to as many threads as it has packs.
+template <typename E, int N, int PER>
+cudaError_t launch_forward(const strata::LayerNormArgs& A, int least, bool overlaps, void* stream) {
+  if constexpr (N * PER <= 32 && PER <= 16) {
+    const int packs = (A.H + N - 1) / N, need = (packs + PER - 1) / PER;
+    if (PER < least || need > strata::layer_norm_most_threads(N, PER)) return launch_forward<E, N, PER * 2>(A, least, overlaps, stream);
+    constexpr int ROWS = 4;
+    if (need <= 32)
+      return strata::Launch((static_cast<unsigned>(A.T) + ROWS - 1) / ROWS, 32 * ROWS, 0, stream, overlaps)(strata::layer_norm_kernel<E, N, PER, false>, A);
+    return strata::Launch(A.T, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::layer_norm_kernel<E, N, PER, true>, A);
+  } else {
+    return strata::Launch(A.T, 1024, 0, stream, overlaps)(strata::layer_norm_wide_kernel<E>, A);
+  }
+}
+template <typename E>
+cudaError_t launch_forward(const strata::LayerNormArgs& A, bool packed, int sms, bool overlaps, void* stream) {
+  constexpr int N = 16 / static_cast<int>(sizeof(E));
+  const int packs = A.H / (packed ? N : 1);
+  const int least = A.T < 2 * sms ? 1 : packs > 64 ? 4 : packs > 32 ? 2 : 1;
+  return packed ? launch_forward<E, N, 1>(A, least, overlaps, stream) : launch_forward<E, 1, 1>(A, least, overlaps, stream);
+}
+
+// Groups of rows whose sums over rows are kept apart, until the last kernel adds them up: a block of 152 SMs has one, and
+// narrow rows several blocks to an SM.  Rows too wide for that have fewer, for the sake of the workspace.
+constexpr int SMS = 152, WIDE_GROUPS = 16, BLOCK_WIDTH = strata::LAYER_NORM_GRAD_THREADS * 16, WARP_WIDTH = 32 * 16;
+int grad_groups(int T, int H) {
+  if (H > BLOCK_WIDTH) return std::min(T, WIDE_GROUPS);
+  if (H > WARP_WIDTH) return std::min(T, SMS * (H > 4096 ? 1 : H > 2048 ? 2 : 4));
+  return std::min((T + strata::LAYER_NORM_GRAD_WARPS - 1) / strata::LAYER_NORM_GRAD_WARPS, SMS * 4);
+}
+
+template <typename E, int N, int PER>
+cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, void* stream) {
+  if constexpr (N * PER <= 16) {
+    const int need = (A.H / N + PER - 1) / PER;
+    if (A.H <= WARP_WIDTH) {
+      if (need > 32) return launch_rows<E, N, PER * 2>(A, overlaps, stream);
+      return strata::Launch(A.groups, 32 * strata::LAYER_NORM_GRAD_WARPS, static_cast<size_t>(A.H) * 8, stream, overlaps)(
+          strata::layer_norm_grad_kernel<E, N, PER, false>, A);
+    }
+    if (need > strata::LAYER_NORM_GRAD_THREADS) return launch_rows<E, N, PER * 2>(A, overlaps, stream);
+    return strata::Launch(A.groups, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::layer_norm_grad_kernel<E, N, PER, true>, A);
+  } else {
+    return cudaErrorInvalidValue;  // not reached: wider rows have their own kernels
+  }
+}
+
+template <typename E>
+cudaError_t launch_grad(const strata::LayerNormGradArgs& A, bool packed, bool overlaps, void* stream) {
+  constexpr int N = 16 / static_cast<int>(sizeof(E));
+  cudaError_t e = cudaSuccess;
+  if (A.T > 0) {
+    if (A.H <= BLOCK_WIDTH) {
+      e = packed ? launch_rows<E, N, 1>(A, overlaps, stream) : launch_rows<E, 1, 1>(A, overlaps, stream);
+      overlaps = true;
+    } else {  // the sums first: dx may be dy or x
+      if (A.part != nullptr) {
+        strata::Launch launch((A.H + 255) / 256, 256, 0, stream, overlaps);
+        launch.cfg.gridDim.y = static_cast<unsigned>(A.groups);
+        e = launch(strata::layer_norm_grad_columns_kernel<E>, A);
+        overlaps = true;
+      }
+      if (e == cudaSuccess && A.dx != nullptr) {
+        e = strata::Launch(A.T, 1024, 0, stream, overlaps)(strata::layer_norm_grad_wide_kernel<E>, A);
+        overlaps = true;
+      }
+    }
+  }
+  if (e != cudaSuccess || A.part == nullptr) return e;
+  return strata::Launch((A.H + 31) / 32, 256, 0, stream, overlaps)(strata::layer_norm_sum_kernel<E>, A);
+}
+
+}  // namespace
+
+extern "C" int strata_layer_norm_rows(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                                      const void* bias, int dtype, int T, int H, float eps, void* residual_out, int64_t ldro,
+                                      void* y, int64_t ldy, float* mean, float* rstd, void* stream) {
+  if (dtype != STRATA_DTYPE_F32 && dtype != STRATA_DTYPE_BF16) return host_fail(STRATA_EINVAL, "dtype %d", dtype);
+  if (T < 0) return host_fail(STRATA_EINVAL, "T=%d", T);
+  if (H < 1 || H > STRATA_TAIL_MAX_WIDTH) return host_fail(STRATA_ERANGE, "H=%d outside 1..%d", H, STRATA_TAIL_MAX_WIDTH);
+  if (!(eps >= 0.0f)) return host_fail(STRATA_EINVAL, "eps=%g is not a number of 0 or more", static_cast<double>(eps));
+  if (ldx < H || (residual != nullptr && ldr < H) || (residual_out != nullptr && ldro < H) || (y != nullptr && ldy < H))
+    return host_fail(STRATA_EINVAL, "a row stride below H=%d", H);
+  if (T == 0) return STRATA_OK;
+  if (residual_out == nullptr && y == nullptr && mean == nullptr && rstd == nullptr) return host_fail(STRATA_EINVAL, "no output");
+  if (x == nullptr || weight == nullptr) return host_fail(STRATA_EINVAL, "null x or weight");
+  const uintptr_t esz = dtype == STRATA_DTYPE_F32 ? 4 : 2;
+  if (misaligned(x, esz) || misaligned(residual, esz) || misaligned(weight, esz) || misaligned(bias, esz) || misaligned(residual_out, esz) ||
+      misaligned(y, esz) || misaligned(mean, 4) || misaligned(rstd, 4))
+    return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
+  strata::LayerNormArgs A{x, residual, weight, bias, residual_out, y, mean, rstd, ldx, ldr, ldro, ldy, T, H, eps};
+  uint32_t* errors = nullptr;
+  int device = 0, sms = 0;
+  if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
+  Packs packs(T, H, static_cast<int>(esz));
+  packs.look(x, ldx);
+  packs.look(residual, ldr);
+  packs.look(weight, 0);
+  packs.look(bias, 0);
+  packs.look(residual_out, ldro);
+  packs.look(y, ldy);
+  const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
+    return dtype == STRATA_DTYPE_F32 ? launch_forward<float>(A, packs.all, sms, overlaps, stream)
+                                     : launch_forward<__nv_bfloat16>(A, packs.all, sms, overlaps, stream);
+  });
+  return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_layer_norm_rows: %s", cudaGetErrorString(e));
+}
+
+extern "C" int64_t strata_layer_norm_workspace(int T, int H) {
+  if (T <= 0 || H <= 0) return 0;
+  return static_cast<int64_t>(grad_groups(T, H)) * 2 * H * 4;
+}
+
+extern "C" int strata_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight, const float* mean,
+                                      const float* rstd, const void* dresidual, int64_t lddr, int dtype, int T, int H, void* dx,
+                                      int64_t lddx, void* dweight, void* dbias, void* workspace, int64_t workspace_bytes,
+                                      void* stream) {
+  if (dtype != STRATA_DTYPE_F32 && dtype != STRATA_DTYPE_BF16) return host_fail(STRATA_EINVAL, "dtype %d", dtype);
+  if (T < 0) return host_fail(STRATA_EINVAL, "T=%d", T);
+  if (H < 1 || H > STRATA_TAIL_MAX_WIDTH) return host_fail(STRATA_ERANGE, "H=%d outside 1..%d", H, STRATA_TAIL_MAX_WIDTH);
+  if (lddy < H || ldx < H || (dresidual != nullptr && lddr < H) || (dx != nullptr && lddx < H))
+    return host_fail(STRATA_EINVAL, "a row stride below H=%d", H);
+  const bool sums = dweight != nullptr || dbias != nullptr;
+  if (!sums && dx == nullptr) return host_fail(STRATA_EINVAL, "no output");
+  if (T == 0 && !sums) return STRATA_OK;
+  const uintptr_t esz = dtype == STRATA_DTYPE_F32 ? 4 : 2;
+  if (misaligned(dweight, esz) || misaligned(dbias, esz)) return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
+  if (T > 0) {
+    if (dy == nullptr || x == nullptr || weight == nullptr || mean == nullptr || rstd == nullptr)
+      return host_fail(STRATA_EINVAL, "null dy, x, weight, mean or rstd");
+    if (misaligned(dy, esz) || misaligned(x, esz) || misaligned(weight, esz) || misaligned(dresidual, esz) || misaligned(dx, esz) ||
+        misaligned(mean, 4) || misaligned(rstd, 4))
+      return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
+    const int64_t need = strata_layer_norm_workspace(T, H);
+    if (sums && (workspace == nullptr || workspace_bytes < need || misaligned(workspace, 256)))
+      return host_fail(STRATA_EINVAL, "the workspace needs %lld bytes on 256 bytes of alignment", static_cast<long long>(need));
+  }
+  uint32_t* errors = nullptr;
+  int device = 0, sms = 0;
+  if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
+  Packs packs(T, H, static_cast<int>(esz));
+  packs.look(dy, lddy);
+  packs.look(x, ldx);
+  packs.look(weight, 0);
+  packs.look(dresidual, lddr);
+  packs.look(dx, lddx);
+  // without rows the sums are those of no groups; the workspace is not touched
+  float* part = !sums ? nullptr : T > 0 ? static_cast<float*>(workspace) : static_cast<float*>(dweight != nullptr ? dweight : dbias);
+  const strata::LayerNormGradArgs A{dy, x, weight, dresidual, mean, rstd, dx, dweight, dbias, part, lddy, ldx, lddr, lddx, T, H,
+                                    T > 0 ? grad_groups(T, H) : 0};
+  const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
+    return dtype == STRATA_DTYPE_F32 ? launch_grad<float>(A, packs.all, overlaps, stream)
+                                     : launch_grad<__nv_bfloat16>(A, packs.all, overlaps, stream);
+  });
+  return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_layer_norm_grad: %s", cudaGetErrorString(e));
+}

@@ -1,0 +1,403 @@
+// strata_loss.cu -- host side of the losses over a vocabulary and their gradients (include/strata_train.h).
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "../../include/strata_train.h"
+#include "strata_chain.h"
+#include "strata_host.h"
+#include "strata_loss.cuh"
+
+using strata::host_fail;
+
+namespace {
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+int cuda_fail(cudaError_t e, const char* what) { return host_fail(STRATA_ECUDA, "%s: %s", what, cudaGetErrorString(e)); }
+
+using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
+using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, strata::LossArgs);
+
+// What the calls need of a device, found at the first call on it.  A failure is not kept: the next call tries again.
+struct Device {
+  std::mutex lock;
+  std::atomic<bool> known{false};
+  EncodeFn encode = nullptr;
+};
+
+cudaError_t find_device(Device& d) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+  if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || p == nullptr)) e = cudaErrorNotSupported;
+  d.encode = reinterpret_cast<EncodeFn>(p);
+  auto shared = [&](Kernel kernel, bool pair) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, strata::loss_smem(pair));
+  };
+  shared(strata::loss_kernel<strata::LOSS_SUMS, false>, false);
+  shared(strata::loss_kernel<strata::LOSS_SUMS, true>, true);
+  shared(strata::loss_kernel<strata::LOSS_DIFFS, true>, true);
+  shared(strata::loss_kernel<strata::LOSS_DW, true>, true);
+  shared(strata::loss_kernel<strata::LOSS_DX, true>, true);
+  return e;
+}
+
+int device_entry(int id, const Device** dev) {
+  static Device devices[64];
+  if (id < 0 || id >= 64) return host_fail(STRATA_ERANGE, "device %d", id);
+  Device& d = devices[id];
+  if (!d.known.load(std::memory_order_acquire)) {
+    try {
+      std::lock_guard<std::mutex> hold(d.lock);
+      if (!d.known.load()) {
+        if (const cudaError_t e = find_device(d); e != cudaSuccess) return cuda_fail(e, "device setup");
+        d.known.store(true, std::memory_order_release);
+      }
+    } catch (...) {  // no exception leaves a C call
+      return host_fail(STRATA_ECUDA, "device setup");
+    }
+  }
+  *dev = &d;
+  return STRATA_OK;
+}
+
+// A map of `rows` rows of `width` elements (bfloat16, or float32), cut into boxes of 128 bytes by `box_rows`.
+bool map_rows(const Device& dev, CUtensorMap* m, bool f32, const void* p, int64_t width, int64_t rows, int64_t ld, int box_rows) {
+  const cuuint64_t esz = f32 ? 4 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)}, strides[1] = {static_cast<cuuint64_t>(ld) * esz};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(strata::LOSS_LINE / esz), static_cast<cuuint32_t>(box_rows)}, ones[2] = {1, 1};
+  return dev.encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, ones,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ------------------------------------------------------------------------------ a call's plan
+// It goes by the sizes alone, so that the workspace's size can be asked for without a device.
+constexpr int SMS = 152, PAIRS = SMS / 2;
+constexpr int ALONE_ROWS = 128;           // a call with more works by pairs of SMs, on a copy of the rows that take part
+constexpr int SLAB_ROWS = 8192;           // whose tiles' sums are held at a time
+constexpr int64_t PIECE_BYTES = int64_t{512} << 20, PARTS_BYTES = int64_t{1} << 30;
+
+int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+
+// Columns of a tile: those whose tiles come out most even on the SMs.  A stage of a pair's tile costs about as much as 80
+// columns more (as measured for the projection); a tile of one SM is bound by reading w.
+int sums_columns(int T, int V) {
+  const bool pair = T > ALONE_ROWS;
+  const int64_t rows = pair ? tiles_of(std::min(T, SLAB_ROWS), 256) : 1;
+  int best = 256;
+  int64_t least = INT64_MAX;
+  for (int bn = 256; bn >= (pair ? 128 : 32); bn -= 32) {
+    const int64_t cost = tiles_of(rows * tiles_of(V, bn), pair ? PAIRS : SMS) * (bn + (pair ? 80 : 16));
+    if (cost < least) {
+      least = cost;
+      best = bn;
+    }
+  }
+  return best;
+}
+
+struct Plan {
+  int T, V, H, K;
+  bool lists, grad, moved;          // a teacher's tokens; for a gradient; works on a copy of the rows
+  int rows_pad = 0, bn = 0, n_tiles = 0, slab = 0;
+  int piece = 0, splits = 1, width = 0;  // ids of a piece; parts of dx; columns of a tile of dw and dx
+  int64_t sorted = 0, q = 0, logq = 0, state = 0, rows = 0, place = 0, count = 0, by = 0, copy = 0, scaled = 0, parts = 0, picks = 0, d = 0, dx = 0,
+          bytes = 0;                // places in the workspace
+
+  Plan(int T, int V, int H, int K, bool grad) : T(T), V(V), H(H), K(std::max(K, 1)), lists(K > 0), grad(grad), moved(grad || T > ALONE_ROWS) {
+    auto take = [&](int64_t n) {
+      const int64_t at = bytes;
+      bytes += (n + 255) / 256 * 256;
+      return at;
+    };
+    const int64_t t = T, words = t * this->K * 4;
+    rows_pad = static_cast<int>(tiles_of(T, 256) * 256);
+    if (lists) {
+      sorted = take(words);
+      q = take(words);
+      logq = take(words);
+      state = take(t * 4);
+    }
+    if (moved) {
+      rows = take(t * 4);
+      place = take(t * 4);
+      count = take(4);
+      by = take(4);
+      copy = take(static_cast<int64_t>(rows_pad) * H * 2);
+    }
+    if (!grad) {
+      bn = sums_columns(T, V);
+      n_tiles = static_cast<int>(tiles_of(V, bn));
+      slab = std::min(T, SLAB_ROWS);
+      parts = take(static_cast<int64_t>(slab) * n_tiles * 8);
+      picks = take(static_cast<int64_t>(slab) * this->K * 4);
+      return;
+    }
+    scaled = take(static_cast<int64_t>(rows_pad) * H * 2);
+    const int64_t all = tiles_of(V, 256) * 256;
+    piece = static_cast<int>(std::min(all, std::max<int64_t>(256, PIECE_BYTES / (rows_pad * int64_t{2}) / 256 * 256)));
+    d = take(static_cast<int64_t>(rows_pad) * piece * 2);
+    width = H <= 128 ? 128 : 256;
+    // Few tiles of dx leave pairs idle in the last turn: the sum over a piece's ids is cut into the parts that leave the least
+    const int64_t tiles = rows_pad / 256 * tiles_of(H, width), one = static_cast<int64_t>(rows_pad) * H * 4;
+    double least = 1e30;
+    for (int s = 1; s <= 16 && (s == 1 || (s * one <= PARTS_BYTES && piece / 64 >= 8 * s)); ++s) {
+      const double cost = static_cast<double>(tiles_of(tiles * s, PAIRS)) / s + 0.02 * s;
+      if (cost < least) {
+        least = cost;
+        splits = s;
+      }
+    }
+    dx = take(splits * one);
+  }
+};
+
+struct Loss {
+  const void *x, *w;
+  int64_t ldx, ldw;
+  int T, V, H, K;
+  const int32_t* ids;
+  const float* teacher;  // NULL: a cross entropy
+  float temperature;
+  void* workspace;
+  int64_t workspace_bytes;
+  void* stream;
+};
+
+// What both directions check.
+int check(const Loss& C, bool grad) {
+  if (C.T < 0 || C.V < 1) return host_fail(STRATA_EINVAL, "T=%d V=%d", C.T, C.V);
+  if (C.T > STRATA_LOSS_MAX_ROWS) return host_fail(STRATA_ERANGE, "T=%d above %d", C.T, STRATA_LOSS_MAX_ROWS);
+  if (C.V > STRATA_MAX_VOCAB) return host_fail(STRATA_ERANGE, "V=%d above %d", C.V, STRATA_MAX_VOCAB);
+  if (C.H < 1 || C.H > STRATA_LOSS_MAX_WIDTH) return host_fail(STRATA_ERANGE, "H=%d outside 1..%d", C.H, STRATA_LOSS_MAX_WIDTH);
+  if (C.K < 0 || C.K > STRATA_DISTILL_MAX_TOKENS) return host_fail(STRATA_ERANGE, "K=%d outside 1..%d", C.K, STRATA_DISTILL_MAX_TOKENS);
+  if (C.ldx < C.H || C.ldw < C.H) return host_fail(STRATA_EINVAL, "a row stride below H=%d", C.H);
+  if (!(C.temperature > 0.0f) || C.temperature - C.temperature != 0.0f || !(1.0f / C.temperature < 1e30f))
+    return host_fail(STRATA_EINVAL, "temperature=%g", static_cast<double>(C.temperature));
+  if (C.H % 8 != 0 || C.ldx % 8 != 0 || C.ldw % 8 != 0) return host_fail(STRATA_EALIGN, "H or a row stride is not a multiple of 8");
+  if (C.T == 0) return STRATA_OK;
+  if (C.x == nullptr || C.w == nullptr || C.ids == nullptr || (C.K > 0 && C.teacher == nullptr))
+    return host_fail(STRATA_EINVAL, "null x, w, ids or teacher");
+  if (misaligned(C.x, 16) || misaligned(C.w, 16)) return host_fail(STRATA_EALIGN, "x or w not 16-byte aligned");
+  if (misaligned(C.ids, 4) || misaligned(C.teacher, 4)) return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
+  const int64_t need = strata_loss_workspace(C.T, C.V, C.H, C.K, grad);
+  if (C.workspace == nullptr || C.workspace_bytes < need || misaligned(C.workspace, 256))
+    return host_fail(STRATA_EINVAL, "the workspace needs %lld bytes on 256 bytes of alignment", static_cast<long long>(need));
+  return STRATA_OK;
+}
+
+template <typename T>
+T* at(const Loss& C, int64_t place) {
+  return reinterpret_cast<T*>(static_cast<char*>(C.workspace) + place);
+}
+
+// Launches one kernel after another, the first as the chain of its stream says.
+struct Run {
+  void* stream;
+  bool overlaps;
+  cudaError_t e = cudaSuccess;
+  template <typename K, typename... A>
+  void operator()(K kernel, unsigned grid, unsigned block, size_t smem, unsigned cluster, A... args) {
+    if (e != cudaSuccess) return;
+    e = strata::Launch(grid, block, smem, stream, overlaps, cluster)(kernel, args...);
+    overlaps = true;
+  }
+  void products(Kernel kernel, bool pair, int64_t tiles, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const strata::LossArgs& A) {
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(tiles, pair ? PAIRS : SMS)) * (pair ? 2 : 1);
+    (*this)(kernel, blocks, strata::LOSS_THREADS, strata::loss_smem(pair), pair ? 2 : 1, a, b, o, A);
+  }
+};
+
+// A teacher's tokens in order, and the copies of the rows that take part.
+void launch_plan(Run& run, const Loss& C, const Plan& P, const float* g, float* loss, float* lse, void* dx, int64_t lddx) {
+  if (P.lists) {
+    const strata::LossListArgs A{C.ids, C.teacher, at<int32_t>(C, P.sorted), at<float>(C, P.q), at<float>(C, P.logq), at<int32_t>(C, P.state),
+                                 1.0f / C.temperature, C.T, C.V, P.K};
+    run(strata::loss_list_kernel, static_cast<unsigned>((C.T + 3) / 4), 128, 0, 1, A);
+  }
+  if (!P.moved) return;
+  strata::LossPlanArgs A{};
+  A.ids = C.ids;
+  A.state = P.lists ? at<int32_t>(C, P.state) : nullptr;
+  A.g = g;
+  A.x = static_cast<const __nv_bfloat16*>(C.x);
+  A.ldx = C.ldx;
+  A.rows = at<int32_t>(C, P.rows);
+  A.place = at<int32_t>(C, P.place);
+  A.count = at<int32_t>(C, P.count);
+  A.by = at<float>(C, P.by);
+  A.copy = at<__nv_bfloat16>(C, P.copy);
+  A.scaled = P.grad ? at<__nv_bfloat16>(C, P.scaled) : nullptr;
+  A.loss = loss;
+  A.lse = lse;
+  A.dx = static_cast<__nv_bfloat16*>(dx);
+  A.lddx = lddx;
+  A.T = C.T;
+  A.V = C.V;
+  A.H = C.H;
+  run(strata::loss_plan_kernel, 1, 1024, 0, 1, A);
+  run(strata::loss_gather_kernel, static_cast<unsigned>(C.T) + 256, 128, 0, 1, A);
+}
+
+strata::LossArgs products_args(const Loss& C, const Plan& P, uint32_t* errors) {
+  strata::LossArgs A{};
+  A.count = P.moved ? at<int32_t>(C, P.count) : nullptr;
+  A.rows = P.moved ? at<int32_t>(C, P.rows) : nullptr;
+  A.ids = P.lists ? at<int32_t>(C, P.sorted) : C.ids;
+  A.q = P.lists ? at<float>(C, P.q) : nullptr;
+  A.errors = errors;
+  A.scale = static_cast<float>(1.4426950408889634 / static_cast<double>(C.temperature));
+  A.dw_scale = C.temperature;
+  A.T = C.T;
+  A.V = C.V;
+  A.H = C.H;
+  A.K = P.K;
+  A.rows_most = P.rows_pad;
+  A.rows_pad = P.rows_pad;
+  A.splits = 1;
+  return A;
+}
+
+int forward(const Loss& C, float* loss, float* lse, const char* name) {
+  if (const int rc = check(C, false); rc != STRATA_OK) return rc;
+  if (C.T == 0) return STRATA_OK;
+  if (loss == nullptr || lse == nullptr) return host_fail(STRATA_EINVAL, "null loss or lse");
+  if (misaligned(loss, 4) || misaligned(lse, 4)) return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
+  uint32_t* errors = nullptr;
+  int device = 0, sms = 0;
+  if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
+  const Device* dev = nullptr;
+  if (const int rc = device_entry(device, &dev); rc != STRATA_OK) return rc;
+  const Plan P(C.T, C.V, C.H, C.K, false);
+  const bool pair = P.moved;
+  CUtensorMap mx, mw;
+  if (!(pair ? map_rows(*dev, &mx, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, 128) : map_rows(*dev, &mx, false, C.x, C.H, C.T, C.ldx, 128)))
+    return host_fail(STRATA_EINVAL, "x cannot be mapped");
+  if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, pair ? P.bn / 2 : P.bn)) return host_fail(STRATA_EINVAL, "w cannot be mapped");
+  const cudaError_t e = strata::launch_operator(device, C.stream, [&](bool overlaps) {
+    Run run{C.stream, overlaps};
+    launch_plan(run, C, P, nullptr, loss, lse, nullptr, 0);
+    strata::LossArgs A = products_args(C, P, errors);
+    A.columns = C.V;
+    A.bn = P.bn;
+    A.n_tiles = P.n_tiles;
+    A.parts = at<float2>(C, P.parts);
+    A.picks = at<float>(C, P.picks);
+    strata::LossJoinArgs J{A.count, A.rows, A.ids, P.lists ? at<int32_t>(C, P.state) : nullptr, A.q, P.lists ? at<float>(C, P.logq) : nullptr,
+                           A.picks, A.parts, loss, lse, C.temperature, C.T, C.V, P.K, 0, P.n_tiles};
+    for (int row0 = 0; row0 < C.T; row0 += P.slab) {
+      A.row0 = J.row0 = row0;
+      A.rows_most = std::min(P.slab, C.T - row0);
+      run.products(pair ? strata::loss_kernel<strata::LOSS_SUMS, true> : strata::loss_kernel<strata::LOSS_SUMS, false>, pair,
+                   tiles_of(A.rows_most, pair ? 256 : 128) * P.n_tiles, mx, mw, mw, A);
+      run(strata::loss_join_kernel, static_cast<unsigned>(A.rows_most), 128, 0, 1, J);
+    }
+    return run.e;
+  });
+  return e == cudaSuccess ? STRATA_OK : cuda_fail(e, name);
+}
+
+int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t lddx, void* dw, int64_t lddw, const char* name) {
+  if (dx == nullptr && dw == nullptr) return host_fail(STRATA_EINVAL, "no output");
+  if (const int rc = check(C, true); rc != STRATA_OK) return rc;
+  if ((dx != nullptr && lddx < C.H) || (dw != nullptr && lddw < C.H)) return host_fail(STRATA_EINVAL, "a row stride below H=%d", C.H);
+  if (misaligned(dx, 16) || misaligned(dw, 16)) return host_fail(STRATA_EALIGN, "dx or dw not 16-byte aligned");
+  if ((dx != nullptr && lddx % 8 != 0) || (dw != nullptr && lddw % 8 != 0)) return host_fail(STRATA_EALIGN, "a row stride is not a multiple of 8");
+  if (C.T == 0 && dw == nullptr) return STRATA_OK;
+  if (C.T > 0 && (lse == nullptr || g == nullptr)) return host_fail(STRATA_EINVAL, "null lse or g");
+  if (misaligned(lse, 4) || misaligned(g, 4)) return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
+  uint32_t* errors = nullptr;
+  int device = 0, sms = 0;
+  if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
+  cudaError_t e;
+  if (C.T == 0) {
+    e = strata::launch_operator(device, C.stream, [&](bool overlaps) {
+      return strata::Launch(static_cast<unsigned>(C.V), 256, 0, C.stream, overlaps)(strata::loss_zero_kernel, static_cast<__nv_bfloat16*>(dw), lddw, C.H);
+    });
+    return e == cudaSuccess ? STRATA_OK : cuda_fail(e, name);
+  }
+  const Device* dev = nullptr;
+  if (const int rc = device_entry(device, &dev); rc != STRATA_OK) return rc;
+  const Plan P(C.T, C.V, C.H, C.K, true);
+  CUtensorMap mx, mw, mxs, mws, md, mds, mdo, mdw{}, mdx;
+  if (!map_rows(*dev, &mx, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, 128) ||
+      !map_rows(*dev, &mxs, false, at<void>(C, P.scaled), C.H, P.rows_pad, C.H, 64) ||
+      !map_rows(*dev, &md, false, at<void>(C, P.d), P.piece, P.rows_pad, P.piece, 128) ||
+      !map_rows(*dev, &mds, false, at<void>(C, P.d), P.piece, P.rows_pad, P.piece, 64) ||
+      !map_rows(*dev, &mdo, false, at<void>(C, P.d), P.piece, P.rows_pad, P.piece, 32) ||
+      !map_rows(*dev, &mdx, true, at<void>(C, P.dx), C.H, static_cast<int64_t>(P.splits) * P.rows_pad, C.H, 32))
+    return host_fail(STRATA_EINVAL, "the workspace cannot be mapped");
+  if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, 128) || !map_rows(*dev, &mws, false, C.w, C.H, C.V, C.ldw, 64) ||
+      (dw != nullptr && !map_rows(*dev, &mdw, false, dw, C.H, C.V, lddw, 32)))
+    return host_fail(STRATA_EINVAL, "w or dw cannot be mapped");
+  e = strata::launch_operator(device, C.stream, [&](bool overlaps) {
+    Run run{C.stream, overlaps};
+    launch_plan(run, C, P, g, nullptr, nullptr, dx, lddx);
+    strata::LossArgs A = products_args(C, P, errors);
+    A.lse = lse;
+    A.by = at<float>(C, P.by);
+    const int64_t row_tiles = P.rows_pad / 256, across = tiles_of(C.H, P.width);
+    for (int v0 = 0; v0 < C.V; v0 += P.piece) {
+      A.v0 = v0;
+      A.columns = std::min(P.piece, C.V - v0);
+      A.bn = 256;
+      A.n_tiles = static_cast<int>(tiles_of(A.columns, 256));
+      run.products(strata::loss_kernel<strata::LOSS_DIFFS, true>, true, row_tiles * A.n_tiles, mx, mw, mdo, A);
+      A.bn = P.width;
+      A.n_tiles = static_cast<int>(across);
+      if (dw != nullptr) run.products(strata::loss_kernel<strata::LOSS_DW, true>, true, tiles_of(A.columns, 256) * across, mds, mxs, mdw, A);
+      if (dx != nullptr) {
+        A.splits = P.splits;
+        A.add = v0 > 0;
+        run.products(strata::loss_kernel<strata::LOSS_DX, true>, true, row_tiles * across * P.splits, md, mws, mdx, A);
+      }
+    }
+    if (dx != nullptr) {
+      const strata::LossDxArgs D{A.count, A.rows, at<float>(C, P.dx), g, static_cast<__nv_bfloat16*>(dx), lddx,
+                                 static_cast<int64_t>(P.rows_pad) * C.H, C.temperature, C.H, P.splits};
+      run(strata::loss_dx_kernel, static_cast<unsigned>(C.T), 128, 0, 1, D);
+    }
+    return run.e;
+  });
+  return e == cudaSuccess ? STRATA_OK : cuda_fail(e, name);
+}
+
+}  // namespace
+
+extern "C" int64_t strata_loss_workspace(int T, int V, int H, int K, int grad) {
+  if (T <= 0 || V <= 0 || H <= 0 || K < 0) return 0;
+  return Plan(T, V, H, K, grad != 0).bytes;
+}
+
+extern "C" int strata_cross_entropy_rows(const void* x, int64_t ldx, const void* w, int64_t ldw, int T, int V, int H, const int32_t* ids,
+                                         float* loss, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  return forward(Loss{x, w, ldx, ldw, T, V, H, 0, ids, nullptr, 1.0f, workspace, workspace_bytes, stream}, loss, lse, "strata_cross_entropy_rows");
+}
+
+extern "C" int strata_cross_entropy_grad(const void* x, int64_t ldx, const void* w, int64_t ldw, int T, int V, int H, const int32_t* ids,
+                                         const float* lse, const float* g, void* dx, int64_t lddx, void* dw, int64_t lddw, void* workspace,
+                                         int64_t workspace_bytes, void* stream) {
+  return backward(Loss{x, w, ldx, ldw, T, V, H, 0, ids, nullptr, 1.0f, workspace, workspace_bytes, stream}, lse, g, dx, lddx, dw, lddw,
+                  "strata_cross_entropy_grad");
+}
+
+extern "C" int strata_distill_rows(const void* x, int64_t ldx, const void* w, int64_t ldw, int T, int V, int H, int K, const int32_t* ids,
+                                   const float* teacher, float temperature, float* loss, float* lse, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+  if (K < 1) return host_fail(STRATA_ERANGE, "K=%d outside 1..%d", K, STRATA_DISTILL_MAX_TOKENS);
+  return forward(Loss{x, w, ldx, ldw, T, V, H, K, ids, teacher, temperature, workspace, workspace_bytes, stream}, loss, lse, "strata_distill_rows");
+}
+
+extern "C" int strata_distill_grad(const void* x, int64_t ldx, const void* w, int64_t ldw, int T, int V, int H, int K, const int32_t* ids,
+                                   const float* teacher, float temperature, const float* lse, const float* g, void* dx, int64_t lddx, void* dw,
+                                   int64_t lddw, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (K < 1) return host_fail(STRATA_ERANGE, "K=%d outside 1..%d", K, STRATA_DISTILL_MAX_TOKENS);
+  return backward(Loss{x, w, ldx, ldw, T, V, H, K, ids, teacher, temperature, workspace, workspace_bytes, stream}, lse, g, dx, lddx, dw, lddw,
+                  "strata_distill_grad");
+}

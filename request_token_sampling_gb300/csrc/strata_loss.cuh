@@ -1,0 +1,724 @@
+// strata_loss.cuh -- losses over a whole vocabulary straight from the rows and the head, and their gradients.
+//
+//   z = x w^T / s;  lse = log sum exp z;  loss = s^2 sum_k q_k (log q_k - (z_k - lse));  dz = g s (exp(z - lse) - q)
+//   dx = dz w;  dw = dz^T x            (a cross entropy has one k with q = 1, and s = 1)
+//
+// The logits exist as tiles of tensor memory only.  One kernel makes all four kinds of products on the tensor cores:
+//   LOSS_SUMS   z of 256 rows and up to 256 ids: a maximum and a sum of exponentials for each row, and z of the row's ids
+//   LOSS_DIFFS  z again, and d = exp(z - lse) - q in bfloat16 to the workspace, for a piece of the vocabulary
+//   LOSS_DW     dw of the piece: d^T xs over the rows (both operands with the sum's index outermost in memory)
+//   LOSS_DX     parts of dx: d w over the piece's ids (w with the sum's index outermost), in 32 bits
+// Between d and its products stands one rounding to bfloat16, the type of w and x, which the tensor cores ask for: at most 2^-8 of
+// each term, as far off as the results' own rounding.  g stays out of d: dx is scaled in 32 bits at the end, and
+// x of a row is scaled by g / max|g| in xs, which changes nothing where all g are equal (a mean).
+//
+// Rows that are left out do not take part: the others are copied one after another first (loss_gather_kernel).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "strata_mma.cuh"
+#include "strata_norm.cuh"
+
+namespace strata {
+
+enum LossMode { LOSS_SUMS, LOSS_DIFFS, LOSS_DW, LOSS_DX };
+
+constexpr int LOSS_LINE = 128;        // bytes of a row that one stage holds: 64 bfloat16
+constexpr int LOSS_THREADS = 192;     // warp 0 loads, warp 1 issues the products, warps 2-5 write the tile
+constexpr int LOSS_BAND = 16;         // tiles of the inner index that a band has: what its operands take stays in L2
+constexpr int LOSS_NO_ID = 0x7FFFFFFF;
+// Two SMs share a tile: 128 rows and half of the columns each; one SM alone has 128 rows and all columns.
+__host__ __device__ constexpr int loss_stages(bool pair) { return pair ? 6 : 4; }
+__host__ __device__ constexpr int loss_stage_bytes(bool pair) { return (128 + (pair ? 128 : 256)) * LOSS_LINE; }
+constexpr int LOSS_STAGING = 4096;    // of 32 rows' results on their way to memory; two for each writing warp
+__host__ __device__ constexpr int loss_smem(bool pair) { return loss_stages(pair) * loss_stage_bytes(pair) + 8 * LOSS_STAGING + 1024 + 512; }
+
+struct LossArgs {
+  const int32_t* count;   // rows that take part, as the plan found them; NULL: all T
+  const int32_t* rows;    // which they are; NULL: row r itself
+  const int32_t* ids;     // [T][K], ascending where K > 1, those that are not there last as LOSS_NO_ID
+  const float* q;         // [T][K] beside them; NULL: 1
+  const float* lse;       // of row t, for LOSS_DIFFS
+  const float* by;        // scale of LOSS_DW's results, NULL: none
+  float2* parts;          // [rows][n_tiles]: exponent and sum of a tile's columns, for LOSS_SUMS
+  float* picks;           // [rows][K]: z of the row's ids
+  uint32_t* errors;
+  float scale;            // log2(e) / s
+  float dw_scale;         // s
+  int T, V, H, K;
+  int row0, rows_most;    // rows row0 .. of this launch
+  int v0, columns;        // the piece of the vocabulary
+  int bn, n_tiles;        // columns of a tile, and tiles of them
+  int splits, rows_pad;   // LOSS_DX: parts that the ids are cut into, and rows of each
+  int add;                // LOSS_DX: onto what is there
+};
+
+struct LossBars {
+  uint64_t full[6], empty[6], done[2], freed[2], drained;
+  uint32_t tmem, dead;
+};
+
+// Shared-memory operand descriptor of an operand whose index of the sum is outermost: blocks of 64 rows or columns, each
+// 64 lines (one for each step of the sum) of 128 bytes, a block 8,192 bytes from the next; eight lines make a swizzle group.
+__device__ __forceinline__ uint64_t loss_desc_outer(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(8192 >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// 32-bit sums of bfloat16; A and B with the sum's index innermost, or outermost (bits 15 and 16).
+__device__ __forceinline__ uint32_t loss_idesc(int m, int n, bool a_outer, bool b_outer) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_outer ? 1u << 15 : 0u) | (b_outer ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x), "r"(y), "r"(src) : "memory");
+}
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* m, int x, int y, uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x), "r"(y), "r"(src) : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Tile `tile` of `outer` x `inner`: bands of LOSS_BAND inner ones, which go fastest.
+__device__ __forceinline__ void loss_place(int tile, int outer, int inner, int& o, int& i) {
+  const int band = tile / (LOSS_BAND * outer), width = min(LOSS_BAND, inner - band * LOSS_BAND), rest = tile - band * LOSS_BAND * outer;
+  o = rest / width;
+  i = band * LOSS_BAND + rest % width;
+}
+
+// The next of a row's ids from `from` on, in ascending order.
+struct LossIds {
+  const int32_t* ids;
+  const float* q;
+  int at, K, next;
+  __device__ __forceinline__ void start(const LossArgs& A, int64_t t, int from) {
+    K = t < 0 ? 0 : A.K;
+    ids = A.ids + (t < 0 ? 0 : t) * A.K;
+    q = A.q != nullptr ? A.q + (t < 0 ? 0 : t) * A.K : nullptr;
+    at = 0;
+    if (K == 1) {
+      if (ids[0] < from) at = 1;
+    } else {
+      for (int upto = K; at < upto;) {
+        const int mid = (at + upto) / 2;
+        if (ids[mid] < from)
+          at = mid + 1;
+        else
+          upto = mid;
+      }
+    }
+    next = at < K ? ids[at] : LOSS_NO_ID;
+  }
+  __device__ __forceinline__ float weight() const { return q != nullptr ? q[at] : 1.0f; }
+  __device__ __forceinline__ void advance() { next = ++at < K ? ids[at] : LOSS_NO_ID; }
+};
+
+template <int MODE, bool PAIR>
+__global__ void __launch_bounds__(LOSS_THREADS, 1)
+    loss_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mo,
+                const __grid_constant__ LossArgs A) {
+  constexpr int STAGES = loss_stages(PAIR), STAGE = loss_stage_bytes(PAIR), TILE_M = PAIR ? 256 : 128;
+  constexpr bool A_OUTER = MODE == LOSS_DW, B_OUTER = MODE == LOSS_DW || MODE == LOSS_DX;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint8_t* staging = smem + STAGES * STAGE;
+  LossBars* B = reinterpret_cast<LossBars*>(staging + 8 * LOSS_STAGING);
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool lead = rank == 0;
+  volatile uint32_t* dead = &B->dead;
+  const uint32_t bit = 0x08u;  // STRATA_DEVERR_TIMEOUT
+  constexpr uint32_t TMEM_COLS = 512;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&B->full[i], 1);
+      mbar_init(&B->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->done[i], 1);
+      mbar_init(&B->freed[i], PAIR ? 8 : 4);  // the first block's: four warps of each
+    }
+    mbar_init(&B->drained, 1);
+    B->dead = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B->tmem)), "r"(TMEM_COLS) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B->tmem)), "r"(TMEM_COLS) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+  if constexpr (PAIR) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  tc_fence_after();
+  const uint32_t tmem = B->tmem;
+
+  // this launch's rows and tiles
+  const int live = max(0, min((A.count != nullptr ? *A.count : A.T) - A.row0, A.rows_most));
+  const int row_tiles = (live + TILE_M - 1) / TILE_M;
+  int outer, inner, k_all, splits = 1;
+  if constexpr (MODE == LOSS_SUMS || MODE == LOSS_DIFFS) {
+    outer = A.n_tiles, inner = row_tiles, k_all = (A.H + 63) / 64;
+  } else if constexpr (MODE == LOSS_DW) {
+    outer = (A.columns + TILE_M - 1) / TILE_M, inner = A.n_tiles, k_all = (live + 63) / 64;
+  } else {
+    outer = A.n_tiles, inner = row_tiles, k_all = (A.columns + 63) / 64, splits = A.splits;
+  }
+  const int per_split = outer * inner, tiles = per_split * splits;
+  const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+  const int half = PAIR ? A.bn / 2 : A.bn;  // columns that this block brings
+  auto stages_of = [&](int split, int& from, int& to) {
+    from = static_cast<int>(static_cast<int64_t>(k_all) * split / splits);
+    to = static_cast<int>(static_cast<int64_t>(k_all) * (split + 1) / splits);
+  };
+
+  Ring<STAGES> ring;  // of the loading and of the issuing warp
+  bool alive = true;
+  uint32_t turn = 0;  // tiles so far, of the issuing warp and of those that write
+  if (warp == 0) {
+    asm volatile("fence.proxy.async;" ::: "memory");  // rows and d were written by ordinary stores of kernels before
+    const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * (128 + half) * LOSS_LINE);
+    for (int tile = first; tile < tiles && alive; tile += step) {
+      int o, i, from, to;
+      const int split = MODE == LOSS_DX ? tile / per_split : 0;
+      loss_place(tile - split * per_split, outer, inner, o, i);
+      stages_of(split, from, to);
+      for (int s = from; s < to; ++s, ring.next()) {
+        if (ring.begun >= STAGES && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) {
+          alive = false;
+          break;
+        }
+        const uint32_t at = smem_u32(smem + ring.slot * STAGE), at_b = at + 128 * LOSS_LINE;
+        const uint32_t bar = PAIR ? dsmem_addr(smem_u32(&B->full[ring.slot]), 0) : smem_u32(&B->full[ring.slot]);
+        auto load = [&](uint32_t to_, const CUtensorMap* m, int x, int y) {
+          if constexpr (PAIR)
+            pair_tma_2d(to_, m, x, y, bar);
+          else
+            tma_2d(to_, m, x, y, bar);
+        };
+        if (elect_one()) {
+          if (lead) mbar_arrive_expect_tx(&B->full[ring.slot], bytes);
+          if constexpr (MODE == LOSS_SUMS || MODE == LOSS_DIFFS) {
+            load(at, &ma, s * 64, A.row0 + i * TILE_M + rank * 128);
+            load(at_b, &mb, s * 64, A.v0 + o * A.bn + rank * half);
+          } else if constexpr (MODE == LOSS_DW) {
+            for (int b = 0; b < 2; ++b) load(at + b * 8192, &ma, o * TILE_M + rank * 128 + b * 64, s * 64);
+            for (int b = 0; b < half / 64; ++b) load(at_b + b * 8192, &mb, i * A.bn + rank * half + b * 64, s * 64);
+          } else {
+            load(at, &ma, s * 64, i * TILE_M + rank * 128);
+            for (int b = 0; b < half / 64; ++b) load(at_b + b * 8192, &mb, o * A.bn + rank * half + b * 64, A.v0 + s * 64);
+          }
+        }
+      }
+    }
+    if (!alive && lead) ring.drain(B->full);
+  } else if (warp == 1 && lead) {
+    const uint32_t idesc = loss_idesc(TILE_M, A.bn, A_OUTER, B_OUTER);
+    constexpr uint32_t STEP_A = A_OUTER ? 128 : 2, STEP_B = B_OUTER ? 128 : 2;  // 16 steps of the sum, in 16 bytes
+    for (int tile = first; tile < tiles && alive; tile += step, ++turn) {
+      const uint32_t buf = turn & 1, sum = tmem + buf * 256;
+      if (turn >= 2 && !proj_wait(&B->freed[buf], (turn / 2 + 1) & 1, dead, A.errors, bit)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      int from, to;
+      stages_of(MODE == LOSS_DX ? tile / per_split : 0, from, to);
+      for (int s = from; s < to; ++s, ring.next()) {
+        if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = smem_u32(smem + ring.slot * STAGE), at_b = at + 128 * LOSS_LINE;
+        const uint64_t da = A_OUTER ? loss_desc_outer(at) : mma_desc(at, LOSS_LINE), db = B_OUTER ? loss_desc_outer(at_b) : mma_desc(at_b, LOSS_LINE);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (PAIR)
+              pair_mma(sum, da + STEP_A * i, db + STEP_B * i, idesc, s > from || i > 0);
+            else
+              mma<false>(sum, da + STEP_A * i, db + STEP_B * i, idesc, s > from || i > 0);
+          }
+          if constexpr (PAIR)
+            pair_commit(&B->empty[ring.slot]);
+          else
+            mma_commit(&B->empty[ring.slot]);
+        }
+      }
+      if (alive && elect_one()) {
+        if constexpr (PAIR)
+          pair_commit(&B->done[buf]);
+        else
+          mma_commit(&B->done[buf]);
+      }
+    }
+    if (!alive) {  // the products in flight end before the blocks give their tensor memory back
+      if (elect_one()) {
+        if constexpr (PAIR)
+          pair_commit(&B->drained);
+        else
+          mma_commit(&B->drained);
+      }
+      for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&B->drained, 0); ++spin) {
+      }
+    }
+  } else if (warp >= 2) {
+    const uint32_t quarter = warp & 3;
+    uint8_t* mine = staging + (warp - 2) * 2 * LOSS_STAGING;  // this warp's two halves of staging, in turns
+    uint32_t flip = 0;
+    // the line that this lane fills, its 16-byte pieces swizzled as the copy out expects them
+    auto line = [&]() { return smem_u32(mine + flip * LOSS_STAGING) + lane * 128; };
+    auto put = [&](uint32_t at, int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((piece ^ (lane & 7)) << 4)), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+    };
+    auto open = [&]() {  // the copy before the last has read its half
+      if (lane == 0) tma_store_wait_read1();
+      __syncwarp();
+    };
+    auto send = [&](int x, int y, bool add) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t src = smem_u32(mine + flip * LOSS_STAGING);
+        if (add)
+          tma_add_2d(&mo, x, y, src);
+        else
+          tma_store_2d(&mo, x, y, src);
+        tma_store_commit();
+      }
+      flip ^= 1;
+    };
+    for (int tile = first; tile < tiles; tile += step, ++turn) {
+      int o, i, from, to;
+      const int split = MODE == LOSS_DX ? tile / per_split : 0;
+      loss_place(tile - split * per_split, outer, inner, o, i);
+      stages_of(split, from, to);
+      const uint32_t buf = turn & 1, sum = tmem + buf * 256 + (quarter << 21);
+      const int in_tile = static_cast<int>(rank * 128 + quarter * 32);  // this warp's first lane
+      const int r = i * TILE_M + in_tile + lane;                         // of SUMS and DIFFS: the row of this launch
+      [[maybe_unused]] int64_t t = -1;
+      [[maybe_unused]] LossIds ids;
+      [[maybe_unused]] int n0 = 0;
+      [[maybe_unused]] float lse2 = 0.0f;
+      if constexpr (MODE == LOSS_SUMS || MODE == LOSS_DIFFS) {
+        if (r < live) t = A.rows != nullptr ? A.rows[A.row0 + r] : A.row0 + r;
+        n0 = A.v0 + o * A.bn;
+        ids.start(A, t, n0);
+        if (MODE == LOSS_DIFFS && t >= 0) lse2 = A.lse[t] * 1.44269504088896340736f;
+      }
+      [[maybe_unused]] const float by = MODE == LOSS_DW ? (A.by != nullptr ? *A.by : 1.0f) * A.dw_scale : 1.0f;
+      if (!proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      if constexpr (MODE == LOSS_SUMS) {
+        const int columns = min(A.bn, A.v0 + A.columns - n0);
+        float top = -INFINITY, base = 0.0f, total = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < columns; c += 32) {
+          float v[32];
+          tmem_ld32(sum + c, v);
+          tmem_wait_ld();
+          if (columns - c < 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = c + e < columns ? v[e] : -INFINITY;
+          }
+          while (__any_sync(FULL_MASK, ids.next < n0 + c + 32)) {
+            if (ids.next < n0 + c + 32) {
+              float z = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) z = ids.next == n0 + c + e ? v[e] : z;
+              A.picks[static_cast<int64_t>(r) * A.K + ids.at] = z;
+              ids.advance();
+            }
+          }
+          float m = v[0];
+#pragma unroll
+          for (int e = 1; e < 32; ++e) m = fmaxf(m, v[e]);
+          top = fmaxf(top, m);
+          const float now = fabsf(top) < INFINITY ? top * A.scale : 0.0f;
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            s0 += ex2_approx(fmaf(v[e], A.scale, -now));
+            s1 += ex2_approx(fmaf(v[e + 1], A.scale, -now));
+          }
+          total = (total > 0.0f ? total * ex2_approx(base - now) : total) + (s0 + s1);
+          base = now;
+        }
+        if (t >= 0) A.parts[static_cast<int64_t>(r) * A.n_tiles + o] = make_float2(base, total);
+      } else {
+        // results of 128 bytes a lane at a time
+        constexpr int COLUMNS = MODE == LOSS_DX ? 32 : 64;
+        const bool none = from == to;  // no rows, or a part without ids: nothing was added up
+#pragma unroll 1
+        for (int c = 0; c < A.bn; c += COLUMNS) {
+          float v[COLUMNS];
+#pragma unroll
+          for (int h = 0; h < COLUMNS; h += 32) tmem_ld32(sum + c + h, *reinterpret_cast<float(*)[32]>(v + h));
+          tmem_wait_ld();
+          if constexpr (MODE == LOSS_DIFFS) {
+#pragma unroll
+            for (int e = 0; e < COLUMNS; ++e) v[e] = ex2_approx(fmaf(v[e], A.scale, -lse2));
+            while (__any_sync(FULL_MASK, ids.next < n0 + c + COLUMNS)) {
+              if (ids.next < n0 + c + COLUMNS) {
+                const float q = ids.weight();
+#pragma unroll
+                for (int e = 0; e < COLUMNS; ++e) v[e] -= ids.next == n0 + c + e ? q : 0.0f;
+                ids.advance();
+              }
+            }
+            const int upto = t < 0 ? 0 : A.v0 + A.columns - n0 - c;  // zeros beyond the rows and the vocabulary
+            if (upto < COLUMNS) {
+#pragma unroll
+              for (int e = 0; e < COLUMNS; ++e) v[e] = e < upto ? v[e] : 0.0f;
+            }
+          } else if constexpr (MODE == LOSS_DW) {
+#pragma unroll
+            for (int e = 0; e < COLUMNS; ++e) v[e] = none ? 0.0f : v[e] * by;
+          } else if (none) {
+#pragma unroll
+            for (int e = 0; e < COLUMNS; ++e) v[e] = 0.0f;
+          }
+          open();
+          const uint32_t at = line();
+          if constexpr (MODE == LOSS_DX) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+              put(at, p, __float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]), __float_as_uint(v[4 * p + 3]));
+          } else {
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(v[8 * p + 2 * e], v[8 * p + 2 * e + 1]);
+                w[e] = *reinterpret_cast<const uint32_t*>(&two);
+              }
+              put(at, p, w[0], w[1], w[2], w[3]);
+            }
+          }
+          if constexpr (MODE == LOSS_DIFFS) {
+            send(o * A.bn + c, i * TILE_M + in_tile, false);
+          } else if constexpr (MODE == LOSS_DW) {
+            const int x = i * A.bn + c, y = o * TILE_M + in_tile;
+            if (x < A.H && y < A.columns) send(x, A.v0 + y, false);
+          } else {
+            const int x = o * A.bn + c;
+            if (x < A.H) send(x, split * A.rows_pad + i * TILE_M + in_tile, A.add != 0);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_remote(dsmem_addr(smem_u32(&B->freed[buf]), 0));
+        else
+          mbar_arrive(&B->freed[buf]);
+      }
+    }
+    if (lane == 0) tma_store_wait_all();
+  }
+  __syncthreads();
+  if constexpr (PAIR) {  // neither block's shared or tensor memory is given back while the other's products use it
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------------------ a teacher's tokens
+struct LossListArgs {
+  const int32_t* ids;
+  const float* teacher;
+  int32_t* sorted;      // [T][K], ascending, those that are not there last
+  float *q, *logq;      // [T][K] in that order
+  int32_t* state;       // [T]: 1 takes part, 0 left out, -1 has an id of V or more
+  float over;           // 1 / s
+  int T, V, K;
+};
+
+// A warp for each row: up to four tokens a lane, ranked by comparison with all others (equal ids by their place).
+__global__ void __launch_bounds__(128) loss_list_kernel(const __grid_constant__ LossListArgs A) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (t >= A.T) return;
+  int id[4], rank[4] = {};
+  float l[4], top = -INFINITY;
+  bool beyond = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = i * 32 + lane;
+    id[i] = k < A.K ? A.ids[t * A.K + k] : -1;
+    l[i] = k < A.K ? A.teacher[t * A.K + k] * A.over : -INFINITY;
+    if (id[i] < 0 || l[i] == -INFINITY) id[i] = LOSS_NO_ID;
+    if (id[i] != LOSS_NO_ID) {
+      beyond |= id[i] >= A.V;
+      top = max_nan(top, l[i]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
+  float p[4], total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[i] = id[i] != LOSS_NO_ID ? expf(l[i] - top) : 0.0f;
+    total += p[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(FULL_MASK, total, o);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j * 32 >= A.K) break;
+    for (int from = 0; from < 32; ++from) {
+      const int other = __shfl_sync(FULL_MASK, id[j], from), place = j * 32 + from;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rank[i] += other < id[i] || (other == id[i] && place < i * 32 + lane);
+    }
+  }
+  const float log_total = logf(total);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i * 32 + lane >= A.K) continue;
+    A.sorted[t * A.K + rank[i]] = id[i];
+    A.q[t * A.K + rank[i]] = id[i] != LOSS_NO_ID ? p[i] / total : 0.0f;
+    A.logq[t * A.K + rank[i]] = l[i] - top - log_total;
+  }
+  const bool any = __any_sync(FULL_MASK, id[0] != LOSS_NO_ID || id[1] != LOSS_NO_ID || id[2] != LOSS_NO_ID || id[3] != LOSS_NO_ID);
+  beyond = __any_sync(FULL_MASK, beyond);
+  if (lane == 0) A.state[t] = beyond ? -1 : any ? 1 : 0;
+}
+
+// ------------------------------------------------------------------------------ rows that take part
+struct LossPlanArgs {
+  const int32_t *ids, *state;  // state NULL: by the row's one id
+  const float* g;              // NULL: no gradient
+  const __nv_bfloat16* x;
+  int64_t ldx;
+  int32_t *rows, *place, *count;  // [T] both ways (place -1 and -2: left out, id of V or more), and how many
+  float* by;                      // max |g|
+  __nv_bfloat16 *copy, *scaled;   // the rows, and with a gradient also scaled by g / max |g|
+  float *loss, *lse;              // of rows that do not take part
+  __nv_bfloat16* dx;
+  int64_t lddx;
+  int T, V, H;
+};
+
+__device__ __forceinline__ int loss_state(const int32_t* ids, const int32_t* state, int64_t t, int V) {
+  if (state != nullptr) return state[t];
+  return ids[t] < 0 ? 0 : ids[t] < V ? 1 : -1;
+}
+
+// One block numbers the rows that take part in ascending order.
+__global__ void __launch_bounds__(1024) loss_plan_kernel(const __grid_constant__ LossPlanArgs A) {
+  __shared__ int sums[32];
+  __shared__ float tops[32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int each = (A.T + 1023) / 1024, from = min(A.T, static_cast<int>(threadIdx.x) * each), to = min(A.T, from + each);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto takes_part = [&](int t) { return loss_state(A.ids, A.state, t, A.V) == 1 && (A.g == nullptr || A.g[t] != 0.0f); };
+  int mine = 0;
+  float top = 0.0f;
+  for (int t = from; t < to; ++t) {
+    if (!takes_part(t)) continue;
+    ++mine;
+    if (A.g != nullptr && fabsf(A.g[t]) < INFINITY) top = fmaxf(top, fabsf(A.g[t]));
+  }
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL_MASK, before, o);
+    if (lane >= o) before += v;
+    top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+  }
+  if (lane == 31) sums[warp] = before;
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+  int all = sums[lane];
+  top = tops[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL_MASK, all, o);
+    if (lane >= o) all += v;
+    top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+  }
+  int r = before - mine + (warp > 0 ? __shfl_sync(FULL_MASK, all, max(warp - 1, 0)) : 0);
+  for (int t = from; t < to; ++t) {
+    if (takes_part(t)) {
+      A.rows[r] = t;
+      A.place[t] = r++;
+    } else {
+      A.place[t] = loss_state(A.ids, A.state, t, A.V) < 0 ? -2 : -1;
+    }
+  }
+  if (threadIdx.x == 31) {
+    *A.count = all;
+    if (A.by != nullptr) *A.by = top > 0.0f ? top : 1.0f;
+  }
+}
+
+// A block for each row: copies of those that take part, results of the others.  The last 256 blocks write the rows of
+// zeros behind the last one, up to the end of its tile.
+__global__ void __launch_bounds__(128) loss_gather_kernel(const __grid_constant__ LossPlanArgs A) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int packs = A.H / 8;
+  int64_t r;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  if (static_cast<int>(blockIdx.x) >= A.T) {
+    const int count = *A.count;
+    r = static_cast<int64_t>(count) + blockIdx.x - A.T;
+    if (r >= (count + 255) / 256 * 256) return;
+    for (int i = threadIdx.x; i < packs; i += 128) {
+      reinterpret_cast<uint4*>(A.copy + r * A.H)[i] = zero;
+      if (A.scaled != nullptr) reinterpret_cast<uint4*>(A.scaled + r * A.H)[i] = zero;
+    }
+    return;
+  }
+  const int64_t t = blockIdx.x;
+  r = A.place[t];
+  if (r < 0) {
+    if (threadIdx.x == 0 && A.loss != nullptr) A.loss[t] = r == -2 ? NAN : 0.0f;
+    if (threadIdx.x == 0 && A.g == nullptr && A.lse != nullptr) A.lse[t] = r == -2 ? NAN : 0.0f;
+    if (A.dx != nullptr)
+      for (int i = threadIdx.x; i < packs; i += 128) reinterpret_cast<uint4*>(A.dx + t * A.lddx)[i] = zero;
+    return;
+  }
+  const float by = A.g != nullptr ? A.g[t] / *A.by : 1.0f;
+  for (int i = threadIdx.x; i < packs; i += 128) {
+    Pack<__nv_bfloat16, 8> v = reinterpret_cast<const Pack<__nv_bfloat16, 8>*>(A.x + t * A.ldx)[i];
+    reinterpret_cast<Pack<__nv_bfloat16, 8>*>(A.copy + r * A.H)[i] = v;
+    if (A.scaled != nullptr) {
+      float f[8];
+      unpack(v, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] *= by;
+      reinterpret_cast<Pack<__nv_bfloat16, 8>*>(A.scaled + r * A.H)[i] = pack<__nv_bfloat16>(f);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ results
+struct LossJoinArgs {
+  const int32_t *count, *rows, *ids, *state;
+  const float *q, *logq, *picks;
+  const float2* parts;
+  float *loss, *lse;
+  float s;
+  int T, V, K, row0, n_tiles;
+};
+
+// A block for each row: the tiles' sums together, and the loss.
+__global__ void __launch_bounds__(128) loss_join_kernel(const __grid_constant__ LossJoinArgs A) {
+  __shared__ float joined[4][2];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t r = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (A.count != nullptr && A.row0 + r >= *A.count) return;
+  const int64_t t = A.rows != nullptr ? A.rows[A.row0 + r] : A.row0 + r;
+  const int state = loss_state(A.ids, A.state, t, A.V);
+  if (state != 1) {
+    if (threadIdx.x == 0) A.loss[t] = A.lse[t] = state < 0 ? NAN : 0.0f;
+    return;
+  }
+  // sums of nothing but exp(-inf) say nothing of their exponent
+  const float2* parts = A.parts + r * A.n_tiles;
+  float top = -INFINITY;
+  for (int i = threadIdx.x; i < A.n_tiles; i += 128)
+    if (parts[i].y != 0.0f) top = fmaxf(top, parts[i].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+  if (lane == 0) joined[warp][0] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(joined[0][0], joined[1][0]), fmaxf(joined[2][0], joined[3][0]));
+  float total = 0.0f;
+  for (int i = threadIdx.x; i < A.n_tiles; i += 128)
+    if (parts[i].y != 0.0f) total += parts[i].y * ex2_approx(parts[i].x - top);
+  total = warp_sum(total);
+  if (lane == 0) joined[warp][1] = total;
+  __syncthreads();
+  if (warp > 0) return;
+  total = (joined[0][1] + joined[1][1]) + (joined[2][1] + joined[3][1]);
+  const float lse = total > 0.0f || total != total ? top * 0.693147180559945309417f + logf(total) : -INFINITY;
+  float loss = 0.0f;
+  if (A.q == nullptr) {
+    loss = lse - A.picks[r];
+  } else {
+    for (int k = lane; k < A.K; k += 32) {
+      const float q = A.q[t * A.K + k];
+      if (q != 0.0f) loss += q * (A.logq[t * A.K + k] - (A.picks[r * A.K + k] / A.s - lse));
+    }
+    loss = warp_sum(loss) * A.s * A.s;
+  }
+  if (lane == 0) {
+    A.loss[t] = loss;
+    A.lse[t] = lse;
+  }
+}
+
+struct LossDxArgs {
+  const int32_t *count, *rows;
+  const float *parts, *g;
+  __nv_bfloat16* dx;
+  int64_t lddx, part;  // elements from one part to the next
+  float s;
+  int H, splits;
+};
+
+// A block for each row: dx from its parts, added up in order.
+__global__ void __launch_bounds__(128) loss_dx_kernel(const __grid_constant__ LossDxArgs A) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t r = blockIdx.x;
+  if (r >= *A.count) return;
+  const int64_t t = A.rows[r];
+  const float by = A.g[t] * A.s;
+  for (int i = threadIdx.x; i < A.H / 8; i += 128) {
+    float f[8] = {};
+    for (int p = 0; p < A.splits; ++p) {
+      const float4* at = reinterpret_cast<const float4*>(A.parts + p * A.part + r * A.H) + 2 * i;
+      const float4 a = at[0], b = at[1];
+      f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
+      f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= by;
+    reinterpret_cast<Pack<__nv_bfloat16, 8>*>(A.dx + t * A.lddx)[i] = pack<__nv_bfloat16>(f);
+  }
+}
+
+// dw of no rows.
+__global__ void __launch_bounds__(256) loss_zero_kernel(__nv_bfloat16* dw, int64_t lddw, int H) {
+  grid_dep_wait();
+  grid_dep_launch();
+  uint4* to = reinterpret_cast<uint4*>(dw + blockIdx.x * lddw);
+  for (int i = threadIdx.x; i < H / 8; i += 256) to[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+}  // namespace strata

@@ -1,4 +1,4 @@
-// tail_binding.cpp -- Python calls of include/strata_tail.h on PyTorch tensors.
+// tail_binding.cpp -- Python calls of include/strata_tail.h and include/strata_train.h on PyTorch tensors.
 //
 // Checks what the C ABI cannot see (types, shapes, devices of tensors), allocates the outputs that the
 // caller left out, and makes the C call on the tensors' addresses without holding the interpreter's lock.
@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/strata_tail.h"
+#include "../../include/strata_train.h"
 
 namespace {
 
@@ -270,13 +271,204 @@ TAIL_CALL(draw) {
   return done(rc, out);
 }
 
+const Tensor* given(const Tensor& t) { return t.defined() ? &t : nullptr; }
+
+// An output: the caller's from `out`, or a new one that is put there, or none.
+Tensor output(PyObject* out, const char* key, PyObject* wanted, at::IntArrayRef shape, ScalarType type, const Tensor& like) {
+  PyObject* had = PyDict_GetItemString(out, key);
+  if (had != nullptr && had != Py_None) return needed(had, key);
+  if (wanted != Py_True) return Tensor();
+  Tensor made = fresh(shape, type, like);
+  put(out, key, made);
+  return made;
+}
+
+// The caller's workspace, or (`allocate`) a new one.
+void* workspace_of(PyObject* o, PyObject* allocate, int64_t need, const Tensor& like, int device, int64_t& bytes, Tensor& hold) {
+  const Tensor* had = tensor(o, "workspace");
+  if (had != nullptr) {
+    bytes = had->numel();
+    return dense(had, "workspace", {bytes}, at::kByte, device);
+  }
+  if (allocate != Py_True || need <= 0) return nullptr;
+  bytes = need;
+  hold = fresh({need}, at::kByte, like);
+  return hold.data_ptr();
+}
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused();
+  return v;
+}
+
+void dictionary(PyObject* o) {
+  if (!PyDict_Check(o)) refuse(PyExc_TypeError, "out", "must be a dict");
+}
+
+// (x, weight, bias, residual, eps, want residual, want y, want mean and rstd, out, stream) -> out, a dict
+TAIL_CALL(layer_norm) {
+  arguments(n, 10);
+  const Tensor &x = needed(a[0], "x"), &weight = needed(a[1], "weight");
+  const Tensor *bias = tensor(a[2], "bias"), *residual = tensor(a[3], "residual");
+  const double eps = number(a[4]);
+  const ScalarType type = x.scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16) refuse(PyExc_TypeError, "x", "must be float32 or bfloat16");
+  const int device = call_device(x, "x");
+  const int64_t T = x.size(0), H = x.size(1);
+  PyObject* out = a[8];
+  dictionary(out);
+  const Tensor ro = output(out, "residual", a[5], {T, H}, type, x), y = output(out, "y", a[6], {T, H}, type, x),
+               mean = output(out, "mean", a[7], {T}, at::kFloat, x), rstd = output(out, "rstd", a[7], {T}, at::kFloat, x);
+  const Rows rx = rows(&x, "x", T, H, type, device), rr = rows(residual, "residual", T, H, type, device),
+             rro = rows(given(ro), "residual", T, H, type, device), ry = rows(given(y), "y", T, H, type, device);
+  void *pw = dense(&weight, "weight", {H}, type, device), *pb = dense(bias, "bias", {H}, type, device),
+       *pm = dense(given(mean), "mean", {T}, at::kFloat, device), *ps = dense(given(rstd), "rstd", {T}, at::kFloat, device);
+  void* stream = stream_of(a[9], device);
+  const int t32 = narrow(T, "T"), h32 = narrow(H, "H");
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = strata_layer_norm_rows(rx.p, rx.ld, rr.p, rr.ld, pw, pb, type == at::kFloat ? STRATA_DTYPE_F32 : STRATA_DTYPE_BF16, t32, h32,
+                              static_cast<float>(eps), rro.p, rro.ld, ry.p, ry.ld, static_cast<float*>(pm), static_cast<float*>(ps),
+                              stream);
+  Py_END_ALLOW_THREADS
+  Py_INCREF(out);
+  return done(rc, out);
+}
+
+// (dy, x, weight, mean, rstd, dresidual, want dx, want dweight, want dbias, out, workspace, allocate it, stream) -> out, a dict
+TAIL_CALL(layer_norm_grad) {
+  arguments(n, 13);
+  const Tensor &dy = needed(a[0], "dy"), &x = needed(a[1], "x"), &weight = needed(a[2], "weight"), &mean = needed(a[3], "mean"),
+               &rstd = needed(a[4], "rstd");
+  const Tensor* dresidual = tensor(a[5], "dresidual");
+  const ScalarType type = x.scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16) refuse(PyExc_TypeError, "x", "must be float32 or bfloat16");
+  const int device = call_device(x, "x");
+  const int64_t T = x.size(0), H = x.size(1);
+  PyObject* out = a[9];
+  dictionary(out);
+  const Tensor dx = output(out, "dx", a[6], {T, H}, type, x), dweight = output(out, "dweight", a[7], {H}, type, x),
+               dbias = output(out, "dbias", a[8], {H}, type, x);
+  const Rows rdy = rows(&dy, "dy", T, H, type, device), rx = rows(&x, "x", T, H, type, device),
+             rdr = rows(dresidual, "dresidual", T, H, type, device), rdx = rows(given(dx), "dx", T, H, type, device);
+  void *pw = dense(&weight, "weight", {H}, type, device), *pm = dense(&mean, "mean", {T}, at::kFloat, device),
+       *ps = dense(&rstd, "rstd", {T}, at::kFloat, device), *pdw = dense(given(dweight), "dweight", {H}, type, device),
+       *pdb = dense(given(dbias), "dbias", {H}, type, device);
+  const int t32 = narrow(T, "T"), h32 = narrow(H, "H");
+  int64_t bytes = 0;
+  Tensor hold;
+  void* ws = workspace_of(a[10], pdw != nullptr || pdb != nullptr ? a[11] : Py_False, strata_layer_norm_workspace(t32, h32), x, device, bytes, hold);
+  void* stream = stream_of(a[12], device);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = strata_layer_norm_grad(rdy.p, rdy.ld, rx.p, rx.ld, pw, static_cast<float*>(pm), static_cast<float*>(ps), rdr.p, rdr.ld,
+                              type == at::kFloat ? STRATA_DTYPE_F32 : STRATA_DTYPE_BF16, t32, h32, rdx.p, rdx.ld, pdw, pdb, ws, bytes, stream);
+  Py_END_ALLOW_THREADS
+  Py_INCREF(out);
+  return done(rc, out);
+}
+
+// The rows, the head and the tokens of a loss.
+struct LossOperands {
+  Rows x, w;
+  int T = 0, V = 0, H = 0, K = 0;
+  int32_t* ids = nullptr;
+  float* teacher = nullptr;
+};
+LossOperands loss_operands(const Tensor& x, const Tensor& w, const Tensor& ids, const Tensor* teacher, int& device) {
+  device = call_device(x, "x");
+  if (w.dim() != 2) refuse(PyExc_ValueError, "w", "must be [ids, width]");
+  const int64_t T = x.size(0), H = x.size(1), V = w.size(0);
+  LossOperands o;
+  o.x = rows(&x, "x", T, H, at::kBFloat16, device);
+  o.w = rows(&w, "w", V, H, at::kBFloat16, device);
+  if (T == 1) o.x.ld = (H + 7) / 8 * 8;  // the stride of one row means nothing
+  if (V == 1) o.w.ld = (H + 7) / 8 * 8;
+  if (teacher != nullptr) {
+    if (teacher->dim() != 2) refuse(PyExc_ValueError, "teacher", "must be [rows, tokens]");
+    const int64_t K = teacher->size(1);
+    o.K = narrow(K, "K");
+    o.teacher = static_cast<float*>(dense(teacher, "teacher", {T, K}, at::kFloat, device));
+    o.ids = static_cast<int32_t*>(dense(&ids, "ids", {T, K}, at::kInt, device));
+  } else {
+    o.ids = static_cast<int32_t*>(dense(&ids, "ids", {T}, at::kInt, device));
+  }
+  o.T = narrow(T, "T");
+  o.V = narrow(V, "V");
+  o.H = narrow(H, "H");
+  return o;
+}
+
+// (x, w, ids, teacher or None, temperature, want loss and lse, out, workspace, allocate it, stream) -> out, a dict
+TAIL_CALL(loss) {
+  arguments(n, 10);
+  const Tensor &x = needed(a[0], "x"), &w = needed(a[1], "w"), &ids = needed(a[2], "ids");
+  const Tensor* teacher = tensor(a[3], "teacher");
+  const float temperature = static_cast<float>(number(a[4]));
+  if (x.scalar_type() != at::kBFloat16) refuse(PyExc_TypeError, "x", "must be bfloat16");
+  int device;
+  const LossOperands o = loss_operands(x, w, ids, teacher, device);
+  PyObject* out = a[6];
+  dictionary(out);
+  const Tensor loss = output(out, "loss", a[5], {o.T}, at::kFloat, x), lse = output(out, "lse", a[5], {o.T}, at::kFloat, x);
+  float *pl = static_cast<float*>(dense(given(loss), "loss", {o.T}, at::kFloat, device)),
+        *pe = static_cast<float*>(dense(given(lse), "lse", {o.T}, at::kFloat, device));
+  int64_t bytes = 0;
+  Tensor hold;
+  void* ws = workspace_of(a[7], a[8], strata_loss_workspace(o.T, o.V, o.H, o.K, 0), x, device, bytes, hold);
+  void* stream = stream_of(a[9], device);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = teacher != nullptr ? strata_distill_rows(o.x.p, o.x.ld, o.w.p, o.w.ld, o.T, o.V, o.H, o.K, o.ids, o.teacher, temperature, pl, pe, ws, bytes, stream)
+                          : strata_cross_entropy_rows(o.x.p, o.x.ld, o.w.p, o.w.ld, o.T, o.V, o.H, o.ids, pl, pe, ws, bytes, stream);
+  Py_END_ALLOW_THREADS
+  Py_INCREF(out);
+  return done(rc, out);
+}
+
+// (x, w, ids, teacher or None, temperature, lse, g, want dx, want dw, out, workspace, allocate it, stream) -> out, a dict
+TAIL_CALL(loss_grad) {
+  arguments(n, 13);
+  const Tensor &x = needed(a[0], "x"), &w = needed(a[1], "w"), &ids = needed(a[2], "ids"), &lse = needed(a[5], "lse"), &g = needed(a[6], "g");
+  const Tensor* teacher = tensor(a[3], "teacher");
+  const float temperature = static_cast<float>(number(a[4]));
+  if (x.scalar_type() != at::kBFloat16) refuse(PyExc_TypeError, "x", "must be bfloat16");
+  int device;
+  const LossOperands o = loss_operands(x, w, ids, teacher, device);
+  float *pe = static_cast<float*>(dense(&lse, "lse", {o.T}, at::kFloat, device)), *pg = static_cast<float*>(dense(&g, "g", {o.T}, at::kFloat, device));
+  PyObject* out = a[9];
+  dictionary(out);
+  const Tensor dx = output(out, "dx", a[7], {o.T, o.H}, at::kBFloat16, x), dw = output(out, "dw", a[8], {o.V, o.H}, at::kBFloat16, x);
+  Rows rdx = rows(given(dx), "dx", o.T, o.H, at::kBFloat16, device), rdw = rows(given(dw), "dw", o.V, o.H, at::kBFloat16, device);
+  if (o.T == 1) rdx.ld = o.x.ld;
+  if (o.V == 1) rdw.ld = o.w.ld;
+  int64_t bytes = 0;
+  Tensor hold;
+  void* ws = workspace_of(a[10], a[11], strata_loss_workspace(o.T, o.V, o.H, o.K, 1), x, device, bytes, hold);
+  void* stream = stream_of(a[12], device);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = teacher != nullptr ? strata_distill_grad(o.x.p, o.x.ld, o.w.p, o.w.ld, o.T, o.V, o.H, o.K, o.ids, o.teacher, temperature, pe, pg, rdx.p, rdx.ld,
+                                                rdw.p, rdw.ld, ws, bytes, stream)
+                          : strata_cross_entropy_grad(o.x.p, o.x.ld, o.w.p, o.w.ld, o.T, o.V, o.H, o.ids, pe, pg, rdx.p, rdx.ld, rdw.p, rdw.ld, ws,
+                                                      bytes, stream);
+  Py_END_ALLOW_THREADS
+  Py_INCREF(out);
+  return done(rc, out);
+}
+
 PyMethodDef methods[] = {
     {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm)), METH_FASTCALL, nullptr},
     {"project", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(project)), METH_FASTCALL, nullptr},
     {"draw", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(draw)), METH_FASTCALL, nullptr},
+    {"layer_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(layer_norm)), METH_FASTCALL, nullptr},
+    {"layer_norm_grad", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(layer_norm_grad)), METH_FASTCALL, nullptr},
+    {"loss", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(loss)), METH_FASTCALL, nullptr},
+    {"loss_grad", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(loss_grad)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_strata_tail", "Calls of strata_tail.h on PyTorch tensors.", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_strata_tail", "Calls of strata_tail.h and strata_train.h on PyTorch tensors.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -49,6 +49,7 @@ _declare()
 def _load_module() -> None:
     """Load the compiled half of this binding (csrc/tail_binding.cpp) at the first call of an operator: the rest of
     the package does not need it, nor PyTorch.  Like the library that it calls, it has to be built."""
+    global _module
     global _norm, _project, _draw
     from importlib.machinery import ExtensionFileLoader
     from importlib.util import module_from_spec, spec_from_loader
@@ -60,6 +61,17 @@ def _load_module() -> None:
     module = module_from_spec(spec_from_loader("_strata_tail", loader))
     loader.exec_module(module)
     _norm, _project, _draw = module.norm, module.project, module.draw
+    _module = module
+
+
+_module = None
+
+
+def _compiled():
+    """The compiled module, loaded."""
+    if _module is None:
+        _load_module()
+    return _module
 
 
 def _norm(*args):
