@@ -54,6 +54,7 @@ int grad_groups(int T, int H) {
   return std::min((T + strata::LAYER_NORM_GRAD_WARPS - 1) / strata::LAYER_NORM_GRAD_WARPS, SMS * 4);
 }
 
+// Narrow rows by warps; wider ones that do not lie on 16 bytes by a block, element by element.
 template <typename E, int N, int PER>
 cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, void* stream) {
   if constexpr (N * PER <= 16) {
@@ -63,8 +64,25 @@ cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, void*
       return strata::Launch(A.groups, 32 * strata::LAYER_NORM_GRAD_WARPS, static_cast<size_t>(A.H) * 8, stream, overlaps)(
           strata::layer_norm_grad_kernel<E, N, PER, false>, A);
     }
-    if (need > strata::LAYER_NORM_GRAD_THREADS) return launch_rows<E, N, PER * 2>(A, overlaps, stream);
-    return strata::Launch(A.groups, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::layer_norm_grad_kernel<E, N, PER, true>, A);
+    if (need > strata::layer_norm_grad_most_threads(N, PER)) return launch_rows<E, N, PER * 2>(A, overlaps, stream);
+    if constexpr (N == 1)
+      return strata::Launch(A.groups, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::layer_norm_grad_kernel<E, N, PER, true>, A);
+  }
+  return cudaErrorInvalidValue;  // not reached: wider rows have their own kernels
+}
+
+// Rows on 16 bytes by a block: as many rows on their way as an SM's shared memory has room for beside its other blocks.
+template <typename E, int PER>
+cudaError_t launch_ring(strata::LayerNormGradArgs A, bool overlaps, void* stream) {
+  constexpr int N = 16 / static_cast<int>(sizeof(E)), SM_BYTES = 220 * 1024;
+  if constexpr (N * PER <= 16) {
+    const int need = (A.H / N + PER - 1) / PER;
+    if (need > strata::LAYER_NORM_GRAD_THREADS) return launch_ring<E, PER * 2>(A, overlaps, stream);
+    const int row = A.H * static_cast<int>(sizeof(E)) * (A.dresidual != nullptr ? 3 : 2), blocks = std::max(1, (A.groups + SMS - 1) / SMS);
+    A.depth = std::max(1, std::min(strata::LAYER_NORM_RING, (SM_BYTES / blocks - 2048) / row));
+    const auto kernel = strata::layer_norm_ring_kernel<E, PER>;
+    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES); e != cudaSuccess) return e;
+    return strata::Launch(A.groups, (need + 31) / 32 * 32, static_cast<size_t>(A.depth) * row, stream, overlaps)(kernel, A);
   } else {
     return cudaErrorInvalidValue;  // not reached: wider rows have their own kernels
   }
@@ -76,7 +94,9 @@ cudaError_t launch_grad(const strata::LayerNormGradArgs& A, bool packed, bool ov
   cudaError_t e = cudaSuccess;
   if (A.T > 0) {
     if (A.H <= BLOCK_WIDTH) {
-      e = packed ? launch_rows<E, N, 1>(A, overlaps, stream) : launch_rows<E, 1, 1>(A, overlaps, stream);
+      e = !packed               ? launch_rows<E, 1, 1>(A, overlaps, stream)
+          : A.H > WARP_WIDTH ? launch_ring<E, 1>(A, overlaps, stream)
+                             : launch_rows<E, N, 1>(A, overlaps, stream);
       overlaps = true;
     } else {  // the sums first: dx may be dy or x
       if (A.part != nullptr) {
@@ -92,7 +112,7 @@ cudaError_t launch_grad(const strata::LayerNormGradArgs& A, bool packed, bool ov
     }
   }
   if (e != cudaSuccess || A.part == nullptr) return e;
-  return strata::Launch((A.H + 31) / 32, 256, 0, stream, overlaps)(strata::layer_norm_sum_kernel<E>, A);
+  return strata::Launch((A.H + 31) / 32, 1024, 0, stream, overlaps)(strata::layer_norm_sum_kernel<E>, A);
 }
 
 }  // namespace
@@ -171,8 +191,8 @@ extern "C" int strata_layer_norm_grad(const void* dy, int64_t lddy, const void* 
   packs.look(dx, lddx);
   // without rows the sums are those of no groups; the workspace is not touched
   float* part = !sums ? nullptr : T > 0 ? static_cast<float*>(workspace) : static_cast<float*>(dweight != nullptr ? dweight : dbias);
-  const strata::LayerNormGradArgs A{dy, x, weight, dresidual, mean, rstd, dx, dweight, dbias, part, lddy, ldx, lddr, lddx, T, H,
-                                    T > 0 ? grad_groups(T, H) : 0};
+  const strata::LayerNormGradArgs A{dy, x, weight, dresidual, mean, rstd, dx, dweight, dbias, part, errors, lddy, ldx, lddr, lddx, T, H,
+                                    T > 0 ? grad_groups(T, H) : 0, 0};
   const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
     return dtype == STRATA_DTYPE_F32 ? launch_grad<float>(A, packs.all, overlaps, stream)
                                      : launch_grad<__nv_bfloat16>(A, packs.all, overlaps, stream);

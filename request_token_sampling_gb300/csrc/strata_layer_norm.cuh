@@ -22,10 +22,43 @@ struct LayerNormArgs {
 
 __host__ __device__ constexpr int layer_norm_most_threads(int n, int per) { return n * per > 8 ? 512 : 1024; }  // by registers
 
+// The joins of a row's sum and of its squared differences.  Each warp takes both about its own mean, by shuffles, and the
+// warps' come together behind one barrier: the squares about the row's mean are the warps' and, for each warp, its elements times
+// the square of what the means differ by.  `mine`: this warp's elements.
+template <bool BLOCK>
+__device__ __forceinline__ float layer_norm_mean(float s, int mine) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  return mine > 0 ? s / static_cast<float>(mine) : 0.0f;
+}
+template <bool BLOCK>
+__device__ __forceinline__ void layer_norm_join(float& mean, float& squares, int mine, int H, float (*part)[32]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(0xFFFFFFFFu, squares, o);
+  if constexpr (BLOCK) {
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) {
+      part[0][threadIdx.x >> 5] = mean;
+      part[1][threadIdx.x >> 5] = squares;
+      part[2][threadIdx.x >> 5] = static_cast<float>(mine);
+    }
+    __syncthreads();
+    const float m = lane < warps ? part[0][lane] : 0.0f, n = lane < warps ? part[2][lane] : 0.0f;
+    mean = m * n;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mean += __shfl_xor_sync(0xFFFFFFFFu, mean, o);
+    mean /= static_cast<float>(H);
+    const float d = m - mean;
+    squares = lane < warps ? fmaf(n * d, d, part[1][lane]) : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(0xFFFFFFFFu, squares, o);
+  }
+}
+
 // PER packs of N elements in each thread of a warp (BLOCK false: a row for each warp) or of the block.
 template <typename E, int N, int PER, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? layer_norm_most_threads(N, PER) : 128) layer_norm_kernel(const __grid_constant__ LayerNormArgs A) {
-  __shared__ float part[2][32];
+  __shared__ float part[3][32];
   grid_dep_wait();
   grid_dep_launch();
   const int threads = BLOCK ? blockDim.x : 32, me = BLOCK ? threadIdx.x : threadIdx.x & 31;
@@ -47,16 +80,20 @@ __global__ void __launch_bounds__(BLOCK ? layer_norm_most_threads(N, PER) : 128)
       if (A.residual != nullptr) pr[i] = r[at(i)];
     }
   }
+  // few rows ask for the weight at once; many find it in the caches when they need it, and their registers hold more rows on an SM
+  constexpr bool EARLY = PER == 1;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (at(i) < packs && A.y != nullptr) {
+    if (EARLY && at(i) < packs && A.y != nullptr) {
       pw[i] = w[at(i)];
       if (A.bias != nullptr) pb[i] = b[at(i)];
     }
   }
   float h[PER][N] = {}, s = 0.0f;
+  int mine = 0;  // elements of this warp
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
+    mine += max(0, min(32, packs - (at(i) - (me & 31)))) * N;
     if (at(i) >= packs) continue;
     unpack(px[i], h[i]);
     if (A.residual != nullptr) {
@@ -71,18 +108,18 @@ __global__ void __launch_bounds__(BLOCK ? layer_norm_most_threads(N, PER) : 128)
 #pragma unroll
     for (int e = 0; e < N; ++e) s += h[i][e];
   }
-  const float mean = norm_join<false, BLOCK>(s, part[0]) / static_cast<float>(A.H);
-  float ss = 0.0f;
+  float mean = layer_norm_mean<BLOCK>(s, mine), ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     if (at(i) >= packs) continue;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      h[i][e] -= mean;
-      ss = fmaf(h[i][e], h[i][e], ss);
+      const float d = h[i][e] - mean;
+      ss = fmaf(d, d, ss);
     }
   }
-  const float rstd = 1.0f / sqrtf(norm_join<false, BLOCK>(ss, part[1]) / static_cast<float>(A.H) + A.eps);
+  layer_norm_join<BLOCK>(mean, ss, mine, A.H, part);
+  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(A.H) + A.eps);
   if (me == 0) {
     if (A.mean != nullptr) A.mean[t] = mean;
     if (A.rstd != nullptr) A.rstd[t] = rstd;
@@ -92,10 +129,10 @@ __global__ void __launch_bounds__(BLOCK ? layer_norm_most_threads(N, PER) : 128)
   for (int i = 0; i < PER; ++i) {
     if (at(i) >= packs) continue;
     float f[N], c[N] = {};
-    unpack(pw[i], f);
-    if (A.bias != nullptr) unpack(pb[i], c);
+    unpack(EARLY ? pw[i] : w[at(i)], f);
+    if (A.bias != nullptr) unpack(EARLY ? pb[i] : b[at(i)], c);
 #pragma unroll
-    for (int e = 0; e < N; ++e) h[i][e] = fmaf(h[i][e] * rstd, f[e], c[e]);
+    for (int e = 0; e < N; ++e) h[i][e] = fmaf((h[i][e] - mean) * rstd, f[e], c[e]);
     y[at(i)] = pack<E>(h[i]);
   }
 }
@@ -138,8 +175,9 @@ struct LayerNormGradArgs {
   const float *mean, *rstd;
   void *dx, *dweight, *dbias;
   float* part;  // [groups][2][H]: sums of dy v and of dy over a group of rows
+  uint32_t* errors;
   int64_t lddy, ldx, lddr, lddx;
-  int T, H, groups;
+  int T, H, groups, depth;  // depth: rows on their way at a time (layer_norm_ring_kernel)
 };
 
 // Joins two sums over the threads of a row.  `part` holds two floats for each warp; rows take turns with two of them, so
@@ -167,12 +205,13 @@ __device__ __forceinline__ void layer_norm_join2(float& a, float& b, float2* par
 }
 
 constexpr int LAYER_NORM_GRAD_THREADS = 512, LAYER_NORM_GRAD_WARPS = 8;
+__host__ __device__ constexpr int layer_norm_grad_most_threads(int n, int per) { return n * per > 8 ? LAYER_NORM_GRAD_THREADS : 704; }  // by registers
 
 // Rows b, b + groups, ... of a block (BLOCK), or of its warps one after another (eight rows of it at a time): a
 // thread has the same columns of all of them, so the sums over rows stay in its registers, in 32 bits.  The
 // next row is on its way while this one's sums are joined.
 template <typename E, int N, int PER, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? LAYER_NORM_GRAD_THREADS : 32 * LAYER_NORM_GRAD_WARPS) layer_norm_grad_kernel(const __grid_constant__ LayerNormGradArgs A) {
+__global__ void __launch_bounds__(BLOCK ? layer_norm_grad_most_threads(N, PER) : 32 * LAYER_NORM_GRAD_WARPS) layer_norm_grad_kernel(const __grid_constant__ LayerNormGradArgs A) {
   __shared__ float2 part[2][32];
   extern __shared__ float sums[];  // warps alone: [2][H]
   grid_dep_wait();
@@ -183,7 +222,7 @@ __global__ void __launch_bounds__(BLOCK ? LAYER_NORM_GRAD_THREADS : 32 * LAYER_N
   const int first = BLOCK ? blockIdx.x : blockIdx.x * LAYER_NORM_GRAD_WARPS + warp, step = BLOCK ? gridDim.x : gridDim.x * LAYER_NORM_GRAD_WARPS;
   auto at = [&](int i) { return i * threads + me; };
   auto row = [&](const void* p, int64_t ld, int64_t t) { return reinterpret_cast<const P*>(static_cast<const E*>(p) + t * ld); };
-  P pw[PER], pdy[PER], px[PER], pdr[PER];
+  P pdy[PER], px[PER], pdr[PER];
   float dw[PER][N] = {}, db[PER][N] = {}, mean = 0.0f, rstd = 0.0f;
   auto load = [&](int64_t t) {
 #pragma unroll
@@ -196,9 +235,6 @@ __global__ void __launch_bounds__(BLOCK ? LAYER_NORM_GRAD_THREADS : 32 * LAYER_N
     mean = A.mean[t];
     rstd = A.rstd[t];
   };
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (at(i) < packs) pw[i] = static_cast<const P*>(A.weight)[at(i)];
   if (first < A.T) load(first);
   int turn = 0;
   for (int64_t t = first; t < A.T; t += step, turn ^= 1) {
@@ -209,7 +245,7 @@ __global__ void __launch_bounds__(BLOCK ? LAYER_NORM_GRAD_THREADS : 32 * LAYER_N
     for (int i = 0; i < PER; ++i) {
       if (at(i) >= packs) continue;
       float w[N];
-      unpack(pw[i], w);
+      unpack(static_cast<const P*>(A.weight)[at(i)], w);  // from the nearest cache, for the registers' sake
       unpack(pdy[i], a[i]);
       unpack(px[i], v[i]);
       dr[i] = pdr[i];
@@ -271,6 +307,110 @@ __global__ void __launch_bounds__(BLOCK ? LAYER_NORM_GRAD_THREADS : 32 * LAYER_N
   }
 }
 
+// Rows on 16 bytes, too wide for a warp: as above, by a block, but the rows to come are on their way to shared memory, as bulk
+// copies, `depth` of them ahead.  A row's copies start when every thread has read the one that had its place, which the
+// join's barrier tells.
+constexpr int LAYER_NORM_RING = 16;
+constexpr uint32_t LAYER_NORM_SPINS = 1u << 22;
+template <typename E, int PER>
+__global__ void __launch_bounds__(LAYER_NORM_GRAD_THREADS) layer_norm_ring_kernel(const __grid_constant__ LayerNormGradArgs A) {
+  constexpr int N = 16 / static_cast<int>(sizeof(E));
+  __shared__ float2 part[2][32];
+  __shared__ uint64_t full[LAYER_NORM_RING];
+  extern __shared__ __align__(16) uint8_t rows[];  // [depth][dy, x, dresidual][H]
+  using P = Pack<E, N>;
+  const int packs = A.H / N, me = threadIdx.x, threads = blockDim.x, step = gridDim.x;
+  const uint32_t bytes = static_cast<uint32_t>(A.H) * sizeof(E), tensors = A.dresidual != nullptr ? 3 : 2;
+  if (me == 0) {
+    for (int i = 0; i < A.depth; ++i) mbar_init(&full[i], 1);
+    fence_proxy_async_smem();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+  auto fetch = [&](int64_t t, int slot) {
+    uint8_t* to = rows + static_cast<size_t>(slot) * tensors * bytes;
+    mbar_arrive_expect_tx(&full[slot], tensors * bytes);
+    bulk_g2s(to, static_cast<const E*>(A.dy) + t * A.lddy, bytes, &full[slot]);
+    bulk_g2s(to + bytes, static_cast<const E*>(A.x) + t * A.ldx, bytes, &full[slot]);
+    if (A.dresidual != nullptr) bulk_g2s(to + 2 * bytes, static_cast<const E*>(A.dresidual) + t * A.lddr, bytes, &full[slot]);
+  };
+  if (me == 0)
+    for (int i = 0; i < A.depth && blockIdx.x + static_cast<int64_t>(i) * step < A.T; ++i) fetch(blockIdx.x + static_cast<int64_t>(i) * step, i);
+  auto at = [&](int i) { return i * threads + me; };
+  P pw[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (at(i) < packs) pw[i] = static_cast<const P*>(A.weight)[at(i)];
+  float dw[PER][N] = {}, db[PER][N] = {};
+  int slot = 0, turn = 0;
+  uint32_t phase = 0;
+  float mean = blockIdx.x < A.T ? A.mean[blockIdx.x] : 0.0f, rstd = blockIdx.x < A.T ? A.rstd[blockIdx.x] : 0.0f;
+  for (int64_t t = blockIdx.x; t < A.T; t += step, turn ^= 1) {
+    // copies that do not arrive leave the results without meaning; all waits end, and so does the kernel
+    uint32_t spin = 0;
+    while (!mbar_try_wait(&full[slot], phase) && ++spin < LAYER_NORM_SPINS) {
+    }
+    if (spin >= LAYER_NORM_SPINS) atomicOr(A.errors, 0x08u);  // STRATA_DEVERR_TIMEOUT
+    const P* in = reinterpret_cast<const P*>(rows + static_cast<size_t>(slot) * tensors * bytes);
+    float a[PER][N], v[PER][N], sa = 0.0f, sav = 0.0f;
+    P dr[PER];
+    const float scale = rstd;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (at(i) >= packs) continue;
+      float w[N];
+      unpack(pw[i], w);
+      unpack(in[at(i)], a[i]);
+      unpack(in[packs + at(i)], v[i]);
+      if (A.dresidual != nullptr) dr[i] = in[2 * packs + at(i)];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        v[i][e] = (v[i][e] - mean) * rstd;
+        dw[i][e] = fmaf(a[i][e], v[i][e], dw[i][e]);
+        db[i][e] += a[i][e];
+        a[i][e] *= w[e];
+        sa += a[i][e];
+        sav = fmaf(a[i][e], v[i][e], sav);
+      }
+    }
+    if (t + step < A.T) {
+      mean = A.mean[t + step];
+      rstd = A.rstd[t + step];
+    }
+    layer_norm_join2<true>(sa, sav, part[turn]);
+    if (me == 0 && t + static_cast<int64_t>(A.depth) * step < A.T) fetch(t + static_cast<int64_t>(A.depth) * step, slot);
+    if (++slot == A.depth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    if (A.dx == nullptr) continue;
+    sa /= static_cast<float>(A.H);
+    sav /= static_cast<float>(A.H);
+    P* dx = reinterpret_cast<P*>(static_cast<E*>(A.dx) + t * A.lddx);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (at(i) >= packs) continue;
+      float c[N] = {};
+      if (A.dresidual != nullptr) unpack(dr[i], c);
+#pragma unroll
+      for (int e = 0; e < N; ++e) c[e] = fmaf(scale, a[i][e] - sa - v[i][e] * sav, c[e]);
+      dx[at(i)] = pack<E>(c);
+    }
+  }
+  if (A.part == nullptr) return;
+  float* out = A.part + static_cast<int64_t>(blockIdx.x) * 2 * A.H;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (at(i) >= packs) continue;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      out[at(i) * N + e] = dw[i][e];
+      out[A.H + at(i) * N + e] = db[i][e];
+    }
+  }
+}
+
 // Rows too wide for that: dx by a block for each row, which reads it twice, ...
 template <typename E>
 __global__ void __launch_bounds__(1024) layer_norm_grad_wide_kernel(const __grid_constant__ LayerNormGradArgs A) {
@@ -313,31 +453,35 @@ __global__ void __launch_bounds__(256) layer_norm_grad_columns_kernel(const __gr
   out[A.H + c] = db;
 }
 
-// The groups' sums of 32 columns: eight warps take every eighth group, and are added up in order.
+// The groups' sums of 32 columns: 32 warps take every 32nd group, and are added up in order.
 template <typename E>
-__global__ void __launch_bounds__(256) layer_norm_sum_kernel(const __grid_constant__ LayerNormGradArgs A) {
-  __shared__ float2 of[8][32];
+__global__ void __launch_bounds__(1024) layer_norm_sum_kernel(const __grid_constant__ LayerNormGradArgs A) {
+  __shared__ float2 of[32][33];
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   float dw = 0.0f, db = 0.0f;
   if (c < A.H) {
 #pragma unroll 4
-    for (int g = warp; g < A.groups; g += 8) {
+    for (int g = warp; g < A.groups; g += 32) {
       dw += A.part[static_cast<int64_t>(g) * 2 * A.H + c];
       db += A.part[static_cast<int64_t>(g) * 2 * A.H + A.H + c];
     }
   }
   of[warp][lane] = make_float2(dw, db);
   __syncthreads();
-  if (warp > 0 || c >= A.H) return;
+  const float2 v = of[lane][warp];  // warp w: column w, a lane for each of the 32
+  dw = v.x;
+  db = v.y;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    dw += of[i][lane].x;
-    db += of[i][lane].y;
+  for (int o = 16; o > 0; o >>= 1) {
+    dw += __shfl_xor_sync(0xFFFFFFFFu, dw, o);
+    db += __shfl_xor_sync(0xFFFFFFFFu, db, o);
   }
-  if (A.dweight != nullptr) from_f32(dw, static_cast<E*>(A.dweight) + c);
-  if (A.dbias != nullptr) from_f32(db, static_cast<E*>(A.dbias) + c);
+  const int column = blockIdx.x * 32 + warp;
+  if (lane > 0 || column >= A.H) return;
+  if (A.dweight != nullptr) from_f32(dw, static_cast<E*>(A.dweight) + column);
+  if (A.dbias != nullptr) from_f32(db, static_cast<E*>(A.dbias) + column);
 }
 
 }  // namespace strata

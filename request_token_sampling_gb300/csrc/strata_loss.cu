@@ -20,7 +20,11 @@ bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_
 int cuda_fail(cudaError_t e, const char* what) { return host_fail(STRATA_ECUDA, "%s: %s", what, cudaGetErrorString(e)); }
 
 using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
-using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, strata::LossArgs);
+using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, strata::LossArgs);
+template <int MODE>
+Kernel kernel_for(bool pair) {
+  return pair ? strata::loss_kernel<MODE, true> : strata::loss_kernel<MODE, false>;
+}
 
 // What the calls need of a device, found at the first call on it.  A failure is not kept: the next call tries again.
 struct Device {
@@ -35,15 +39,16 @@ cudaError_t find_device(Device& d) {
   cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
   if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || p == nullptr)) e = cudaErrorNotSupported;
   d.encode = reinterpret_cast<EncodeFn>(p);
-  auto shared = [&](Kernel kernel, bool pair) {
+  auto shared = [&](Kernel kernel, int mode, bool pair) {
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, strata::loss_smem(pair));
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, strata::loss_smem(mode, pair));
   };
-  shared(strata::loss_kernel<strata::LOSS_SUMS, false>, false);
-  shared(strata::loss_kernel<strata::LOSS_SUMS, true>, true);
-  shared(strata::loss_kernel<strata::LOSS_DIFFS, true>, true);
-  shared(strata::loss_kernel<strata::LOSS_DW, true>, true);
-  shared(strata::loss_kernel<strata::LOSS_DX, true>, true);
+  for (bool pair : {false, true}) {
+    shared(kernel_for<strata::LOSS_SUMS>(pair), strata::LOSS_SUMS, pair);
+    shared(kernel_for<strata::LOSS_DIFFS>(pair), strata::LOSS_DIFFS, pair);
+    shared(kernel_for<strata::LOSS_DX>(pair), strata::LOSS_DX, pair);
+  }
+  shared(strata::loss_kernel<strata::LOSS_DW, true>, strata::LOSS_DW, true);
   return e;
 }
 
@@ -81,19 +86,17 @@ bool map_rows(const Device& dev, CUtensorMap* m, bool f32, const void* p, int64_
 constexpr int SMS = 152, PAIRS = SMS / 2;
 constexpr int ALONE_ROWS = 128;           // a call with more works by pairs of SMs, on a copy of the rows that take part
 constexpr int SLAB_ROWS = 8192;           // whose tiles' sums are held at a time
-constexpr int64_t PIECE_BYTES = int64_t{512} << 20, PARTS_BYTES = int64_t{1} << 30;
+constexpr int64_t PIECE_BYTES = int64_t{512} << 20, PARTS_BYTES = int64_t{256} << 20;
 
 int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 
 // Columns of a tile: those whose tiles come out most even on the SMs.  A stage of a pair's tile costs about as much as 80
 // columns more (as measured for the projection); a tile of one SM is bound by reading w.
-int sums_columns(int T, int V) {
-  const bool pair = T > ALONE_ROWS;
-  const int64_t rows = pair ? tiles_of(std::min(T, SLAB_ROWS), 256) : 1;
+int tile_columns(int64_t row_tiles, int64_t columns, bool pair, int least_columns, int step) {
   int best = 256;
   int64_t least = INT64_MAX;
-  for (int bn = 256; bn >= (pair ? 128 : 32); bn -= 32) {
-    const int64_t cost = tiles_of(rows * tiles_of(V, bn), pair ? PAIRS : SMS) * (bn + (pair ? 80 : 16));
+  for (int bn = 256; bn >= least_columns; bn -= step) {
+    const int64_t cost = tiles_of(row_tiles * tiles_of(columns, bn), pair ? PAIRS : SMS) * (bn + (pair ? 80 : 16));
     if (cost < least) {
       least = cost;
       best = bn;
@@ -104,20 +107,21 @@ int sums_columns(int T, int V) {
 
 struct Plan {
   int T, V, H, K;
-  bool lists, grad, moved;          // a teacher's tokens; for a gradient; works on a copy of the rows
-  int rows_pad = 0, bn = 0, n_tiles = 0, slab = 0;
-  int piece = 0, splits = 1, width = 0;  // ids of a piece; parts of dx; columns of a tile of dw and dx
-  int64_t sorted = 0, q = 0, logq = 0, state = 0, rows = 0, place = 0, count = 0, by = 0, copy = 0, scaled = 0, parts = 0, picks = 0, d = 0, dx = 0,
-          bytes = 0;                // places in the workspace
+  bool lists, grad, pair, moved;    // a teacher's tokens; for a gradient; tiles of two SMs; works on a copy of the rows
+  int tile_rows, rows_pad, slab = 0, bn = 0;  // slab: rows whose tiles' sums are held at a time; bn: columns of a tile of logits
+  int piece = 0, splits = 1, width = 0;       // ids of a piece; most parts of dx; columns of a tile of dw and dx
+  int64_t sorted = 0, q = 0, logq = 0, state = 0, rows = 0, place = 0, count = 0, by = 0, same = 0, copy = 0, scaled = 0, parts = 0, picks = 0,
+          d = 0, dx = 0, bytes = 0;           // places in the workspace
 
-  Plan(int T, int V, int H, int K, bool grad) : T(T), V(V), H(H), K(std::max(K, 1)), lists(K > 0), grad(grad), moved(grad || T > ALONE_ROWS) {
+  Plan(int T, int V, int H, int K, bool grad)
+      : T(T), V(V), H(H), K(std::max(K, 1)), lists(K > 0), grad(grad), pair(T > ALONE_ROWS), moved(grad || pair), tile_rows(pair ? 256 : 128) {
     auto take = [&](int64_t n) {
       const int64_t at = bytes;
       bytes += (n + 255) / 256 * 256;
       return at;
     };
     const int64_t t = T, words = t * this->K * 4;
-    rows_pad = static_cast<int>(tiles_of(T, 256) * 256);
+    rows_pad = static_cast<int>(tiles_of(T, tile_rows) * tile_rows);
     if (lists) {
       sorted = take(words);
       q = take(words);
@@ -129,31 +133,25 @@ struct Plan {
       place = take(t * 4);
       count = take(4);
       by = take(4);
+      same = take(4);
       copy = take(static_cast<int64_t>(rows_pad) * H * 2);
     }
     if (!grad) {
-      bn = sums_columns(T, V);
-      n_tiles = static_cast<int>(tiles_of(V, bn));
       slab = std::min(T, SLAB_ROWS);
-      parts = take(static_cast<int64_t>(slab) * n_tiles * 8);
+      bn = tile_columns(tiles_of(slab, tile_rows), V, pair, pair ? 128 : 16, pair ? 32 : 16);
+      parts = take(slab * tiles_of(V, bn) * 8);
       picks = take(static_cast<int64_t>(slab) * this->K * 4);
       return;
     }
     scaled = take(static_cast<int64_t>(rows_pad) * H * 2);
     const int64_t all = tiles_of(V, 256) * 256;
     piece = static_cast<int>(std::min(all, std::max<int64_t>(256, PIECE_BYTES / (rows_pad * int64_t{2}) / 256 * 256)));
+    bn = tile_columns(rows_pad / tile_rows, std::min(piece, V), pair, 64, 32);
+    piece = static_cast<int>(tiles_of(piece, 2 * bn) * 2 * bn);  // whole tiles, and steps of 64
     d = take(static_cast<int64_t>(rows_pad) * piece * 2);
     width = H <= 128 ? 128 : 256;
-    // Few tiles of dx leave pairs idle in the last turn: the sum over a piece's ids is cut into the parts that leave the least
-    const int64_t tiles = rows_pad / 256 * tiles_of(H, width), one = static_cast<int64_t>(rows_pad) * H * 4;
-    double least = 1e30;
-    for (int s = 1; s <= 16 && (s == 1 || (s * one <= PARTS_BYTES && piece / 64 >= 8 * s)); ++s) {
-      const double cost = static_cast<double>(tiles_of(tiles * s, PAIRS)) / s + 0.02 * s;
-      if (cost < least) {
-        least = cost;
-        splits = s;
-      }
-    }
+    const int64_t one = static_cast<int64_t>(rows_pad) * H * 4;
+    splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(32, PARTS_BYTES / one)));
     dx = take(splits * one);
   }
 };
@@ -208,9 +206,11 @@ struct Run {
     e = strata::Launch(grid, block, smem, stream, overlaps, cluster)(kernel, args...);
     overlaps = true;
   }
-  void products(Kernel kernel, bool pair, int64_t tiles, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const strata::LossArgs& A) {
+  template <int MODE>
+  void products(Kernel kernel, bool pair, int64_t tiles, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CUtensorMap& o,
+                const strata::LossArgs& A) {
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(tiles, pair ? PAIRS : SMS)) * (pair ? 2 : 1);
-    (*this)(kernel, blocks, strata::LOSS_THREADS, strata::loss_smem(pair), pair ? 2 : 1, a, b, o, A);
+    (*this)(kernel, blocks, strata::LOSS_THREADS, strata::loss_smem(MODE, pair), pair ? 2 : 1, a, b, c, o, A);
   }
 };
 
@@ -232,6 +232,7 @@ void launch_plan(Run& run, const Loss& C, const Plan& P, const float* g, float* 
   A.place = at<int32_t>(C, P.place);
   A.count = at<int32_t>(C, P.count);
   A.by = at<float>(C, P.by);
+  A.same = at<int32_t>(C, P.same);
   A.copy = at<__nv_bfloat16>(C, P.copy);
   A.scaled = P.grad ? at<__nv_bfloat16>(C, P.scaled) : nullptr;
   A.loss = loss;
@@ -241,8 +242,10 @@ void launch_plan(Run& run, const Loss& C, const Plan& P, const float* g, float* 
   A.T = C.T;
   A.V = C.V;
   A.H = C.H;
-  run(strata::loss_plan_kernel, 1, 1024, 0, 1, A);
-  run(strata::loss_gather_kernel, static_cast<unsigned>(C.T) + 256, 128, 0, 1, A);
+  A.tile_rows = P.tile_rows;
+  const bool plans = C.T <= strata::LOSS_PLAN_ROWS;
+  if (!plans) run(strata::loss_plan_kernel, 1, 1024, 0, 1, A);
+  run(plans ? strata::loss_gather_kernel<true> : strata::loss_gather_kernel<false>, static_cast<unsigned>(C.T + P.tile_rows), 128, 0, 1, A);
 }
 
 strata::LossArgs products_args(const Loss& C, const Plan& P, uint32_t* errors) {
@@ -260,7 +263,10 @@ strata::LossArgs products_args(const Loss& C, const Plan& P, uint32_t* errors) {
   A.K = P.K;
   A.rows_most = P.rows_pad;
   A.rows_pad = P.rows_pad;
-  A.splits = 1;
+  A.a_rows = std::min(128, (C.T + 7) / 8 * 8);
+  A.splits = P.splits;
+  A.k_piece = P.piece / 64;
+  A.units = P.pair ? PAIRS : SMS;
   return A;
 }
 
@@ -275,27 +281,26 @@ int forward(const Loss& C, float* loss, float* lse, const char* name) {
   const Device* dev = nullptr;
   if (const int rc = device_entry(device, &dev); rc != STRATA_OK) return rc;
   const Plan P(C.T, C.V, C.H, C.K, false);
-  const bool pair = P.moved;
   CUtensorMap mx, mw;
-  if (!(pair ? map_rows(*dev, &mx, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, 128) : map_rows(*dev, &mx, false, C.x, C.H, C.T, C.ldx, 128)))
+  if (!(P.pair ? map_rows(*dev, &mx, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, 128)
+               : map_rows(*dev, &mx, false, C.x, C.H, C.T, C.ldx, std::min(128, (C.T + 7) / 8 * 8))))
     return host_fail(STRATA_EINVAL, "x cannot be mapped");
-  if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, pair ? P.bn / 2 : P.bn)) return host_fail(STRATA_EINVAL, "w cannot be mapped");
+  if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, P.pair ? P.bn / 2 : P.bn)) return host_fail(STRATA_EINVAL, "w cannot be mapped");
   const cudaError_t e = strata::launch_operator(device, C.stream, [&](bool overlaps) {
     Run run{C.stream, overlaps};
     launch_plan(run, C, P, nullptr, loss, lse, nullptr, 0);
     strata::LossArgs A = products_args(C, P, errors);
     A.columns = C.V;
     A.bn = P.bn;
-    A.n_tiles = P.n_tiles;
+    A.n_tiles = static_cast<int>(tiles_of(C.V, P.bn));
     A.parts = at<float2>(C, P.parts);
     A.picks = at<float>(C, P.picks);
     strata::LossJoinArgs J{A.count, A.rows, A.ids, P.lists ? at<int32_t>(C, P.state) : nullptr, A.q, P.lists ? at<float>(C, P.logq) : nullptr,
-                           A.picks, A.parts, loss, lse, C.temperature, C.T, C.V, P.K, 0, P.n_tiles};
+                           A.picks, A.parts, loss, lse, C.temperature, C.T, C.V, P.K, 0, A.n_tiles};
     for (int row0 = 0; row0 < C.T; row0 += P.slab) {
       A.row0 = J.row0 = row0;
       A.rows_most = std::min(P.slab, C.T - row0);
-      run.products(pair ? strata::loss_kernel<strata::LOSS_SUMS, true> : strata::loss_kernel<strata::LOSS_SUMS, false>, pair,
-                   tiles_of(A.rows_most, pair ? 256 : 128) * P.n_tiles, mx, mw, mw, A);
+      run.products<strata::LOSS_SUMS>(kernel_for<strata::LOSS_SUMS>(P.pair), P.pair, tiles_of(A.rows_most, P.tile_rows) * A.n_tiles, mx, mw, mw, mw, A);
       run(strata::loss_join_kernel, static_cast<unsigned>(A.rows_most), 128, 0, 1, J);
     }
     return run.e;
@@ -325,43 +330,54 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
   const Device* dev = nullptr;
   if (const int rc = device_entry(device, &dev); rc != STRATA_OK) return rc;
   const Plan P(C.T, C.V, C.H, C.K, true);
-  CUtensorMap mx, mw, mxs, mws, md, mds, mdo, mdw{}, mdx;
-  if (!map_rows(*dev, &mx, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, 128) ||
+  CUtensorMap mx, mw, mxo, mxs, mwo, md, mds, mdx;
+  const int a_rows = P.pair ? 128 : std::min(128, (C.T + 7) / 8 * 8);
+  if (!map_rows(*dev, &mx, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, a_rows) ||
+      !map_rows(*dev, &mxo, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, 64) ||
       !map_rows(*dev, &mxs, false, at<void>(C, P.scaled), C.H, P.rows_pad, C.H, 64) ||
-      !map_rows(*dev, &md, false, at<void>(C, P.d), P.piece, P.rows_pad, P.piece, 128) ||
-      !map_rows(*dev, &mds, false, at<void>(C, P.d), P.piece, P.rows_pad, P.piece, 64) ||
-      !map_rows(*dev, &mdo, false, at<void>(C, P.d), P.piece, P.rows_pad, P.piece, 32) ||
       !map_rows(*dev, &mdx, true, at<void>(C, P.dx), C.H, static_cast<int64_t>(P.splits) * P.rows_pad, C.H, 32))
     return host_fail(STRATA_EINVAL, "the workspace cannot be mapped");
-  if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, 128) || !map_rows(*dev, &mws, false, C.w, C.H, C.V, C.ldw, 64) ||
-      (dw != nullptr && !map_rows(*dev, &mdw, false, dw, C.H, C.V, lddw, 32)))
-    return host_fail(STRATA_EINVAL, "w or dw cannot be mapped");
+  if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, P.pair ? P.bn / 2 : P.bn) || !map_rows(*dev, &mwo, false, C.w, C.H, C.V, C.ldw, 64))
+    return host_fail(STRATA_EINVAL, "w cannot be mapped");
   e = strata::launch_operator(device, C.stream, [&](bool overlaps) {
     Run run{C.stream, overlaps};
     launch_plan(run, C, P, g, nullptr, nullptr, dx, lddx);
     strata::LossArgs A = products_args(C, P, errors);
     A.lse = lse;
+    A.wide = !misaligned(dw, 32) && lddw % 16 == 0 && C.H % 16 == 0;
     A.by = at<float>(C, P.by);
-    const int64_t row_tiles = P.rows_pad / 256, across = tiles_of(C.H, P.width);
+    A.same = at<int32_t>(C, P.same);
+    const int64_t row_tiles = P.rows_pad / P.tile_rows, across = tiles_of(C.H, P.width);
     for (int v0 = 0; v0 < C.V; v0 += P.piece) {
       A.v0 = v0;
       A.columns = std::min(P.piece, C.V - v0);
-      A.bn = 256;
-      A.n_tiles = static_cast<int>(tiles_of(A.columns, 256));
-      run.products(strata::loss_kernel<strata::LOSS_DIFFS, true>, true, row_tiles * A.n_tiles, mx, mw, mdo, A);
+      // what lies beyond the piece's ids is not looked at, but read as zeros
+      if (!map_rows(*dev, &md, false, at<void>(C, P.d), A.columns, P.rows_pad, P.piece, a_rows) ||
+          !map_rows(*dev, &mds, false, at<void>(C, P.d), A.columns, P.rows_pad, P.piece, 64))
+        return cudaErrorInvalidValue;
+      A.bn = P.bn;
+      A.n_tiles = static_cast<int>(tiles_of(A.columns, P.bn));
+      A.out = at<__nv_bfloat16>(C, P.d);
+      A.ldo = P.piece;
+      run.products<strata::LOSS_DIFFS>(kernel_for<strata::LOSS_DIFFS>(P.pair), P.pair, row_tiles * A.n_tiles, mx, mw, mw, mw, A);
       A.bn = P.width;
       A.n_tiles = static_cast<int>(across);
-      if (dw != nullptr) run.products(strata::loss_kernel<strata::LOSS_DW, true>, true, tiles_of(A.columns, 256) * across, mds, mxs, mdw, A);
-      if (dx != nullptr) {
-        A.splits = P.splits;
-        A.add = v0 > 0;
-        run.products(strata::loss_kernel<strata::LOSS_DX, true>, true, row_tiles * across * P.splits, md, mws, mdx, A);
-      }
+      A.out = static_cast<__nv_bfloat16*>(dw);
+      A.ldo = lddw;
+      if (dw != nullptr)
+        run.products<strata::LOSS_DW>(strata::loss_kernel<strata::LOSS_DW, true>, true, tiles_of(A.columns, 256) * across, mds, mxo, mxs, mxs, A);
+      A.add = v0 > 0;
+      if (dx != nullptr)
+        run.products<strata::LOSS_DX>(kernel_for<strata::LOSS_DX>(P.pair), P.pair, row_tiles * across * P.splits, md, mwo, mwo, mdx, A);
     }
     if (dx != nullptr) {
-      const strata::LossDxArgs D{A.count, A.rows, at<float>(C, P.dx), g, static_cast<__nv_bfloat16*>(dx), lddx,
-                                 static_cast<int64_t>(P.rows_pad) * C.H, C.temperature, C.H, P.splits};
-      run(strata::loss_dx_kernel, static_cast<unsigned>(C.T), 128, 0, 1, D);
+      const strata::LossDxArgs D{A.count, A.rows, at<float>(C, P.dx), g, static_cast<__nv_bfloat16*>(dx), lddx, static_cast<int64_t>(P.rows_pad) * C.H,
+                                 C.temperature, C.H, P.splits, A.k_piece, A.units, P.width, P.tile_rows};
+      if (run.e == cudaSuccess) {
+        strata::Launch launch(static_cast<unsigned>(C.T), 128, 0, C.stream, run.overlaps);
+        launch.cfg.gridDim.y = static_cast<unsigned>((C.H + 511) / 512);
+        run.e = launch(strata::loss_dx_kernel, D);
+      }
     }
     return run.e;
   });

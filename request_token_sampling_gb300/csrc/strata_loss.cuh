@@ -25,14 +25,19 @@ namespace strata {
 enum LossMode { LOSS_SUMS, LOSS_DIFFS, LOSS_DW, LOSS_DX };
 
 constexpr int LOSS_LINE = 128;        // bytes of a row that one stage holds: 64 bfloat16
-constexpr int LOSS_THREADS = 192;     // warp 0 loads, warp 1 issues the products, warps 2-5 write the tile
+constexpr int LOSS_THREADS = 320;     // warp 0 loads, warp 1 issues the products, warps 2-9 write the tile
+constexpr int LOSS_WRITERS = 8;       // four for each of the two accumulators: they write one tile after another by turns
 constexpr int LOSS_BAND = 16;         // tiles of the inner index that a band has: what its operands take stays in L2
+constexpr int LOSS_RUNS = 4;          // steps of 64 rows up to which dw's tiles go in runs
 constexpr int LOSS_NO_ID = 0x7FFFFFFF;
-// Two SMs share a tile: 128 rows and half of the columns each; one SM alone has 128 rows and all columns.
-__host__ __device__ constexpr int loss_stages(bool pair) { return pair ? 6 : 4; }
+// Two SMs share a tile: 128 rows and half of the columns each; one SM alone has 128 rows and all columns.  What is left of
+// shared memory holds results on their way out, a piece of 32 rows for each writing warp.
+constexpr int LOSS_PIECE = 4096;
+__host__ __device__ constexpr int loss_stages(int mode, bool pair) { return !pair ? 4 : mode == LOSS_SUMS ? 7 : 6; }
 __host__ __device__ constexpr int loss_stage_bytes(bool pair) { return (128 + (pair ? 128 : 256)) * LOSS_LINE; }
-constexpr int LOSS_STAGING = 4096;    // of 32 rows' results on their way to memory; two for each writing warp
-__host__ __device__ constexpr int loss_smem(bool pair) { return loss_stages(pair) * loss_stage_bytes(pair) + 8 * LOSS_STAGING + 1024 + 512; }
+__host__ __device__ constexpr int loss_smem(int mode, bool pair) {
+  return loss_stages(mode, pair) * loss_stage_bytes(pair) + (mode == LOSS_SUMS ? 0 : LOSS_WRITERS * LOSS_PIECE) + 1024 + 512;
+}
 
 struct LossArgs {
   const int32_t* count;   // rows that take part, as the plan found them; NULL: all T
@@ -40,9 +45,13 @@ struct LossArgs {
   const int32_t* ids;     // [T][K], ascending where K > 1, those that are not there last as LOSS_NO_ID
   const float* q;         // [T][K] beside them; NULL: 1
   const float* lse;       // of row t, for LOSS_DIFFS
-  const float* by;        // scale of LOSS_DW's results, NULL: none
+  const float* by;        // scale of LOSS_DW's results
+  const int32_t* same;    // LOSS_DW: not 0 where all rows' scales are equal, and the rows need no scaled copy
   float2* parts;          // [rows][n_tiles]: exponent and sum of a tile's columns, for LOSS_SUMS
   float* picks;           // [rows][K]: z of the row's ids
+  __nv_bfloat16* out;     // d or dw
+  int64_t ldo;
+  int wide;               // dw's rows start on 32 bytes and are so many times as wide
   uint32_t* errors;
   float scale;            // log2(e) / s
   float dw_scale;         // s
@@ -50,12 +59,14 @@ struct LossArgs {
   int row0, rows_most;    // rows row0 .. of this launch
   int v0, columns;        // the piece of the vocabulary
   int bn, n_tiles;        // columns of a tile, and tiles of them
-  int splits, rows_pad;   // LOSS_DX: parts that the ids are cut into, and rows of each
+  int a_rows;             // of A that one SM's tile brings; the accumulator's other rows are not looked at
+  int splits, rows_pad;   // LOSS_DX: parts that a piece may be cut into, and rows of each
+  int k_piece, units;     // steps of 64 ids in a piece, and tiles that run at a time
   int add;                // LOSS_DX: onto what is there
 };
 
 struct LossBars {
-  uint64_t full[6], empty[6], done[2], freed[2], drained;
+  uint64_t full[7], empty[7], done[2], freed[2], drained;
   uint32_t tmem, dead;
 };
 
@@ -78,14 +89,29 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* m, int x, int y, u
   asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x), "r"(y), "r"(src) : "memory");
 }
 __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void tma_store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Few tiles of dx leave SMs idle in the last turn, so the sum over a piece's ids is cut into parts; the whole warp.  In
+// eighths of a stage's time (0.33 us): turns of so many stages and three to start and end with, and each part's way
+// to memory and back (4 bytes each way and element: 0.23 stages for a pair's tile).
+__device__ __forceinline__ int loss_splits(int tiles, int k, int most, int units, bool pair) {
+  const int s = static_cast<int>(threadIdx.x & 31) + 1;
+  uint32_t cost = 0x07FFFFFFu;
+  if (s <= most && (s == 1 || k >= 4 * s)) cost = min(cost, static_cast<uint32_t>((tiles * s + units - 1) / units * ((k + s - 1) / s + 3) * 8 + s * tiles * (pair ? 2 : 1)));
+  return static_cast<int>(__reduce_min_sync(FULL_MASK, cost << 5 | static_cast<uint32_t>(s - 1)) & 31u) + 1;
+}
 
 // Tile `tile` of `outer` x `inner`: bands of LOSS_BAND inner ones, which go fastest.
 __device__ __forceinline__ void loss_place(int tile, int outer, int inner, int& o, int& i) {
+  if (inner <= LOSS_BAND) {
+    o = tile / inner;
+    i = tile - o * inner;
+    return;
+  }
   const int band = tile / (LOSS_BAND * outer), width = min(LOSS_BAND, inner - band * LOSS_BAND), rest = tile - band * LOSS_BAND * outer;
   o = rest / width;
-  i = band * LOSS_BAND + rest % width;
+  i = band * LOSS_BAND + rest - o * width;
 }
 
 // The next of a row's ids from `from` on, in ascending order.
@@ -117,14 +143,14 @@ struct LossIds {
 
 template <int MODE, bool PAIR>
 __global__ void __launch_bounds__(LOSS_THREADS, 1)
-    loss_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mo,
-                const __grid_constant__ LossArgs A) {
-  constexpr int STAGES = loss_stages(PAIR), STAGE = loss_stage_bytes(PAIR), TILE_M = PAIR ? 256 : 128;
+    loss_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mc,
+                const __grid_constant__ CUtensorMap mo, const __grid_constant__ LossArgs A) {
+  constexpr int STAGES = loss_stages(MODE, PAIR), STAGE = loss_stage_bytes(PAIR), TILE_M = PAIR ? 256 : 128;
   constexpr bool A_OUTER = MODE == LOSS_DW, B_OUTER = MODE == LOSS_DW || MODE == LOSS_DX;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint8_t* staging = smem + STAGES * STAGE;
-  LossBars* B = reinterpret_cast<LossBars*>(staging + 8 * LOSS_STAGING);
+  LossBars* B = reinterpret_cast<LossBars*>(staging + (MODE == LOSS_SUMS ? 0 : LOSS_WRITERS * LOSS_PIECE));
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool lead = rank == 0;
@@ -139,7 +165,7 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->done[i], 1);
-      mbar_init(&B->freed[i], PAIR ? 8 : 4);  // the first block's: four warps of each
+      mbar_init(&B->freed[i], PAIR ? LOSS_WRITERS : LOSS_WRITERS / 2);  // the first block's: four warps of each
     }
     mbar_init(&B->drained, 1);
     B->dead = 0;
@@ -175,14 +201,29 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
   } else if constexpr (MODE == LOSS_DW) {
     outer = (A.columns + TILE_M - 1) / TILE_M, inner = A.n_tiles, k_all = (live + 63) / 64;
   } else {
-    outer = A.n_tiles, inner = row_tiles, k_all = (A.columns + 63) / 64, splits = A.splits;
+    outer = A.n_tiles, inner = row_tiles, k_all = (A.columns + 63) / 64;
+    splits = loss_splits(outer * inner, A.k_piece, A.splits, A.units, PAIR);
   }
-  const int per_split = outer * inner, tiles = per_split * splits;
-  const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+  const int per_split = outer * inner;
+  int tiles = per_split * splits, first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+  // Few rows: dw is bound by its writing, and a pair that writes one tile after another of the same ids leaves memory fuller
+  // pages (96 rows, 1 GB: 262 us, by turns 283; with 32 bytes a store 247).  With more rows the pairs' parts of d would
+  // not fit in L2 together.
+  if (MODE == LOSS_DW && k_all <= LOSS_RUNS) {
+    const int64_t all = tiles;
+    tiles = static_cast<int>(all * (first + 1) / step);
+    first = static_cast<int>(all * first / step);
+    step = 1;
+  }
   const int half = PAIR ? A.bn / 2 : A.bn;  // columns that this block brings
   auto stages_of = [&](int split, int& from, int& to) {
-    from = static_cast<int>(static_cast<int64_t>(k_all) * split / splits);
-    to = static_cast<int>(static_cast<int64_t>(k_all) * (split + 1) / splits);
+    if constexpr (MODE == LOSS_DX) {  // 8,192 steps and 32 parts at most
+      from = k_all * split / splits;
+      to = k_all * (split + 1) / splits;
+    } else {
+      from = 0;
+      to = k_all;
+    }
   };
 
   Ring<STAGES> ring;  // of the loading and of the issuing warp
@@ -190,7 +231,8 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
   uint32_t turn = 0;  // tiles so far, of the issuing warp and of those that write
   if (warp == 0) {
     asm volatile("fence.proxy.async;" ::: "memory");  // rows and d were written by ordinary stores of kernels before
-    const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * (128 + half) * LOSS_LINE);
+    const uint32_t bytes = static_cast<uint32_t>(PAIR ? 2 * (128 + half) : A.a_rows + half) * LOSS_LINE;
+    const CUtensorMap* mx = MODE == LOSS_DW && *A.same == 0 ? &mc : &mb;
     for (int tile = first; tile < tiles && alive; tile += step) {
       int o, i, from, to;
       const int split = MODE == LOSS_DX ? tile / per_split : 0;
@@ -216,7 +258,7 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
             load(at_b, &mb, s * 64, A.v0 + o * A.bn + rank * half);
           } else if constexpr (MODE == LOSS_DW) {
             for (int b = 0; b < 2; ++b) load(at + b * 8192, &ma, o * TILE_M + rank * 128 + b * 64, s * 64);
-            for (int b = 0; b < half / 64; ++b) load(at_b + b * 8192, &mb, i * A.bn + rank * half + b * 64, s * 64);
+            for (int b = 0; b < half / 64; ++b) load(at_b + b * 8192, mx, i * A.bn + rank * half + b * 64, s * 64);
           } else {
             load(at, &ma, s * 64, i * TILE_M + rank * 128);
             for (int b = 0; b < half / 64; ++b) load(at_b + b * 8192, &mb, o * A.bn + rank * half + b * 64, A.v0 + s * 64);
@@ -278,36 +320,77 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
     }
   } else if (warp >= 2) {
     const uint32_t quarter = warp & 3;
-    uint8_t* mine = staging + (warp - 2) * 2 * LOSS_STAGING;  // this warp's two halves of staging, in turns
-    uint32_t flip = 0;
-    // the line that this lane fills, its 16-byte pieces swizzled as the copy out expects them
-    auto line = [&]() { return smem_u32(mine + flip * LOSS_STAGING) + lane * 128; };
-    auto put = [&](uint32_t at, int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((piece ^ (lane & 7)) << 4)), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+    const uint32_t buf = (warp - 2) / 4;  // the accumulator that this warp empties
+    const uint32_t mine = smem_u32(staging) + (warp - 2) * LOSS_PIECE;  // this warp's piece
+    // A lane fills the line of its row, 16 bytes at a time, swizzled so that lines and columns both go without bank conflicts
+    // (and as a tensor copy expects it).
+    auto put = [&](int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 128 + ((piece ^ (lane & 7)) << 4)), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
     };
-    auto open = [&]() {  // the copy before the last has read its half
-      if (lane == 0) tma_store_wait_read1();
+    auto put32 = [&](int column, const float (&v)[32]) {  // as bfloat16
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 two = __floats2bfloat162_rn(v[8 * p + 2 * e], v[8 * p + 2 * e + 1]);
+          w[e] = *reinterpret_cast<const uint32_t*>(&two);
+        }
+        put(column / 8 + p, w[0], w[1], w[2], w[3]);
+      }
+    };
+    // Whole lines of 128 bytes to memory: rows y .., columns x .. of A.out, 32 bytes a lane where they lie on that, else 16.
+    // (Tensor copies want a fence between the proxies for each piece, in which the warps spent a third of their time.)
+    auto write_lines = [&](int64_t y, int x, int rows, int columns) {
+      __syncwarp();
+      auto get = [&](int row, int piece) {
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(mine + row * 128 + ((piece ^ (row & 7)) << 4)) : "memory");
+        return v;
+      };
+      if (MODE == LOSS_DIFFS || A.wide != 0) {
+        const int row = lane >> 2, piece = (lane & 3) * 2;
+        __nv_bfloat16* to = A.out + (y + row) * A.ldo + x + piece * 8;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint4 v = get(n * 8 + row, piece), u = get(n * 8 + row, piece + 1);
+          if (n * 8 + row < rows && piece * 8 < columns)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + n * 8 * A.ldo), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
+        }
+      } else {
+        const int row = lane >> 3, piece = lane & 7;
+        __nv_bfloat16* to = A.out + (y + row) * A.ldo + x + piece * 8;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const uint4 v = get(n * 4 + row, piece);
+          if (n * 4 + row < rows && piece * 8 < columns) *reinterpret_cast<uint4*>(to + n * 4 * A.ldo) = v;
+        }
+      }
+      __syncwarp();
+    };
+    // 32 bits: by a tensor copy, which also adds
+    auto open = [&]() {
+      if (lane == 0) tma_store_wait_read();
       __syncwarp();
     };
     auto send = [&](int x, int y, bool add) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        const uint32_t src = smem_u32(mine + flip * LOSS_STAGING);
         if (add)
-          tma_add_2d(&mo, x, y, src);
+          tma_add_2d(&mo, x, y, mine);
         else
-          tma_store_2d(&mo, x, y, src);
+          tma_store_2d(&mo, x, y, mine);
         tma_store_commit();
       }
-      flip ^= 1;
     };
-    for (int tile = first; tile < tiles; tile += step, ++turn) {
+    [[maybe_unused]] const float by = MODE == LOSS_DW ? *A.by * A.dw_scale : 1.0f;
+    const uint32_t sum = tmem + buf * 256 + (quarter << 21);
+    for (int tile = first + static_cast<int>(buf) * step; tile < tiles; tile += 2 * step, ++turn) {
       int o, i, from, to;
       const int split = MODE == LOSS_DX ? tile / per_split : 0;
       loss_place(tile - split * per_split, outer, inner, o, i);
       stages_of(split, from, to);
-      const uint32_t buf = turn & 1, sum = tmem + buf * 256 + (quarter << 21);
       const int in_tile = static_cast<int>(rank * 128 + quarter * 32);  // this warp's first lane
       const int r = i * TILE_M + in_tile + lane;                         // of SUMS and DIFFS: the row of this launch
       [[maybe_unused]] int64_t t = -1;
@@ -320,8 +403,7 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
         ids.start(A, t, n0);
         if (MODE == LOSS_DIFFS && t >= 0) lse2 = A.lse[t] * 1.44269504088896340736f;
       }
-      [[maybe_unused]] const float by = MODE == LOSS_DW ? (A.by != nullptr ? *A.by : 1.0f) * A.dw_scale : 1.0f;
-      if (!proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit)) {
+      if (!proj_wait(&B->done[buf], turn & 1, dead, A.errors, bit)) {
         alive = false;
         break;
       }
@@ -338,8 +420,9 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = c + e < columns ? v[e] : -INFINITY;
           }
-          while (__any_sync(FULL_MASK, ids.next < n0 + c + 32)) {
-            if (ids.next < n0 + c + 32) {
+          const int end = n0 + min(c + 32, columns);
+          while (__any_sync(FULL_MASK, ids.next < end)) {
+            if (ids.next < end) {
               float z = 0.0f;
 #pragma unroll
               for (int e = 0; e < 32; ++e) z = ids.next == n0 + c + e ? v[e] : z;
@@ -362,65 +445,60 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
           base = now;
         }
         if (t >= 0) A.parts[static_cast<int64_t>(r) * A.n_tiles + o] = make_float2(base, total);
+      } else if constexpr (MODE == LOSS_DIFFS) {
+        const int upto = t < 0 ? 0 : A.v0 + A.columns - n0;  // zeros beyond the rows and the vocabulary
+#pragma unroll 1
+        for (int c = 0; c < A.bn; c += 32) {
+          float v[32];
+          tmem_ld32(sum + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = ex2_approx(fmaf(v[e], A.scale, -lse2));
+          while (__any_sync(FULL_MASK, ids.next < n0 + c + 32)) {
+            if (ids.next < n0 + c + 32) {
+              const float q = ids.weight();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] -= ids.next == n0 + c + e ? q : 0.0f;
+              ids.advance();
+            }
+          }
+          if (upto - c < 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = c + e < upto ? v[e] : 0.0f;
+          }
+          put32(c & 32, v);
+          if ((c & 32) != 0 || c + 32 >= A.bn) write_lines(i * TILE_M + in_tile, o * A.bn + (c & ~32), 32, (c & 32) + 32);
+        }
       } else {
-        // results of 128 bytes a lane at a time
-        constexpr int COLUMNS = MODE == LOSS_DX ? 32 : 64;
         const bool none = from == to;  // no rows, or a part without ids: nothing was added up
+        constexpr int COLUMNS = MODE == LOSS_DX ? 32 : 64;  // 128 bytes of results
 #pragma unroll 1
         for (int c = 0; c < A.bn; c += COLUMNS) {
+          const int x = (MODE == LOSS_DX ? o : i) * A.bn + c;
+          if (x >= A.H) break;
           float v[COLUMNS];
 #pragma unroll
           for (int h = 0; h < COLUMNS; h += 32) tmem_ld32(sum + c + h, *reinterpret_cast<float(*)[32]>(v + h));
           tmem_wait_ld();
-          if constexpr (MODE == LOSS_DIFFS) {
-#pragma unroll
-            for (int e = 0; e < COLUMNS; ++e) v[e] = ex2_approx(fmaf(v[e], A.scale, -lse2));
-            while (__any_sync(FULL_MASK, ids.next < n0 + c + COLUMNS)) {
-              if (ids.next < n0 + c + COLUMNS) {
-                const float q = ids.weight();
-#pragma unroll
-                for (int e = 0; e < COLUMNS; ++e) v[e] -= ids.next == n0 + c + e ? q : 0.0f;
-                ids.advance();
-              }
-            }
-            const int upto = t < 0 ? 0 : A.v0 + A.columns - n0 - c;  // zeros beyond the rows and the vocabulary
-            if (upto < COLUMNS) {
-#pragma unroll
-              for (int e = 0; e < COLUMNS; ++e) v[e] = e < upto ? v[e] : 0.0f;
-            }
-          } else if constexpr (MODE == LOSS_DW) {
-#pragma unroll
-            for (int e = 0; e < COLUMNS; ++e) v[e] = none ? 0.0f : v[e] * by;
-          } else if (none) {
+          if (none) {
 #pragma unroll
             for (int e = 0; e < COLUMNS; ++e) v[e] = 0.0f;
           }
-          open();
-          const uint32_t at = line();
-          if constexpr (MODE == LOSS_DX) {
+          if constexpr (MODE == LOSS_DW) {
+#pragma unroll
+            for (int h = 0; h < COLUMNS; h += 32) {
+#pragma unroll
+              for (int e = h; e < h + 32; ++e) v[e] *= by;
+              put32(h, *reinterpret_cast<float(*)[32]>(v + h));
+            }
+            const int y = o * TILE_M + in_tile;
+            write_lines(A.v0 + y, x, A.columns - y, A.H - x);
+          } else {
+            open();
 #pragma unroll
             for (int p = 0; p < 8; ++p)
-              put(at, p, __float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]), __float_as_uint(v[4 * p + 3]));
-          } else {
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 two = __floats2bfloat162_rn(v[8 * p + 2 * e], v[8 * p + 2 * e + 1]);
-                w[e] = *reinterpret_cast<const uint32_t*>(&two);
-              }
-              put(at, p, w[0], w[1], w[2], w[3]);
-            }
-          }
-          if constexpr (MODE == LOSS_DIFFS) {
-            send(o * A.bn + c, i * TILE_M + in_tile, false);
-          } else if constexpr (MODE == LOSS_DW) {
-            const int x = i * A.bn + c, y = o * TILE_M + in_tile;
-            if (x < A.H && y < A.columns) send(x, A.v0 + y, false);
-          } else {
-            const int x = o * A.bn + c;
-            if (x < A.H) send(x, split * A.rows_pad + i * TILE_M + in_tile, A.add != 0);
+              put(p, __float_as_uint(v[4 * p]), __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]), __float_as_uint(v[4 * p + 3]));
+            send(x, split * A.rows_pad + i * TILE_M + in_tile, A.add != 0);
           }
         }
       }
@@ -433,7 +511,7 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
           mbar_arrive(&B->freed[buf]);
       }
     }
-    if (lane == 0) tma_store_wait_all();
+    if (MODE == LOSS_DX && lane == 0) tma_store_wait_all();
   }
   __syncthreads();
   if constexpr (PAIR) {  // neither block's shared or tensor memory is given back while the other's products use it
@@ -520,12 +598,13 @@ struct LossPlanArgs {
   const __nv_bfloat16* x;
   int64_t ldx;
   int32_t *rows, *place, *count;  // [T] both ways (place -1 and -2: left out, id of V or more), and how many
-  float* by;                      // max |g|
-  __nv_bfloat16 *copy, *scaled;   // the rows, and with a gradient also scaled by g / max |g|
+  float* by;                      // max |g|, or g where all rows have the same ...
+  int32_t* same;                  // ... which this tells
+  __nv_bfloat16 *copy, *scaled;   // the rows, and with unequal g also scaled by g / max |g|
   float *loss, *lse;              // of rows that do not take part
   __nv_bfloat16* dx;
   int64_t lddx;
-  int T, V, H;
+  int T, V, H, tile_rows;
 };
 
 __device__ __forceinline__ int loss_state(const int32_t* ids, const int32_t* state, int64_t t, int V) {
@@ -533,87 +612,120 @@ __device__ __forceinline__ int loss_state(const int32_t* ids, const int32_t* sta
   return ids[t] < 0 ? 0 : ids[t] < V ? 1 : -1;
 }
 
-// One block numbers the rows that take part in ascending order.
-__global__ void __launch_bounds__(1024) loss_plan_kernel(const __grid_constant__ LossPlanArgs A) {
-  __shared__ int sums[32];
-  __shared__ float tops[32];
-  grid_dep_wait();
-  grid_dep_launch();
-  const int each = (A.T + 1023) / 1024, from = min(A.T, static_cast<int>(threadIdx.x) * each), to = min(A.T, from + each);
+// What all rows together say: where row `mine` goes among those that take part, how many there are, and their scale.  By the
+// whole block, each thread a run of rows; `A.place` and `A.rows` are filled in where `writes`.
+struct LossPlan {
+  int place, count;
+  float by;
+  bool same;
+};
+template <int THREADS>
+__device__ __forceinline__ LossPlan loss_plan(const LossPlanArgs& A, int mine, bool writes) {
+  constexpr int WARPS = THREADS / 32;
+  __shared__ int sums[WARPS], found;
+  __shared__ float tops[WARPS], lows[WARPS], highs[WARPS];
+  const int each = (A.T + THREADS - 1) / THREADS, from = min(A.T, static_cast<int>(threadIdx.x) * each), to = min(A.T, from + each);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto takes_part = [&](int t) { return loss_state(A.ids, A.state, t, A.V) == 1 && (A.g == nullptr || A.g[t] != 0.0f); };
-  int mine = 0;
-  float top = 0.0f;
+  int own = 0;
+  float top = 0.0f, low = INFINITY, high = -INFINITY;  // of |g| where it is finite, and of g
   for (int t = from; t < to; ++t) {
     if (!takes_part(t)) continue;
-    ++mine;
-    if (A.g != nullptr && fabsf(A.g[t]) < INFINITY) top = fmaxf(top, fabsf(A.g[t]));
+    ++own;
+    if (A.g == nullptr) continue;
+    const float g = A.g[t];
+    if (fabsf(g) < INFINITY) top = fmaxf(top, fabsf(g));
+    low = g == g ? fminf(low, g) : -INFINITY;
+    high = fmaxf(high, g);
   }
-  int before = mine;
+  int before = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(FULL_MASK, before, o);
     if (lane >= o) before += v;
     top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+    low = fminf(low, __shfl_xor_sync(FULL_MASK, low, o));
+    high = fmaxf(high, __shfl_xor_sync(FULL_MASK, high, o));
   }
   if (lane == 31) sums[warp] = before;
-  if (lane == 0) tops[warp] = top;
+  if (lane == 0) tops[warp] = top, lows[warp] = low, highs[warp] = high;
+  if (threadIdx.x == 0) found = -1;
   __syncthreads();
-  int all = sums[lane];
-  top = tops[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(FULL_MASK, all, o);
-    if (lane >= o) all += v;
-    top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+  int all = 0, r = before - own;
+  for (int w = 0; w < WARPS; ++w) {
+    r += w < warp ? sums[w] : 0;
+    all += sums[w];
+    top = fmaxf(top, tops[w]);
+    low = fminf(low, lows[w]);
+    high = fmaxf(high, highs[w]);
   }
-  int r = before - mine + (warp > 0 ? __shfl_sync(FULL_MASK, all, max(warp - 1, 0)) : 0);
   for (int t = from; t < to; ++t) {
-    if (takes_part(t)) {
-      A.rows[r] = t;
-      A.place[t] = r++;
-    } else {
-      A.place[t] = loss_state(A.ids, A.state, t, A.V) < 0 ? -2 : -1;
+    const bool part = takes_part(t);
+    const int place = part ? r++ : loss_state(A.ids, A.state, t, A.V) < 0 ? -2 : -1;
+    if (t == mine) found = place;
+    if (writes) {
+      if (part) A.rows[place] = t;
+      A.place[t] = place;
     }
   }
-  if (threadIdx.x == 31) {
-    *A.count = all;
-    if (A.by != nullptr) *A.by = top > 0.0f ? top : 1.0f;
-  }
+  __syncthreads();
+  const bool same = low == high && fabsf(low) < INFINITY;
+  return {found, all, same ? low : top > 0.0f ? top : 1.0f, same};
+}
+__device__ __forceinline__ void loss_plan_told(const LossPlanArgs& A, const LossPlan& p) {
+  *A.count = p.count;
+  *A.same = p.same;
+  *A.by = p.by;
 }
 
-// A block for each row: copies of those that take part, results of the others.  The last 256 blocks write the rows of
-// zeros behind the last one, up to the end of its tile.
+// One block numbers the rows that take part in ascending order.
+__global__ void __launch_bounds__(1024) loss_plan_kernel(const __grid_constant__ LossPlanArgs A) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const LossPlan p = loss_plan<1024>(A, -1, true);
+  if (threadIdx.x == 0) loss_plan_told(A, p);
+}
+
+// A block for each row: copies of those that take part, results of the others.  The last `tile_rows` blocks write the rows
+// of zeros behind the last one, up to the end of its tile.  PLANS: there was no plan, and each block makes it for itself, which
+// for up to LOSS_PLAN_ROWS rows takes less than a kernel before this one (128 rows: 1 us against 4).
+constexpr int LOSS_PLAN_ROWS = 1024;
+template <bool PLANS>
 __global__ void __launch_bounds__(128) loss_gather_kernel(const __grid_constant__ LossPlanArgs A) {
   grid_dep_wait();
   grid_dep_launch();
-  const int packs = A.H / 8;
-  int64_t r;
+  const int packs = A.H / 8, t = static_cast<int>(blockIdx.x);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  if (static_cast<int>(blockIdx.x) >= A.T) {
-    const int count = *A.count;
-    r = static_cast<int64_t>(count) + blockIdx.x - A.T;
-    if (r >= (count + 255) / 256 * 256) return;
+  LossPlan p{};
+  if constexpr (PLANS) {
+    p = loss_plan<128>(A, t, t == 0);
+    if (t == 0 && threadIdx.x == 0) loss_plan_told(A, p);
+  } else {
+    p = {t < A.T ? A.place[t] : -1, *A.count, *A.by, *A.same != 0};
+  }
+  const bool scales = A.scaled != nullptr && !p.same;
+  int64_t r = p.place;
+  if (t >= A.T) {
+    r = static_cast<int64_t>(p.count) + t - A.T;
+    if (r >= (p.count + A.tile_rows - 1) / A.tile_rows * A.tile_rows) return;
     for (int i = threadIdx.x; i < packs; i += 128) {
       reinterpret_cast<uint4*>(A.copy + r * A.H)[i] = zero;
-      if (A.scaled != nullptr) reinterpret_cast<uint4*>(A.scaled + r * A.H)[i] = zero;
+      if (scales) reinterpret_cast<uint4*>(A.scaled + r * A.H)[i] = zero;
     }
     return;
   }
-  const int64_t t = blockIdx.x;
-  r = A.place[t];
   if (r < 0) {
     if (threadIdx.x == 0 && A.loss != nullptr) A.loss[t] = r == -2 ? NAN : 0.0f;
-    if (threadIdx.x == 0 && A.g == nullptr && A.lse != nullptr) A.lse[t] = r == -2 ? NAN : 0.0f;
+    if (threadIdx.x == 0 && A.lse != nullptr) A.lse[t] = r == -2 ? NAN : 0.0f;
     if (A.dx != nullptr)
       for (int i = threadIdx.x; i < packs; i += 128) reinterpret_cast<uint4*>(A.dx + t * A.lddx)[i] = zero;
     return;
   }
-  const float by = A.g != nullptr ? A.g[t] / *A.by : 1.0f;
+  const float by = scales ? A.g[t] / p.by : 1.0f;
   for (int i = threadIdx.x; i < packs; i += 128) {
-    Pack<__nv_bfloat16, 8> v = reinterpret_cast<const Pack<__nv_bfloat16, 8>*>(A.x + t * A.ldx)[i];
+    const Pack<__nv_bfloat16, 8> v = reinterpret_cast<const Pack<__nv_bfloat16, 8>*>(A.x + t * A.ldx)[i];
     reinterpret_cast<Pack<__nv_bfloat16, 8>*>(A.copy + r * A.H)[i] = v;
-    if (A.scaled != nullptr) {
+    if (scales) {
       float f[8];
       unpack(v, f);
 #pragma unroll
@@ -688,29 +800,30 @@ struct LossDxArgs {
   __nv_bfloat16* dx;
   int64_t lddx, part;  // elements from one part to the next
   float s;
-  int H, splits;
+  int H, splits, k_piece, units, width, tile_rows;  // as LOSS_DX had them
 };
 
-// A block for each row: dx from its parts, added up in order.
+// dx from its parts, added up in order: 512 columns of a row a block, four a thread.
 __global__ void __launch_bounds__(128) loss_dx_kernel(const __grid_constant__ LossDxArgs A) {
   grid_dep_wait();
   grid_dep_launch();
   const int64_t r = blockIdx.x;
-  if (r >= *A.count) return;
+  const int count = *A.count, c = (blockIdx.y * 128 + threadIdx.x) * 4;
+  if (r >= count) return;
+  const int tiles = (count + A.tile_rows - 1) / A.tile_rows * ((A.H + A.width - 1) / A.width);
+  const int splits = loss_splits(tiles, A.k_piece, A.splits, A.units, A.tile_rows == 256);
+  if (c >= A.H) return;
   const int64_t t = A.rows[r];
   const float by = A.g[t] * A.s;
-  for (int i = threadIdx.x; i < A.H / 8; i += 128) {
-    float f[8] = {};
-    for (int p = 0; p < A.splits; ++p) {
-      const float4* at = reinterpret_cast<const float4*>(A.parts + p * A.part + r * A.H) + 2 * i;
-      const float4 a = at[0], b = at[1];
-      f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
-      f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= by;
-    reinterpret_cast<Pack<__nv_bfloat16, 8>*>(A.dx + t * A.lddx)[i] = pack<__nv_bfloat16>(f);
+  const float* at = A.parts + r * A.H + c;
+  float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int p = 0; p < splits; ++p, at += A.part) {
+    const float4 v = *reinterpret_cast<const float4*>(at);
+    f.x += v.x, f.y += v.y, f.z += v.z, f.w += v.w;
   }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(f.x * by, f.y * by), hi = __floats2bfloat162_rn(f.z * by, f.w * by);
+  *reinterpret_cast<uint2*>(A.dx + t * A.lddx + c) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 // dw of no rows.

@@ -288,7 +288,7 @@ class Exact:
 
 
 SHAPES = [(1, 1, 8), (1, 1000, 64), (3, 7, 72), (5, 257, 136), (64, 5003, 128), (128, 300, 520), (129, 255, 64), (129, 1, 8), (200, 256, 264),
-          (300, 1031, 72), (515, 2100, 40), (1000, 513, 1024)]
+          (300, 1031, 72), (515, 2100, 40), (1000, 513, 1024), (1300, 300, 64), (27, 4001, 1176), (40, 1000, 4104)]
 
 
 @pytest.mark.parametrize("T,V,H", SHAPES)
@@ -311,3 +311,14 @@ def test_distill(G, T, V, H, K, s):
     e.check_rows(o)
     for g in (torch.full((T,), 1 / 3, device="cuda"), _normal(_gen(1), T)):
         e.check_grad(G.distill_grad(x, w, ids, teacher, o["lse"], g, temperature=s), g)
+
+
+@pytest.mark.parametrize("T,V,H", [(2049, 140001, 16), (8300, 515, 24)])
+def test_pieces_of_the_vocabulary_and_slabs_of_rows(G, T, V, H):
+    """More logits than a piece of their differences holds, more rows than a slab of the tiles' sums."""
+    x, w, ids, _ = loss_case(T, V, H, 5)
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    e.check_rows(o)
+    g = torch.full((T,), 1 / T, device="cuda")
+    e.check_grad(G.cross_entropy_grad(x, w, ids, o["lse"], g), g)
