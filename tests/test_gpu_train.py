@@ -322,3 +322,362 @@ def test_pieces_of_the_vocabulary_and_slabs_of_rows(G, T, V, H):
     e.check_rows(o)
     g = torch.full((T,), 1 / T, device="cuda")
     e.check_grad(G.cross_entropy_grad(x, w, ids, o["lse"], g), g)
+
+
+# ------------------------------------------------------------------------------ where losses can go wrong
+@pytest.mark.parametrize("T", [20, 300])
+def test_rows_left_out_may_hold_anything(G, T):
+    """NaN and infinities in rows without an id reach nothing; all rows left out is zeros; an id beyond the vocabulary is NaN
+    for its row alone, and no gradient."""
+    x, w, ids, _ = loss_case(T, 700, 72, T)
+    ids[3], ids[7] = 700, 2 ** 31 - 1
+    ids[5] = -1
+    x[ids < 0] = math.nan
+    x[5, 3] = math.inf
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    e.check_rows(o)
+    assert o["loss"][3].isnan() and o["lse"][7].isnan() and (o["loss"][ids < 0] == 0).all() and (o["lse"][ids < 0] == 0).all()
+    g = torch.ones(T, device="cuda")
+    d = G.cross_entropy_grad(x, w, ids, o["lse"], g)
+    e.check_grad(d, g)
+    assert (d["dx"][ids < 0] == 0).all() and (d["dx"][3] == 0).all()
+    g[::2] = 0.0  # rows without weight take no part either, whatever their lse
+    lse = o["lse"].clone()
+    lse[::2] = math.nan
+    d = G.cross_entropy_grad(x, w, ids, lse, g)
+    e.check_grad(d, g)
+    assert (d["dx"][::2] == 0).all()
+    none = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    o = G.cross_entropy_rows(x, w, none)
+    assert (o["loss"] == 0).all() and (o["lse"] == 0).all()
+    out = dict(dx=torch.full((T, 72), 5.0, device="cuda").to(BF), dw=torch.full((700, 72), 5.0, device="cuda").to(BF))
+    d = G.cross_entropy_grad(x, w, none, o["lse"], torch.ones(T, device="cuda"), out=out)
+    assert (d["dx"] == 0).all() and (d["dw"] == 0).all()
+    empty = G.cross_entropy_grad(x[:0], w, none[:0], o["lse"][:0], o["lse"][:0], out=dict(dw=torch.full((700, 72), 5.0, device="cuda").to(BF)))
+    assert (empty["dw"] == 0).all() and empty["dx"].shape == (0, 72)
+    assert G.cross_entropy_rows(x[:0], w, none[:0])["loss"].numel() == 0
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_a_broken_row_keeps_to_itself(G, T):
+    """A NaN in a row that takes part: its loss, lse and dx, and what the formula makes of dw; no other row's."""
+    x, w, ids, _ = loss_case(T, 600, 64, T, skip=0.0)
+    x[4, 9] = math.nan
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    assert o["loss"][4].isnan() and o["lse"][4].isnan()
+    rest = torch.arange(T, device="cuda") != 4
+    near(o["loss"][rest], e.loss[rest], e.off_loss[rest])
+    g = torch.ones(T, device="cuda")
+    d = G.cross_entropy_grad(x, w, ids, o["lse"], g)
+    assert d["dx"][4].isnan().all() and not d["dx"][rest].isnan().any() and d["dw"].isnan().all()
+    r = Exact(x[rest], w, ids[rest])
+    d = G.cross_entropy_grad(x[rest].contiguous(), w, ids[rest].contiguous(), o["lse"][rest].contiguous(), g[rest])
+    r.check_grad(d, g[rest])
+
+
+def test_infinite_logits(G):
+    """A logit of -inf has no part in the sum; one of +inf makes lse infinite, as log of a sum with it is."""
+    w = torch.zeros(300, 8, device="cuda").to(BF)
+    x = torch.zeros(3, 8, device="cuda").to(BF)
+    x[:, 0] = 1.0
+    w[:, 0] = 1.0
+    w[7, 0], w[200, 0] = -math.inf, 2.0
+    ids = torch.tensor([200, 7, 3], dtype=torch.int32, device="cuda")
+    o = G.cross_entropy_rows(x, w, ids)
+    lse = math.log(298 * math.e + math.exp(2.0))
+    near(o["lse"], torch.full((3,), lse, device="cuda"), torch.full((3,), 1e-5, device="cuda"))
+    near(o["loss"], torch.tensor([lse - 2.0, math.inf, lse - 1.0], device="cuda"), torch.full((3,), 1e-5, device="cuda"))
+    w[9, 0] = math.inf
+    assert (G.cross_entropy_rows(x, w, ids)["lse"] == math.inf).all()
+
+
+def test_large_logits(G):
+    """Logits of thousands: the sum of exponentials is about the largest."""
+    x, w, ids, _ = loss_case(150, 1000, 64, 3)
+    x = (x.float() * 300).to(BF)
+    e = Exact(x, w, ids)
+    assert float(e.lse.abs().max()) > 2000
+    e.check_rows(G.cross_entropy_rows(x, w, ids))
+
+
+@pytest.mark.parametrize("T", [33, 260])
+def test_the_same_id_twice_and_few_tokens(G, T):
+    """A teacher that names a token several times, rows with one token, with none, with all -inf, and of one only probability."""
+    x, w, ids, teacher = loss_case(T, 500, 64, T, K=40)
+    ids[1, :] = 17
+    ids[2, 1:] = -1
+    ids[2, 0] = 499
+    ids[3] = -1
+    teacher[4] = -math.inf
+    ids[6, 5] = 500
+    ids[8, ::2] = ids[8, 1::2]
+    teacher[9] = 200.0 * torch.arange(40, device="cuda")  # all but one underflow
+    e = Exact(x, w, ids, teacher, 0.7)
+    o = G.distill_rows(x, w, ids, teacher, temperature=0.7)
+    e.check_rows(o)
+    assert o["loss"][3] == 0 and o["loss"][4] == 0
+    assert bool(o["loss"][6].isnan()) == (float(teacher[6, 5]) > -math.inf)  # an id beyond the vocabulary, if it is there at all
+    g = torch.ones(T, device="cuda")
+    e.check_grad(G.distill_grad(x, w, ids, teacher, o["lse"], g, temperature=0.7), g)
+
+
+@pytest.mark.parametrize("T", [33, 260])
+def test_a_teachers_id_beyond_the_vocabulary(G, T):
+    """It makes its row's loss and lse NaN and takes the row out of the gradients; one that the teacher rules out is not there."""
+    x, w, ids, teacher = loss_case(T, 500, 64, T + 1, K=7, skip=0.0)
+    ids[5, 2], teacher[5, 2] = 500, 1.0
+    ids[6, 3], teacher[6, 3] = 2 ** 31 - 1, -math.inf
+    e = Exact(x, w, ids, teacher)
+    o = G.distill_rows(x, w, ids, teacher)
+    e.check_rows(o)
+    assert o["loss"][5].isnan() and o["lse"][5].isnan() and not o["loss"][6].isnan()
+    g = torch.ones(T, device="cuda")
+    d = G.distill_grad(x, w, ids, teacher, o["lse"], g)
+    e.check_grad(d, g)
+    assert (d["dx"][5] == 0).all()
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_strides_gaps_and_parts_of_the_outputs(G, T):
+    """Rows inside wider tensors; the gaps stay as they are; dx alone, dw alone; dw on 16 bytes and no more."""
+    V, H = 333, 72
+    x, w, ids, _ = loss_case(T, V, H, 9)
+    for gap, off in ((8, 0), (24, 8), (56, 16)):
+        def wide(n, fill=None):
+            t = torch.full((n, H + gap), -7.0, device="cuda").to(BF)
+            if fill is not None:
+                t[:, off:off + H] = fill
+            return t, t[:, off:off + H]
+        xs, ws = wide(T, x)[1], wide(V, w)[1]
+        e = Exact(x, w, ids)
+        o = G.cross_entropy_rows(xs, ws, ids)
+        e.check_rows(o)
+        g = _normal(_gen(2), T)
+        (xb, dx), (wb, dw) = wide(T), wide(V)
+        full = G.cross_entropy_grad(xs, ws, ids, o["lse"], g, out=dict(dx=dx, dw=dw))
+        e.check_grad(full, g)
+        for buf in (xb, wb):
+            assert (torch.cat([buf[:, :off], buf[:, off + H:]], 1).float() == -7.0).all()
+        a = G.cross_entropy_grad(xs, ws, ids, o["lse"], g, dw=False)
+        b = G.cross_entropy_grad(xs, ws, ids, o["lse"], g, dx=False)
+        assert set(a) == {"dx"} and set(b) == {"dw"}
+        assert torch.equal(a["dx"], dx) and torch.equal(b["dw"], dw)
+
+
+@pytest.mark.parametrize("T,V,H", [(1, 1000, 64), (96, 5000, 264), (700, 3000, 136)])
+def test_the_same_call_gives_the_same_bits(G, T, V, H):
+    x, w, ids, teacher = loss_case(T, V, H, 4, K=20)
+    g = _normal(_gen(2), T)
+
+    def call():
+        o = G.distill_rows(x, w, ids, teacher)
+        return dict(o, **G.distill_grad(x, w, ids, teacher, o["lse"], g))
+
+    first = call()
+    for _ in range(5):
+        again = call()
+        assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_loss_gradients_against_differences(G, T):
+    """(f(x + e u) - f(x - e u)) / 2e of f = sum of g loss in 64 bits, along random directions of the rows and of the head."""
+    x, w, ids, teacher = loss_case(T, 300, 64, 6, K=8)
+    g, s = torch.rand(T, device="cuda", generator=_gen(3)) + 0.5, 1.5
+    o = G.distill_rows(x, w, ids, teacher, temperature=s)
+    d = G.distill_grad(x, w, ids, teacher, o["lse"], g, temperature=s)
+
+    def f(xx, ww):
+        return (Exact(xx, ww, ids, teacher, s).loss * g.double()).sum()
+
+    step = 1e-5
+    for key, at in (("dx", 0), ("dw", 1)):
+        u = _normal(_gen(7 + at), *d[key].shape).double()
+        args = [x.double(), w.double()]
+        up, down = list(args), list(args)
+        up[at], down[at] = args[at] + step * u, args[at] - step * u
+        want = float((f(*up) - f(*down)) / (2 * step))
+        got = float((d[key].double() * u).sum())
+        # each element of the gradient may be off by a rounding of dz and one of its own
+        assert abs(want - got) < 3 * HALF * float(d[key].double().norm() * u.norm()) / math.sqrt(u.numel()) + 1e-6 * abs(want) + 3 * HALF * float(d[key].double().norm())
+
+
+# ------------------------------------------------------------------------------ streams, graphs, neighbours
+def _step(G, x, r, ids, w, nw, nb, g, out=None):
+    n = G.layer_norm_rows(x, nw, bias=nb, residual=r)
+    o = G.cross_entropy_rows(n["y"], w, ids)
+    d = G.cross_entropy_grad(n["y"], w, ids, o["lse"], g)
+    e = G.layer_norm_grad(d["dx"], n["residual"], nw, n["mean"], n["rstd"])
+    return dict(loss=o["loss"], dw=d["dw"], y=n["y"], **e)
+
+
+def _step_case(T, V, H, seed):
+    g = _gen(seed)
+    x, w, ids, _ = loss_case(T, V, H, seed)
+    return dict(x=x, r=_normal(g, T, H, to=BF), ids=ids, w=w, nw=(1 + _normal(g, H, by=0.2)).to(BF), nb=_normal(g, H, by=0.1, to=BF),
+                g=torch.full((T,), 1.0 / T, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [60, 400])
+def test_a_step_of_the_end_of_a_model(G, T):
+    """Norm, head, loss and back to the norm's input, against the whole in 64 bits by automatic differentiation."""
+    c = _step_case(T, 900, 136, T)
+    o = _step(G, **c)
+    leaf = {k: c[k].double().requires_grad_() for k in ("x", "w", "nw", "nb")}
+    h = leaf["x"] + c["r"].double()
+    v = (h - h.mean(1, keepdim=True)) / (h.var(1, unbiased=False, keepdim=True) + 1e-5).sqrt()
+    z = (v * leaf["nw"] + leaf["nb"]) @ leaf["w"].T
+    ok = c["ids"] >= 0
+    loss = (torch.logsumexp(z, 1) - z.gather(1, c["ids"].clamp(min=0).long()[:, None])[:, 0]) * ok
+    (loss * c["g"].double()).sum().backward()
+    # y is rounded before the head, dz and the gradient of y before what follows: a few roundings of the norms
+    for got, want in ((o["loss"], loss), (o["dw"], leaf["w"].grad), (o["dx"], leaf["x"].grad), (o["dweight"], leaf["nw"].grad), (o["dbias"], leaf["nb"].grad)):
+        assert float((got.double() - want).norm()) <= 4 * HALF * float(want.norm())
+
+
+def test_on_another_stream(G):
+    c, side = _step_case(200, 600, 72, 1), torch.cuda.Stream()
+    want = _step(G, **c)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = _step(G, **c)
+    side.synchronize()
+    assert all(torch.equal(want[k], got[k]) for k in want)
+    o = G.cross_entropy_rows(want["y"], c["w"], c["ids"], stream=side)
+    d = G.cross_entropy_grad(want["y"], c["w"], c["ids"], o["lse"], c["g"], stream=side)
+    n = G.layer_norm_rows(c["x"], c["nw"], bias=c["nb"], residual=c["r"], stream=side)
+    side.synchronize()
+    assert torch.equal(o["loss"], want["loss"]) and torch.equal(d["dw"], want["dw"]) and torch.equal(n["y"], want["y"])
+
+
+def test_two_streams_at_once(G):
+    """Calls on two streams have workspaces of their own and do not disturb one another."""
+    cases = [_step_case(T, 4000, 136, T) for T in (90, 500)]
+    want = [_step(G, **c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(_step(G, **cases[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            assert all(torch.equal(want[i][k], o[k]) for k in o)
+    assert G.tail_errors() == 0
+
+
+@pytest.mark.parametrize("T", [60, 400])
+def test_captured_and_replayed(G, T):
+    """A captured step follows its inputs from replay to replay, rows that are left out among them."""
+    c = _step_case(T, 900, 72, 2)
+    _step(G, **c)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = _step(G, **c)
+    for seed in (3, 4):
+        n = _step_case(T, 900, 72, seed)
+        for k in c:
+            c[k].copy_(n[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = _step(G, **n)
+        assert all(torch.equal(want[k], out[k]) for k in want)
+
+
+def test_a_teacher_from_the_sampler(G):
+    """What ``Sampler.logprobs`` reports of a teacher's rows goes to the distillation of a student as it is."""
+    V, H, T, K = 5000, 128, 48, 20
+    x, w, _, _ = loss_case(T, V, H, 8)
+    logits = G.project_rows(x, w)
+    with G.Sampler(device=0, max_slots=T, max_vocab=V, max_rows=T) as s:
+        top = s.logprobs(logits, top_n=K)
+        torch.cuda.synchronize()
+    student = (w.float() + 0.02 * _normal(_gen(1), V, H)).to(BF)
+    ids, teacher = top["top_ids"], top["top_lps"]
+    o = G.distill_rows(x, student, ids, teacher)
+    e = Exact(x, student, ids, teacher)
+    e.check_rows(o)
+    g = torch.full((T,), 1 / T, device="cuda")
+    e.check_grad(G.distill_grad(x, student, ids, teacher, o["lse"], g), g)
+    same = G.distill_rows(x, w, ids, teacher)["loss"]
+    assert (same < o["loss"]).float().mean() > 0.5 and (same > -1e-4).all()
+
+
+def test_between_other_operators_of_a_stream(G):
+    """Norm, projection, losses and draws behind one another, each set up while the one before runs: the same as one by one."""
+    g = _gen(12)
+    T, V, H = 64, 3000, 264
+    x, w, ids, _ = loss_case(T, V, H, 12)
+    nw = torch.ones(H, device="cuda").to(BF)
+    u = torch.rand(T, generator=g, device="cuda")
+
+    def chain(wait):
+        out = []
+        for _ in range(6):
+            n = G.norm_rows(x, nw)["y"]
+            wait()
+            l = G.project_rows(n, w)
+            wait()
+            o = G.cross_entropy_rows(n, w, ids)
+            wait()
+            i = G.draw_rows(l, u)["ids"]
+            wait()
+            d = G.cross_entropy_grad(n, w, i, o["lse"], u)
+            wait()
+            out += [n, l, o["loss"], i, d["dx"], d["dw"]]
+        return out
+
+    want = chain(torch.cuda.synchronize)
+    got = chain(lambda: None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_the_c_names_write_into_the_callers_tensors(G):
+    T, V, H = 30, 400, 64
+    x, w, ids, teacher = loss_case(T, V, H, 15, K=6)
+    one = ids[:, 0].contiguous()
+    g = torch.ones(T, device="cuda")
+    f = lambda *shape, t=F32: torch.empty(*shape, dtype=t, device="cuda")  # noqa: E731
+    ws = lambda K, grad: f(G.strata_loss_workspace(T, V, H, K, grad), t=torch.uint8)  # noqa: E731
+    loss, lse, dx, dw = f(T), f(T), f(T, H, t=BF), f(V, H, t=BF)
+    G.strata_cross_entropy_rows(x, w, one, loss, lse, ws(0, False))
+    G.strata_cross_entropy_grad(x, w, one, lse, g, dx, dw, ws(0, True))
+    o = G.cross_entropy_rows(x, w, one)
+    d = G.cross_entropy_grad(x, w, one, o["lse"], g)
+    assert torch.equal(loss, o["loss"]) and torch.equal(lse, o["lse"]) and torch.equal(dx, d["dx"]) and torch.equal(dw, d["dw"])
+    G.strata_distill_rows(x, w, ids, teacher, 2.0, loss, lse, ws(6, False))
+    G.strata_distill_grad(x, w, ids, teacher, 2.0, lse, g, dx, dw, ws(6, True))
+    o = G.distill_rows(x, w, ids, teacher, temperature=2.0)
+    d = G.distill_grad(x, w, ids, teacher, o["lse"], g, temperature=2.0)
+    assert torch.equal(loss, o["loss"]) and torch.equal(lse, o["lse"]) and torch.equal(dx, d["dx"]) and torch.equal(dw, d["dw"])
+    mean, rstd, y, nw = f(T), f(T), f(T, H, t=BF), torch.ones(H, device="cuda").to(BF)
+    G.strata_layer_norm_rows(x, nw, y=y, mean=mean, rstd=rstd)
+    n = G.layer_norm_rows(x, nw)
+    assert torch.equal(y, n["y"]) and torch.equal(mean, n["mean"]) and torch.equal(rstd, n["rstd"])
+    dn, db = f(H, t=BF), f(H, t=BF)
+    G.strata_layer_norm_grad(y, x, nw, mean, rstd, dx=dx, dweight=dn, dbias=db, workspace=f(G.strata_layer_norm_workspace(T, H), t=torch.uint8))
+    d = G.layer_norm_grad(y, x, nw, mean, rstd)
+    assert torch.equal(dx, d["dx"]) and torch.equal(dn, d["dweight"]) and torch.equal(db, d["dbias"])
+
+
+def test_refusals_on_tensors(G):
+    x, w, ids, teacher = loss_case(8, 100, 64, 1, K=4)
+    one, lse = ids[:, 0].contiguous(), torch.zeros(8, device="cuda")
+    for call in (lambda: G.cross_entropy_rows(x[:, :60], w[:, :60], one), lambda: G.cross_entropy_rows(x, w[:, 8:], one),
+                 lambda: G.cross_entropy_rows(x, w, one[:4]), lambda: G.cross_entropy_rows(x.t(), w, one),
+                 lambda: G.distill_rows(x, w, ids, teacher[:, :3]), lambda: G.distill_rows(x, w, ids, teacher, temperature=0.0),
+                 lambda: G.cross_entropy_grad(x, w, one, lse[:3], lse), lambda: G.cross_entropy_grad(x, w, one, lse, lse, dx=False, dw=False),
+                 lambda: G.layer_norm_grad(x, x, x[0], lse, lse[:2]), lambda: G.layer_norm_rows(x, x[0, :60])):
+        with pytest.raises((ValueError, G.StrataError)):
+            call()
+    for call in (lambda: G.cross_entropy_rows(x, w, one.long()), lambda: G.cross_entropy_rows(x, w.float(), one),
+                 lambda: G.distill_rows(x, w, ids, teacher.to(BF)), lambda: G.layer_norm_rows(x, x[0].float())):
+        with pytest.raises(TypeError):
+            call()
+    assert G.tail_errors() == 0
