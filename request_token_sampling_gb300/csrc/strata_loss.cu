@@ -46,9 +46,11 @@ cudaError_t find_device(Device& d) {
   for (bool pair : {false, true}) {
     shared(kernel_for<strata::LOSS_SUMS>(pair), strata::LOSS_SUMS, pair);
     shared(kernel_for<strata::LOSS_DIFFS>(pair), strata::LOSS_DIFFS, pair);
-    shared(kernel_for<strata::LOSS_DX>(pair), strata::LOSS_DX, pair);
   }
   shared(strata::loss_kernel<strata::LOSS_DW, true>, strata::LOSS_DW, true);
+  shared(strata::loss_kernel<strata::LOSS_DX, true>, strata::LOSS_DX, true);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(strata::loss_both_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, strata::loss_smem(strata::LOSS_DW, false));
   return e;
 }
 
@@ -84,6 +86,7 @@ bool map_rows(const Device& dev, CUtensorMap* m, bool f32, const void* p, int64_
 // ------------------------------------------------------------------------------ a call's plan
 // It goes by the sizes alone, so that the workspace's size can be asked for without a device.
 constexpr int SMS = 152, PAIRS = SMS / 2;
+constexpr int DX_BLOCKS = 64;             // of few rows' both products, with dw's in the others (96 x 248,320 x 2,048, the step, us: 40 729, 52 695, 64 664, 76 726)
 constexpr int ALONE_ROWS = 128;           // a call with more works by pairs of SMs, on a copy of the rows that take part
 constexpr int SLAB_ROWS = 8192;           // whose tiles' sums are held at a time
 constexpr int64_t PIECE_BYTES = int64_t{512} << 20, PARTS_BYTES = int64_t{256} << 20;
@@ -266,7 +269,6 @@ strata::LossArgs products_args(const Loss& C, const Plan& P, uint32_t* errors) {
   A.a_rows = std::min(128, (C.T + 7) / 8 * 8);
   A.splits = P.splits;
   A.k_piece = P.piece / 64;
-  A.units = P.pair ? PAIRS : SMS;
   return A;
 }
 
@@ -343,6 +345,8 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
     Run run{C.stream, overlaps};
     launch_plan(run, C, P, g, nullptr, nullptr, dx, lddx);
     strata::LossArgs A = products_args(C, P, errors);
+    const int dx_blocks = dx == nullptr ? 0 : dw == nullptr ? SMS : DX_BLOCKS;  // of few rows
+    A.units = P.pair ? PAIRS : dx_blocks;
     A.lse = lse;
     A.wide = !misaligned(dw, 32) && lddw % 16 == 0 && C.H % 16 == 0;
     A.by = at<float>(C, P.by);
@@ -364,11 +368,15 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
       A.n_tiles = static_cast<int>(across);
       A.out = static_cast<__nv_bfloat16*>(dw);
       A.ldo = lddw;
+      A.add = v0 > 0;
+      if (!P.pair) {
+        run(strata::loss_both_kernel, SMS, strata::LOSS_THREADS, strata::loss_smem(strata::LOSS_DW, false), 1, mds, mxo, mxs, md, mwo, mdx, A, A, dx_blocks);
+        continue;
+      }
       if (dw != nullptr)
         run.products<strata::LOSS_DW>(strata::loss_kernel<strata::LOSS_DW, true>, true, tiles_of(A.columns, 256) * across, mds, mxo, mxs, mxs, A);
-      A.add = v0 > 0;
       if (dx != nullptr)
-        run.products<strata::LOSS_DX>(kernel_for<strata::LOSS_DX>(P.pair), P.pair, row_tiles * across * P.splits, md, mwo, mwo, mdx, A);
+        run.products<strata::LOSS_DX>(strata::loss_kernel<strata::LOSS_DX, true>, true, row_tiles * across * P.splits, md, mwo, mwo, mdx, A);
     }
     if (dx != nullptr) {
       const strata::LossDxArgs D{A.count, A.rows, at<float>(C, P.dx), g, static_cast<__nv_bfloat16*>(dx), lddx, static_cast<int64_t>(P.rows_pad) * C.H,

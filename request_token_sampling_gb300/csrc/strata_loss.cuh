@@ -59,7 +59,7 @@ struct LossArgs {
   int row0, rows_most;    // rows row0 .. of this launch
   int v0, columns;        // the piece of the vocabulary
   int bn, n_tiles;        // columns of a tile, and tiles of them
-  int a_rows;             // of A that one SM's tile brings; the accumulator's other rows are not looked at
+  int a_rows;             // rows that one SM's tile brings where they are A; the accumulator's other rows are not looked at
   int splits, rows_pad;   // LOSS_DX: parts that a piece may be cut into, and rows of each
   int k_piece, units;     // steps of 64 ids in a piece, and tiles that run at a time
   int add;                // LOSS_DX: onto what is there
@@ -141,10 +141,10 @@ struct LossIds {
   __device__ __forceinline__ void advance() { next = ++at < K ? ids[at] : LOSS_NO_ID; }
 };
 
+// As block `block` of `blocks`.  Maps: A, B, B of scaled rows (LOSS_DW), results (LOSS_DX).
 template <int MODE, bool PAIR>
-__global__ void __launch_bounds__(LOSS_THREADS, 1)
-    loss_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mc,
-                const __grid_constant__ CUtensorMap mo, const __grid_constant__ LossArgs A) {
+__device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& mo, const LossArgs& A,
+                                              int block, int blocks) {
   constexpr int STAGES = loss_stages(MODE, PAIR), STAGE = loss_stage_bytes(PAIR), TILE_M = PAIR ? 256 : 128;
   constexpr bool A_OUTER = MODE == LOSS_DW, B_OUTER = MODE == LOSS_DW || MODE == LOSS_DX;
   extern __shared__ uint8_t raw[];
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
     splits = loss_splits(outer * inner, A.k_piece, A.splits, A.units, PAIR);
   }
   const int per_split = outer * inner;
-  int tiles = per_split * splits, first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+  int tiles = per_split * splits, first = PAIR ? block / 2 : block, step = PAIR ? blocks / 2 : blocks;
   // Few rows: dw is bound by its writing, and a pair that writes one tile after another of the same ids leaves memory fuller
   // pages (96 rows, 1 GB: 262 us, by turns 283; with 32 bytes a store 247).  With more rows the pairs' parts of d would
   // not fit in L2 together.
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
   uint32_t turn = 0;  // tiles so far, of the issuing warp and of those that write
   if (warp == 0) {
     asm volatile("fence.proxy.async;" ::: "memory");  // rows and d were written by ordinary stores of kernels before
-    const uint32_t bytes = static_cast<uint32_t>(PAIR ? 2 * (128 + half) : A.a_rows + half) * LOSS_LINE;
+    const uint32_t bytes = static_cast<uint32_t>(PAIR ? 2 * (128 + half) : (MODE == LOSS_DW ? 128 : A.a_rows) + half) * LOSS_LINE;
     const CUtensorMap* mx = MODE == LOSS_DW && *A.same == 0 ? &mc : &mb;
     for (int tile = first; tile < tiles && alive; tile += step) {
       int o, i, from, to;
@@ -525,6 +525,26 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
     else
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
   }
+}
+
+template <int MODE, bool PAIR>
+__global__ void __launch_bounds__(LOSS_THREADS, 1)
+    loss_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mc,
+                const __grid_constant__ CUtensorMap mo, const __grid_constant__ LossArgs A) {
+  loss_products<MODE, PAIR>(ma, mb, mc, mo, A, blockIdx.x, gridDim.x);
+}
+
+// Both products of few rows: dw is bound by writing to memory, dx by reading w, so blocks of both kinds (`dx_blocks` of dx,
+// spread evenly) keep memory busy both ways at once.
+__global__ void __launch_bounds__(LOSS_THREADS, 1)
+    loss_both_kernel(const __grid_constant__ CUtensorMap wa, const __grid_constant__ CUtensorMap wb, const __grid_constant__ CUtensorMap wc,
+                     const __grid_constant__ CUtensorMap xa, const __grid_constant__ CUtensorMap xb, const __grid_constant__ CUtensorMap xo,
+                     const __grid_constant__ LossArgs W, const __grid_constant__ LossArgs X, int dx_blocks) {
+  const int block = static_cast<int>(blockIdx.x), blocks = static_cast<int>(gridDim.x), before = block * dx_blocks / blocks;
+  if ((block + 1) * dx_blocks / blocks > before)
+    loss_products<LOSS_DX, false>(xa, xb, xb, xo, X, before, dx_blocks);
+  else
+    loss_products<LOSS_DW, false>(wa, wb, wc, wc, W, block - before, blocks - dx_blocks);
 }
 
 // ------------------------------------------------------------------------------ a teacher's tokens
