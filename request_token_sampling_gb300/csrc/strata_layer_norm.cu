@@ -14,13 +14,47 @@ namespace {
 
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
-// 16 bytes at a time where the width, every stride and every address allow it.
-struct Packs {
+// How a call's rows lie: all on 16 bytes, with a width of whole packs (`packed`); or anywhere, but in all tensors the same way
+// (`alike`: packs on the boundaries).
+struct Lie {
+  const void* first = nullptr;
+  int64_t ld = 0;
   int T, n;
-  bool all;
-  Packs(int T, int H, int esz) : T(T), n(16 / esz), all(H % (16 / esz) == 0) {}
-  void look(const void* p, int64_t ld) { all = all && (p == nullptr || (!misaligned(p, 16) && (T == 1 || ld % n == 0))); }
+  bool packed, alike = true;
+  Lie(const void* x, int64_t ldx, int T, int H, int esz) : first(x), ld(ldx), T(T), n(16 / esz), packed(H % (16 / esz) == 0) { look(x, ldx); }
+  void look(const void* p, int64_t ldp) {
+    if (p == nullptr) return;
+    packed = packed && !misaligned(p, 16) && (T == 1 || ldp % n == 0);
+    alike = alike && (reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(first)) % 16 == 0 && (T == 1 || (ldp - ld) % n == 0);
+  }
+  void look_column(const void* p) { packed = packed && !misaligned(p, 16); }
 };
+
+constexpr int SMS = 152, SM_BYTES = 224 * 1024;          // shared memory of an SM for rows on their way
+constexpr int BLOCK_WIDTH = strata::LAYER_NORM_RING_THREADS * 16, WARP_WIDTH = 32 * 16;
+
+// Registers of a kernel's thread, for the number of its blocks on an SM; found once.
+template <typename K>
+int registers(K kernel) {
+  cudaFuncAttributes a;
+  return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 128;
+}
+
+// How rows go through rings: a block's threads (PER packs each, and the warp of the copies), blocks of an SM (as many as its
+// registers, threads and shared memory hold, with two rows on their way at least), and rows on their way.  `ring`: bytes of a
+// row in it, `beside`: of the weight.
+struct RingShape {
+  int threads, blocks, depth;
+  size_t smem;
+  RingShape(int packs, int per, int copier, int ring, int beside, int regs) {
+    threads = ((packs + per - 1) / per + 31) / 32 * 32 + copier;
+    blocks = std::max(1, std::min({8, 65536 / ((regs + 7) / 8 * 8 * threads), 2048 / threads, SM_BYTES / (2 * ring + beside + 1024)}));
+    depth = std::max(2, std::min(strata::LAYER_NORM_RING, (SM_BYTES / blocks - 1024 - beside) / ring));
+    smem = static_cast<size_t>(depth) * ring + beside;
+  }
+};
+// A multiple of eight that leaves each block some rows, or a block for each row.
+int ring_grid(int T, int blocks) { return T <= SMS ? T : std::min(SMS * blocks, std::max(SMS, T / 8 / 8 * 8)); }
 
 // The shape of a call, as the root-mean-square norm's: many rows are bound by HBM, a thread takes up to 16
 // elements, so that enough bytes are on their way; few rows are bound by latency: a row goes to as many threads as it has packs.
@@ -37,66 +71,88 @@ cudaError_t launch_forward(const strata::LayerNormArgs& A, int least, bool overl
     return strata::Launch(A.T, 1024, 0, stream, overlaps)(strata::layer_norm_wide_kernel<E>, A);
   }
 }
-template <typename E>
-cudaError_t launch_forward(const strata::LayerNormArgs& A, bool packed, int sms, bool overlaps, void* stream) {
+// Many rows that start anywhere.
+template <typename E, int PER>
+cudaError_t launch_ring(strata::LayerNormArgs A, bool overlaps, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
-  const int packs = A.H / (packed ? N : 1);
-  const int least = A.T < 2 * sms ? 1 : packs > 64 ? 4 : packs > 32 ? 2 : 1;
-  return packed ? launch_forward<E, N, 1>(A, least, overlaps, stream) : launch_forward<E, 1, 1>(A, least, overlaps, stream);
+  if constexpr (N * PER <= 16) {
+    if ((A.H / N + PER - 1) / PER > strata::LAYER_NORM_RING_THREADS) return launch_ring<E, PER * 2>(A, overlaps, stream);
+    const int row = (A.H * static_cast<int>(sizeof(E)) + 15) / 16 * 16;
+    const auto kernel = strata::layer_norm_ring_kernel<E, PER>;
+    static const int regs = registers(kernel);
+    const RingShape ring(A.H / N, PER, 32, row * (A.residual != nullptr ? 2 : 1), 2 * row, regs);
+    A.depth = ring.depth;
+    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES); e != cudaSuccess) return e;
+    return strata::Launch(ring_grid(A.T, ring.blocks), ring.threads, ring.smem, stream, overlaps)(kernel, A);
+  } else {
+    return cudaErrorInvalidValue;  // not reached: wider rows have their own kernels
+  }
+}
+template <typename E>
+cudaError_t launch_forward(const strata::LayerNormArgs& A, const Lie& lie, bool overlaps, void* stream) {
+  constexpr int N = 16 / static_cast<int>(sizeof(E));
+  if (A.T >= 4 * SMS && A.H > WARP_WIDTH && A.H <= BLOCK_WIDTH && lie.alike && !lie.packed) return launch_ring<E, 1>(A, overlaps, stream);
+  const int packs = A.H / (lie.packed ? N : 1);
+  const int least = A.T < 2 * SMS ? 1 : packs > 64 ? 4 : packs > 32 ? 2 : 1;
+  return lie.packed ? launch_forward<E, N, 1>(A, least, overlaps, stream) : launch_forward<E, 1, 1>(A, least, overlaps, stream);
 }
 
-// Groups of rows whose sums over rows are kept apart, until the last kernel adds them up: a block of 152 SMs has one, and
-// narrow rows several blocks to an SM.  Rows too wide for that have fewer, for the sake of the workspace.
-constexpr int SMS = 152, WIDE_GROUPS = 16, BLOCK_WIDTH = strata::LAYER_NORM_GRAD_THREADS * 16, WARP_WIDTH = 32 * 16;
+// Groups of rows whose sums over rows are kept apart, until the last kernel adds them up: those of a block.  Rows too wide for a
+// ring have few, for the sake of the workspace.
+constexpr int WIDE_GROUPS = 16;
 int grad_groups(int T, int H) {
   if (H > BLOCK_WIDTH) return std::min(T, WIDE_GROUPS);
-  if (H > WARP_WIDTH) return std::min(T, SMS * (H > 4096 ? 1 : H > 2048 ? 2 : 4));
-  return std::min((T + strata::LAYER_NORM_GRAD_WARPS - 1) / strata::LAYER_NORM_GRAD_WARPS, SMS * 4);
+  if (H > WARP_WIDTH) return ring_grid(T, 4);
+  return std::min((T + strata::LAYER_NORM_GRAD_WARPS - 1) / strata::LAYER_NORM_GRAD_WARPS, SMS * 2);
 }
 
-// Narrow rows by warps; wider ones that do not lie on 16 bytes by a block, element by element.
-template <typename E, int N, int PER>
+// Narrow rows by warps; wider ones that lie in no common way by a block, element by element.
+template <typename E, int N, int PER, bool SHIFT>
 cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, void* stream) {
   if constexpr (N * PER <= 16) {
     const int need = (A.H / N + PER - 1) / PER;
     if (A.H <= WARP_WIDTH) {
-      if (need > 32) return launch_rows<E, N, PER * 2>(A, overlaps, stream);
-      return strata::Launch(A.groups, 32 * strata::LAYER_NORM_GRAD_WARPS, static_cast<size_t>(A.H) * 8, stream, overlaps)(
-          strata::layer_norm_grad_kernel<E, N, PER, false>, A);
+      if (need > 32) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, stream);
+      return strata::Launch(A.groups, 32 * strata::LAYER_NORM_GRAD_WARPS, static_cast<size_t>((A.H + N - 1) / N * N) * 8, stream, overlaps)(
+          strata::layer_norm_grad_kernel<E, N, PER, false, SHIFT>, A);
     }
-    if (need > strata::layer_norm_grad_most_threads(N, PER)) return launch_rows<E, N, PER * 2>(A, overlaps, stream);
+    if (need > strata::layer_norm_grad_most_threads(N, PER)) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, stream);
     if constexpr (N == 1)
-      return strata::Launch(A.groups, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::layer_norm_grad_kernel<E, N, PER, true>, A);
+      return strata::Launch(A.groups, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::layer_norm_grad_kernel<E, N, PER, true, false>, A);
   }
   return cudaErrorInvalidValue;  // not reached: wider rows have their own kernels
 }
 
-// Rows on 16 bytes by a block: as many rows on their way as an SM's shared memory has room for beside its other blocks.
-template <typename E, int PER>
-cudaError_t launch_ring(strata::LayerNormGradArgs A, bool overlaps, void* stream) {
-  constexpr int N = 16 / static_cast<int>(sizeof(E)), SM_BYTES = 220 * 1024;
+// Rows through a ring: as many on their way as an SM's shared memory has room for beside its other blocks.
+template <typename E, int PER, bool SHIFT>
+cudaError_t launch_ring(strata::LayerNormGradArgs& A, bool overlaps, void* stream) {
+  constexpr int N = 16 / static_cast<int>(sizeof(E));
   if constexpr (N * PER <= 16) {
     const int need = (A.H / N + PER - 1) / PER;
-    if (need > strata::LAYER_NORM_GRAD_THREADS) return launch_ring<E, PER * 2>(A, overlaps, stream);
-    const int row = A.H * static_cast<int>(sizeof(E)) * (A.dresidual != nullptr ? 3 : 2), blocks = std::max(1, (A.groups + SMS - 1) / SMS);
-    A.depth = std::max(1, std::min(strata::LAYER_NORM_RING, (SM_BYTES / blocks - 2048) / row));
-    const auto kernel = strata::layer_norm_ring_kernel<E, PER>;
+    if (need > strata::LAYER_NORM_RING_THREADS) return launch_ring<E, PER * 2, SHIFT>(A, overlaps, stream);
+    const int row = (A.H * static_cast<int>(sizeof(E)) + 15) / 16 * 16;
+    const auto kernel = strata::layer_norm_grad_ring_kernel<E, PER, SHIFT>;
+    static const int regs = registers(kernel);
+    const RingShape ring(A.H / N, PER, strata::layer_norm_copier(N, PER), row * (A.dresidual != nullptr ? 3 : 2), row, regs);
+    A.depth = ring.depth;
+    A.groups = std::min(A.groups, ring_grid(A.T, ring.blocks));
     if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES); e != cudaSuccess) return e;
-    return strata::Launch(A.groups, (need + 31) / 32 * 32, static_cast<size_t>(A.depth) * row, stream, overlaps)(kernel, A);
+    return strata::Launch(A.groups, ring.threads, ring.smem, stream, overlaps)(kernel, A);
   } else {
     return cudaErrorInvalidValue;  // not reached: wider rows have their own kernels
   }
 }
 
 template <typename E>
-cudaError_t launch_grad(const strata::LayerNormGradArgs& A, bool packed, bool overlaps, void* stream) {
+cudaError_t launch_grad(strata::LayerNormGradArgs A, const Lie& lie, bool overlaps, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   cudaError_t e = cudaSuccess;
   if (A.T > 0) {
     if (A.H <= BLOCK_WIDTH) {
-      e = !packed               ? launch_rows<E, 1, 1>(A, overlaps, stream)
-          : A.H > WARP_WIDTH ? launch_ring<E, 1>(A, overlaps, stream)
-                             : launch_rows<E, N, 1>(A, overlaps, stream);
+      const bool warps = A.H <= WARP_WIDTH;
+      e = lie.packed  ? (warps ? launch_rows<E, N, 1, false>(A, overlaps, stream) : launch_ring<E, 1, false>(A, overlaps, stream))
+          : lie.alike ? (warps ? launch_rows<E, N, 1, true>(A, overlaps, stream) : launch_ring<E, 1, true>(A, overlaps, stream))
+                      : launch_rows<E, 1, 1, false>(A, overlaps, stream);
       overlaps = true;
     } else {  // the sums first: dx may be dy or x
       if (A.part != nullptr) {
@@ -112,7 +168,9 @@ cudaError_t launch_grad(const strata::LayerNormGradArgs& A, bool packed, bool ov
     }
   }
   if (e != cudaSuccess || A.part == nullptr) return e;
-  return strata::Launch((A.H + 31) / 32, 1024, 0, stream, overlaps)(strata::layer_norm_sum_kernel<E>, A);
+  strata::Launch launch((A.H + 31) / 32, 1024, 0, stream, overlaps);
+  launch.cfg.gridDim.y = 2;
+  return launch(strata::layer_norm_sum_kernel<E>, A);
 }
 
 }  // namespace
@@ -133,20 +191,17 @@ extern "C" int strata_layer_norm_rows(const void* x, int64_t ldx, const void* re
   if (misaligned(x, esz) || misaligned(residual, esz) || misaligned(weight, esz) || misaligned(bias, esz) || misaligned(residual_out, esz) ||
       misaligned(y, esz) || misaligned(mean, 4) || misaligned(rstd, 4))
     return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
-  strata::LayerNormArgs A{x, residual, weight, bias, residual_out, y, mean, rstd, ldx, ldr, ldro, ldy, T, H, eps};
-  uint32_t* errors = nullptr;
+  strata::LayerNormArgs A{x, residual, weight, bias, residual_out, y, mean, rstd, ldx, ldr, ldro, ldy, nullptr, T, H, eps, 0};
   int device = 0, sms = 0;
-  if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
-  Packs packs(T, H, static_cast<int>(esz));
-  packs.look(x, ldx);
-  packs.look(residual, ldr);
-  packs.look(weight, 0);
-  packs.look(bias, 0);
-  packs.look(residual_out, ldro);
-  packs.look(y, ldy);
+  if (const int rc = strata::tail_device(&device, &A.errors, &sms); rc != STRATA_OK) return rc;
+  Lie lie(x, ldx, T, H, static_cast<int>(esz));
+  lie.look(residual, ldr);
+  lie.look(residual_out, ldro);
+  lie.look(y, ldy);
+  lie.look_column(weight);
+  lie.look_column(bias);
   const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
-    return dtype == STRATA_DTYPE_F32 ? launch_forward<float>(A, packs.all, sms, overlaps, stream)
-                                     : launch_forward<__nv_bfloat16>(A, packs.all, sms, overlaps, stream);
+    return dtype == STRATA_DTYPE_F32 ? launch_forward<float>(A, lie, overlaps, stream) : launch_forward<__nv_bfloat16>(A, lie, overlaps, stream);
   });
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_layer_norm_rows: %s", cudaGetErrorString(e));
 }
@@ -183,19 +238,18 @@ extern "C" int strata_layer_norm_grad(const void* dy, int64_t lddy, const void* 
   uint32_t* errors = nullptr;
   int device = 0, sms = 0;
   if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
-  Packs packs(T, H, static_cast<int>(esz));
-  packs.look(dy, lddy);
-  packs.look(x, ldx);
-  packs.look(weight, 0);
-  packs.look(dresidual, lddr);
-  packs.look(dx, lddx);
+  Lie lie(x, ldx, T, H, static_cast<int>(esz));
+  lie.look(dy, lddy);
+  lie.look(dresidual, lddr);
+  lie.look(dx, lddx);
+  lie.look_column(weight);
   // without rows the sums are those of no groups; the workspace is not touched
   float* part = !sums ? nullptr : T > 0 ? static_cast<float*>(workspace) : static_cast<float*>(dweight != nullptr ? dweight : dbias);
   const strata::LayerNormGradArgs A{dy, x, weight, dresidual, mean, rstd, dx, dweight, dbias, part, errors, lddy, ldx, lddr, lddx, T, H,
                                     T > 0 ? grad_groups(T, H) : 0, 0};
   const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
-    return dtype == STRATA_DTYPE_F32 ? launch_grad<float>(A, packs.all, overlaps, stream)
-                                     : launch_grad<__nv_bfloat16>(A, packs.all, overlaps, stream);
+    return dtype == STRATA_DTYPE_F32 ? launch_grad<float>(A, lie, overlaps, stream)
+                                     : launch_grad<__nv_bfloat16>(A, lie, overlaps, stream);
   });
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_layer_norm_grad: %s", cudaGetErrorString(e));
 }

@@ -11,13 +11,46 @@
 
 namespace strata {
 
+// How a row that starts anywhere is cut: packs of N elements on the 16-byte boundaries, and up to 2 (N - 1) elements before the
+// first and behind the last, which go one to a thread (`edge`: this one's column, or -1).  SHIFT false: it starts on 16 bytes
+// and ends with a pack.  Rows that are a multiple of eight apart are cut alike, so that a thread that goes through such
+// rows keeps its columns.
+template <typename E, int N, bool SHIFT>
+struct RowCut {
+  int head = 0, packs, edge = -1, edges = 0;
+  __device__ __forceinline__ RowCut(const E* row, int H, int me) {
+    if constexpr (SHIFT) {
+      head = min(H, static_cast<int>(-(reinterpret_cast<uintptr_t>(row) / sizeof(E)) & (N - 1)));
+      packs = (H - head) / N;
+      edges = H - packs * N;
+      if (me < edges) edge = me < head ? me : packs * N + me;
+    } else {
+      packs = H / N;
+    }
+  }
+};
+// The weight, or the bias, of a pack's columns.
+template <typename E, int N, bool SHIFT>
+__device__ __forceinline__ Pack<E, N> column_pack(const E* w, int column) {
+  Pack<E, N> p;
+  if constexpr (SHIFT) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) p.v[e] = w[column + e];
+  } else {
+    p = *reinterpret_cast<const Pack<E, N>*>(w + column);
+  }
+  return p;
+}
+
 struct LayerNormArgs {
   const void *x, *residual, *weight, *bias;
   void *residual_out, *y;
   float *mean, *rstd;
   int64_t ldx, ldr, ldro, ldy;
+  uint32_t* errors;
   int T, H;
   float eps;
+  int depth;  // rows on their way at a time (layer_norm_ring_kernel)
 };
 
 __host__ __device__ constexpr int layer_norm_most_threads(int n, int per) { return n * per > 8 ? 512 : 1024; }  // by registers
@@ -25,7 +58,6 @@ __host__ __device__ constexpr int layer_norm_most_threads(int n, int per) { retu
 // The joins of a row's sum and of its squared differences.  Each warp takes both about its own mean, by shuffles, and the
 // warps' come together behind one barrier: the squares about the row's mean are the warps' and, for each warp, its elements times
 // the square of what the means differ by.  `mine`: this warp's elements.
-template <bool BLOCK>
 __device__ __forceinline__ float layer_norm_mean(float s, int mine) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -108,7 +140,7 @@ __global__ void __launch_bounds__(BLOCK ? layer_norm_most_threads(N, PER) : 128)
 #pragma unroll
     for (int e = 0; e < N; ++e) s += h[i][e];
   }
-  float mean = layer_norm_mean<BLOCK>(s, mine), ss = 0.0f;
+  float mean = layer_norm_mean(s, mine), ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     if (at(i) >= packs) continue;
@@ -134,6 +166,168 @@ __global__ void __launch_bounds__(BLOCK ? layer_norm_most_threads(N, PER) : 128)
 #pragma unroll
     for (int e = 0; e < N; ++e) h[i][e] = fmaf((h[i][e] - mean) * rstd, f[e], c[e]);
     y[at(i)] = pack<E>(h[i]);
+  }
+}
+
+// Rows that come as bulk copies into a ring of shared memory, `depth` of them (two at least).  A row's place is free when all
+// threads are past the next row's join; a warp that has nothing else to do starts the copies (thread 0 of the others took
+// 0.3 us a row for it).  Each row's packs alone are copied: what lies before and behind them is read by the threads that
+// have it.
+constexpr int LAYER_NORM_RING = 16, LAYER_NORM_RING_THREADS = 512;  // and a warp that starts the copies
+constexpr uint32_t LAYER_NORM_SPINS = 1u << 22;
+template <typename E, int TENSORS>
+struct RowRing {
+  uint64_t* full;
+  uint8_t* rows;
+  const E* from[TENSORS];
+  int64_t ld[TENSORS];
+  uint32_t bytes, place;  // of a row's packs; of a row in the ring
+  int tensors, depth, slot = 0, before = -1;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void fetch(int64_t t, int to) {
+    mbar_arrive_expect_tx(&full[to], static_cast<uint32_t>(tensors) * bytes);
+#pragma unroll
+    for (int i = 0; i < TENSORS; ++i)
+      if (i < tensors) bulk_g2s(rows + (static_cast<size_t>(to) * tensors + i) * place, from[i] + t * ld[i], bytes, &full[to]);
+  }
+  __device__ __forceinline__ void start(int64_t first, int64_t step, int64_t T) {
+    for (int i = 0; i < depth && first + i * step < T; ++i) fetch(first + i * step, i);
+  }
+  // Behind the join of row `t`: the place of the row before it is free.
+  __device__ __forceinline__ void refill(int64_t t, int64_t step, int64_t T) {
+    if (before >= 0 && t + (depth - 1) * step < T) fetch(t + (depth - 1) * step, before);
+  }
+  // Copies that do not arrive leave the results without meaning; all waits end, and so does the kernel.
+  __device__ __forceinline__ void wait(uint32_t* errors) {
+    uint32_t spin = 0;
+    while (!mbar_try_wait(&full[slot], phase) && ++spin < LAYER_NORM_SPINS) {
+    }
+    if (spin >= LAYER_NORM_SPINS) atomicOr(errors, 0x08u);  // STRATA_DEVERR_TIMEOUT
+  }
+  template <int N>
+  __device__ __forceinline__ const Pack<E, N>& pack_of(int i, int at) const {
+    return reinterpret_cast<const Pack<E, N>*>(rows + (static_cast<size_t>(slot) * tensors + i) * place)[at];
+  }
+  __device__ __forceinline__ void next() {
+    before = slot;
+    if (++slot == depth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Many rows that start anywhere: a block goes through rows that are cut alike, the weight's packs beside the ring.  (Rows that all
+// start on 16 bytes are faster a block each: 8192 x 8192 bfloat16 81 us against 85, 8192 x 2048 24 against 26; of those that do
+// not, 8192 x 5003 takes 62 here, element by element 160, 8192 x 1135 25 and 27.)
+template <typename E, int PER>
+__global__ void __launch_bounds__(LAYER_NORM_RING_THREADS + 32, 1) layer_norm_ring_kernel(const __grid_constant__ LayerNormArgs A) {
+  constexpr int N = 16 / static_cast<int>(sizeof(E));
+  __shared__ float part[2][3][32];
+  __shared__ uint64_t full[LAYER_NORM_RING];
+  extern __shared__ __align__(16) uint8_t ring_rows[];  // [depth][x, residual][H], weight, bias
+  using P = Pack<E, N>;
+  const int me = threadIdx.x, threads = blockDim.x - 32, step = gridDim.x;
+  const int64_t first = blockIdx.x;
+  if (me == 0) {
+    for (int i = 0; i < A.depth; ++i) mbar_init(&full[i], 1);
+    fence_proxy_async_smem();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+  const E *x = static_cast<const E*>(A.x), *r = static_cast<const E*>(A.residual), *w = static_cast<const E*>(A.weight), *b = static_cast<const E*>(A.bias);
+  const RowCut<E, N, true> cut(x + first * A.ldx, A.H, me);
+  const uint32_t place = (static_cast<uint32_t>(A.H) * static_cast<uint32_t>(sizeof(E)) + 15) / 16 * 16;
+  RowRing<E, 2> ring{full, ring_rows, {x + cut.head, r + cut.head}, {A.ldx, A.ldr}, static_cast<uint32_t>(cut.packs) * 16, place, r != nullptr ? 2 : 1, A.depth};
+  if (me >= threads) {
+    if (me == threads) ring.start(first, step, A.T);
+    for (int64_t t = first, turn = 0; t < A.T; t += step, turn ^= 1) {
+      float none = 0.0f, nothing = 0.0f;
+      layer_norm_join<true>(none, nothing, 0, A.H, part[turn]);
+      if (me == threads) ring.refill(t, step, A.T);
+      ring.next();
+    }
+    return;
+  }
+  P* sw = reinterpret_cast<P*>(ring_rows + static_cast<size_t>(A.depth) * ring.tensors * place);
+  P* sb = reinterpret_cast<P*>(reinterpret_cast<uint8_t*>(sw) + place);
+  auto at = [&](int i) { return i * threads + me; };  // the pack, of column head + N at(i)
+  int mine = me < 32 ? cut.edges : 0;  // elements of this warp
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    mine += max(0, min(32, cut.packs - (i * threads + (me & ~31)))) * N;
+    if (at(i) >= cut.packs) continue;
+    sw[at(i)] = column_pack<E, N, true>(w, cut.head + at(i) * N);  // read by this thread alone
+    if (A.bias != nullptr) sb[at(i)] = column_pack<E, N, true>(b, cut.head + at(i) * N);
+  }
+  float xe = 0.0f, re = 0.0f, we = 0.0f, be = 0.0f;
+  auto load_edge = [&](int64_t t) {
+    if (cut.edge >= 0) {
+      xe = to_f32(x[t * A.ldx + cut.edge]);
+      if (r != nullptr) re = to_f32(r[t * A.ldr + cut.edge]);
+    }
+  };
+  load_edge(first);
+  if (cut.edge >= 0) {
+    we = to_f32(w[cut.edge]);
+    if (A.bias != nullptr) be = to_f32(b[cut.edge]);
+  }
+  const float over = 1.0f / static_cast<float>(A.H);
+  int turn = 0;
+  for (int64_t t = first; t < A.T; t += step, turn ^= 1) {
+    E *ro = static_cast<E*>(A.residual_out) + t * A.ldro, *y = static_cast<E*>(A.y) + t * A.ldy;
+    float h[PER][N] = {}, s = 0.0f;
+    const float he = xe + re;
+    ring.wait(A.errors);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (at(i) >= cut.packs) continue;
+      unpack(ring.template pack_of<N>(0, at(i)), h[i]);
+      if (r != nullptr) {
+        float f[N];
+        unpack(ring.template pack_of<N>(1, at(i)), f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[i][e] += f[e];
+      }
+      if (A.residual_out != nullptr) *reinterpret_cast<P*>(ro + cut.head + at(i) * N) = pack<E>(h[i]);
+#pragma unroll
+      for (int e = 0; e < N; ++e) s += h[i][e];
+    }
+    if (cut.edge >= 0) {
+      s += he;
+      if (A.residual_out != nullptr) from_f32(he, ro + cut.edge);
+    }
+    if (t + step < A.T) load_edge(t + step);
+    float mean = layer_norm_mean(s, mine), ss = cut.edge >= 0 ? (he - mean) * (he - mean) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (at(i) >= cut.packs) continue;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float d = h[i][e] - mean;
+        ss = fmaf(d, d, ss);
+      }
+    }
+    layer_norm_join<true>(mean, ss, mine, A.H, part[turn]);
+    ring.next();
+    const float rstd = rsqrtf(fmaf(ss, over, A.eps));
+    if (me == 0) {
+      if (A.mean != nullptr) A.mean[t] = mean;
+      if (A.rstd != nullptr) A.rstd[t] = rstd;
+    }
+    if (A.y == nullptr) continue;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (at(i) >= cut.packs) continue;
+      float f[N], c[N] = {};
+      unpack(sw[at(i)], f);
+      if (A.bias != nullptr) unpack(sb[at(i)], c);
+#pragma unroll
+      for (int e = 0; e < N; ++e) c[e] = fmaf((h[i][e] - mean) * rstd, f[e], c[e]);
+      *reinterpret_cast<P*>(y + cut.head + at(i) * N) = pack<E>(c);
+    }
+    if (cut.edge >= 0) from_f32(fmaf((he - mean) * rstd, we, be), y + cut.edge);
   }
 }
 
@@ -210,27 +404,35 @@ __host__ __device__ constexpr int layer_norm_grad_most_threads(int n, int per) {
 // Rows b, b + groups, ... of a block (BLOCK), or of its warps one after another (eight rows of it at a time): a
 // thread has the same columns of all of them, so the sums over rows stay in its registers, in 32 bits.  The
 // next row is on its way while this one's sums are joined.
-template <typename E, int N, int PER, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? layer_norm_grad_most_threads(N, PER) : 32 * LAYER_NORM_GRAD_WARPS) layer_norm_grad_kernel(const __grid_constant__ LayerNormGradArgs A) {
+template <typename E, int N, int PER, bool BLOCK, bool SHIFT>
+__global__ void __launch_bounds__(BLOCK ? layer_norm_grad_most_threads(N, PER) : 32 * LAYER_NORM_GRAD_WARPS, BLOCK ? 1 : 2) layer_norm_grad_kernel(const __grid_constant__ LayerNormGradArgs A) {
   __shared__ float2 part[2][32];
-  extern __shared__ float sums[];  // warps alone: [2][H]
+  extern __shared__ float sums[];  // warps alone: [2][H to whole packs]
   grid_dep_wait();
   grid_dep_launch();
   using P = Pack<E, N>;
-  const int threads = BLOCK ? blockDim.x : 32, me = BLOCK ? threadIdx.x : threadIdx.x & 31;
-  const int packs = A.H / N, warp = threadIdx.x >> 5;
+  const int threads = BLOCK ? blockDim.x : 32, me = BLOCK ? threadIdx.x : threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int first = BLOCK ? blockIdx.x : blockIdx.x * LAYER_NORM_GRAD_WARPS + warp, step = BLOCK ? gridDim.x : gridDim.x * LAYER_NORM_GRAD_WARPS;
-  auto at = [&](int i) { return i * threads + me; };
-  auto row = [&](const void* p, int64_t ld, int64_t t) { return reinterpret_cast<const P*>(static_cast<const E*>(p) + t * ld); };
+  auto row = [&](const void* p, int64_t ld, int64_t t) { return static_cast<const E*>(p) + t * ld; };
+  const RowCut<E, N, SHIFT> cut(row(A.x, A.ldx, first), A.H, me);
+  auto has = [&](int i) { return i * threads + me < cut.packs; };
+  auto at = [&](int i) { return cut.head + (i * threads + me) * N; };
   P pdy[PER], px[PER], pdr[PER];
   float dw[PER][N] = {}, db[PER][N] = {}, mean = 0.0f, rstd = 0.0f;
+  float dye = 0.0f, xe = 0.0f, dre = 0.0f, dwe = 0.0f, dbe = 0.0f;
+  const float we = SHIFT && cut.edge >= 0 ? to_f32(static_cast<const E*>(A.weight)[cut.edge]) : 0.0f;
   auto load = [&](int64_t t) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (at(i) >= packs) continue;
-      pdy[i] = row(A.dy, A.lddy, t)[at(i)];
-      px[i] = row(A.x, A.ldx, t)[at(i)];
-      if (A.dresidual != nullptr) pdr[i] = row(A.dresidual, A.lddr, t)[at(i)];
+      if (!has(i)) continue;
+      pdy[i] = *reinterpret_cast<const P*>(row(A.dy, A.lddy, t) + at(i));
+      px[i] = *reinterpret_cast<const P*>(row(A.x, A.ldx, t) + at(i));
+      if (A.dresidual != nullptr) pdr[i] = *reinterpret_cast<const P*>(row(A.dresidual, A.lddr, t) + at(i));
+    }
+    if (SHIFT && cut.edge >= 0) {
+      dye = to_f32(row(A.dy, A.lddy, t)[cut.edge]);
+      xe = to_f32(row(A.x, A.ldx, t)[cut.edge]);
+      if (A.dresidual != nullptr) dre = to_f32(row(A.dresidual, A.lddr, t)[cut.edge]);
     }
     mean = A.mean[t];
     rstd = A.rstd[t];
@@ -240,12 +442,12 @@ __global__ void __launch_bounds__(BLOCK ? layer_norm_grad_most_threads(N, PER) :
   for (int64_t t = first; t < A.T; t += step, turn ^= 1) {
     float a[PER][N], v[PER][N], sa = 0.0f, sav = 0.0f;
     P dr[PER];
-    const float scale = rstd;
+    const float scale = rstd, ce = dre;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (at(i) >= packs) continue;
+      if (!has(i)) continue;
       float w[N];
-      unpack(static_cast<const P*>(A.weight)[at(i)], w);  // from the nearest cache, for the registers' sake
+      unpack(column_pack<E, N, SHIFT>(static_cast<const E*>(A.weight), at(i)), w);  // from the nearest cache, for the registers' sake
       unpack(pdy[i], a[i]);
       unpack(px[i], v[i]);
       dr[i] = pdr[i];
@@ -259,68 +461,81 @@ __global__ void __launch_bounds__(BLOCK ? layer_norm_grad_most_threads(N, PER) :
         sav = fmaf(a[i][e], v[i][e], sav);
       }
     }
+    const float ve = (xe - mean) * rstd, ae = dye * we;
+    if (SHIFT && cut.edge >= 0) {
+      dwe = fmaf(dye, ve, dwe);
+      dbe += dye;
+      sa += ae;
+      sav = fmaf(ae, ve, sav);
+    }
     if (t + step < A.T) load(t + step);
     layer_norm_join2<BLOCK>(sa, sav, part[turn]);
     sa /= static_cast<float>(A.H);
     sav /= static_cast<float>(A.H);
     if (A.dx == nullptr) continue;
-    P* dx = reinterpret_cast<P*>(static_cast<E*>(A.dx) + t * A.lddx);
+    E* dx = static_cast<E*>(A.dx) + t * A.lddx;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (at(i) >= packs) continue;
+      if (!has(i)) continue;
       float c[N] = {};
       if (A.dresidual != nullptr) unpack(dr[i], c);
 #pragma unroll
       for (int e = 0; e < N; ++e) c[e] = fmaf(scale, a[i][e] - sa - v[i][e] * sav, c[e]);
-      dx[at(i)] = pack<E>(c);
+      *reinterpret_cast<P*>(dx + at(i)) = pack<E>(c);
     }
+    if (SHIFT && cut.edge >= 0) from_f32(fmaf(scale, ae - sa - ve * sav, ce), dx + cut.edge);
   }
   if (A.part == nullptr) return;
   float* out = A.part + static_cast<int64_t>(blockIdx.x) * 2 * A.H;
   if constexpr (BLOCK) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (at(i) >= packs) continue;
+      if (!has(i)) continue;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        out[at(i) * N + e] = dw[i][e];
-        out[A.H + at(i) * N + e] = db[i][e];
+        out[at(i) + e] = dw[i][e];
+        out[A.H + at(i) + e] = db[i][e];
       }
     }
-  } else {  // one warp after another: always the same order
+  } else {  // one warp after another: always the same order; columns of neighbouring lanes lie beside one another
+    const int eighth = (A.H + N - 1) / N, half = N * eighth;
+    auto spread = [&](int c) { return c % N * eighth + c / N; };
     for (int turn = 0; turn < LAYER_NORM_GRAD_WARPS; ++turn) {
       if (warp == turn) {
+        auto add = [&](int c, float w, float b) {
+          sums[spread(c)] = (turn > 0 ? sums[spread(c)] : 0.0f) + w;
+          sums[half + spread(c)] = (turn > 0 ? sums[half + spread(c)] : 0.0f) + b;
+        };
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          if (at(i) >= packs) continue;
+          if (!has(i)) continue;
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const int c = at(i) * N + e;
-            sums[c] = (turn > 0 ? sums[c] : 0.0f) + dw[i][e];
-            sums[A.H + c] = (turn > 0 ? sums[A.H + c] : 0.0f) + db[i][e];
-          }
+          for (int e = 0; e < N; ++e) add(at(i) + e, dw[i][e], db[i][e]);
         }
+        if (SHIFT && cut.edge >= 0) add(cut.edge, dwe, dbe);
       }
       __syncthreads();
     }
-    for (int c = threadIdx.x; c < 2 * A.H; c += blockDim.x) out[c] = sums[c];
+    for (int c = threadIdx.x; c < A.H; c += blockDim.x) {
+      out[c] = sums[spread(c)];
+      out[A.H + c] = sums[half + spread(c)];
+    }
   }
 }
 
-// Rows on 16 bytes, too wide for a warp: as above, by a block, but the rows to come are on their way to shared memory, as bulk
-// copies, `depth` of them ahead.  A row's copies start when every thread has read the one that had its place, which the
-// join's barrier tells.
-constexpr int LAYER_NORM_RING = 16;
-constexpr uint32_t LAYER_NORM_SPINS = 1u << 22;
-template <typename E, int PER>
-__global__ void __launch_bounds__(LAYER_NORM_GRAD_THREADS) layer_norm_ring_kernel(const __grid_constant__ LayerNormGradArgs A) {
+// Wider rows: as above, by a block, through a ring.  Threads with 16 elements need the registers that a further warp would
+// take: there thread 0 starts the copies.
+__host__ __device__ constexpr int layer_norm_copier(int n, int per) { return n * per > 8 ? 0 : 32; }
+template <typename E, int PER, bool SHIFT>
+__global__ void __launch_bounds__(LAYER_NORM_RING_THREADS + layer_norm_copier(16 / static_cast<int>(sizeof(E)), PER), 1) layer_norm_grad_ring_kernel(const __grid_constant__ LayerNormGradArgs A) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   __shared__ float2 part[2][32];
   __shared__ uint64_t full[LAYER_NORM_RING];
-  extern __shared__ __align__(16) uint8_t rows[];  // [depth][dy, x, dresidual][H]
+  extern __shared__ __align__(16) uint8_t ring_rows[];  // [depth][dy, x, dresidual][H], weight
   using P = Pack<E, N>;
-  const int packs = A.H / N, me = threadIdx.x, threads = blockDim.x, step = gridDim.x;
-  const uint32_t bytes = static_cast<uint32_t>(A.H) * sizeof(E), tensors = A.dresidual != nullptr ? 3 : 2;
+  constexpr int COPIER = layer_norm_copier(N, PER);
+  const int me = threadIdx.x, threads = blockDim.x - COPIER, step = gridDim.x;
+  const int64_t first = blockIdx.x;
   if (me == 0) {
     for (int i = 0; i < A.depth; ++i) mbar_init(&full[i], 1);
     fence_proxy_async_smem();
@@ -328,86 +543,105 @@ __global__ void __launch_bounds__(LAYER_NORM_GRAD_THREADS) layer_norm_ring_kerne
   grid_dep_wait();
   grid_dep_launch();
   __syncthreads();
-  auto fetch = [&](int64_t t, int slot) {
-    uint8_t* to = rows + static_cast<size_t>(slot) * tensors * bytes;
-    mbar_arrive_expect_tx(&full[slot], tensors * bytes);
-    bulk_g2s(to, static_cast<const E*>(A.dy) + t * A.lddy, bytes, &full[slot]);
-    bulk_g2s(to + bytes, static_cast<const E*>(A.x) + t * A.ldx, bytes, &full[slot]);
-    if (A.dresidual != nullptr) bulk_g2s(to + 2 * bytes, static_cast<const E*>(A.dresidual) + t * A.lddr, bytes, &full[slot]);
-  };
-  if (me == 0)
-    for (int i = 0; i < A.depth && blockIdx.x + static_cast<int64_t>(i) * step < A.T; ++i) fetch(blockIdx.x + static_cast<int64_t>(i) * step, i);
-  auto at = [&](int i) { return i * threads + me; };
-  P pw[PER];
+  const E *dy = static_cast<const E*>(A.dy), *x = static_cast<const E*>(A.x), *r = static_cast<const E*>(A.dresidual), *w = static_cast<const E*>(A.weight);
+  const RowCut<E, N, SHIFT> cut(x + first * A.ldx, A.H, me);
+  const uint32_t place = (static_cast<uint32_t>(A.H) * static_cast<uint32_t>(sizeof(E)) + 15) / 16 * 16;
+  RowRing<E, 3> ring{full, ring_rows, {dy + cut.head, x + cut.head, r + cut.head}, {A.lddy, A.ldx, A.lddr}, static_cast<uint32_t>(cut.packs) * 16, place,
+                     r != nullptr ? 3 : 2, A.depth};
+  if (COPIER == 0 && me == 0) ring.start(first, step, A.T);
+  if (me >= threads) {
+    if (me == threads) ring.start(first, step, A.T);
+    for (int64_t t = first, turn = 0; t < A.T; t += step, turn ^= 1) {
+      float none = 0.0f, nothing = 0.0f;
+      layer_norm_join2<true>(none, nothing, part[turn]);
+      if (me == threads) ring.refill(t, step, A.T);
+      ring.next();
+    }
+    return;
+  }
+  P* sw = reinterpret_cast<P*>(ring_rows + static_cast<size_t>(A.depth) * ring.tensors * place);
+  auto at = [&](int i) { return i * threads + me; };  // the pack, of column head + N at(i)
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (at(i) < packs) pw[i] = static_cast<const P*>(A.weight)[at(i)];
+    if (at(i) < cut.packs) sw[at(i)] = column_pack<E, N, SHIFT>(w, cut.head + at(i) * N);  // read by this thread alone
   float dw[PER][N] = {}, db[PER][N] = {};
-  int slot = 0, turn = 0;
-  uint32_t phase = 0;
-  float mean = blockIdx.x < A.T ? A.mean[blockIdx.x] : 0.0f, rstd = blockIdx.x < A.T ? A.rstd[blockIdx.x] : 0.0f;
-  for (int64_t t = blockIdx.x; t < A.T; t += step, turn ^= 1) {
-    // copies that do not arrive leave the results without meaning; all waits end, and so does the kernel
-    uint32_t spin = 0;
-    while (!mbar_try_wait(&full[slot], phase) && ++spin < LAYER_NORM_SPINS) {
+  float dye = 0.0f, xe = 0.0f, dre = 0.0f, dwe = 0.0f, dbe = 0.0f;
+  const float we = SHIFT && cut.edge >= 0 ? to_f32(w[cut.edge]) : 0.0f, over = 1.0f / static_cast<float>(A.H);
+  auto load_edge = [&](int64_t t) {
+    if (SHIFT && cut.edge >= 0) {
+      dye = to_f32(dy[t * A.lddy + cut.edge]);
+      xe = to_f32(x[t * A.ldx + cut.edge]);
+      if (r != nullptr) dre = to_f32(r[t * A.lddr + cut.edge]);
     }
-    if (spin >= LAYER_NORM_SPINS) atomicOr(A.errors, 0x08u);  // STRATA_DEVERR_TIMEOUT
-    const P* in = reinterpret_cast<const P*>(rows + static_cast<size_t>(slot) * tensors * bytes);
+  };
+  load_edge(first);
+  int turn = 0;
+  float next_mean = A.mean[first], next_rstd = A.rstd[first];
+  for (int64_t t = first; t < A.T; t += step, turn ^= 1) {
+    const float mean = next_mean, rstd = next_rstd, ve = (xe - mean) * rstd, ae = dye * we, ce = dre;
     float a[PER][N], v[PER][N], sa = 0.0f, sav = 0.0f;
-    P dr[PER];
-    const float scale = rstd;
+    ring.wait(A.errors);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (at(i) >= packs) continue;
-      float w[N];
-      unpack(pw[i], w);
-      unpack(in[at(i)], a[i]);
-      unpack(in[packs + at(i)], v[i]);
-      if (A.dresidual != nullptr) dr[i] = in[2 * packs + at(i)];
+      if (at(i) >= cut.packs) continue;
+      float f[N];
+      unpack(sw[at(i)], f);
+      unpack(ring.template pack_of<N>(0, at(i)), a[i]);
+      unpack(ring.template pack_of<N>(1, at(i)), v[i]);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         v[i][e] = (v[i][e] - mean) * rstd;
         dw[i][e] = fmaf(a[i][e], v[i][e], dw[i][e]);
         db[i][e] += a[i][e];
-        a[i][e] *= w[e];
+        a[i][e] *= f[e];
         sa += a[i][e];
         sav = fmaf(a[i][e], v[i][e], sav);
       }
     }
+    if (SHIFT && cut.edge >= 0) {
+      dwe = fmaf(dye, ve, dwe);
+      dbe += dye;
+      sa += ae;
+      sav = fmaf(ae, ve, sav);
+    }
     if (t + step < A.T) {
-      mean = A.mean[t + step];
-      rstd = A.rstd[t + step];
+      next_mean = A.mean[t + step];
+      next_rstd = A.rstd[t + step];
+      load_edge(t + step);
     }
     layer_norm_join2<true>(sa, sav, part[turn]);
-    if (me == 0 && t + static_cast<int64_t>(A.depth) * step < A.T) fetch(t + static_cast<int64_t>(A.depth) * step, slot);
-    if (++slot == A.depth) {
-      slot = 0;
-      phase ^= 1u;
-    }
-    if (A.dx == nullptr) continue;
-    sa /= static_cast<float>(A.H);
-    sav /= static_cast<float>(A.H);
-    P* dx = reinterpret_cast<P*>(static_cast<E*>(A.dx) + t * A.lddx);
+    if (COPIER == 0 && me == 0) ring.refill(t, step, A.T);
+    if (A.dx != nullptr) {
+      sa *= over;
+      sav *= over;
+      E* dx = static_cast<E*>(A.dx) + t * A.lddx;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (at(i) >= packs) continue;
-      float c[N] = {};
-      if (A.dresidual != nullptr) unpack(dr[i], c);
+      for (int i = 0; i < PER; ++i) {
+        if (at(i) >= cut.packs) continue;
+        float c[N] = {};
+        if (r != nullptr) unpack(ring.template pack_of<N>(2, at(i)), c);
 #pragma unroll
-      for (int e = 0; e < N; ++e) c[e] = fmaf(scale, a[i][e] - sa - v[i][e] * sav, c[e]);
-      dx[at(i)] = pack<E>(c);
+        for (int e = 0; e < N; ++e) c[e] = fmaf(rstd, a[i][e] - sa - v[i][e] * sav, c[e]);
+        *reinterpret_cast<P*>(dx + cut.head + at(i) * N) = pack<E>(c);
+      }
+      if (SHIFT && cut.edge >= 0) from_f32(fmaf(rstd, ae - sa - ve * sav, ce), dx + cut.edge);
     }
+    ring.next();
   }
   if (A.part == nullptr) return;
   float* out = A.part + static_cast<int64_t>(blockIdx.x) * 2 * A.H;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (at(i) >= packs) continue;
+    if (at(i) >= cut.packs) continue;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      out[at(i) * N + e] = dw[i][e];
-      out[A.H + at(i) * N + e] = db[i][e];
+      out[cut.head + at(i) * N + e] = dw[i][e];
+      out[A.H + cut.head + at(i) * N + e] = db[i][e];
     }
+  }
+  if (SHIFT && cut.edge >= 0) {
+    out[cut.edge] = dwe;
+    out[A.H + cut.edge] = dbe;
   }
 }
 
@@ -453,35 +687,26 @@ __global__ void __launch_bounds__(256) layer_norm_grad_columns_kernel(const __gr
   out[A.H + c] = db;
 }
 
-// The groups' sums of 32 columns: 32 warps take every 32nd group, and are added up in order.
+// The groups' sums of 32 columns, of dweight (blockIdx.y 0) or of dbias: 32 warps take every 32nd group, and are added up in order.
 template <typename E>
 __global__ void __launch_bounds__(1024) layer_norm_sum_kernel(const __grid_constant__ LayerNormGradArgs A) {
-  __shared__ float2 of[32][33];
+  __shared__ float of[32][33];
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
-  float dw = 0.0f, db = 0.0f;
+  E* to = static_cast<E*>(blockIdx.y == 0 ? A.dweight : A.dbias);
+  if (to == nullptr) return;
+  float s = 0.0f;
   if (c < A.H) {
-#pragma unroll 4
-    for (int g = warp; g < A.groups; g += 32) {
-      dw += A.part[static_cast<int64_t>(g) * 2 * A.H + c];
-      db += A.part[static_cast<int64_t>(g) * 2 * A.H + A.H + c];
-    }
+    const float* from = A.part + static_cast<int64_t>(blockIdx.y) * A.H + c;
+#pragma unroll 8
+    for (int g = warp; g < A.groups; g += 32) s += from[static_cast<int64_t>(g) * 2 * A.H];
   }
-  of[warp][lane] = make_float2(dw, db);
+  of[warp][lane] = s;
   __syncthreads();
-  const float2 v = of[lane][warp];  // warp w: column w, a lane for each of the 32
-  dw = v.x;
-  db = v.y;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    dw += __shfl_xor_sync(0xFFFFFFFFu, dw, o);
-    db += __shfl_xor_sync(0xFFFFFFFFu, db, o);
-  }
+  s = warp_sum(of[lane][warp]);  // warp w: column w, a lane for each of the 32
   const int column = blockIdx.x * 32 + warp;
-  if (lane > 0 || column >= A.H) return;
-  if (A.dweight != nullptr) from_f32(dw, static_cast<E*>(A.dweight) + column);
-  if (A.dbias != nullptr) from_f32(db, static_cast<E*>(A.dbias) + column);
+  if (lane == 0 && column < A.H) from_f32(s, to + column);
 }
 
 }  // namespace strata

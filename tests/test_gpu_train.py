@@ -97,6 +97,25 @@ def test_layer_norm_strides_offsets_and_gaps(G, dtype, H):
             assert (torch.cat([buf[:, :off], buf[:, off + H:]], 1).float() == -7.0).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,H", [(617, 513), (700, 1135), (1300, 2049), (650, 5003), (640, 8191), (620, 8192), (1000, 24), (2600, 97), (1301, 301), (900, 512)])
+def test_layer_norm_of_many_rows(G, dtype, T, H):
+    """Rows that start anywhere, in all tensors the same way and not; both directions."""
+    g = _gen(T + H)
+    w, b = (1 + _normal(g, H, by=0.3)).to(dtype), _normal(g, H, to=dtype)
+    for offs in ((0, 0, 0), (1, 1, 1), (0, 1, 3)):
+        x, r, dy = (torch.cat([_normal(g, T, H, to=dtype).view(-1), w.new_zeros(8)]).roll(o)[o:o + T * H].view(T, H) for o in offs)
+        x[:, ::29] *= 20
+        o = G.layer_norm_rows(x, w, bias=b, residual=r)
+        check_layer_norm(x, w, b, r, 1e-5, o)
+        check_layer_norm(x, w, None, None, 1e-5, G.layer_norm_rows(x, w))
+        n = G.layer_norm_rows(x, w)
+        check_layer_norm_grad(dy, x, w, n["mean"], n["rstd"], r, G.layer_norm_grad(dy, x, w, n["mean"], n["rstd"], dresidual=r))
+        check_layer_norm_grad(dy, x, w, n["mean"], n["rstd"], None, G.layer_norm_grad(dy, x, w, n["mean"], n["rstd"]))
+        again = G.layer_norm_grad(dy, x, w, n["mean"], n["rstd"], dresidual=r, out=dict(dx=dy.clone() if offs[2] == 0 else torch.empty_like(x)))
+        check_layer_norm_grad(dy, x, w, n["mean"], n["rstd"], r, again)
+
+
 def test_layer_norm_far_from_zero(G):
     """Rows whose mean is a thousand times their spread: a variance from sums of squares would lose all of it."""
     x = _normal(_gen(3), 64, 1024) + 1000.0
