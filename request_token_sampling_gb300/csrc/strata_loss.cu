@@ -87,22 +87,38 @@ bool map_rows(const Device& dev, CUtensorMap* m, bool f32, const void* p, int64_
 // It goes by the sizes alone, so that the workspace's size can be asked for without a device.
 constexpr int SMS = 152, PAIRS = SMS / 2;
 constexpr int DX_BLOCKS = 64;             // of few rows' both products, with dw's in the others (96 x 248,320 x 2,048, the step, us: 40 729, 52 695, 64 664, 76 726)
-constexpr int ALONE_ROWS = 128;           // a call with more works by pairs of SMs, on a copy of the rows that take part
+constexpr int ALONE_ROWS = 128;           // a call with more may work by pairs of SMs
+// A score that takes longer works on a copy of the rows that take part.  The copy costs 4 us and rows that are left out save their
+// share: with a quarter of them it pays from here on (ns).
+constexpr double MOVE_COST = 30000;
 constexpr int SLAB_ROWS = 8192;           // whose tiles' sums are held at a time
 constexpr int64_t PIECE_BYTES = int64_t{512} << 20, PARTS_BYTES = int64_t{256} << 20;
 
 int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 
-// Columns of a tile: those whose tiles come out most even on the SMs.  A stage of a pair's tile costs about as much as 80
-// columns more (as measured for the projection); a tile of one SM is bound by reading w.
-int tile_columns(int64_t row_tiles, int64_t columns, bool pair, int least_columns, int step) {
-  int best = 256;
-  int64_t least = INT64_MAX;
-  for (int bn = 256; bn >= least_columns; bn -= step) {
-    const int64_t cost = tiles_of(row_tiles * tiles_of(columns, bn), pair ? PAIRS : SMS) * (bn + (pair ? 80 : 16));
-    if (cost < least) {
-      least = cost;
-      best = bn;
+// Tiles of the logits: of two SMs or of one, and how many columns, by what their turns cost.  In ns, as measured: a step of 64
+// of a pair's tile (columns + 80), and each turn 900 beside it; tiles of one SM cost 20 % more a step and 600, but bring fewer
+// rows that are none, and start and hand their tiles over 4 us sooner.  (Score of 300 rows x 32,000 x 1,024, us: one SM 20, two
+// 28; 512 x 128,000 x 1,024: 98 and 82; the gradients of 300 x 8,000 x 2,048: 51 and 59, of 1,024 x 32,000 x 1,024: 168 and
+// 152.)  On the way back two more products follow, in which pairs gain another tenth.
+struct Tiles {
+  bool pair;
+  int columns;
+  double cost;
+};
+Tiles tiles_for(int rows, int64_t columns, int H, bool grad) {
+  Tiles best{false, 256, 1e30};
+  const double steps = static_cast<double>(tiles_of(H, 64));
+  for (bool pair : {false, true}) {
+    if (pair && rows <= ALONE_ROWS) break;
+    const int64_t row_tiles = tiles_of(rows, pair ? 256 : 128);
+    const int step = pair || grad ? 32 : 16;
+    for (int bn = 256; bn >= (grad ? 64 : pair ? 128 : 16); bn -= step) {
+      const double turns = static_cast<double>(tiles_of(row_tiles * tiles_of(columns, bn), pair ? PAIRS : SMS));
+      // few rows are bound by reading w
+      double cost = pair ? turns * (steps * (bn + 80) + 900) + 4000 : rows <= ALONE_ROWS ? turns * (bn + 16) : turns * (steps * (bn + 80) * 1.2 + 600);
+      if (grad && !pair) cost *= 1.1;
+      if (cost < best.cost) best = {pair, bn, cost};
     }
   }
   return best;
@@ -111,13 +127,21 @@ int tile_columns(int64_t row_tiles, int64_t columns, bool pair, int least_column
 struct Plan {
   int T, V, H, K;
   bool lists, grad, pair, moved;    // a teacher's tokens; for a gradient; tiles of two SMs; works on a copy of the rows
-  int tile_rows, rows_pad, slab = 0, bn = 0;  // slab: rows whose tiles' sums are held at a time; bn: columns of a tile of logits
+  int tile_rows = 0, rows_pad = 0, slab = 0, bn = 0;  // slab: rows whose tiles' sums are held at a time; bn: columns of a tile of logits
   int piece = 0, splits = 1, width = 0;       // ids of a piece; most parts of dx; columns of a tile of dw and dx
   int64_t sorted = 0, q = 0, logq = 0, state = 0, rows = 0, place = 0, count = 0, by = 0, same = 0, copy = 0, scaled = 0, parts = 0, picks = 0,
           d = 0, dx = 0, bytes = 0;           // places in the workspace
 
   Plan(int T, int V, int H, int K, bool grad)
-      : T(T), V(V), H(H), K(std::max(K, 1)), lists(K > 0), grad(grad), pair(T > ALONE_ROWS), moved(grad || pair), tile_rows(pair ? 256 : 128) {
+      : T(T), V(V), H(H), K(std::max(K, 1)), lists(K > 0), grad(grad), pair(false), moved(grad) {
+    slab = std::min(T, SLAB_ROWS);
+    // a piece of the vocabulary whose differences are held at a time
+    piece = static_cast<int>(std::min<int64_t>(tiles_of(V, 256) * 256, std::max<int64_t>(256, PIECE_BYTES / (tiles_of(T, 256) * 512) / 256 * 256)));
+    const Tiles tiles = tiles_for(grad ? T : slab, grad ? std::min(piece, V) : V, H, grad);
+    pair = tiles.pair;
+    moved = grad || (T > ALONE_ROWS && (tiles.cost > MOVE_COST || T > slab));
+    bn = tiles.columns;
+    tile_rows = pair ? 256 : 128;
     auto take = [&](int64_t n) {
       const int64_t at = bytes;
       bytes += (n + 255) / 256 * 256;
@@ -140,16 +164,11 @@ struct Plan {
       copy = take(static_cast<int64_t>(rows_pad) * H * 2);
     }
     if (!grad) {
-      slab = std::min(T, SLAB_ROWS);
-      bn = tile_columns(tiles_of(slab, tile_rows), V, pair, pair ? 128 : 16, pair ? 32 : 16);
       parts = take(slab * tiles_of(V, bn) * 8);
       picks = take(static_cast<int64_t>(slab) * this->K * 4);
       return;
     }
     scaled = take(static_cast<int64_t>(rows_pad) * H * 2);
-    const int64_t all = tiles_of(V, 256) * 256;
-    piece = static_cast<int>(std::min(all, std::max<int64_t>(256, PIECE_BYTES / (rows_pad * int64_t{2}) / 256 * 256)));
-    bn = tile_columns(rows_pad / tile_rows, std::min(piece, V), pair, 64, 32);
     piece = static_cast<int>(tiles_of(piece, 2 * bn) * 2 * bn);  // whole tiles, and steps of 64
     d = take(static_cast<int64_t>(rows_pad) * piece * 2);
     width = H <= 128 ? 128 : 256;
@@ -284,8 +303,8 @@ int forward(const Loss& C, float* loss, float* lse, const char* name) {
   if (const int rc = device_entry(device, &dev); rc != STRATA_OK) return rc;
   const Plan P(C.T, C.V, C.H, C.K, false);
   CUtensorMap mx, mw;
-  if (!(P.pair ? map_rows(*dev, &mx, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, 128)
-               : map_rows(*dev, &mx, false, C.x, C.H, C.T, C.ldx, std::min(128, (C.T + 7) / 8 * 8))))
+  if (!(P.moved ? map_rows(*dev, &mx, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, 128)
+                : map_rows(*dev, &mx, false, C.x, C.H, C.T, C.ldx, P.pair ? 128 : std::min(128, (C.T + 7) / 8 * 8))))
     return host_fail(STRATA_EINVAL, "x cannot be mapped");
   if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, P.pair ? P.bn / 2 : P.bn)) return host_fail(STRATA_EINVAL, "w cannot be mapped");
   const cudaError_t e = strata::launch_operator(device, C.stream, [&](bool overlaps) {
@@ -345,7 +364,7 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
     Run run{C.stream, overlaps};
     launch_plan(run, C, P, g, nullptr, nullptr, dx, lddx);
     strata::LossArgs A = products_args(C, P, errors);
-    const int dx_blocks = dx == nullptr ? 0 : dw == nullptr ? SMS : DX_BLOCKS;  // of few rows
+    const int dx_blocks = dx == nullptr ? 0 : dw == nullptr ? SMS : C.T <= ALONE_ROWS ? DX_BLOCKS : SMS / 2;  // both products cost the same
     A.units = P.pair ? PAIRS : dx_blocks;
     A.lse = lse;
     A.wide = !misaligned(dw, 32) && lddw % 16 == 0 && C.H % 16 == 0;

@@ -700,3 +700,15 @@ def test_refusals_on_tensors(G):
         with pytest.raises(TypeError):
             call()
     assert G.tail_errors() == 0
+
+
+@pytest.mark.parametrize("T,V,H", [(129, 20000, 256), (700, 5000, 512), (1024, 20000, 264), (260, 100000, 128), (2000, 40000, 512), (600, 70000, 1024)])
+def test_tiles_of_one_sm_and_of_two(G, T, V, H):
+    """Sizes on both sides of the choices between tiles, and between the rows themselves and a copy of them."""
+    x, w, ids, _ = loss_case(T, V, H, 21, skip=0.3)
+    x[ids < 0] = math.nan
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    e.check_rows(o)
+    g = torch.full((T,), 1 / T, device="cuda")
+    e.check_grad(G.cross_entropy_grad(x, w, ids, o["lse"], g), g)
