@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/strata_train.h"
 #include "strata_chain.h"
@@ -31,13 +32,23 @@ struct Lie {
 };
 
 constexpr int SMS = 152, SM_BYTES = 224 * 1024;          // shared memory of an SM for rows on their way
-constexpr int BLOCK_WIDTH = strata::LAYER_NORM_RING_THREADS * 16, WARP_WIDTH = 32 * 16;
+constexpr int BLOCK_WIDTH = 512 * 16, WARP_WIDTH = 32 * 16;
 
 // Registers of a kernel's thread, for the number of its blocks on an SM; found once.
 template <typename K>
 int registers(K kernel) {
   cudaFuncAttributes a;
   return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 128;
+}
+
+// Lets a kernel have an SM's shared memory, once on each device.
+template <typename K>
+cudaError_t allow_shared(K kernel, std::atomic<uint64_t>& done, int device) {
+  const uint64_t bit = uint64_t{1} << (device & 63);
+  if ((done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // How rows go through rings: a block's threads (PER packs each, and the warp of the copies), blocks of an SM (as many as its
@@ -59,10 +70,10 @@ int ring_grid(int T, int blocks) { return T <= SMS ? T : std::min(SMS * blocks, 
 // The shape of a call, as the root-mean-square norm's: many rows are bound by HBM, a thread takes up to 16
 // elements, so that enough bytes are on their way; few rows are bound by latency: a row goes to as many threads as it has packs.
 template <typename E, int N, int PER>
-cudaError_t launch_forward(const strata::LayerNormArgs& A, int least, bool overlaps, void* stream) {
+cudaError_t launch_forward(const strata::LayerNormArgs& A, int least, bool overlaps, int device, void* stream) {
   if constexpr (N * PER <= 32 && PER <= 16) {
     const int packs = (A.H + N - 1) / N, need = (packs + PER - 1) / PER;
-    if (PER < least || need > strata::layer_norm_most_threads(N, PER)) return launch_forward<E, N, PER * 2>(A, least, overlaps, stream);
+    if (PER < least || need > strata::layer_norm_most_threads(N, PER)) return launch_forward<E, N, PER * 2>(A, least, overlaps, device, stream);
     constexpr int ROWS = 4;
     if (need <= 32)
       return strata::Launch((static_cast<unsigned>(A.T) + ROWS - 1) / ROWS, 32 * ROWS, 0, stream, overlaps)(strata::layer_norm_kernel<E, N, PER, false>, A);
@@ -73,28 +84,29 @@ cudaError_t launch_forward(const strata::LayerNormArgs& A, int least, bool overl
 }
 // Many rows that start anywhere.
 template <typename E, int PER>
-cudaError_t launch_ring(strata::LayerNormArgs A, bool overlaps, void* stream) {
+cudaError_t launch_ring(strata::LayerNormArgs A, bool overlaps, int device, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   if constexpr (N * PER <= 16) {
-    if ((A.H / N + PER - 1) / PER > strata::LAYER_NORM_RING_THREADS) return launch_ring<E, PER * 2>(A, overlaps, stream);
+    if ((A.H / N + PER - 1) / PER > strata::LAYER_NORM_RING_THREADS) return launch_ring<E, PER * 2>(A, overlaps, device, stream);
     const int row = (A.H * static_cast<int>(sizeof(E)) + 15) / 16 * 16;
     const auto kernel = strata::layer_norm_ring_kernel<E, PER>;
     static const int regs = registers(kernel);
     const RingShape ring(A.H / N, PER, 32, row * (A.residual != nullptr ? 2 : 1), 2 * row, regs);
     A.depth = ring.depth;
-    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES); e != cudaSuccess) return e;
+    static std::atomic<uint64_t> allowed{0};
+    if (const cudaError_t e = allow_shared(kernel, allowed, device); e != cudaSuccess) return e;
     return strata::Launch(ring_grid(A.T, ring.blocks), ring.threads, ring.smem, stream, overlaps)(kernel, A);
   } else {
     return cudaErrorInvalidValue;  // not reached: wider rows have their own kernels
   }
 }
 template <typename E>
-cudaError_t launch_forward(const strata::LayerNormArgs& A, const Lie& lie, bool overlaps, void* stream) {
+cudaError_t launch_forward(const strata::LayerNormArgs& A, const Lie& lie, bool overlaps, int device, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
-  if (A.T >= 4 * SMS && A.H > WARP_WIDTH && A.H <= BLOCK_WIDTH && lie.alike && !lie.packed) return launch_ring<E, 1>(A, overlaps, stream);
+  if (A.T >= 4 * SMS && A.H > WARP_WIDTH && A.H <= BLOCK_WIDTH && lie.alike && !lie.packed) return launch_ring<E, 1>(A, overlaps, device, stream);
   const int packs = A.H / (lie.packed ? N : 1);
   const int least = A.T < 2 * SMS ? 1 : packs > 64 ? 4 : packs > 32 ? 2 : 1;
-  return lie.packed ? launch_forward<E, N, 1>(A, least, overlaps, stream) : launch_forward<E, 1, 1>(A, least, overlaps, stream);
+  return lie.packed ? launch_forward<E, N, 1>(A, least, overlaps, device, stream) : launch_forward<E, 1, 1>(A, least, overlaps, device, stream);
 }
 
 // Groups of rows whose sums over rows are kept apart, until the last kernel adds them up: those of a block.  Rows too wide for a
@@ -108,15 +120,15 @@ int grad_groups(int T, int H) {
 
 // Narrow rows by warps; wider ones that lie in no common way by a block, element by element.
 template <typename E, int N, int PER, bool SHIFT>
-cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, void* stream) {
+cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, int device, void* stream) {
   if constexpr (N * PER <= 16) {
     const int need = (A.H / N + PER - 1) / PER;
     if (A.H <= WARP_WIDTH) {
-      if (need > 32) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, stream);
+      if (need > 32) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, device, stream);
       return strata::Launch(A.groups, 32 * strata::LAYER_NORM_GRAD_WARPS, static_cast<size_t>((A.H + N - 1) / N * N) * 8, stream, overlaps)(
           strata::layer_norm_grad_kernel<E, N, PER, false, SHIFT>, A);
     }
-    if (need > strata::layer_norm_grad_most_threads(N, PER)) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, stream);
+    if (need > strata::layer_norm_grad_most_threads(N, PER)) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, device, stream);
     if constexpr (N == 1)
       return strata::Launch(A.groups, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::layer_norm_grad_kernel<E, N, PER, true, false>, A);
   }
@@ -125,18 +137,19 @@ cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, void*
 
 // Rows through a ring: as many on their way as an SM's shared memory has room for beside its other blocks.
 template <typename E, int PER, bool SHIFT>
-cudaError_t launch_ring(strata::LayerNormGradArgs& A, bool overlaps, void* stream) {
+cudaError_t launch_ring(strata::LayerNormGradArgs& A, bool overlaps, int device, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   if constexpr (N * PER <= 16) {
     const int need = (A.H / N + PER - 1) / PER;
-    if (need > strata::LAYER_NORM_RING_THREADS) return launch_ring<E, PER * 2, SHIFT>(A, overlaps, stream);
+    if (need > strata::layer_norm_grad_ring_threads(N, PER)) return launch_ring<E, PER * 2, SHIFT>(A, overlaps, device, stream);
     const int row = (A.H * static_cast<int>(sizeof(E)) + 15) / 16 * 16;
     const auto kernel = strata::layer_norm_grad_ring_kernel<E, PER, SHIFT>;
     static const int regs = registers(kernel);
     const RingShape ring(A.H / N, PER, strata::layer_norm_copier(N, PER), row * (A.dresidual != nullptr ? 3 : 2), row, regs);
     A.depth = ring.depth;
     A.groups = std::min(A.groups, ring_grid(A.T, ring.blocks));
-    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES); e != cudaSuccess) return e;
+    static std::atomic<uint64_t> allowed{0};
+    if (const cudaError_t e = allow_shared(kernel, allowed, device); e != cudaSuccess) return e;
     return strata::Launch(A.groups, ring.threads, ring.smem, stream, overlaps)(kernel, A);
   } else {
     return cudaErrorInvalidValue;  // not reached: wider rows have their own kernels
@@ -144,15 +157,15 @@ cudaError_t launch_ring(strata::LayerNormGradArgs& A, bool overlaps, void* strea
 }
 
 template <typename E>
-cudaError_t launch_grad(strata::LayerNormGradArgs A, const Lie& lie, bool overlaps, void* stream) {
+cudaError_t launch_grad(strata::LayerNormGradArgs A, const Lie& lie, bool overlaps, int device, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   cudaError_t e = cudaSuccess;
   if (A.T > 0) {
     if (A.H <= BLOCK_WIDTH) {
       const bool warps = A.H <= WARP_WIDTH;
-      e = lie.packed  ? (warps ? launch_rows<E, N, 1, false>(A, overlaps, stream) : launch_ring<E, 1, false>(A, overlaps, stream))
-          : lie.alike ? (warps ? launch_rows<E, N, 1, true>(A, overlaps, stream) : launch_ring<E, 1, true>(A, overlaps, stream))
-                      : launch_rows<E, 1, 1, false>(A, overlaps, stream);
+      e = lie.packed  ? (warps ? launch_rows<E, N, 1, false>(A, overlaps, device, stream) : launch_ring<E, 1, false>(A, overlaps, device, stream))
+          : lie.alike ? (warps ? launch_rows<E, N, 1, true>(A, overlaps, device, stream) : launch_ring<E, 1, true>(A, overlaps, device, stream))
+                      : launch_rows<E, 1, 1, false>(A, overlaps, device, stream);
       overlaps = true;
     } else {  // the sums first: dx may be dy or x
       if (A.part != nullptr) {
@@ -201,7 +214,7 @@ extern "C" int strata_layer_norm_rows(const void* x, int64_t ldx, const void* re
   lie.look_column(weight);
   lie.look_column(bias);
   const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
-    return dtype == STRATA_DTYPE_F32 ? launch_forward<float>(A, lie, overlaps, stream) : launch_forward<__nv_bfloat16>(A, lie, overlaps, stream);
+    return dtype == STRATA_DTYPE_F32 ? launch_forward<float>(A, lie, overlaps, device, stream) : launch_forward<__nv_bfloat16>(A, lie, overlaps, device, stream);
   });
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_layer_norm_rows: %s", cudaGetErrorString(e));
 }
@@ -248,8 +261,8 @@ extern "C" int strata_layer_norm_grad(const void* dy, int64_t lddy, const void* 
   const strata::LayerNormGradArgs A{dy, x, weight, dresidual, mean, rstd, dx, dweight, dbias, part, errors, lddy, ldx, lddr, lddx, T, H,
                                     T > 0 ? grad_groups(T, H) : 0, 0};
   const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
-    return dtype == STRATA_DTYPE_F32 ? launch_grad<float>(A, lie, overlaps, stream)
-                                     : launch_grad<__nv_bfloat16>(A, lie, overlaps, stream);
+    return dtype == STRATA_DTYPE_F32 ? launch_grad<float>(A, lie, overlaps, device, stream)
+                                     : launch_grad<__nv_bfloat16>(A, lie, overlaps, device, stream);
   });
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_layer_norm_grad: %s", cudaGetErrorString(e));
 }

@@ -525,9 +525,10 @@ __global__ void __launch_bounds__(BLOCK ? layer_norm_grad_most_threads(N, PER) :
 
 // Wider rows: as above, by a block, through a ring.  Threads with 16 elements need the registers that a further warp would
 // take: there thread 0 starts the copies.
+__host__ __device__ constexpr int layer_norm_grad_ring_threads(int n, int per) { return n * per > 8 ? 512 : 704; }
 __host__ __device__ constexpr int layer_norm_copier(int n, int per) { return n * per > 8 ? 0 : 32; }
 template <typename E, int PER, bool SHIFT>
-__global__ void __launch_bounds__(LAYER_NORM_RING_THREADS + layer_norm_copier(16 / static_cast<int>(sizeof(E)), PER), 1) layer_norm_grad_ring_kernel(const __grid_constant__ LayerNormGradArgs A) {
+__global__ void __launch_bounds__(layer_norm_grad_ring_threads(16 / static_cast<int>(sizeof(E)), PER) + layer_norm_copier(16 / static_cast<int>(sizeof(E)), PER), 1) layer_norm_grad_ring_kernel(const __grid_constant__ LayerNormGradArgs A) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   __shared__ float2 part[2][32];
   __shared__ uint64_t full[LAYER_NORM_RING];

@@ -275,7 +275,7 @@ const Tensor* given(const Tensor& t) { return t.defined() ? &t : nullptr; }
 
 // An output: the caller's from `out`, or a new one that is put there, or none.
 Tensor output(PyObject* out, const char* key, PyObject* wanted, at::IntArrayRef shape, ScalarType type, const Tensor& like) {
-  PyObject* had = PyDict_GetItemString(out, key);
+  PyObject* had = PyDict_GET_SIZE(out) > 0 ? PyDict_GetItemString(out, key) : nullptr;
   if (had != nullptr && had != Py_None) return needed(had, key);
   if (wanted != Py_True) return Tensor();
   Tensor made = fresh(shape, type, like);

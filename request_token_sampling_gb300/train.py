@@ -52,11 +52,34 @@ def _declare() -> None:
 _declare()
 
 
+def _load(name):
+    """The compiled call `name`, loaded; later calls go to it directly."""
+    call = getattr(tail._compiled(), name)
+    globals()["_" + name] = call
+    return call
+
+
+def _layer_norm(*args):
+    return _load("layer_norm")(*args)
+
+
+def _layer_norm_grad(*args):
+    return _load("layer_norm_grad")(*args)
+
+
+def _loss(*args):
+    return _load("loss")(*args)
+
+
+def _loss_grad(*args):
+    return _load("loss_grad")(*args)
+
+
 # ------------------------------------------------------------------------------ C-named calls
 def strata_layer_norm_rows(x, weight, bias=None, residual=None, eps: float = 1e-5, residual_out=None, y=None, mean=None, rstd=None,
                            stream=None) -> None:
-    _done(tail._compiled().layer_norm(x, weight, bias, residual, eps, False, False, False,
-                                      dict(residual=residual_out, y=y, mean=mean, rstd=rstd), _handle(stream)))
+    _done(_layer_norm(x, weight, bias, residual, eps, False, False, False,
+                      dict(residual=residual_out, y=y, mean=mean, rstd=rstd), _handle(stream)))
 
 
 def strata_layer_norm_workspace(T: int, H: int) -> int:
@@ -65,8 +88,8 @@ def strata_layer_norm_workspace(T: int, H: int) -> int:
 
 def strata_layer_norm_grad(dy, x, weight, mean, rstd, dresidual=None, dx=None, dweight=None, dbias=None, workspace=None,
                            stream=None) -> None:
-    _done(tail._compiled().layer_norm_grad(dy, x, weight, mean, rstd, dresidual, False, False, False,
-                                           dict(dx=dx, dweight=dweight, dbias=dbias), workspace, False, _handle(stream)))
+    _done(_layer_norm_grad(dy, x, weight, mean, rstd, dresidual, False, False, False,
+                           dict(dx=dx, dweight=dweight, dbias=dbias), workspace, False, _handle(stream)))
 
 
 def strata_loss_workspace(T: int, V: int, H: int, K: int = 0, grad: bool = False) -> int:
@@ -74,21 +97,21 @@ def strata_loss_workspace(T: int, V: int, H: int, K: int = 0, grad: bool = False
 
 
 def strata_cross_entropy_rows(x, w, ids, loss, lse, workspace, stream=None) -> None:
-    _done(tail._compiled().loss(x, w, ids, None, 1.0, False, dict(loss=loss, lse=lse), workspace, False, _handle(stream)))
+    _done(_loss(x, w, ids, None, 1.0, False, dict(loss=loss, lse=lse), workspace, False, _handle(stream)))
 
 
 def strata_cross_entropy_grad(x, w, ids, lse, g, dx=None, dw=None, workspace=None, stream=None) -> None:
-    _done(tail._compiled().loss_grad(x, w, ids, None, 1.0, lse, g, False, False, dict(dx=dx, dw=dw), workspace, False, _handle(stream)))
+    _done(_loss_grad(x, w, ids, None, 1.0, lse, g, False, False, dict(dx=dx, dw=dw), workspace, False, _handle(stream)))
 
 
 def strata_distill_rows(x, w, ids, teacher, temperature, loss, lse, workspace, stream=None) -> None:
-    _done(tail._compiled().loss(x, w, ids, _teacher(teacher), temperature, False, dict(loss=loss, lse=lse), workspace, False,
-                                _handle(stream)))
+    _done(_loss(x, w, ids, _teacher(teacher), temperature, False, dict(loss=loss, lse=lse), workspace, False,
+                _handle(stream)))
 
 
 def strata_distill_grad(x, w, ids, teacher, temperature, lse, g, dx=None, dw=None, workspace=None, stream=None) -> None:
-    _done(tail._compiled().loss_grad(x, w, ids, _teacher(teacher), temperature, lse, g, False, False, dict(dx=dx, dw=dw), workspace,
-                                     False, _handle(stream)))
+    _done(_loss_grad(x, w, ids, _teacher(teacher), temperature, lse, g, False, False, dict(dx=dx, dw=dw), workspace,
+                     False, _handle(stream)))
 
 
 def _teacher(teacher):
@@ -105,8 +128,8 @@ def layer_norm_rows(x, weight, bias=None, residual=None, eps: float = 1e-5, y: b
     if stream is not None:
         with _side(stream, x):
             return layer_norm_rows(x, weight, bias, residual, eps, y, stats, None, out)
-    return _done(tail._compiled().layer_norm(x, weight, bias, residual, eps, residual is not None, bool(y), bool(stats),
-                                             {} if out is None else out, None))
+    return _done(_layer_norm(x, weight, bias, residual, eps, residual is not None, bool(y), bool(stats),
+                             {} if out is None else out, None))
 
 
 def layer_norm_grad(dy, x, weight, mean, rstd, dresidual=None, dx: bool = True, dweight: bool = True, bias: bool = True, stream=None,
@@ -116,8 +139,8 @@ def layer_norm_grad(dy, x, weight, mean, rstd, dresidual=None, dx: bool = True, 
     if stream is not None:
         with _side(stream, x):
             return layer_norm_grad(dy, x, weight, mean, rstd, dresidual, dx, dweight, bias, None, out)
-    return _done(tail._compiled().layer_norm_grad(dy, x, weight, mean, rstd, dresidual, bool(dx), bool(dweight), bool(bias),
-                                                  {} if out is None else out, None, True, None))
+    return _done(_layer_norm_grad(dy, x, weight, mean, rstd, dresidual, bool(dx), bool(dweight), bool(bias),
+                                  {} if out is None else out, None, True, None))
 
 
 def cross_entropy_rows(x, w, ids, stream=None, out=None) -> dict:
@@ -126,7 +149,7 @@ def cross_entropy_rows(x, w, ids, stream=None, out=None) -> dict:
     if stream is not None:
         with _side(stream, x):
             return cross_entropy_rows(x, w, ids, None, out)
-    return _done(tail._compiled().loss(x, w, ids, None, 1.0, True, {} if out is None else out, None, True, None))
+    return _done(_loss(x, w, ids, None, 1.0, True, {} if out is None else out, None, True, None))
 
 
 def cross_entropy_grad(x, w, ids, lse, g, dx: bool = True, dw: bool = True, stream=None, out=None) -> dict:
@@ -134,7 +157,7 @@ def cross_entropy_grad(x, w, ids, lse, g, dx: bool = True, dw: bool = True, stre
     if stream is not None:
         with _side(stream, x):
             return cross_entropy_grad(x, w, ids, lse, g, dx, dw, None, out)
-    return _done(tail._compiled().loss_grad(x, w, ids, None, 1.0, lse, g, bool(dx), bool(dw), {} if out is None else out, None, True, None))
+    return _done(_loss_grad(x, w, ids, None, 1.0, lse, g, bool(dx), bool(dw), {} if out is None else out, None, True, None))
 
 
 def distill_rows(x, w, ids, teacher, temperature: float = 1.0, stream=None, out=None) -> dict:
@@ -143,7 +166,7 @@ def distill_rows(x, w, ids, teacher, temperature: float = 1.0, stream=None, out=
     if stream is not None:
         with _side(stream, x):
             return distill_rows(x, w, ids, teacher, temperature, None, out)
-    return _done(tail._compiled().loss(x, w, ids, _teacher(teacher), temperature, True, {} if out is None else out, None, True, None))
+    return _done(_loss(x, w, ids, _teacher(teacher), temperature, True, {} if out is None else out, None, True, None))
 
 
 def distill_grad(x, w, ids, teacher, lse, g, temperature: float = 1.0, dx: bool = True, dw: bool = True, stream=None, out=None) -> dict:
@@ -151,5 +174,5 @@ def distill_grad(x, w, ids, teacher, lse, g, temperature: float = 1.0, dx: bool 
     if stream is not None:
         with _side(stream, x):
             return distill_grad(x, w, ids, teacher, lse, g, temperature, dx, dw, None, out)
-    return _done(tail._compiled().loss_grad(x, w, ids, _teacher(teacher), temperature, lse, g, bool(dx), bool(dw),
-                                            {} if out is None else out, None, True, None))
+    return _done(_loss_grad(x, w, ids, _teacher(teacher), temperature, lse, g, bool(dx), bool(dw),
+                            {} if out is None else out, None, True, None))
