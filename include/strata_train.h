@@ -82,7 +82,8 @@ int strata_cross_entropy_rows(const void* x, int64_t ldx, const void* w, int64_t
  * dx [T][H] and dw [V][H] are bfloat16 (either may be NULL).  The logits are computed again, in pieces of the vocabulary;
  * dz / g is rounded to bfloat16 between the products, and so is x[t] g[t] / max|g| (x itself where
  * all g are equal).  A row that is left out, whose id is V or more or whose g is 0 gets dx = 0 and adds nothing to dw.
- * With T = 0 dw is set to zeros.  dx and dw start on 16 bytes, and their strides are multiples of 8.
+ * With T = 0 dw is set to zeros.  dx and dw start on 16 bytes, their strides are multiples of 8, and they do not overlap an
+ * input or one another.
  * `workspace`: strata_loss_workspace(T, V, H, 0, 1) bytes, which hold a piece of dz (512 MB, or 256
  * columns) and parts of dx beside copies of the rows.
  */
@@ -92,7 +93,7 @@ int strata_cross_entropy_grad(const void* x, int64_t ldx, const void* w, int64_t
 
 /*
  * A teacher gives K tokens ids[t][k] for each row and their logits or log-probabilities teacher[t][k] (what is common to
- * a row's falls out).  With the temperature s, over the tokens given
+ * a row's falls out).  With the temperature s (0.001 to 1000), over the tokens given
  *   q[t] = softmax(teacher[t] / s),   lse[t] = log sum_v exp(z[t][v] / s),
  *   loss[t] = s^2 * sum_k q[t][k] * (log q[t][k] - (z[t][ids[t][k]] / s - lse[t]))
  * An id that is negative or whose teacher value is -inf is not there; a row without ids is left out, as above.  An id of

@@ -198,8 +198,8 @@ int check(const Loss& C, bool grad) {
   if (C.H < 1 || C.H > STRATA_LOSS_MAX_WIDTH) return host_fail(STRATA_ERANGE, "H=%d outside 1..%d", C.H, STRATA_LOSS_MAX_WIDTH);
   if (C.K < 0 || C.K > STRATA_DISTILL_MAX_TOKENS) return host_fail(STRATA_ERANGE, "K=%d outside 1..%d", C.K, STRATA_DISTILL_MAX_TOKENS);
   if (C.ldx < C.H || C.ldw < C.H) return host_fail(STRATA_EINVAL, "a row stride below H=%d", C.H);
-  if (!(C.temperature > 0.0f) || C.temperature - C.temperature != 0.0f || !(1.0f / C.temperature < 1e30f))
-    return host_fail(STRATA_EINVAL, "temperature=%g", static_cast<double>(C.temperature));
+  if (!(C.temperature >= 0.001f && C.temperature <= 1000.0f))
+    return host_fail(STRATA_EINVAL, "temperature=%g outside 0.001..1000", static_cast<double>(C.temperature));
   if (C.H % 8 != 0 || C.ldx % 8 != 0 || C.ldw % 8 != 0) return host_fail(STRATA_EALIGN, "H or a row stride is not a multiple of 8");
   if (C.T == 0) return STRATA_OK;
   if (C.x == nullptr || C.w == nullptr || C.ids == nullptr || (C.K > 0 && C.teacher == nullptr))

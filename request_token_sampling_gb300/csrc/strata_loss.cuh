@@ -573,8 +573,9 @@ __global__ void __launch_bounds__(128) loss_list_kernel(const __grid_constant__ 
     const int k = i * 32 + lane;
     id[i] = k < A.K ? A.ids[t * A.K + k] : -1;
     l[i] = k < A.K ? A.teacher[t * A.K + k] * A.over : -INFINITY;
-    if (id[i] < 0 || l[i] == -INFINITY) id[i] = LOSS_NO_ID;
-    if (id[i] != LOSS_NO_ID) {
+    if (id[i] < 0 || l[i] == -INFINITY) {
+      id[i] = LOSS_NO_ID;
+    } else {
       beyond |= id[i] >= A.V;
       top = max_nan(top, l[i]);
     }
@@ -791,7 +792,7 @@ __global__ void __launch_bounds__(128) loss_join_kernel(const __grid_constant__ 
   top = fmaxf(fmaxf(joined[0][0], joined[1][0]), fmaxf(joined[2][0], joined[3][0]));
   float total = 0.0f;
   for (int i = threadIdx.x; i < A.n_tiles; i += 128)
-    if (parts[i].y != 0.0f) total += parts[i].y * ex2_approx(parts[i].x - top);
+    if (parts[i].y != 0.0f) total += parts[i].y < INFINITY ? parts[i].y * ex2_approx(parts[i].x - top) : parts[i].y;
   total = warp_sum(total);
   if (lane == 0) joined[warp][1] = total;
   __syncthreads();

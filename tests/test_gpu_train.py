@@ -712,3 +712,56 @@ def test_tiles_of_one_sm_and_of_two(G, T, V, H):
     e.check_rows(o)
     g = torch.full((T,), 1 / T, device="cuda")
     e.check_grad(G.cross_entropy_grad(x, w, ids, o["lse"], g), g)
+
+
+@pytest.mark.parametrize("T", [5, 200])
+def test_the_largest_id_is_beyond_the_vocabulary_too(G, T):
+    x, w, ids, teacher = loss_case(T, 90, 64, T, K=3, skip=0.0)
+    ids[2, 1], teacher[2, 1] = 2 ** 31 - 1, 0.5
+    ids[3, :] = 2 ** 31 - 1
+    teacher[3] = 0.0
+    e = Exact(x, w, ids, teacher)
+    o = G.distill_rows(x, w, ids, teacher)
+    e.check_rows(o)
+    assert o["loss"][2].isnan() and o["lse"][3].isnan()
+    d = G.distill_grad(x, w, ids, teacher, o["lse"], torch.ones(T, device="cuda"))
+    e.check_grad(d, torch.ones(T, device="cuda"))
+
+
+def test_an_infinite_logit_beside_large_ones(G):
+    """lse is infinite whatever else there is, in its tile and in others."""
+    w = torch.zeros(2000, 8, device="cuda").to(BF)
+    w[:, 0] = 150.0
+    w[1500, 0] = math.inf
+    x = torch.zeros(2, 8, device="cuda").to(BF)
+    x[:, 0] = torch.tensor([1.0, 20.0])
+    o = G.cross_entropy_rows(x, w, torch.tensor([3, 1500], dtype=torch.int32, device="cuda"))
+    assert (o["lse"] == math.inf).all() and o["loss"][0] == math.inf and o["loss"][1].isnan()
+
+
+@pytest.mark.parametrize("T,V,H", [(3, 200, 32768), (2, 524288, 16), (131072, 300, 8), (140, 70, 32768)])
+def test_the_largest_sizes(G, T, V, H):
+    x, w, ids, _ = loss_case(T, V, H, 2)
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    e.check_rows(o)
+    g = torch.full((T,), 1 / T, device="cuda")
+    e.check_grad(G.cross_entropy_grad(x, w, ids, o["lse"], g), g)
+
+
+@pytest.mark.parametrize("T", [50, 300])
+def test_scales_of_any_size_and_sign(G, T):
+    """One negative scale for all rows, scales that differ by 2^60, an infinite and a NaN one beside others."""
+    x, w, ids, _ = loss_case(T, 400, 64, T + 3, skip=0.0)
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    for g in (torch.full((T,), -3e-5, device="cuda"), 2.0 ** torch.linspace(-40, 20, T, device="cuda") * torch.where(torch.arange(T, device="cuda") % 2 == 0, 1.0, -1.0)):
+        e.check_grad(G.cross_entropy_grad(x, w, ids, o["lse"], g), g)
+    for bad in (math.nan, math.inf):
+        g = torch.ones(T, device="cuda")
+        g[7] = bad
+        d = G.cross_entropy_grad(x, w, ids, o["lse"], g)
+        rest = torch.arange(T, device="cuda") != 7
+        want = G.cross_entropy_grad(x, w, ids, o["lse"], torch.ones(T, device="cuda"))["dx"]
+        assert torch.equal(d["dx"][rest], want[rest]) and not d["dx"][7].isfinite().any()
+        assert not d["dw"][ids[7].long()].isfinite().any()

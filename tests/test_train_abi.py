@@ -108,6 +108,7 @@ TEACHER = [
     (dict(K=0), "STRATA_ERANGE"), (dict(K=-1), "STRATA_ERANGE"), (dict(K=129), "STRATA_ERANGE"), (dict(teacher=None), "STRATA_EINVAL"),
     (dict(teacher=P + 2), "STRATA_EALIGN"), (dict(temperature=0.0), "STRATA_EINVAL"), (dict(temperature=-1.0), "STRATA_EINVAL"),
     (dict(temperature=float("nan")), "STRATA_EINVAL"), (dict(temperature=float("inf")), "STRATA_EINVAL"), (dict(temperature=1e-35), "STRATA_EINVAL"),
+    (dict(temperature=0.0009), "STRATA_EINVAL"), (dict(temperature=1001.0), "STRATA_EINVAL"),
 ]
 
 
