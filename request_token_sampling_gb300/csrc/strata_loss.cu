@@ -113,9 +113,10 @@ Tiles tiles_for(int rows, int64_t columns, int H, bool grad) {
     if (pair && rows <= ALONE_ROWS) break;
     const int64_t row_tiles = tiles_of(rows, pair ? 256 : 128);
     const int step = pair || grad ? 32 : 16;
-    for (int bn = 256; bn >= (grad ? 64 : pair ? 128 : 16); bn -= step) {
+    // few rows are bound by reading w whatever the tiles: scores of long rows take narrow ones, which have two sums (below 1,024
+    // their lse is within 5e-7 with one)
+    for (int bn = rows <= ALONE_ROWS && H > 1024 && !grad ? 128 : 256; bn >= (grad ? 64 : pair ? 128 : 16); bn -= step) {
       const double turns = static_cast<double>(tiles_of(row_tiles * tiles_of(columns, bn), pair ? PAIRS : SMS));
-      // few rows are bound by reading w
       double cost = pair ? turns * (steps * (bn + 80) + 900) + 4000 : rows <= ALONE_ROWS ? turns * (bn + 16) : turns * (steps * (bn + 80) * 1.2 + 600);
       if (grad && !pair) cost *= 1.1;
       if (cost < best.cost) best = {pair, bn, cost};

@@ -33,10 +33,19 @@ constexpr int LOSS_NO_ID = 0x7FFFFFFF;
 // Two SMs share a tile: 128 rows and half of the columns each; one SM alone has 128 rows and all columns.  What is left of
 // shared memory holds results on their way out, a piece of 32 rows for each writing warp.
 constexpr int LOSS_PIECE = 4096;
-__host__ __device__ constexpr int loss_stages(int mode, bool pair) { return !pair ? 4 : mode == LOSS_SUMS ? 7 : 6; }
-__host__ __device__ constexpr int loss_stage_bytes(bool pair) { return (128 + (pair ? 128 : 256)) * LOSS_LINE; }
+constexpr int LOSS_MOST_STAGES = 8;
+__host__ __device__ constexpr int loss_ring_bytes(int mode, bool pair) { return (!pair || mode != LOSS_SUMS ? 192 : 224) * 1024; }
 __host__ __device__ constexpr int loss_smem(int mode, bool pair) {
-  return loss_stages(mode, pair) * loss_stage_bytes(pair) + (mode == LOSS_SUMS ? 0 : LOSS_WRITERS * LOSS_PIECE) + 1024 + 512;
+  return loss_ring_bytes(mode, pair) + (mode == LOSS_SUMS ? 0 : LOSS_WRITERS * LOSS_PIECE) + 1024 + 512;
+}
+// Where B lies in a stage, and a stage's bytes.  A's products read 128 rows wherever they end: the rows behind `a_rows` are some
+// of B's, and of what they give nothing is looked at.
+__host__ __device__ constexpr int loss_b_place(int a_rows) { return a_rows * LOSS_LINE; }
+__host__ __device__ constexpr int loss_stage_bytes(int a_rows, int b_rows) { return (a_rows + b_rows) * LOSS_LINE; }
+__host__ __device__ constexpr int loss_stages(int ring, int stage) {
+  const int n = (ring - 128 * LOSS_LINE) / stage + 1, m = ring / stage;  // the last one's 128 rows lie in the ring, too
+  const int least = n < m ? n : m;
+  return least < LOSS_MOST_STAGES ? least : LOSS_MOST_STAGES;
 }
 
 struct LossArgs {
@@ -66,7 +75,7 @@ struct LossArgs {
 };
 
 struct LossBars {
-  uint64_t full[7], empty[7], done[2], freed[2], drained;
+  uint64_t full[LOSS_MOST_STAGES], empty[LOSS_MOST_STAGES], done[2], freed[2], drained;
   uint32_t tmem, dead;
 };
 
@@ -101,6 +110,27 @@ __device__ __forceinline__ int loss_splits(int tiles, int k, int most, int units
   if (s <= most && (s == 1 || k >= 4 * s)) cost = min(cost, static_cast<uint32_t>((tiles * s + units - 1) / units * ((k + s - 1) / s + 3) * 8 + s * tiles * (pair ? 2 : 1)));
   return static_cast<int>(__reduce_min_sync(FULL_MASK, cost << 5 | static_cast<uint32_t>(s - 1)) & 31u) + 1;
 }
+
+// The stages' ring as one warp goes through it.
+struct LossRing {
+  uint32_t stages, slot = 0, phase = 0, begun = 0;
+  __device__ __forceinline__ void next() {
+    ++begun;
+    if (++slot == stages) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  // Waits until the copies of the newest stages have landed: no copy of a block may be in flight when it ends.
+  __device__ __forceinline__ void drain(uint64_t* full) {
+    for (uint32_t i = 0; i < stages && begun > 0; ++i, --begun) {
+      phase ^= slot == 0;
+      slot = slot == 0 ? stages - 1 : slot - 1;
+      for (uint32_t spin = 0; spin < PROJ_SPINS && !mbar_try_wait(&full[slot], phase); ++spin) {
+      }
+    }
+  }
+};
 
 // Tile `tile` of `outer` x `inner`: bands of LOSS_BAND inner ones, which go fastest.
 __device__ __forceinline__ void loss_place(int tile, int outer, int inner, int& o, int& i) {
@@ -145,11 +175,11 @@ struct LossIds {
 template <int MODE, bool PAIR>
 __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& mo, const LossArgs& A,
                                               int block, int blocks) {
-  constexpr int STAGES = loss_stages(MODE, PAIR), STAGE = loss_stage_bytes(PAIR), TILE_M = PAIR ? 256 : 128;
+  constexpr int RING = loss_ring_bytes(MODE, PAIR), TILE_M = PAIR ? 256 : 128;
   constexpr bool A_OUTER = MODE == LOSS_DW, B_OUTER = MODE == LOSS_DW || MODE == LOSS_DX;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  uint8_t* staging = smem + STAGES * STAGE;
+  uint8_t* staging = smem + RING;
   LossBars* B = reinterpret_cast<LossBars*>(staging + (MODE == LOSS_SUMS ? 0 : LOSS_WRITERS * LOSS_PIECE));
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
@@ -159,7 +189,7 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
   constexpr uint32_t TMEM_COLS = 512;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < LOSS_MOST_STAGES; ++i) {
       mbar_init(&B->full[i], 1);
       mbar_init(&B->empty[i], 1);
     }
@@ -226,12 +256,21 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
     }
   };
 
-  Ring<STAGES> ring;  // of the loading and of the issuing warp
+  // The tensor cores cut their sums off to 32 bits after every 16 products, always towards zero.  Narrow tiles of logits have
+  // room for two sums, one of each half of the width, which leaves half of that (score of 64 rows x 2,048 wide: lse off by
+  // 4e-7 instead of 8e-7).
+  const int half_k = (k_all + 1) / 2;
+  const bool halves = (MODE == LOSS_SUMS || MODE == LOSS_DIFFS) && A.bn <= 128 && k_all > 1;
+
+  // rows that a stage holds: a pair's always as many, so that the numbers are known; of rows as B all that the tile has
+  const int a_rows = PAIR || MODE == LOSS_DW ? 128 : A.a_rows, b_place = loss_b_place(a_rows);
+  const int stage_bytes = PAIR ? loss_stage_bytes(128, 128) : loss_stage_bytes(a_rows, A.bn);
+  LossRing ring{static_cast<uint32_t>(PAIR ? RING / loss_stage_bytes(128, 128) : loss_stages(RING, stage_bytes))};  // of the loading and of the issuing warp
   bool alive = true;
   uint32_t turn = 0;  // tiles so far, of the issuing warp and of those that write
   if (warp == 0) {
     asm volatile("fence.proxy.async;" ::: "memory");  // rows and d were written by ordinary stores of kernels before
-    const uint32_t bytes = static_cast<uint32_t>(PAIR ? 2 * (128 + half) : (MODE == LOSS_DW ? 128 : A.a_rows) + half) * LOSS_LINE;
+    const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * (a_rows + half)) * LOSS_LINE;
     const CUtensorMap* mx = MODE == LOSS_DW && *A.same == 0 ? &mc : &mb;
     for (int tile = first; tile < tiles && alive; tile += step) {
       int o, i, from, to;
@@ -239,11 +278,11 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
       loss_place(tile - split * per_split, outer, inner, o, i);
       stages_of(split, from, to);
       for (int s = from; s < to; ++s, ring.next()) {
-        if (ring.begun >= STAGES && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) {
+        if (ring.begun >= ring.stages && !proj_wait(&B->empty[ring.slot], ring.phase ^ 1u, dead, A.errors, bit)) {
           alive = false;
           break;
         }
-        const uint32_t at = smem_u32(smem + ring.slot * STAGE), at_b = at + 128 * LOSS_LINE;
+        const uint32_t at = smem_u32(smem + ring.slot * stage_bytes), at_b = at + b_place;
         const uint32_t bar = PAIR ? dsmem_addr(smem_u32(&B->full[ring.slot]), 0) : smem_u32(&B->full[ring.slot]);
         auto load = [&](uint32_t to_, const CUtensorMap* m, int x, int y) {
           if constexpr (PAIR)
@@ -285,15 +324,18 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
           break;
         }
         tc_fence_after();
-        const uint32_t at = smem_u32(smem + ring.slot * STAGE), at_b = at + 128 * LOSS_LINE;
+        const uint32_t at = smem_u32(smem + ring.slot * stage_bytes), at_b = at + b_place;
         const uint64_t da = A_OUTER ? loss_desc_outer(at) : mma_desc(at, LOSS_LINE), db = B_OUTER ? loss_desc_outer(at_b) : mma_desc(at_b, LOSS_LINE);
+        const bool later = halves && s >= half_k;
+        const uint32_t to_sum = later ? sum + 128 : sum;
+        const bool adds = s > (later ? half_k : from);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if constexpr (PAIR)
-              pair_mma(sum, da + STEP_A * i, db + STEP_B * i, idesc, s > from || i > 0);
+              pair_mma(to_sum, da + STEP_A * i, db + STEP_B * i, idesc, adds || i > 0);
             else
-              mma<false>(sum, da + STEP_A * i, db + STEP_B * i, idesc, s > from || i > 0);
+              mma<false>(to_sum, da + STEP_A * i, db + STEP_B * i, idesc, adds || i > 0);
           }
           if constexpr (PAIR)
             pair_commit(&B->empty[ring.slot]);
@@ -386,6 +428,18 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
     };
     [[maybe_unused]] const float by = MODE == LOSS_DW ? *A.by * A.dw_scale : 1.0f;
     const uint32_t sum = tmem + buf * 256 + (quarter << 21);
+    auto logits = [&](int c, float (&v)[32]) {
+      tmem_ld32(sum + c, v);
+      if (halves) {
+        float u[32];
+        tmem_ld32(sum + 128 + c, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] += u[e];
+      } else {
+        tmem_wait_ld();
+      }
+    };
     for (int tile = first + static_cast<int>(buf) * step; tile < tiles; tile += 2 * step, ++turn) {
       int o, i, from, to;
       const int split = MODE == LOSS_DX ? tile / per_split : 0;
@@ -414,8 +468,7 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
 #pragma unroll 1
         for (int c = 0; c < columns; c += 32) {
           float v[32];
-          tmem_ld32(sum + c, v);
-          tmem_wait_ld();
+          logits(c, v);
           if (columns - c < 32) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = c + e < columns ? v[e] : -INFINITY;
@@ -425,7 +478,11 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
             if (ids.next < end) {
               float z = 0.0f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) z = ids.next == n0 + c + e ? v[e] : z;
+              for (int e = 0; e < 32; ++e) {
+                const bool it = ids.next == n0 + c + e;
+                z = it ? v[e] : z;
+                if (A.q == nullptr) v[e] = it ? -INFINITY : v[e];  // a cross entropy: the sum is that of the other ids
+              }
               A.picks[static_cast<int64_t>(r) * A.K + ids.at] = z;
               ids.advance();
             }
@@ -450,8 +507,7 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
 #pragma unroll 1
         for (int c = 0; c < A.bn; c += 32) {
           float v[32];
-          tmem_ld32(sum + c, v);
-          tmem_wait_ld();
+          logits(c, v);
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = ex2_approx(fmaf(v[e], A.scale, -lse2));
           while (__any_sync(FULL_MASK, ids.next < n0 + c + 32)) {
@@ -766,7 +822,7 @@ struct LossJoinArgs {
   int T, V, K, row0, n_tiles;
 };
 
-// A block for each row: the tiles' sums together, and the loss.
+// A block for each row: the tiles' sums together (of a cross entropy those of the other ids), and the loss.
 __global__ void __launch_bounds__(128) loss_join_kernel(const __grid_constant__ LossJoinArgs A) {
   __shared__ float joined[4][2];
   grid_dep_wait();
@@ -798,10 +854,13 @@ __global__ void __launch_bounds__(128) loss_join_kernel(const __grid_constant__ 
   __syncthreads();
   if (warp > 0) return;
   total = (joined[0][1] + joined[1][1]) + (joined[2][1] + joined[3][1]);
-  const float lse = total > 0.0f || total != total ? top * 0.693147180559945309417f + logf(total) : -INFINITY;
-  float loss = 0.0f;
+  float lse = total > 0.0f || total != total ? top * 0.693147180559945309417f + logf(total) : -INFINITY, loss = 0.0f;
   if (A.q == nullptr) {
-    loss = lse - A.picks[r];
+    // log(1 + exp(d)), d = the others' lse - z: a loss near 0 keeps its digits
+    const float z = A.picks[r], d = lse - z, more = log1pf(expf(-fabsf(d)));
+    const bool infinite = z == INFINITY || lse == INFINITY;
+    loss = z == INFINITY ? NAN : fmaxf(d, 0.0f) + (d != d ? d : more);
+    lse = infinite && z == z && lse == lse ? INFINITY : (d > 0.0f ? lse : z) + (d != d ? d : more);
   } else {
     for (int k = lane; k < A.K; k += 32) {
       const float q = A.q[t * A.K + k];

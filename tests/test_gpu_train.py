@@ -765,3 +765,20 @@ def test_scales_of_any_size_and_sign(G, T):
         want = G.cross_entropy_grad(x, w, ids, o["lse"], torch.ones(T, device="cuda"))["dx"]
         assert torch.equal(d["dx"][rest], want[rest]) and not d["dx"][7].isfinite().any()
         assert not d["dw"][ids[7].long()].isfinite().any()
+
+
+@pytest.mark.parametrize("T,V,H", [(1, 2000, 64), (100, 5000, 128), (400, 3000, 64)])
+def test_losses_near_zero_keep_their_digits(G, T, V, H):
+    """Rows that are all but sure of their token: the loss is log(1 + the sum over the other ids of exp(z - z of the id)), to whose
+    terms an error of z is a relative one."""
+    x, w, ids, _ = loss_case(T, V, H, 31, skip=0.0)
+    x = (x.float() + 8 * w[ids.long()].float()).to(BF)
+    e = Exact(x, w, ids)
+    z = x.double() @ w.double().T
+    at = ids.long()[:, None]
+    others = (z - z.gather(1, at)).exp().scatter_(1, at, 0.0).sum(1)
+    want = torch.log1p(others)
+    assert float(want.min()) < 1e-6
+    o = G.cross_entropy_rows(x, w, ids)
+    near(o["loss"], want, want * (2 * e.off_z.amax(1) + (V / 256 + 316) * U))
+    e.check_rows(o)
