@@ -12,6 +12,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <utility>
+
 #include "../../include/strata_tail.h"
 #include "../../include/strata_train.h"
 
@@ -283,6 +285,27 @@ Tensor output(PyObject* out, const char* key, PyObject* wanted, at::IntArrayRef 
   return made;
 }
 
+// Two outputs of one small shape, which share an allocation where both are new: one takes half a microsecond and more.
+std::pair<Tensor, Tensor> outputs(PyObject* out, const char* first, const char* second, PyObject* wanted_first, PyObject* wanted_second, int64_t n,
+                                  ScalarType type, const Tensor& like) {
+  const bool given_one = PyDict_GET_SIZE(out) > 0 && (PyDict_GetItemString(out, first) != nullptr || PyDict_GetItemString(out, second) != nullptr);
+  if (!given_one && wanted_first == Py_True && wanted_second == Py_True) {
+    const Tensor both = fresh({2, n}, type, like);
+    auto part = [&](int64_t offset) {
+      Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(both.storage()), both.key_set(), both.dtype());
+      t.unsafeGetTensorImpl()->set_storage_offset(offset);
+      t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef({n}), at::IntArrayRef({int64_t{1}}));
+      return t;
+    };
+    const Tensor a = part(0), b = part(n);
+    put(out, first, a);
+    put(out, second, b);
+    return {a, b};
+  }
+  const Tensor a = output(out, first, wanted_first, {n}, type, like);
+  return {a, output(out, second, wanted_second, {n}, type, like)};
+}
+
 // The caller's workspace, or (`allocate`) a new one.
 void* workspace_of(PyObject* o, PyObject* allocate, int64_t need, const Tensor& like, int device, int64_t& bytes, Tensor& hold) {
   const Tensor* had = tensor(o, "workspace");
@@ -318,8 +341,8 @@ TAIL_CALL(layer_norm) {
   const int64_t T = x.size(0), H = x.size(1);
   PyObject* out = a[8];
   dictionary(out);
-  const Tensor ro = output(out, "residual", a[5], {T, H}, type, x), y = output(out, "y", a[6], {T, H}, type, x),
-               mean = output(out, "mean", a[7], {T}, at::kFloat, x), rstd = output(out, "rstd", a[7], {T}, at::kFloat, x);
+  const Tensor ro = output(out, "residual", a[5], {T, H}, type, x), y = output(out, "y", a[6], {T, H}, type, x);
+  const auto [mean, rstd] = outputs(out, "mean", "rstd", a[7], a[7], T, at::kFloat, x);
   const Rows rx = rows(&x, "x", T, H, type, device), rr = rows(residual, "residual", T, H, type, device),
              rro = rows(given(ro), "residual", T, H, type, device), ry = rows(given(y), "y", T, H, type, device);
   void *pw = dense(&weight, "weight", {H}, type, device), *pb = dense(bias, "bias", {H}, type, device),
@@ -348,8 +371,8 @@ TAIL_CALL(layer_norm_grad) {
   const int64_t T = x.size(0), H = x.size(1);
   PyObject* out = a[9];
   dictionary(out);
-  const Tensor dx = output(out, "dx", a[6], {T, H}, type, x), dweight = output(out, "dweight", a[7], {H}, type, x),
-               dbias = output(out, "dbias", a[8], {H}, type, x);
+  const Tensor dx = output(out, "dx", a[6], {T, H}, type, x);
+  const auto [dweight, dbias] = outputs(out, "dweight", "dbias", a[7], a[8], H, type, x);
   const Rows rdy = rows(&dy, "dy", T, H, type, device), rx = rows(&x, "x", T, H, type, device),
              rdr = rows(dresidual, "dresidual", T, H, type, device), rdx = rows(given(dx), "dx", T, H, type, device);
   void *pw = dense(&weight, "weight", {H}, type, device), *pm = dense(&mean, "mean", {T}, at::kFloat, device),
@@ -411,7 +434,7 @@ TAIL_CALL(loss) {
   const LossOperands o = loss_operands(x, w, ids, teacher, device);
   PyObject* out = a[6];
   dictionary(out);
-  const Tensor loss = output(out, "loss", a[5], {o.T}, at::kFloat, x), lse = output(out, "lse", a[5], {o.T}, at::kFloat, x);
+  const auto [loss, lse] = outputs(out, "loss", "lse", a[5], a[5], o.T, at::kFloat, x);
   float *pl = static_cast<float*>(dense(given(loss), "loss", {o.T}, at::kFloat, device)),
         *pe = static_cast<float*>(dense(given(lse), "lse", {o.T}, at::kFloat, device));
   int64_t bytes = 0;
