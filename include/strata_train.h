@@ -69,7 +69,8 @@ int strata_layer_norm_grad(const void* dy, int64_t lddy, const void* x, int64_t 
  * or more gives NaN for both.
  * x and w start on 16 bytes; H and the strides ldx and ldw are multiples of 8.
  * `workspace`: strata_loss_workspace(T, V, H, 0, 0) bytes on 256 bytes of alignment, free to be reused
- * when the stream has passed the call; K = 0 says that it is for a cross entropy, grad = 1 that it is for a gradient.
+ * when the stream has passed the call; K = 0 says that it is for a cross entropy, grad = 1 that it is for a gradient (and 0 is
+ * the size for a call that would be refused).
  */
 int64_t strata_loss_workspace(int T, int V, int H, int K, int grad);
 int strata_cross_entropy_rows(const void* x, int64_t ldx, const void* w, int64_t ldw, int T, int V, int H,

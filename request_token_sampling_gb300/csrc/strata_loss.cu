@@ -416,6 +416,7 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
 
 extern "C" int64_t strata_loss_workspace(int T, int V, int H, int K, int grad) {
   if (T <= 0 || V <= 0 || H <= 0 || K < 0) return 0;
+  if (T > STRATA_LOSS_MAX_ROWS || V > STRATA_MAX_VOCAB || H > STRATA_LOSS_MAX_WIDTH || K > STRATA_DISTILL_MAX_TOKENS) return 0;  // calls that are refused
   return Plan(T, V, H, K, grad != 0).bytes;
 }
 

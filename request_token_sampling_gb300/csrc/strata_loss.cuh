@@ -4,7 +4,7 @@
 //   dx = dz w;  dw = dz^T x            (a cross entropy has one k with q = 1, and s = 1)
 //
 // The logits exist as tiles of tensor memory only.  One kernel makes all four kinds of products on the tensor cores:
-//   LOSS_SUMS   z of 256 rows and up to 256 ids: a maximum and a sum of exponentials for each row, and z of the row's ids
+//   LOSS_SUMS   z of up to 256 rows and 256 ids: a maximum and a sum of exponentials for each row, and z of the row's ids
 //   LOSS_DIFFS  z again, and d = exp(z - lse) - q in bfloat16 to the workspace, for a piece of the vocabulary
 //   LOSS_DW     dw of the piece: d^T xs over the rows (both operands with the sum's index outermost in memory)
 //   LOSS_DX     parts of dx: d w over the piece's ids (w with the sum's index outermost), in 32 bits
@@ -12,7 +12,16 @@
 // each term, as far off as the results' own rounding.  g stays out of d: dx is scaled in 32 bits at the end, and
 // x of a row is scaled by g / max|g| in xs, which changes nothing where all g are equal (a mean).
 //
-// Rows that are left out do not take part: the others are copied one after another first (loss_gather_kernel).
+// Rows that are left out do not take part: the others are copied one after another first (loss_gather_kernel), but for scores
+// that take less than the copy would save.
+//
+// Many rows are bound by the tensor cores: tiles of 256 x 256 on two SMs, half of the columns brought by each (64 bytes a cycle
+// where a tile on one SM takes 96), six or seven stages of 32 KB on their way, and two accumulators, which four writing warps each
+// empty by turns.  Measured (one GB300, rows x ids x width): the sums of 2,048 x 32,000 x 2,048 140 us (1.92 PFLOP/s, a library
+// product's rate), differences, dw and dx 145, 148 and 149; a whole step of 4,096 x 32,000 x 4,096, an eighth of the rows left
+// out, 2,172 us in a stream of steps, which the power limit sets (1,893 alone).  Few rows are bound by HBM: tiles of 128 rows on one
+// SM, whose rows past the last one are neither loaded nor looked at: the sums of 64 x 248,320 x 2,048 150 us (6.8 TB/s); the step
+// of 96 such rows 666, of which w's three readings and dw's writing take 600 at the copy's rate.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,7 +37,7 @@ constexpr int LOSS_LINE = 128;        // bytes of a row that one stage holds: 64
 constexpr int LOSS_THREADS = 320;     // warp 0 loads, warp 1 issues the products, warps 2-9 write the tile
 constexpr int LOSS_WRITERS = 8;       // four for each of the two accumulators: they write one tile after another by turns
 constexpr int LOSS_BAND = 16;         // tiles of the inner index that a band has: what its operands take stays in L2
-constexpr int LOSS_RUNS = 4;          // steps of 64 rows up to which dw's tiles go in runs
+constexpr int LOSS_RUNS = 4;          // steps of 64 rows up to which dw's tiles go in runs (below, where they are)
 constexpr int LOSS_NO_ID = 0x7FFFFFFF;
 // Two SMs share a tile: 128 rows and half of the columns each; one SM alone has 128 rows and all columns.  What is left of
 // shared memory holds results on their way out, a piece of 32 rows for each writing warp.
@@ -236,8 +245,8 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
   }
   const int per_split = outer * inner;
   int tiles = per_split * splits, first = PAIR ? block / 2 : block, step = PAIR ? blocks / 2 : blocks;
-  // Few rows: dw is bound by its writing, and a pair that writes one tile after another of the same ids leaves memory fuller
-  // pages (96 rows, 1 GB: 262 us, by turns 283; with 32 bytes a store 247).  With more rows the pairs' parts of d would
+  // Few rows: dw is bound by its writing, and blocks that write one tile after another of the same ids leave memory fuller
+  // pages (96 rows, 1 GB: 262 us, by turns 283; with 32 bytes a store 247).  With more rows the blocks' parts of d would
   // not fit in L2 together.
   if (MODE == LOSS_DW && k_all <= LOSS_RUNS) {
     const int64_t all = tiles;

@@ -152,6 +152,8 @@ def test_workspace_sizes(S):
             for t, n in zip((1, 64, 128, 129, 4096, 131072), sizes):
                 pad = (t + 255) // 256 * 256
                 assert n <= pad * 64 * 2 * 2 + max(600 << 20, pad * 1024) + max(256 << 20, pad * 64 * 4) + 16 * t * (K + 2) + (8192 * 2048 * 8) + 65536
+    for over in ((2 ** 31 - 1, 100, 64, 0), (131073, 100, 64, 0), (4, 524289, 64, 0), (4, 100, 32776, 0), (4, 100, 64, 129), (4, 100, 64, -1)):
+        assert S.strata_loss_workspace(*over, False) == 0 and S.strata_loss_workspace(*over, True) == 0
     big = S.strata_loss_workspace(131072, 524288, 32768, 128, True)
     assert 0 < big < 64 << 30
     assert 0 < S.strata_layer_norm_workspace(2 ** 31 - 1, 131072) <= 16 * 2 * 131072 * 4
