@@ -12,7 +12,6 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <utility>
 
 #include "../../include/strata_tail.h"
 #include "../../include/strata_train.h"
@@ -275,58 +274,91 @@ TAIL_CALL(draw) {
 
 const Tensor* given(const Tensor& t) { return t.defined() ? &t : nullptr; }
 
-// An output: the caller's from `out`, or a new one that is put there, or none.
-Tensor output(PyObject* out, const char* key, PyObject* wanted, at::IntArrayRef shape, ScalarType type, const Tensor& like) {
-  PyObject* had = PyDict_GET_SIZE(out) > 0 ? PyDict_GetItemString(out, key) : nullptr;
-  if (had != nullptr && had != Py_None) return needed(had, key);
-  if (wanted != Py_True) return Tensor();
-  Tensor made = fresh(shape, type, like);
-  put(out, key, made);
-  return made;
-}
-
-// Two outputs of one small shape, which share an allocation where both are new: one takes half a microsecond and more.
-std::pair<Tensor, Tensor> outputs(PyObject* out, const char* first, const char* second, PyObject* wanted_first, PyObject* wanted_second, int64_t n,
-                                  ScalarType type, const Tensor& like) {
-  const bool given_one = PyDict_GET_SIZE(out) > 0 && (PyDict_GetItemString(out, first) != nullptr || PyDict_GetItemString(out, second) != nullptr);
-  if (!given_one && wanted_first == Py_True && wanted_second == Py_True) {
-    const Tensor both = fresh({2, n}, type, like);
-    auto part = [&](int64_t offset) {
-      Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(both.storage()), both.key_set(), both.dtype());
-      t.unsafeGetTensorImpl()->set_storage_offset(offset);
-      t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef({n}), at::IntArrayRef({int64_t{1}}));
-      return t;
-    };
-    const Tensor a = part(0), b = part(n);
-    put(out, first, a);
-    put(out, second, b);
-    return {a, b};
+// The outputs and the workspace of a call: the caller's from `out`, or new ones (which are put there), or none.  New ones of up
+// to 32 KB share an allocation, since each takes more than half a microsecond and the smallest calls three on the GPU.
+class Made {
+ public:
+  Made(PyObject* out, const Tensor& like) : out_(out), like_(like) {
+    if (!PyDict_Check(out)) refuse(PyExc_TypeError, "out", "must be a dict");
   }
-  const Tensor a = output(out, first, wanted_first, {n}, type, like);
-  return {a, output(out, second, wanted_second, {n}, type, like)};
-}
-
-// The caller's workspace, or (`allocate`) a new one.
-void* workspace_of(PyObject* o, PyObject* allocate, int64_t need, const Tensor& like, int device, int64_t& bytes, Tensor& hold) {
-  const Tensor* had = tensor(o, "workspace");
-  if (had != nullptr) {
-    bytes = had->numel();
-    return dense(had, "workspace", {bytes}, at::kByte, device);
+  void want(const char* key, PyObject* wanted, at::IntArrayRef shape, ScalarType type) {
+    Item& i = items_[n_++];
+    i.key = key;
+    PyObject* had = PyDict_GET_SIZE(out_) > 0 ? PyDict_GetItemString(out_, key) : nullptr;
+    if (had != nullptr && had != Py_None) {
+      i.t = needed(had, key);
+      return;
+    }
+    if (wanted != Py_True) return;
+    size(i, shape, type);
   }
-  if (allocate != Py_True || need <= 0) return nullptr;
-  bytes = need;
-  hold = fresh({need}, at::kByte, like);
-  return hold.data_ptr();
+  void want_workspace(int64_t bytes) {
+    Item& i = items_[n_++];
+    if (bytes > 0) size(i, at::IntArrayRef(&bytes, 1), at::kByte);
+  }
+  void make() {
+    int64_t shared = 0, small = 0;
+    for (int k = 0; k < n_; ++k) {
+      if (items_[k].bytes <= 0 || items_[k].bytes > SMALL) continue;
+      shared += (items_[k].bytes + 255) / 256 * 256;
+      ++small;
+    }
+    Tensor whole;
+    int64_t at = 0;
+    for (int k = 0; k < n_; ++k) {
+      Item& i = items_[k];
+      if (i.bytes < 0) continue;
+      const at::IntArrayRef shape(i.shape, i.dims);
+      if (i.bytes == 0 || i.bytes > SMALL || small == 1) {
+        i.t = fresh(shape, i.type, like_);
+      } else {
+        if (!whole.defined()) whole = fresh({shared}, at::kByte, like_);
+        i.t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(i.type));
+        const int64_t strides[2] = {i.dims == 2 ? i.shape[1] : 1, 1};
+        i.t.unsafeGetTensorImpl()->set_storage_offset(at / static_cast<int64_t>(c10::elementSize(i.type)));
+        i.t.unsafeGetTensorImpl()->set_sizes_and_strides(shape, at::IntArrayRef(strides, i.dims));
+        at += (i.bytes + 255) / 256 * 256;
+      }
+      if (i.key != nullptr) put(out_, i.key, i.t);
+    }
+  }
+  const Tensor* operator[](int k) const { return given(items_[k].t); }
+
+ private:
+  static constexpr int64_t SMALL = 32768;
+  struct Item {
+    const char* key = nullptr;
+    int64_t shape[2] = {}, bytes = -1;  // -1: nothing to make
+    int dims = 0;
+    ScalarType type = at::kByte;
+    Tensor t;
+  };
+  static void size(Item& i, at::IntArrayRef shape, ScalarType type) {
+    i.type = type;
+    i.bytes = static_cast<int64_t>(c10::elementSize(type));
+    for (const int64_t s : shape) {
+      i.shape[i.dims++] = s;
+      i.bytes *= s;
+    }
+  }
+  PyObject* out_;
+  const Tensor& like_;
+  Item items_[5];
+  int n_ = 0;
+};
+
+// The caller's workspace, or (`allocate`) the bytes to make.
+int64_t workspace_bytes(const Tensor* had, PyObject* allocate, int64_t need) { return had == nullptr && allocate == Py_True ? need : 0; }
+void* workspace_at(const Tensor* had, const Tensor* made, int device, int64_t& bytes) {
+  const Tensor* t = had != nullptr ? had : made;
+  bytes = t != nullptr ? t->numel() : 0;
+  return dense(t, "workspace", {bytes}, at::kByte, device);
 }
 
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Refused();
   return v;
-}
-
-void dictionary(PyObject* o) {
-  if (!PyDict_Check(o)) refuse(PyExc_TypeError, "out", "must be a dict");
 }
 
 // (x, weight, bias, residual, eps, want residual, want y, want mean and rstd, out, stream) -> out, a dict
@@ -340,13 +372,16 @@ TAIL_CALL(layer_norm) {
   const int device = call_device(x, "x");
   const int64_t T = x.size(0), H = x.size(1);
   PyObject* out = a[8];
-  dictionary(out);
-  const Tensor ro = output(out, "residual", a[5], {T, H}, type, x), y = output(out, "y", a[6], {T, H}, type, x);
-  const auto [mean, rstd] = outputs(out, "mean", "rstd", a[7], a[7], T, at::kFloat, x);
+  Made made(out, x);
+  made.want("residual", a[5], {T, H}, type);
+  made.want("y", a[6], {T, H}, type);
+  made.want("mean", a[7], {T}, at::kFloat);
+  made.want("rstd", a[7], {T}, at::kFloat);
+  made.make();
   const Rows rx = rows(&x, "x", T, H, type, device), rr = rows(residual, "residual", T, H, type, device),
-             rro = rows(given(ro), "residual", T, H, type, device), ry = rows(given(y), "y", T, H, type, device);
+             rro = rows(made[0], "residual", T, H, type, device), ry = rows(made[1], "y", T, H, type, device);
   void *pw = dense(&weight, "weight", {H}, type, device), *pb = dense(bias, "bias", {H}, type, device),
-       *pm = dense(given(mean), "mean", {T}, at::kFloat, device), *ps = dense(given(rstd), "rstd", {T}, at::kFloat, device);
+       *pm = dense(made[2], "mean", {T}, at::kFloat, device), *ps = dense(made[3], "rstd", {T}, at::kFloat, device);
   void* stream = stream_of(a[9], device);
   const int t32 = narrow(T, "T"), h32 = narrow(H, "H");
   int rc;
@@ -370,18 +405,22 @@ TAIL_CALL(layer_norm_grad) {
   const int device = call_device(x, "x");
   const int64_t T = x.size(0), H = x.size(1);
   PyObject* out = a[9];
-  dictionary(out);
-  const Tensor dx = output(out, "dx", a[6], {T, H}, type, x);
-  const auto [dweight, dbias] = outputs(out, "dweight", "dbias", a[7], a[8], H, type, x);
-  const Rows rdy = rows(&dy, "dy", T, H, type, device), rx = rows(&x, "x", T, H, type, device),
-             rdr = rows(dresidual, "dresidual", T, H, type, device), rdx = rows(given(dx), "dx", T, H, type, device);
-  void *pw = dense(&weight, "weight", {H}, type, device), *pm = dense(&mean, "mean", {T}, at::kFloat, device),
-       *ps = dense(&rstd, "rstd", {T}, at::kFloat, device), *pdw = dense(given(dweight), "dweight", {H}, type, device),
-       *pdb = dense(given(dbias), "dbias", {H}, type, device);
   const int t32 = narrow(T, "T"), h32 = narrow(H, "H");
+  const Tensor* ws_given = tensor(a[10], "workspace");
+  Made made(out, x);
+  made.want("dx", a[6], {T, H}, type);
+  made.want("dweight", a[7], {H}, type);
+  made.want("dbias", a[8], {H}, type);
+  const bool sums = a[7] == Py_True || a[8] == Py_True || made[1] != nullptr || made[2] != nullptr;
+  made.want_workspace(sums ? workspace_bytes(ws_given, a[11], strata_layer_norm_workspace(t32, h32)) : 0);
+  made.make();
+  const Rows rdy = rows(&dy, "dy", T, H, type, device), rx = rows(&x, "x", T, H, type, device),
+             rdr = rows(dresidual, "dresidual", T, H, type, device), rdx = rows(made[0], "dx", T, H, type, device);
+  void *pw = dense(&weight, "weight", {H}, type, device), *pm = dense(&mean, "mean", {T}, at::kFloat, device),
+       *ps = dense(&rstd, "rstd", {T}, at::kFloat, device), *pdw = dense(made[1], "dweight", {H}, type, device),
+       *pdb = dense(made[2], "dbias", {H}, type, device);
   int64_t bytes = 0;
-  Tensor hold;
-  void* ws = workspace_of(a[10], pdw != nullptr || pdb != nullptr ? a[11] : Py_False, strata_layer_norm_workspace(t32, h32), x, device, bytes, hold);
+  void* ws = workspace_at(ws_given, made[3], device, bytes);
   void* stream = stream_of(a[12], device);
   int rc;
   Py_BEGIN_ALLOW_THREADS
@@ -433,13 +472,16 @@ TAIL_CALL(loss) {
   int device;
   const LossOperands o = loss_operands(x, w, ids, teacher, device);
   PyObject* out = a[6];
-  dictionary(out);
-  const auto [loss, lse] = outputs(out, "loss", "lse", a[5], a[5], o.T, at::kFloat, x);
-  float *pl = static_cast<float*>(dense(given(loss), "loss", {o.T}, at::kFloat, device)),
-        *pe = static_cast<float*>(dense(given(lse), "lse", {o.T}, at::kFloat, device));
+  const Tensor* ws_given = tensor(a[7], "workspace");
+  Made made(out, x);
+  made.want("loss", a[5], {o.T}, at::kFloat);
+  made.want("lse", a[5], {o.T}, at::kFloat);
+  made.want_workspace(workspace_bytes(ws_given, a[8], strata_loss_workspace(o.T, o.V, o.H, o.K, 0)));
+  made.make();
+  float *pl = static_cast<float*>(dense(made[0], "loss", {o.T}, at::kFloat, device)),
+        *pe = static_cast<float*>(dense(made[1], "lse", {o.T}, at::kFloat, device));
   int64_t bytes = 0;
-  Tensor hold;
-  void* ws = workspace_of(a[7], a[8], strata_loss_workspace(o.T, o.V, o.H, o.K, 0), x, device, bytes, hold);
+  void* ws = workspace_at(ws_given, made[2], device, bytes);
   void* stream = stream_of(a[9], device);
   int rc;
   Py_BEGIN_ALLOW_THREADS
@@ -461,14 +503,17 @@ TAIL_CALL(loss_grad) {
   const LossOperands o = loss_operands(x, w, ids, teacher, device);
   float *pe = static_cast<float*>(dense(&lse, "lse", {o.T}, at::kFloat, device)), *pg = static_cast<float*>(dense(&g, "g", {o.T}, at::kFloat, device));
   PyObject* out = a[9];
-  dictionary(out);
-  const Tensor dx = output(out, "dx", a[7], {o.T, o.H}, at::kBFloat16, x), dw = output(out, "dw", a[8], {o.V, o.H}, at::kBFloat16, x);
-  Rows rdx = rows(given(dx), "dx", o.T, o.H, at::kBFloat16, device), rdw = rows(given(dw), "dw", o.V, o.H, at::kBFloat16, device);
+  const Tensor* ws_given = tensor(a[10], "workspace");
+  Made made(out, x);
+  made.want("dx", a[7], {o.T, o.H}, at::kBFloat16);
+  made.want("dw", a[8], {o.V, o.H}, at::kBFloat16);
+  made.want_workspace(workspace_bytes(ws_given, a[11], strata_loss_workspace(o.T, o.V, o.H, o.K, 1)));
+  made.make();
+  Rows rdx = rows(made[0], "dx", o.T, o.H, at::kBFloat16, device), rdw = rows(made[1], "dw", o.V, o.H, at::kBFloat16, device);
   if (o.T == 1) rdx.ld = o.x.ld;
   if (o.V == 1) rdw.ld = o.w.ld;
   int64_t bytes = 0;
-  Tensor hold;
-  void* ws = workspace_of(a[10], a[11], strata_loss_workspace(o.T, o.V, o.H, o.K, 1), x, device, bytes, hold);
+  void* ws = workspace_at(ws_given, made[2], device, bytes);
   void* stream = stream_of(a[12], device);
   int rc;
   Py_BEGIN_ALLOW_THREADS

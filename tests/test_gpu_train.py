@@ -782,3 +782,26 @@ def test_losses_near_zero_keep_their_digits(G, T, V, H):
     o = G.cross_entropy_rows(x, w, ids)
     near(o["loss"], want, want * (2 * e.off_z.amax(1) + (V / 256 + 316) * U))
     e.check_rows(o)
+
+
+def test_outputs_that_share_an_allocation_are_apart(G):
+    """Small outputs of a call lie in one allocation: each is whole, contiguous and does not touch another's elements, also with
+    some of them given, and large ones beside."""
+    g = _gen(40)
+    for T, H in ((1, 8), (3, 40), (9, 256), (40, 4096), (5000, 8)):
+        x, w, b, r = _normal(g, T, H, to=BF), (1 + _normal(g, H, by=0.2)).to(BF), _normal(g, H, to=BF), _normal(g, T, H, to=BF)
+        mine = torch.full((T,), -1.0, device="cuda")
+        for out in ({}, dict(mean=mine), dict(y=torch.empty_like(x), rstd=None)):
+            o = G.layer_norm_rows(x, w, bias=b, residual=r, out=dict(out))
+            check_layer_norm(x, w, b, r, 1e-5, o)
+            assert all(v.is_contiguous() and v.data_ptr() % 16 == 0 for v in o.values())
+            spans = sorted((v.data_ptr(), v.data_ptr() + v.numel() * v.element_size()) for v in o.values())
+            assert all(a[1] <= c[0] for a, c in zip(spans, spans[1:]))
+        assert (mine != -1).any()
+        d = G.layer_norm_grad(r, x, w, o["mean"], o["rstd"])
+        check_layer_norm_grad(r, x, w, o["mean"], o["rstd"], None, d)
+        given = torch.empty(H, dtype=BF, device="cuda")
+        e = G.layer_norm_grad(r, x, w, o["mean"], o["rstd"], dweight=False, bias=False, out=dict(dweight=given))
+        assert torch.equal(given, d["dweight"]) and set(e) == {"dx", "dweight"}
+        spans = sorted((v.data_ptr(), v.data_ptr() + v.numel() * v.element_size()) for v in d.values())
+        assert all(a[1] <= c[0] for a, c in zip(spans, spans[1:]))
