@@ -21,10 +21,11 @@ int cuda_fail(cudaError_t e, const char* what) { return host_fail(STRATA_ECUDA, 
 
 using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
 using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, strata::LossArgs);
-template <int MODE>
-Kernel kernel_for(bool pair) {
-  return pair ? strata::loss_kernel<MODE, true> : strata::loss_kernel<MODE, false>;
+Kernel sums_kernel(bool pair, bool is_long) {
+  return pair ? (is_long ? strata::loss_kernel<strata::LOSS_SUMS, true, true> : strata::loss_kernel<strata::LOSS_SUMS, true, false>)
+              : (is_long ? strata::loss_kernel<strata::LOSS_SUMS, false, true> : strata::loss_kernel<strata::LOSS_SUMS, false, false>);
 }
+Kernel diffs_kernel(bool pair) { return pair ? strata::loss_kernel<strata::LOSS_DIFFS, true, false> : strata::loss_kernel<strata::LOSS_DIFFS, false, false>; }
 
 // What the calls need of a device, found at the first call on it.  A failure is not kept: the next call tries again.
 struct Device {
@@ -44,11 +45,11 @@ cudaError_t find_device(Device& d) {
       e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, strata::loss_smem(mode, pair));
   };
   for (bool pair : {false, true}) {
-    shared(kernel_for<strata::LOSS_SUMS>(pair), strata::LOSS_SUMS, pair);
-    shared(kernel_for<strata::LOSS_DIFFS>(pair), strata::LOSS_DIFFS, pair);
+    for (bool is_long : {false, true}) shared(sums_kernel(pair, is_long), strata::LOSS_SUMS, pair);
+    shared(diffs_kernel(pair), strata::LOSS_DIFFS, pair);
   }
-  shared(strata::loss_kernel<strata::LOSS_DW, true>, strata::LOSS_DW, true);
-  shared(strata::loss_kernel<strata::LOSS_DX, true>, strata::LOSS_DX, true);
+  shared(strata::loss_kernel<strata::LOSS_DW, true, false>, strata::LOSS_DW, true);
+  shared(strata::loss_kernel<strata::LOSS_DX, true, false>, strata::LOSS_DX, true);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(strata::loss_both_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, strata::loss_smem(strata::LOSS_DW, false));
   return e;
@@ -113,9 +114,8 @@ Tiles tiles_for(int rows, int64_t columns, int H, bool grad) {
     if (pair && rows <= ALONE_ROWS) break;
     const int64_t row_tiles = tiles_of(rows, pair ? 256 : 128);
     const int step = pair || grad ? 32 : 16;
-    // few rows are bound by reading w whatever the tiles: scores of long rows take narrow ones, which have two sums (below 1,024
-    // their lse is within 5e-7 with one)
-    for (int bn = rows <= ALONE_ROWS && H > 1024 && !grad ? 128 : 256; bn >= (grad ? 64 : pair ? 128 : 16); bn -= step) {
+    // few rows are bound by reading w whatever the tiles: scores of wide ones take narrow tiles, which have two sums
+    for (int bn = rows <= ALONE_ROWS && !grad && H > 512 ? 128 : 256; bn >= (grad ? 64 : pair ? 128 : 16); bn -= step) {
       const double turns = static_cast<double>(tiles_of(row_tiles * tiles_of(columns, bn), pair ? PAIRS : SMS));
       double cost = pair ? turns * (steps * (bn + 80) + 900) + 4000 : rows <= ALONE_ROWS ? turns * (bn + 16) : turns * (steps * (bn + 80) * 1.2 + 600);
       if (grad && !pair) cost *= 1.1;
@@ -165,7 +165,7 @@ struct Plan {
       copy = take(static_cast<int64_t>(rows_pad) * H * 2);
     }
     if (!grad) {
-      parts = take(slab * tiles_of(V, bn) * 8);
+      parts = take(slab * tiles_of(V, bn) * (is_long() ? 16 : 8));
       picks = take(static_cast<int64_t>(slab) * this->K * 4);
       return;
     }
@@ -177,6 +177,7 @@ struct Plan {
     splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(32, PARTS_BYTES / one)));
     dx = take(splits * one);
   }
+  bool is_long() const { return T > ALONE_ROWS && H > 64 * strata::LOSS_LONG; }
 };
 
 struct Loss {
@@ -318,11 +319,11 @@ int forward(const Loss& C, float* loss, float* lse, const char* name) {
     A.parts = at<float2>(C, P.parts);
     A.picks = at<float>(C, P.picks);
     strata::LossJoinArgs J{A.count, A.rows, A.ids, P.lists ? at<int32_t>(C, P.state) : nullptr, A.q, P.lists ? at<float>(C, P.logq) : nullptr,
-                           A.picks, A.parts, loss, lse, C.temperature, C.T, C.V, P.K, 0, A.n_tiles};
+                           A.picks, A.parts, loss, lse, C.temperature, C.T, C.V, P.K, 0, A.n_tiles * (P.is_long() ? 2 : 1)};
     for (int row0 = 0; row0 < C.T; row0 += P.slab) {
       A.row0 = J.row0 = row0;
       A.rows_most = std::min(P.slab, C.T - row0);
-      run.products<strata::LOSS_SUMS>(kernel_for<strata::LOSS_SUMS>(P.pair), P.pair, tiles_of(A.rows_most, P.tile_rows) * A.n_tiles, mx, mw, mw, mw, A);
+      run.products<strata::LOSS_SUMS>(sums_kernel(P.pair, P.is_long()), P.pair, tiles_of(A.rows_most, P.tile_rows) * A.n_tiles, mx, mw, mw, mw, A);
       run(strata::loss_join_kernel, static_cast<unsigned>(A.rows_most), 128, 0, 1, J);
     }
     return run.e;
@@ -383,7 +384,7 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
       A.n_tiles = static_cast<int>(tiles_of(A.columns, P.bn));
       A.out = at<__nv_bfloat16>(C, P.d);
       A.ldo = P.piece;
-      run.products<strata::LOSS_DIFFS>(kernel_for<strata::LOSS_DIFFS>(P.pair), P.pair, row_tiles * A.n_tiles, mx, mw, mw, mw, A);
+      run.products<strata::LOSS_DIFFS>(diffs_kernel(P.pair), P.pair, row_tiles * A.n_tiles, mx, mw, mw, mw, A);
       A.bn = P.width;
       A.n_tiles = static_cast<int>(across);
       A.out = static_cast<__nv_bfloat16*>(dw);
@@ -394,9 +395,9 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
         continue;
       }
       if (dw != nullptr)
-        run.products<strata::LOSS_DW>(strata::loss_kernel<strata::LOSS_DW, true>, true, tiles_of(A.columns, 256) * across, mds, mxo, mxs, mxs, A);
+        run.products<strata::LOSS_DW>(strata::loss_kernel<strata::LOSS_DW, true, false>, true, tiles_of(A.columns, 256) * across, mds, mxo, mxs, mxs, A);
       if (dx != nullptr)
-        run.products<strata::LOSS_DX>(strata::loss_kernel<strata::LOSS_DX, true>, true, row_tiles * across * P.splits, md, mwo, mwo, mdx, A);
+        run.products<strata::LOSS_DX>(strata::loss_kernel<strata::LOSS_DX, true, false>, true, row_tiles * across * P.splits, md, mwo, mwo, mdx, A);
     }
     if (dx != nullptr) {
       const strata::LossDxArgs D{A.count, A.rows, at<float>(C, P.dx), g, static_cast<__nv_bfloat16*>(dx), lddx, static_cast<int64_t>(P.rows_pad) * C.H,

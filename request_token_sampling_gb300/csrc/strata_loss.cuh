@@ -19,7 +19,7 @@
 // where a tile on one SM takes 96), six or seven stages of 32 KB on their way, and two accumulators, which four writing warps each
 // empty by turns.  Measured (one GB300, rows x ids x width): the sums of 2,048 x 32,000 x 2,048 140 us (1.92 PFLOP/s, a library
 // product's rate), differences, dw and dx 145, 148 and 149; a whole step of 4,096 x 32,000 x 4,096, an eighth of the rows left
-// out, 2,172 us in a stream of steps, which the power limit sets (1,893 alone).  Few rows are bound by HBM: tiles of 128 rows on one
+// out, 2,209 us in a stream of steps, which the power limit sets (1,893 alone).  Few rows are bound by HBM: tiles of 128 rows on one
 // SM, whose rows past the last one are neither loaded nor looked at: the sums of 64 x 248,320 x 2,048 150 us (6.8 TB/s); the step
 // of 96 such rows 666, of which w's three readings and dw's writing take 600 at the copy's rate.
 #pragma once
@@ -39,6 +39,11 @@ constexpr int LOSS_WRITERS = 8;       // four for each of the two accumulators: 
 constexpr int LOSS_BAND = 16;         // tiles of the inner index that a band has: what its operands take stays in L2
 constexpr int LOSS_RUNS = 4;          // steps of 64 rows up to which dw's tiles go in runs (below, where they are)
 constexpr int LOSS_NO_ID = 0x7FFFFFFF;
+// The tensor cores cut their sums off to 32 bits after every 16 products, always towards zero: lse of rows 1,024 wide is off by
+// 5e-7 of itself, of rows 4,096 wide by 2.4e-6.  So the scores' sums of many wider rows (LONG) are taken out of tensor memory and
+// added up in registers, rounded, every 16 steps of 64 (6e-7, for 1 % of a step's time; every 8 steps 3e-7, for 2 to 11 %).  Few
+// rows, where that takes 4 %, have narrow tiles instead, with two sums in tensor memory, one of each half of the width.
+constexpr int LOSS_LONG = 16;
 // Two SMs share a tile: 128 rows and half of the columns each; one SM alone has 128 rows and all columns.  What is left of
 // shared memory holds results on their way out, a piece of 32 rows for each writing warp.
 constexpr int LOSS_PIECE = 4096;
@@ -65,7 +70,7 @@ struct LossArgs {
   const float* lse;       // of row t, for LOSS_DIFFS
   const float* by;        // scale of LOSS_DW's results
   const int32_t* same;    // LOSS_DW: not 0 where all rows' scales are equal, and the rows need no scaled copy
-  float2* parts;          // [rows][n_tiles]: exponent and sum of a tile's columns, for LOSS_SUMS
+  float2* parts;          // [rows][n_tiles], or two of each tile (LONG): exponent and sum of the columns, for LOSS_SUMS
   float* picks;           // [rows][K]: z of the row's ids
   __nv_bfloat16* out;     // d or dw
   int64_t ldo;
@@ -99,6 +104,15 @@ __device__ __forceinline__ uint32_t loss_idesc(int m, int n, bool a_outer, bool 
   return (1u << 4) | (1u << 7) | (1u << 10) | (a_outer ? 1u << 15 : 0u) | (b_outer ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
 }
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]),
+      "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x), "r"(y), "r"(src) : "memory");
@@ -181,7 +195,7 @@ struct LossIds {
 };
 
 // As block `block` of `blocks`.  Maps: A, B, B of scaled rows (LOSS_DW), results (LOSS_DX).
-template <int MODE, bool PAIR>
+template <int MODE, bool PAIR, bool LONG>
 __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const CUtensorMap& mo, const LossArgs& A,
                                               int block, int blocks) {
   constexpr int RING = loss_ring_bytes(MODE, PAIR), TILE_M = PAIR ? 256 : 128;
@@ -204,7 +218,7 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->done[i], 1);
-      mbar_init(&B->freed[i], PAIR ? LOSS_WRITERS : LOSS_WRITERS / 2);  // the first block's: four warps of each
+      mbar_init(&B->freed[i], LOSS_WRITERS / (PAIR ? 1 : 2) * (LONG ? 2 : 1));  // the first block's: four warps of each, or all
     }
     mbar_init(&B->drained, 1);
     B->dead = 0;
@@ -265,18 +279,16 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
     }
   };
 
-  // The tensor cores cut their sums off to 32 bits after every 16 products, always towards zero.  Narrow tiles of logits have
-  // room for two sums, one of each half of the width, which leaves half of that (score of 64 rows x 2,048 wide: lse off by
-  // 4e-7 instead of 8e-7).
+  // two sums of a narrow tile of logits
   const int half_k = (k_all + 1) / 2;
-  const bool halves = (MODE == LOSS_SUMS || MODE == LOSS_DIFFS) && A.bn <= 128 && k_all > 1;
+  const bool halves = MODE == LOSS_SUMS && !LONG && A.bn <= 128 && k_all > 1;
 
   // rows that a stage holds: a pair's always as many, so that the numbers are known; of rows as B all that the tile has
   const int a_rows = PAIR || MODE == LOSS_DW ? 128 : A.a_rows, b_place = loss_b_place(a_rows);
   const int stage_bytes = PAIR ? loss_stage_bytes(128, 128) : loss_stage_bytes(a_rows, A.bn);
   LossRing ring{static_cast<uint32_t>(PAIR ? RING / loss_stage_bytes(128, 128) : loss_stages(RING, stage_bytes))};  // of the loading and of the issuing warp
   bool alive = true;
-  uint32_t turn = 0;  // tiles so far, of the issuing warp and of those that write
+  uint32_t turn = 0;  // accumulators so far, of the issuing warp and of those that write
   if (warp == 0) {
     asm volatile("fence.proxy.async;" ::: "memory");  // rows and d were written by ordinary stores of kernels before
     const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * (a_rows + half)) * LOSS_LINE;
@@ -318,45 +330,53 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
   } else if (warp == 1 && lead) {
     const uint32_t idesc = loss_idesc(TILE_M, A.bn, A_OUTER, B_OUTER);
     constexpr uint32_t STEP_A = A_OUTER ? 128 : 2, STEP_B = B_OUTER ? 128 : 2;  // 16 steps of the sum, in 16 bytes
-    for (int tile = first; tile < tiles && alive; tile += step, ++turn) {
-      const uint32_t buf = turn & 1, sum = tmem + buf * 256;
-      if (turn >= 2 && !proj_wait(&B->freed[buf], (turn / 2 + 1) & 1, dead, A.errors, bit)) {
-        alive = false;
-        break;
-      }
-      tc_fence_after();
+    for (int tile = first; tile < tiles && alive; tile += step) {
       int from, to;
       stages_of(MODE == LOSS_DX ? tile / per_split : 0, from, to);
-      for (int s = from; s < to; ++s, ring.next()) {
-        if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit)) {
+      // one accumulator for a tile, or for each 16 steps of it
+      for (int begin = from; alive; begin += LOSS_LONG, ++turn) {
+        const int end = LONG ? min(begin + LOSS_LONG, to) : to;
+        const uint32_t buf = turn & 1, sum = tmem + buf * 256;
+        if (turn >= 2 && !proj_wait(&B->freed[buf], (turn / 2 + 1) & 1, dead, A.errors, bit)) {
           alive = false;
           break;
         }
         tc_fence_after();
-        const uint32_t at = smem_u32(smem + ring.slot * stage_bytes), at_b = at + b_place;
-        const uint64_t da = A_OUTER ? loss_desc_outer(at) : mma_desc(at, LOSS_LINE), db = B_OUTER ? loss_desc_outer(at_b) : mma_desc(at_b, LOSS_LINE);
-        const bool later = halves && s >= half_k;
-        const uint32_t to_sum = later ? sum + 128 : sum;
-        const bool adds = s > (later ? half_k : from);
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (PAIR)
-              pair_mma(to_sum, da + STEP_A * i, db + STEP_B * i, idesc, adds || i > 0);
-            else
-              mma<false>(to_sum, da + STEP_A * i, db + STEP_B * i, idesc, adds || i > 0);
+        for (int s = begin; s < end; ++s, ring.next()) {
+          if (!proj_wait(&B->full[ring.slot], ring.phase, dead, A.errors, bit)) {
+            alive = false;
+            break;
           }
-          if constexpr (PAIR)
-            pair_commit(&B->empty[ring.slot]);
-          else
-            mma_commit(&B->empty[ring.slot]);
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem + ring.slot * stage_bytes), at_b = at + b_place;
+          const uint64_t da = A_OUTER ? loss_desc_outer(at) : mma_desc(at, LOSS_LINE), db = B_OUTER ? loss_desc_outer(at_b) : mma_desc(at_b, LOSS_LINE);
+          const bool later = halves && s >= half_k;
+          const uint32_t to_sum = later ? sum + 128 : sum;
+          const bool adds = s > (later ? half_k : begin);
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (PAIR)
+                pair_mma(to_sum, da + STEP_A * i, db + STEP_B * i, idesc, adds || i > 0);
+              else
+                mma<false>(to_sum, da + STEP_A * i, db + STEP_B * i, idesc, adds || i > 0);
+            }
+            if constexpr (PAIR)
+              pair_commit(&B->empty[ring.slot]);
+            else
+              mma_commit(&B->empty[ring.slot]);
+          }
         }
-      }
-      if (alive && elect_one()) {
-        if constexpr (PAIR)
-          pair_commit(&B->done[buf]);
-        else
-          mma_commit(&B->done[buf]);
+        if (alive && elect_one()) {
+          if constexpr (PAIR)
+            pair_commit(&B->done[buf]);
+          else
+            mma_commit(&B->done[buf]);
+        }
+        if (end >= to) {
+          ++turn;
+          break;
+        }
       }
     }
     if (!alive) {  // the products in flight end before the blocks give their tensor memory back
@@ -371,7 +391,9 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
     }
   } else if (warp >= 2) {
     const uint32_t quarter = warp & 3;
-    const uint32_t buf = (warp - 2) / 4;  // the accumulator that this warp empties
+    const uint32_t group = (warp - 2) / 4;
+    uint32_t buf = group;  // the accumulator that this warp empties: always the same one, but for LONG, where both groups share each
+    const int from_c = LONG ? static_cast<int>(group) * 128 : 0;  // and have half of the columns
     const uint32_t mine = smem_u32(staging) + (warp - 2) * LOSS_PIECE;  // this warp's piece
     // A lane fills the line of its row, 16 bytes at a time, swizzled so that lines and columns both go without bank conflicts
     // (and as a tensor copy expects it).
@@ -436,20 +458,19 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
       }
     };
     [[maybe_unused]] const float by = MODE == LOSS_DW ? *A.by * A.dw_scale : 1.0f;
-    const uint32_t sum = tmem + buf * 256 + (quarter << 21);
-    auto logits = [&](int c, float (&v)[32]) {
-      tmem_ld32(sum + c, v);
-      if (halves) {
-        float u[32];
-        tmem_ld32(sum + 128 + c, u);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] += u[e];
-      } else {
-        tmem_wait_ld();
+    const uint32_t lanes = quarter << 21;
+    auto empties = [&](uint32_t b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_remote(dsmem_addr(smem_u32(&B->freed[b]), 0));
+        else
+          mbar_arrive(&B->freed[b]);
       }
     };
-    for (int tile = first + static_cast<int>(buf) * step; tile < tiles; tile += 2 * step, ++turn) {
+    const int step_w = LONG ? step : 2 * step;
+    for (int tile = first + (LONG ? 0 : static_cast<int>(group) * step); tile < tiles; tile += step_w) {
       int o, i, from, to;
       const int split = MODE == LOSS_DX ? tile / per_split : 0;
       loss_place(tile - split * per_split, outer, inner, o, i);
@@ -457,66 +478,109 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
       const int in_tile = static_cast<int>(rank * 128 + quarter * 32);  // this warp's first lane
       const int r = i * TILE_M + in_tile + lane;                         // of SUMS and DIFFS: the row of this launch
       [[maybe_unused]] int64_t t = -1;
-      [[maybe_unused]] LossIds ids;
+      [[maybe_unused]] LossIds ids{};
       [[maybe_unused]] int n0 = 0;
       [[maybe_unused]] float lse2 = 0.0f;
       if constexpr (MODE == LOSS_SUMS || MODE == LOSS_DIFFS) {
         if (r < live) t = A.rows != nullptr ? A.rows[A.row0 + r] : A.row0 + r;
         n0 = A.v0 + o * A.bn;
-        ids.start(A, t, n0);
+        ids.start(A, t, n0 + from_c);
         if (MODE == LOSS_DIFFS && t >= 0) lse2 = A.lse[t] * 1.44269504088896340736f;
       }
-      if (!proj_wait(&B->done[buf], turn & 1, dead, A.errors, bit)) {
-        alive = false;
-        break;
-      }
-      tc_fence_after();
-      if constexpr (MODE == LOSS_SUMS) {
-        const int columns = min(A.bn, A.v0 + A.columns - n0);
-        float top = -INFINITY, base = 0.0f, total = 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < columns; c += 32) {
-          float v[32];
-          logits(c, v);
-          if (columns - c < 32) {
+      const int columns = min(A.bn, A.v0 + A.columns - n0);  // of LOSS_SUMS
+      [[maybe_unused]] float top = -INFINITY, base = 0.0f, total = 0.0f;
+      // 32 logits of the row, of columns c ..
+      [[maybe_unused]] auto add_logits = [&](float (&v)[32], int c) {
+        if (columns - c < 32) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = c + e < columns ? v[e] : -INFINITY;
-          }
-          const int end = n0 + min(c + 32, columns);
-          while (__any_sync(FULL_MASK, ids.next < end)) {
-            if (ids.next < end) {
-              float z = 0.0f;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const bool it = ids.next == n0 + c + e;
-                z = it ? v[e] : z;
-                if (A.q == nullptr) v[e] = it ? -INFINITY : v[e];  // a cross entropy: the sum is that of the other ids
-              }
-              A.picks[static_cast<int64_t>(r) * A.K + ids.at] = z;
-              ids.advance();
-            }
-          }
-          float m = v[0];
-#pragma unroll
-          for (int e = 1; e < 32; ++e) m = fmaxf(m, v[e]);
-          top = fmaxf(top, m);
-          const float now = fabsf(top) < INFINITY ? top * A.scale : 0.0f;
-          float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            s0 += ex2_approx(fmaf(v[e], A.scale, -now));
-            s1 += ex2_approx(fmaf(v[e + 1], A.scale, -now));
-          }
-          total = (total > 0.0f ? total * ex2_approx(base - now) : total) + (s0 + s1);
-          base = now;
+          for (int e = 0; e < 32; ++e) v[e] = c + e < columns ? v[e] : -INFINITY;
         }
-        if (t >= 0) A.parts[static_cast<int64_t>(r) * A.n_tiles + o] = make_float2(base, total);
+        const int end = n0 + min(c + 32, columns);
+        while (__any_sync(FULL_MASK, ids.next < end)) {
+          if (ids.next < end) {
+            float z = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const bool it = ids.next == n0 + c + e;
+              z = it ? v[e] : z;
+              if (A.q == nullptr) v[e] = it ? -INFINITY : v[e];  // a cross entropy: the sum is that of the other ids
+            }
+            A.picks[static_cast<int64_t>(r) * A.K + ids.at] = z;
+            ids.advance();
+          }
+        }
+        float m = v[0];
+#pragma unroll
+        for (int e = 1; e < 32; ++e) m = fmaxf(m, v[e]);
+        top = fmaxf(top, m);
+        const float now = fabsf(top) < INFINITY ? top * A.scale : 0.0f;
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          s0 += ex2_approx(fmaf(v[e], A.scale, -now));
+          s1 += ex2_approx(fmaf(v[e + 1], A.scale, -now));
+        }
+        total = (total > 0.0f ? total * ex2_approx(base - now) : total) + (s0 + s1);
+        base = now;
+      };
+      if constexpr (LONG) {
+        // this warp's 128 columns: what the accumulators had is added up, and put back into the last one
+        float z[8][16] = {};
+        for (int begin = from; begin < to; begin += LOSS_LONG, ++turn) {
+          buf = turn & 1;
+          if (!proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          const bool last = begin + LOSS_LONG >= to;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // columns beyond the tile's are there, and not looked at
+            float v[16];
+            const uint32_t at = tmem + buf * 256 + lanes + from_c + j * 16;
+            tmem_ld16(at, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z[j][e] += v[e];
+            if (last) tmem_st16(at, z[j]);
+          }
+          if (!last) empties(buf);
+        }
+        if (!alive) break;
+        tmem_wait_st();
+      } else {
+        if (!proj_wait(&B->done[buf], turn & 1, dead, A.errors, bit)) {
+          alive = false;
+          break;
+        }
+        ++turn;
+        tc_fence_after();
+      }
+      const uint32_t sum = tmem + buf * 256 + lanes;
+      if constexpr (MODE == LOSS_SUMS) {
+#pragma unroll 1
+        for (int c = from_c; c < (LONG ? min(columns, from_c + 128) : columns); c += 32) {
+          float v[32];
+          tmem_ld32(sum + c, v);
+          if (halves) {
+            float u[32];
+            tmem_ld32(sum + 128 + c, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] += u[e];
+          } else {
+            tmem_wait_ld();
+          }
+          add_logits(v, c);
+        }
+        if (t >= 0) A.parts[(static_cast<int64_t>(r) * A.n_tiles + o) * (LONG ? 2 : 1) + (LONG ? group : 0)] = make_float2(base, total);
       } else if constexpr (MODE == LOSS_DIFFS) {
         const int upto = t < 0 ? 0 : A.v0 + A.columns - n0;  // zeros beyond the rows and the vocabulary
 #pragma unroll 1
         for (int c = 0; c < A.bn; c += 32) {
           float v[32];
-          logits(c, v);
+          tmem_ld32(sum + c, v);
+          tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = ex2_approx(fmaf(v[e], A.scale, -lse2));
           while (__any_sync(FULL_MASK, ids.next < n0 + c + 32)) {
@@ -567,14 +631,7 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR)
-          mbar_arrive_remote(dsmem_addr(smem_u32(&B->freed[buf]), 0));
-        else
-          mbar_arrive(&B->freed[buf]);
-      }
+      empties(buf);
     }
     if (MODE == LOSS_DX && lane == 0) tma_store_wait_all();
   }
@@ -592,11 +649,11 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
   }
 }
 
-template <int MODE, bool PAIR>
+template <int MODE, bool PAIR, bool LONG>
 __global__ void __launch_bounds__(LOSS_THREADS, 1)
     loss_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mc,
                 const __grid_constant__ CUtensorMap mo, const __grid_constant__ LossArgs A) {
-  loss_products<MODE, PAIR>(ma, mb, mc, mo, A, blockIdx.x, gridDim.x);
+  loss_products<MODE, PAIR, LONG>(ma, mb, mc, mo, A, blockIdx.x, gridDim.x);
 }
 
 // Both products of few rows: dw is bound by writing to memory, dx by reading w, so blocks of both kinds (`dx_blocks` of dx,
@@ -607,9 +664,9 @@ __global__ void __launch_bounds__(LOSS_THREADS, 1)
                      const __grid_constant__ LossArgs W, const __grid_constant__ LossArgs X, int dx_blocks) {
   const int block = static_cast<int>(blockIdx.x), blocks = static_cast<int>(gridDim.x), before = block * dx_blocks / blocks;
   if ((block + 1) * dx_blocks / blocks > before)
-    loss_products<LOSS_DX, false>(xa, xb, xb, xo, X, before, dx_blocks);
+    loss_products<LOSS_DX, false, false>(xa, xb, xb, xo, X, before, dx_blocks);
   else
-    loss_products<LOSS_DW, false>(wa, wb, wc, wc, W, block - before, blocks - dx_blocks);
+    loss_products<LOSS_DW, false, false>(wa, wb, wc, wc, W, block - before, blocks - dx_blocks);
 }
 
 // ------------------------------------------------------------------------------ a teacher's tokens
