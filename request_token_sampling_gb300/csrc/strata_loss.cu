@@ -93,6 +93,8 @@ constexpr int ALONE_ROWS = 128;           // a call with more may work by pairs 
 // share: with a quarter of them it pays from here on (ns).
 constexpr double MOVE_COST = 30000;
 constexpr int SLAB_ROWS = 8192;           // whose tiles' sums are held at a time
+// Of differences held at a time: pieces that would stay in L2 have more turns that leave SMs idle (distillation of 1,024 rows x
+// 248,320 x 2,048, us: 64 MB 2,694, 128 MB 2,633, 512 MB 2,559, 2 GB 2,564).  And of parts of dx.
 constexpr int64_t PIECE_BYTES = int64_t{512} << 20, PARTS_BYTES = int64_t{256} << 20;
 
 int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
@@ -372,6 +374,10 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
     A.wide = !misaligned(dw, 32) && lddw % 16 == 0 && C.H % 16 == 0;
     A.by = at<float>(C, P.by);
     A.same = at<int32_t>(C, P.same);
+    const bool whole = P.piece >= C.V;
+    A.dx = whole ? static_cast<__nv_bfloat16*>(dx) : nullptr;
+    A.lddx = lddx;
+    A.g = g;
     const int64_t row_tiles = P.rows_pad / P.tile_rows, across = tiles_of(C.H, P.width);
     for (int v0 = 0; v0 < C.V; v0 += P.piece) {
       A.v0 = v0;
@@ -401,7 +407,7 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
     }
     if (dx != nullptr) {
       const strata::LossDxArgs D{A.count, A.rows, at<float>(C, P.dx), g, static_cast<__nv_bfloat16*>(dx), lddx, static_cast<int64_t>(P.rows_pad) * C.H,
-                                 C.temperature, C.H, P.splits, A.k_piece, A.units, P.width, P.tile_rows};
+                                 C.temperature, C.H, P.splits, A.k_piece, A.units, P.width, P.tile_rows, whole};
       if (run.e == cudaSuccess) {
         strata::Launch launch(static_cast<unsigned>(C.T), 128, 0, C.stream, run.overlaps);
         launch.cfg.gridDim.y = static_cast<unsigned>((C.H + 511) / 512);

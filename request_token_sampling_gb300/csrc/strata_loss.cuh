@@ -7,7 +7,7 @@
 //   LOSS_SUMS   z of up to 256 rows and 256 ids: a maximum and a sum of exponentials for each row, and z of the row's ids
 //   LOSS_DIFFS  z again, and d = exp(z - lse) - q in bfloat16 to the workspace, for a piece of the vocabulary
 //   LOSS_DW     dw of the piece: d^T xs over the rows (both operands with the sum's index outermost in memory)
-//   LOSS_DX     parts of dx: d w over the piece's ids (w with the sum's index outermost), in 32 bits
+//   LOSS_DX     parts of dx: d w over the piece's ids (w with the sum's index outermost), in 32 bits, or dx where one is all
 // Between d and its products stands one rounding to bfloat16, the type of w and x, which the tensor cores ask for: at most 2^-8 of
 // each term, as far off as the results' own rounding.  g stays out of d: dx is scaled in 32 bits at the end, and
 // x of a row is scaled by g / max|g| in xs, which changes nothing where all g are equal (a mean).
@@ -19,7 +19,7 @@
 // where a tile on one SM takes 96), six or seven stages of 32 KB on their way, and two accumulators, which four writing warps each
 // empty by turns.  Measured (one GB300, rows x ids x width): the sums of 2,048 x 32,000 x 2,048 140 us (1.92 PFLOP/s, a library
 // product's rate), differences, dw and dx 145, 148 and 149; a whole step of 4,096 x 32,000 x 4,096, an eighth of the rows left
-// out, 2,209 us in a stream of steps, which the power limit sets (1,893 alone).  Few rows are bound by HBM: tiles of 128 rows on one
+// out, 2,169 us in a stream of steps, which the power limit sets (1,893 alone).  Few rows are bound by HBM: tiles of 128 rows on one
 // SM, whose rows past the last one are neither loaded nor looked at: the sums of 64 x 248,320 x 2,048 150 us (6.8 TB/s); the step
 // of 96 such rows 666, of which w's three readings and dw's writing take 600 at the copy's rate.
 #pragma once
@@ -86,6 +86,9 @@ struct LossArgs {
   int splits, rows_pad;   // LOSS_DX: parts that a piece may be cut into, and rows of each
   int k_piece, units;     // steps of 64 ids in a piece, and tiles that run at a time
   int add;                // LOSS_DX: onto what is there
+  __nv_bfloat16* dx;      // LOSS_DX: where one part is all, the results themselves, scaled by g; NULL: there are more pieces
+  int64_t lddx;
+  const float* g;
 };
 
 struct LossBars {
@@ -414,19 +417,19 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
     };
     // Whole lines of 128 bytes to memory: rows y .., columns x .. of A.out, 32 bytes a lane where they lie on that, else 16.
     // (Tensor copies want a fence between the proxies for each piece, in which the warps spent a third of their time.)
+    auto line_piece = [&](int row, int piece) {
+      uint4 v;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(mine + row * 128 + ((piece ^ (row & 7)) << 4)) : "memory");
+      return v;
+    };
     auto write_lines = [&](int64_t y, int x, int rows, int columns) {
       __syncwarp();
-      auto get = [&](int row, int piece) {
-        uint4 v;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(mine + row * 128 + ((piece ^ (row & 7)) << 4)) : "memory");
-        return v;
-      };
       if (MODE == LOSS_DIFFS || A.wide != 0) {
         const int row = lane >> 2, piece = (lane & 3) * 2;
         __nv_bfloat16* to = A.out + (y + row) * A.ldo + x + piece * 8;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const uint4 v = get(n * 8 + row, piece), u = get(n * 8 + row, piece + 1);
+          const uint4 v = line_piece(n * 8 + row, piece), u = line_piece(n * 8 + row, piece + 1);
           if (n * 8 + row < rows && piece * 8 < columns)
             asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + n * 8 * A.ldo), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
         }
@@ -435,7 +438,7 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
         __nv_bfloat16* to = A.out + (y + row) * A.ldo + x + piece * 8;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          const uint4 v = get(n * 4 + row, piece);
+          const uint4 v = line_piece(n * 4 + row, piece);
           if (n * 4 + row < rows && piece * 8 < columns) *reinterpret_cast<uint4*>(to + n * 4 * A.ldo) = v;
         }
       }
@@ -597,6 +600,31 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
           }
           put32(c & 32, v);
           if ((c & 32) != 0 || c + 32 >= A.bn) write_lines(i * TILE_M + in_tile, o * A.bn + (c & ~32), 32, (c & 32) + 32);
+        }
+      } else if (MODE == LOSS_DX && splits == 1 && A.dx != nullptr) {
+        if (r < live) t = A.rows[r];
+        const float scale = t >= 0 ? A.g[t] * A.dw_scale : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < A.bn; c += 64) {
+          const int x = o * A.bn + c;
+          if (x >= A.H) break;
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            float v[32];
+            tmem_ld32(sum + c + h, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= scale;
+            put32(h, v);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {  // rows wherever they belong, four lines at a time
+            const int row = n * 4 + (lane >> 3), piece = lane & 7, to = __shfl_sync(FULL_MASK, static_cast<int>(t), row);
+            const uint4 v = line_piece(row, piece);
+            if (to >= 0 && piece * 8 < A.H - x) *reinterpret_cast<uint4*>(A.dx + to * A.lddx + x + piece * 8) = v;
+          }
         }
       } else {
         const bool none = from == to;  // no rows, or a part without ids: nothing was added up
@@ -947,6 +975,7 @@ struct LossDxArgs {
   int64_t lddx, part;  // elements from one part to the next
   float s;
   int H, splits, k_piece, units, width, tile_rows;  // as LOSS_DX had them
+  bool whole;                                       // one piece: one part of it has been written already
 };
 
 // dx from its parts, added up in order: 512 columns of a row a block, four a thread.
@@ -958,7 +987,7 @@ __global__ void __launch_bounds__(128) loss_dx_kernel(const __grid_constant__ Lo
   if (r >= count) return;
   const int tiles = (count + A.tile_rows - 1) / A.tile_rows * ((A.H + A.width - 1) / A.width);
   const int splits = loss_splits(tiles, A.k_piece, A.splits, A.units, A.tile_rows == 256);
-  if (c >= A.H) return;
+  if (c >= A.H || (A.whole && splits == 1)) return;
   const int64_t t = A.rows[r];
   const float by = A.g[t] * A.s;
   const float* at = A.parts + r * A.H + c;

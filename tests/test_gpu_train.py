@@ -805,3 +805,16 @@ def test_outputs_that_share_an_allocation_are_apart(G):
         assert torch.equal(given, d["dweight"]) and set(e) == {"dx", "dweight"}
         spans = sorted((v.data_ptr(), v.data_ptr() + v.numel() * v.element_size()) for v in d.values())
         assert all(a[1] <= c[0] for a, c in zip(spans, spans[1:]))
+
+
+@pytest.mark.parametrize("T,V,H", [(40000, 70, 72), (20000, 300, 264), (4100, 90, 4096)])
+def test_dx_of_many_rows_in_one_part(G, T, V, H):
+    """Enough tiles of dx that the sum over the ids is not cut: written straight to the rows that take part, any distance apart."""
+    x, w, ids, _ = loss_case(T, V, H, 17, skip=0.4)
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    g = _normal(_gen(5), T)
+    buf = torch.full((T, H + 24), -7.0, device="cuda").to(BF)
+    d = G.cross_entropy_grad(x, w, ids, o["lse"], g, dw=False, out=dict(dx=buf[:, 8:8 + H]))
+    e.check_grad(d, g)
+    assert (torch.cat([buf[:, :8], buf[:, 8 + H:]], 1).float() == -7.0).all()
