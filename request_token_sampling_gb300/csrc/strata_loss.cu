@@ -130,7 +130,7 @@ Tiles tiles_for(int rows, int64_t columns, int H, bool grad) {
 struct Plan {
   int T, V, H, K;
   bool lists, grad, pair, moved;    // a teacher's tokens; for a gradient; tiles of two SMs; works on a copy of the rows
-  int tile_rows = 0, rows_pad = 0, slab = 0, bn = 0;  // slab: rows whose tiles' sums are held at a time; bn: columns of a tile of logits
+  int tile_rows = 0, rows_pad = 0, d_rows = 0, slab = 0, bn = 0;  // slab: rows whose tiles' sums are held at a time; bn: columns of a tile of logits
   int piece = 0, splits = 1, width = 0;       // ids of a piece; most parts of dx; columns of a tile of dw and dx
   int64_t sorted = 0, q = 0, logq = 0, state = 0, rows = 0, place = 0, count = 0, by = 0, same = 0, copy = 0, scaled = 0, parts = 0, picks = 0,
           d = 0, dx = 0, bytes = 0;           // places in the workspace
@@ -173,7 +173,8 @@ struct Plan {
     }
     scaled = take(static_cast<int64_t>(rows_pad) * H * 2);
     piece = static_cast<int>(tiles_of(piece, 2 * bn) * 2 * bn);  // whole tiles, and steps of 64
-    d = take(static_cast<int64_t>(rows_pad) * piece * 2);
+    d_rows = T <= ALONE_ROWS ? (T + 7) / 8 * 8 : rows_pad;  // few rows: no more than they have; beyond, copies bring zeros
+    d = take(static_cast<int64_t>(d_rows) * piece * 2);
     width = H <= 128 ? 128 : 256;
     const int64_t one = static_cast<int64_t>(rows_pad) * H * 4;
     splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(32, PARTS_BYTES / one)));
@@ -290,6 +291,7 @@ strata::LossArgs products_args(const Loss& C, const Plan& P, uint32_t* errors) {
   A.rows_most = P.rows_pad;
   A.rows_pad = P.rows_pad;
   A.a_rows = std::min(128, (C.T + 7) / 8 * 8);
+  A.d_rows = P.d_rows;
   A.splits = P.splits;
   A.k_piece = P.piece / 64;
   return A;
@@ -358,8 +360,8 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
   CUtensorMap mx, mw, mxo, mxs, mwo, md, mds, mdx;
   const int a_rows = P.pair ? 128 : std::min(128, (C.T + 7) / 8 * 8);
   if (!map_rows(*dev, &mx, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, a_rows) ||
-      !map_rows(*dev, &mxo, false, at<void>(C, P.copy), C.H, P.rows_pad, C.H, 64) ||
-      !map_rows(*dev, &mxs, false, at<void>(C, P.scaled), C.H, P.rows_pad, C.H, 64) ||
+      !map_rows(*dev, &mxo, false, at<void>(C, P.copy), C.H, P.d_rows, C.H, 64) ||
+      !map_rows(*dev, &mxs, false, at<void>(C, P.scaled), C.H, P.d_rows, C.H, 64) ||
       !map_rows(*dev, &mdx, true, at<void>(C, P.dx), C.H, static_cast<int64_t>(P.splits) * P.rows_pad, C.H, 32))
     return host_fail(STRATA_EINVAL, "the workspace cannot be mapped");
   if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, P.pair ? P.bn / 2 : P.bn) || !map_rows(*dev, &mwo, false, C.w, C.H, C.V, C.ldw, 64))
@@ -383,8 +385,8 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
       A.v0 = v0;
       A.columns = std::min(P.piece, C.V - v0);
       // what lies beyond the piece's ids is not looked at, but read as zeros
-      if (!map_rows(*dev, &md, false, at<void>(C, P.d), A.columns, P.rows_pad, P.piece, a_rows) ||
-          !map_rows(*dev, &mds, false, at<void>(C, P.d), A.columns, P.rows_pad, P.piece, 64))
+      if (!map_rows(*dev, &md, false, at<void>(C, P.d), A.columns, P.d_rows, P.piece, a_rows) ||
+          !map_rows(*dev, &mds, false, at<void>(C, P.d), A.columns, P.d_rows, P.piece, 64))
         return cudaErrorInvalidValue;
       A.bn = P.bn;
       A.n_tiles = static_cast<int>(tiles_of(A.columns, P.bn));

@@ -83,6 +83,7 @@ struct LossArgs {
   int v0, columns;        // the piece of the vocabulary
   int bn, n_tiles;        // columns of a tile, and tiles of them
   int a_rows;             // rows that one SM's tile brings where they are A; the accumulator's other rows are not looked at
+  int d_rows;             // rows that d has
   int splits, rows_pad;   // LOSS_DX: parts that a piece may be cut into, and rows of each
   int k_piece, units;     // steps of 64 ids in a piece, and tiles that run at a time
   int add;                // LOSS_DX: onto what is there
@@ -480,6 +481,8 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
       stages_of(split, from, to);
       const int in_tile = static_cast<int>(rank * 128 + quarter * 32);  // this warp's first lane
       const int r = i * TILE_M + in_tile + lane;                         // of SUMS and DIFFS: the row of this launch
+      // of these 32 rows none takes part (those of d that the products for dw read are zeros)
+      const bool idle = MODE != LOSS_DW && r - lane >= (MODE == LOSS_DIFFS ? min(A.d_rows, (live + 63) / 64 * 64) : live);
       [[maybe_unused]] int64_t t = -1;
       [[maybe_unused]] LossIds ids{};
       [[maybe_unused]] int n0 = 0;
@@ -539,6 +542,7 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
           const bool last = begin + LOSS_LONG >= to;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {  // columns beyond the tile's are there, and not looked at
+            if (idle) break;
             float v[16];
             const uint32_t at = tmem + buf * 256 + lanes + from_c + j * 16;
             tmem_ld16(at, v);
@@ -560,7 +564,8 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
         tc_fence_after();
       }
       const uint32_t sum = tmem + buf * 256 + lanes;
-      if constexpr (MODE == LOSS_SUMS) {
+      if (idle) {
+      } else if constexpr (MODE == LOSS_SUMS) {
 #pragma unroll 1
         for (int c = from_c; c < (LONG ? min(columns, from_c + 128) : columns); c += 32) {
           float v[32];
@@ -599,7 +604,7 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
             for (int e = 0; e < 32; ++e) v[e] = c + e < upto ? v[e] : 0.0f;
           }
           put32(c & 32, v);
-          if ((c & 32) != 0 || c + 32 >= A.bn) write_lines(i * TILE_M + in_tile, o * A.bn + (c & ~32), 32, (c & 32) + 32);
+          if ((c & 32) != 0 || c + 32 >= A.bn) write_lines(i * TILE_M + in_tile, o * A.bn + (c & ~32), A.d_rows - i * TILE_M - in_tile, (c & 32) + 32);
         }
       } else if (MODE == LOSS_DX && splits == 1 && A.dx != nullptr) {
         if (r < live) t = A.rows[r];
