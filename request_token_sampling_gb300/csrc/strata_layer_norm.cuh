@@ -61,32 +61,25 @@ __host__ __device__ constexpr int layer_norm_most_threads(int n, int per) { retu
 // The joins of a row's sum and of its squared differences.  Each warp takes both about its own mean, by shuffles, and the
 // warps' come together behind one barrier: the squares about the row's mean are the warps' and, for each warp, its elements times
 // the square of what the means differ by.  `mine`: this warp's elements.
-__device__ __forceinline__ float layer_norm_mean(float s, int mine) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  return mine > 0 ? s / static_cast<float>(mine) : 0.0f;
+__device__ __forceinline__ float layer_norm_mean(float& sum, int mine) {
+  sum = warp_sum(sum);
+  return mine > 0 ? sum / static_cast<float>(mine) : 0.0f;
 }
 template <bool BLOCK>
-__device__ __forceinline__ void layer_norm_join(float& mean, float& squares, int mine, int H, float (*part)[32]) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(0xFFFFFFFFu, squares, o);
+__device__ __forceinline__ void layer_norm_join(float& mean, float& squares, float sum, int mine, int H, float (*part)[32]) {
+  squares = warp_sum(squares);
   if constexpr (BLOCK) {
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) {
-      part[0][threadIdx.x >> 5] = mean;
+      part[0][threadIdx.x >> 5] = sum;
       part[1][threadIdx.x >> 5] = squares;
       part[2][threadIdx.x >> 5] = static_cast<float>(mine);
     }
     __syncthreads();
-    const float m = lane < warps ? part[0][lane] : 0.0f, n = lane < warps ? part[2][lane] : 0.0f;
-    mean = m * n;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mean += __shfl_xor_sync(0xFFFFFFFFu, mean, o);
-    mean /= static_cast<float>(H);
-    const float d = m - mean;
-    squares = lane < warps ? fmaf(n * d, d, part[1][lane]) : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) squares += __shfl_xor_sync(0xFFFFFFFFu, squares, o);
+    const float s = lane < warps ? part[0][lane] : 0.0f, n = lane < warps ? part[2][lane] : 0.0f;
+    mean = warp_sum(s) / static_cast<float>(H);
+    const float d = n > 0.0f ? s / n - mean : 0.0f;
+    squares = warp_sum(lane < warps ? fmaf(n * d, d, part[1][lane]) : 0.0f);
   }
 }
 
@@ -153,7 +146,7 @@ __global__ void __launch_bounds__(BLOCK ? layer_norm_most_threads(N, PER) : 128)
       ss = fmaf(d, d, ss);
     }
   }
-  layer_norm_join<BLOCK>(mean, ss, mine, A.H, part);
+  layer_norm_join<BLOCK>(mean, ss, s, mine, A.H, part);
   const float rstd = 1.0f / sqrtf(ss / static_cast<float>(A.H) + A.eps);
   if (me == 0) {
     if (A.mean != nullptr) A.mean[t] = mean;
@@ -247,7 +240,7 @@ __global__ void __launch_bounds__(LAYER_NORM_RING_THREADS + 32, 1) layer_norm_ri
     if (me == threads) ring.start(first, step, A.T);
     for (int64_t t = first, turn = 0; t < A.T; t += step, turn ^= 1) {
       float none = 0.0f, nothing = 0.0f;
-      layer_norm_join<true>(none, nothing, 0, A.H, part[turn]);
+      layer_norm_join<true>(none, nothing, 0.0f, 0, A.H, part[turn]);
       if (me == threads) ring.refill(t, step, A.T);
       ring.next();
     }
@@ -312,7 +305,7 @@ __global__ void __launch_bounds__(LAYER_NORM_RING_THREADS + 32, 1) layer_norm_ri
         ss = fmaf(d, d, ss);
       }
     }
-    layer_norm_join<true>(mean, ss, mine, A.H, part[turn]);
+    layer_norm_join<true>(mean, ss, s, mine, A.H, part[turn]);
     ring.next();
     const float rstd = rsqrtf(fmaf(ss, over, A.eps));
     if (me == 0) {

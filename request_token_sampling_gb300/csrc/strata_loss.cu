@@ -87,7 +87,10 @@ bool map_rows(const Device& dev, CUtensorMap* m, bool f32, const void* p, int64_
 // ------------------------------------------------------------------------------ a call's plan
 // It goes by the sizes alone, so that the workspace's size can be asked for without a device.
 constexpr int SMS = 152, PAIRS = SMS / 2;
-constexpr int DX_BLOCKS = 64;             // of few rows' both products, with dw's in the others (96 x 248,320 x 2,048, the step, us: 40 729, 52 695, 64 664, 76 726)
+// Blocks of dx's product where few rows have both in one launch, dw's in the others.  dx's bring d's rows beside w, dw's write: up to
+// 32 rows want fewer (17 x 177,128 x 480, the way back, us: 44 112, 54 107, 64 115, 72 115; 5 x 84,656 x 984: 113, 108, 113, 119),
+// more rows more (96 x 248,320 x 2,048: 560, 539, 507, 542; 128 x 32,000 x 4,096: 170, 161, 155, 168).
+int dx_blocks_for(int T) { return T <= 32 ? 54 : 64; }
 constexpr int ALONE_ROWS = 128;           // a call with more may work by pairs of SMs
 // A score that takes longer works on a copy of the rows that take part.  The copy costs 4 us and rows that are left out save their
 // share: with a quarter of them it pays from here on (ns).
@@ -370,7 +373,7 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
     Run run{C.stream, overlaps};
     launch_plan(run, C, P, g, nullptr, nullptr, dx, lddx);
     strata::LossArgs A = products_args(C, P, errors);
-    const int dx_blocks = dx == nullptr ? 0 : dw == nullptr ? SMS : C.T <= ALONE_ROWS ? DX_BLOCKS : SMS / 2;  // both products cost the same
+    const int dx_blocks = dx == nullptr ? 0 : dw == nullptr ? SMS : C.T <= ALONE_ROWS ? dx_blocks_for(C.T) : SMS / 2;  // both products cost the same
     A.units = P.pair ? PAIRS : dx_blocks;
     A.lse = lse;
     A.wide = !misaligned(dw, 32) && lddw % 16 == 0 && C.H % 16 == 0;

@@ -19,9 +19,9 @@
 // where a tile on one SM takes 96), six or seven stages of 32 KB on their way, and two accumulators, which four writing warps each
 // empty by turns.  Measured (one GB300, rows x ids x width): the sums of 2,048 x 32,000 x 2,048 140 us (1.92 PFLOP/s, a library
 // product's rate), differences, dw and dx 145, 148 and 149; a whole step of 4,096 x 32,000 x 4,096, an eighth of the rows left
-// out, 2,169 us in a stream of steps, which the power limit sets (1,893 alone).  Few rows are bound by HBM: tiles of 128 rows on one
+// out, 2,140 us in a stream of steps, which the power limit sets (1,893 alone).  Few rows are bound by HBM: tiles of 128 rows on one
 // SM, whose rows past the last one are neither loaded nor looked at: the sums of 64 x 248,320 x 2,048 150 us (6.8 TB/s); the step
-// of 96 such rows 666, of which w's three readings and dw's writing take 600 at the copy's rate.
+// of 96 such rows 662, of which w's three readings and dw's writing take 600 at the copy's rate.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -818,3 +818,60 @@ def test_dx_of_many_rows_in_one_part(G, T, V, H):
     d = G.cross_entropy_grad(x, w, ids, o["lse"], g, dw=False, out=dict(dx=buf[:, 8:8 + H]))
     e.check_grad(d, g)
     assert (torch.cat([buf[:, :8], buf[:, 8 + H:]], 1).float() == -7.0).all()
+
+
+@pytest.mark.parametrize("T,V,H,K", [(5, 777, 64, 0), (17, 3001, 1096, 5), (100, 513, 72, 0), (128, 300, 520, 3), (130, 1000, 64, 0), (700, 2100, 1096, 2),
+                                     (1500, 130, 264, 0), (20000, 300, 72, 0)])
+def test_what_the_workspace_held_before_does_not_matter(G, T, V, H, K):
+    """A workspace full of NaN patterns, and outputs full of them: everything that is read has been written by the call."""
+    x, w, ids, teacher = loss_case(T, V, H, T + K, K=K, skip=0.4)
+    e = Exact(x, w, ids, teacher)
+    g = _normal(_gen(1), T)
+    f = lambda *shape, t=F32: torch.full(shape, math.nan, device="cuda").to(t)  # noqa: E731
+    ws = lambda grad: torch.full((G.strata_loss_workspace(T, V, H, K, grad),), 255, dtype=torch.uint8, device="cuda")  # noqa: E731
+    loss, lse, dx, dw = f(T), f(T), f(T, H, t=BF), f(V, H, t=BF)
+    for scale in (g, torch.full_like(g, 0.25)):
+        if K:
+            G.strata_distill_rows(x, w, ids, teacher, 1.0, loss, lse, ws(False))
+            G.strata_distill_grad(x, w, ids, teacher, 1.0, lse, scale, dx, dw, ws(True))
+        else:
+            G.strata_cross_entropy_rows(x, w, ids, loss, lse, ws(False))
+            G.strata_cross_entropy_grad(x, w, ids, lse, scale, dx, dw, ws(True))
+        e.check_rows(dict(loss=loss, lse=lse))
+        e.check_grad(dict(dx=dx, dw=dw), scale)
+    o = G.layer_norm_rows(x, w[0])
+    y, mean, rstd, dn, db = f(T, H, t=BF), f(T), f(T), f(H, t=BF), f(H, t=BF)
+    G.strata_layer_norm_rows(x, w[0], y=y, mean=mean, rstd=rstd)
+    assert torch.equal(y, o["y"]) and torch.equal(rstd, o["rstd"])
+    wn = torch.full((G.strata_layer_norm_workspace(T, H),), 255, dtype=torch.uint8, device="cuda")
+    G.strata_layer_norm_grad(y, x, w[0], mean, rstd, dx=dx, dweight=dn, dbias=db, workspace=wn)
+    check_layer_norm_grad(y, x, w[0], mean, rstd, None, dict(dx=dx, dweight=dn, dbias=db))
+
+
+@pytest.mark.parametrize("T,V,H,K", [(1, 9, 8, 0), (17, 3001, 1096, 5), (100, 513, 72, 0), (130, 1000, 64, 128), (700, 2100, 1096, 2), (1500, 130, 264, 0),
+                                     (2049, 140001, 16, 0)])
+def test_nothing_is_written_behind_the_workspace_and_the_outputs(G, T, V, H, K):
+    x, w, ids, teacher = loss_case(T, V, H, T + K, K=K, skip=0.1)
+    g = torch.ones(T, device="cuda")
+    guards = []
+
+    def guarded(n, t):
+        size = n * torch.empty(0, dtype=t).element_size()
+        buf = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        guards.append(buf[size:])
+        return buf[:size].view(t)
+
+    loss, lse, dx, dw = guarded(T, F32), guarded(T, F32), guarded(T * H, BF).view(T, H), guarded(V * H, BF).view(V, H)
+    ws, wg = (guarded(G.strata_loss_workspace(T, V, H, K, grad), torch.uint8) for grad in (False, True))
+    if K:
+        G.strata_distill_rows(x, w, ids, teacher, 1.0, loss, lse, ws)
+        G.strata_distill_grad(x, w, ids, teacher, 1.0, lse, g, dx, dw, wg)
+    else:
+        G.strata_cross_entropy_rows(x, w, ids, loss, lse, ws)
+        G.strata_cross_entropy_grad(x, w, ids, lse, g, dx, dw, wg)
+    mean, rstd, y, dn, db = guarded(T, F32), guarded(T, F32), guarded(T * H, BF).view(T, H), guarded(H, BF), guarded(H, BF)
+    wn = guarded(G.strata_layer_norm_workspace(T, H), torch.uint8)
+    G.strata_layer_norm_rows(x, w[0], y=y, mean=mean, rstd=rstd)
+    G.strata_layer_norm_grad(y, x, w[0], mean, rstd, dx=dx, dweight=dn, dbias=db, workspace=wn)
+    torch.cuda.synchronize()
+    assert all((b == 0xA5).all() for b in guards)
