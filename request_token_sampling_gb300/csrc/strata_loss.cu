@@ -102,6 +102,11 @@ constexpr int64_t PIECE_BYTES = int64_t{512} << 20, PARTS_BYTES = int64_t{256} <
 
 int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 
+// Whether a score's sums are taken out of tensor memory on the way.  Of few rows from twice the width on: up to there narrow tiles'
+// two sums cost less, beyond they are too long.  (Narrow tiles and these, us: 64 rows x 248,320 x 2,048 153.0 and 158.2, x 2,056
+// 185.6 and 173.6; 96 x 64,000 x 4,096 81.6 and 84.7; 16 x 8,000 x 8,192 28.9 and 30.0, and lse off by 1.8e-6 and 4e-7.)
+bool sums_long(int rows, int H) { return H > 64 * strata::LOSS_LONG * (rows <= ALONE_ROWS ? 2 : 1); }
+
 // Tiles of the logits: of two SMs or of one, and how many columns, by what their turns cost.  In ns, as measured: a step of 64
 // of a pair's tile (columns + 80), and each turn 900 beside it; tiles of one SM cost 20 % more a step and 600, but bring fewer
 // rows that are none, and start and hand their tiles over 4 us sooner.  (Score of 300 rows x 32,000 x 1,024, us: one SM 20, two
@@ -119,8 +124,8 @@ Tiles tiles_for(int rows, int64_t columns, int H, bool grad) {
     if (pair && rows <= ALONE_ROWS) break;
     const int64_t row_tiles = tiles_of(rows, pair ? 256 : 128);
     const int step = pair || grad ? 32 : 16;
-    // few rows are bound by reading w whatever the tiles: scores of wide ones take narrow tiles, which have two sums
-    for (int bn = rows <= ALONE_ROWS && !grad && H > 512 ? 128 : 256; bn >= (grad ? 64 : pair ? 128 : 16); bn -= step) {
+    // few rows are bound by reading w whatever the tiles: scores of wider ones take narrow tiles, which have two sums
+    for (int bn = rows <= ALONE_ROWS && !grad && H > 512 && !sums_long(rows, H) ? 128 : 256; bn >= (grad ? 64 : pair ? 128 : 16); bn -= step) {
       const double turns = static_cast<double>(tiles_of(row_tiles * tiles_of(columns, bn), pair ? PAIRS : SMS));
       double cost = pair ? turns * (steps * (bn + 80) + 900) + 4000 : rows <= ALONE_ROWS ? turns * (bn + 16) : turns * (steps * (bn + 80) * 1.2 + 600);
       if (grad && !pair) cost *= 1.1;
@@ -183,7 +188,7 @@ struct Plan {
     splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(32, PARTS_BYTES / one)));
     dx = take(splits * one);
   }
-  bool is_long() const { return T > ALONE_ROWS && H > 64 * strata::LOSS_LONG; }
+  bool is_long() const { return sums_long(T, H); }
 };
 
 struct Loss {

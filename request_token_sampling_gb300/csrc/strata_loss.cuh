@@ -40,9 +40,9 @@ constexpr int LOSS_BAND = 16;         // tiles of the inner index that a band ha
 constexpr int LOSS_RUNS = 4;          // steps of 64 rows up to which dw's tiles go in runs (below, where they are)
 constexpr int LOSS_NO_ID = 0x7FFFFFFF;
 // The tensor cores cut their sums off to 32 bits after every 16 products, always towards zero: lse of rows 1,024 wide is off by
-// 5e-7 of itself, of rows 4,096 wide by 2.4e-6.  So the scores' sums of many wider rows (LONG) are taken out of tensor memory and
-// added up in registers, rounded, every 16 steps of 64 (6e-7, for 1 % of a step's time; every 8 steps 3e-7, for 2 to 11 %).  Few
-// rows, where that takes 4 %, have narrow tiles instead, with two sums in tensor memory, one of each half of the width.
+// 5e-7 of itself, of rows 4,096 wide by 2.4e-6.  So the scores' sums of wider rows (LONG) are taken out of tensor memory and added up
+// in registers, rounded, every 16 steps of 64 (6e-7, for 1 % of a step's time; every 8 steps 3e-7, for 2 to 11 %).  Up to twice that
+// width few rows, where it takes 4 %, have narrow tiles instead, with two sums in tensor memory, one of each half of the width.
 constexpr int LOSS_LONG = 16;
 // Two SMs share a tile: 128 rows and half of the columns each; one SM alone has 128 rows and all columns.  What is left of
 // shared memory holds results on their way out, a piece of 32 rows for each writing warp.

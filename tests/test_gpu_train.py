@@ -875,3 +875,20 @@ def test_nothing_is_written_behind_the_workspace_and_the_outputs(G, T, V, H, K):
     G.strata_layer_norm_grad(y, x, w[0], mean, rstd, dx=dx, dweight=dn, dbias=db, workspace=wn)
     torch.cuda.synchronize()
     assert all((b == 0xA5).all() for b in guards)
+
+
+@pytest.mark.parametrize("T,V,H", [(1, 1310, 2056), (3, 2100, 8192), (33, 517, 4104), (128, 700, 2080), (9, 300, 32768), (130, 300, 32768)])
+def test_sums_of_wide_rows(G, T, V, H):
+    """Of products above 0 every partial sum is below the whole.  The tensor cores cut two times for 16 products (aligning them, and
+    the sum), each time at most 2^-23 of what is there, and 64 such steps at most follow one another before sums are added up,
+    rounded, at 2^-24: in all (128 + H / 2048) 2^-23 of z.  The rest of lse: scale * z and its way back, the maximum's
+    rounding and the sum's, 8 * 2^-24 of it."""
+    g = _gen(T + V + H)
+    x = (0.5 + torch.rand(T, H, generator=g, device="cuda")).to(BF)
+    w = ((0.5 + torch.rand(V, H, generator=g, device="cuda")) * (60.0 / H)).to(BF)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    o = G.cross_entropy_rows(x, w, ids)
+    z = x.double() @ w.double().T
+    want = torch.logsumexp(z, 1)
+    bound = (128 + H / 2048) * 2.0**-23 * z.amax(1) + 8 * 2.0**-24 * want
+    assert bool(((o["lse"].double() - want).abs() <= bound).all())
