@@ -82,7 +82,9 @@ int strata_cross_entropy_rows(const void* x, int64_t ldx, const void* w, int64_t
  *   dz[t][v] = g[t] * (exp(z[t][v] - lse[t]) - [v = ids[t]]),    dx = dz w,    dw = dz^T x
  * dx [T][H] and dw [V][H] are bfloat16 (either may be NULL).  The logits are computed again, in pieces of the vocabulary;
  * dz / g is rounded to bfloat16 between the products, and so is x[t] g[t] / max|g| (x itself where
- * all g are equal).  A row that is left out, whose id is V or more or whose g is 0 gets dx = 0 and adds nothing to dw.
+ * all g are equal).  With the T, V and H of the call that gave lse they are the same bits of z; so what is left of dz / g where a
+ * row is all but sure of its token is off by the rounding of lse, 3 * 2^-24 (|lse| + 1) at most (rows in other batches: by z's error, up to
+ * 3e-6 of z).  A row that is left out, whose id is V or more or whose g is 0 gets dx = 0 and adds nothing to dw.
  * With T = 0 dw is set to zeros.  dx and dw start on 16 bytes, their strides are multiples of 8, and they do not overlap an
  * input or one another.
  * `workspace`: strata_loss_workspace(T, V, H, 0, 1) bytes, which hold a piece of dz (512 MB, or 256

@@ -25,7 +25,10 @@ Kernel sums_kernel(bool pair, bool is_long) {
   return pair ? (is_long ? strata::loss_kernel<strata::LOSS_SUMS, true, true> : strata::loss_kernel<strata::LOSS_SUMS, true, false>)
               : (is_long ? strata::loss_kernel<strata::LOSS_SUMS, false, true> : strata::loss_kernel<strata::LOSS_SUMS, false, false>);
 }
-Kernel diffs_kernel(bool pair) { return pair ? strata::loss_kernel<strata::LOSS_DIFFS, true, false> : strata::loss_kernel<strata::LOSS_DIFFS, false, false>; }
+Kernel diffs_kernel(bool pair, bool is_long) {
+  return pair ? (is_long ? strata::loss_kernel<strata::LOSS_DIFFS, true, true> : strata::loss_kernel<strata::LOSS_DIFFS, true, false>)
+              : (is_long ? strata::loss_kernel<strata::LOSS_DIFFS, false, true> : strata::loss_kernel<strata::LOSS_DIFFS, false, false>);
+}
 
 // What the calls need of a device, found at the first call on it.  A failure is not kept: the next call tries again.
 struct Device {
@@ -45,8 +48,10 @@ cudaError_t find_device(Device& d) {
       e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, strata::loss_smem(mode, pair));
   };
   for (bool pair : {false, true}) {
-    for (bool is_long : {false, true}) shared(sums_kernel(pair, is_long), strata::LOSS_SUMS, pair);
-    shared(diffs_kernel(pair), strata::LOSS_DIFFS, pair);
+    for (bool is_long : {false, true}) {
+      shared(sums_kernel(pair, is_long), strata::LOSS_SUMS, pair);
+      shared(diffs_kernel(pair, is_long), strata::LOSS_DIFFS, pair);
+    }
   }
   shared(strata::loss_kernel<strata::LOSS_DW, true, false>, strata::LOSS_DW, true);
   shared(strata::loss_kernel<strata::LOSS_DX, true, false>, strata::LOSS_DX, true);
@@ -139,6 +144,7 @@ struct Plan {
   int T, V, H, K;
   bool lists, grad, pair, moved;    // a teacher's tokens; for a gradient; tiles of two SMs; works on a copy of the rows
   int tile_rows = 0, rows_pad = 0, d_rows = 0, slab = 0, bn = 0;  // slab: rows whose tiles' sums are held at a time; bn: columns of a tile of logits
+  int run = 0;                                // steps of 64 whose products one sum of a logit has in tensor memory
   int piece = 0, splits = 1, width = 0;       // ids of a piece; most parts of dx; columns of a tile of dw and dx
   int64_t sorted = 0, q = 0, logq = 0, state = 0, rows = 0, place = 0, count = 0, by = 0, same = 0, copy = 0, scaled = 0, parts = 0, picks = 0,
           d = 0, dx = 0, bytes = 0;           // places in the workspace
@@ -148,7 +154,10 @@ struct Plan {
     slab = std::min(T, SLAB_ROWS);
     // a piece of the vocabulary whose differences are held at a time
     piece = static_cast<int>(std::min<int64_t>(tiles_of(V, 256) * 256, std::max<int64_t>(256, PIECE_BYTES / (tiles_of(T, 256) * 512) / 256 * 256)));
-    const Tiles tiles = tiles_for(grad ? T : slab, grad ? std::min(piece, V) : V, H, grad);
+    const Tiles scores = tiles_for(slab, V, H, false), tiles = grad ? tiles_for(T, std::min(piece, V), H, true) : scores;
+    // a gradient's logits are added up as its score's were, whatever its tiles
+    const int steps = static_cast<int>(tiles_of(H, 64));
+    run = is_long() ? strata::LOSS_LONG : scores.columns <= 128 ? (steps + 1) / 2 : steps;
     pair = tiles.pair;
     moved = grad || (T > ALONE_ROWS && (tiles.cost > MOVE_COST || T > slab));
     bn = tiles.columns;
@@ -189,6 +198,7 @@ struct Plan {
     dx = take(splits * one);
   }
   bool is_long() const { return sums_long(T, H); }
+  bool in_runs() const { return run < tiles_of(H, 64); }  // of a gradient, whose tiles may be too wide for two sums
 };
 
 struct Loss {
@@ -300,6 +310,7 @@ strata::LossArgs products_args(const Loss& C, const Plan& P, uint32_t* errors) {
   A.rows_pad = P.rows_pad;
   A.a_rows = std::min(128, (C.T + 7) / 8 * 8);
   A.d_rows = P.d_rows;
+  A.run = P.run;
   A.splits = P.splits;
   A.k_piece = P.piece / 64;
   return A;
@@ -400,7 +411,7 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
       A.n_tiles = static_cast<int>(tiles_of(A.columns, P.bn));
       A.out = at<__nv_bfloat16>(C, P.d);
       A.ldo = P.piece;
-      run.products<strata::LOSS_DIFFS>(diffs_kernel(P.pair), P.pair, row_tiles * A.n_tiles, mx, mw, mw, mw, A);
+      run.products<strata::LOSS_DIFFS>(diffs_kernel(P.pair, P.in_runs()), P.pair, row_tiles * A.n_tiles, mx, mw, mw, mw, A);
       A.bn = P.width;
       A.n_tiles = static_cast<int>(across);
       A.out = static_cast<__nv_bfloat16*>(dw);

@@ -43,6 +43,9 @@ constexpr int LOSS_NO_ID = 0x7FFFFFFF;
 // 5e-7 of itself, of rows 4,096 wide by 2.4e-6.  So the scores' sums of wider rows (LONG) are taken out of tensor memory and added up
 // in registers, rounded, every 16 steps of 64 (6e-7, for 1 % of a step's time; every 8 steps 3e-7, for 2 to 11 %).  Up to twice that
 // width few rows, where it takes 4 %, have narrow tiles instead, with two sums in tensor memory, one of each half of the width.
+// The differences take z in the same runs (LossArgs::run), and so the same bits of it that lse was made of: what is left of a row that
+// is all but sure of its token is z - lse, which an error in only one of the two would drown (2.4e-6 of a z of 20 is as
+// much as a 1 - p of 5e-5).
 constexpr int LOSS_LONG = 16;
 // Two SMs share a tile: 128 rows and half of the columns each; one SM alone has 128 rows and all columns.  What is left of
 // shared memory holds results on their way out, a piece of 32 rows for each writing warp.
@@ -84,6 +87,7 @@ struct LossArgs {
   int bn, n_tiles;        // columns of a tile, and tiles of them
   int a_rows;             // rows that one SM's tile brings where they are A; the accumulator's other rows are not looked at
   int d_rows;             // rows that d has
+  int run;                // LOSS_SUMS, LOSS_DIFFS: steps of 64 that one sum in tensor memory has
   int splits, rows_pad;   // LOSS_DX: parts that a piece may be cut into, and rows of each
   int k_piece, units;     // steps of 64 ids in a piece, and tiles that run at a time
   int add;                // LOSS_DX: onto what is there
@@ -284,8 +288,7 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
   };
 
   // two sums of a narrow tile of logits
-  const int half_k = (k_all + 1) / 2;
-  const bool halves = MODE == LOSS_SUMS && !LONG && A.bn <= 128 && k_all > 1;
+  const bool halves = MODE == LOSS_SUMS && !LONG && A.run < k_all;
 
   // rows that a stage holds: a pair's always as many, so that the numbers are known; of rows as B all that the tile has
   const int a_rows = PAIR || MODE == LOSS_DW ? 128 : A.a_rows, b_place = loss_b_place(a_rows);
@@ -337,9 +340,9 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
     for (int tile = first; tile < tiles && alive; tile += step) {
       int from, to;
       stages_of(MODE == LOSS_DX ? tile / per_split : 0, from, to);
-      // one accumulator for a tile, or for each 16 steps of it
-      for (int begin = from; alive; begin += LOSS_LONG, ++turn) {
-        const int end = LONG ? min(begin + LOSS_LONG, to) : to;
+      // one accumulator for a tile, or for each run of its steps
+      for (int begin = from; alive; begin += A.run, ++turn) {
+        const int end = LONG ? min(begin + A.run, to) : to;
         const uint32_t buf = turn & 1, sum = tmem + buf * 256;
         if (turn >= 2 && !proj_wait(&B->freed[buf], (turn / 2 + 1) & 1, dead, A.errors, bit)) {
           alive = false;
@@ -354,9 +357,9 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
           tc_fence_after();
           const uint32_t at = smem_u32(smem + ring.slot * stage_bytes), at_b = at + b_place;
           const uint64_t da = A_OUTER ? loss_desc_outer(at) : mma_desc(at, LOSS_LINE), db = B_OUTER ? loss_desc_outer(at_b) : mma_desc(at_b, LOSS_LINE);
-          const bool later = halves && s >= half_k;
+          const bool later = halves && s >= A.run;
           const uint32_t to_sum = later ? sum + 128 : sum;
-          const bool adds = s > (later ? half_k : begin);
+          const bool adds = s > (later ? A.run : begin);
           if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -486,12 +489,15 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
       [[maybe_unused]] int64_t t = -1;
       [[maybe_unused]] LossIds ids{};
       [[maybe_unused]] int n0 = 0;
-      [[maybe_unused]] float lse2 = 0.0f;
+      [[maybe_unused]] float lse = 0.0f, lse2 = 0.0f;
       if constexpr (MODE == LOSS_SUMS || MODE == LOSS_DIFFS) {
         if (r < live) t = A.rows != nullptr ? A.rows[A.row0 + r] : A.row0 + r;
         n0 = A.v0 + o * A.bn;
         ids.start(A, t, n0 + from_c);
-        if (MODE == LOSS_DIFFS && t >= 0) lse2 = A.lse[t] * 1.44269504088896340736f;
+        if (MODE == LOSS_DIFFS && t >= 0) {
+          lse = A.lse[t];
+          lse2 = lse * 1.44269504088896340736f;
+        }
       }
       const int columns = min(A.bn, A.v0 + A.columns - n0);  // of LOSS_SUMS
       [[maybe_unused]] float top = -INFINITY, base = 0.0f, total = 0.0f;
@@ -532,14 +538,14 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
       if constexpr (LONG) {
         // this warp's 128 columns: what the accumulators had is added up, and put back into the last one
         float z[8][16] = {};
-        for (int begin = from; begin < to; begin += LOSS_LONG, ++turn) {
+        for (int begin = from; begin < to; begin += A.run, ++turn) {
           buf = turn & 1;
           if (!proj_wait(&B->done[buf], (turn / 2) & 1, dead, A.errors, bit)) {
             alive = false;
             break;
           }
           tc_fence_after();
-          const bool last = begin + LOSS_LONG >= to;
+          const bool last = begin + A.run >= to;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {  // columns beyond the tile's are there, and not looked at
             if (idle) break;
@@ -585,19 +591,36 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
       } else if constexpr (MODE == LOSS_DIFFS) {
         const int upto = t < 0 ? 0 : A.v0 + A.columns - n0;  // zeros beyond the rows and the vocabulary
 #pragma unroll 1
-        for (int c = 0; c < A.bn; c += 32) {
+        for (int c = from_c; c < (LONG ? min(A.bn, from_c + 128) : A.bn); c += 32) {
           float v[32];
           tmem_ld32(sum + c, v);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = ex2_approx(fmaf(v[e], A.scale, -lse2));
-          while (__any_sync(FULL_MASK, ids.next < n0 + c + 32)) {
-            if (ids.next < n0 + c + 32) {
-              const float q = ids.weight();
+          // p - q of the row's ids, from z again: near 1 both are 1 - exp(z - lse) and 1 - q away from it, which keeps the digits
+          if (__any_sync(FULL_MASK, ids.next < n0 + c + 32)) {
+            float z[32];
+            tmem_ld32(sum + c, z);
+            tmem_wait_ld();
+            int had = -1;
+            do {
+              if (ids.next < n0 + c + 32) {
+                const float q = ids.weight();
+                float d = 0.0f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] -= ids.next == n0 + c + e ? q : 0.0f;
-              ids.advance();
-            }
+                for (int e = 0; e < 32; ++e) d = ids.next == n0 + c + e ? (ids.next == had ? v[e] : z[e]) : d;
+                if (ids.next != had) {
+                  const float x = d / A.dw_scale - lse;
+                  d = x > -0.5f ? expm1f(x) + (1.0f - q) : expf(x) - q;
+                } else {
+                  d -= q;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = ids.next == n0 + c + e ? d : v[e];
+                had = ids.next;
+                ids.advance();
+              }
+            } while (__any_sync(FULL_MASK, ids.next < n0 + c + 32));
           }
           if (upto - c < 32) {
 #pragma unroll

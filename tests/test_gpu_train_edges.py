@@ -1,0 +1,63 @@
+"""Calls of the operators that score and train the end of a model at the edges of what they take."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_train import BF, F32, HALF, TINY, U, Exact, G, _gen, _normal, loss_case, near  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------ rows that are sure of their token
+def sure_case(T, V, H, seed):
+    """Logits of the rows' own tokens from 16 to 32 among others of about +-2: 1 - p from about 1e-3 down to 1e-10."""
+    g = _gen(seed)
+    w = _normal(g, V, H, by=2 * H ** -0.5, to=BF)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    own = 4 + 4 * torch.rand(T, 1, generator=g, device="cuda")
+    return (_normal(g, T, H) + own * w[ids.long()].float()).to(BF), w, ids
+
+
+def check_sure(e, d, steps):
+    """dz of a row's token is p - q, of which little is left: its error is that of z - lse, which is the rounding of lse where both calls
+    took the same z: `steps` roundings of it, at 2^-24 each.  An error that z has in both moves the other ids' shares, by as much
+    of themselves.  Then one rounding of dz to bfloat16, and the products' 32-bit sums and results as everywhere."""
+    T, V = e.p.shape
+    z_off = 2 * e.off_z.amax(1, keepdim=True)
+    lse_off = steps * U * (e.lse.abs()[:, None] + 1)
+    # p - q without the loss of digits: of the ids but a row's own p itself, of its own what the others leave of 1
+    top = e.q.argmax(1, keepdim=True)
+    rest = e.p.clone().scatter_(1, top, 0.0)
+    left = e.q.clone().scatter_(1, top, 0.0).sum(1, keepdim=True) - rest.sum(1, keepdim=True)
+    want = (rest - e.q).scatter_(1, top, left)
+    off_d = (want.abs() * (z_off + HALF) + (e.p + e.q) * lse_off + rest * 2.0 ** -20) * (1 + HALF)
+    dx, dw = want @ e.w * e.s, want.T @ e.clean * e.s
+    near(d["dx"], dx, (off_d + want.abs() * (V / 16 + 32) * 2 * U) @ e.w.abs() * e.s * (1 + HALF) + dx.abs() * (HALF + 4 * U) + TINY[BF])
+    near(d["dw"], dw, (off_d + want.abs() * (T / 16 + 32) * 2 * U).T @ e.clean.abs() * e.s * (1 + HALF) + dw.abs() * (HALF + 4 * U) + TINY[BF])
+
+
+SURE = [(3, 1000, 520), (100, 1000, 2048), (100, 1000, 2056), (17, 600, 8192), (128, 500, 4096), (300, 1000, 1024), (300, 1000, 1032), (300, 1000, 4096),
+        (700, 2100, 2056), (140, 300, 32768)]
+
+
+@pytest.mark.parametrize("T,V,H", SURE)
+def test_the_gradients_of_sure_rows(G, T, V, H):
+    """The way back takes the logits that the way there took, bit for bit: lse is the sum's with one rounding, expm1 adds none of its size."""
+    x, w, ids = sure_case(T, V, H, T + H)
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    check_sure(e, G.cross_entropy_grad(x, w, ids, o["lse"], torch.ones(T, device="cuda")), 3)
+
+
+@pytest.mark.parametrize("s", [1.0, 0.5])
+@pytest.mark.parametrize("T,V,H", [(100, 1000, 2048), (17, 600, 8192), (300, 1000, 1032), (300, 1000, 4096)])
+def test_the_gradients_of_a_student_as_sure_as_its_teacher(G, T, V, H, s):
+    """lse is a maximum in steps of log2 e / s and back, and the log of a sum: five roundings; z / s, q and 1 - q have three more."""
+    x, w, one = sure_case(T, V, H, T + H + 1)
+    ids = torch.stack([one, (one + 1) % V, (one + 7) % V], 1).contiguous()
+    teacher = torch.tensor([30.0, 12.0, -4.0], device="cuda").repeat(T, 1)
+    e = Exact(x, w, ids, teacher, s)
+    o = G.distill_rows(x, w, ids, teacher, temperature=s)
+    check_sure(e, G.distill_grad(x, w, ids, teacher, o["lse"], torch.ones(T, device="cuda"), temperature=s), 8)
