@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(128) loss_list_kernel(const __grid_constant__ 
   for (int i = 0; i < 4; ++i) {
     const int k = i * 32 + lane;
     id[i] = k < A.K ? A.ids[t * A.K + k] : -1;
-    l[i] = k < A.K ? A.teacher[t * A.K + k] * A.over : -INFINITY;
+    l[i] = k < A.K ? A.teacher[t * A.K + k] : -INFINITY;
     if (id[i] < 0 || l[i] == -INFINITY) {
       id[i] = LOSS_NO_ID;
     } else {
@@ -760,10 +760,12 @@ __global__ void __launch_bounds__(128) loss_list_kernel(const __grid_constant__ 
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(FULL_MASK, top, o));
+  // the largest first, then the temperature: finite values of any size stay so, or have no share
   float p[4], total = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    p[i] = id[i] != LOSS_NO_ID ? expf(l[i] - top) : 0.0f;
+    l[i] = (l[i] - top) * A.over;
+    p[i] = id[i] != LOSS_NO_ID ? expf(l[i]) : 0.0f;
     total += p[i];
   }
 #pragma unroll
@@ -783,7 +785,7 @@ __global__ void __launch_bounds__(128) loss_list_kernel(const __grid_constant__ 
     if (i * 32 + lane >= A.K) continue;
     A.sorted[t * A.K + rank[i]] = id[i];
     A.q[t * A.K + rank[i]] = id[i] != LOSS_NO_ID ? p[i] / total : 0.0f;
-    A.logq[t * A.K + rank[i]] = l[i] - top - log_total;
+    A.logq[t * A.K + rank[i]] = l[i] - log_total;
   }
   const bool any = __any_sync(FULL_MASK, id[0] != LOSS_NO_ID || id[1] != LOSS_NO_ID || id[2] != LOSS_NO_ID || id[3] != LOSS_NO_ID);
   beyond = __any_sync(FULL_MASK, beyond);

@@ -61,3 +61,30 @@ def test_the_gradients_of_a_student_as_sure_as_its_teacher(G, T, V, H, s):
     e = Exact(x, w, ids, teacher, s)
     o = G.distill_rows(x, w, ids, teacher, temperature=s)
     check_sure(e, G.distill_grad(x, w, ids, teacher, o["lse"], torch.ones(T, device="cuda"), temperature=s), 8)
+
+
+# ------------------------------------------------------------------------------ a teacher's largest and smallest values
+@pytest.mark.parametrize("s", [1.0, 0.7, 0.001, 1000.0])
+@pytest.mark.parametrize("T", [9, 200])
+def test_a_teachers_values_at_the_types_ends(G, T, s):
+    """Finite values are there, whatever the temperature: the lowest one beside others has no share, all of them the same are equal shares."""
+    x, w, ids, teacher = loss_case(T, 500, 64, T, K=6, skip=0.0)
+    ids = torch.randint(0, 500, (T, 6), generator=_gen(T), device="cuda", dtype=torch.int32)
+    teacher[teacher == -math.inf] = 0.0
+    low, high = torch.finfo(F32).min, torch.finfo(F32).max
+    teacher[0] = low
+    teacher[1, 1:] = low
+    teacher[2] = high
+    teacher[3, ::2] = high
+    teacher[4] = low
+    teacher[4, 2:] = -math.inf
+    teacher[5] = low
+    ids[5, 3] = 500  # beyond the vocabulary, and there
+    teacher[6] = 0.9 * low
+    teacher[6, 1] = high
+    e = Exact(x, w, ids, teacher, s)
+    o = G.distill_rows(x, w, ids, teacher, temperature=s)
+    assert o["loss"][5].isnan() and not o["loss"][:5].isnan().any()
+    e.check_rows(o)
+    g = torch.ones(T, device="cuda")
+    e.check_grad(G.distill_grad(x, w, ids, teacher, o["lse"], g, temperature=s), g)
