@@ -234,8 +234,8 @@ extern "C" int strata_layer_norm_grad(const void* dy, int64_t lddy, const void* 
   if (lddy < H || ldx < H || (dresidual != nullptr && lddr < H) || (dx != nullptr && lddx < H))
     return host_fail(STRATA_EINVAL, "a row stride below H=%d", H);
   const bool sums = dweight != nullptr || dbias != nullptr;
+  if (T == 0 && !sums) return STRATA_OK;  // an empty dx may have no address
   if (!sums && dx == nullptr) return host_fail(STRATA_EINVAL, "no output");
-  if (T == 0 && !sums) return STRATA_OK;
   const uintptr_t esz = dtype == STRATA_DTYPE_F32 ? 4 : 2;
   if (misaligned(dweight, esz) || misaligned(dbias, esz)) return host_fail(STRATA_EALIGN, "a pointer is not aligned to its element");
   if (T > 0) {

@@ -88,3 +88,16 @@ def test_a_teachers_values_at_the_types_ends(G, T, s):
     e.check_rows(o)
     g = torch.ones(T, device="cuda")
     e.check_grad(G.distill_grad(x, w, ids, teacher, o["lse"], g, temperature=s), g)
+
+
+# ------------------------------------------------------------------------------ no rows
+def test_no_rows_and_dx_alone(G):
+    """An empty batch asked for dx alone gets an empty dx."""
+    x, w, ids, teacher = loss_case(4, 50, 64, 1, K=3)
+    none = torch.zeros(0, device="cuda")
+    d = G.cross_entropy_grad(x[:0], w, ids[:0, 0].contiguous(), none, none, dw=False)
+    assert set(d) == {"dx"} and d["dx"].shape == (0, 64)
+    d = G.distill_grad(x[:0], w, ids[:0], teacher[:0], none, none, dw=False)
+    assert set(d) == {"dx"} and d["dx"].shape == (0, 64)
+    d = G.layer_norm_grad(x[:0], x[:0], w[0], none, none, dweight=False, bias=False)
+    assert set(d) == {"dx"} and d["dx"].shape == (0, 64)
