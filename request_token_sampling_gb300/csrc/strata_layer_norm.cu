@@ -115,7 +115,7 @@ constexpr int WIDE_GROUPS = 16;
 int grad_groups(int T, int H) {
   if (H > BLOCK_WIDTH) return std::min(T, WIDE_GROUPS);
   if (H > WARP_WIDTH) return ring_grid(T, 4);
-  return std::min((T + strata::LAYER_NORM_GRAD_WARPS - 1) / strata::LAYER_NORM_GRAD_WARPS, SMS * 2);
+  return std::min((T - 1) / strata::LAYER_NORM_GRAD_WARPS + 1, SMS * 2);
 }
 
 // Narrow rows by warps; wider ones that lie in no common way by a block, element by element.
