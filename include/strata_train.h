@@ -87,8 +87,8 @@ int strata_cross_entropy_rows(const void* x, int64_t ldx, const void* w, int64_t
  * 3e-6 of z).  A row that is left out, whose id is V or more or whose g is 0 gets dx = 0 and adds nothing to dw.
  * With T = 0 dw is set to zeros.  dx and dw start on 16 bytes, their strides are multiples of 8, and they do not overlap an
  * input or one another.
- * `workspace`: strata_loss_workspace(T, V, H, 0, 1) bytes, which hold a piece of dz (512 MB, or 256
- * columns) and parts of dx beside copies of the rows.
+ * `workspace`: strata_loss_workspace(T, V, H, 0, 1) bytes, which hold a piece of dz (at most 512 MB, or 511 columns more where
+ * that is all of the vocabulary) and parts of dx (256 MB, or one of them) beside copies of the rows.
  */
 int strata_cross_entropy_grad(const void* x, int64_t ldx, const void* w, int64_t ldw, int T, int V, int H,
                               const int32_t* ids, const float* lse, const float* g, void* dx, int64_t lddx, void* dw,

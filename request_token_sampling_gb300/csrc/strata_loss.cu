@@ -152,9 +152,9 @@ struct Plan {
   Plan(int T, int V, int H, int K, bool grad)
       : T(T), V(V), H(H), K(std::max(K, 1)), lists(K > 0), grad(grad), pair(false), moved(grad) {
     slab = std::min(T, SLAB_ROWS);
-    // a piece of the vocabulary whose differences are held at a time
-    piece = static_cast<int>(std::min<int64_t>(tiles_of(V, 256) * 256, std::max<int64_t>(256, PIECE_BYTES / (tiles_of(T, 256) * 512) / 256 * 256)));
-    const Tiles scores = tiles_for(slab, V, H, false), tiles = grad ? tiles_for(T, std::min(piece, V), H, true) : scores;
+    // a piece of the vocabulary whose differences are held at a time: 2,048 ids of the most rows
+    const int64_t most = PIECE_BYTES / (tiles_of(T, 256) * 512);
+    const Tiles scores = tiles_for(slab, V, H, false), tiles = grad ? tiles_for(T, std::min<int64_t>(most, V), H, true) : scores;
     // a gradient's logits are added up as its score's were, whatever its tiles
     const int steps = static_cast<int>(tiles_of(H, 64));
     run = is_long() ? strata::LOSS_LONG : scores.columns <= 128 ? (steps + 1) / 2 : steps;
@@ -189,7 +189,7 @@ struct Plan {
       return;
     }
     scaled = take(static_cast<int64_t>(rows_pad) * H * 2);
-    piece = static_cast<int>(tiles_of(piece, 2 * bn) * 2 * bn);  // whole tiles, and steps of 64
+    piece = static_cast<int>((V <= most ? tiles_of(V, 2 * bn) : most / (2 * bn)) * 2 * bn);  // whole tiles, and steps of 64
     d_rows = T <= ALONE_ROWS ? (T + 7) / 8 * 8 : rows_pad;  // few rows: no more than they have; beyond, copies bring zeros
     d = take(static_cast<int64_t>(d_rows) * piece * 2);
     width = H <= 128 ? 128 : 256;

@@ -35,3 +35,8 @@ def test_no_size_of_a_norm_overflows(tmp_path):
     exe = _program(tmp_path, "norm_sizes_check", "-Xcompiler", "-fsanitize=signed-integer-overflow", "-Xcompiler", "-fsanitize-undefined-trap-on-error")
     r = subprocess.run([exe], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and r.stdout == "0 bad\n", (r.returncode, r.stdout[-2000:])
+
+
+def test_the_sizes_of_every_loss(tmp_path):
+    r = subprocess.run([_program(tmp_path, "loss_sizes_check")], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.endswith(" 0 bad\n"), r.stdout[-2000:]
