@@ -274,8 +274,9 @@ TAIL_CALL(draw) {
 
 const Tensor* given(const Tensor& t) { return t.defined() ? &t : nullptr; }
 
-// The outputs and the workspace of a call: the caller's from `out`, or new ones (which are put there), or none.  New ones of up
-// to 32 KB share an allocation, since each takes more than half a microsecond and the smallest calls three on the GPU.
+// The outputs and the workspace of a call: the caller's from `out`, or new ones (which are put there), or none.  New outputs of up
+// to 32 KB share an allocation, since each takes more than half a microsecond and the smallest calls three on the GPU.  The
+// workspace has its own, which ends with the call: an output that is kept keeps no more than its neighbours.
 class Made {
  public:
   Made(PyObject* out, const Tensor& like) : out_(out), like_(like) {
@@ -299,7 +300,7 @@ class Made {
   void make() {
     int64_t shared = 0, small = 0;
     for (int k = 0; k < n_; ++k) {
-      if (items_[k].bytes <= 0 || items_[k].bytes > SMALL) continue;
+      if (!shares(items_[k])) continue;
       shared += (items_[k].bytes + 255) / 256 * 256;
       ++small;
     }
@@ -309,7 +310,7 @@ class Made {
       Item& i = items_[k];
       if (i.bytes < 0) continue;
       const at::IntArrayRef shape(i.shape, i.dims);
-      if (i.bytes == 0 || i.bytes > SMALL || small == 1) {
+      if (!shares(i) || small == 1) {
         i.t = fresh(shape, i.type, like_);
       } else {
         if (!whole.defined()) whole = fresh({shared}, at::kByte, like_);
@@ -333,6 +334,7 @@ class Made {
     ScalarType type = at::kByte;
     Tensor t;
   };
+  static bool shares(const Item& i) { return i.key != nullptr && i.bytes > 0 && i.bytes <= SMALL; }
   static void size(Item& i, at::IntArrayRef shape, ScalarType type) {
     i.type = type;
     i.bytes = static_cast<int64_t>(c10::elementSize(type));

@@ -10,6 +10,9 @@ A step of the end of a model is
     e = layer_norm_grad(d["dx"], n["residual"], weight, n["mean"], n["rstd"])  # dx, dweight, dbias
 
 and a prompt's log-probabilities are ``-cross_entropy_rows(...)["loss"]``.
+
+Outputs of up to 32 KB that one call allocates share a storage: what keeps one of them, or writes its storage out
+(``torch.save``), has them all; ``clone()`` parts them.
 """
 from __future__ import annotations
 

@@ -101,3 +101,17 @@ def test_no_rows_and_dx_alone(G):
     assert set(d) == {"dx"} and d["dx"].shape == (0, 64)
     d = G.layer_norm_grad(x[:0], x[:0], w[0], none, none, dweight=False, bias=False)
     assert set(d) == {"dx"} and d["dx"].shape == (0, 64)
+
+
+# ------------------------------------------------------------------------------ what a kept output keeps
+def test_a_kept_output_does_not_keep_the_workspace(G):
+    """Small outputs share an allocation with one another, and with nothing else."""
+    x, w, ids, teacher = loss_case(4, 400, 64, 1, K=6, skip=0.0)
+    one, g = ids[:, 0].contiguous(), torch.ones(4, device="cuda")
+    n = G.layer_norm_rows(x, w[0])
+    lse = torch.zeros(4, device="cuda")
+    for o in (G.cross_entropy_rows(x, w, one), G.distill_rows(x, w, ids, teacher), n, G.layer_norm_grad(x, x, w[0], n["mean"], n["rstd"]),
+              G.cross_entropy_grad(x, w, one, lse, g, dw=False), G.distill_grad(x, w, ids, teacher, lse, g, dw=False)):
+        own = sum((t.numel() * t.element_size() + 255) // 256 * 256 for t in o.values())
+        for t in o.values():
+            assert t.untyped_storage().nbytes() <= own
