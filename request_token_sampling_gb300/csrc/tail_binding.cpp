@@ -7,6 +7,7 @@
 // which the Python side turns into StrataError.
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -363,6 +364,20 @@ double number(PyObject* o) {
   return v;
 }
 
+// Automatic differentiation passes these calls by.  One that it would have to record says so, or a model would train without
+// it; the warning is the caller's line's, once for each.
+void unrecorded(std::initializer_list<const Tensor*> inputs, const char* by) {
+  if (!c10::GradMode::is_enabled()) return;
+  for (const Tensor* t : inputs) {
+    if (t == nullptr || !t->requires_grad()) continue;
+    if (PyErr_WarnFormat(PyExc_UserWarning, 2,
+                         "an input requires a gradient, and this call is not recorded: %s computes its gradients. "
+                         "Call it under torch.no_grad(), or with detached tensors", by) != 0)
+      throw Refused();
+    return;
+  }
+}
+
 // (x, weight, bias, residual, eps, want residual, want y, want mean and rstd, out, stream) -> out, a dict
 TAIL_CALL(layer_norm) {
   arguments(n, 10);
@@ -386,6 +401,7 @@ TAIL_CALL(layer_norm) {
        *pm = dense(made[2], "mean", {T}, at::kFloat, device), *ps = dense(made[3], "rstd", {T}, at::kFloat, device);
   void* stream = stream_of(a[9], device);
   const int t32 = narrow(T, "T"), h32 = narrow(H, "H");
+  unrecorded({&x, &weight, bias, residual}, "layer_norm_grad");
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = strata_layer_norm_rows(rx.p, rx.ld, rr.p, rr.ld, pw, pb, type == at::kFloat ? STRATA_DTYPE_F32 : STRATA_DTYPE_BF16, t32, h32,
@@ -485,6 +501,7 @@ TAIL_CALL(loss) {
   int64_t bytes = 0;
   void* ws = workspace_at(ws_given, made[2], device, bytes);
   void* stream = stream_of(a[9], device);
+  unrecorded({&x, &w, teacher}, teacher != nullptr ? "distill_grad" : "cross_entropy_grad");
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = teacher != nullptr ? strata_distill_rows(o.x.p, o.x.ld, o.w.p, o.w.ld, o.T, o.V, o.H, o.K, o.ids, o.teacher, temperature, pl, pe, ws, bytes, stream)

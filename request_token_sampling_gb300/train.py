@@ -9,7 +9,9 @@ A step of the end of a model is
     d = cross_entropy_grad(n["y"], head, ids, o["lse"], g)                   # dx, dw
     e = layer_norm_grad(d["dx"], n["residual"], weight, n["mean"], n["rstd"])  # dx, dweight, dbias
 
-and a prompt's log-probabilities are ``-cross_entropy_rows(...)["loss"]``.
+and a prompt's log-probabilities are ``-cross_entropy_rows(...)["loss"]``.  Automatic differentiation passes these calls by: the
+``_grad`` of each is its way back, and a call of the others that it would have to record (an input requires a gradient, outside of
+``torch.no_grad()``) warns.
 
 Outputs of up to 32 KB that one call allocates share a storage: what keeps one of them, or writes its storage out
 (``torch.save``), has them all; ``clone()`` parts them.

@@ -115,3 +115,29 @@ def test_a_kept_output_does_not_keep_the_workspace(G):
         own = sum((t.numel() * t.element_size() + 255) // 256 * 256 for t in o.values())
         for t in o.values():
             assert t.untyped_storage().nbytes() <= own
+
+
+# ------------------------------------------------------------------------------ automatic differentiation
+def test_gradients_that_nothing_records_are_told(G):
+    """Automatic differentiation passes these calls by: one that it would have to record says so."""
+    import warnings
+    x, w, ids, teacher = loss_case(4, 400, 64, 1, K=6, skip=0.0)
+    one = ids[:, 0].contiguous()
+    leaf, head = x.clone().requires_grad_(), w.clone().requires_grad_()
+    for call in (lambda x, w: G.cross_entropy_rows(x, w, one), lambda x, w: G.distill_rows(x, w, ids, teacher), lambda x, w: G.layer_norm_rows(x, w[0].detach())):
+        with pytest.warns(UserWarning, match="not recorded"):
+            o = call(leaf, w)
+        assert not any(t.requires_grad for t in o.values())
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            call(x, w)
+            with torch.no_grad():
+                call(leaf, head)
+            call(leaf.detach(), head.detach())
+    with pytest.warns(UserWarning, match="not recorded"):
+        G.cross_entropy_rows(x, head, one)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(UserWarning):
+            G.cross_entropy_rows(leaf, w, one)
+    assert G.tail_errors() == 0
