@@ -90,7 +90,8 @@ bool map_rows(const Device& dev, CUtensorMap* m, bool f32, const void* p, int64_
 }
 
 // ------------------------------------------------------------------------------ a call's plan
-// It goes by the sizes alone, so that the workspace's size can be asked for without a device.
+// It goes by the sizes alone, so that the workspace's size can be asked for without a device.  Its tiles are for as many SMs; on a device
+// with fewer as many blocks are launched as that one has, since each goes through the tiles by its number and has an SM alone.
 constexpr int SMS = 152, PAIRS = SMS / 2;
 // Blocks of dx's product where few rows have both in one launch, dw's in the others.  dx's bring d's rows beside w, dw's write: up to
 // 32 rows want fewer (17 x 177,128 x 480, the way back, us: 44 112, 54 107, 64 115, 72 115; 5 x 84,656 x 984: 113, 108, 113, 119),
@@ -244,6 +245,7 @@ T* at(const Loss& C, int64_t place) {
 struct Run {
   void* stream;
   bool overlaps;
+  int sms;  // that the products' blocks have
   cudaError_t e = cudaSuccess;
   template <typename K, typename... A>
   void operator()(K kernel, unsigned grid, unsigned block, size_t smem, unsigned cluster, A... args) {
@@ -254,7 +256,7 @@ struct Run {
   template <int MODE>
   void products(Kernel kernel, bool pair, int64_t tiles, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const CUtensorMap& o,
                 const strata::LossArgs& A) {
-    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(tiles, pair ? PAIRS : SMS)) * (pair ? 2 : 1);
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(tiles, pair ? sms / 2 : sms)) * (pair ? 2 : 1);
     (*this)(kernel, blocks, strata::LOSS_THREADS, strata::loss_smem(MODE, pair), pair ? 2 : 1, a, b, c, o, A);
   }
 };
@@ -324,6 +326,7 @@ int forward(const Loss& C, float* loss, float* lse, const char* name) {
   uint32_t* errors = nullptr;
   int device = 0, sms = 0;
   if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
+  sms = std::max(2, std::min(SMS, sms));
   const Device* dev = nullptr;
   if (const int rc = device_entry(device, &dev); rc != STRATA_OK) return rc;
   const Plan P(C.T, C.V, C.H, C.K, false);
@@ -333,7 +336,7 @@ int forward(const Loss& C, float* loss, float* lse, const char* name) {
     return host_fail(STRATA_EINVAL, "x cannot be mapped");
   if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, P.pair ? P.bn / 2 : P.bn)) return host_fail(STRATA_EINVAL, "w cannot be mapped");
   const cudaError_t e = strata::launch_operator(device, C.stream, [&](bool overlaps) {
-    Run run{C.stream, overlaps};
+    Run run{C.stream, overlaps, sms};
     launch_plan(run, C, P, nullptr, loss, lse, nullptr, 0);
     strata::LossArgs A = products_args(C, P, errors);
     A.columns = C.V;
@@ -366,6 +369,7 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
   uint32_t* errors = nullptr;
   int device = 0, sms = 0;
   if (const int rc = strata::tail_device(&device, &errors, &sms); rc != STRATA_OK) return rc;
+  sms = std::max(2, std::min(SMS, sms));
   cudaError_t e;
   if (C.T == 0) {
     e = strata::launch_operator(device, C.stream, [&](bool overlaps) {
@@ -386,11 +390,12 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
   if (!map_rows(*dev, &mw, false, C.w, C.H, C.V, C.ldw, P.pair ? P.bn / 2 : P.bn) || !map_rows(*dev, &mwo, false, C.w, C.H, C.V, C.ldw, 64))
     return host_fail(STRATA_EINVAL, "w cannot be mapped");
   e = strata::launch_operator(device, C.stream, [&](bool overlaps) {
-    Run run{C.stream, overlaps};
+    Run run{C.stream, overlaps, sms};
     launch_plan(run, C, P, g, nullptr, nullptr, dx, lddx);
     strata::LossArgs A = products_args(C, P, errors);
-    const int dx_blocks = dx == nullptr ? 0 : dw == nullptr ? SMS : C.T <= ALONE_ROWS ? dx_blocks_for(C.T) : SMS / 2;  // both products cost the same
-    A.units = P.pair ? PAIRS : dx_blocks;
+    const int dx_share = C.T <= ALONE_ROWS ? dx_blocks_for(C.T) : SMS / 2;  // of many rows both products cost the same
+    const int dx_blocks = dx == nullptr ? 0 : dw == nullptr ? sms : std::max(1, dx_share * sms / SMS);
+    A.units = P.pair ? sms / 2 : dx_blocks;
     A.lse = lse;
     A.wide = !misaligned(dw, 32) && lddw % 16 == 0 && C.H % 16 == 0;
     A.by = at<float>(C, P.by);
@@ -418,7 +423,7 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
       A.ldo = lddw;
       A.add = v0 > 0;
       if (!P.pair) {
-        run(strata::loss_both_kernel, SMS, strata::LOSS_THREADS, strata::loss_smem(strata::LOSS_DW, false), 1, mds, mxo, mxs, md, mwo, mdx, A, A, dx_blocks);
+        run(strata::loss_both_kernel, static_cast<unsigned>(sms), strata::LOSS_THREADS, strata::loss_smem(strata::LOSS_DW, false), 1, mds, mxo, mxs, md, mwo, mdx, A, A, dx_blocks);
         continue;
       }
       if (dw != nullptr)
