@@ -141,3 +141,32 @@ def test_gradients_that_nothing_records_are_told(G):
         with pytest.raises(UserWarning):
             G.cross_entropy_rows(leaf, w, one)
     assert G.tail_errors() == 0
+
+
+# ------------------------------------------------------------------------------ accumulators that go from tile to tile
+# rows, ids, width: blocks with several tiles one after another, of two SMs and of one, whose logits are one sum, two, or runs of an even or
+# an odd number (tests/loss_kinds_check.cu holds which they are)
+KINDS = [(400, 90000, 1088), (500, 50000, 2056), (600, 40000, 1032), (100, 60000, 2056), (64, 90000, 576), (100, 90000, 1536), (90, 120000, 264),
+         (2000, 40000, 520)]
+
+
+@pytest.mark.parametrize("T,V,H", KINDS)
+def test_sums_handed_from_tile_to_tile(G, T, V, H):
+    x, w, ids, _ = loss_case(T, V, H, T + H)
+    x[ids < 0] = math.nan
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    e.check_rows(o)
+    g = _normal(_gen(1), T)
+    e.check_grad(G.cross_entropy_grad(x, w, ids, o["lse"], g), g)
+    again = G.cross_entropy_rows(x, w, ids)
+    assert all(torch.equal(o[k], again[k]) for k in o) and G.tail_errors() == 0
+
+
+@pytest.mark.parametrize("T,V,H", [(400, 90000, 1088), (500, 50000, 2056), (100, 60000, 2056), (64, 90000, 576)])
+def test_the_gradients_of_sure_rows_over_many_tiles(G, T, V, H):
+    x, w, ids = sure_case(T, V, H, T + H)
+    x = (x.float() + 2 * w[ids.long()].float()).to(BF)  # sure among more ids, too
+    e = Exact(x, w, ids)
+    o = G.cross_entropy_rows(x, w, ids)
+    check_sure(e, G.cross_entropy_grad(x, w, ids, o["lse"], torch.ones(T, device="cuda")), 3)
