@@ -64,16 +64,19 @@ struct RingShape {
     smem = static_cast<size_t>(depth) * ring + beside;
   }
 };
-// A multiple of eight that leaves each block some rows, or a block for each row.
-int ring_grid(int T, int blocks) { return T <= SMS ? T : std::min(SMS * blocks, std::max(SMS, T / 8 / 8 * 8)); }
+// A multiple of eight that leaves each block some rows, or a block for each row.  On a device with fewer SMs there are no more than run
+// at a time: one that starts when others end would have its share of the rows still to go through.
+int ring_grid(int T, int blocks, int sms = SMS) {
+  return T <= SMS ? T : std::max(8, std::min(std::min(sms, SMS) * blocks / 8 * 8, std::max(SMS, T / 8 / 8 * 8)));
+}
 
 // The shape of a call, as the root-mean-square norm's: many rows are bound by HBM, a thread takes up to 16
 // elements, so that enough bytes are on their way; few rows are bound by latency: a row goes to as many threads as it has packs.
 template <typename E, int N, int PER>
-cudaError_t launch_forward(const strata::LayerNormArgs& A, int least, bool overlaps, int device, void* stream) {
+cudaError_t launch_forward(const strata::LayerNormArgs& A, int least, bool overlaps, int device, int sms, void* stream) {
   if constexpr (N * PER <= 32 && PER <= 16) {
     const int packs = (A.H + N - 1) / N, need = (packs + PER - 1) / PER;
-    if (PER < least || need > strata::layer_norm_most_threads(N, PER)) return launch_forward<E, N, PER * 2>(A, least, overlaps, device, stream);
+    if (PER < least || need > strata::layer_norm_most_threads(N, PER)) return launch_forward<E, N, PER * 2>(A, least, overlaps, device, sms, stream);
     constexpr int ROWS = 4;
     if (need <= 32)
       return strata::Launch((static_cast<unsigned>(A.T) + ROWS - 1) / ROWS, 32 * ROWS, 0, stream, overlaps)(strata::layer_norm_kernel<E, N, PER, false>, A);
@@ -84,10 +87,10 @@ cudaError_t launch_forward(const strata::LayerNormArgs& A, int least, bool overl
 }
 // Many rows that start anywhere.
 template <typename E, int PER>
-cudaError_t launch_ring(strata::LayerNormArgs A, bool overlaps, int device, void* stream) {
+cudaError_t launch_ring(strata::LayerNormArgs A, bool overlaps, int device, int sms, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   if constexpr (N * PER <= 16) {
-    if ((A.H / N + PER - 1) / PER > strata::LAYER_NORM_RING_THREADS) return launch_ring<E, PER * 2>(A, overlaps, device, stream);
+    if ((A.H / N + PER - 1) / PER > strata::LAYER_NORM_RING_THREADS) return launch_ring<E, PER * 2>(A, overlaps, device, sms, stream);
     const int row = (A.H * static_cast<int>(sizeof(E)) + 15) / 16 * 16;
     const auto kernel = strata::layer_norm_ring_kernel<E, PER>;
     static const int regs = registers(kernel);
@@ -95,18 +98,18 @@ cudaError_t launch_ring(strata::LayerNormArgs A, bool overlaps, int device, void
     A.depth = ring.depth;
     static std::atomic<uint64_t> allowed{0};
     if (const cudaError_t e = allow_shared(kernel, allowed, device); e != cudaSuccess) return e;
-    return strata::Launch(ring_grid(A.T, ring.blocks), ring.threads, ring.smem, stream, overlaps)(kernel, A);
+    return strata::Launch(ring_grid(A.T, ring.blocks, sms), ring.threads, ring.smem, stream, overlaps)(kernel, A);
   } else {
     return cudaErrorInvalidValue;  // not reached: wider rows have their own kernels
   }
 }
 template <typename E>
-cudaError_t launch_forward(const strata::LayerNormArgs& A, const Lie& lie, bool overlaps, int device, void* stream) {
+cudaError_t launch_forward(const strata::LayerNormArgs& A, const Lie& lie, bool overlaps, int device, int sms, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
-  if (A.T >= 4 * SMS && A.H > WARP_WIDTH && A.H <= BLOCK_WIDTH && lie.alike && !lie.packed) return launch_ring<E, 1>(A, overlaps, device, stream);
+  if (A.T >= 4 * SMS && A.H > WARP_WIDTH && A.H <= BLOCK_WIDTH && lie.alike && !lie.packed) return launch_ring<E, 1>(A, overlaps, device, sms, stream);
   const int packs = A.H / (lie.packed ? N : 1);
   const int least = A.T < 2 * SMS ? 1 : packs > 64 ? 4 : packs > 32 ? 2 : 1;
-  return lie.packed ? launch_forward<E, N, 1>(A, least, overlaps, device, stream) : launch_forward<E, 1, 1>(A, least, overlaps, device, stream);
+  return lie.packed ? launch_forward<E, N, 1>(A, least, overlaps, device, sms, stream) : launch_forward<E, 1, 1>(A, least, overlaps, device, sms, stream);
 }
 
 // Groups of rows whose sums over rows are kept apart, until the last kernel adds them up: those of a block.  Rows too wide for a
@@ -120,15 +123,15 @@ int grad_groups(int T, int H) {
 
 // Narrow rows by warps; wider ones that lie in no common way by a block, element by element.
 template <typename E, int N, int PER, bool SHIFT>
-cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, int device, void* stream) {
+cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, int device, int sms, void* stream) {
   if constexpr (N * PER <= 16) {
     const int need = (A.H / N + PER - 1) / PER;
     if (A.H <= WARP_WIDTH) {
-      if (need > 32) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, device, stream);
+      if (need > 32) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, device, sms, stream);
       return strata::Launch(A.groups, 32 * strata::LAYER_NORM_GRAD_WARPS, static_cast<size_t>((A.H + N - 1) / N * N) * 8, stream, overlaps)(
           strata::layer_norm_grad_kernel<E, N, PER, false, SHIFT>, A);
     }
-    if (need > strata::layer_norm_grad_most_threads(N, PER)) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, device, stream);
+    if (need > strata::layer_norm_grad_most_threads(N, PER)) return launch_rows<E, N, PER * 2, SHIFT>(A, overlaps, device, sms, stream);
     if constexpr (N == 1)
       return strata::Launch(A.groups, (need + 31) / 32 * 32, 0, stream, overlaps)(strata::layer_norm_grad_kernel<E, N, PER, true, false>, A);
   }
@@ -137,17 +140,17 @@ cudaError_t launch_rows(const strata::LayerNormGradArgs& A, bool overlaps, int d
 
 // Rows through a ring: as many on their way as an SM's shared memory has room for beside its other blocks.
 template <typename E, int PER, bool SHIFT>
-cudaError_t launch_ring(strata::LayerNormGradArgs& A, bool overlaps, int device, void* stream) {
+cudaError_t launch_ring(strata::LayerNormGradArgs& A, bool overlaps, int device, int sms, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   if constexpr (N * PER <= 16) {
     const int need = (A.H / N + PER - 1) / PER;
-    if (need > strata::layer_norm_grad_ring_threads(N, PER)) return launch_ring<E, PER * 2, SHIFT>(A, overlaps, device, stream);
+    if (need > strata::layer_norm_grad_ring_threads(N, PER)) return launch_ring<E, PER * 2, SHIFT>(A, overlaps, device, sms, stream);
     const int row = (A.H * static_cast<int>(sizeof(E)) + 15) / 16 * 16;
     const auto kernel = strata::layer_norm_grad_ring_kernel<E, PER, SHIFT>;
     static const int regs = registers(kernel);
     const RingShape ring(A.H / N, PER, strata::layer_norm_copier(N, PER), row * (A.dresidual != nullptr ? 3 : 2), row, regs);
     A.depth = ring.depth;
-    A.groups = std::min(A.groups, ring_grid(A.T, ring.blocks));
+    A.groups = std::min(A.groups, ring_grid(A.T, ring.blocks, sms));
     static std::atomic<uint64_t> allowed{0};
     if (const cudaError_t e = allow_shared(kernel, allowed, device); e != cudaSuccess) return e;
     return strata::Launch(A.groups, ring.threads, ring.smem, stream, overlaps)(kernel, A);
@@ -157,15 +160,15 @@ cudaError_t launch_ring(strata::LayerNormGradArgs& A, bool overlaps, int device,
 }
 
 template <typename E>
-cudaError_t launch_grad(strata::LayerNormGradArgs A, const Lie& lie, bool overlaps, int device, void* stream) {
+cudaError_t launch_grad(strata::LayerNormGradArgs A, const Lie& lie, bool overlaps, int device, int sms, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));
   cudaError_t e = cudaSuccess;
   if (A.T > 0) {
     if (A.H <= BLOCK_WIDTH) {
       const bool warps = A.H <= WARP_WIDTH;
-      e = lie.packed  ? (warps ? launch_rows<E, N, 1, false>(A, overlaps, device, stream) : launch_ring<E, 1, false>(A, overlaps, device, stream))
-          : lie.alike ? (warps ? launch_rows<E, N, 1, true>(A, overlaps, device, stream) : launch_ring<E, 1, true>(A, overlaps, device, stream))
-                      : launch_rows<E, 1, 1, false>(A, overlaps, device, stream);
+      e = lie.packed  ? (warps ? launch_rows<E, N, 1, false>(A, overlaps, device, sms, stream) : launch_ring<E, 1, false>(A, overlaps, device, sms, stream))
+          : lie.alike ? (warps ? launch_rows<E, N, 1, true>(A, overlaps, device, sms, stream) : launch_ring<E, 1, true>(A, overlaps, device, sms, stream))
+                      : launch_rows<E, 1, 1, false>(A, overlaps, device, sms, stream);
       overlaps = true;
     } else {  // the sums first: dx may be dy or x
       if (A.part != nullptr) {
@@ -214,7 +217,7 @@ extern "C" int strata_layer_norm_rows(const void* x, int64_t ldx, const void* re
   lie.look_column(weight);
   lie.look_column(bias);
   const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
-    return dtype == STRATA_DTYPE_F32 ? launch_forward<float>(A, lie, overlaps, device, stream) : launch_forward<__nv_bfloat16>(A, lie, overlaps, device, stream);
+    return dtype == STRATA_DTYPE_F32 ? launch_forward<float>(A, lie, overlaps, device, sms, stream) : launch_forward<__nv_bfloat16>(A, lie, overlaps, device, sms, stream);
   });
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_layer_norm_rows: %s", cudaGetErrorString(e));
 }
@@ -261,8 +264,8 @@ extern "C" int strata_layer_norm_grad(const void* dy, int64_t lddy, const void* 
   const strata::LayerNormGradArgs A{dy, x, weight, dresidual, mean, rstd, dx, dweight, dbias, part, errors, lddy, ldx, lddr, lddx, T, H,
                                     T > 0 ? grad_groups(T, H) : 0, 0};
   const cudaError_t e = strata::launch_operator(device, stream, [&](bool overlaps) {
-    return dtype == STRATA_DTYPE_F32 ? launch_grad<float>(A, lie, overlaps, device, stream)
-                                     : launch_grad<__nv_bfloat16>(A, lie, overlaps, device, stream);
+    return dtype == STRATA_DTYPE_F32 ? launch_grad<float>(A, lie, overlaps, device, sms, stream)
+                                     : launch_grad<__nv_bfloat16>(A, lie, overlaps, device, sms, stream);
   });
   return e == cudaSuccess ? STRATA_OK : host_fail(STRATA_ECUDA, "strata_layer_norm_grad: %s", cudaGetErrorString(e));
 }

@@ -50,3 +50,8 @@ def test_no_loss_launches_more_blocks_than_sms(tmp_path):
 def test_the_sizes_of_the_gpu_tests_are_of_all_kinds(tmp_path):
     r = subprocess.run([_program(tmp_path, "loss_kinds_check")], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and r.stdout == "0 bad\n", r.stdout[-2000:]
+
+
+def test_no_norm_launches_more_turning_blocks_than_run_at_a_time(tmp_path):
+    r = subprocess.run([_program(tmp_path, "norm_blocks_check")], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.endswith(" 0 bad\n"), r.stdout[-2000:]
