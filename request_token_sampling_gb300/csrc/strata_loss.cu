@@ -93,10 +93,12 @@ bool map_rows(const Device& dev, CUtensorMap* m, bool f32, const void* p, int64_
 // It goes by the sizes alone, so that the workspace's size can be asked for without a device.  Its tiles are for as many SMs; on a device
 // with fewer as many blocks are launched as that one has, since each goes through the tiles by its number and has an SM alone.
 constexpr int SMS = 152, PAIRS = SMS / 2;
-// Blocks of dx's product where few rows have both in one launch, dw's in the others.  dx's bring d's rows beside w, dw's write: up to
-// 32 rows want fewer (17 x 177,128 x 480, the way back, us: 44 112, 54 107, 64 115, 72 115; 5 x 84,656 x 984: 113, 108, 113, 119),
-// more rows more (96 x 248,320 x 2,048: 560, 539, 507, 542; 128 x 32,000 x 4,096: 170, 161, 155, 168).
-int dx_blocks_for(int T) { return T <= 32 ? 54 : 64; }
+// Blocks of dx's product where few rows have both in one launch, dw's in the others.  dx's bring d's rows beside w, dw's write.  Which
+// share is better goes by the width, hardly by the rows (the way back of 5, 32 and 96 rows, us, 54 blocks and 64: x 177,128 x 480 106, 108,
+// 117 and 113, 114, 117; x 150,000 x 744 148, 153, 159 and 155, 160, 165; x 84,656 x 984 112, 115, 118 and 118, 122, 126; x 150,000 x 1,024
+// 164, 165, 180 and 161, 161, 176; x 150,000 x 1,280 205, 209, 231 and 196, 197, 214; 32 and 96 rows x 248,320 x 2,048 494, 539 and 482, 511;
+// x 32,000 x 4,096 145, 158 and 141, 155.  Of 64 rows 64 blocks are better for narrow ones too, 111 and 107 at a width of 480.)
+int dx_blocks_for(int H) { return H < 1024 ? 54 : 64; }
 constexpr int ALONE_ROWS = 128;           // a call with more may work by pairs of SMs
 // A score that takes longer works on a copy of the rows that take part.  The copy costs 4 us and rows that are left out save their
 // share: with a quarter of them it pays from here on (ns).
@@ -393,7 +395,7 @@ int backward(const Loss& C, const float* lse, const float* g, void* dx, int64_t 
     Run run{C.stream, overlaps, sms};
     launch_plan(run, C, P, g, nullptr, nullptr, dx, lddx);
     strata::LossArgs A = products_args(C, P, errors);
-    const int dx_share = C.T <= ALONE_ROWS ? dx_blocks_for(C.T) : SMS / 2;  // of many rows both products cost the same
+    const int dx_share = C.T <= ALONE_ROWS ? dx_blocks_for(C.H) : SMS / 2;  // of many rows both products cost the same
     const int dx_blocks = dx == nullptr ? 0 : dw == nullptr ? sms : std::max(1, dx_share * sms / SMS);
     A.units = P.pair ? sms / 2 : dx_blocks;
     A.lse = lse;
