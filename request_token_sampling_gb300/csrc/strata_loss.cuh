@@ -602,23 +602,20 @@ __device__ __forceinline__ void loss_products(const CUtensorMap& ma, const CUten
             float z[32];
             tmem_ld32(sum + c, z);
             tmem_wait_ld();
-            int had = -1;
             do {
               if (ids.next < n0 + c + 32) {
-                const float q = ids.weight();
-                float d = 0.0f;
+                const int at = ids.next - n0 - c;
+                float q = 0.0f, d = 0.0f;
+                do {  // one that comes twice counts twice
+                  q += ids.weight();
+                  ids.advance();
+                } while (ids.next == n0 + c + at);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) d = ids.next == n0 + c + e ? (ids.next == had ? v[e] : z[e]) : d;
-                if (ids.next != had) {
-                  const float x = d / A.dw_scale - lse;
-                  d = x > -0.5f ? expm1f(x) + (1.0f - q) : expf(x) - q;
-                } else {
-                  d -= q;
-                }
+                for (int e = 0; e < 32; ++e) d = at == e ? z[e] : d;
+                d = d / A.dw_scale - lse;
+                d = d > -0.5f ? expm1f(d) + (1.0f - q) : expf(d) - q;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = ids.next == n0 + c + e ? d : v[e];
-                had = ids.next;
-                ids.advance();
+                for (int e = 0; e < 32; ++e) v[e] = at == e ? d : v[e];
               }
             } while (__any_sync(FULL_MASK, ids.next < n0 + c + 32));
           }
