@@ -83,8 +83,8 @@ int strata_cross_entropy_rows(const void* x, int64_t ldx, const void* w, int64_t
  * dx [T][H] and dw [V][H] are bfloat16 (either may be NULL).  The logits are computed again, in pieces of the vocabulary;
  * dz / g is rounded to bfloat16 between the products, and so is x[t] g[t] / max|g| (x itself where
  * all g are equal).  With the T, V and H of the call that gave lse they are the same bits of z; so what is left of dz / g where a
- * row is all but sure of its token is off by the rounding of lse, 3 * 2^-24 (|lse| + 1) at most (rows in other batches: by z's error, up to
- * 3e-6 of z).  A row that is left out, whose id is V or more or whose g is 0 gets dx = 0 and adds nothing to dw.
+ * row is all but sure of its token is off by the rounding of lse, 3 * 2^-24 (|lse| + 1) at most (with the lse of a call of
+ * another size: by 1e-6 of z, too).  A row that is left out, whose id is V or more or whose g is 0 gets dx = 0 and adds nothing to dw.
  * With T = 0 dw is set to zeros.  dx and dw start on 16 bytes, their strides are multiples of 8, and they do not overlap an
  * input or one another.
  * `workspace`: strata_loss_workspace(T, V, H, 0, 1) bytes, which hold a piece of dz (at most 512 MB, or 511 columns more where
@@ -108,7 +108,7 @@ int strata_distill_rows(const void* x, int64_t ldx, const void* w, int64_t ldw, 
                         int64_t workspace_bytes, void* stream);
 
 /*
- * The gradients of sum_t g[t] * loss[t]:
+ * The gradients of sum_t g[t] * loss[t] (a student as sure as its teacher: dz / (g s) off by 8 * 2^-24 (|lse| + 1) at most):
  *   dz[t][v] = g[t] * s * (exp(z[t][v] / s - lse[t]) - sum of q[t][k] with ids[t][k] = v),    dx = dz w,    dw = dz^T x
  * workspace: strata_loss_workspace(T, V, H, K, 1).  Else as strata_cross_entropy_grad.
  */

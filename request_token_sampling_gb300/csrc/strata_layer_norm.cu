@@ -85,7 +85,8 @@ cudaError_t launch_forward(const strata::LayerNormArgs& A, int least, bool overl
     return strata::Launch(A.T, 1024, 0, stream, overlaps)(strata::layer_norm_wide_kernel<E>, A);
   }
 }
-// Many rows that start anywhere.
+// Many rows that start anywhere (the boundary is that of rows up to some 2,000 wide: 600 rows x 2,049, us, 6.1 element by element and 6.8
+// here, x 1,135 4.4 and 6.3; x 5,003 11.6 and 8.2; 8,192 rows x 1,135 27 and 25).
 template <typename E, int PER>
 cudaError_t launch_ring(strata::LayerNormArgs A, bool overlaps, int device, int sms, void* stream) {
   constexpr int N = 16 / static_cast<int>(sizeof(E));

@@ -9,7 +9,8 @@
 //   LOSS_DW     dw of the piece: d^T xs over the rows (both operands with the sum's index outermost in memory)
 //   LOSS_DX     parts of dx: d w over the piece's ids (w with the sum's index outermost), in 32 bits, or dx where one is all
 // Between d and its products stands one rounding to bfloat16, the type of w and x, which the tensor cores ask for: at most 2^-8 of
-// each term, as far off as the results' own rounding.  g stays out of d: dx is scaled in 32 bits at the end, and
+// each term, as far off as the results' own rounding (together 1.1 to 1.5 times that, as a rule; up to 2.3 times of one to four
+// rows, where one d is most of a result).  g stays out of d: dx is scaled in 32 bits at the end, and
 // x of a row is scaled by g / max|g| in xs, which changes nothing where all g are equal (a mean).
 //
 // Rows that are left out do not take part: the others are copied one after another first (loss_gather_kernel), but for scores
@@ -17,11 +18,11 @@
 //
 // Many rows are bound by the tensor cores: tiles of 256 x 256 on two SMs, half of the columns brought by each (64 bytes a cycle
 // where a tile on one SM takes 96), six or seven stages of 32 KB on their way, and two accumulators, which four writing warps each
-// empty by turns.  Measured (one GB300, rows x ids x width): the sums of 2,048 x 32,000 x 2,048 140 us (1.92 PFLOP/s, a library
-// product's rate), differences, dw and dx 145, 148 and 149; a whole step of 4,096 x 32,000 x 4,096, an eighth of the rows left
-// out, 2,140 us in a stream of steps, which the power limit sets (1,893 alone).  Few rows are bound by HBM: tiles of 128 rows on one
+// empty by turns.  Measured (one GB300, rows x ids x width): the sums of 2,048 x 32,000 x 2,048 144 us (1.87 PFLOP/s, a library
+// product's rate), differences, dw and dx 154, 150 and 151; a whole step of 4,096 x 32,000 x 4,096, an eighth of the rows left
+// out, 2,190 us in a stream of steps, which the power limit sets (1,990 alone).  Few rows are bound by HBM: tiles of 128 rows on one
 // SM, whose rows past the last one are neither loaded nor looked at: the sums of 64 x 248,320 x 2,048 150 us (6.8 TB/s); the step
-// of 96 such rows 662, of which w's three readings and dw's writing take 600 at the copy's rate.
+// of 96 such rows 661, of which w's three readings and dw's writing take 600 at the copy's rate.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -41,7 +42,7 @@ constexpr int LOSS_RUNS = 4;          // steps of 64 rows up to which dw's tiles
 constexpr int LOSS_NO_ID = 0x7FFFFFFF;
 // The tensor cores cut their sums off to 32 bits after every 16 products, always towards zero: lse of rows 1,024 wide is off by
 // 5e-7 of itself, of rows 4,096 wide by 2.4e-6.  So the scores' sums of wider rows (LONG) are taken out of tensor memory and added up
-// in registers, rounded, every 16 steps of 64 (6e-7, for 1 % of a step's time; every 8 steps 3e-7, for 2 to 11 %).  Up to twice that
+// in registers, rounded, every 16 steps of 64 (up to 8e-7, for 1 % of a step's time; every 8 steps 3e-7, for 2 to 11 %).  Up to twice that
 // width few rows, where it takes 4 %, have narrow tiles instead, with two sums in tensor memory, one of each half of the width.
 // The differences take z in the same runs (LossArgs::run), and so the same bits of it that lse was made of: what is left of a row that
 // is all but sure of its token is z - lse, which an error in only one of the two would drown (2.4e-6 of a z of 20 is as
