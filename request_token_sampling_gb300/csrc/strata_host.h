@@ -14,6 +14,9 @@ __attribute__((visibility("hidden"), format(printf, 2, 3))) int host_fail(int co
 // The current device, its word of STRATA_DEVERR_* bits and its number of SMs.
 __attribute__((visibility("hidden"))) int tail_device(int* device, uint32_t** errors, int* sms);
 
+// SMs of a GB300, which sizes that are asked for without a device go by.
+constexpr int GB300_SMS = 152;
+
 // A launch.  One that overlaps may be set up while the kernel before it on the stream still runs: the kernel waits
 // for that one (griddepcontrol.wait) before it reads or writes anything of the caller's, or of the workspace.
 struct Launch {

@@ -31,7 +31,7 @@ struct Lie {
   void look_column(const void* p) { packed = packed && !misaligned(p, 16); }
 };
 
-constexpr int SMS = 152, SM_BYTES = 224 * 1024;          // shared memory of an SM for rows on their way
+constexpr int SMS = strata::GB300_SMS, SM_BYTES = 224 * 1024;          // shared memory of an SM for rows on their way
 constexpr int BLOCK_WIDTH = 512 * 16, WARP_WIDTH = 32 * 16;
 
 // Registers of a kernel's thread, for the number of its blocks on an SM; found once.

@@ -92,7 +92,7 @@ bool map_rows(const Device& dev, CUtensorMap* m, bool f32, const void* p, int64_
 // ------------------------------------------------------------------------------ a call's plan
 // It goes by the sizes alone, so that the workspace's size can be asked for without a device.  Its tiles are for as many SMs; on a device
 // with fewer as many blocks are launched as that one has, since each goes through the tiles by its number and has an SM alone.
-constexpr int SMS = 152, PAIRS = SMS / 2;
+constexpr int SMS = strata::GB300_SMS, PAIRS = SMS / 2;
 // Blocks of dx's product where few rows have both in one launch, dw's in the others.  dx's bring d's rows beside w, dw's write.  Which
 // share is better goes by the width, hardly by the rows (the way back of 5, 32 and 96 rows, us, 54 blocks and 64: x 177,128 x 480 106, 108,
 // 117 and 113, 114, 117; x 150,000 x 744 148, 153, 159 and 155, 160, 165; x 84,656 x 984 112, 115, 118 and 118, 122, 126; x 150,000 x 1,024
